@@ -7,6 +7,10 @@ library libmuon_adamw.so, which must have been built (there is no fallback).
 
 `MuonAdamW` is a small convenience holder: it allocates the optimizer state
 and workspace as torch tensors and calls `muon_adamw_step`.
+
+The operators that produce gradients (include/ma_grads.h: embedding lookup and
+gradient, activations held in 8 bits and the gradients formed from them) are
+in `grads` and under their names here.
 """
 
 from __future__ import annotations
@@ -15,7 +19,7 @@ import ctypes as C
 from typing import Dict, List, Optional, Sequence, Tuple
 
 from . import _abi
-from ._abi import (MA_ERR_CAPTURE, MA_ERR_HIP, MA_ERR_INVALID_ARG, MA_ERR_SHAPE, MA_ERR_UNSUPPORTED,  # noqa: F401
+from ._abi import (MA_ACT_GELU_TANH, MA_ACT_GROUP, MA_ACT_SILU, MA_ERR_CAPTURE, MA_ERR_HIP, MA_ERR_INVALID_ARG, MA_ERR_SHAPE, MA_ERR_UNSUPPORTED,  # noqa: F401
                    MA_ERR_WORKSPACE, MA_GROUP_ADAMW, MA_GROUP_MUON, MA_GROUP_NONE,
                    MA_LR_CONSTANT, MA_LR_COSINE_MIN, MA_MODE_ADAMW, MA_MODE_MUON_ADAMW,
                    MA_NOALLOC_SCRATCH_BYTES, MA_NS_BF16, MA_NS_FP32, MA_OK, MA_PARAM_BF16,
@@ -28,7 +32,26 @@ __all__ = [
     "muon_adamw_step", "muon_adamw_step_profiled", "muon_adamw_step_noalloc",
     "muon_adamw_plan_free", "muon_adamw_last_error",
     "muon_adamw_version", "MuonAdamW", "load_library",
+    "ActCheckpoint", "EmbeddingGrad", "LinearGrad",
+    "ma_act_pack", "ma_act_unpack", "ma_embedding_lookup", "ma_embedding_grad",
+    "ma_embedding_grad_workspace_size", "ma_linear_grad", "ma_linear_grad_workspace_size",
+    "ma_glu_forward", "ma_glu_backward",
 ]
+
+# The gradient operators need torch at import (the optimizer step only when it
+# is called), so they are loaded on first use.
+_GRADS = ("ActCheckpoint", "EmbeddingGrad", "LinearGrad", "ma_act_pack", "ma_act_unpack",
+          "ma_embedding_lookup", "ma_embedding_grad", "ma_embedding_grad_workspace_size",
+          "ma_linear_grad", "ma_linear_grad_workspace_size", "ma_glu_forward", "ma_glu_backward")
+
+
+def __getattr__(name):
+    if name in _GRADS:
+        from . import grads
+        for n in _GRADS:
+            globals()[n] = getattr(grads, n)
+        return globals()[name]
+    raise AttributeError("module %r has no attribute %r" % (__name__, name))
 
 
 class MuonAdamWError(RuntimeError):
@@ -340,9 +363,48 @@ class MuonAdamW:
                 self.state.adam_m[i] = torch.zeros_like(p, dtype=torch.float32)
                 self.state.adam_v[i] = torch.zeros_like(p, dtype=torch.float32)
         dev = next((p.device for p in self.params if p is not None), torch.device("cuda"))
+        self.grad_buffers = [None] * len(self.names)    # gradients formed by step
+        self.sum_buffers = [None] * len(self.names)     # float32 sums of bf16 ones
         nbytes = muon_adamw_workspace_size(self.plan, self.hp.ns_precision)
         self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
 
+    def _formed(self, i, g, stream):
+        """Entry i's gradient: a tensor as it is; an EmbeddingGrad or LinearGrad,
+        or a list of them (micro-batches, added up in float32), formed in a
+        buffer this object keeps for the entry."""
+        from . import grads as G
+        sources = g if isinstance(g, list) else [g]
+        if not sources or not all(isinstance(s, (G.EmbeddingGrad, G.LinearGrad)) for s in sources):
+            if isinstance(g, list):
+                raise TypeError("grad %d: a list holds EmbeddingGrad or LinearGrad items" % i)
+            return g
+        import torch
+        p = self.params[i]
+        if p.dim() != 2:
+            raise ValueError("grad %d: entry %s is not a matrix" % (i, self.names[i]))
+        if self.grad_buffers[i] is None:
+            self.grad_buffers[i] = torch.empty_like(p, memory_format=torch.contiguous_format)
+        out = self.grad_buffers[i]
+        if len(sources) == 1 or out.dtype == torch.float32:
+            for k, s in enumerate(sources):
+                G.form_gradient(s, p.shape, out, k > 0, stream)
+            return out
+        # bf16 storage: one rounding, after the last micro-batch
+        if self.sum_buffers[i] is None:
+            self.sum_buffers[i] = torch.empty(p.shape, dtype=torch.float32, device=p.device)
+        for k, s in enumerate(sources):
+            G.form_gradient(s, p.shape, self.sum_buffers[i], k > 0, stream)
+        with G._On(p.device, stream, (out, self.sum_buffers[i])):
+            out.copy_(self.sum_buffers[i])
+        return out
+
     def step(self, grads, stream=None, grad_norm_out=None, muon_update_out=None):
+        """One optimizer step.  grads[i] is entry i's gradient: a tensor, or an
+        EmbeddingGrad or LinearGrad (or a list of them, one per micro-batch),
+        formed first, on the same stream, into a buffer kept in grad_buffers[i]."""
+        if any(not (g is None or isinstance(g, int) or hasattr(g, "data_ptr")) for g in grads):
+            if len(grads) > len(self.names):
+                raise ValueError("%d gradients for %d entries" % (len(grads), len(self.names)))
+            grads = [self._formed(i, g, stream) for i, g in enumerate(grads)]
         muon_adamw_step(self.plan, self.params, grads, self.state, self.hp, self.workspace,
                         stream, grad_norm_out, muon_update_out)

@@ -1,4 +1,4 @@
-"""ctypes mirror of include/muon_adamw.h.
+"""ctypes mirror of include/muon_adamw.h and include/ma_grads.h.
 
 Argument marshalling only: every step of the optimizer runs in the HIP
 library.  Loading fails loudly when the library has not been built; there is
@@ -27,6 +27,8 @@ MA_NS_BF16, MA_NS_FP32 = 0, 1
 MA_LR_CONSTANT, MA_LR_COSINE_MIN = 0, 1
 MA_PARAM_FP32, MA_PARAM_BF16 = 0, 1
 MA_MAX_NDIM = 8
+MA_ACT_GROUP = 32
+MA_ACT_SILU, MA_ACT_GELU_TANH = 0, 1
 MA_PROFILE_EVENTS = 5
 MA_NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -66,7 +68,7 @@ class ma_hparams(C.Structure):
                 ("total_steps", C.c_int64), ("min_lr_rate", C.c_double)]
 
 
-# (name, restype, argtypes) of every exported symbol of the header
+# (name, restype, argtypes) of every exported symbol of muon_adamw.h
 SIGNATURES = [
     ("muon_adamw_default_hparams", C.c_int, [C.POINTER(ma_hparams)]),
     ("muon_adamw_plan", C.c_int, [C.POINTER(ma_param_desc), C.c_int32,
@@ -94,6 +96,27 @@ SIGNATURES = [
     ("muon_adamw_version", C.c_char_p, []),
 ]
 
+_I32, _I64, _P, _F64, _SZ = C.c_int32, C.c_int64, C.c_void_p, C.c_double, C.c_size_t
+
+# and of ma_grads.h
+GRAD_SIGNATURES = [
+    ("ma_act_pitch", C.c_int, [_I64, C.POINTER(_I64), C.POINTER(_I64)]),
+    ("ma_act_pack", C.c_int, [_P, _I32, _I64, _I64, _I64, _P, _P, _P]),
+    ("ma_act_unpack", C.c_int, [_P, _P, _I64, _I64, _P, _I32, _I64, _P]),
+    ("ma_embedding_lookup", C.c_int, [_P, _I32, _I64, _I64, _I64, _P, _I32, _I64, _F64, _P, _I32,
+                                      _I64, _P]),
+    ("ma_embedding_grad_workspace_size", C.c_int, [_I64, _I64, _I64, C.POINTER(_SZ)]),
+    ("ma_embedding_grad", C.c_int, [_P, _I32, _I64, _P, _I32, _I64, _I64, _I64, _F64, _I64, _P,
+                                    _I32, _I32, _P, _SZ, _P]),
+    ("ma_linear_grad_workspace_size", C.c_int, [_I64, _I64, _I64, _I32, C.POINTER(_SZ)]),
+    ("ma_linear_grad", C.c_int, [_P, _I32, _I64, _I64, _I64, _P, _P, _I64, _P, _I32, _I32, _P,
+                                 _SZ, _P]),
+    ("ma_glu_forward", C.c_int, [_P, _P, _I32, _I64, _I64, _I64, _I64, _I32, _P, _I64, _P, _P, _P,
+                                 _P, _P]),
+    ("ma_glu_backward", C.c_int, [_P, _I32, _I64, _I64, _I64, _P, _P, _P, _P, _I32, _P, _I64, _P,
+                                  _I64, _P, _P, _P]),
+]
+
 _lib = None
 
 
@@ -107,7 +130,7 @@ def load(path: str = LIB_PATH):
             "libmuon_adamw.so is not built (%s); run "
             "`python -m muon_newton_schulz_02_amd.build` first" % path)
     lib = C.CDLL(path)
-    for name, res, args in SIGNATURES:
+    for name, res, args in SIGNATURES + GRAD_SIGNATURES:
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args

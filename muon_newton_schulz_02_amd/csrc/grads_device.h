@@ -1,0 +1,108 @@
+// Device helpers shared by the gradient operators' kernels: element types,
+// vector access, and the 8-bit form of activations.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+namespace ma {
+namespace {
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+
+// V consecutive elements of type T, widened to float: one or two 16-byte
+// accesses for V = 8 (or 4 floats), else element by element.
+template <typename T, int V>
+__device__ __forceinline__ void load_v(const T* p, float* v) {
+    if constexpr (V * sizeof(T) % 16 == 0) {
+#pragma unroll
+        for (int q = 0; q < (int)(V * sizeof(T) / 16); ++q) {
+            const u32x4 w = *(reinterpret_cast<const u32x4*>(p) + q);
+            if constexpr (sizeof(T) == 4) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[4 * q + e] = __uint_as_float(w[e]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    v[8 * q + 2 * e] = __uint_as_float(w[e] << 16);
+                    v[8 * q + 2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+                }
+            }
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[e] = (float)p[e];
+    }
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    const bf16x2 p = {(__bf16)a, (__bf16)b};
+    return __builtin_bit_cast(uint32_t, p);
+}
+
+// The reverse: V floats rounded to T (nearest even) and stored.
+template <typename T, int V>
+__device__ __forceinline__ void store_v(T* p, const float* v) {
+    if constexpr (V * sizeof(T) % 16 == 0) {
+#pragma unroll
+        for (int q = 0; q < (int)(V * sizeof(T) / 16); ++q) {
+            u32x4 w;
+            if constexpr (sizeof(T) == 4) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[e] = __float_as_uint(v[4 * q + e]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[e] = pack_bf16(v[8 * q + 2 * e], v[8 * q + 2 * e + 1]);
+            }
+            *(reinterpret_cast<u32x4*>(p) + q) = w;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) p[e] = (T)v[e];
+    }
+}
+
+// ------------------------------------------------- activations in 8 bits --
+// A group of 32 features is held as codes q and one exponent byte b = e + 127:
+// x stands for q 2^e.  With the group's largest magnitude m 2^k (1 <= m < 2),
+// e = k - 6 makes the largest quotient 64 m, which rounds to at most 127 for
+// 64 m < 127.5; above that e = k - 5.  The byte is kept within [1, 248], so the
+// scale and its inverse are normal floats and 127 2^e is finite; quotients are
+// exact (powers of two) and rounded once, to nearest even.
+
+// Exponent byte of a group from the bits of its largest magnitude (as an
+// unsigned integer: NaN above infinity above every finite value).
+__device__ __forceinline__ uint32_t act_exp_byte(uint32_t top) {
+    const int k = (int)(top >> 23);                              // biased exponent
+    if (k == 255) return 255u;                                   // infinity or NaN
+    const int b = k - 6 + ((top & 0x7fffffu) >= 0x7f0000u ? 1 : 0);
+    return (uint32_t)min(max(b, 1), 248);
+}
+
+// 2^(b - 127); infinity for the NaN mark 255, so that code 0 times it is NaN.
+__device__ __forceinline__ float act_scale(uint32_t b) { return __uint_as_float(b << 23); }
+// 2^(127 - b) for b in [1, 248]; 0 for the NaN mark.
+__device__ __forceinline__ float act_inv_scale(uint32_t b) {
+    return b == 255u ? 0.f : __uint_as_float((254u - b) << 23);
+}
+
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+// Four codes of one 32-bit word, lowest byte first.  A NaN group's inverse
+// scale is 0: its codes are forced to 0 (infinity times 0 converts to 0).
+__device__ __forceinline__ uint32_t act_code(float x, float inv) {
+    const float q = __builtin_amdgcn_fmed3f(rintf(x * inv), -127.f, 127.f);
+    return (uint32_t)(int)q & 0xffu;
+}
+
+__device__ __forceinline__ float act_value(uint32_t w, int byte, float scale) {
+    return (float)(int)(int8_t)(w >> (8 * byte)) * scale;
+}
+
+}  // namespace
+}  // namespace ma
