@@ -319,7 +319,10 @@ int ma_linear_grad_workspace_size(int64_t n_tokens, int64_t n_out, int64_t n_in,
         return MA_ERR_INVALID_ARG;
     }
     TRY(check_lg_shape(fn, n_tokens, n_out, n_in, dy_dtype));
-    *bytes = linear_grad_plan(n_tokens, n_out, n_in, dy_dtype).total;
+    // enough for any dy address and stride
+    const size_t a = linear_grad_plan(n_tokens, n_out, n_in, dy_dtype, false).total;
+    const size_t b = linear_grad_plan(n_tokens, n_out, n_in, dy_dtype, n_out % 8 == 0).total;
+    *bytes = a > b ? a : b;
     clear_error();
     return MA_OK;
 }
@@ -333,7 +336,8 @@ int ma_linear_grad(const void* dy, int32_t dy_dtype, int64_t n_tokens, int64_t n
     TRY(check_flag(fn, "accumulate", accumulate));
     TRY(check_lg_shape(fn, n_tokens, n_out, n_in, dy_dtype));
     TRY(check_stride(fn, "dy", dy_stride, 0, n_tokens));
-    const LgPlan p = linear_grad_plan(n_tokens, n_out, n_in, dy_dtype);
+    const LgPlan p = linear_grad_plan(n_tokens, n_out, n_in, dy_dtype,
+                                      linear_grad_big_rows(dy, n_out, dy_stride));
     TRY(check_workspace(fn, workspace, ws_bytes, p.total));
     TRY(check_spans(fn, {matrix("dy", dy, dy_dtype, n_tokens, n_out, dy_stride, false),
                          codes_of("codes", codes, n_tokens, n_in, false),

@@ -246,6 +246,288 @@ __global__ __launch_bounds__(kThreads) void k_linear_grad(LgArgs a, int64_t tile
         }
 }
 
+// ---------------------------------------------------------------------------
+// Large products: 256 x 256 tiles, eight waves, operands copied from global
+// memory straight into LDS.
+//
+// Codes turned into bf16 inside the GEMM would be turned again by every tile
+// row, so a first launch (k_lg_expand) turns X once into bf16 in the workspace,
+// in the order the GEMM reads it: per 32 tokens, per 32 features, a 2 KB block
+// of 32 feature rows of 32 tokens each, 16-byte chunk c (8 tokens) of row k at
+// slot c ^ ((k >> 2) & 3).  A stage of a tile (32 tokens by 256 features) is
+// then 16 KB in one piece, and a fragment (8 tokens of a feature) one 16-byte
+// LDS read, at twice the rate of the transposing read that dY's fragments need.
+// The wave tile is 128 features by 64 outputs, so four of a wave's six fragments
+// per step are such reads.  Both expanded axes are padded with zeros (tokens to 32,
+// features to 256).
+//
+// A ring of five stages (16 KB of dY, 16 KB of X each) is filled four stages
+// ahead by buffer loads that write LDS; two waves per SIMD cover each other's
+// waits.  Rows of dY past the last token and stages past the slice's end lie outside the
+// buffer's extent, and arrive as zeros.
+// ---------------------------------------------------------------------------
+constexpr int kBigTile = 256;
+constexpr int kBigThreads = 512;
+constexpr int kBigRegion = 16384;               // one operand's part of a stage
+constexpr int kBigStage = 2 * kBigRegion;
+constexpr int kBigStages = 5;
+constexpr int kBigRow = 512;                    // LDS bytes of a token row of dY
+
+__global__ __launch_bounds__(kThreads) void k_lg_expand(const int8_t* __restrict__ codes,
+                                                        const uint8_t* __restrict__ exps,
+                                                        char* __restrict__ out, int64_t n_tokens,
+                                                        int64_t stages, int64_t cp, int64_t ep,
+                                                        int64_t blocks_k) {
+    __shared__ __attribute__((aligned(16))) char buf[kBigRegion];
+    const int tid = threadIdx.x, oct = tid >> 6, f = (tid & 63) * 4;
+    const int64_t k = (int64_t)blockIdx.x * kBigTile + f;
+    for (int64_t s = blockIdx.y; s < stages; s += gridDim.y) {
+        const int64_t t0 = s * kLgStage + oct * 8;
+        uint32_t w[8], e[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            w[r] = 0u;
+            e[r] = 0u;
+            if (t0 + r < n_tokens && k < cp) {
+                w[r] = *reinterpret_cast<const uint32_t*>(codes + (t0 + r) * cp + k);
+                e[r] = exps[(t0 + r) * ep + (k >> 5)];
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            u32x4 v;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                v[q] = pack_bf16(act_value(w[2 * q], c, act_scale(e[2 * q])),
+                                 act_value(w[2 * q + 1], c, act_scale(e[2 * q + 1])));
+            const int row = f + c;
+            const int slot = oct ^ (((row & 31) >> 2) & 3);
+            *reinterpret_cast<u32x4*>(buf + row * 64 + slot * 16) = v;
+        }
+        __syncthreads();
+        char* o = out + (s * blocks_k + (int64_t)blockIdx.x * 8) * 2048;
+#pragma unroll
+        for (int i = 0; i < kBigRegion / (kThreads * 16); ++i) {
+            const int at = (i * kThreads + tid) * 16;
+            *reinterpret_cast<u32x4*>(o + at) = *reinterpret_cast<const u32x4*>(buf + at);
+        }
+        __syncthreads();
+    }
+}
+
+// Buffer resource: base address, stride 0, extent in bytes (accesses past it
+// read zero), raw format.
+__device__ __forceinline__ u32x4 make_rsrc(const void* base, int64_t bytes) {
+    const uint64_t a = (uint64_t)base;
+    u32x4 r;
+    r.x = (uint32_t)a;
+    r.y = (uint32_t)(a >> 32) & 0xffffu;
+    r.z = bytes <= 0 ? 0u : bytes > 0x7fffffffLL ? 0x7fffffffu : (uint32_t)bytes;
+    r.w = 0x00020000u;
+    return r;
+}
+
+__device__ __forceinline__ uint32_t lds_addr(const void* p) {
+    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)p;
+}
+
+// 16 bytes per lane from global memory straight into LDS: lane t of the wave
+// writes bytes [lds + 16 t, lds + 16 t + 16).  The kernel orders these copies
+// itself, with explicit vmcnt waits and barriers.
+__device__ __forceinline__ void dma16(u32x4 rsrc, uint32_t lds, uint32_t voff) {
+    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :
+                 : "s"(lds), "v"(voff), "s"(rsrc)
+                 : "memory", "m0");
+}
+
+// s_waitcnt vmcnt(n) alone, n = 8 or 12.
+__device__ __forceinline__ void wait_vm8() { __builtin_amdgcn_s_waitcnt(0x0F78); }
+__device__ __forceinline__ void wait_vm12() { __builtin_amdgcn_s_waitcnt(0x0F7C); }
+
+// Workgroup barrier that orders this wave's LDS reads around it without
+// waiting for outstanding copies into LDS.
+__device__ __forceinline__ void stage_barrier() {
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+struct BigArgs {
+    const char* dy;
+    const char* xt;            // the expanded X
+    void* grad;
+    float* partials;
+    int64_t n_tokens, n_out, n_in, dy_stride, blocks_k;
+    int64_t tiles_n, tiles_k, slices, per;
+    int32_t accumulate;
+};
+
+// This wave's copies of one stage: two 1 KB pieces of dY (two token rows each)
+// and two of X.
+struct BigCopy {
+    const char* dy;            // this tile's columns of the stage's first token
+    const char* xt;            // the stage's 16 KB of X
+    int64_t dy_bytes;          // extent from dy to the end of the last row
+    int64_t dy_step, xt_step;  // bytes from stage to stage
+    int64_t left;              // stages not copied yet
+    uint32_t voff_d[2], voff_x[2];
+    uint32_t wbase;
+
+    __device__ __forceinline__ void piece(uint32_t buf, int i) const {
+        if (i < 2) dma16(make_rsrc(dy, left > 0 ? dy_bytes : 0), buf + wbase + i * 1024, voff_d[i]);
+        else
+            dma16(make_rsrc(xt, left > 0 ? kBigRegion : 0),
+                  buf + kBigRegion + wbase + (i - 2) * 1024, voff_x[i - 2]);
+    }
+    __device__ __forceinline__ void next() {
+        dy += dy_step;
+        xt += xt_step;
+        dy_bytes -= dy_step;
+        --left;
+    }
+};
+
+template <typename TG>
+__global__ __launch_bounds__(kBigThreads) void k_linear_grad_big(BigArgs a) {
+    __shared__ __attribute__((aligned(1024))) char ring[kBigStages * kBigStage];
+    const Work wk = work_of(blockIdx.x, (int64_t)gridDim.x, a.tiles_n, a.tiles_k);
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wn = wave & 3, wx = wave >> 2;         // 64 outputs, 128 features each
+    const int64_t n0 = wk.tn * kBigTile, k0 = wk.tk * kBigTile;
+    const int64_t st0 = wk.slice * a.per;            // first stage of the slice
+    const int64_t all = (a.n_tokens + kLgStage - 1) / kLgStage;
+    const int nk = (int)min(a.per, all - st0);
+
+    BigCopy cp;
+    cp.dy = a.dy + (st0 * kLgStage * a.dy_stride + n0) * 2;
+    cp.dy_bytes = ((a.n_tokens - st0 * kLgStage - 1) * a.dy_stride + a.n_out - n0) * 2;
+    cp.dy_step = kLgStage * a.dy_stride * 2;
+    cp.xt = a.xt + (st0 * a.blocks_k + k0 / 32) * 2048;
+    cp.xt_step = a.blocks_k * 2048;
+    cp.left = nk;
+    cp.wbase = (uint32_t)wave * 2048u;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int row = 4 * wave + 2 * i + (lane >> 5);
+        const int chunk = (lane & 31) ^ ((row & 3) << 2);
+        cp.voff_d[i] = (uint32_t)row * (uint32_t)(a.dy_stride * 2) + (uint32_t)chunk * 16u;
+        cp.voff_x[i] = (uint32_t)(wave * 2048 + i * 1024 + lane * 16);
+    }
+    uint32_t fx[2], fd[2];
+    {
+        const int r32 = lane & 31, sw = (r32 >> 2) & 3, half = lane >> 5;
+#pragma unroll
+        for (int kg = 0; kg < 2; ++kg)
+            fx[kg] = (uint32_t)(kBigRegion + (wx * 128 + r32) * 64 + (((2 * kg + half) ^ sw) << 4));
+        const int g = lane >> 4, j = lane & 15, tsw = (j >> 2) & 3;
+        const int row = 8 * (g >> 1) + (j >> 2);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int chunk = (((wn * 2 + i) ^ tsw) << 2) + 2 * (g & 1) + ((j & 3) >> 1);
+            fd[i] = (uint32_t)(row * kBigRow + (chunk << 4) + 8 * (j & 1));
+        }
+    }
+    auto frag_x = [&](const char* buf, int kg, int i) {
+        return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(buf + fx[kg] + i * 2048));
+    };
+    auto frag_d = [&](const char* buf, int kg, int j) {
+        const char* p = buf + fd[j] + kg * 16 * kBigRow;
+        const u32x2 lo = lds_tr8(p), hi = lds_tr8(p + 4 * kBigRow);
+        return __builtin_bit_cast(bf16x8, (u32x4){lo[0], lo[1], hi[0], hi[1]});
+    };
+
+    f32x16 acc[4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+
+    const uint32_t lring = lds_addr(ring);
+#pragma unroll
+    for (int st = 0; st < kBigStages - 1; ++st) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) cp.piece(lring + st * kBigStage, i);
+        cp.next();
+    }
+    // every wave always has the copies of four stages in flight (past the
+    // slice's end they are empty), so the counts below hold for every stage
+    wait_vm12();
+    stage_barrier();
+    bf16x8 xa[4], da[2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) xa[i] = frag_x(ring, 0, i);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) da[j] = frag_d(ring, 0, j);
+
+    int slot = 0;
+#pragma unroll 1
+    for (int s = 0; s < nk; ++s) {
+        const int nslot = slot == kBigStages - 1 ? 0 : slot + 1;
+        const int tslot = slot == 0 ? kBigStages - 1 : slot - 1;    // stage s + 4
+        const char* cur = ring + slot * kBigStage;
+        const char* nxt = ring + nslot * kBigStage;
+        const uint32_t tgt = lring + tslot * kBigStage;
+        bf16x8 xb[4], db[2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            acc[i][0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(da[0], xa[i], acc[i][0], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+            xb[i] = frag_x(cur, 1, i);
+            __builtin_amdgcn_sched_barrier(0);
+            acc[i][1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(da[1], xa[i], acc[i][1], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+            if (i < 2) db[i] = frag_d(cur, 1, i);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        // stage s + 1 has landed once only those of the two after it are in flight; past
+        // the barrier every wave has read stage s - 1 to its end
+        wait_vm8();
+        stage_barrier();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            acc[i][0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(db[0], xb[i], acc[i][0], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+            cp.piece(tgt, i);
+            __builtin_amdgcn_sched_barrier(0);
+            acc[i][1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(db[1], xb[i], acc[i][1], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+            xa[i] = frag_x(nxt, 0, i);
+            __builtin_amdgcn_sched_barrier(0);
+            if (i < 2) da[i] = frag_d(nxt, 0, i);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        cp.next();
+        slot = nslot;
+    }
+
+    // (the empty copies past the end)
+    __builtin_amdgcn_s_waitcnt(0x0F70);
+    // accumulator register r of lane l: output row 8 (r / 4) + 4 (l / 32) + r % 4,
+    // feature l % 32
+    float* part = a.slices > 1 ? a.partials + wk.slice * a.n_out * a.n_in : nullptr;
+    TG* grad = static_cast<TG*>(a.grad);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t col = k0 + wx * 128 + i * 32 + (lane & 31);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int64_t row = n0 + wn * 64 + j * 32 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+                if (row >= a.n_out || col >= a.n_in) continue;
+                const int64_t o = row * a.n_in + col;
+                if (part) part[o] = acc[i][j][r];
+                else if (a.accumulate) grad[o] = (TG)((float)grad[o] + acc[i][j][r]);
+                else grad[o] = (TG)acc[i][j][r];
+            }
+        }
+}
+
 // The slices' partial sums, added in slice order.
 template <typename TG, int V>
 __global__ __launch_bounds__(kThreads) void k_linear_join(const float* __restrict__ partials,
@@ -273,62 +555,130 @@ __global__ __launch_bounds__(kThreads) void k_linear_join(const float* __restric
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
+// Time of one stage of a workgroup, its fixed cost in stages, and the float32
+// values per microsecond that partial sums are written and read back at: what the
+// number of slices is chosen by.
+struct Cost {
+    double stage_us, fixed;
+    int groups;                // workgroups that run at once
+};
+constexpr Cost kBigCost = {0.75, 16.0, kCus};
+constexpr Cost kSmallCost = {0.45, 12.0, 2 * kCus};
+constexpr double kJoinPerUs = 6e5;
+
 }  // namespace
 
-LgPlan linear_grad_plan(int64_t n_tokens, int64_t n_out, int64_t n_in, int32_t dy_dtype) {
-    (void)dy_dtype;
+bool linear_grad_big_rows(const void* dy, int64_t n_out, int64_t stride) {
+    return aligned16(dy) && n_out % 8 == 0 && stride % 8 == 0 && stride >= n_out &&
+           stride <= (int64_t(1) << 24);
+}
+
+LgPlan linear_grad_plan(int64_t n_tokens, int64_t n_out, int64_t n_in, int32_t dy_dtype,
+                        bool big_rows) {
     LgPlan p;
-    p.tile = kTile;
-    p.tiles_n = ceil_div(n_out, kTile);
-    p.tiles_k = ceil_div(n_in, kTile);
+    p.big = big_rows && dy_dtype == MA_PARAM_BF16 && n_out >= 1024 && n_in >= 256 &&
+            n_tokens >= 1024;
+    const int64_t tile = p.big ? kBigTile : kTile;
+    const Cost& c = p.big ? kBigCost : kSmallCost;
     const int64_t stages = ceil_div(n_tokens, kLgStage);
+    p.tiles_n = ceil_div(n_out, tile);
+    p.tiles_k = ceil_div(n_in, tile);
     const int64_t tiles = p.tiles_n * p.tiles_k;
-    // enough slices for two workgroups per CU, of at least 8 stages each
-    int64_t slices = std::max<int64_t>(1, std::min<int64_t>(ceil_div(2 * kCus, tiles), stages / 8));
-    p.per = std::max<int64_t>(1, ceil_div(stages, slices));
-    p.slices = std::max<int64_t>(1, ceil_div(stages, p.per));
-    if (p.slices > 1) p.total = (size_t)p.slices * (size_t)n_out * (size_t)n_in * 4;
+    const double elems = (double)n_out * (double)n_in;
+    // the slice count with the least predicted time: rounds of workgroups, each
+    // its stages and fixed cost, then the partial sums' way out and back
+    double best = 0.0;
+    p.per = std::max<int64_t>(1, stages);
+    for (int64_t n = 1; n <= 64 && n <= std::max<int64_t>(1, stages / 4); ++n) {
+        const int64_t per = ceil_div(stages, n), used = stages ? ceil_div(stages, per) : 1;
+        const double t = (double)ceil_div(tiles * used, c.groups) * (per + c.fixed) * c.stage_us +
+                         (used > 1 ? 4.0 + used * elems / kJoinPerUs : 0.0);
+        if (n == 1 || t < best) {
+            best = t;
+            p.slices = used;
+            p.per = std::max<int64_t>(1, per);
+        }
+    }
+    p.total = p.slices > 1 ? (size_t)round_up(p.slices * n_out * n_in * 4, 256) : 0;
+    if (p.big) {
+        p.xt_off = p.total;
+        p.total += (size_t)(stages * kLgStage) * (size_t)round_up(n_in, kBigTile) * 2;
+    }
     return p;
 }
 
+namespace {
+
+int launch_big(const LgArgs& a, const LgPlan& p, hipStream_t st) {
+    char* xt = reinterpret_cast<char*>(a.partials) + p.xt_off;
+    BigArgs b{};
+    b.dy = static_cast<const char*>(a.dy);
+    b.xt = xt;
+    b.grad = a.grad;
+    b.partials = a.partials;
+    b.n_tokens = a.n_tokens;
+    b.n_out = a.n_out;
+    b.n_in = a.n_in;
+    b.dy_stride = a.dy_stride;
+    b.blocks_k = round_up(a.n_in, kBigTile) / 32;
+    b.tiles_n = p.tiles_n;
+    b.tiles_k = p.tiles_k;
+    b.slices = p.slices;
+    b.per = p.per;
+    b.accumulate = a.accumulate;
+    const int64_t stages = ceil_div(a.n_tokens, kLgStage);
+    const dim3 egrid((unsigned)p.tiles_k, (unsigned)std::min<int64_t>(stages, 65535));
+    hipLaunchKernelGGL(k_lg_expand, egrid, dim3(kThreads), 0, st, a.codes, a.exps, xt, a.n_tokens,
+                       stages, act_code_pitch(a.n_in), act_exp_pitch(a.n_in), b.blocks_k);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return (int)e;
+    const dim3 grid((unsigned)(p.tiles_n * p.tiles_k * p.slices));
+    if (a.grad_dtype == MA_PARAM_BF16)
+        hipLaunchKernelGGL((k_linear_grad_big<__bf16>), grid, dim3(kBigThreads), 0, st, b);
+    else
+        hipLaunchKernelGGL((k_linear_grad_big<float>), grid, dim3(kBigThreads), 0, st, b);
+    return (int)hipGetLastError();
+}
+
+template <typename TD, bool VEC>
+int launch_small_as(const LgArgs& a, const LgPlan& p, hipStream_t st) {
+    const dim3 grid((unsigned)(p.tiles_n * p.tiles_k * p.slices));
+    if (a.grad_dtype == MA_PARAM_BF16)
+        hipLaunchKernelGGL((k_linear_grad<TD, VEC, __bf16>), grid, dim3(kThreads), 0, st, a,
+                           p.tiles_n, p.tiles_k, p.slices, p.per);
+    else
+        hipLaunchKernelGGL((k_linear_grad<TD, VEC, float>), grid, dim3(kThreads), 0, st, a,
+                           p.tiles_n, p.tiles_k, p.slices, p.per);
+    return (int)hipGetLastError();
+}
+
+int launch_small(const LgArgs& a, const LgPlan& p, hipStream_t st) {
+    const bool bf16 = a.dy_dtype == MA_PARAM_BF16;
+    const bool vec = aligned16(a.dy) && a.n_out % 8 == 0 && a.dy_stride % (bf16 ? 8 : 4) == 0;
+    if (bf16) return vec ? launch_small_as<__bf16, true>(a, p, st) : launch_small_as<__bf16, false>(a, p, st);
+    return vec ? launch_small_as<float, true>(a, p, st) : launch_small_as<float, false>(a, p, st);
+}
+
+template <typename TG, int V>
+void launch_join(const LgArgs& a, const LgPlan& p, hipStream_t st) {
+    const int64_t units = a.n_out * a.n_in / V;
+    hipLaunchKernelGGL((k_linear_join<TG, V>), dim3((unsigned)ceil_div(units, kThreads)),
+                       dim3(kThreads), 0, st, a.partials, static_cast<TG*>(a.grad), units,
+                       p.slices, a.accumulate);
+}
+
+}  // namespace
+
 int launch_linear_grad(const LgArgs& a, const LgPlan& p, void* stream) {
     hipStream_t st = (hipStream_t)stream;
-    const bool bd = a.dy_dtype == MA_PARAM_BF16, bg = a.grad_dtype == MA_PARAM_BF16;
-    const bool vec = aligned16(a.dy) && a.n_out % 8 == 0 && a.dy_stride % (bd ? 8 : 4) == 0;
-    const dim3 grid((unsigned)(p.tiles_n * p.tiles_k * p.slices));
-#define GO(TD, V, TG)                                                                           \
-    hipLaunchKernelGGL((k_linear_grad<TD, V, TG>), grid, dim3(kThreads), 0, st, a, p.tiles_n,   \
-                       p.tiles_k, p.slices, p.per)
-#define GO_G(TD, V)                                                                             \
-    do {                                                                                        \
-        if (bg) GO(TD, V, __bf16);                                                              \
-        else GO(TD, V, float);                                                                  \
-    } while (0)
-    if (bd) {
-        if (vec) GO_G(__bf16, true); else GO_G(__bf16, false);
+    const int e = p.big ? launch_big(a, p, st) : launch_small(a, p, st);
+    if (e != (int)hipSuccess || p.slices == 1) return e;
+    const bool v8 = a.n_out * a.n_in % 8 == 0 && aligned16(a.grad);
+    if (a.grad_dtype == MA_PARAM_BF16) {
+        if (v8) launch_join<__bf16, 8>(a, p, st); else launch_join<__bf16, 1>(a, p, st);
     } else {
-        if (vec) GO_G(float, true); else GO_G(float, false);
+        if (v8) launch_join<float, 8>(a, p, st); else launch_join<float, 1>(a, p, st);
     }
-#undef GO_G
-#undef GO
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || p.slices == 1) return (int)e;
-    const int64_t n = a.n_out * a.n_in;
-    const bool v8 = n % 8 == 0 && aligned16(a.grad);
-    const int64_t units = v8 ? n / 8 : n;
-    const dim3 jgrid((unsigned)ceil_div(units, kThreads));
-#define GO(TG)                                                                                  \
-    do {                                                                                        \
-        if (v8)                                                                                 \
-            hipLaunchKernelGGL((k_linear_join<TG, 8>), jgrid, dim3(kThreads), 0, st, a.partials, \
-                               static_cast<TG*>(a.grad), units, p.slices, a.accumulate);        \
-        else                                                                                    \
-            hipLaunchKernelGGL((k_linear_join<TG, 1>), jgrid, dim3(kThreads), 0, st, a.partials, \
-                               static_cast<TG*>(a.grad), units, p.slices, a.accumulate);        \
-    } while (0)
-    if (bg) GO(__bf16);
-    else GO(float);
-#undef GO
     return (int)hipGetLastError();
 }
 

@@ -284,7 +284,9 @@ def _ckpt(x):
 @pytest.mark.parametrize("m,n,k,pad", [
     (1, 1, 1, 0), (1, 256, 256, 0), (0, 40, 33, 0), (31, 16, 32, 0), (32, 128, 128, 8),
     (33, 130, 70, 1), (77, 256, 256, 0), (64, 257, 129, 0), (300, 24, 1000, 0),
-    (5000, 24, 40, 0), (2049, 264, 136, 8), (1000, 520, 300, 4), (700, 7, 8, 0)])
+    (5000, 24, 40, 0), (2049, 264, 136, 8), (1000, 520, 300, 4), (700, 7, 8, 0),
+    (1024, 1024, 256, 0), (1025, 1032, 300, 8), (2100, 1288, 513, 0), (1500, 1030, 256, 3),
+    (8191, 1024, 257, 16)])
 def test_linear_grad(td, tg, m, n, k, pad):
     rng = np.random.default_rng(m + 3 * n + 7 * k)
     dy, wide = _strided(rng.standard_normal((m, n)), pad, td)
@@ -317,6 +319,32 @@ def test_linear_grad_units(td):
     ident = M.ma_act_pack(torch.eye(m, k, device="cuda"))
     # (float32 dy: the three parts add up to it)
     assert np.array_equal(_f64(M.ma_linear_grad(dy, ident)), _f64(dy)[:k].T)
+
+
+@pytest.mark.parametrize("m", [1024, 1055])
+def test_linear_grad_large_product_values(m):
+    """The large-product kernel, value by value: one token of dy is one, so the
+    gradient's rows are that token's x; and NaN stays in its row or columns, although
+    the last stage of tokens is partly empty."""
+    n, k = 1024, 320
+    rng = np.random.default_rng(6)
+    xs = _activation(rng, m, k)
+    c, x = _ckpt(xs)
+    dy = torch.zeros((m, n), device="cuda", dtype=torch.bfloat16)
+    at = torch.from_numpy(rng.integers(0, m, n)).cuda()
+    at[-1] = m - 1
+    dy[at, torch.arange(n, device="cuda")] = 1.0
+    assert np.array_equal(_f64(M.ma_linear_grad(dy, c)), x[at.cpu().numpy()])
+    dy[m - 1, 5] = float("nan")
+    dy[m // 2, 700] = float("inf")
+    xs[m - 1, 40] = np.nan
+    c2, _ = _ckpt(xs)
+    got = _f64(M.ma_linear_grad(dy, c))
+    assert np.isnan(got[5]).all() and not np.isfinite(got[700]).any()
+    assert np.isfinite(np.delete(got, [5, 700], axis=0)).all()
+    got = _f64(M.ma_linear_grad(dy, c2))
+    assert np.isnan(got[:, 32:64]).all()
+    assert np.isfinite(np.delete(np.delete(got, [5, 700], axis=0), np.s_[32:64], axis=1)).all()
 
 
 @pytest.mark.parametrize("td", ["bf16", "fp32"])
@@ -679,6 +707,9 @@ def test_long_offsets_rows():
     want = torch.full((cols,), 5.0, device="cuda")
     want[::32] += 1.0
     assert torch.equal(g, want[:, None].expand(cols, 32))
+    wide = M.ma_act_pack(torch.ones((rows, 256), dtype=torch.bfloat16, device="cuda"))
+    assert torch.equal(M.ma_linear_grad(x, wide), want[:, None].expand(cols, 256))
+    del wide
     dy = torch.zeros((rows, 8), dtype=torch.bfloat16, device="cuda")
     dy[-1] = 1.0
     assert torch.equal(M.ma_linear_grad(dy, c), torch.full((8, cols), 5.0, device="cuda"))
