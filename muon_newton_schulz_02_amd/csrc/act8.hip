@@ -38,30 +38,19 @@ __device__ __forceinline__ Unit unit_at(int64_t u, uint32_t upr) {
 }
 
 // 8 features from column `col` on, zeros past the last column.
-template <typename T, bool VEC>
+template <typename T, bool AL>
 __device__ __forceinline__ void load8(const T* row, int col, int cols, float* v) {
-    if (VEC) {
-        if (col < cols) {
-            load_v<T, 8>(row + col, v);
-            return;
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = 0.f;
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = col + e < cols ? (float)row[col + e] : 0.f;
+    if (col < cols) {
+        load_unit<T, AL>(row + col, cols - col, v);
+        return;
     }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = 0.f;
 }
 
-template <typename T, bool VEC>
+template <typename T, bool AL>
 __device__ __forceinline__ void store8(T* row, int col, int cols, const float* v) {
-    if (VEC) {
-        if (col < cols) store_v<T, 8>(row + col, v);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (col + e < cols) row[col + e] = (T)v[e];
-    }
+    if (col < cols) store_unit<T, AL>(row + col, cols - col, v);
 }
 
 // Hold 8 features of each lane: codes and exponent byte of its group of four
@@ -98,7 +87,7 @@ __device__ __forceinline__ void held8(const int8_t* codes, const uint8_t* exps, 
     }
 }
 
-template <typename T, bool VEC>
+template <typename T, bool AL>
 __global__ __launch_bounds__(kThreads) void k_act_pack(const T* __restrict__ x, int64_t stride,
                                                        int8_t* __restrict__ codes,
                                                        uint8_t* __restrict__ exps, int cols,
@@ -110,12 +99,12 @@ __global__ __launch_bounds__(kThreads) void k_act_pack(const T* __restrict__ x, 
          u += (int64_t)gridDim.x * kThreads) {
         const Unit at = unit_at(u, upr);
         float v[8];
-        load8<T, VEC>(x + at.row * stride, at.col, cols, v);
+        load8<T, AL>(x + at.row * stride, at.col, cols, v);
         hold8(v, codes, exps, at.row, at.col, code_pitch, exp_pitch);
     }
 }
 
-template <typename T, bool VEC>
+template <typename T, bool AL>
 __global__ __launch_bounds__(kThreads) void k_act_unpack(const int8_t* __restrict__ codes,
                                                          const uint8_t* __restrict__ exps,
                                                          T* __restrict__ out, int64_t stride,
@@ -126,7 +115,7 @@ __global__ __launch_bounds__(kThreads) void k_act_unpack(const int8_t* __restric
         const Unit at = unit_at(u, upr);
         float v[8];
         held8(codes, exps, at.row, at.col, code_pitch, exp_pitch, v);
-        store8<T, VEC>(out + at.row * stride, at.col, cols, v);
+        store8<T, AL>(out + at.row * stride, at.col, cols, v);
     }
 }
 
@@ -154,7 +143,7 @@ __device__ __forceinline__ float act_slope(float g, float s) {
     return p > 0.f ? fmaf(p, g * da, s) : s;
 }
 
-template <typename T, bool VEC, int ACT>
+template <typename T, bool AL, int ACT>
 __global__ __launch_bounds__(kThreads) void k_glu_forward(GluArgs a, int cols, int code_pitch,
                                                           int exp_pitch, uint32_t upr,
                                                           int64_t units) {
@@ -165,17 +154,17 @@ __global__ __launch_bounds__(kThreads) void k_glu_forward(GluArgs a, int cols, i
          u += (int64_t)gridDim.x * kThreads) {
         const Unit at = unit_at(u, upr);
         float gv[8], uv[8], hv[8];
-        load8<T, VEC>(gate + at.row * a.gate_stride, at.col, cols, gv);
-        load8<T, VEC>(up + at.row * a.up_stride, at.col, cols, uv);
+        load8<T, AL>(gate + at.row * a.gate_stride, at.col, cols, gv);
+        load8<T, AL>(up + at.row * a.up_stride, at.col, cols, uv);
 #pragma unroll
         for (int e = 0; e < 8; ++e) hv[e] = gv[e] * act_sig<ACT>(gv[e]) * uv[e];
-        store8<T, VEC>(h + at.row * a.h_stride, at.col, cols, hv);
+        store8<T, AL>(h + at.row * a.h_stride, at.col, cols, hv);
         hold8(gv, a.gate_codes, a.gate_exps, at.row, at.col, code_pitch, exp_pitch);
         hold8(uv, a.up_codes, a.up_exps, at.row, at.col, code_pitch, exp_pitch);
     }
 }
 
-template <typename T, bool VEC, int ACT, bool HOLD>
+template <typename T, bool AL, int ACT, bool HOLD>
 __global__ __launch_bounds__(kThreads) void k_glu_backward(GluArgs a, int cols, int code_pitch,
                                                            int exp_pitch, uint32_t upr,
                                                            int64_t units) {
@@ -193,20 +182,20 @@ __global__ __launch_bounds__(kThreads) void k_glu_backward(GluArgs a, int cols, 
 #pragma unroll
             for (int e = 0; e < 8; ++e) gv[e] = uv[e] = 0.f;
         }
-        load8<T, VEC>(dh + at.row * a.dh_stride, at.col, cols, dv);
+        load8<T, AL>(dh + at.row * a.dh_stride, at.col, cols, dv);
         float sv[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) sv[e] = act_sig<ACT>(gv[e]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] = dv[e] * uv[e] * act_slope<ACT>(gv[e], sv[e]);
-        store8<T, VEC>(dgate + at.row * a.dgate_stride, at.col, cols, o);
+        store8<T, AL>(dgate + at.row * a.dgate_stride, at.col, cols, o);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const float av = gv[e] * sv[e];
             o[e] = dv[e] * av;
             hv[e] = at.col + e < cols ? av * uv[e] : 0.f;
         }
-        store8<T, VEC>(dup + at.row * a.dup_stride, at.col, cols, o);
+        store8<T, AL>(dup + at.row * a.dup_stride, at.col, cols, o);
         if (HOLD) hold8(hv, a.h_codes, a.h_exps, at.row, at.col, code_pitch, exp_pitch);
     }
 }
@@ -221,7 +210,7 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 
 
 // 16-byte accesses to rows of 8-element units: every row starts 16-byte aligned
 // and holds whole units.
-bool vec_rows(const void* p, int64_t stride, int64_t cols, int32_t dtype) {
+bool al_rows(const void* p, int64_t stride, int64_t cols, int32_t dtype) {
     const int64_t per = dtype == MA_PARAM_BF16 ? 8 : 4;
     return aligned16(p) && stride % per == 0 && cols % 8 == 0;
 }
@@ -234,15 +223,15 @@ int launch_act_pack(const void* x, int32_t dtype, int64_t rows, int64_t cols, in
     const int cp = (int)act_code_pitch(cols), ep = (int)act_exp_pitch(cols);
     const uint32_t upr = (uint32_t)ep * 4;
     const int64_t units = rows * upr;
-    const bool vec = vec_rows(x, stride, cols, dtype);
+    const bool al = al_rows(x, stride, cols, dtype);
     const dim3 grid((unsigned)stream_grid(units));
 #define GO(T, V)                                                                               \
     hipLaunchKernelGGL((k_act_pack<T, V>), grid, dim3(kThreads), 0, (hipStream_t)stream,        \
                        static_cast<const T*>(x), stride, codes, exps, (int)cols, cp, ep, upr, units)
     if (dtype == MA_PARAM_BF16) {
-        if (vec) GO(__bf16, true); else GO(__bf16, false);
+        if (al) GO(__bf16, true); else GO(__bf16, false);
     } else {
-        if (vec) GO(float, true); else GO(float, false);
+        if (al) GO(float, true); else GO(float, false);
     }
 #undef GO
     return (int)hipGetLastError();
@@ -254,15 +243,15 @@ int launch_act_unpack(const int8_t* codes, const uint8_t* exps, int64_t rows, in
     const int cp = (int)act_code_pitch(cols), ep = (int)act_exp_pitch(cols);
     const uint32_t upr = (uint32_t)cp / 8;
     const int64_t units = rows * upr;
-    const bool vec = vec_rows(out, stride, cols, dtype);
+    const bool al = al_rows(out, stride, cols, dtype);
     const dim3 grid((unsigned)stream_grid(units));
 #define GO(T, V)                                                                               \
     hipLaunchKernelGGL((k_act_unpack<T, V>), grid, dim3(kThreads), 0, (hipStream_t)stream,      \
                        codes, exps, static_cast<T*>(out), stride, (int)cols, cp, ep, upr, units)
     if (dtype == MA_PARAM_BF16) {
-        if (vec) GO(__bf16, true); else GO(__bf16, false);
+        if (al) GO(__bf16, true); else GO(__bf16, false);
     } else {
-        if (vec) GO(float, true); else GO(float, false);
+        if (al) GO(float, true); else GO(float, false);
     }
 #undef GO
     return (int)hipGetLastError();
@@ -273,9 +262,9 @@ int launch_glu_forward(const GluArgs& a, void* stream) {
     const int cp = (int)act_code_pitch(a.cols), ep = (int)act_exp_pitch(a.cols);
     const uint32_t upr = (uint32_t)ep * 4;
     const int64_t units = a.rows * upr;
-    const bool vec = vec_rows(a.gate, a.gate_stride, a.cols, a.dtype) &&
-                     vec_rows(a.up, a.up_stride, a.cols, a.dtype) &&
-                     vec_rows(a.h, a.h_stride, a.cols, a.dtype);
+    const bool al = al_rows(a.gate, a.gate_stride, a.cols, a.dtype) &&
+                     al_rows(a.up, a.up_stride, a.cols, a.dtype) &&
+                     al_rows(a.h, a.h_stride, a.cols, a.dtype);
     const dim3 grid((unsigned)stream_grid(units));
 #define GO(T, V, A)                                                                            \
     hipLaunchKernelGGL((k_glu_forward<T, V, A>), grid, dim3(kThreads), 0, (hipStream_t)stream, a, \
@@ -286,9 +275,9 @@ int launch_glu_forward(const GluArgs& a, void* stream) {
         else GO(T, V, MA_ACT_GELU_TANH);                                                       \
     } while (0)
     if (a.dtype == MA_PARAM_BF16) {
-        if (vec) GO_ACT(__bf16, true); else GO_ACT(__bf16, false);
+        if (al) GO_ACT(__bf16, true); else GO_ACT(__bf16, false);
     } else {
-        if (vec) GO_ACT(float, true); else GO_ACT(float, false);
+        if (al) GO_ACT(float, true); else GO_ACT(float, false);
     }
 #undef GO_ACT
 #undef GO
@@ -301,9 +290,9 @@ int launch_glu_backward(const GluArgs& a, void* stream) {
     const bool hold = a.h_codes != nullptr;
     const uint32_t upr = hold ? (uint32_t)ep * 4 : (uint32_t)cp / 8;
     const int64_t units = a.rows * upr;
-    const bool vec = vec_rows(a.dh, a.dh_stride, a.cols, a.dtype) &&
-                     vec_rows(a.dgate, a.dgate_stride, a.cols, a.dtype) &&
-                     vec_rows(a.dup, a.dup_stride, a.cols, a.dtype);
+    const bool al = al_rows(a.dh, a.dh_stride, a.cols, a.dtype) &&
+                     al_rows(a.dgate, a.dgate_stride, a.cols, a.dtype) &&
+                     al_rows(a.dup, a.dup_stride, a.cols, a.dtype);
     const dim3 grid((unsigned)stream_grid(units));
 #define GO(T, V, A, H)                                                                          \
     hipLaunchKernelGGL((k_glu_backward<T, V, A, H>), grid, dim3(kThreads), 0, (hipStream_t)stream, \
@@ -319,9 +308,9 @@ int launch_glu_backward(const GluArgs& a, void* stream) {
         else GO_ACT(T, V, false);                                                              \
     } while (0)
     if (a.dtype == MA_PARAM_BF16) {
-        if (vec) GO_HOLD(__bf16, true); else GO_HOLD(__bf16, false);
+        if (al) GO_HOLD(__bf16, true); else GO_HOLD(__bf16, false);
     } else {
-        if (vec) GO_HOLD(float, true); else GO_HOLD(float, false);
+        if (al) GO_HOLD(float, true); else GO_HOLD(float, false);
     }
 #undef GO_HOLD
 #undef GO_ACT

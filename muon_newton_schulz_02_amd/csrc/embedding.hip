@@ -9,12 +9,20 @@
 // equal rows inside one chunk is summed in registers and written; the pieces
 // of a run that crosses chunks go to the workspace as float32 partial sums,
 // and a last launch adds them in order.  Rows without a token are zeroed by
-// further workgroups of the chunk launch.  No atomic touches a sum, so reruns
-// are bitwise equal.
+// further workgroups of the chunk launch, told by one flag byte per row that
+// the sort leaves.  No atomic touches a sum, so reruns are bitwise equal.
+//
+// Three sizes of sort: up to kDirectTokens tokens none at all (one launch, in which
+// every workgroup picks its own few rows' tokens out of all of them); up to
+// kLdsSortTokens one workgroup sorts in its LDS; above, passes over many
+// workgroups.
+//
+// A row is handled in units of 8 columns, one thread each.
 
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "grads_device.h"
 #include "grads_internal.h"
@@ -30,13 +38,13 @@ constexpr int kThreads = 256;
 // gathered rows are in flight per thread.
 constexpr int kLookRows = 4;
 
-template <typename TI, typename TO, typename TOK, int V>
+template <typename TI, typename TO, typename TOK, bool AL>
 __global__ __launch_bounds__(kThreads) void k_emb_lookup(const TI* __restrict__ table,
                                                          int64_t table_stride, int64_t vocab,
                                                          const TOK* __restrict__ tokens,
                                                          int64_t n, float scale,
                                                          TO* __restrict__ out, int64_t out_stride,
-                                                         int units, int lane_bits) {
+                                                         int hidden, int lane_bits) {
     const int lanes = 1 << lane_bits, per = kThreads >> lane_bits;
     const int lane = threadIdx.x & (lanes - 1), sub = threadIdx.x >> lane_bits;
     const int64_t t0 = (int64_t)blockIdx.x * per * kLookRows + sub;
@@ -50,15 +58,15 @@ __global__ __launch_bounds__(kThreads) void k_emb_lookup(const TI* __restrict__ 
             if (row[r] < 0 || row[r] >= vocab) row[r] = -1;
         }
     }
-    for (int u = lane; u < units; u += lanes) {
-        float v[kLookRows][V];
+    for (int col = lane * 8; col < hidden; col += lanes * 8) {
+        float v[kLookRows][8];
 #pragma unroll
         for (int r = 0; r < kLookRows; ++r) {
             if (row[r] >= 0) {
-                load_v<TI, V>(table + row[r] * table_stride + (int64_t)u * V, v[r]);
+                load_unit<TI, AL>(table + row[r] * table_stride + col, hidden - col, v[r]);
             } else {
 #pragma unroll
-                for (int e = 0; e < V; ++e) v[r][e] = 0.f;
+                for (int e = 0; e < 8; ++e) v[r][e] = 0.f;
             }
         }
 #pragma unroll
@@ -67,9 +75,9 @@ __global__ __launch_bounds__(kThreads) void k_emb_lookup(const TI* __restrict__ 
             if (t >= n) continue;
             if (row[r] >= 0) {
 #pragma unroll
-                for (int e = 0; e < V; ++e) v[r][e] *= scale;
+                for (int e = 0; e < 8; ++e) v[r][e] *= scale;
             }
-            store_v<TO, V>(out + t * out_stride + (int64_t)u * V, v[r]);
+            store_unit<TO, AL>(out + t * out_stride + col, hidden - col, v[r]);
         }
     }
 }
@@ -85,7 +93,8 @@ __device__ __forceinline__ uint32_t token_key(const TOK* tokens, int64_t i, int6
 }
 
 constexpr int kMaxDigits = 1024;    // digits of a pass: at most 10 bits
-constexpr int kSortWaves = kThreads / 64;
+constexpr int kSortThreads = 1024;
+constexpr int kSortWaves = kSortThreads / 64;
 
 // Where a pass reads its keys and positions: the tokens themselves (pass 0) or
 // the previous pass's output.
@@ -93,6 +102,7 @@ struct SortIn {
     const void* tokens;
     const uint32_t* keys;
     const int32_t* pos;
+    uint8_t* flags;         // one byte per table row: has it a token?
     int64_t n, vocab, pad;
     int32_t token_bytes;    // 4, 8; 0: keys and pos
     int32_t shift, bits;
@@ -105,31 +115,31 @@ __device__ __forceinline__ uint32_t sort_key(const SortIn& s, int64_t i) {
     return s.keys[i];
 }
 
-// Digit counts of each block's entries: counts[block][digit].
-__global__ __launch_bounds__(kThreads) void k_sort_count(SortIn s, uint32_t* __restrict__ counts) {
+// Digit counts of each block's entries: counts[block][digit].  The first pass
+// also clears the flags.
+__global__ __launch_bounds__(kSortThreads) void k_sort_count(SortIn s, uint32_t* __restrict__ counts) {
     __shared__ uint32_t hist[kMaxDigits];
     const int nd = 1 << s.bits;
-    for (int d = threadIdx.x; d < nd; d += kThreads) hist[d] = 0;
+    for (int d = threadIdx.x; d < nd; d += kSortThreads) hist[d] = 0;
     __syncthreads();
     const int64_t i0 = (int64_t)blockIdx.x * s.per, i1 = min(s.n, i0 + s.per);
-    for (int64_t i = i0 + threadIdx.x; i < i1; i += kThreads)
+    for (int64_t i = i0 + threadIdx.x; i < i1; i += kSortThreads)
         atomicAdd(&hist[(sort_key(s, i) >> s.shift) & (nd - 1)], 1u);
+    if (s.token_bytes) {
+        // (the flags' memory is 16-byte aligned and padded to 16)
+        for (int64_t v = ((int64_t)blockIdx.x * kSortThreads + threadIdx.x) * 16; v < s.vocab;
+             v += (int64_t)gridDim.x * kSortThreads * 16)
+            *reinterpret_cast<u32x4*>(s.flags + v) = (u32x4){0u, 0u, 0u, 0u};
+    }
     __syncthreads();
-    for (int d = threadIdx.x; d < nd; d += kThreads)
+    for (int d = threadIdx.x; d < nd; d += kSortThreads)
         counts[(int64_t)blockIdx.x * nd + d] = hist[d];
 }
 
-// Exclusive prefix of val[0 .. nd) into val, by one block.
-__device__ __forceinline__ void block_prefix(uint32_t* val, int nd, uint32_t* wave_sum) {
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int nt = (int)blockDim.x;
-    const int per = (nd + nt - 1) / nt;
-    uint32_t sum = 0;
-    for (int k = 0; k < per; ++k) {
-        const int d = tid * per + k;
-        if (d < nd) sum += val[d];
-    }
-    uint32_t inc = sum;
+// Exclusive prefix over the digits, digit `tid` each (nd <= kSortThreads).
+__device__ __forceinline__ uint32_t digit_prefix(uint32_t count, uint32_t* wave_sum) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    uint32_t inc = count;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
         const uint32_t o = (uint32_t)__shfl_up((int)inc, off, 64);
@@ -137,17 +147,10 @@ __device__ __forceinline__ void block_prefix(uint32_t* val, int nd, uint32_t* wa
     }
     if (lane == 63) wave_sum[wave] = inc;
     __syncthreads();
-    uint32_t base = inc - sum;
-    for (int w = 0; w < wave; ++w) base += wave_sum[w];
-    for (int k = 0; k < per; ++k) {
-        const int d = tid * per + k;
-        if (d < nd) {
-            const uint32_t c = val[d];
-            val[d] = base;
-            base += c;
-        }
-    }
-    __syncthreads();
+    uint32_t base = 0;
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) base += w < wave ? wave_sum[w] : 0u;
+    return base + inc - count;
 }
 
 // Lanes of this wave whose (valid) digit equals this lane's.
@@ -160,15 +163,34 @@ __device__ __forceinline__ uint64_t same_digit(uint32_t digit, int bits, bool va
     return m;
 }
 
+__device__ __forceinline__ void wave_lds_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// Place of a lane's entry among its wave's entries of the same digit so far
+// (`count`: this wave's counters), which it joins.
+__device__ __forceinline__ uint32_t wave_rank(uint32_t* count, uint32_t digit, int bits, bool valid) {
+    const int lane = threadIdx.x & 63;
+    const uint64_t peers = same_digit(digit, bits, valid);
+    const uint32_t rank = (uint32_t)__popcll(peers & ((uint64_t(1) << lane) - 1));
+    const uint32_t base = valid ? count[digit] : 0u;
+    // every lane has read the counter before the last of its peers moves it on
+    wave_lds_sync();
+    if (valid && (peers >> lane) == 1u) count[digit] = base + rank + 1u;
+    wave_lds_sync();
+    return base + rank;
+}
+
 // Stable scatter of each block's entries to their sorted places: the entries of
 // a digit go after those of smaller digits, then of earlier blocks, then of
 // earlier waves (each wave owns a contiguous part of the block's range and
-// walks it 64 entries at a time).
-__global__ __launch_bounds__(kThreads) void k_sort_scatter(SortIn s,
-                                                           const uint32_t* __restrict__ counts,
-                                                           uint32_t* __restrict__ keys_out,
-                                                           int32_t* __restrict__ pos_out) {
-    __shared__ uint32_t total[kMaxDigits];
+// walks it 64 entries at a time).  The first pass also sets the flags.
+__global__ __launch_bounds__(kSortThreads) void k_sort_scatter(SortIn s,
+                                                               const uint32_t* __restrict__ counts,
+                                                               uint32_t* __restrict__ keys_out,
+                                                               int32_t* __restrict__ pos_out) {
     __shared__ uint32_t next[kSortWaves][kMaxDigits];
     __shared__ uint32_t wave_sum[kSortWaves];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -176,62 +198,120 @@ __global__ __launch_bounds__(kThreads) void k_sort_scatter(SortIn s,
     const int64_t i0 = (int64_t)blockIdx.x * s.per, i1 = min(s.n, i0 + s.per);
     const int64_t part = (s.per + kSortWaves - 1) / kSortWaves;
     const int64_t w0 = min(i1, i0 + wave * part), w1 = min(i1, w0 + part);
-    for (int d = lane; d < nd; d += 64) next[wave][d] = 0;
-    __syncthreads();
-    for (int64_t i = w0 + lane; i < w1; i += 64)
-        atomicAdd(&next[wave][(sort_key(s, i) >> s.shift) & (nd - 1)], 1u);
-    // over all blocks: totals per digit, and what earlier blocks hold of it
-    uint32_t before[kMaxDigits / kThreads];
-#pragma unroll
-    for (int k = 0; k < kMaxDigits / kThreads; ++k) {
-        before[k] = 0;
-        const int d = k * kThreads + tid;
-        if (d >= nd) continue;
-        uint32_t all = 0;
+    // over all blocks: total of this thread's digit, and what earlier blocks hold of it
+    uint32_t all = 0, before = 0;
+    if (tid < nd) {
 #pragma unroll 8
         for (int b = 0; b < (int)gridDim.x; ++b) {
-            const uint32_t c = counts[(int64_t)b * nd + d];
+            const uint32_t c = counts[(int64_t)b * nd + tid];
             all += c;
-            if (b < (int)blockIdx.x) before[k] += c;
+            before += b < (int)blockIdx.x ? c : 0u;
         }
-        total[d] = all;
     }
-    __syncthreads();
-    block_prefix(total, nd, wave_sum);
-#pragma unroll
-    for (int k = 0; k < kMaxDigits / kThreads; ++k) {
-        const int d = k * kThreads + tid;
-        if (d >= nd) continue;
-        uint32_t at = total[d] + before[k];
+    for (int d = lane; d < nd; d += 64) next[wave][d] = 0;
+    wave_lds_sync();
+    for (int64_t i = w0 + lane; i < w1; i += 64)
+        atomicAdd(&next[wave][(sort_key(s, i) >> s.shift) & (nd - 1)], 1u);
+    const uint32_t start = digit_prefix(all, wave_sum);     // (a barrier: all counts are in)
+    if (tid < nd) {
+        uint32_t at = start + before;
 #pragma unroll
         for (int w = 0; w < kSortWaves; ++w) {
-            const uint32_t c = next[w][d];
-            next[w][d] = at;
+            const uint32_t c = next[w][tid];
+            next[w][tid] = at;
             at += c;
         }
     }
     __syncthreads();
-    // (the loop is uniform over the wave; `next` is this wave's own)
+    // (the loop is uniform over the wave; next[wave] is this wave's own)
     for (int64_t i = w0; i < w1; i += 64) {
         const bool valid = i + lane < w1;
         const uint32_t key = valid ? sort_key(s, i + lane) : 0u;
         const int32_t pos = valid ? (s.token_bytes ? (int32_t)(i + lane) : s.pos[i + lane]) : 0;
-        const uint32_t digit = (key >> s.shift) & (uint32_t)(nd - 1);
-        const uint64_t peers = same_digit(digit, s.bits, valid);
-        const int rank = __popcll(peers & ((uint64_t(1) << lane) - 1));
+        const uint32_t at = wave_rank(next[wave], (key >> s.shift) & (uint32_t)(nd - 1), s.bits, valid);
         if (valid) {
-            const uint32_t at = next[wave][digit] + (uint32_t)rank;
             keys_out[at] = key;
             pos_out[at] = pos;
+            if (s.token_bytes && key < (uint32_t)s.vocab) s.flags[key] = 1;
         }
-        // every lane has read its digit's place before the last peer moves it on
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-        if (valid && (peers >> lane) == 1u) next[wave][digit] += (uint32_t)rank + 1u;
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    }
+}
+
+// The whole sort of at most 1024 * ROUNDS tokens by one workgroup: entries in
+// registers, all passes through LDS.
+template <int ROUNDS>
+__global__ __launch_bounds__(kSortThreads) void k_sort_lds(SortIn s, int passes,
+                                                           uint32_t* __restrict__ keys_out,
+                                                           int32_t* __restrict__ pos_out) {
+    __shared__ uint32_t keys[kSortThreads * ROUNDS];
+    __shared__ uint16_t poss[kSortThreads * ROUNDS];
+    __shared__ uint32_t next[kSortWaves][kMaxDigits];
+    __shared__ uint32_t wave_sum[kSortWaves];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int nd = 1 << s.bits, n = (int)s.n;
+    for (int64_t v = (int64_t)tid * 16; v < s.vocab; v += kSortThreads * 16)
+        *reinterpret_cast<u32x4*>(s.flags + v) = (u32x4){0u, 0u, 0u, 0u};
+    uint32_t key[ROUNDS], at[ROUNDS];
+    int pos[ROUNDS];
+#pragma unroll
+    for (int r = 0; r < ROUNDS; ++r) {
+        const int i = (wave * ROUNDS + r) * 64 + lane;
+        key[r] = i < n ? sort_key(s, i) : 0u;
+        pos[r] = i;
+    }
+    __syncthreads();              // (the flags are cleared before any is set)
+#pragma unroll
+    for (int r = 0; r < ROUNDS; ++r)
+        if ((wave * ROUNDS + r) * 64 + lane < n && key[r] < (uint32_t)s.vocab) s.flags[key[r]] = 1;
+    for (int p = 0; p < passes; ++p) {
+        const int shift = p * s.bits;
+        for (int d = lane; d < nd; d += 64) next[wave][d] = 0;
+        wave_lds_sync();
+#pragma unroll
+        for (int r = 0; r < ROUNDS; ++r)
+            at[r] = wave_rank(next[wave], (key[r] >> shift) & (uint32_t)(nd - 1), s.bits,
+                              (wave * ROUNDS + r) * 64 + lane < n);
+        __syncthreads();
+        uint32_t all = 0;
+        if (tid < nd) {
+#pragma unroll
+            for (int w = 0; w < kSortWaves; ++w) all += next[w][tid];
+        }
+        uint32_t start = digit_prefix(all, wave_sum);
+        if (tid < nd) {
+#pragma unroll
+            for (int w = 0; w < kSortWaves; ++w) {
+                const uint32_t c = next[w][tid];
+                next[w][tid] = start;
+                start += c;
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < ROUNDS; ++r) {
+            if ((wave * ROUNDS + r) * 64 + lane < n) {
+                const uint32_t to = next[wave][(key[r] >> shift) & (uint32_t)(nd - 1)] + at[r];
+                keys[to] = key[r];
+                poss[to] = (uint16_t)pos[r];
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < ROUNDS; ++r) {
+            const int i = (wave * ROUNDS + r) * 64 + lane;
+            if (i < n) {
+                key[r] = keys[i];
+                pos[r] = poss[i];
+            }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < ROUNDS; ++r) {
+        const int i = (wave * ROUNDS + r) * 64 + lane;
+        if (i < n) {
+            keys_out[i] = key[r];
+            pos_out[i] = pos[r];
+        }
     }
 }
 
@@ -239,18 +319,23 @@ __global__ __launch_bounds__(kThreads) void k_sort_scatter(SortIn s,
 struct SumArgs {
     const void* dout;
     void* grad;
-    float* partials;              // [n_chunks][2][hidden]: head, tail
+    float* partials;              // [n_chunks][2][pitch]: head, tail
     const uint32_t* keys;
     const int32_t* pos;
-    int64_t dout_stride, n, vocab, hidden, chunk, n_chunks;
+    const uint8_t* flags;
+    int64_t dout_stride, n, vocab, n_chunks;
     int64_t sum_blocks;           // workgroups before those that zero rows
+    int64_t pitch;                // of a partial row: hidden rounded up to 8
     float scale;
     int32_t accumulate;
-    int32_t units, lane_bits;     // column units of a row, and lanes (log2) that take them
+    int32_t hidden, chunk;
+    int32_t lane_bits;            // lanes (log2) that take a row
 };
 
 constexpr int kFillRows = 32;     // rows a zeroing workgroup looks at
 constexpr int kSumDepth = 8;      // rows of dout in flight per thread
+constexpr int kMaxChunk = 256;
+constexpr int kMinSumLanes = 32;  // so a workgroup holds at most 8 chunks
 
 // First sorted entry whose key is at least `key`.
 __device__ __forceinline__ int64_t lower_bound(const uint32_t* keys, int64_t n, uint32_t key) {
@@ -263,170 +348,329 @@ __device__ __forceinline__ int64_t lower_bound(const uint32_t* keys, int64_t n, 
     return lo;
 }
 
-template <typename TG, int V>
-__device__ __forceinline__ void write_row(const SumArgs& a, uint32_t key, int64_t col, float* acc) {
+template <typename TG, bool AL>
+__device__ __forceinline__ void write_row(const SumArgs& a, uint32_t key, int col, float* acc) {
     TG* g = static_cast<TG*>(a.grad) + (int64_t)key * a.hidden + col;
-    float old[V];
-    if (a.accumulate) load_v<TG, V>(g, old);
+    if (a.accumulate) {
+        float old[8];
+        load_unit<TG, AL>(g, a.hidden - col, old);
 #pragma unroll
-    for (int e = 0; e < V; ++e) acc[e] = a.accumulate ? fmaf(acc[e], a.scale, old[e]) : acc[e] * a.scale;
-    store_v<TG, V>(g, acc);
+        for (int e = 0; e < 8; ++e) acc[e] = fmaf(acc[e], a.scale, old[e]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] *= a.scale;
+    }
+    store_unit<TG, AL>(g, a.hidden - col, acc);
+}
+
+template <typename TG, bool AL>
+__device__ __forceinline__ void zero_row(TG* g, int hidden, int first, int step) {
+    const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int col = first * 8; col < hidden; col += step * 8)
+        store_unit<TG, AL>(g + col, hidden - col, zero);
+}
+
+// acc += rows at[0 .. cnt) of dout from column `col` on, in order, kSumDepth at a time.
+template <typename TD, bool AL, typename AT>
+__device__ __forceinline__ void add_rows(float* acc, const TD* dout, int64_t stride, int hidden,
+                                         int col, const AT* at, int cnt) {
+    for (int i = 0; i < cnt; i += kSumDepth) {
+        float v[kSumDepth][8];
+#pragma unroll
+        for (int k = 0; k < kSumDepth; ++k)
+            if (i + k < cnt) load_unit<TD, AL>(dout + (int64_t)at[i + k] * stride + col, hidden - col, v[k]);
+#pragma unroll
+        for (int k = 0; k < kSumDepth; ++k) {
+            if (i + k >= cnt) break;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[e] += v[k][e];
+        }
+    }
 }
 
 // Workgroups [0, sum_blocks): the chunks; the rest: rows without a token.
-template <typename TD, typename TG, int V>
+template <typename TD, typename TG, bool AL>
 __global__ __launch_bounds__(kThreads) void k_emb_sum(SumArgs a) {
+    __shared__ uint32_t s_key[kThreads / kMinSumLanes][kMaxChunk];
+    __shared__ int32_t s_pos[kThreads / kMinSumLanes][kMaxChunk];
     if ((int64_t)blockIdx.x >= a.sum_blocks) {
-        __shared__ int empty[kFillRows];
         const int64_t r0 = ((int64_t)blockIdx.x - a.sum_blocks) * kFillRows;
-        if (threadIdx.x < kFillRows) {
-            const int64_t r = r0 + threadIdx.x;
-            int e = 0;
-            if (r < a.vocab) {
-                const int64_t at = lower_bound(a.keys, a.n, (uint32_t)r);
-                e = at >= a.n || a.keys[at] != (uint32_t)r;
-            }
-            empty[threadIdx.x] = e;
-        }
-        __syncthreads();
-        const float zero[V] = {};
-        for (int r = 0; r < kFillRows; ++r) {
-            if (!empty[r]) continue;
-            TG* g = static_cast<TG*>(a.grad) + (r0 + r) * a.hidden;
-            for (int u = threadIdx.x; u < a.units; u += kThreads) store_v<TG, V>(g + (int64_t)u * V, zero);
-        }
+        const int rows = (int)min<int64_t>(kFillRows, a.vocab - r0);
+        // (without any token there are no flags: every row is empty)
+        for (int r = 0; r < rows; ++r)
+            if (a.n == 0 || a.flags[r0 + r] == 0)
+                zero_row<TG, AL>(static_cast<TG*>(a.grad) + (r0 + r) * a.hidden, a.hidden, threadIdx.x, kThreads);
         return;
     }
     const int lanes = 1 << a.lane_bits, per = kThreads >> a.lane_bits;
     const int lane = threadIdx.x & (lanes - 1), sub = threadIdx.x >> a.lane_bits;
     const int64_t c = (int64_t)blockIdx.x * per + sub;
-    if (c >= a.n_chunks) return;
-    const int64_t i0 = c * a.chunk, i1 = min(a.n, i0 + a.chunk);
-    const uint32_t first = a.keys[i0], last = a.keys[i1 - 1];
-    const uint32_t none = (uint32_t)a.vocab;
+    const int64_t i0 = c * a.chunk;
+    const int cnt = c < a.n_chunks ? (int)min<int64_t>(a.chunk, a.n - i0) : 0;
+    for (int i = lane; i < cnt; i += lanes) {
+        s_key[sub][i] = a.keys[i0 + i];
+        s_pos[sub][i] = a.pos[i0 + i];
+    }
+    __syncthreads();
+    if (cnt == 0) return;
+    const uint32_t* key = s_key[sub];
+    const int32_t* pos = s_pos[sub];
+    const uint32_t first = key[0], last = key[cnt - 1], none = (uint32_t)a.vocab;
     const bool from_before = i0 > 0 && a.keys[i0 - 1] == first;
-    const bool goes_on = i1 < a.n && a.keys[i1] == last;
+    const bool goes_on = i0 + cnt < a.n && a.keys[i0 + cnt] == last;
     const TD* dout = static_cast<const TD*>(a.dout);
-    for (int u = lane; u < a.units; u += lanes) {
-        const int64_t col = (int64_t)u * V;
-        float acc[V];
+    for (int col = lane * 8; col < a.hidden; col += lanes * 8) {
+        float acc[8];
 #pragma unroll
-        for (int e = 0; e < V; ++e) acc[e] = 0.f;
+        for (int e = 0; e < 8; ++e) acc[e] = 0.f;
         uint32_t cur = first;
         bool head = from_before;      // the current run began in an earlier chunk
-        for (int64_t i = i0; i < i1; i += kSumDepth) {
-            uint32_t key[kSumDepth];
-            float v[kSumDepth][V];
+        float* part = a.partials + c * 2 * a.pitch + col;
+        for (int i = 0; i < cnt && key[i] != none; i += kSumDepth) {
+            float v[kSumDepth][8];
+#pragma unroll
+            for (int k = 0; k < kSumDepth; ++k)
+                if (i + k < cnt && key[i + k] != none)
+                    load_unit<TD, AL>(dout + (int64_t)pos[i + k] * a.dout_stride + col, a.hidden - col, v[k]);
 #pragma unroll
             for (int k = 0; k < kSumDepth; ++k) {
-                key[k] = i + k < i1 ? a.keys[i + k] : none;
-                if (key[k] != none)
-                    load_v<TD, V>(dout + (int64_t)a.pos[i + k] * a.dout_stride + col, v[k]);
-            }
-#pragma unroll
-            for (int k = 0; k < kSumDepth; ++k) {
-                if (i + k >= i1) break;
-                if (key[k] != cur) {
-                    // (a run of no row never comes first and then ends)
-                    if (head) store_v<float, V>(a.partials + (c * 2) * a.hidden + col, acc);
-                    else write_row<TG, V>(a, cur, col, acc);
+                if (i + k >= cnt) break;
+                const uint32_t kk = key[i + k];
+                if (kk != cur) {
+                    if (head) store_v<float, 8>(part, acc);
+                    else write_row<TG, AL>(a, cur, col, acc);
                     head = false;
-                    cur = key[k];
+                    cur = kk;
 #pragma unroll
-                    for (int e = 0; e < V; ++e) acc[e] = 0.f;
+                    for (int e = 0; e < 8; ++e) acc[e] = 0.f;
                 }
-                if (key[k] != none) {
+                if (kk == none) break;
 #pragma unroll
-                    for (int e = 0; e < V; ++e) acc[e] += v[k][e];
-                }
+                for (int e = 0; e < 8; ++e) acc[e] += v[k][e];
             }
         }
         if (cur == none) continue;
-        if (head) store_v<float, V>(a.partials + (c * 2) * a.hidden + col, acc);
-        else if (goes_on) store_v<float, V>(a.partials + (c * 2 + 1) * a.hidden + col, acc);
-        else write_row<TG, V>(a, cur, col, acc);
+        // (where entries of no row follow cur's run, `last` is theirs)
+        if (head) store_v<float, 8>(part, acc);
+        else if (goes_on && cur == last) store_v<float, 8>(part + a.pitch, acc);
+        else write_row<TG, AL>(a, cur, col, acc);
     }
 }
 
-// Runs that cross chunks: the workgroups of the chunk in which such a run
-// begins (grid.y: column slabs) add its pieces: the tail of that chunk, then
-// the heads of the following ones.  kJoinWays threads share a column, each
-// taking every kJoinWays-th piece in rising order; their sums are added in
-// thread order.
-constexpr int kJoinWays = 16;
-constexpr int kJoinCols = kThreads / kJoinWays;    // column units of a slab
+// Runs that cross chunks: a workgroup looks at kJoinChunks chunks; for each in
+// which such a run begins (grid.y: column slabs) it adds the run's pieces: the tail of
+// that chunk, then the heads of the following ones.  kJoinWays threads share
+// a column unit, each taking every kJoinWays-th piece in rising order; their sums
+// are added in thread order.
+constexpr int kJoinChunks = 8;
+constexpr int kJoinWays = 8;
+constexpr int kJoinLanes = kThreads / kJoinWays;    // column units of a slab
 
-template <typename TG, int V>
+template <typename TG, bool AL>
 __global__ __launch_bounds__(kThreads) void k_emb_join(SumArgs a) {
-    __shared__ float part[kJoinWays][kJoinCols][V];
-    const int64_t c = blockIdx.x;
-    const int64_t i0 = c * a.chunk, i1 = min(a.n, i0 + a.chunk);
-    const uint32_t key = a.keys[i1 - 1];
-    if (key == (uint32_t)a.vocab || i1 >= a.n || a.keys[i1] != key) return;
-    if (i0 > 0 && a.keys[i0] == key && a.keys[i0 - 1] == key) return;   // began earlier
-    const int64_t end = lower_bound(a.keys, a.n, key + 1u);             // one past the run
-    const int64_t pieces = (end - 1) / a.chunk - c + 1;
-    const int way = threadIdx.x / kJoinCols, lane = threadIdx.x % kJoinCols;
-    const int u = (int)blockIdx.y * kJoinCols + lane;
-    const int64_t col = (int64_t)u * V;
-    float acc[V];
+    __shared__ float part[kJoinWays][kJoinLanes][8];
+    __shared__ int s_pieces[kJoinChunks];
+    const int64_t c0 = (int64_t)blockIdx.x * kJoinChunks;
+    if (threadIdx.x < kJoinChunks) {
+        const int64_t c = c0 + threadIdx.x;
+        int pieces = 0;
+        const int64_t i0 = c * a.chunk, i1 = i0 + a.chunk;
+        if (c < a.n_chunks && i1 < a.n) {
+            const uint32_t key = a.keys[i1 - 1];
+            if (key != (uint32_t)a.vocab && a.keys[i1] == key &&
+                !(i0 > 0 && a.keys[i0] == key && a.keys[i0 - 1] == key)) {
+                const int64_t end = lower_bound(a.keys, a.n, key + 1u);     // one past the run
+                pieces = (int)((end - 1) / a.chunk - c + 1);
+            }
+        }
+        s_pieces[threadIdx.x] = pieces;
+    }
+    __syncthreads();
+    const int way = threadIdx.x / kJoinLanes, lane = threadIdx.x % kJoinLanes;
+    const int col = ((int)blockIdx.y * kJoinLanes + lane) * 8;
+    for (int j = 0; j < kJoinChunks; ++j) {
+        const int pieces = s_pieces[j];
+        if (pieces == 0) continue;
+        const int64_t c = c0 + j;
+        float acc[8];
 #pragma unroll
-    for (int e = 0; e < V; ++e) acc[e] = 0.f;
-    if (u < a.units) {
+        for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+        if (col < a.hidden) {
 #pragma unroll 4
-        for (int64_t p = way; p < pieces; p += kJoinWays) {
-            float v[V];
-            load_v<float, V>(a.partials + ((c + p) * 2 + (p == 0 ? 1 : 0)) * a.hidden + col, v);
+            for (int p = way; p < pieces; p += kJoinWays) {
+                float v[8];
+                load_v<float, 8>(a.partials + ((c + p) * 2 + (p == 0 ? 1 : 0)) * a.pitch + col, v);
 #pragma unroll
-            for (int e = 0; e < V; ++e) acc[e] += v[e];
+                for (int e = 0; e < 8; ++e) acc[e] += v[e];
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) part[way][lane][e] = acc[e];
+        __syncthreads();
+        if (way == 0 && col < a.hidden) {
+            const int ways = min(pieces, kJoinWays);
+            for (int w = 1; w < ways; ++w) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) acc[e] += part[w][lane][e];
+            }
+            write_row<TG, AL>(a, a.keys[(c + 1) * a.chunk - 1], col, acc);
+        }
+        __syncthreads();
+    }
+}
+
+// Few tokens: one launch.  A workgroup owns `rows` rows of the table and up to 64
+// column units (grid.y: slabs of them); it lists the positions of the tokens of its rows,
+// by row and then in token order, and then writes every row: zeros, or the sum
+// of its list, which `ways` groups of threads share (contiguous parts, added in
+// group order).
+constexpr int kDirectTokens = 1024;
+constexpr int kDirectRows = 32;
+constexpr int kDirectLanes = 64;
+
+struct DirectArgs {
+    SortIn in;
+    SumArgs sum;
+    int32_t rows;
+};
+
+template <typename TD, typename TG, bool AL>
+__global__ __launch_bounds__(kThreads) void k_emb_direct(DirectArgs d) {
+    constexpr int W = kThreads / 64;
+    __shared__ int s_row[kDirectTokens];        // table rows (local) of the listed tokens,
+    __shared__ uint16_t s_tok[kDirectTokens];   // and their positions, in token order
+    __shared__ uint16_t s_pos[kDirectTokens];   // positions by row
+    __shared__ int s_count[W], s_start[kDirectRows + 1];
+    __shared__ float part[W][kDirectLanes][8];
+    const SumArgs& a = d.sum;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int64_t r0 = (int64_t)blockIdx.x * d.rows;
+    const int rows = (int)min<int64_t>(d.rows, a.vocab - r0);
+    const int n = (int)d.in.n;
+    int listed = 0;
+    for (int i0 = 0; i0 < n; i0 += kThreads) {
+        const int i = i0 + tid;
+        const int64_t row = i < n ? (int64_t)sort_key(d.in, i) - r0 : -1;
+        const bool mine = row >= 0 && row < rows;
+        const uint64_t m = __ballot(mine);
+        if (lane == 0) s_count[wave] = __popcll(m);
+        __syncthreads();
+        int at = listed + __popcll(m & ((uint64_t(1) << lane) - 1));
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            at += w < wave ? s_count[w] : 0;
+            listed += s_count[w];
+        }
+        if (mine) {
+            s_row[at] = (int)row;
+            s_tok[at] = (uint16_t)i;
+        }
+        __syncthreads();
+    }
+    // where each row's list begins: entries of smaller rows (a wave counts a row)
+    for (int r = wave; r <= rows; r += W) {
+        int before = 0;
+        for (int i = lane; i < listed; i += 64) before += s_row[i] < r;
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1) before += __shfl_xor(before, off, 64);
+        if (lane == 0) s_start[r] = before;
+    }
+    __syncthreads();
+    for (int r = wave; r < rows; r += W) {
+        int at = s_start[r];
+        if (at == s_start[r + 1]) continue;
+        for (int i = 0; i < listed; i += 64) {
+            const bool hit = i + lane < listed && s_row[i + lane] == r;
+            const uint64_t m = __ballot(hit);
+            if (hit) s_pos[at + __popcll(m & ((uint64_t(1) << lane) - 1))] = s_tok[i + lane];
+            at += __popcll(m);
         }
     }
-#pragma unroll
-    for (int e = 0; e < V; ++e) part[way][lane][e] = acc[e];
     __syncthreads();
-    if (way != 0 || u >= a.units) return;
-    for (int w = 1; w < kJoinWays; ++w) {
+    const int lanes = 1 << a.lane_bits, groups = kThreads >> a.lane_bits;
+    const int gl = tid & (lanes - 1), group = tid >> a.lane_bits;
+    const int col = ((int)blockIdx.y * kDirectLanes + gl) * 8;
+    const TD* dout = static_cast<const TD*>(a.dout);
+    // lists of up to 16 tokens, and none: a group a row
+    for (int r = group; r < rows; r += groups) {
+        const int b = s_start[r], cnt = s_start[r + 1] - b;
+        if (cnt > 16 || col >= a.hidden) continue;
+        float acc[8];
 #pragma unroll
-        for (int e = 0; e < V; ++e) acc[e] += part[w][lane][e];
+        for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+        add_rows<TD, AL>(acc, dout, a.dout_stride, a.hidden, col, s_pos + b, cnt);
+        if (cnt > 0 || !a.accumulate) write_row<TG, AL>(a, (uint32_t)(r0 + r), col, acc);
     }
-    write_row<TG, V>(a, key, col, acc);
+    // longer ones: all groups (at most W of them) share a row
+    const int ways = min(groups, W);
+    for (int r = 0; r < rows; ++r) {
+        const int b = s_start[r], cnt = s_start[r + 1] - b;
+        if (cnt <= 16) continue;
+        const int each = (cnt + ways - 1) / ways;
+        const int p0 = min(cnt, group * each), p1 = min(cnt, p0 + each);
+        float acc[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+        if (group < ways) {
+            if (col < a.hidden)
+                add_rows<TD, AL>(acc, dout, a.dout_stride, a.hidden, col, s_pos + b + p0, p1 - p0);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) part[group][gl][e] = acc[e];
+        }
+        __syncthreads();
+        if (group == 0 && col < a.hidden) {
+            for (int w = 1; w < ways; ++w) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) acc[e] += part[w][gl][e];
+            }
+            write_row<TG, AL>(a, (uint32_t)(r0 + r), col, acc);
+        }
+        __syncthreads();
+    }
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 int64_t per16(int32_t dtype) { return dtype == MA_PARAM_BF16 ? 8 : 4; }
 
-// log2 of the threads that share a row of `units` column units.
-int lane_bits_for(int64_t units) {
-    int b = 0;
-    while ((1 << b) < kThreads && (int64_t(1) << b) < units) ++b;
+// log2 of the threads that share a row of `units` column units, within [least, most].
+int lane_bits_for(int64_t units, int least, int most) {
+    int b = least;
+    while (b < most && (int64_t(1) << b) < units) ++b;
     return b;
 }
 
 }  // namespace
 
+// Up to this many tokens one workgroup sorts: its two passes take 6 us at 4096
+// tokens, four launches over many workgroups 15 us.
+static constexpr int64_t kLdsSortTokens = 4096;
+
 EmbPlan embedding_plan(int64_t n_tokens, int64_t vocab, int64_t hidden) {
     EmbPlan p;
-    if (n_tokens == 0) return p;
+    if (n_tokens <= kDirectTokens) return p;
     int nbits = 1;
     while ((int64_t(1) << nbits) <= vocab) ++nbits;       // keys 0 .. vocab
     p.passes = (nbits + 9) / 10;
     p.bits = (nbits + p.passes - 1) / p.passes;
-    p.per = std::max<int64_t>(1024, round_up(ceil_div(n_tokens, 128), 256));
+    p.per = std::max<int64_t>(kSortThreads, round_up(ceil_div(n_tokens, 128), kSortThreads));
     p.blocks = ceil_div(n_tokens, p.per);
-    p.chunk = std::min<int64_t>(256, std::max<int64_t>(32, round_up(ceil_div(n_tokens, 2048), 8)));
+    p.chunk = std::min<int64_t>(kMaxChunk, std::max<int64_t>(16, round_up(ceil_div(n_tokens, 1024), 8)));
     p.n_chunks = ceil_div(n_tokens, p.chunk);
+    p.pitch = round_up(hidden, 8);
     size_t off = 0;
     auto take = [&](size_t bytes) {
         const size_t at = off;
         off += (bytes + 255) / 256 * 256;
         return at;
     };
-    for (int k = 0; k < 2; ++k) {
+    p.flags = take((size_t)vocab);
+    const int bufs = n_tokens <= kLdsSortTokens ? 1 : 2;
+    for (int k = 0; k < bufs; ++k) {
         p.keys[k] = take((size_t)n_tokens * 4);
         p.pos[k] = take((size_t)n_tokens * 4);
     }
-    p.counts = take((size_t)p.blocks * ((size_t)1 << p.bits) * 4);
-    p.partials = take((size_t)p.n_chunks * 2 * (size_t)hidden * 4);
+    if (n_tokens > kLdsSortTokens) p.counts = take((size_t)p.blocks * ((size_t)1 << p.bits) * 4);
+    p.partials = take((size_t)p.n_chunks * 2 * (size_t)p.pitch * 4);
     p.total = off;
     return p;
 }
@@ -436,26 +680,25 @@ int launch_embedding_lookup(const void* table, int32_t table_dtype, int64_t voca
                             int64_t n_tokens, float scale, void* out, int32_t out_dtype,
                             int64_t out_stride, void* stream) {
     if (n_tokens == 0) return (int)hipSuccess;
-    const bool vec = aligned16(table) && aligned16(out) && hidden % 8 == 0 &&
-                     table_stride % per16(table_dtype) == 0 && out_stride % per16(out_dtype) == 0;
-    const int64_t units = vec ? hidden / 8 : hidden;
-    const int lb = lane_bits_for(units);
+    const bool al = aligned16(table) && aligned16(out) && hidden % 8 == 0 &&
+                    table_stride % per16(table_dtype) == 0 && out_stride % per16(out_dtype) == 0;
+    const int lb = lane_bits_for(ceil_div(hidden, 8), 0, 8);
     const int64_t rows = (int64_t)(kThreads >> lb) * kLookRows;
     const dim3 grid((unsigned)ceil_div(n_tokens, rows));
-#define GO(TI, TO, TOK, V)                                                                      \
-    hipLaunchKernelGGL((k_emb_lookup<TI, TO, TOK, V>), grid, dim3(kThreads), 0,                  \
+#define GO(TI, TO, TOK, AL)                                                                     \
+    hipLaunchKernelGGL((k_emb_lookup<TI, TO, TOK, AL>), grid, dim3(kThreads), 0,                 \
                        (hipStream_t)stream, static_cast<const TI*>(table), table_stride, vocab,  \
                        static_cast<const TOK*>(tokens), n_tokens, scale, static_cast<TO*>(out),   \
-                       out_stride, (int)units, lb)
-#define GO_V(TI, TO, TOK)                                                                       \
+                       out_stride, (int)hidden, lb)
+#define GO_AL(TI, TO, TOK)                                                                      \
     do {                                                                                        \
-        if (vec) GO(TI, TO, TOK, 8);                                                            \
-        else GO(TI, TO, TOK, 1);                                                                \
+        if (al) GO(TI, TO, TOK, true);                                                          \
+        else GO(TI, TO, TOK, false);                                                            \
     } while (0)
 #define GO_TOK(TI, TO)                                                                          \
     do {                                                                                        \
-        if (token_bytes == 8) GO_V(TI, TO, int64_t);                                            \
-        else GO_V(TI, TO, int32_t);                                                             \
+        if (token_bytes == 8) GO_AL(TI, TO, int64_t);                                           \
+        else GO_AL(TI, TO, int32_t);                                                            \
     } while (0)
     const bool ti = table_dtype == MA_PARAM_BF16, to = out_dtype == MA_PARAM_BF16;
     if (ti && to) GO_TOK(__bf16, __bf16);
@@ -463,87 +706,129 @@ int launch_embedding_lookup(const void* table, int32_t table_dtype, int64_t voca
     else if (to) GO_TOK(float, __bf16);
     else GO_TOK(float, float);
 #undef GO_TOK
-#undef GO_V
+#undef GO_AL
 #undef GO
     return (int)hipGetLastError();
 }
 
+namespace {
+
+// Calls f(TD{}, TG{}, aligned) with the call's types.
+template <typename F>
+void by_types(bool dout_bf16, bool grad_bf16, bool al, F f) {
+    auto with = [&](auto td, auto tg) {
+        if (al) f(td, tg, std::true_type{});
+        else f(td, tg, std::false_type{});
+    };
+    if (dout_bf16 && grad_bf16) with(__bf16{}, __bf16{});
+    else if (dout_bf16) with(__bf16{}, float{});
+    else if (grad_bf16) with(float{}, __bf16{});
+    else with(float{}, float{});
+}
+
+int launch_sort(const EmbGradArgs& g, const EmbPlan& p, SortIn s, int& at, hipStream_t st) {
+    auto keys = [&](int k) { return reinterpret_cast<uint32_t*>(g.ws + p.keys[k]); };
+    auto pos = [&](int k) { return reinterpret_cast<int32_t*>(g.ws + p.pos[k]); };
+    if (g.n_tokens <= kLdsSortTokens) {
+        at = 0;
+        if (g.n_tokens <= 2 * kSortThreads)
+            hipLaunchKernelGGL((k_sort_lds<2>), dim3(1), dim3(kSortThreads), 0, st, s, p.passes, keys(0), pos(0));
+        else
+            hipLaunchKernelGGL((k_sort_lds<4>), dim3(1), dim3(kSortThreads), 0, st, s, p.passes, keys(0), pos(0));
+        return (int)hipGetLastError();
+    }
+    uint32_t* counts = reinterpret_cast<uint32_t*>(g.ws + p.counts);
+    for (int k = 0; k < p.passes; ++k) {
+        s.token_bytes = k == 0 ? g.token_bytes : 0;
+        s.shift = k * p.bits;
+        if (k > 0) {
+            s.keys = keys((k - 1) & 1);
+            s.pos = pos((k - 1) & 1);
+        }
+        hipLaunchKernelGGL(k_sort_count, dim3((unsigned)p.blocks), dim3(kSortThreads), 0, st, s, counts);
+        hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return (int)e;
+        hipLaunchKernelGGL(k_sort_scatter, dim3((unsigned)p.blocks), dim3(kSortThreads), 0, st, s, counts,
+                           keys(k & 1), pos(k & 1));
+        e = hipGetLastError();
+        if (e != hipSuccess) return (int)e;
+    }
+    at = (p.passes - 1) & 1;
+    return (int)hipSuccess;
+}
+
+}  // namespace
+
 int launch_embedding_grad(const EmbGradArgs& g, const EmbPlan& p, void* stream) {
     hipStream_t st = (hipStream_t)stream;
+    if (g.n_tokens == 0 && g.accumulate) return (int)hipSuccess;
+    const bool al = aligned16(g.dout) && aligned16(g.grad) && g.hidden % 8 == 0 &&
+                    g.dout_stride % per16(g.dout_dtype) == 0;
+    const bool bd = g.dout_dtype == MA_PARAM_BF16, bg = g.grad_dtype == MA_PARAM_BF16;
+    const int64_t units = ceil_div(g.hidden, 8);
     SumArgs a{};
     a.dout = g.dout;
     a.grad = g.grad;
     a.dout_stride = g.dout_stride;
     a.n = g.n_tokens;
     a.vocab = g.vocab;
-    a.hidden = g.hidden;
-    a.chunk = p.chunk;
+    a.hidden = (int)g.hidden;
+    a.chunk = (int)p.chunk;
     a.n_chunks = p.n_chunks;
+    a.pitch = p.pitch;
     a.scale = g.scale;
     a.accumulate = g.accumulate;
+    SortIn s{};
+    s.tokens = g.tokens;
+    s.n = g.n_tokens;
+    s.vocab = g.vocab;
+    s.pad = g.padding_token;
+    s.bits = p.bits;
+    s.per = p.per;
+    s.token_bytes = g.token_bytes;
+    if (g.n_tokens > 0 && g.n_tokens <= kDirectTokens) {
+        DirectArgs d{};
+        d.in = s;
+        a.lane_bits = lane_bits_for(units, 0, 6);
+        d.sum = a;
+        const unsigned slabs = (unsigned)ceil_div(units, kDirectLanes);
+        // about four workgroups per CU, of at most kDirectRows rows
+        d.rows = (int)std::min<int64_t>(kDirectRows, std::max<int64_t>(1, ceil_div(g.vocab * slabs, 4 * kCus)));
+        const dim3 grid((unsigned)ceil_div(g.vocab, d.rows), slabs);
+        by_types(bd, bg, al, [&](auto td, auto tg, auto w) {
+            hipLaunchKernelGGL((k_emb_direct<decltype(td), decltype(tg), decltype(w)::value>), grid,
+                               dim3(kThreads), 0, st, d);
+        });
+        return (int)hipGetLastError();
+    }
     if (g.n_tokens > 0) {
-        SortIn s{};
-        s.tokens = g.tokens;
-        s.n = g.n_tokens;
-        s.vocab = g.vocab;
-        s.pad = g.padding_token;
-        s.bits = p.bits;
-        s.per = p.per;
-        uint32_t* counts = reinterpret_cast<uint32_t*>(g.ws + p.counts);
-        for (int k = 0; k < p.passes; ++k) {
-            s.token_bytes = k == 0 ? g.token_bytes : 0;
-            s.shift = k * p.bits;
-            if (k > 0) {
-                s.keys = reinterpret_cast<const uint32_t*>(g.ws + p.keys[(k - 1) & 1]);
-                s.pos = reinterpret_cast<const int32_t*>(g.ws + p.pos[(k - 1) & 1]);
-            }
-            hipLaunchKernelGGL(k_sort_count, dim3((unsigned)p.blocks), dim3(kThreads), 0, st, s,
-                               counts);
-            hipError_t e = hipGetLastError();
-            if (e != hipSuccess) return (int)e;
-            hipLaunchKernelGGL(k_sort_scatter, dim3((unsigned)p.blocks), dim3(kThreads), 0, st, s,
-                               counts, reinterpret_cast<uint32_t*>(g.ws + p.keys[k & 1]),
-                               reinterpret_cast<int32_t*>(g.ws + p.pos[k & 1]));
-            e = hipGetLastError();
-            if (e != hipSuccess) return (int)e;
-        }
-        const int at = (p.passes - 1) & 1;
+        s.flags = reinterpret_cast<uint8_t*>(g.ws + p.flags);
+        int at = 0;
+        const int e = launch_sort(g, p, s, at, st);
+        if (e != (int)hipSuccess) return e;
         a.keys = reinterpret_cast<const uint32_t*>(g.ws + p.keys[at]);
         a.pos = reinterpret_cast<const int32_t*>(g.ws + p.pos[at]);
+        a.flags = s.flags;
         a.partials = reinterpret_cast<float*>(g.ws + p.partials);
-    } else if (g.accumulate) {
-        return (int)hipSuccess;
     }
-    const bool vec = aligned16(g.dout) && aligned16(g.grad) && g.hidden % 8 == 0 &&
-                     g.dout_stride % per16(g.dout_dtype) == 0;
-    const int64_t units = vec ? g.hidden / 8 : g.hidden;
-    a.units = (int)units;
-    a.lane_bits = lane_bits_for(units);
+    a.lane_bits = lane_bits_for(units, 5, 8);
     a.sum_blocks = ceil_div(a.n_chunks, kThreads >> a.lane_bits);
     const int64_t fill = g.accumulate ? 0 : ceil_div(g.vocab, kFillRows);
-    const bool bd = g.dout_dtype == MA_PARAM_BF16, bg = g.grad_dtype == MA_PARAM_BF16;
     const dim3 grid((unsigned)(a.sum_blocks + fill));
-#define GO(TD, TG)                                                                              \
-    do {                                                                                        \
-        if (vec) hipLaunchKernelGGL((k_emb_sum<TD, TG, 8>), grid, dim3(kThreads), 0, st, a);    \
-        else hipLaunchKernelGGL((k_emb_sum<TD, TG, 1>), grid, dim3(kThreads), 0, st, a);        \
-    } while (0)
-    if (bd && bg) GO(__bf16, __bf16);
-    else if (bd) GO(__bf16, float);
-    else if (bg) GO(float, __bf16);
-    else GO(float, float);
-#undef GO
-    hipError_t e = hipGetLastError();
+    by_types(bd, bg, al, [&](auto td, auto tg, auto w) {
+        hipLaunchKernelGGL((k_emb_sum<decltype(td), decltype(tg), decltype(w)::value>), grid,
+                           dim3(kThreads), 0, st, a);
+    });
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.n_chunks < 2) return (int)e;
-    const dim3 jgrid((unsigned)a.n_chunks, (unsigned)ceil_div(units, kJoinCols));
-#define GO(TG)                                                                                  \
-    do {                                                                                        \
-        if (vec) hipLaunchKernelGGL((k_emb_join<TG, 8>), jgrid, dim3(kThreads), 0, st, a);      \
-        else hipLaunchKernelGGL((k_emb_join<TG, 1>), jgrid, dim3(kThreads), 0, st, a);          \
-    } while (0)
-    if (bg) GO(__bf16);
-    else GO(float);
-#undef GO
+    const dim3 jgrid((unsigned)ceil_div(a.n_chunks, kJoinChunks), (unsigned)ceil_div(units, kJoinLanes));
+    if (bg) {
+        if (al) hipLaunchKernelGGL((k_emb_join<__bf16, true>), jgrid, dim3(kThreads), 0, st, a);
+        else hipLaunchKernelGGL((k_emb_join<__bf16, false>), jgrid, dim3(kThreads), 0, st, a);
+    } else {
+        if (al) hipLaunchKernelGGL((k_emb_join<float, true>), jgrid, dim3(kThreads), 0, st, a);
+        else hipLaunchKernelGGL((k_emb_join<float, false>), jgrid, dim3(kThreads), 0, st, a);
+    }
     return (int)hipGetLastError();
 }
 

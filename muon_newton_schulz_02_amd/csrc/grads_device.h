@@ -67,6 +67,65 @@ __device__ __forceinline__ void store_v(T* p, const float* v) {
     }
 }
 
+// A column unit of 8 elements.  AL: whole and 16-byte aligned; otherwise
+// only the first `cnt` (at least 1) exist, at any element's address: whole units
+// still move as 16-byte accesses (global memory takes them at any alignment), the
+// row's last part element by element.
+typedef unsigned int u32x4u2 __attribute__((ext_vector_type(4), aligned(2)));
+typedef unsigned int u32x4u4 __attribute__((ext_vector_type(4), aligned(4)));
+
+template <typename T, bool AL>
+__device__ __forceinline__ void load_unit(const T* p, int cnt, float* v) {
+    if constexpr (AL) {
+        load_v<T, 8>(p, v);
+    } else if (cnt >= 8) {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const u32x4 w = *(reinterpret_cast<const u32x4u4*>(p) + q);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[4 * q + e] = __uint_as_float(w[e]);
+            }
+        } else {
+            const u32x4 w = *reinterpret_cast<const u32x4u2*>(p);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[2 * e] = __uint_as_float(w[e] << 16);
+                v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = e < cnt ? (float)p[e] : 0.f;
+    }
+}
+
+template <typename T, bool AL>
+__device__ __forceinline__ void store_unit(T* p, int cnt, const float* v) {
+    if constexpr (AL) {
+        store_v<T, 8>(p, v);
+    } else if (cnt >= 8) {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                u32x4 w;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[e] = __float_as_uint(v[4 * q + e]);
+                *(reinterpret_cast<u32x4u4*>(p) + q) = w;
+            }
+        } else {
+            u32x4 w;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
+            *reinterpret_cast<u32x4u2*>(p) = w;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e < cnt) p[e] = (T)v[e];
+    }
+}
+
 // ------------------------------------------------- activations in 8 bits --
 // A group of 32 features is held as codes q and one exponent byte b = e + 127:
 // x stands for q 2^e.  With the group's largest magnitude m 2^k (1 <= m < 2),

@@ -36,15 +36,18 @@ int launch_glu_backward(const GluArgs& a, void* stream);
 
 // ---------------------------------------------------------- embedding --
 // How ma_embedding_grad splits its work: a radix sort of (row, position)
-// pairs in `passes` passes of `bits` bits over `blocks` blocks of `per`
-// tokens, then chunks of `chunk` sorted entries.
+// pairs in `passes` passes of `bits` bits (over `blocks` blocks of `per`
+// tokens, where one workgroup does not do it), then chunks of `chunk` sorted
+// entries.  All zero for so few tokens that no sort is needed.
 struct EmbPlan {
     int32_t bits = 0, passes = 0;
     int64_t per = 0, blocks = 0;
     int64_t chunk = 0, n_chunks = 0;
-    // workspace offsets: two pairs of (row, position) arrays, the digit
-    // counts of a pass, and the partial sums of runs that cross chunks
-    size_t keys[2] = {0, 0}, pos[2] = {0, 0}, counts = 0, partials = 0, total = 0;
+    int64_t pitch = 0;            // columns of a partial sum
+    // workspace offsets: a flag byte per row, two pairs of (row, position)
+    // arrays, the digit counts of a pass, and the partial sums of runs that
+    // cross chunks
+    size_t flags = 0, keys[2] = {0, 0}, pos[2] = {0, 0}, counts = 0, partials = 0, total = 0;
 };
 EmbPlan embedding_plan(int64_t n_tokens, int64_t vocab, int64_t hidden);
 

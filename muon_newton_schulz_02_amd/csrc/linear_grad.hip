@@ -98,7 +98,7 @@ __device__ __forceinline__ uint32_t high_halves(uint32_t lo, uint32_t hi) {
 
 // The simple kernel: 128 x 128 tiles, four waves of 64 x 64, two LDS stages,
 // operands staged through registers.  It takes any types, strides and sizes.
-template <typename TD, bool VEC, typename TG>
+template <typename TD, bool AL, typename TG>
 __global__ __launch_bounds__(kThreads) void k_linear_grad(LgArgs a, int64_t tiles_n,
                                                           int64_t tiles_k, int64_t slices,
                                                           int64_t per) {
@@ -147,17 +147,12 @@ __global__ __launch_bounds__(kThreads) void k_linear_grad(LgArgs a, int64_t tile
         const TD* d = static_cast<const TD*>(a.dy) + (t + srow) * a.dy_stride + n0 + scol;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            if (VEC) {
-                if (in && n0 + scol + 8 * h < a.n_out) {
-                    load_v<TD, 8>(d + 8 * h, dv + 8 * h);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) dv[8 * h + e] = 0.f;
-                }
+            const int64_t col = n0 + scol + 8 * h;
+            if (in && col < a.n_out) {
+                load_unit<TD, AL>(d + 8 * h, (int)min<int64_t>(8, a.n_out - col), dv + 8 * h);
             } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    dv[8 * h + e] = in && n0 + scol + 8 * h + e < a.n_out ? (float)d[8 * h + e] : 0.f;
+                for (int e = 0; e < 8; ++e) dv[8 * h + e] = 0.f;
             }
         }
         xc = (u32x4){0u, 0u, 0u, 0u};
@@ -640,23 +635,23 @@ int launch_big(const LgArgs& a, const LgPlan& p, hipStream_t st) {
     return (int)hipGetLastError();
 }
 
-template <typename TD, bool VEC>
+template <typename TD, bool AL>
 int launch_small_as(const LgArgs& a, const LgPlan& p, hipStream_t st) {
     const dim3 grid((unsigned)(p.tiles_n * p.tiles_k * p.slices));
     if (a.grad_dtype == MA_PARAM_BF16)
-        hipLaunchKernelGGL((k_linear_grad<TD, VEC, __bf16>), grid, dim3(kThreads), 0, st, a,
+        hipLaunchKernelGGL((k_linear_grad<TD, AL, __bf16>), grid, dim3(kThreads), 0, st, a,
                            p.tiles_n, p.tiles_k, p.slices, p.per);
     else
-        hipLaunchKernelGGL((k_linear_grad<TD, VEC, float>), grid, dim3(kThreads), 0, st, a,
+        hipLaunchKernelGGL((k_linear_grad<TD, AL, float>), grid, dim3(kThreads), 0, st, a,
                            p.tiles_n, p.tiles_k, p.slices, p.per);
     return (int)hipGetLastError();
 }
 
 int launch_small(const LgArgs& a, const LgPlan& p, hipStream_t st) {
     const bool bf16 = a.dy_dtype == MA_PARAM_BF16;
-    const bool vec = aligned16(a.dy) && a.n_out % 8 == 0 && a.dy_stride % (bf16 ? 8 : 4) == 0;
-    if (bf16) return vec ? launch_small_as<__bf16, true>(a, p, st) : launch_small_as<__bf16, false>(a, p, st);
-    return vec ? launch_small_as<float, true>(a, p, st) : launch_small_as<float, false>(a, p, st);
+    const bool al = aligned16(a.dy) && a.n_out % 8 == 0 && a.dy_stride % (bf16 ? 8 : 4) == 0;
+    if (bf16) return al ? launch_small_as<__bf16, true>(a, p, st) : launch_small_as<__bf16, false>(a, p, st);
+    return al ? launch_small_as<float, true>(a, p, st) : launch_small_as<float, false>(a, p, st);
 }
 
 template <typename TG, int V>

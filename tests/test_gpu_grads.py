@@ -207,7 +207,9 @@ def _tokens(rng, how, n, v):
     (32, 40, 16, "zipf"), (33, 40, 16, "one"), (64, 5, 24, "mixed"), (512, 1000, 256, "zipf"),
     (1000, 1023, 40, "mixed"), (1025, 1024, 8, "uniform"), (3000, 70000, 24, "zipf"),
     (5000, 300, 17, "mixed"), (4097, 2, 8, "uniform"), (2500, 1100000, 8, "mixed"),
-    (700, 50, 2048, "one"), (257, 9, 12, "none")])
+    (700, 50, 2048, "one"), (257, 9, 12, "none"), (1024, 40, 520, "one"), (1024, 9000, 16, "zipf"),
+    (2048, 3, 40, "mixed"), (2049, 40, 264, "one"), (4096, 600, 16, "zipf"), (4096, 9, 8, "none"),
+    (9000, 5000, 300, "zipf"), (20000, 3, 24, "one"), (140000, 700, 8, "mixed")])
 def test_embedding_grad(td, tg, n, v, h, how):
     rng = np.random.default_rng(n * 31 + v + h)
     ids = _tokens(rng, how, n, v)

@@ -118,9 +118,9 @@ def test_lookup_refusals(lib):
 
 
 def test_embedding_grad_refusals(lib):
-    need = M.ma_embedding_grad_workspace_size(100, 50, 16)
+    need = M.ma_embedding_grad_workspace_size(5000, 50, 16)
     assert need % 256 == 0 and need > 0
-    base = dict(dout=at(0), ddt=1, dstride=16, tokens=at(1), tb=4, n=100, vocab=50, hidden=16,
+    base = dict(dout=at(0), ddt=1, dstride=16, tokens=at(1), tb=4, n=5000, vocab=50, hidden=16,
                 scale=2.0, pad=-1, grad=at(2), gdt=0, acc=0, ws=at(3), wsb=need, stream=None)
     I, S, W = M.MA_ERR_INVALID_ARG, M.MA_ERR_SHAPE, M.MA_ERR_WORKSPACE
     for code, change in [(I, dict(ddt=2)), (I, dict(gdt=2)), (I, dict(tb=1)), (I, dict(acc=2)),
