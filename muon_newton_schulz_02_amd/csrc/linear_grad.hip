@@ -17,6 +17,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "grads_device.h"
 #include "grads_internal.h"
@@ -31,6 +32,7 @@ constexpr int kThreads = 256;
 constexpr int kTile = 128;                       // output tile side
 constexpr int kRow = 2 * kTile;                  // LDS bytes of a token row
 constexpr int kRegion = kLgStage * kRow;         // LDS bytes of an operand's stage
+constexpr int kAhead = 3;                        // stages loaded ahead into registers
 
 __device__ __forceinline__ u32x2 lds_tr8(const char* p) {
     const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(p));
@@ -41,23 +43,17 @@ __device__ __forceinline__ u32x2 lds_tr8(const char* p) {
 // the XCDs in turn; each XCD gets a contiguous range of the work list, in which
 // tiles that share operand columns are neighbours.
 struct Work {
-    int64_t tn, tk, slice;
+    int tn, tk, slice;
 };
-__device__ __forceinline__ Work work_of(int64_t id, int64_t total, int64_t tiles_n, int64_t tiles_k) {
-    const int64_t q = total / kXcds, r = total % kXcds;
-    const int64_t xcd = id % kXcds, local = id / kXcds;
-    const int64_t i = xcd * q + min(xcd, r) + local;
-    Work w;
-    const int64_t tiles = tiles_n * tiles_k;
-    w.slice = i / tiles;
-    const int64_t t = i - w.slice * tiles;
-    // blocks of four tile rows, walked column by column
-    const int64_t band = t / (4 * tiles_k);
-    const int64_t rows = min<int64_t>(4, tiles_n - band * 4);
-    const int64_t in = t - band * 4 * tiles_k;
-    w.tk = in / rows;
-    w.tn = band * 4 + in % rows;
-    return w;
+__device__ __forceinline__ Work work_of(uint32_t id, uint32_t total, uint32_t tiles_n, uint32_t tiles_k) {
+    const uint32_t q = total / kXcds, r = total % kXcds;
+    const uint32_t xcd = id % kXcds, local = id / kXcds;
+    const uint32_t i = xcd * q + min(xcd, r) + local;
+    const uint32_t tiles = tiles_n * tiles_k, slice = i / tiles, t = i - slice * tiles;
+    // bands of four tile rows, walked column by column
+    const uint32_t band = t / (4 * tiles_k), in = t - band * 4 * tiles_k;
+    const uint32_t rows = min(4u, tiles_n - band * 4), tk = in / rows;
+    return {(int)(band * 4 + in - tk * rows), (int)tk, (int)slice};
 }
 
 // 16 held values of a token as bf16 (exact), packed in pairs.
@@ -96,22 +92,101 @@ __device__ __forceinline__ uint32_t high_halves(uint32_t lo, uint32_t hi) {
     return (lo >> 16) | (hi & 0xffff0000u);
 }
 
-// The simple kernel: 128 x 128 tiles, four waves of 64 x 64, two LDS stages,
-// operands staged through registers.  It takes any types, strides and sizes.
+// One 32 x 32 accumulator block into rows of `ld` elements: register r of lane l
+// holds row 8 (r / 4) + 4 (l / 32) + r % 4, column l % 32, so a store covers two row
+// pieces of 32 columns.  `rows` and `cols` from the block's origin exist (WHOLE:
+// all 32).
+template <typename T, bool WHOLE, bool ADD>
+__device__ __forceinline__ void store_block(const f32x16& v, T* p, int64_t ld, int64_t rows,
+                                            int64_t cols, int lane) {
+    const int r0 = 4 * (lane >> 5), c = lane & 31;
+    if (!WHOLE && c >= cols) return;
+    T* q = p + r0 * ld + c;
+    if (ADD) {
+        float old[16];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int d = 8 * (r >> 2) + (r & 3);
+            old[r] = WHOLE || r0 + d < rows ? (float)q[d * ld] : 0.f;
+        }
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int d = 8 * (r >> 2) + (r & 3);
+            if (WHOLE || r0 + d < rows) q[d * ld] = (T)(old[r] + v[r]);
+        }
+    } else {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int d = 8 * (r >> 2) + (r & 3);
+            if (WHOLE || r0 + d < rows) q[d * ld] = (T)v[r];
+        }
+    }
+}
+
+// A wave's NI x NJ blocks (rows first) from output row `row`, column `col` on: partial
+// sums, or the gradient, written or added to.
+template <typename TG, int NI, int NJ, typename ACC>
+__device__ __forceinline__ void store_wave(ACC acc, float* part, TG* grad, int accumulate,
+                                           int64_t row, int64_t col, int64_t n_out, int64_t n_in,
+                                           int lane) {
+    const int64_t rows = n_out - row, cols = n_in - col, o = row * n_in + col;
+    auto each = [&](auto whole, auto add, auto* base) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+                store_block<std::remove_pointer_t<decltype(base)>, decltype(whole)::value, decltype(add)::value>(
+                    acc(i, j), base + o + i * 32 * n_in + j * 32, n_in, rows - i * 32, cols - j * 32, lane);
+    };
+    auto by_size = [&](auto add, auto* base) {
+        if (rows >= NI * 32 && cols >= NJ * 32) each(std::true_type{}, add, base);
+        else each(std::false_type{}, add, base);
+    };
+    if (part) by_size(std::false_type{}, part);
+    else if (accumulate) by_size(std::true_type{}, grad);
+    else by_size(std::false_type{}, grad);
+}
+
+// 8 values as they lie in memory (T's 16 or 32 bytes), zeros past the first cnt.
+template <typename T, bool AL>
+__device__ __forceinline__ void load_raw8(const T* p, int cnt, u32x4* w) {
+    if constexpr (AL) {
+#pragma unroll
+        for (int q = 0; q < (int)sizeof(T) / 2; ++q) w[q] = *(reinterpret_cast<const u32x4*>(p) + q);
+    } else if (cnt >= 8) {
+        if constexpr (sizeof(T) == 4) {
+            w[0] = *reinterpret_cast<const u32x4u4*>(p);
+            w[1] = *(reinterpret_cast<const u32x4u4*>(p) + 1);
+        } else {
+            w[0] = *reinterpret_cast<const u32x4u2*>(p);
+        }
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e >> 2][e & 3] = e < cnt ? __float_as_uint(p[e]) : 0u;
+    } else {
+        const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            w[0][e] = (2 * e < cnt ? (uint32_t)h[2 * e] : 0u) |
+                      (2 * e + 1 < cnt ? (uint32_t)h[2 * e + 1] << 16 : 0u);
+    }
+}
+
+// The kernel for any type, stride and size: 128 x 128 tiles, four waves of 64
+// x 64, two LDS stages, operands staged through registers.
 template <typename TD, bool AL, typename TG>
-__global__ __launch_bounds__(kThreads) void k_linear_grad(LgArgs a, int64_t tiles_n,
-                                                          int64_t tiles_k, int64_t slices,
-                                                          int64_t per) {
+__global__ __launch_bounds__(kThreads) void k_linear_grad(LgArgs a, int tiles_n,
+                                                          int tiles_k, int slices, int per) {
     constexpr int NP = sizeof(TD) == 4 ? 3 : 1;         // bf16 parts of dY
     constexpr int kStageBytes = (NP + 1) * kRegion;
     __shared__ __attribute__((aligned(1024))) char ring[2 * kStageBytes];
-    const Work wk = work_of(blockIdx.x, (int64_t)gridDim.x, tiles_n, tiles_k);
+    const Work wk = work_of(blockIdx.x, gridDim.x, tiles_n, tiles_k);
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave >> 1, wn = wave & 1;
-    const int64_t n0 = wk.tn * kTile, k0 = wk.tk * kTile;
-    const int64_t t0 = wk.slice * per * kLgStage;
-    const int64_t t1 = min(a.n_tokens, t0 + per * kLgStage);
+    const int64_t n0 = (int64_t)wk.tn * kTile, k0 = (int64_t)wk.tk * kTile;
+    const int64_t t0 = (int64_t)wk.slice * per * kLgStage;
+    const int64_t t1 = min<int64_t>(a.n_tokens, t0 + (int64_t)per * kLgStage);
     const int64_t cp = (a.n_in + 31) / 32 * 32, ep = ((cp / 32) + 3) / 4 * 4;
 
     // staging: this thread's token row and first of 16 columns
@@ -139,53 +214,62 @@ __global__ __launch_bounds__(kThreads) void k_linear_grad(LgArgs a, int64_t tile
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
 
-    float dv[16];
-    u32x4 xc;
-    uint32_t xe;
-    auto load = [&](int64_t t) {
-        const bool in = t + srow < t1;
-        const TD* d = static_cast<const TD*>(a.dy) + (t + srow) * a.dy_stride + n0 + scol;
+    // a stage's share of this thread: 16 values of dY (bf16, or float) and 16 codes
+    constexpr int ND = (int)sizeof(TD);
+    struct Regs {
+        u32x4 d[ND], c;
+        uint32_t e;
+    };
+    // (running pointers: loads are issued in stage order)
+    int64_t lt = t0 + srow;
+    const TD* ld = static_cast<const TD*>(a.dy) + lt * a.dy_stride + n0 + scol;
+    const int8_t* lc = a.codes + lt * cp + k0 + scol;
+    const uint8_t* le = a.exps + lt * ep + ((k0 + scol) >> 5);
+    const int64_t dstep = kLgStage * a.dy_stride, cstep = kLgStage * cp, estep = kLgStage * ep;
+    const int left = (int)min<int64_t>(16, a.n_out - n0 - scol);      // columns of dY
+    const bool xin = k0 + scol < cp;
+    auto load = [&](Regs& v) {
+        const bool in = lt < t1;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int64_t col = n0 + scol + 8 * h;
-            if (in && col < a.n_out) {
-                load_unit<TD, AL>(d + 8 * h, (int)min<int64_t>(8, a.n_out - col), dv + 8 * h);
-            } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) dv[8 * h + e] = 0.f;
-            }
+            for (int q = 0; q < ND / 2; ++q) v.d[h * ND / 2 + q] = (u32x4){0u, 0u, 0u, 0u};
+            if (in && left > 8 * h) load_raw8<TD, AL>(ld + 8 * h, left - 8 * h, v.d + h * ND / 2);
         }
-        xc = (u32x4){0u, 0u, 0u, 0u};
-        xe = 0;
-        if (in && k0 + scol < cp) {
-            xc = *reinterpret_cast<const u32x4*>(a.codes + (t + srow) * cp + k0 + scol);
-            xe = a.exps[(t + srow) * ep + ((k0 + scol) >> 5)];
+        v.c = (u32x4){0u, 0u, 0u, 0u};
+        v.e = 0;
+        if (in && xin) {
+            v.c = *reinterpret_cast<const u32x4*>(lc);
+            v.e = *le;
         }
+        lt += kLgStage;
+        ld += dstep;
+        lc += cstep;
+        le += estep;
     };
-    auto put = [&](char* buf) {
-        uint32_t w[NP][8];
+    auto put = [&](const Regs& v, char* buf) {
         if constexpr (NP == 1) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                w[0][e] = high_halves(__float_as_uint(dv[2 * e]), __float_as_uint(dv[2 * e + 1]));
+            *reinterpret_cast<u32x4*>(buf + s0) = v.d[0];
+            *reinterpret_cast<u32x4*>(buf + s1) = v.d[1];
         } else {
+            uint32_t w[NP][8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 uint32_t h0, m0, l0, h1, m1, l1;
-                split3(dv[2 * e], h0, m0, l0);
-                split3(dv[2 * e + 1], h1, m1, l1);
+                split3(__uint_as_float(v.d[e / 2][2 * (e & 1)]), h0, m0, l0);
+                split3(__uint_as_float(v.d[e / 2][2 * (e & 1) + 1]), h1, m1, l1);
                 w[0][e] = high_halves(h0, h1);
                 w[1][e] = high_halves(m0, m1);
                 w[2][e] = high_halves(l0, l1);
             }
-        }
 #pragma unroll
-        for (int p = 0; p < NP; ++p) {
-            *reinterpret_cast<u32x4*>(buf + p * kRegion + s0) = (u32x4){w[p][0], w[p][1], w[p][2], w[p][3]};
-            *reinterpret_cast<u32x4*>(buf + p * kRegion + s1) = (u32x4){w[p][4], w[p][5], w[p][6], w[p][7]};
+            for (int p = 0; p < NP; ++p) {
+                *reinterpret_cast<u32x4*>(buf + p * kRegion + s0) = (u32x4){w[p][0], w[p][1], w[p][2], w[p][3]};
+                *reinterpret_cast<u32x4*>(buf + p * kRegion + s1) = (u32x4){w[p][4], w[p][5], w[p][6], w[p][7]};
+            }
         }
         u32x4 lo, hi;
-        held16(xc, act_scale(xe), lo, hi);
+        held16(v.c, act_scale(v.e), lo, hi);
         *reinterpret_cast<u32x4*>(buf + NP * kRegion + s0) = lo;
         *reinterpret_cast<u32x4*>(buf + NP * kRegion + s1) = hi;
     };
@@ -194,13 +278,15 @@ __global__ __launch_bounds__(kThreads) void k_linear_grad(LgArgs a, int64_t tile
         return __builtin_bit_cast(bf16x8, (u32x4){lo[0], lo[1], hi[0], hi[1]});
     };
 
-    const int stages = (int)((t1 - t0 + kLgStage - 1) / kLgStage);   // (0 or less: no token)
-    if (stages > 0) load(t0);
-    for (int s = 0; s < stages; ++s) {
+    const int stages = t1 > t0 ? (int)((t1 - t0 + kLgStage - 1) / kLgStage) : 0;
+    Regs reg[kAhead];
+    // stage s from its registers into LDS, the load kAhead stages on in their
+    // place (past the slice it loads nothing), and the products
+    auto step = [&](Regs& v, int s) {
         // (the buffer was last read two stages ago, before the barrier in between)
         char* buf = ring + (s & 1) * kStageBytes;
-        put(buf);
-        if (s + 1 < stages) load(t0 + (int64_t)(s + 1) * kLgStage);
+        put(v, buf);
+        load(v);
         __syncthreads();
 #pragma unroll
         for (int kg = 0; kg < 2; ++kg) {
@@ -218,27 +304,22 @@ __global__ __launch_bounds__(kThreads) void k_linear_grad(LgArgs a, int64_t tile
                 }
             }
         }
+    };
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) load(reg[k]);
+    int s = 0;
+    for (; s + kAhead <= stages; s += kAhead) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) step(reg[k], s + k);
     }
+#pragma unroll
+    for (int k = 0; k < kAhead - 1; ++k)
+        if (s + k < stages) step(reg[k], s + k);
 
-    // accumulator register r of lane l: row 8 (r / 4) + 4 (l / 32) + r % 4,
-    // column l % 32: a wave stores two row pieces of 32 columns at a time
-    float* part = slices > 1 ? a.partials + wk.slice * a.n_out * a.n_in : nullptr;
-    TG* grad = static_cast<TG*>(a.grad);
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int64_t col = k0 + wn * 64 + j * 32 + (lane & 31);
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int64_t row = n0 + wm * 64 + i * 32 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
-                if (row >= a.n_out || col >= a.n_in) continue;
-                const int64_t o = row * a.n_in + col;
-                if (part) part[o] = acc[i][j][r];
-                else if (a.accumulate) grad[o] = (TG)((float)grad[o] + acc[i][j][r]);
-                else grad[o] = (TG)acc[i][j][r];
-            }
-        }
+    store_wave<TG, 2, 2>([&](int i, int j) -> const f32x16& { return acc[i][j]; },
+                         slices > 1 ? a.partials + wk.slice * a.n_out * a.n_in : nullptr,
+                         static_cast<TG*>(a.grad), a.accumulate, n0 + wm * 64, k0 + wn * 64, a.n_out,
+                         a.n_in, lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -355,7 +436,7 @@ struct BigArgs {
     void* grad;
     float* partials;
     int64_t n_tokens, n_out, n_in, dy_stride, blocks_k;
-    int64_t tiles_n, tiles_k, slices, per;
+    int32_t tiles_n, tiles_k, slices, per;
     int32_t accumulate;
 };
 
@@ -387,14 +468,14 @@ struct BigCopy {
 template <typename TG>
 __global__ __launch_bounds__(kBigThreads) void k_linear_grad_big(BigArgs a) {
     __shared__ __attribute__((aligned(1024))) char ring[kBigStages * kBigStage];
-    const Work wk = work_of(blockIdx.x, (int64_t)gridDim.x, a.tiles_n, a.tiles_k);
+    const Work wk = work_of(blockIdx.x, gridDim.x, a.tiles_n, a.tiles_k);
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wn = wave & 3, wx = wave >> 2;         // 64 outputs, 128 features each
-    const int64_t n0 = wk.tn * kBigTile, k0 = wk.tk * kBigTile;
-    const int64_t st0 = wk.slice * a.per;            // first stage of the slice
+    const int64_t n0 = (int64_t)wk.tn * kBigTile, k0 = (int64_t)wk.tk * kBigTile;
+    const int64_t st0 = (int64_t)wk.slice * a.per;   // first stage of the slice
     const int64_t all = (a.n_tokens + kLgStage - 1) / kLgStage;
-    const int nk = (int)min(a.per, all - st0);
+    const int nk = (int)min<int64_t>(a.per, all - st0);
 
     BigCopy cp;
     cp.dy = a.dy + (st0 * kLgStage * a.dy_stride + n0) * 2;
@@ -502,25 +583,10 @@ __global__ __launch_bounds__(kBigThreads) void k_linear_grad_big(BigArgs a) {
 
     // (the empty copies past the end)
     __builtin_amdgcn_s_waitcnt(0x0F70);
-    // accumulator register r of lane l: output row 8 (r / 4) + 4 (l / 32) + r % 4,
-    // feature l % 32
-    float* part = a.slices > 1 ? a.partials + wk.slice * a.n_out * a.n_in : nullptr;
-    TG* grad = static_cast<TG*>(a.grad);
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t col = k0 + wx * 128 + i * 32 + (lane & 31);
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int64_t row = n0 + wn * 64 + j * 32 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
-                if (row >= a.n_out || col >= a.n_in) continue;
-                const int64_t o = row * a.n_in + col;
-                if (part) part[o] = acc[i][j][r];
-                else if (a.accumulate) grad[o] = (TG)((float)grad[o] + acc[i][j][r]);
-                else grad[o] = (TG)acc[i][j][r];
-            }
-        }
+    store_wave<TG, 2, 4>([&](int j, int i) -> const f32x16& { return acc[i][j]; },
+                         a.slices > 1 ? a.partials + wk.slice * a.n_out * a.n_in : nullptr,
+                         static_cast<TG*>(a.grad), a.accumulate, n0 + wn * 64, k0 + wx * 128, a.n_out,
+                         a.n_in, lane);
 }
 
 // The slices' partial sums, added in slice order.
@@ -616,10 +682,10 @@ int launch_big(const LgArgs& a, const LgPlan& p, hipStream_t st) {
     b.n_in = a.n_in;
     b.dy_stride = a.dy_stride;
     b.blocks_k = round_up(a.n_in, kBigTile) / 32;
-    b.tiles_n = p.tiles_n;
-    b.tiles_k = p.tiles_k;
-    b.slices = p.slices;
-    b.per = p.per;
+    b.tiles_n = (int)p.tiles_n;
+    b.tiles_k = (int)p.tiles_k;
+    b.slices = (int)p.slices;
+    b.per = (int)p.per;
     b.accumulate = a.accumulate;
     const int64_t stages = ceil_div(a.n_tokens, kLgStage);
     const dim3 egrid((unsigned)p.tiles_k, (unsigned)std::min<int64_t>(stages, 65535));
@@ -640,10 +706,10 @@ int launch_small_as(const LgArgs& a, const LgPlan& p, hipStream_t st) {
     const dim3 grid((unsigned)(p.tiles_n * p.tiles_k * p.slices));
     if (a.grad_dtype == MA_PARAM_BF16)
         hipLaunchKernelGGL((k_linear_grad<TD, AL, __bf16>), grid, dim3(kThreads), 0, st, a,
-                           p.tiles_n, p.tiles_k, p.slices, p.per);
+                           (int)p.tiles_n, (int)p.tiles_k, (int)p.slices, (int)p.per);
     else
         hipLaunchKernelGGL((k_linear_grad<TD, AL, float>), grid, dim3(kThreads), 0, st, a,
-                           p.tiles_n, p.tiles_k, p.slices, p.per);
+                           (int)p.tiles_n, (int)p.tiles_k, (int)p.slices, (int)p.per);
     return (int)hipGetLastError();
 }
 
