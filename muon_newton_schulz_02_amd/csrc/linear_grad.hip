@@ -32,7 +32,7 @@ constexpr int kThreads = 256;
 constexpr int kTile = 128;                       // output tile side
 constexpr int kRow = 2 * kTile;                  // LDS bytes of a token row
 constexpr int kRegion = kLgStage * kRow;         // LDS bytes of an operand's stage
-constexpr int kAhead = 3;                        // stages loaded ahead into registers
+constexpr int kAhead = 2;                        // stages loaded ahead into registers
 
 __device__ __forceinline__ u32x2 lds_tr8(const char* p) {
     const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(p));
@@ -90,6 +90,12 @@ __device__ __forceinline__ void split3(float x, uint32_t& h, uint32_t& m, uint32
 
 __device__ __forceinline__ uint32_t high_halves(uint32_t lo, uint32_t hi) {
     return (lo >> 16) | (hi & 0xffff0000u);
+}
+
+// A buffer of `bytes` from p on: loads past it give zeros.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p, int64_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0,
+                                             (int)min<int64_t>(bytes, 0x7fffffff), 0x00020000);
 }
 
 // One 32 x 32 accumulator block into rows of `ld` elements: register r of lane l
@@ -173,9 +179,10 @@ __device__ __forceinline__ void load_raw8(const T* p, int cnt, u32x4* w) {
 }
 
 // The kernel for any type, stride and size: 128 x 128 tiles, four waves of 64
-// x 64, two LDS stages, operands staged through registers.
+// x 64, two LDS stages, operands staged through registers.  AL: rows of dY in
+// 16-byte pieces, and a slice's operands within 2 GB of their start.
 template <typename TD, bool AL, typename TG>
-__global__ __launch_bounds__(kThreads) void k_linear_grad(LgArgs a, int tiles_n,
+__global__ __launch_bounds__(kThreads, 2) void k_linear_grad(LgArgs a, int tiles_n,
                                                           int tiles_k, int slices, int per) {
     constexpr int NP = sizeof(TD) == 4 ? 3 : 1;         // bf16 parts of dY
     constexpr int kStageBytes = (NP + 1) * kRegion;
@@ -220,32 +227,61 @@ __global__ __launch_bounds__(kThreads) void k_linear_grad(LgArgs a, int tiles_n,
         u32x4 d[ND], c;
         uint32_t e;
     };
-    // (running pointers: loads are issued in stage order)
-    int64_t lt = t0 + srow;
-    const TD* ld = static_cast<const TD*>(a.dy) + lt * a.dy_stride + n0 + scol;
-    const int8_t* lc = a.codes + lt * cp + k0 + scol;
-    const uint8_t* le = a.exps + lt * ep + ((k0 + scol) >> 5);
-    const int64_t dstep = kLgStage * a.dy_stride, cstep = kLgStage * cp, estep = kLgStage * ep;
-    const int left = (int)min<int64_t>(16, a.n_out - n0 - scol);      // columns of dY
-    const bool xin = k0 + scol < cp;
+    // Loads are issued in stage order.  AL: buffer loads at running offsets, so that
+    // what lies past the slice's last token arrives as zeros without a branch
+    // (which would end the load's flight); what lies past a row's last column is
+    // another row's, and ends in outputs that do not exist.
+    const int64_t ld = a.dy_stride;
+    const int64_t es = (int64_t)sizeof(TD);
+    const char* bd = static_cast<const char*>(a.dy) + (t0 * ld + n0) * es;
+    const int8_t* bc = a.codes + t0 * cp + k0;
+    const uint8_t* be = a.exps + t0 * ep + (k0 >> 5);
+    int64_t rows = t1 - t0;                               // left from the next load's first token on
+    const auto rd = buffer(bd, ((rows - 1) * ld + a.n_out - n0) * es);
+    const auto rc = buffer(bc, rows * cp - k0);
+    const auto re = buffer(be, rows * ep - (k0 >> 5));
+    uint32_t vd = (uint32_t)((srow * ld + scol) * es), vc = (uint32_t)(srow * cp + scol);
+    uint32_t ve = (uint32_t)(srow * ep + (scol >> 5));
+    const uint32_t sd = (uint32_t)(kLgStage * ld * es), sc = (uint32_t)(kLgStage * cp), se = (uint32_t)(kLgStage * ep);
+    const int left = (int)max<int64_t>(0, min<int64_t>(16, a.n_out - n0 - scol));   // columns of dY
     auto load = [&](Regs& v) {
-        const bool in = lt < t1;
+        if constexpr (AL) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+            for (int q = 0; q < ND; ++q)
+                v.d[q] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rd, vd + q * 16, 0, 0));
+            v.c = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rc, vc, 0, 0));
+            v.e = __builtin_amdgcn_raw_buffer_load_b8(re, ve, 0, 0);
+            vd += sd;
+            vc += sc;
+            ve += se;
+        } else {
+            // any alignment, stride and size: one of the slice's rows in any case,
+            // cleared if it is not this thread's own
 #pragma unroll
-            for (int q = 0; q < ND / 2; ++q) v.d[h * ND / 2 + q] = (u32x4){0u, 0u, 0u, 0u};
-            if (in && left > 8 * h) load_raw8<TD, AL>(ld + 8 * h, left - 8 * h, v.d + h * ND / 2);
+            for (int q = 0; q < ND; ++q) v.d[q] = (u32x4){0u, 0u, 0u, 0u};
+            v.c = (u32x4){0u, 0u, 0u, 0u};
+            v.e = 0;
+            if (rows > 0) {
+                const int64_t row = min<int64_t>(srow, rows - 1);
+                const TD* d = reinterpret_cast<const TD*>(bd) + row * ld + scol;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (left > 8 * h) load_raw8<TD, false>(d + 8 * h, left - 8 * h, v.d + h * ND / 2);
+                if (k0 + scol < cp) {
+                    v.c = *reinterpret_cast<const u32x4*>(bc + row * cp + scol);
+                    v.e = be[row * ep + (scol >> 5)];
+                }
+                if (srow >= rows) {
+#pragma unroll
+                    for (int q = 0; q < ND; ++q) v.d[q] = (u32x4){0u, 0u, 0u, 0u};
+                    v.e = 0;
+                }
+            }
+            rows -= kLgStage;
+            bd += kLgStage * ld * es;
+            bc += kLgStage * cp;
+            be += kLgStage * ep;
         }
-        v.c = (u32x4){0u, 0u, 0u, 0u};
-        v.e = 0;
-        if (in && xin) {
-            v.c = *reinterpret_cast<const u32x4*>(lc);
-            v.e = *le;
-        }
-        lt += kLgStage;
-        ld += dstep;
-        lc += cstep;
-        le += estep;
     };
     auto put = [&](const Regs& v, char* buf) {
         if constexpr (NP == 1) {
@@ -277,44 +313,60 @@ __global__ __launch_bounds__(kThreads) void k_linear_grad(LgArgs a, int tiles_n,
         const u32x2 lo = lds_tr8(p), hi = lds_tr8(p + 4 * kRow);
         return __builtin_bit_cast(bf16x8, (u32x4){lo[0], lo[1], hi[0], hi[1]});
     };
+    struct Frags {
+        bf16x8 a[NP][2], b[2];
+    };
+    auto read = [&](Frags& f, const char* buf, int kg) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) f.b[j] = frag(buf + NP * kRegion + fb[j] + kg * 16 * kRow);
+#pragma unroll
+        for (int p = 0; p < NP; ++p)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) f.a[p][i] = frag(buf + p * kRegion + fa[i] + kg * 16 * kRow);
+    };
+    auto multiply = [&](const Frags& f) {
+#pragma unroll
+        for (int p = NP - 1; p >= 0; --p)            // smallest part first
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.a[p][i], f.b[j], acc[i][j], 0, 0, 0);
+    };
 
+    // Stage s in two halves of 16 tokens.  While the first is multiplied, the
+    // second's fragments are read and stage s + 1 goes from its registers into the other
+    // LDS buffer (last read in stage s - 1, before that stage's barrier), the
+    // load kAhead stages on taking its place (past the slice it loads zeros);
+    // while the second is multiplied, the next stage's first fragments are read.
     const int stages = t1 > t0 ? (int)((t1 - t0 + kLgStage - 1) / kLgStage) : 0;
     Regs reg[kAhead];
-    // stage s from its registers into LDS, the load kAhead stages on in their
-    // place (past the slice it loads nothing), and the products
-    auto step = [&](Regs& v, int s) {
-        // (the buffer was last read two stages ago, before the barrier in between)
-        char* buf = ring + (s & 1) * kStageBytes;
-        put(v, buf);
-        load(v);
+    Frags f0, f1;
+    auto step = [&](Regs& next, int s) {
+        char* cur = ring + (s & 1) * kStageBytes;
+        char* nxt = ring + ((s + 1) & 1) * kStageBytes;
+        read(f1, cur, 1);
+        put(next, nxt);
+        load(next);
+        multiply(f0);
         __syncthreads();
-#pragma unroll
-        for (int kg = 0; kg < 2; ++kg) {
-            bf16x8 b[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) b[j] = frag(buf + NP * kRegion + fb[j] + kg * 16 * kRow);
-#pragma unroll
-            for (int p = NP - 1; p >= 0; --p) {      // smallest part first
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const bf16x8 f = frag(buf + p * kRegion + fa[i] + kg * 16 * kRow);
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, b[j], acc[i][j], 0, 0, 0);
-                }
-            }
-        }
+        read(f0, nxt, 0);
+        multiply(f1);
     };
+    if (stages > 0) {
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) load(reg[k]);
-    int s = 0;
-    for (; s + kAhead <= stages; s += kAhead) {
+        for (int k = 0; k < kAhead; ++k) load(reg[k]);
+        put(reg[0], ring);
+        load(reg[0]);
+        __syncthreads();
+        read(f0, ring, 0);
+        // (in whole rounds of kAhead: stages past the last are zeros)
+#pragma unroll 1
+        for (int s = 0; s < stages; s += kAhead) {
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) step(reg[k], s + k);
+            for (int k = 0; k < kAhead; ++k) step(reg[(k + 1) % kAhead], s + k);
+        }
     }
-#pragma unroll
-    for (int k = 0; k < kAhead - 1; ++k)
-        if (s + k < stages) step(reg[k], s + k);
 
     store_wave<TG, 2, 2>([&](int i, int j) -> const f32x16& { return acc[i][j]; },
                          slices > 1 ? a.partials + wk.slice * a.n_out * a.n_in : nullptr,
@@ -616,16 +668,32 @@ __global__ __launch_bounds__(kThreads) void k_linear_join(const float* __restric
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-// Time of one stage of a workgroup, its fixed cost in stages, and the float32
-// values per microsecond that partial sums are written and read back at: what the
-// number of slices is chosen by.
-struct Cost {
-    double stage_us, fixed;
-    int groups;                // workgroups that run at once
+// What the kernel and the number of slices are chosen by: a model of a call's time
+// in microseconds, fitted to sweeps of both kernels over 1 to 64 slices, 1024 to 32768
+// tokens and 256 to 8192 outputs and inputs (its choice is within about 10 % of the best swept).
+// stage: a workgroup's time per stage where 1, 2 or 3 of them share a CU (0: they
+// do not fit); idle: how much less of it there is where nearly no CU is busy.
+struct Model {
+    double stage[3];
+    double idle;
+    double fixed;              // a workgroup's prologue and epilogue
 };
-constexpr Cost kBigCost = {0.75, 16.0, kCus};
-constexpr Cost kSmallCost = {0.45, 12.0, 2 * kCus};
-constexpr double kJoinPerUs = 6e5;
+constexpr Model kBigModel = {{0.66, 0.0, 0.0}, 0.14, 4.0};
+constexpr Model kSmallBf16 = {{0.48, 0.60, 0.78}, 0.0, 4.7};
+constexpr Model kSmallFp32 = {{1.37, 1.70, 0.0}, 0.0, 5.0};
+constexpr double kLaunchUs = 3.0;
+constexpr double kPartialsPerUs = 7.5e5;   // partial sums written and read back
+constexpr double kExpandPerUs = 1.7e6;     // codes expanded to bf16
+
+double modelled(const Model& m, int64_t groups, int64_t per, int64_t slices, double elems) {
+    int most = 1;
+    while (most < 3 && m.stage[most] > 0.0) ++most;
+    const int64_t rounds = ceil_div(groups, kCus * most);
+    const int64_t share = std::min<int64_t>(most, ceil_div(groups, kCus));
+    const double busy = groups < kCus ? (double)groups / kCus : 1.0;
+    return rounds * (per * (m.stage[share - 1] - m.idle * (1.0 - busy)) + m.fixed) +
+           (slices > 1 ? kLaunchUs + slices * elems / kPartialsPerUs : 0.0);
+}
 
 }  // namespace
 
@@ -636,36 +704,39 @@ bool linear_grad_big_rows(const void* dy, int64_t n_out, int64_t stride) {
 
 LgPlan linear_grad_plan(int64_t n_tokens, int64_t n_out, int64_t n_in, int32_t dy_dtype,
                         bool big_rows) {
-    LgPlan p;
-    p.big = big_rows && dy_dtype == MA_PARAM_BF16 && n_out >= 1024 && n_in >= 256 &&
-            n_tokens >= 1024;
-    const int64_t tile = p.big ? kBigTile : kTile;
-    const Cost& c = p.big ? kBigCost : kSmallCost;
     const int64_t stages = ceil_div(n_tokens, kLgStage);
-    p.tiles_n = ceil_div(n_out, tile);
-    p.tiles_k = ceil_div(n_in, tile);
-    const int64_t tiles = p.tiles_n * p.tiles_k;
     const double elems = (double)n_out * (double)n_in;
-    // the slice count with the least predicted time: rounds of workgroups, each
-    // its stages and fixed cost, then the partial sums' way out and back
-    double best = 0.0;
-    p.per = std::max<int64_t>(1, stages);
-    for (int64_t n = 1; n <= 64 && n <= std::max<int64_t>(1, stages / 4); ++n) {
-        const int64_t per = ceil_div(stages, n), used = stages ? ceil_div(stages, per) : 1;
-        const double t = (double)ceil_div(tiles * used, c.groups) * (per + c.fixed) * c.stage_us +
-                         (used > 1 ? 4.0 + used * elems / kJoinPerUs : 0.0);
-        if (n == 1 || t < best) {
-            best = t;
-            p.slices = used;
-            p.per = std::max<int64_t>(1, per);
+    const bool bf16 = dy_dtype == MA_PARAM_BF16;
+    LgPlan best;
+    double least = -1.0;
+    for (int big = 0; big < 2; ++big) {
+        // (below 512 outputs the expansion of X costs more than it saves)
+        if (big && !(big_rows && bf16 && n_out >= 512 && n_in >= 256 && n_tokens >= 512)) continue;
+        const int64_t tile = big ? kBigTile : kTile;
+        const Model& m = big ? kBigModel : bf16 ? kSmallBf16 : kSmallFp32;
+        LgPlan p;
+        p.big = big != 0;
+        p.tiles_n = ceil_div(n_out, tile);
+        p.tiles_k = ceil_div(n_in, tile);
+        const int64_t tiles = p.tiles_n * p.tiles_k;
+        const double expand =
+            big ? kLaunchUs + (double)n_tokens * (double)round_up(n_in, kBigTile) / kExpandPerUs : 0.0;
+        for (int64_t n = 1; n <= 64 && n <= std::max<int64_t>(1, stages / 4); ++n) {
+            p.per = std::max<int64_t>(1, ceil_div(stages, n));
+            p.slices = std::max<int64_t>(1, ceil_div(stages, p.per));
+            const double t = expand + modelled(m, tiles * p.slices, p.per, p.slices, elems);
+            if (least < 0.0 || t < least) {
+                least = t;
+                best = p;
+            }
         }
     }
-    p.total = p.slices > 1 ? (size_t)round_up(p.slices * n_out * n_in * 4, 256) : 0;
-    if (p.big) {
-        p.xt_off = p.total;
-        p.total += (size_t)(stages * kLgStage) * (size_t)round_up(n_in, kBigTile) * 2;
+    best.total = best.slices > 1 ? (size_t)round_up(best.slices * n_out * n_in * 4, 256) : 0;
+    if (best.big) {
+        best.xt_off = best.total;
+        best.total += (size_t)(stages * kLgStage) * (size_t)round_up(n_in, kBigTile) * 2;
     }
-    return p;
+    return best;
 }
 
 namespace {
@@ -715,7 +786,10 @@ int launch_small_as(const LgArgs& a, const LgPlan& p, hipStream_t st) {
 
 int launch_small(const LgArgs& a, const LgPlan& p, hipStream_t st) {
     const bool bf16 = a.dy_dtype == MA_PARAM_BF16;
-    const bool al = aligned16(a.dy) && a.n_out % 8 == 0 && a.dy_stride % (bf16 ? 8 : 4) == 0;
+    const bool al = aligned16(a.dy) && a.n_out % 8 == 0 && a.dy_stride % (bf16 ? 8 : 4) == 0 &&
+                    a.dy_stride >= a.n_out &&
+                    p.per * kLgStage * std::max(a.dy_stride * (bf16 ? 2 : 4), act_code_pitch(a.n_in)) <
+                        (int64_t(1) << 31);
     if (bf16) return al ? launch_small_as<__bf16, true>(a, p, st) : launch_small_as<__bf16, false>(a, p, st);
     return al ? launch_small_as<float, true>(a, p, st) : launch_small_as<float, false>(a, p, st);
 }

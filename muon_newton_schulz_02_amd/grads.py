@@ -104,27 +104,55 @@ def _token_bytes(tokens) -> int:
     raise TypeError("tokens must be int32 or int64 (got %s)" % tokens.dtype)
 
 
-class _On(contextlib.ExitStack):
-    """The device and stream of a call made current, for its allocations and
-    launches, where they are not already; `.raw` is the stream's handle."""
+# (the same numbers as torch.cuda.current_device() and current_stream(), without
+# building the objects around them: a quarter of a small call's host time)
+_device_now = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
-    def __init__(self, dev, stream, tensors=()):
+
+class _Here:
+    """The current stream of the current device, already right."""
+
+    __slots__ = ("raw",)
+
+    def __init__(self, raw):
+        self.raw = raw
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        return False
+
+
+class _Elsewhere(contextlib.ExitStack):
+    """Another device or stream, made current for a call's allocations and
+    launches."""
+
+    def __init__(self, dev, stream, tensors):
         super().__init__()
-        if dev.index != torch.cuda.current_device():
-            self.enter_context(torch.cuda.device(dev))
+        self.enter_context(torch.cuda.device(dev))
         if stream is None:
-            self.raw = torch.cuda.current_stream(dev).cuda_stream
+            self.raw = _raw_stream(dev.index)
             return
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=dev)
         self.raw = stream.cuda_stream
-        if self.raw != torch.cuda.current_stream(dev).cuda_stream:
+        if self.raw != _raw_stream(dev.index):
             # memory of another stream's tensors is not handed out again before this
             # stream is done with them
             for t in tensors:
                 if t is not None:
                     t.record_stream(stream)
             self.enter_context(torch.cuda.stream(stream))
+
+
+def _on(dev, stream, tensors):
+    """The context a call allocates and launches in; `.raw` is its stream."""
+    if stream is None and dev.index == _device_now():
+        return _Here(_raw_stream(dev.index))
+    return _Elsewhere(dev, stream, tensors)
 
 
 def _out_like(out, what: str, shape, dtype, dev):
@@ -135,6 +163,15 @@ def _out_like(out, what: str, shape, dtype, dev):
         raise ValueError("%s has shape %s, the call gives %s" % (what, tuple(out.shape),
                                                                  tuple(shape)))
     return out
+
+
+def _out_as(out, what: str, x):
+    """An output of x's shape and type."""
+    if out is None:
+        return torch.empty_like(x, memory_format=torch.contiguous_format)
+    if out.dtype != x.dtype:
+        raise TypeError("%s must be %s" % (what, x.dtype))
+    return _out_like(out, what, x.shape, x.dtype, x.device)
 
 
 def _workspace(workspace, need: int, dev):
@@ -198,6 +235,10 @@ class ActCheckpoint:
         cols, rows = shape[-1], 1
         for d in shape[:-1]:
             rows *= d
+        return ActCheckpoint._empty(shape, rows, cols, device)
+
+    @staticmethod
+    def _empty(shape, rows, cols, device):
         if cols < 1:
             raise ValueError("an activation needs at least one feature")
         pitch = -(-cols // MA_ACT_GROUP) * MA_ACT_GROUP
@@ -205,7 +246,13 @@ class ActCheckpoint:
         c.codes = torch.empty((rows, pitch), dtype=torch.int8, device=device)
         c.exps = torch.empty((rows, -(-pitch // (4 * MA_ACT_GROUP)) * 4), dtype=torch.uint8,
                              device=device)
-        c.cols, c.shape = cols, shape
+        c.cols, c.shape = cols, tuple(shape)
+        return c
+
+    def _like(self):
+        c = object.__new__(ActCheckpoint)
+        c.codes, c.exps = torch.empty_like(self.codes), torch.empty_like(self.exps)
+        c.cols, c.shape = self.cols, self.shape
         return c
 
 
@@ -229,9 +276,9 @@ def ma_act_pack(x, out: Optional[ActCheckpoint] = None, stream=None) -> ActCheck
     if out is not None:
         _held(out, "out", rows, cols)
         _same_device(dev, ("out", out.codes), ("out", out.exps))
-    with _On(dev, stream, (x,) if out is None else (x, out.codes, out.exps)) as on:
+    with _on(dev, stream, (x,) if out is None else (x, out.codes, out.exps)) as on:
         if out is None:
-            out = ActCheckpoint.empty(x.shape, dev)
+            out = ActCheckpoint._empty(x.shape, rows, cols, dev)
         rc = _abi.load().ma_act_pack(x.data_ptr(), dt, rows, cols, ld, out.codes.data_ptr(),
                                      out.exps.data_ptr(), on.raw)
     if rc:
@@ -244,7 +291,7 @@ def ma_act_unpack(ckpt: ActCheckpoint, dtype=torch.float32, out=None, stream=Non
     _held(ckpt, "ckpt")
     dev = ckpt.codes.device
     _same_device(dev, ("exps", ckpt.exps), ("out", out))
-    with _On(dev, stream, (ckpt.codes, ckpt.exps, out)) as on:
+    with _on(dev, stream, (ckpt.codes, ckpt.exps, out)) as on:
         out = _out_like(out, "out", ckpt.shape, dtype, dev)
         rows, cols, ld = _rows(out, "out")
         rc = _abi.load().ma_act_unpack(ckpt.codes.data_ptr(), ckpt.exps.data_ptr(), rows, cols,
@@ -270,7 +317,7 @@ def ma_embedding_lookup(table, tokens, scale: float = 1.0, out=None, out_dtype=N
     dt = _dtype(table, "table")
     dev = table.device
     _same_device(dev, ("tokens", tokens), ("out", out))
-    with _On(dev, stream, (table, tokens, out)) as on:
+    with _on(dev, stream, (table, tokens, out)) as on:
         out = _out_like(out, "out", tuple(tokens.shape) + (hidden,), out_dtype or table.dtype, dev)
         rows, _, old = _rows(out, "out")
         rc = _abi.load().ma_embedding_lookup(table.data_ptr(), dt, vocab, hidden, ld,
@@ -282,8 +329,9 @@ def ma_embedding_lookup(table, tokens, scale: float = 1.0, out=None, out_dtype=N
 
 
 def ma_embedding_grad_workspace_size(n_tokens: int, vocab: int, hidden: int) -> int:
+    lib = _abi.load()
     n = C.c_size_t()
-    rc = _abi.load().ma_embedding_grad_workspace_size(n_tokens, vocab, hidden, C.byref(n))
+    rc = lib.ma_embedding_grad_workspace_size(n_tokens, vocab, hidden, C.byref(n))
     if rc:
         _fail(rc, "ma_embedding_grad_workspace_size")
     return n.value
@@ -313,7 +361,7 @@ def ma_embedding_grad(dout, tokens, vocab: int, scale: float = 1.0, padding_toke
     _same_device(dev, ("tokens", tokens), ("out", out))
     vocab = int(vocab)
     need = ma_embedding_grad_workspace_size(rows, vocab, hidden)
-    with _On(dev, stream, (dout, tokens, out, workspace)) as on:
+    with _on(dev, stream, (dout, tokens, out, workspace)) as on:
         out = _out_like(out, "out", (vocab, hidden), grad_dtype, dev)
         if not out.is_contiguous():
             raise ValueError("out must be contiguous")
@@ -359,7 +407,7 @@ def ma_linear_grad(dy, x: ActCheckpoint, out=None, accumulate: bool = False,
     rc = lib.ma_linear_grad_workspace_size(rows, n_out, x.cols, dt, C.byref(size))
     if rc:
         _fail(rc, "ma_linear_grad")
-    with _On(dev, stream, (dy, x.codes, x.exps, out, workspace)) as on:
+    with _on(dev, stream, (dy, x.codes, x.exps, out, workspace)) as on:
         out = _out_like(out, "out", (n_out, x.cols), grad_dtype, dev)
         if not out.is_contiguous():
             raise ValueError("out must be contiguous")
@@ -402,12 +450,10 @@ def ma_glu_forward(gate, up, act="silu", out=None, gate_ckpt: Optional[ActCheckp
             _same_device(dev, (what, c.codes), (what, c.exps))
     used = [gate, up, out] + [t for c in (gate_ckpt, up_ckpt) if c is not None
                               for t in (c.codes, c.exps)]
-    with _On(dev, stream, used) as on:
-        out = _out_like(out, "out", gate.shape, gate.dtype, dev)
-        if out.dtype != gate.dtype:
-            raise TypeError("out must be %s" % gate.dtype)
-        gate_ckpt = gate_ckpt or ActCheckpoint.empty(gate.shape, dev)
-        up_ckpt = up_ckpt or ActCheckpoint.empty(gate.shape, dev)
+    with _on(dev, stream, used) as on:
+        out = _out_as(out, "out", gate)
+        gate_ckpt = gate_ckpt or ActCheckpoint._empty(gate.shape, rows, cols, dev)
+        up_ckpt = up_ckpt or gate_ckpt._like()
         rc = _abi.load().ma_glu_forward(
             gate.data_ptr(), up.data_ptr(), dt, rows, cols, gld, uld, _act(act), out.data_ptr(),
             _rows(out, "out")[2], gate_ckpt.codes.data_ptr(), gate_ckpt.exps.data_ptr(),
@@ -437,13 +483,11 @@ def ma_glu_backward(dh, gate: ActCheckpoint, up: ActCheckpoint, act="silu", dgat
         _held(h_ckpt, "h_ckpt", rows, cols)
         _same_device(dev, ("h_ckpt", h_ckpt.codes), ("h_ckpt", h_ckpt.exps))
         used += [h_ckpt.codes, h_ckpt.exps]
-    with _On(dev, stream, used) as on:
-        dgate = _out_like(dgate, "dgate", dh.shape, dh.dtype, dev)
-        dup = _out_like(dup, "dup", dh.shape, dh.dtype, dev)
-        if dgate.dtype != dh.dtype or dup.dtype != dh.dtype:
-            raise TypeError("dgate and dup must be %s" % dh.dtype)
+    with _on(dev, stream, used) as on:
+        dgate = _out_as(dgate, "dgate", dh)
+        dup = _out_as(dup, "dup", dh)
         if hold and h_ckpt is True:
-            h_ckpt = ActCheckpoint.empty(dh.shape, dev)
+            h_ckpt = ActCheckpoint._empty(dh.shape, rows, cols, dev)
         rc = _abi.load().ma_glu_backward(
             dh.data_ptr(), dt, rows, cols, ld, gate.codes.data_ptr(), gate.exps.data_ptr(),
             up.codes.data_ptr(), up.exps.data_ptr(), _act(act), dgate.data_ptr(),
