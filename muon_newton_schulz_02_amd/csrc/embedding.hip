@@ -106,6 +106,7 @@ struct SortIn {
     int64_t n, vocab, pad;
     int32_t token_bytes;    // 4, 8; 0: keys and pos
     int32_t shift, bits;
+    int32_t blocks;
     int64_t per;            // entries per block
 };
 
@@ -113,27 +114,6 @@ __device__ __forceinline__ uint32_t sort_key(const SortIn& s, int64_t i) {
     if (s.token_bytes == 8) return token_key((const int64_t*)s.tokens, i, s.vocab, s.pad);
     if (s.token_bytes == 4) return token_key((const int32_t*)s.tokens, i, s.vocab, s.pad);
     return s.keys[i];
-}
-
-// Digit counts of each block's entries: counts[block][digit].  The first pass
-// also clears the flags.
-__global__ __launch_bounds__(kSortThreads) void k_sort_count(SortIn s, uint32_t* __restrict__ counts) {
-    __shared__ uint32_t hist[kMaxDigits];
-    const int nd = 1 << s.bits;
-    for (int d = threadIdx.x; d < nd; d += kSortThreads) hist[d] = 0;
-    __syncthreads();
-    const int64_t i0 = (int64_t)blockIdx.x * s.per, i1 = min(s.n, i0 + s.per);
-    for (int64_t i = i0 + threadIdx.x; i < i1; i += kSortThreads)
-        atomicAdd(&hist[(sort_key(s, i) >> s.shift) & (nd - 1)], 1u);
-    if (s.token_bytes) {
-        // (the flags' memory is 16-byte aligned and padded to 16)
-        for (int64_t v = ((int64_t)blockIdx.x * kSortThreads + threadIdx.x) * 16; v < s.vocab;
-             v += (int64_t)gridDim.x * kSortThreads * 16)
-            *reinterpret_cast<u32x4*>(s.flags + v) = (u32x4){0u, 0u, 0u, 0u};
-    }
-    __syncthreads();
-    for (int d = threadIdx.x; d < nd; d += kSortThreads)
-        counts[(int64_t)blockIdx.x * nd + d] = hist[d];
 }
 
 // Exclusive prefix over the digits, digit `tid` each (nd <= kSortThreads).
@@ -183,6 +163,82 @@ __device__ __forceinline__ uint32_t wave_rank(uint32_t* count, uint32_t digit, i
     return base + rank;
 }
 
+// Zeroing of rows without a token, by workgroups that ride along in launches which
+// leave most of the GPU idle.
+constexpr int kFillRows = 32;     // rows a workgroup takes at a time
+struct FillArgs {
+    void* grad;
+    const uint8_t* flags;
+    int64_t r0, r1, groups;       // rows, and workgroups that share them
+    int32_t hidden, bf16, al;
+    int32_t lane_bits;            // lanes (log2) that take a row
+};
+
+// Rows [r0, r1) of the gradient that no token has, set to zero by `groups`
+// workgroups of which this is number `g`.
+template <typename TG, bool AL>
+__device__ __forceinline__ void zero_rows(const FillArgs& f, int64_t g) {
+    const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    const int lanes = 1 << f.lane_bits, per = (int)blockDim.x >> f.lane_bits;
+    const int lane = threadIdx.x & (lanes - 1), sub = threadIdx.x >> f.lane_bits;
+    TG* grad = static_cast<TG*>(f.grad);
+    for (int64_t r0 = f.r0 + g * kFillRows; r0 < f.r1; r0 += f.groups * kFillRows) {
+        const int64_t r1 = min(f.r1, r0 + kFillRows);
+        for (int64_t r = r0 + sub; r < r1; r += per) {
+            // (without any token there are no flags: every row is empty)
+            if (f.flags && f.flags[r] != 0) continue;
+            for (int col = lane * 8; col < f.hidden; col += lanes * 8)
+                store_unit<TG, AL>(grad + r * f.hidden + col, f.hidden - col, zero);
+        }
+    }
+}
+
+__device__ __forceinline__ void fill(const FillArgs& f, int64_t g) {
+    if (f.bf16) {
+        if (f.al) zero_rows<__bf16, true>(f, g);
+        else zero_rows<__bf16, false>(f, g);
+    } else {
+        if (f.al) zero_rows<float, true>(f, g);
+        else zero_rows<float, false>(f, g);
+    }
+}
+
+// Digit counts of each block's entries: counts[block][digit].  The first pass
+// also clears the flags; later ones carry workgroups that zero rows.
+__global__ __launch_bounds__(kSortThreads) void k_sort_count(SortIn s, uint32_t* __restrict__ counts,
+                                                             FillArgs f) {
+    if ((int)blockIdx.x >= s.blocks) {
+        fill(f, (int)blockIdx.x - s.blocks);
+        return;
+    }
+    __shared__ uint32_t hist[kSortWaves][kMaxDigits];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int nd = 1 << s.bits;
+    for (int d = lane; d < nd; d += 64) hist[wave][d] = 0;
+    wave_lds_sync();
+    const int64_t i0 = (int64_t)blockIdx.x * s.per, i1 = min(s.n, i0 + s.per);
+    // (uniform over the wave; one addition per digit and wave, since most of a
+    // batch may share a digit)
+    for (int64_t i = i0 + wave * 64; i < i1; i += kSortThreads) {
+        const bool valid = i + lane < i1;
+        const uint32_t d = valid ? (sort_key(s, i + lane) >> s.shift) & (uint32_t)(nd - 1) : 0u;
+        wave_rank(hist[wave], d, s.bits, valid);
+    }
+    if (s.token_bytes) {
+        // (the flags' memory is 16-byte aligned and padded to 16)
+        for (int64_t v = ((int64_t)blockIdx.x * kSortThreads + tid) * 16; v < s.vocab;
+             v += (int64_t)s.blocks * kSortThreads * 16)
+            *reinterpret_cast<u32x4*>(s.flags + v) = (u32x4){0u, 0u, 0u, 0u};
+    }
+    __syncthreads();
+    if (tid < nd) {
+        uint32_t c = 0;
+#pragma unroll
+        for (int w = 0; w < kSortWaves; ++w) c += hist[w][tid];
+        counts[(int64_t)blockIdx.x * nd + tid] = c;
+    }
+}
+
 // Stable scatter of each block's entries to their sorted places: the entries of
 // a digit go after those of smaller digits, then of earlier blocks, then of
 // earlier waves (each wave owns a contiguous part of the block's range and
@@ -190,7 +246,12 @@ __device__ __forceinline__ uint32_t wave_rank(uint32_t* count, uint32_t digit, i
 __global__ __launch_bounds__(kSortThreads) void k_sort_scatter(SortIn s,
                                                                const uint32_t* __restrict__ counts,
                                                                uint32_t* __restrict__ keys_out,
-                                                               int32_t* __restrict__ pos_out) {
+                                                               int32_t* __restrict__ pos_out,
+                                                               FillArgs f) {
+    if ((int)blockIdx.x >= s.blocks) {
+        fill(f, (int)blockIdx.x - s.blocks);
+        return;
+    }
     __shared__ uint32_t next[kSortWaves][kMaxDigits];
     __shared__ uint32_t wave_sum[kSortWaves];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -198,20 +259,33 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_scatter(SortIn s,
     const int64_t i0 = (int64_t)blockIdx.x * s.per, i1 = min(s.n, i0 + s.per);
     const int64_t part = (s.per + kSortWaves - 1) / kSortWaves;
     const int64_t w0 = min(i1, i0 + wave * part), w1 = min(i1, w0 + part);
+    for (int d = lane; d < nd; d += 64) next[wave][d] = 0;
+    wave_lds_sync();
+    // the wave's first entries stay in registers with their ranks; only where it has more
+    // (above 131072 tokens) are those ranked again below
+    uint32_t key0 = 0, at0 = 0;
+    int32_t pos0 = 0;
+    const bool valid0 = w0 + lane < w1;
+    if (valid0) {
+        key0 = sort_key(s, w0 + lane);
+        pos0 = s.token_bytes ? (int32_t)(w0 + lane) : s.pos[w0 + lane];
+    }
     // over all blocks: total of this thread's digit, and what earlier blocks hold of it
     uint32_t all = 0, before = 0;
     if (tid < nd) {
-#pragma unroll 8
-        for (int b = 0; b < (int)gridDim.x; ++b) {
+#pragma unroll 16
+        for (int b = 0; b < s.blocks; ++b) {
             const uint32_t c = counts[(int64_t)b * nd + tid];
             all += c;
             before += b < (int)blockIdx.x ? c : 0u;
         }
     }
-    for (int d = lane; d < nd; d += 64) next[wave][d] = 0;
-    wave_lds_sync();
-    for (int64_t i = w0 + lane; i < w1; i += 64)
-        atomicAdd(&next[wave][(sort_key(s, i) >> s.shift) & (nd - 1)], 1u);
+    if (w0 < w1) at0 = wave_rank(next[wave], (key0 >> s.shift) & (uint32_t)(nd - 1), s.bits, valid0);
+    for (int64_t i = w0 + 64; i < w1; i += 64) {
+        const bool valid = i + lane < w1;
+        const uint32_t d = valid ? (sort_key(s, i + lane) >> s.shift) & (uint32_t)(nd - 1) : 0u;
+        wave_rank(next[wave], d, s.bits, valid);
+    }
     const uint32_t start = digit_prefix(all, wave_sum);     // (a barrier: all counts are in)
     if (tid < nd) {
         uint32_t at = start + before;
@@ -223,17 +297,23 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_scatter(SortIn s,
         }
     }
     __syncthreads();
+    auto place = [&](uint32_t at, uint32_t key, int32_t pos) {
+        keys_out[at] = key;
+        pos_out[at] = pos;
+        if (s.token_bytes && key < (uint32_t)s.vocab) s.flags[key] = 1;
+    };
+    const uint32_t d0 = (key0 >> s.shift) & (uint32_t)(nd - 1);
+    if (w1 - w0 <= 64) {
+        if (valid0) place(next[wave][d0] + at0, key0, pos0);
+        return;
+    }
     // (the loop is uniform over the wave; next[wave] is this wave's own)
     for (int64_t i = w0; i < w1; i += 64) {
         const bool valid = i + lane < w1;
         const uint32_t key = valid ? sort_key(s, i + lane) : 0u;
         const int32_t pos = valid ? (s.token_bytes ? (int32_t)(i + lane) : s.pos[i + lane]) : 0;
         const uint32_t at = wave_rank(next[wave], (key >> s.shift) & (uint32_t)(nd - 1), s.bits, valid);
-        if (valid) {
-            keys_out[at] = key;
-            pos_out[at] = pos;
-            if (s.token_bytes && key < (uint32_t)s.vocab) s.flags[key] = 1;
-        }
+        if (valid) place(at, key, pos);
     }
 }
 
@@ -320,9 +400,10 @@ struct SumArgs {
     const void* dout;
     void* grad;
     float* partials;              // [n_chunks][2][pitch]: head, tail
+    uint32_t* tails;              // per chunk: the row whose run begins in it and goes on, or vocab
+    uint8_t* through;             // per chunk: does the run it begins with go on through it all?
     const uint32_t* keys;
     const int32_t* pos;
-    const uint8_t* flags;
     int64_t dout_stride, n, vocab, n_chunks;
     int64_t sum_blocks;           // workgroups before those that zero rows
     int64_t pitch;                // of a partial row: hidden rounded up to 8
@@ -332,21 +413,9 @@ struct SumArgs {
     int32_t lane_bits;            // lanes (log2) that take a row
 };
 
-constexpr int kFillRows = 32;     // rows a zeroing workgroup looks at
 constexpr int kSumDepth = 8;      // rows of dout in flight per thread
 constexpr int kMaxChunk = 256;
-constexpr int kMinSumLanes = 32;  // so a workgroup holds at most 8 chunks
-
-// First sorted entry whose key is at least `key`.
-__device__ __forceinline__ int64_t lower_bound(const uint32_t* keys, int64_t n, uint32_t key) {
-    int64_t lo = 0, hi = n;
-    while (lo < hi) {
-        const int64_t mid = (lo + hi) >> 1;
-        if (keys[mid] < key) lo = mid + 1;
-        else hi = mid;
-    }
-    return lo;
-}
+constexpr int kSumEntries = 2048; // sorted entries a workgroup holds
 
 template <typename TG, bool AL>
 __device__ __forceinline__ void write_row(const SumArgs& a, uint32_t key, int col, float* acc) {
@@ -361,13 +430,6 @@ __device__ __forceinline__ void write_row(const SumArgs& a, uint32_t key, int co
         for (int e = 0; e < 8; ++e) acc[e] *= a.scale;
     }
     store_unit<TG, AL>(g, a.hidden - col, acc);
-}
-
-template <typename TG, bool AL>
-__device__ __forceinline__ void zero_row(TG* g, int hidden, int first, int step) {
-    const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int col = first * 8; col < hidden; col += step * 8)
-        store_unit<TG, AL>(g + col, hidden - col, zero);
 }
 
 // acc += rows at[0 .. cnt) of dout from column `col` on, in order, kSumDepth at a time.
@@ -390,16 +452,11 @@ __device__ __forceinline__ void add_rows(float* acc, const TD* dout, int64_t str
 
 // Workgroups [0, sum_blocks): the chunks; the rest: rows without a token.
 template <typename TD, typename TG, bool AL>
-__global__ __launch_bounds__(kThreads) void k_emb_sum(SumArgs a) {
-    __shared__ uint32_t s_key[kThreads / kMinSumLanes][kMaxChunk];
-    __shared__ int32_t s_pos[kThreads / kMinSumLanes][kMaxChunk];
+__global__ __launch_bounds__(kThreads) void k_emb_sum(SumArgs a, FillArgs f) {
+    __shared__ uint32_t s_key[kSumEntries];
+    __shared__ int32_t s_pos[kSumEntries];
     if ((int64_t)blockIdx.x >= a.sum_blocks) {
-        const int64_t r0 = ((int64_t)blockIdx.x - a.sum_blocks) * kFillRows;
-        const int rows = (int)min<int64_t>(kFillRows, a.vocab - r0);
-        // (without any token there are no flags: every row is empty)
-        for (int r = 0; r < rows; ++r)
-            if (a.n == 0 || a.flags[r0 + r] == 0)
-                zero_row<TG, AL>(static_cast<TG*>(a.grad) + (r0 + r) * a.hidden, a.hidden, threadIdx.x, kThreads);
+        zero_rows<TG, AL>(f, (int64_t)blockIdx.x - a.sum_blocks);
         return;
     }
     const int lanes = 1 << a.lane_bits, per = kThreads >> a.lane_bits;
@@ -407,17 +464,25 @@ __global__ __launch_bounds__(kThreads) void k_emb_sum(SumArgs a) {
     const int64_t c = (int64_t)blockIdx.x * per + sub;
     const int64_t i0 = c * a.chunk;
     const int cnt = c < a.n_chunks ? (int)min<int64_t>(a.chunk, a.n - i0) : 0;
+    uint32_t* key = s_key + sub * a.chunk;
+    int32_t* pos = s_pos + sub * a.chunk;
+    const uint32_t none = (uint32_t)a.vocab;
+    // the neighbours' nearest keys (none: they do not continue)
+    const uint32_t prev = cnt > 0 && i0 > 0 ? a.keys[i0 - 1] : none;
+    const uint32_t next = cnt > 0 && i0 + cnt < a.n ? a.keys[i0 + cnt] : none;
     for (int i = lane; i < cnt; i += lanes) {
-        s_key[sub][i] = a.keys[i0 + i];
-        s_pos[sub][i] = a.pos[i0 + i];
+        key[i] = a.keys[i0 + i];
+        pos[i] = a.pos[i0 + i];
     }
     __syncthreads();
     if (cnt == 0) return;
-    const uint32_t* key = s_key[sub];
-    const int32_t* pos = s_pos[sub];
-    const uint32_t first = key[0], last = key[cnt - 1], none = (uint32_t)a.vocab;
-    const bool from_before = i0 > 0 && a.keys[i0 - 1] == first;
-    const bool goes_on = i0 + cnt < a.n && a.keys[i0 + cnt] == last;
+    const uint32_t first = key[0], last = key[cnt - 1];
+    const bool from_before = prev == first, goes_on = next == last;
+    if (lane == 0) {
+        const bool through = from_before && goes_on && first == last;
+        a.tails[c] = goes_on && !through ? last : none;     // (none where it is the row of no token, too)
+        a.through[c] = through;
+    }
     const TD* dout = static_cast<const TD*>(a.dout);
     for (int col = lane * 8; col < a.hidden; col += lanes * 8) {
         float acc[8];
@@ -457,63 +522,87 @@ __global__ __launch_bounds__(kThreads) void k_emb_sum(SumArgs a) {
     }
 }
 
-// Runs that cross chunks: a workgroup looks at kJoinChunks chunks; for each in
-// which such a run begins (grid.y: column slabs) it adds the run's pieces: the tail of
-// that chunk, then the heads of the following ones.  kJoinWays threads share
-// a column unit, each taking every kJoinWays-th piece in rising order; their sums
-// are added in thread order.
-constexpr int kJoinChunks = 8;
+// Runs that cross chunks: a workgroup looks at as many chunks as it has groups of
+// threads; for each in which such a run begins (grid.y: column slabs) it adds the
+// run's pieces: the tail of that chunk, then the heads of the following ones.  A group adds a
+// run of up to kJoinShort pieces by itself; the groups share a longer one, each taking
+// every kJoinWays-th piece in rising order, and add their sums in group order.
 constexpr int kJoinWays = 8;
+constexpr int kJoinChunks = kJoinWays;
+constexpr int kJoinShort = 8;
 constexpr int kJoinLanes = kThreads / kJoinWays;    // column units of a slab
 
 template <typename TG, bool AL>
 __global__ __launch_bounds__(kThreads) void k_emb_join(SumArgs a) {
     __shared__ float part[kJoinWays][kJoinLanes][8];
     __shared__ int s_pieces[kJoinChunks];
+    __shared__ uint32_t s_row[kJoinChunks];
     const int64_t c0 = (int64_t)blockIdx.x * kJoinChunks;
-    if (threadIdx.x < kJoinChunks) {
-        const int64_t c = c0 + threadIdx.x;
+    for (int j = threadIdx.x >> 6; j < kJoinChunks; j += kThreads / 64) {      // (a wave each)
+        const int64_t c = c0 + j;
+        const int l = threadIdx.x & 63;
+        const uint32_t row = c < a.n_chunks ? a.tails[c] : (uint32_t)a.vocab;
         int pieces = 0;
-        const int64_t i0 = c * a.chunk, i1 = i0 + a.chunk;
-        if (c < a.n_chunks && i1 < a.n) {
-            const uint32_t key = a.keys[i1 - 1];
-            if (key != (uint32_t)a.vocab && a.keys[i1] == key &&
-                !(i0 > 0 && a.keys[i0] == key && a.keys[i0 - 1] == key)) {
-                const int64_t end = lower_bound(a.keys, a.n, key + 1u);     // one past the run
-                pieces = (int)((end - 1) / a.chunk - c + 1);
+        if (row != (uint32_t)a.vocab) {
+            // the chunk the run ends in: the first after c that it does not go
+            // through, 1024 of them looked at per step
+            for (int64_t base = (c + 1) & ~int64_t(15);; base += 1024) {
+                const int64_t i0 = base + 16 * l;
+                u32x4 w = {0u, 0u, 0u, 0u};
+                if (i0 < a.n_chunks) w = *reinterpret_cast<const u32x4*>(a.through + i0);
+                int stop = 16;
+#pragma unroll
+                for (int k = 15; k >= 0; --k) {
+                    const bool on = ((w[k >> 2] >> (8 * (k & 3))) & 0xffu) != 0 && i0 + k < a.n_chunks;
+                    if (i0 + k > c && !on) stop = k;
+                }
+                const uint64_t any = __ballot(stop < 16);
+                if (any) {
+                    const int at = __builtin_ctzll(any);
+                    pieces = (int)(base + 16 * at + __shfl(stop, at, 64) - c) + 1;
+                    break;
+                }
             }
         }
-        s_pieces[threadIdx.x] = pieces;
+        if (l == 0) {
+            s_pieces[j] = pieces;
+            s_row[j] = row;
+        }
     }
     __syncthreads();
     const int way = threadIdx.x / kJoinLanes, lane = threadIdx.x % kJoinLanes;
     const int col = ((int)blockIdx.y * kJoinLanes + lane) * 8;
-    for (int j = 0; j < kJoinChunks; ++j) {
-        const int pieces = s_pieces[j];
-        if (pieces == 0) continue;
-        const int64_t c = c0 + j;
-        float acc[8];
+    // piece p of the run that begins in chunk c
+    auto add_pieces = [&](float* acc, int64_t c, int p0, int step, int pieces) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-        if (col < a.hidden) {
 #pragma unroll 4
-            for (int p = way; p < pieces; p += kJoinWays) {
-                float v[8];
-                load_v<float, 8>(a.partials + ((c + p) * 2 + (p == 0 ? 1 : 0)) * a.pitch + col, v);
+        for (int p = p0; p < pieces; p += step) {
+            float v[8];
+            load_v<float, 8>(a.partials + ((c + p) * 2 + (p == 0 ? 1 : 0)) * a.pitch + col, v);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) acc[e] += v[e];
-            }
+            for (int e = 0; e < 8; ++e) acc[e] += v[e];
         }
+    };
+    float acc[8];
+    const int own = s_pieces[way];
+    if (own > 0 && own <= kJoinShort && col < a.hidden) {
+        add_pieces(acc, c0 + way, 0, 1, own);
+        write_row<TG, AL>(a, s_row[way], col, acc);
+    }
+    for (int j = 0; j < kJoinChunks; ++j) {
+        if (s_pieces[j] <= kJoinShort) continue;
+        const int64_t c = c0 + j;
+        if (col < a.hidden) add_pieces(acc, c, way, kJoinWays, s_pieces[j]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) part[way][lane][e] = acc[e];
         __syncthreads();
         if (way == 0 && col < a.hidden) {
-            const int ways = min(pieces, kJoinWays);
-            for (int w = 1; w < ways; ++w) {
+            for (int w = 1; w < kJoinWays; ++w) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) acc[e] += part[w][lane][e];
             }
-            write_row<TG, AL>(a, a.keys[(c + 1) * a.chunk - 1], col, acc);
+            write_row<TG, AL>(a, s_row[j], col, acc);
         }
         __syncthreads();
     }
@@ -540,33 +629,43 @@ __global__ __launch_bounds__(kThreads) void k_emb_direct(DirectArgs d) {
     __shared__ int s_row[kDirectTokens];        // table rows (local) of the listed tokens,
     __shared__ uint16_t s_tok[kDirectTokens];   // and their positions, in token order
     __shared__ uint16_t s_pos[kDirectTokens];   // positions by row
-    __shared__ int s_count[W], s_start[kDirectRows + 1];
+    __shared__ int s_count[W * kDirectTokens / kThreads], s_start[kDirectRows + 1];
     __shared__ float part[W][kDirectLanes][8];
     const SumArgs& a = d.sum;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int64_t r0 = (int64_t)blockIdx.x * d.rows;
     const int rows = (int)min<int64_t>(d.rows, a.vocab - r0);
     const int n = (int)d.in.n;
-    int listed = 0;
-    for (int i0 = 0; i0 < n; i0 += kThreads) {
-        const int i = i0 + tid;
-        const int64_t row = i < n ? (int64_t)sort_key(d.in, i) - r0 : -1;
-        const bool mine = row >= 0 && row < rows;
-        const uint64_t m = __ballot(mine);
-        if (lane == 0) s_count[wave] = __popcll(m);
-        __syncthreads();
-        int at = listed + __popcll(m & ((uint64_t(1) << lane) - 1));
+    // token k * kThreads + tid is this thread's k-th
+    constexpr int K = kDirectTokens / kThreads;
+    int row[K], before[K];
 #pragma unroll
-        for (int w = 0; w < W; ++w) {
-            at += w < wave ? s_count[w] : 0;
-            listed += s_count[w];
-        }
-        if (mine) {
-            s_row[at] = (int)row;
-            s_tok[at] = (uint16_t)i;
-        }
-        __syncthreads();
+    for (int k = 0; k < K; ++k) {
+        const int i = k * kThreads + tid;
+        const int64_t r = i < n ? (int64_t)sort_key(d.in, i) - r0 : -1;
+        row[k] = r >= 0 && r < rows ? (int)r : -1;
     }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const uint64_t m = __ballot(row[k] >= 0);
+        if (lane == 0) s_count[k * W + wave] = __popcll(m);
+        before[k] = __popcll(m & ((uint64_t(1) << lane) - 1));
+    }
+    __syncthreads();
+    int listed = 0;
+#pragma unroll
+    for (int c = 0; c < K * W; ++c) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) before[k] += c < k * W + wave ? s_count[c] : 0;
+        listed += s_count[c];
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        if (row[k] < 0) continue;
+        s_row[before[k]] = row[k];
+        s_tok[before[k]] = (uint16_t)(k * kThreads + tid);
+    }
+    __syncthreads();
     // where each row's list begins: entries of smaller rows (a wave counts a row)
     for (int r = wave; r <= rows; r += W) {
         int before = 0;
@@ -645,16 +744,27 @@ int lane_bits_for(int64_t units, int least, int most) {
 // tokens, four launches over many workgroups 15 us.
 static constexpr int64_t kLdsSortTokens = 4096;
 
+// Few tokens into a table of few rows: no sort.  (Each workgroup reads all tokens, so a
+// large table pays for that many times over: 1024 tokens into 151000 x 2048 took 170 us so,
+// against NNN us sorted.)
+static bool direct(int64_t n_tokens, int64_t vocab, int64_t hidden) {
+    return n_tokens <= kDirectTokens && vocab * ceil_div(ceil_div(hidden, 8), kDirectLanes) <= 16384;
+}
+
 EmbPlan embedding_plan(int64_t n_tokens, int64_t vocab, int64_t hidden) {
     EmbPlan p;
-    if (n_tokens <= kDirectTokens) return p;
+    if (n_tokens == 0 || direct(n_tokens, vocab, hidden)) return p;
     int nbits = 1;
     while ((int64_t(1) << nbits) <= vocab) ++nbits;       // keys 0 .. vocab
     p.passes = (nbits + 9) / 10;
     p.bits = (nbits + p.passes - 1) / p.passes;
     p.per = std::max<int64_t>(kSortThreads, round_up(ceil_div(n_tokens, 128), kSortThreads));
     p.blocks = ceil_div(n_tokens, p.per);
-    p.chunk = std::min<int64_t>(kMaxChunk, std::max<int64_t>(16, round_up(ceil_div(n_tokens, 1024), 8)));
+    // chunks for about 256 K threads, of 16 entries at least (a chunk may leave
+    // two partial rows)
+    p.lane_bits = lane_bits_for(ceil_div(hidden, 8), 3, 8);
+    const int64_t most = std::min<int64_t>(kMaxChunk, kSumEntries / (kThreads >> p.lane_bits));
+    p.chunk = std::min(most, std::max<int64_t>(16, round_up((n_tokens << p.lane_bits) >> 18, 8)));
     p.n_chunks = ceil_div(n_tokens, p.chunk);
     p.pitch = round_up(hidden, 8);
     size_t off = 0;
@@ -670,6 +780,8 @@ EmbPlan embedding_plan(int64_t n_tokens, int64_t vocab, int64_t hidden) {
         p.pos[k] = take((size_t)n_tokens * 4);
     }
     if (n_tokens > kLdsSortTokens) p.counts = take((size_t)p.blocks * ((size_t)1 << p.bits) * 4);
+    p.tails = take((size_t)p.n_chunks * 4);
+    p.through = take((size_t)p.n_chunks);
     p.partials = take((size_t)p.n_chunks * 2 * (size_t)p.pitch * 4);
     p.total = off;
     return p;
@@ -726,12 +838,16 @@ void by_types(bool dout_bf16, bool grad_bf16, bool al, F f) {
     else with(float{}, float{});
 }
 
-int launch_sort(const EmbGradArgs& g, const EmbPlan& p, SortIn s, int& at, hipStream_t st) {
+// share(e): the next e eighths of the zeroing, for a launch to carry.
+template <typename F>
+int launch_sort(const EmbGradArgs& g, const EmbPlan& p, SortIn s, int& at, F share, hipStream_t st) {
     auto keys = [&](int k) { return reinterpret_cast<uint32_t*>(g.ws + p.keys[k]); };
     auto pos = [&](int k) { return reinterpret_cast<int32_t*>(g.ws + p.pos[k]); };
     if (g.n_tokens <= kLdsSortTokens) {
         at = 0;
-        if (g.n_tokens <= 2 * kSortThreads)
+        if (g.n_tokens <= kSortThreads)
+            hipLaunchKernelGGL((k_sort_lds<1>), dim3(1), dim3(kSortThreads), 0, st, s, p.passes, keys(0), pos(0));
+        else if (g.n_tokens <= 2 * kSortThreads)
             hipLaunchKernelGGL((k_sort_lds<2>), dim3(1), dim3(kSortThreads), 0, st, s, p.passes, keys(0), pos(0));
         else
             hipLaunchKernelGGL((k_sort_lds<4>), dim3(1), dim3(kSortThreads), 0, st, s, p.passes, keys(0), pos(0));
@@ -745,11 +861,15 @@ int launch_sort(const EmbGradArgs& g, const EmbPlan& p, SortIn s, int& at, hipSt
             s.keys = keys((k - 1) & 1);
             s.pos = pos((k - 1) & 1);
         }
-        hipLaunchKernelGGL(k_sort_count, dim3((unsigned)p.blocks), dim3(kSortThreads), 0, st, s, counts);
+        // (the flags are whole from the second pass on)
+        FillArgs f = share(k == 0 ? 0 : 2);
+        hipLaunchKernelGGL(k_sort_count, dim3((unsigned)(p.blocks + f.groups)), dim3(kSortThreads), 0, st, s,
+                           counts, f);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return (int)e;
-        hipLaunchKernelGGL(k_sort_scatter, dim3((unsigned)p.blocks), dim3(kSortThreads), 0, st, s, counts,
-                           keys(k & 1), pos(k & 1));
+        f = share(k == 0 ? 0 : 2);
+        hipLaunchKernelGGL(k_sort_scatter, dim3((unsigned)(p.blocks + f.groups)), dim3(kSortThreads), 0, st, s,
+                           counts, keys(k & 1), pos(k & 1), f);
         e = hipGetLastError();
         if (e != hipSuccess) return (int)e;
     }
@@ -785,8 +905,9 @@ int launch_embedding_grad(const EmbGradArgs& g, const EmbPlan& p, void* stream) 
     s.pad = g.padding_token;
     s.bits = p.bits;
     s.per = p.per;
+    s.blocks = (int)p.blocks;
     s.token_bytes = g.token_bytes;
-    if (g.n_tokens > 0 && g.n_tokens <= kDirectTokens) {
+    if (g.n_tokens > 0 && direct(g.n_tokens, g.vocab, g.hidden)) {
         DirectArgs d{};
         d.in = s;
         a.lane_bits = lane_bits_for(units, 0, 6);
@@ -801,23 +922,40 @@ int launch_embedding_grad(const EmbGradArgs& g, const EmbPlan& p, void* stream) 
         });
         return (int)hipGetLastError();
     }
+    FillArgs f{};
+    f.grad = g.grad;
+    f.hidden = (int)g.hidden;
+    f.bf16 = bg;
+    f.al = al;
+    f.lane_bits = lane_bits_for(units, 0, 8);
+    // the next `eighths` of the zeroing (8: the rest)
+    auto share = [&](int eighths) {
+        f.r0 = f.r1;
+        if (!g.accumulate)
+            f.r1 = eighths == 8 ? g.vocab : std::min(g.vocab, f.r0 + ceil_div(g.vocab * eighths, 8));
+        f.groups = std::min<int64_t>(ceil_div(f.r1 - f.r0, kFillRows), 32768);
+        return f;
+    };
     if (g.n_tokens > 0) {
         s.flags = reinterpret_cast<uint8_t*>(g.ws + p.flags);
+        f.flags = s.flags;
         int at = 0;
-        const int e = launch_sort(g, p, s, at, st);
+        const int e = launch_sort(g, p, s, at, share, st);
         if (e != (int)hipSuccess) return e;
         a.keys = reinterpret_cast<const uint32_t*>(g.ws + p.keys[at]);
         a.pos = reinterpret_cast<const int32_t*>(g.ws + p.pos[at]);
-        a.flags = s.flags;
         a.partials = reinterpret_cast<float*>(g.ws + p.partials);
+        a.tails = reinterpret_cast<uint32_t*>(g.ws + p.tails);
+        a.through = reinterpret_cast<uint8_t*>(g.ws + p.through);
     }
-    a.lane_bits = lane_bits_for(units, 5, 8);
+    a.lane_bits = p.lane_bits;
     a.sum_blocks = ceil_div(a.n_chunks, kThreads >> a.lane_bits);
-    const int64_t fill = g.accumulate ? 0 : ceil_div(g.vocab, kFillRows);
-    const dim3 grid((unsigned)(a.sum_blocks + fill));
+    const FillArgs rest = share(8);
+    const dim3 grid((unsigned)(a.sum_blocks + rest.groups));
+    if (grid.x == 0) return (int)hipSuccess;
     by_types(bd, bg, al, [&](auto td, auto tg, auto w) {
         hipLaunchKernelGGL((k_emb_sum<decltype(td), decltype(tg), decltype(w)::value>), grid,
-                           dim3(kThreads), 0, st, a);
+                           dim3(kThreads), 0, st, a, rest);
     });
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.n_chunks < 2) return (int)e;

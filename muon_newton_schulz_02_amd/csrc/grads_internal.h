@@ -44,10 +44,12 @@ struct EmbPlan {
     int64_t per = 0, blocks = 0;
     int64_t chunk = 0, n_chunks = 0;
     int64_t pitch = 0;            // columns of a partial sum
+    int32_t lane_bits = 0;        // threads (log2) that take a row's columns
     // workspace offsets: a flag byte per row, two pairs of (row, position)
-    // arrays, the digit counts of a pass, and the partial sums of runs that
-    // cross chunks
-    size_t flags = 0, keys[2] = {0, 0}, pos[2] = {0, 0}, counts = 0, partials = 0, total = 0;
+    // arrays, the digit counts of a pass, and of runs that cross chunks which
+    // ones do and their partial sums
+    size_t flags = 0, keys[2] = {0, 0}, pos[2] = {0, 0}, counts = 0, tails = 0, through = 0,
+           partials = 0, total = 0;
 };
 EmbPlan embedding_plan(int64_t n_tokens, int64_t vocab, int64_t hidden);
 
