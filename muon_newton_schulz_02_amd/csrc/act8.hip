@@ -10,6 +10,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "grads_device.h"
 #include "grads_internal.h"
@@ -38,23 +39,24 @@ __device__ __forceinline__ Unit unit_at(int64_t u, uint32_t upr) {
 }
 
 // 8 features from column `col` on, zeros past the last column.
-template <typename T, bool AL>
+template <typename T, bool AL, bool NT>
 __device__ __forceinline__ void load8(const T* row, int col, int cols, float* v) {
     if (col < cols) {
-        load_unit<T, AL>(row + col, cols - col, v);
+        load_unit<T, AL, NT>(row + col, cols - col, v);
         return;
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = 0.f;
 }
 
-template <typename T, bool AL>
+template <typename T, bool AL, bool NT>
 __device__ __forceinline__ void store8(T* row, int col, int cols, const float* v) {
-    if (col < cols) store_unit<T, AL>(row + col, cols - col, v);
+    if (col < cols) store_unit<T, AL, NT>(row + col, cols - col, v);
 }
 
 // Hold 8 features of each lane: codes and exponent byte of its group of four
 // lanes, into the held matrix's row.
+template <bool NT>
 __device__ __forceinline__ void hold8(const float* v, int8_t* codes, uint8_t* exps, int64_t row,
                                       int col, int code_pitch, int exp_pitch) {
     uint32_t top = 0;
@@ -72,7 +74,11 @@ __device__ __forceinline__ void hold8(const float* v, int8_t* codes, uint8_t* ex
             w[1] |= act_code(v[4 + e], inv) << (8 * e);
         }
     }
-    if (col < code_pitch) *reinterpret_cast<u32x2*>(codes + row * code_pitch + col) = w;
+    if (col < code_pitch) {
+        u32x2* p = reinterpret_cast<u32x2*>(codes + row * code_pitch + col);
+        if constexpr (NT) __builtin_nontemporal_store(w, p);
+        else *p = w;
+    }
     if ((col & 31) == 0) exps[row * exp_pitch + (col >> 5)] = (uint8_t)b;
 }
 
@@ -87,7 +93,7 @@ __device__ __forceinline__ void held8(const int8_t* codes, const uint8_t* exps, 
     }
 }
 
-template <typename T, bool AL>
+template <typename T, bool AL, bool NT>
 __global__ __launch_bounds__(kThreads) void k_act_pack(const T* __restrict__ x, int64_t stride,
                                                        int8_t* __restrict__ codes,
                                                        uint8_t* __restrict__ exps, int cols,
@@ -99,12 +105,12 @@ __global__ __launch_bounds__(kThreads) void k_act_pack(const T* __restrict__ x, 
          u += (int64_t)gridDim.x * kThreads) {
         const Unit at = unit_at(u, upr);
         float v[8];
-        load8<T, AL>(x + at.row * stride, at.col, cols, v);
-        hold8(v, codes, exps, at.row, at.col, code_pitch, exp_pitch);
+        load8<T, AL, NT>(x + at.row * stride, at.col, cols, v);
+        hold8<NT>(v, codes, exps, at.row, at.col, code_pitch, exp_pitch);
     }
 }
 
-template <typename T, bool AL>
+template <typename T, bool AL, bool NT>
 __global__ __launch_bounds__(kThreads) void k_act_unpack(const int8_t* __restrict__ codes,
                                                          const uint8_t* __restrict__ exps,
                                                          T* __restrict__ out, int64_t stride,
@@ -115,7 +121,7 @@ __global__ __launch_bounds__(kThreads) void k_act_unpack(const int8_t* __restric
         const Unit at = unit_at(u, upr);
         float v[8];
         held8(codes, exps, at.row, at.col, code_pitch, exp_pitch, v);
-        store8<T, AL>(out + at.row * stride, at.col, cols, v);
+        store8<T, AL, NT>(out + at.row * stride, at.col, cols, v);
     }
 }
 
@@ -143,7 +149,7 @@ __device__ __forceinline__ float act_slope(float g, float s) {
     return p > 0.f ? fmaf(p, g * da, s) : s;
 }
 
-template <typename T, bool AL, int ACT>
+template <typename T, bool AL, bool NT, int ACT>
 __global__ __launch_bounds__(kThreads) void k_glu_forward(GluArgs a, int cols, int code_pitch,
                                                           int exp_pitch, uint32_t upr,
                                                           int64_t units) {
@@ -154,17 +160,17 @@ __global__ __launch_bounds__(kThreads) void k_glu_forward(GluArgs a, int cols, i
          u += (int64_t)gridDim.x * kThreads) {
         const Unit at = unit_at(u, upr);
         float gv[8], uv[8], hv[8];
-        load8<T, AL>(gate + at.row * a.gate_stride, at.col, cols, gv);
-        load8<T, AL>(up + at.row * a.up_stride, at.col, cols, uv);
+        load8<T, AL, NT>(gate + at.row * a.gate_stride, at.col, cols, gv);
+        load8<T, AL, NT>(up + at.row * a.up_stride, at.col, cols, uv);
 #pragma unroll
         for (int e = 0; e < 8; ++e) hv[e] = gv[e] * act_sig<ACT>(gv[e]) * uv[e];
-        store8<T, AL>(h + at.row * a.h_stride, at.col, cols, hv);
-        hold8(gv, a.gate_codes, a.gate_exps, at.row, at.col, code_pitch, exp_pitch);
-        hold8(uv, a.up_codes, a.up_exps, at.row, at.col, code_pitch, exp_pitch);
+        store8<T, AL, NT>(h + at.row * a.h_stride, at.col, cols, hv);
+        hold8<NT>(gv, a.gate_codes, a.gate_exps, at.row, at.col, code_pitch, exp_pitch);
+        hold8<NT>(uv, a.up_codes, a.up_exps, at.row, at.col, code_pitch, exp_pitch);
     }
 }
 
-template <typename T, bool AL, int ACT, bool HOLD>
+template <typename T, bool AL, bool NT, int ACT, bool HOLD>
 __global__ __launch_bounds__(kThreads) void k_glu_backward(GluArgs a, int cols, int code_pitch,
                                                            int exp_pitch, uint32_t upr,
                                                            int64_t units) {
@@ -182,21 +188,21 @@ __global__ __launch_bounds__(kThreads) void k_glu_backward(GluArgs a, int cols, 
 #pragma unroll
             for (int e = 0; e < 8; ++e) gv[e] = uv[e] = 0.f;
         }
-        load8<T, AL>(dh + at.row * a.dh_stride, at.col, cols, dv);
+        load8<T, AL, NT>(dh + at.row * a.dh_stride, at.col, cols, dv);
         float sv[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) sv[e] = act_sig<ACT>(gv[e]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] = dv[e] * uv[e] * act_slope<ACT>(gv[e], sv[e]);
-        store8<T, AL>(dgate + at.row * a.dgate_stride, at.col, cols, o);
+        store8<T, AL, NT>(dgate + at.row * a.dgate_stride, at.col, cols, o);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const float av = gv[e] * sv[e];
             o[e] = dv[e] * av;
             hv[e] = at.col + e < cols ? av * uv[e] : 0.f;
         }
-        store8<T, AL>(dup + at.row * a.dup_stride, at.col, cols, o);
-        if (HOLD) hold8(hv, a.h_codes, a.h_exps, at.row, at.col, code_pitch, exp_pitch);
+        store8<T, AL, NT>(dup + at.row * a.dup_stride, at.col, cols, o);
+        if (HOLD) hold8<NT>(hv, a.h_codes, a.h_exps, at.row, at.col, code_pitch, exp_pitch);
     }
 }
 
@@ -215,6 +221,30 @@ bool al_rows(const void* p, int64_t stride, int64_t cols, int32_t dtype) {
     return aligned16(p) && stride % per == 0 && cols % 8 == 0;
 }
 
+// Calls f(T{}, aligned, past the caches) with a launch's type and paths (only
+// aligned bf16 streams go past the caches).
+template <typename F>
+int by_paths(int32_t dtype, bool al, bool nt, F f) {
+    if (dtype == MA_PARAM_BF16) {
+        if (al && nt) f(__bf16{}, std::true_type{}, std::true_type{});
+        else if (al) f(__bf16{}, std::true_type{}, std::false_type{});
+        else f(__bf16{}, std::false_type{}, std::false_type{});
+    } else {
+        if (al) f(float{}, std::true_type{}, std::false_type{});
+        else f(float{}, std::false_type{}, std::false_type{});
+    }
+    return (int)hipGetLastError();
+}
+
+// The same with the activation function.
+template <typename F>
+int by_act(int32_t act, int32_t dtype, bool al, bool nt, F f) {
+    return by_paths(dtype, al, nt, [&](auto t, auto a, auto n) {
+        if (act == MA_ACT_SILU) f(t, a, n, std::integral_constant<int, MA_ACT_SILU>{});
+        else f(t, a, n, std::integral_constant<int, MA_ACT_GELU_TANH>{});
+    });
+}
+
 }  // namespace
 
 int launch_act_pack(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t stride,
@@ -223,18 +253,14 @@ int launch_act_pack(const void* x, int32_t dtype, int64_t rows, int64_t cols, in
     const int cp = (int)act_code_pitch(cols), ep = (int)act_exp_pitch(cols);
     const uint32_t upr = (uint32_t)ep * 4;
     const int64_t units = rows * upr;
-    const bool al = al_rows(x, stride, cols, dtype);
     const dim3 grid((unsigned)stream_grid(units));
-#define GO(T, V)                                                                               \
-    hipLaunchKernelGGL((k_act_pack<T, V>), grid, dim3(kThreads), 0, (hipStream_t)stream,        \
-                       static_cast<const T*>(x), stride, codes, exps, (int)cols, cp, ep, upr, units)
-    if (dtype == MA_PARAM_BF16) {
-        if (al) GO(__bf16, true); else GO(__bf16, false);
-    } else {
-        if (al) GO(float, true); else GO(float, false);
-    }
-#undef GO
-    return (int)hipGetLastError();
+    return by_paths(dtype, al_rows(x, stride, cols, dtype), streams_past_caches(rows * cols, dtype),
+                    [&](auto t, auto al, auto nt) {
+        using T = decltype(t);
+        hipLaunchKernelGGL((k_act_pack<T, decltype(al)::value, decltype(nt)::value>), grid, dim3(kThreads), 0,
+                           (hipStream_t)stream, static_cast<const T*>(x), stride, codes, exps, (int)cols, cp,
+                           ep, upr, units);
+    });
 }
 
 int launch_act_unpack(const int8_t* codes, const uint8_t* exps, int64_t rows, int64_t cols,
@@ -243,18 +269,14 @@ int launch_act_unpack(const int8_t* codes, const uint8_t* exps, int64_t rows, in
     const int cp = (int)act_code_pitch(cols), ep = (int)act_exp_pitch(cols);
     const uint32_t upr = (uint32_t)cp / 8;
     const int64_t units = rows * upr;
-    const bool al = al_rows(out, stride, cols, dtype);
     const dim3 grid((unsigned)stream_grid(units));
-#define GO(T, V)                                                                               \
-    hipLaunchKernelGGL((k_act_unpack<T, V>), grid, dim3(kThreads), 0, (hipStream_t)stream,      \
-                       codes, exps, static_cast<T*>(out), stride, (int)cols, cp, ep, upr, units)
-    if (dtype == MA_PARAM_BF16) {
-        if (al) GO(__bf16, true); else GO(__bf16, false);
-    } else {
-        if (al) GO(float, true); else GO(float, false);
-    }
-#undef GO
-    return (int)hipGetLastError();
+    return by_paths(dtype, al_rows(out, stride, cols, dtype), streams_past_caches(rows * cols, dtype),
+                    [&](auto t, auto al, auto nt) {
+        using T = decltype(t);
+        hipLaunchKernelGGL((k_act_unpack<T, decltype(al)::value, decltype(nt)::value>), grid, dim3(kThreads), 0,
+                           (hipStream_t)stream, codes, exps, static_cast<T*>(out), stride, (int)cols, cp, ep,
+                           upr, units);
+    });
 }
 
 int launch_glu_forward(const GluArgs& a, void* stream) {
@@ -262,26 +284,15 @@ int launch_glu_forward(const GluArgs& a, void* stream) {
     const int cp = (int)act_code_pitch(a.cols), ep = (int)act_exp_pitch(a.cols);
     const uint32_t upr = (uint32_t)ep * 4;
     const int64_t units = a.rows * upr;
-    const bool al = al_rows(a.gate, a.gate_stride, a.cols, a.dtype) &&
-                     al_rows(a.up, a.up_stride, a.cols, a.dtype) &&
-                     al_rows(a.h, a.h_stride, a.cols, a.dtype);
     const dim3 grid((unsigned)stream_grid(units));
-#define GO(T, V, A)                                                                            \
-    hipLaunchKernelGGL((k_glu_forward<T, V, A>), grid, dim3(kThreads), 0, (hipStream_t)stream, a, \
-                       (int)a.cols, cp, ep, upr, units)
-#define GO_ACT(T, V)                                                                           \
-    do {                                                                                       \
-        if (a.act == MA_ACT_SILU) GO(T, V, MA_ACT_SILU);                                       \
-        else GO(T, V, MA_ACT_GELU_TANH);                                                       \
-    } while (0)
-    if (a.dtype == MA_PARAM_BF16) {
-        if (al) GO_ACT(__bf16, true); else GO_ACT(__bf16, false);
-    } else {
-        if (al) GO_ACT(float, true); else GO_ACT(float, false);
-    }
-#undef GO_ACT
-#undef GO
-    return (int)hipGetLastError();
+    const bool al = al_rows(a.gate, a.gate_stride, a.cols, a.dtype) &&
+                    al_rows(a.up, a.up_stride, a.cols, a.dtype) &&
+                    al_rows(a.h, a.h_stride, a.cols, a.dtype);
+    return by_act(a.act, a.dtype, al, streams_past_caches(a.rows * a.cols, a.dtype),
+                  [&](auto t, auto w, auto nt, auto act) {
+        hipLaunchKernelGGL((k_glu_forward<decltype(t), decltype(w)::value, decltype(nt)::value, decltype(act)::value>),
+                           grid, dim3(kThreads), 0, (hipStream_t)stream, a, (int)a.cols, cp, ep, upr, units);
+    });
 }
 
 int launch_glu_backward(const GluArgs& a, void* stream) {
@@ -290,32 +301,22 @@ int launch_glu_backward(const GluArgs& a, void* stream) {
     const bool hold = a.h_codes != nullptr;
     const uint32_t upr = hold ? (uint32_t)ep * 4 : (uint32_t)cp / 8;
     const int64_t units = a.rows * upr;
-    const bool al = al_rows(a.dh, a.dh_stride, a.cols, a.dtype) &&
-                     al_rows(a.dgate, a.dgate_stride, a.cols, a.dtype) &&
-                     al_rows(a.dup, a.dup_stride, a.cols, a.dtype);
     const dim3 grid((unsigned)stream_grid(units));
-#define GO(T, V, A, H)                                                                          \
-    hipLaunchKernelGGL((k_glu_backward<T, V, A, H>), grid, dim3(kThreads), 0, (hipStream_t)stream, \
-                       a, (int)a.cols, cp, ep, upr, units)
-#define GO_ACT(T, V, H)                                                                         \
-    do {                                                                                       \
-        if (a.act == MA_ACT_SILU) GO(T, V, MA_ACT_SILU, H);                                    \
-        else GO(T, V, MA_ACT_GELU_TANH, H);                                                    \
-    } while (0)
-#define GO_HOLD(T, V)                                                                           \
-    do {                                                                                       \
-        if (hold) GO_ACT(T, V, true);                                                          \
-        else GO_ACT(T, V, false);                                                              \
-    } while (0)
-    if (a.dtype == MA_PARAM_BF16) {
-        if (al) GO_HOLD(__bf16, true); else GO_HOLD(__bf16, false);
-    } else {
-        if (al) GO_HOLD(float, true); else GO_HOLD(float, false);
-    }
-#undef GO_HOLD
-#undef GO_ACT
-#undef GO
-    return (int)hipGetLastError();
+    const bool al = al_rows(a.dh, a.dh_stride, a.cols, a.dtype) &&
+                    al_rows(a.dgate, a.dgate_stride, a.cols, a.dtype) &&
+                    al_rows(a.dup, a.dup_stride, a.cols, a.dtype);
+    return by_act(a.act, a.dtype, al, streams_past_caches(a.rows * a.cols, a.dtype),
+                  [&](auto t, auto w, auto nt, auto act) {
+        using T = decltype(t);
+        constexpr bool AL = decltype(w)::value, NT = decltype(nt)::value;
+        constexpr int ACT = decltype(act)::value;
+        if (hold)
+            hipLaunchKernelGGL((k_glu_backward<T, AL, NT, ACT, true>), grid, dim3(kThreads), 0, (hipStream_t)stream,
+                               a, (int)a.cols, cp, ep, upr, units);
+        else
+            hipLaunchKernelGGL((k_glu_backward<T, AL, NT, ACT, false>), grid, dim3(kThreads), 0, (hipStream_t)stream,
+                               a, (int)a.cols, cp, ep, upr, units);
+    });
 }
 
 }  // namespace ma

@@ -38,7 +38,7 @@ constexpr int kThreads = 256;
 // gathered rows are in flight per thread.
 constexpr int kLookRows = 4;
 
-template <typename TI, typename TO, typename TOK, bool AL>
+template <typename TI, typename TO, typename TOK, bool AL, bool NT>
 __global__ __launch_bounds__(kThreads) void k_emb_lookup(const TI* __restrict__ table,
                                                          int64_t table_stride, int64_t vocab,
                                                          const TOK* __restrict__ tokens,
@@ -77,7 +77,7 @@ __global__ __launch_bounds__(kThreads) void k_emb_lookup(const TI* __restrict__ 
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[r][e] *= scale;
             }
-            store_unit<TO, AL>(out + t * out_stride + col, hidden - col, v[r]);
+            store_unit<TO, AL, NT>(out + t * out_stride + col, hidden - col, v[r]);
         }
     }
 }
@@ -170,13 +170,13 @@ struct FillArgs {
     void* grad;
     const uint8_t* flags;
     int64_t r0, r1, groups;       // rows, and workgroups that share them
-    int32_t hidden, bf16, al;
+    int32_t hidden, bf16, al, nt;
     int32_t lane_bits;            // lanes (log2) that take a row
 };
 
 // Rows [r0, r1) of the gradient that no token has, set to zero by `groups`
 // workgroups of which this is number `g`.
-template <typename TG, bool AL>
+template <typename TG, bool AL, bool NT>
 __device__ __forceinline__ void zero_rows(const FillArgs& f, int64_t g) {
     const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     const int lanes = 1 << f.lane_bits, per = (int)blockDim.x >> f.lane_bits;
@@ -187,20 +187,30 @@ __device__ __forceinline__ void zero_rows(const FillArgs& f, int64_t g) {
         for (int64_t r = r0 + sub; r < r1; r += per) {
             // (without any token there are no flags: every row is empty)
             if (f.flags && f.flags[r] != 0) continue;
-            for (int col = lane * 8; col < f.hidden; col += lanes * 8)
-                store_unit<TG, AL>(grad + r * f.hidden + col, f.hidden - col, zero);
+            TG* row = grad + r * f.hidden;
+            if constexpr (AL) {
+                // (16 bytes a thread, so that one instruction covers whole lines)
+                const int pieces = f.hidden * (int)sizeof(TG) / 16;
+                for (int i = lane; i < pieces; i += lanes)
+                    put16<NT>(reinterpret_cast<u32x4*>(row) + i, (u32x4){0u, 0u, 0u, 0u});
+            } else {
+                for (int col = lane * 8; col < f.hidden; col += lanes * 8)
+                    store_unit<TG, false>(row + col, f.hidden - col, zero);
+            }
         }
     }
 }
 
+template <typename TG>
+__device__ __forceinline__ void fill_as(const FillArgs& f, int64_t g) {
+    if (f.al && f.nt) zero_rows<TG, true, true>(f, g);
+    else if (f.al) zero_rows<TG, true, false>(f, g);
+    else zero_rows<TG, false, false>(f, g);
+}
+
 __device__ __forceinline__ void fill(const FillArgs& f, int64_t g) {
-    if (f.bf16) {
-        if (f.al) zero_rows<__bf16, true>(f, g);
-        else zero_rows<__bf16, false>(f, g);
-    } else {
-        if (f.al) zero_rows<float, true>(f, g);
-        else zero_rows<float, false>(f, g);
-    }
+    if (f.bf16) fill_as<__bf16>(f, g);
+    else fill_as<float>(f, g);
 }
 
 // Digit counts of each block's entries: counts[block][digit].  The first pass
@@ -456,7 +466,7 @@ __global__ __launch_bounds__(kThreads) void k_emb_sum(SumArgs a, FillArgs f) {
     __shared__ uint32_t s_key[kSumEntries];
     __shared__ int32_t s_pos[kSumEntries];
     if ((int64_t)blockIdx.x >= a.sum_blocks) {
-        zero_rows<TG, AL>(f, (int64_t)blockIdx.x - a.sum_blocks);
+        fill_as<TG>(f, (int64_t)blockIdx.x - a.sum_blocks);
         return;
     }
     const int lanes = 1 << a.lane_bits, per = kThreads >> a.lane_bits;
@@ -502,7 +512,7 @@ __global__ __launch_bounds__(kThreads) void k_emb_sum(SumArgs a, FillArgs f) {
                 if (i + k >= cnt) break;
                 const uint32_t kk = key[i + k];
                 if (kk != cur) {
-                    if (head) store_v<float, 8>(part, acc);
+                    if (head) store_unit<float, true>(part, 8, acc);
                     else write_row<TG, AL>(a, cur, col, acc);
                     head = false;
                     cur = kk;
@@ -516,8 +526,8 @@ __global__ __launch_bounds__(kThreads) void k_emb_sum(SumArgs a, FillArgs f) {
         }
         if (cur == none) continue;
         // (where entries of no row follow cur's run, `last` is theirs)
-        if (head) store_v<float, 8>(part, acc);
-        else if (goes_on && cur == last) store_v<float, 8>(part + a.pitch, acc);
+        if (head) store_unit<float, true>(part, 8, acc);
+        else if (goes_on && cur == last) store_unit<float, true>(part + a.pitch, 8, acc);
         else write_row<TG, AL>(a, cur, col, acc);
     }
 }
@@ -579,7 +589,7 @@ __global__ __launch_bounds__(kThreads) void k_emb_join(SumArgs a) {
 #pragma unroll 4
         for (int p = p0; p < pieces; p += step) {
             float v[8];
-            load_v<float, 8>(a.partials + ((c + p) * 2 + (p == 0 ? 1 : 0)) * a.pitch + col, v);
+            load_unit<float, true>(a.partials + ((c + p) * 2 + (p == 0 ? 1 : 0)) * a.pitch + col, 8, v);
 #pragma unroll
             for (int e = 0; e < 8; ++e) acc[e] += v[e];
         }
@@ -794,18 +804,20 @@ int launch_embedding_lookup(const void* table, int32_t table_dtype, int64_t voca
     if (n_tokens == 0) return (int)hipSuccess;
     const bool al = aligned16(table) && aligned16(out) && hidden % 8 == 0 &&
                     table_stride % per16(table_dtype) == 0 && out_stride % per16(out_dtype) == 0;
+    const bool nt = streams_past_caches(n_tokens * hidden, out_dtype);
     const int lb = lane_bits_for(ceil_div(hidden, 8), 0, 8);
     const int64_t rows = (int64_t)(kThreads >> lb) * kLookRows;
     const dim3 grid((unsigned)ceil_div(n_tokens, rows));
-#define GO(TI, TO, TOK, AL)                                                                     \
-    hipLaunchKernelGGL((k_emb_lookup<TI, TO, TOK, AL>), grid, dim3(kThreads), 0,                 \
+#define GO(TI, TO, TOK, AL, NT)                                                                 \
+    hipLaunchKernelGGL((k_emb_lookup<TI, TO, TOK, AL, NT>), grid, dim3(kThreads), 0,             \
                        (hipStream_t)stream, static_cast<const TI*>(table), table_stride, vocab,  \
                        static_cast<const TOK*>(tokens), n_tokens, scale, static_cast<TO*>(out),   \
                        out_stride, (int)hidden, lb)
 #define GO_AL(TI, TO, TOK)                                                                      \
     do {                                                                                        \
-        if (al) GO(TI, TO, TOK, true);                                                          \
-        else GO(TI, TO, TOK, false);                                                            \
+        if (al && nt) GO(TI, TO, TOK, true, true);                                              \
+        else if (al) GO(TI, TO, TOK, true, false);                                              \
+        else GO(TI, TO, TOK, false, false);                                                     \
     } while (0)
 #define GO_TOK(TI, TO)                                                                          \
     do {                                                                                        \
@@ -927,6 +939,7 @@ int launch_embedding_grad(const EmbGradArgs& g, const EmbPlan& p, void* stream) 
     f.hidden = (int)g.hidden;
     f.bf16 = bg;
     f.al = al;
+    f.nt = streams_past_caches(g.vocab * g.hidden * (bg ? 1 : 2), MA_PARAM_BF16);    // (any type: whole lines)
     f.lane_bits = lane_bits_for(units, 0, 8);
     // the next `eighths` of the zeroing (8: the rest)
     auto share = [&](int eighths) {

@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 namespace ma {
 namespace {
@@ -15,56 +16,9 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 
-// V consecutive elements of type T, widened to float: one or two 16-byte
-// accesses for V = 8 (or 4 floats), else element by element.
-template <typename T, int V>
-__device__ __forceinline__ void load_v(const T* p, float* v) {
-    if constexpr (V * sizeof(T) % 16 == 0) {
-#pragma unroll
-        for (int q = 0; q < (int)(V * sizeof(T) / 16); ++q) {
-            const u32x4 w = *(reinterpret_cast<const u32x4*>(p) + q);
-            if constexpr (sizeof(T) == 4) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[4 * q + e] = __uint_as_float(w[e]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    v[8 * q + 2 * e] = __uint_as_float(w[e] << 16);
-                    v[8 * q + 2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-                }
-            }
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < V; ++e) v[e] = (float)p[e];
-    }
-}
-
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     const bf16x2 p = {(__bf16)a, (__bf16)b};
     return __builtin_bit_cast(uint32_t, p);
-}
-
-// The reverse: V floats rounded to T (nearest even) and stored.
-template <typename T, int V>
-__device__ __forceinline__ void store_v(T* p, const float* v) {
-    if constexpr (V * sizeof(T) % 16 == 0) {
-#pragma unroll
-        for (int q = 0; q < (int)(V * sizeof(T) / 16); ++q) {
-            u32x4 w;
-            if constexpr (sizeof(T) == 4) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) w[e] = __float_as_uint(v[4 * q + e]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) w[e] = pack_bf16(v[8 * q + 2 * e], v[8 * q + 2 * e + 1]);
-            }
-            *(reinterpret_cast<u32x4*>(p) + q) = w;
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < V; ++e) p[e] = (T)v[e];
-    }
 }
 
 // A column unit of 8 elements.  AL: whole and 16-byte aligned; otherwise
@@ -74,51 +28,65 @@ __device__ __forceinline__ void store_v(T* p, const float* v) {
 typedef unsigned int u32x4u2 __attribute__((ext_vector_type(4), aligned(2)));
 typedef unsigned int u32x4u4 __attribute__((ext_vector_type(4), aligned(4)));
 
-template <typename T, bool AL>
-__device__ __forceinline__ void load_unit(const T* p, int cnt, float* v) {
-    if constexpr (AL) {
-        load_v<T, 8>(p, v);
-    } else if (cnt >= 8) {
-        if constexpr (sizeof(T) == 4) {
+// NT: past the caches, for streams larger than they are.
+template <bool NT, typename W>
+__device__ __forceinline__ u32x4 get16(const W* p) {
+    if constexpr (NT) return __builtin_nontemporal_load(p);
+    else return *p;
+}
+template <bool NT, typename W>
+__device__ __forceinline__ void put16(W* p, u32x4 w) {
+    if constexpr (NT) __builtin_nontemporal_store(w, p);
+    else *p = w;
+}
+
+template <typename T>
+__device__ __forceinline__ void widen(const u32x4* w, float* v) {
+    if constexpr (sizeof(T) == 4) {
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const u32x4 w = *(reinterpret_cast<const u32x4u4*>(p) + q);
+        for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(w[e >> 2][e & 3]);
+    } else {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[4 * q + e] = __uint_as_float(w[e]);
-            }
-        } else {
-            const u32x4 w = *reinterpret_cast<const u32x4u2*>(p);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                v[2 * e] = __uint_as_float(w[e] << 16);
-                v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-            }
+        for (int e = 0; e < 4; ++e) {
+            v[2 * e] = __uint_as_float(w[0][e] << 16);
+            v[2 * e + 1] = __uint_as_float(w[0][e] & 0xffff0000u);
         }
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void narrow(const float* v, u32x4* w) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e >> 2][e & 3] = __float_as_uint(v[e]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[0][e] = pack_bf16(v[2 * e], v[2 * e + 1]);
+    }
+}
+
+template <typename T, bool AL, bool NT = false>
+__device__ __forceinline__ void load_unit(const T* p, int cnt, float* v) {
+    using W = std::conditional_t<AL, u32x4, std::conditional_t<sizeof(T) == 4, u32x4u4, u32x4u2>>;
+    if (AL || cnt >= 8) {
+        u32x4 w[sizeof(T) / 2];
+#pragma unroll
+        for (int q = 0; q < (int)sizeof(T) / 2; ++q) w[q] = get16<NT>(reinterpret_cast<const W*>(p) + q);
+        widen<T>(w, v);
     } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = e < cnt ? (float)p[e] : 0.f;
     }
 }
 
-template <typename T, bool AL>
+template <typename T, bool AL, bool NT = false>
 __device__ __forceinline__ void store_unit(T* p, int cnt, const float* v) {
-    if constexpr (AL) {
-        store_v<T, 8>(p, v);
-    } else if (cnt >= 8) {
-        if constexpr (sizeof(T) == 4) {
+    using W = std::conditional_t<AL, u32x4, std::conditional_t<sizeof(T) == 4, u32x4u4, u32x4u2>>;
+    if (AL || cnt >= 8) {
+        u32x4 w[sizeof(T) / 2];
+        narrow<T>(v, w);
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                u32x4 w;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) w[e] = __float_as_uint(v[4 * q + e]);
-                *(reinterpret_cast<u32x4u4*>(p) + q) = w;
-            }
-        } else {
-            u32x4 w;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
-            *reinterpret_cast<u32x4u2*>(p) = w;
-        }
+        for (int q = 0; q < (int)sizeof(T) / 2; ++q) put16<NT>(reinterpret_cast<W*>(p) + q, w[q]);
     } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)

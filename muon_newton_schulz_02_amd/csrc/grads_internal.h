@@ -10,6 +10,17 @@ namespace ma {
 
 constexpr int64_t kMaxCount = int64_t(1) << 30;   // most rows, columns, tokens or ids of a call
 
+// Whether a stream of this many elements goes past the caches: it could not stay
+// in the 32 MB of L2 or much of the 256 MB behind it until it is read, and leaves them to
+// the launch's other data.  Measured: a lookup of 65536 x 2048 bf16 rows (268 MB) 89 us
+// through the caches and 78 past them, packing 32768 x 8192 bf16 143 and 128 us,
+// the gated activation's backward pass at 16384 x 4096 94 and 84; at 33 MB it is no
+// faster.  Only where one instruction covers whole lines: units of 8 floats are two
+// interleaved halves, and a zeroing of 1.2 GB in them took 560 us against 250.
+inline bool streams_past_caches(int64_t elems, int32_t dtype) {
+    return dtype == MA_PARAM_BF16 && elems > (int64_t(32) << 20);
+}
+
 // --------------------------------------------------- 8-bit activations --
 inline int64_t act_code_pitch(int64_t cols) { return round_up(cols, MA_ACT_GROUP); }
 inline int64_t act_exp_pitch(int64_t cols) {

@@ -641,29 +641,31 @@ __global__ __launch_bounds__(kBigThreads) void k_linear_grad_big(BigArgs a) {
                          a.n_in, lane);
 }
 
-// The slices' partial sums, added in slice order.
-template <typename TG, int V>
+// The slices' partial sums, added in slice order.  AL: both arrays in whole,
+// 16-byte aligned units of 8.
+template <typename TG, bool AL>
 __global__ __launch_bounds__(kThreads) void k_linear_join(const float* __restrict__ partials,
-                                                          TG* __restrict__ grad, int64_t units,
+                                                          TG* __restrict__ grad, int64_t n,
                                                           int64_t slices, int accumulate) {
-    const int64_t u = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (u >= units) return;
-    float acc[V];
-    load_v<float, V>(partials + u * V, acc);
+    const int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 8;
+    if (i >= n) return;
+    const int cnt = (int)min<int64_t>(8, n - i);
+    float acc[8];
+    load_unit<float, AL>(partials + i, cnt, acc);
 #pragma unroll 4
     for (int64_t s = 1; s < slices; ++s) {
-        float v[V];
-        load_v<float, V>(partials + (s * units + u) * V, v);
+        float v[8];
+        load_unit<float, AL>(partials + s * n + i, cnt, v);
 #pragma unroll
-        for (int e = 0; e < V; ++e) acc[e] += v[e];
+        for (int e = 0; e < 8; ++e) acc[e] += v[e];
     }
     if (accumulate) {
-        float old[V];
-        load_v<TG, V>(grad + u * V, old);
+        float old[8];
+        load_unit<TG, AL>(grad + i, cnt, old);
 #pragma unroll
-        for (int e = 0; e < V; ++e) acc[e] += old[e];
+        for (int e = 0; e < 8; ++e) acc[e] += old[e];
     }
-    store_v<TG, V>(grad + u * V, acc);
+    store_unit<TG, AL>(grad + i, cnt, acc);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -794,12 +796,12 @@ int launch_small(const LgArgs& a, const LgPlan& p, hipStream_t st) {
     return al ? launch_small_as<float, true>(a, p, st) : launch_small_as<float, false>(a, p, st);
 }
 
-template <typename TG, int V>
+template <typename TG, bool AL>
 void launch_join(const LgArgs& a, const LgPlan& p, hipStream_t st) {
-    const int64_t units = a.n_out * a.n_in / V;
-    hipLaunchKernelGGL((k_linear_join<TG, V>), dim3((unsigned)ceil_div(units, kThreads)),
-                       dim3(kThreads), 0, st, a.partials, static_cast<TG*>(a.grad), units,
-                       p.slices, a.accumulate);
+    const int64_t n = a.n_out * a.n_in;
+    hipLaunchKernelGGL((k_linear_join<TG, AL>), dim3((unsigned)ceil_div(ceil_div(n, 8), kThreads)),
+                       dim3(kThreads), 0, st, a.partials, static_cast<TG*>(a.grad), n, p.slices,
+                       a.accumulate);
 }
 
 }  // namespace
@@ -808,11 +810,11 @@ int launch_linear_grad(const LgArgs& a, const LgPlan& p, void* stream) {
     hipStream_t st = (hipStream_t)stream;
     const int e = p.big ? launch_big(a, p, st) : launch_small(a, p, st);
     if (e != (int)hipSuccess || p.slices == 1) return e;
-    const bool v8 = a.n_out * a.n_in % 8 == 0 && aligned16(a.grad);
+    const bool al = a.n_out * a.n_in % 8 == 0 && aligned16(a.grad);
     if (a.grad_dtype == MA_PARAM_BF16) {
-        if (v8) launch_join<__bf16, 8>(a, p, st); else launch_join<__bf16, 1>(a, p, st);
+        if (al) launch_join<__bf16, true>(a, p, st); else launch_join<__bf16, false>(a, p, st);
     } else {
-        if (v8) launch_join<float, 8>(a, p, st); else launch_join<float, 1>(a, p, st);
+        if (al) launch_join<float, true>(a, p, st); else launch_join<float, false>(a, p, st);
     }
     return (int)hipGetLastError();
 }
