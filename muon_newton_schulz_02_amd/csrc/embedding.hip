@@ -178,7 +178,6 @@ struct FillArgs {
 // workgroups of which this is number `g`.
 template <typename TG, bool AL, bool NT>
 __device__ __forceinline__ void zero_rows(const FillArgs& f, int64_t g) {
-    const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     const int lanes = 1 << f.lane_bits, per = (int)blockDim.x >> f.lane_bits;
     const int lane = threadIdx.x & (lanes - 1), sub = threadIdx.x >> f.lane_bits;
     TG* grad = static_cast<TG*>(f.grad);
@@ -188,24 +187,29 @@ __device__ __forceinline__ void zero_rows(const FillArgs& f, int64_t g) {
             // (without any token there are no flags: every row is empty)
             if (f.flags && f.flags[r] != 0) continue;
             TG* row = grad + r * f.hidden;
-            if constexpr (AL) {
-                // (16 bytes a thread, so that one instruction covers whole lines)
-                const int pieces = f.hidden * (int)sizeof(TG) / 16;
-                for (int i = lane; i < pieces; i += lanes)
-                    put16<NT>(reinterpret_cast<u32x4*>(row) + i, (u32x4){0u, 0u, 0u, 0u});
-            } else {
-                for (int col = lane * 8; col < f.hidden; col += lanes * 8)
-                    store_unit<TG, false>(row + col, f.hidden - col, zero);
+            int n = f.hidden;
+            if constexpr (!AL) {
+                // up to the first 16-byte border, and past the last, element by element
+                const int to = (int)((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / (int)sizeof(TG);
+                const int head = min(n, to);
+                const int tail = (n - head) % (16 / (int)sizeof(TG));
+                if (lane < head) row[lane] = (TG)0.f;
+                if (lane < tail) row[n - tail + lane] = (TG)0.f;
+                row += head;
+                n -= head + tail;
             }
+            // (16 bytes a thread, so that one instruction covers whole lines)
+            const int pieces = n * (int)sizeof(TG) / 16;
+            for (int i = lane; i < pieces; i += lanes)
+                put16<NT>(reinterpret_cast<u32x4*>(row) + i, (u32x4){0u, 0u, 0u, 0u});
         }
     }
 }
 
 template <typename TG>
 __device__ __forceinline__ void fill_as(const FillArgs& f, int64_t g) {
-    if (f.al && f.nt) zero_rows<TG, true, true>(f, g);
-    else if (f.al) zero_rows<TG, true, false>(f, g);
-    else zero_rows<TG, false, false>(f, g);
+    if (f.al) f.nt ? zero_rows<TG, true, true>(f, g) : zero_rows<TG, true, false>(f, g);
+    else f.nt ? zero_rows<TG, false, true>(f, g) : zero_rows<TG, false, false>(f, g);
 }
 
 __device__ __forceinline__ void fill(const FillArgs& f, int64_t g) {
@@ -940,7 +944,7 @@ int launch_embedding_grad(const EmbGradArgs& g, const EmbPlan& p, void* stream) 
     f.bf16 = bg;
     f.al = al;
     f.nt = streams_past_caches(g.vocab * g.hidden * (bg ? 1 : 2), MA_PARAM_BF16);    // (any type: whole lines)
-    f.lane_bits = lane_bits_for(units, 0, 8);
+    f.lane_bits = lane_bits_for(units, 3, 8);     // (8 threads at least: a row's unaligned ends)
     // the next `eighths` of the zeroing (8: the rest)
     auto share = [&](int eighths) {
         f.r0 = f.r1;
