@@ -369,15 +369,16 @@ class MuonAdamW:
         self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
 
     def _formed(self, i, g, stream):
-        """Entry i's gradient: a tensor as it is; an EmbeddingGrad or LinearGrad,
-        or a list of them (micro-batches, added up in float32), formed in a
-        buffer this object keeps for the entry."""
+        """Entry i's gradient from an EmbeddingGrad or LinearGrad, or a list of
+        them (micro-batches, added up in float32), in a buffer this object keeps for
+        the entry.  None for a frozen entry."""
         from . import grads as G
         sources = g if isinstance(g, list) else [g]
         if not sources or not all(isinstance(s, (G.EmbeddingGrad, G.LinearGrad)) for s in sources):
-            if isinstance(g, list):
-                raise TypeError("grad %d: a list holds EmbeddingGrad or LinearGrad items" % i)
-            return g
+            raise TypeError("grad %d must be a tensor, an EmbeddingGrad, a LinearGrad or a list of "
+                            "the latter two" % i)
+        if self.groups[i] == MA_GROUP_NONE:
+            return None
         import torch
         p = self.params[i]
         if p.dim() != 2:
@@ -402,9 +403,10 @@ class MuonAdamW:
         """One optimizer step.  grads[i] is entry i's gradient: a tensor, or an
         EmbeddingGrad or LinearGrad (or a list of them, one per micro-batch),
         formed first, on the same stream, into a buffer kept in grad_buffers[i]."""
-        if any(not (g is None or isinstance(g, int) or hasattr(g, "data_ptr")) for g in grads):
+        if grads is not None and any(isinstance(g, (tuple, list)) for g in grads):
             if len(grads) > len(self.names):
                 raise ValueError("%d gradients for %d entries" % (len(grads), len(self.names)))
-            grads = [self._formed(i, g, stream) for i, g in enumerate(grads)]
+            grads = [self._formed(i, g, stream) if isinstance(g, (tuple, list)) else g
+                     for i, g in enumerate(grads)]
         muon_adamw_step(self.plan, self.params, grads, self.state, self.hp, self.workspace,
                         stream, grad_norm_out, muon_update_out)

@@ -754,13 +754,14 @@ int lane_bits_for(int64_t units, int least, int most) {
 
 }  // namespace
 
-// Up to this many tokens one workgroup sorts: its two passes take 6 us at 4096
-// tokens, four launches over many workgroups 15 us.
+// Up to this many tokens one workgroup sorts: its two passes take 13 us at 4096
+// tokens (6 at 2048), the four launches over many workgroups 22.
 static constexpr int64_t kLdsSortTokens = 4096;
 
 // Few tokens into a table of few rows: no sort.  (Each workgroup reads all tokens, so a
-// large table pays for that many times over: 1024 tokens into 151000 x 2048 took 170 us so,
-// against NNN us sorted.)
+// large table pays for that many times over: 1024 tokens into 151000 x 2048 bf16 took
+// 170 us so, against 124 us sorted.  512 tokens into 1000 x 256 take 6.5 us on the
+// GPU so, and three launches of 6 + 7 + 5 us sorted.)
 static bool direct(int64_t n_tokens, int64_t vocab, int64_t hidden) {
     return n_tokens <= kDirectTokens && vocab * ceil_div(ceil_div(hidden, 8), kDirectLanes) <= 16384;
 }

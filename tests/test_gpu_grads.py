@@ -277,6 +277,7 @@ def test_embedding_grad_strides_and_nan():
 # ------------------------------------------------------------ linear grad --
 
 def _ckpt(x):
+    """x held in 8 bits, and the values that stands for."""
     c = M.ma_act_pack(_dev(x, "bf16"))
     return c, R.unpack(c.codes.cpu().numpy(), c.exps.cpu().numpy(), x.shape[1])
 
@@ -652,6 +653,72 @@ def test_capture_and_replay():
         torch.cuda.synchronize()
 
 
+def test_capture_step_with_sources():
+    """The whole training step captured: gradients formed from sources, then the
+    optimizer step with its counter on the device.  Replays equal eager steps."""
+    outs = []
+    for captured in (False, True):
+        p = _layer_inputs(40)
+        opt, params = _optimizer(p)
+        opt.state.device_step = torch.zeros(1, dtype=torch.int64, device="cuda")
+        opt.step(_layer(p))                       # (allocates the gradient buffers)
+        torch.cuda.synchronize()
+        if captured:
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                opt.step(_layer(p))
+        for seed in (41, 42, 43):
+            q = _layer_inputs(seed)
+            for k in ("ids", "dout"):
+                p[k].copy_(q[k])
+            if captured:
+                g.replay()
+            else:
+                opt.step(_layer(p))
+            torch.cuda.synchronize()
+            M.ma_act_pack(p["dout"])              # eager work in between
+        assert int(opt.state.device_step.item()) == 4
+        outs.append(params)
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+
+
+def test_two_captured_graphs():
+    """Two graphs of the same operators on different data, replayed in turn and
+    then at once on two streams."""
+    ps = [_layer_inputs(50 + k, tokens=3000, vocab=2000) for k in range(2)]
+
+    def work(p):
+        s = _layer(p)
+        return [M.ma_embedding_grad(s[0].dout, s[0].tokens, 2000, scale=8.0)] + \
+            [M.ma_linear_grad(x.dy, x.x) for x in s[1:]]
+
+    want = [work(p) for p in ps]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for p in ps:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(work(p))
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in ps]
+    for r in range(4):
+        for o in outs:
+            for t in o:
+                t.fill_(float("nan"))
+        torch.cuda.synchronize()
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+            if r < 2:
+                st.synchronize()
+        for st in streams:
+            st.synchronize()
+        for o, w in zip(outs, want):
+            for a, b in zip(o, w):
+                assert torch.equal(a, b), r
+
+
 def test_two_streams_at_once():
     """Two calls of each operator in flight at once, on two streams."""
     ps = [_layer_inputs(30 + k, tokens=4000, vocab=2000) for k in range(2)]
@@ -674,6 +741,63 @@ def test_two_streams_at_once():
         for a, b in zip(got, want):
             for x, y in zip(a, b):
                 assert torch.equal(x, y)
+
+
+# ---------------------------------------------------------- random calls --
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_calls(seed):
+    """Every operator at random sizes, types and strides (each a view of a wider
+    array filled with NaN)."""
+    rng = np.random.default_rng(1000 + seed)
+
+    def size(most):
+        return int(np.exp(rng.random() * np.log(most)))
+
+    def kind():
+        return ("fp32", "bf16")[rng.integers(2)]
+
+    def view(x, k):
+        pad = int(rng.integers(0, 20))
+        v, wide = _strided(x, pad, k)
+        wide[:, x.shape[1]:] = float("nan")
+        return v
+
+    n, v, h = size(3000), size(5000), size(700)
+    ids, td, tg = _tokens(rng, ("uniform", "zipf", "mixed", "one")[rng.integers(4)], n, v), kind(), kind()
+    tok = torch.from_numpy(ids).cuda()
+    table = view(rng.standard_normal((v, h)), td)
+    got = M.ma_embedding_lookup(table, tok, scale=-1.5, out_dtype=DT[tg])
+    ok = (ids >= 0) & (ids < v)
+    want = np.where(ok[:, None], -1.5 * _f64(table)[np.where(ok, ids, 0)], 0.0)
+    _close(got, want, R.rounded(want, 2 * R.F32 * np.abs(want), tg), "lookup")
+    d = view(rng.standard_normal((n, h)), td)
+    pad = int(rng.integers(-1, v))
+    got = M.ma_embedding_grad(d, tok, v, scale=-1.5, padding_token=pad, grad_dtype=DT[tg])
+    want, tol = R.embedding_grad(_f64(d), ids, v, -1.5, pad)
+    _close(got, want, R.rounded(want, tol, tg), "embedding grad")
+
+    rows, cols, act = size(400), size(900), ("silu", "gelu_tanh")[rng.integers(2)]
+    g, u = view(_activation(rng, rows, cols), td), view(_activation(rng, rows, cols), td)
+    out, cg, cu = M.ma_glu_forward(g, u, act)
+    a, _, a_tol, _ = R.act(act, _f64(g))
+    want = a * _f64(u)
+    _close(out, want, R.rounded(want, a_tol * np.abs(_f64(u)) + 2 * R.F32 * np.abs(want), td), "h")
+    assert torch.equal(cg.codes, M.ma_act_pack(g).codes)
+    dh = view(rng.standard_normal((rows, cols)), td)
+    dg, du = M.ma_glu_backward(dh, cg, cu, act)
+    gh, uh, dd = R.held(_f64(g)), R.held(_f64(u)), _f64(dh)
+    a, s, a_tol, s_tol = R.act(act, gh)
+    want = dd * a
+    _close(du, want, R.rounded(want, a_tol * np.abs(dd) + 2 * R.F32 * np.abs(want), td), "dup")
+    want = dd * uh * s
+    _close(dg, want, R.rounded(want, np.abs(dd * uh) * s_tol + 4 * R.F32 * np.abs(want), td), "dgate")
+
+    m, n, k = size(3000), size(1500), size(600)
+    dy = view(rng.standard_normal((m, n)), td)
+    c, x = _ckpt(_activation(rng, m, k))
+    want, tol = R.linear_grad(_f64(dy), x)
+    _close(M.ma_linear_grad(dy, c, grad_dtype=DT[tg]), want, R.rounded(want, tol, tg), "linear grad")
 
 
 # ----------------------------------------------------- offsets past 32 bits --

@@ -250,15 +250,24 @@ def test_rows_of_a_tensor():
             _rows(bad, "x")
 
 
-def test_step_refuses_mixed_lists():
-    class Fake:
-        names, params = ["a"], [torch.zeros(4, 4)]
-        grad_buffers = sum_buffers = [None]
-        _formed = M.MuonAdamW._formed
-    with pytest.raises(TypeError, match="list"):
-        Fake()._formed(0, [torch.zeros(4, 4)], None)
-    with pytest.raises(TypeError, match="list"):
-        Fake()._formed(0, [], None)
-    Fake.params = [torch.zeros(4)]
+def _holder(**kw):
+    """A MuonAdamW without a GPU: only what _formed looks at."""
+    o = object.__new__(M.MuonAdamW)
+    o.names, o.params, o.groups = ["a"], [torch.zeros(4, 4)], [M.MA_GROUP_MUON]
+    o.grad_buffers, o.sum_buffers = [None], [None]
+    o.__dict__.update(kw)
+    return o
+
+
+def test_step_refuses_wrong_sources():
+    for bad in ([torch.zeros(4, 4)], [], (1, 2), [M.LinearGrad(None, None), None]):
+        with pytest.raises(TypeError, match="LinearGrad"):
+            _holder()._formed(0, bad, None)
+        with pytest.raises(TypeError, match="LinearGrad"):
+            _holder().step([bad])
     with pytest.raises(ValueError, match="matrix"):
-        Fake()._formed(0, M.LinearGrad(None, None), None)
+        _holder(params=[torch.zeros(4)])._formed(0, M.LinearGrad(None, None), None)
+    with pytest.raises(ValueError, match="entries"):
+        _holder().step([M.LinearGrad(None, None), None])
+    frozen = _holder(groups=[M.MA_GROUP_NONE])
+    assert frozen._formed(0, M.LinearGrad(None, None), None) is None
