@@ -395,7 +395,7 @@ class MuonAdamW:
             self.sum_buffers[i] = torch.empty(p.shape, dtype=torch.float32, device=p.device)
         for k, s in enumerate(sources):
             G.form_gradient(s, p.shape, self.sum_buffers[i], k > 0, stream)
-        with G._on(p.device, stream, (out, self.sum_buffers[i])):
+        with G._At(p.device, stream, (out, self.sum_buffers[i])):
             out.copy_(self.sum_buffers[i])
         return out
 

@@ -111,48 +111,29 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-class _Here:
-    """The current stream of the current device, already right."""
-
-    __slots__ = ("raw",)
-
-    def __init__(self, raw):
-        self.raw = raw
-
-    def __enter__(self):
-        return self
-
-    def __exit__(self, *exc):
-        return False
+def _elsewhere(dev, stream) -> bool:
+    """Whether a call is for another device or stream than the current ones."""
+    return stream is not None or dev.index != _device_now()
 
 
-class _Elsewhere(contextlib.ExitStack):
-    """Another device or stream, made current for a call's allocations and
-    launches."""
+class _At(contextlib.ExitStack):
+    """Another device and stream made current, for a call's allocations and
+    launches.  Tensors: those the call uses."""
 
     def __init__(self, dev, stream, tensors):
         super().__init__()
         self.enter_context(torch.cuda.device(dev))
         if stream is None:
-            self.raw = _raw_stream(dev.index)
             return
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=dev)
-        self.raw = stream.cuda_stream
-        if self.raw != _raw_stream(dev.index):
+        if stream.cuda_stream != _raw_stream(dev.index):
             # memory of another stream's tensors is not handed out again before this
             # stream is done with them
             for t in tensors:
                 if t is not None:
                     t.record_stream(stream)
             self.enter_context(torch.cuda.stream(stream))
-
-
-def _on(dev, stream, tensors):
-    """The context a call allocates and launches in; `.raw` is its stream."""
-    if stream is None and dev.index == _device_now():
-        return _Here(_raw_stream(dev.index))
-    return _Elsewhere(dev, stream, tensors)
 
 
 def _out_like(out, what: str, shape, dtype, dev):
@@ -196,7 +177,9 @@ class ActCheckpoint:
     the activation's (default: rows x cols).  It stands for codes * 2^(exps -
     127), one exponent for every 32 features of a token."""
 
-    __slots__ = ("codes", "exps", "cols", "shape")
+    # (one allocation holds both arrays of a checkpoint made here; its views are
+    # made when asked for)
+    __slots__ = ("cols", "rows", "shape", "device", "_buf", "_codes", "_exps", "_pc", "_pe")
 
     def __init__(self, codes, exps, cols: int, shape=None):
         cols = int(cols)
@@ -210,61 +193,71 @@ class ActCheckpoint:
                 tuple(codes.shape), tuple(exps.shape), cols))
         if not codes.is_contiguous() or not exps.is_contiguous():
             raise ValueError("codes and exps must be contiguous")
-        self.codes, self.exps, self.cols = codes, exps, cols
-        if shape is None:
-            shape = (codes.shape[0], cols)
-        self.shape = tuple(shape)
-        if self.shape[-1] != cols or self.numel() != codes.shape[0] * cols:
-            raise ValueError("shape %s is not %d rows of %d features" % (self.shape,
-                                                                         codes.shape[0], cols))
-
-    def numel(self) -> int:
+        if codes.device != exps.device:
+            raise ValueError("codes are on %s, exps on %s" % (codes.device, exps.device))
+        self._codes, self._exps, self._buf = codes, exps, None
+        self._pc, self._pe = codes.data_ptr(), exps.data_ptr()
+        self.cols, self.rows, self.device = cols, codes.shape[0], codes.device
+        self.shape = (self.rows, cols) if shape is None else tuple(shape)
         n = 1
         for d in self.shape:
             n *= int(d)
-        return n
-
-    @property
-    def rows(self) -> int:
-        return self.codes.shape[0]
+        if self.shape[-1] != cols or n != self.rows * cols:
+            raise ValueError("shape %s is not %d rows of %d features" % (self.shape, self.rows, cols))
 
     @staticmethod
     def empty(shape, device) -> "ActCheckpoint":
         """An uninitialised holder for an activation of this shape."""
         shape = tuple(int(d) for d in shape)
-        cols, rows = shape[-1], 1
+        rows = 1
         for d in shape[:-1]:
             rows *= d
-        return ActCheckpoint._empty(shape, rows, cols, device)
+        return ActCheckpoint._empty(shape, rows, shape[-1], device)
 
     @staticmethod
     def _empty(shape, rows, cols, device):
         if cols < 1:
             raise ValueError("an activation needs at least one feature")
         pitch = -(-cols // MA_ACT_GROUP) * MA_ACT_GROUP
+        after = -(-rows * pitch // 256) * 256
         c = object.__new__(ActCheckpoint)
-        c.codes = torch.empty((rows, pitch), dtype=torch.int8, device=device)
-        c.exps = torch.empty((rows, -(-pitch // (4 * MA_ACT_GROUP)) * 4), dtype=torch.uint8,
-                             device=device)
-        c.cols, c.shape = cols, tuple(shape)
+        c._buf = buf = torch.empty(after + rows * (-(-pitch // (4 * MA_ACT_GROUP)) * 4),
+                                   dtype=torch.uint8, device=device)
+        c._codes = c._exps = None
+        c._pc = buf.data_ptr()
+        c._pe = c._pc + after
+        c.cols, c.rows, c.shape, c.device = cols, rows, tuple(shape), buf.device
         return c
 
-    def _like(self):
-        c = object.__new__(ActCheckpoint)
-        c.codes, c.exps = torch.empty_like(self.codes), torch.empty_like(self.exps)
-        c.cols, c.shape = self.cols, self.shape
-        return c
+    @property
+    def codes(self):
+        if self._codes is None:
+            pitch = -(-self.cols // MA_ACT_GROUP) * MA_ACT_GROUP
+            self._codes = self._buf[:self.rows * pitch].view(torch.int8).view(self.rows, pitch)
+        return self._codes
+
+    @property
+    def exps(self):
+        if self._exps is None:
+            pitch = -(-self.cols // MA_ACT_GROUP) * MA_ACT_GROUP
+            after = -(-self.rows * pitch // 256) * 256
+            self._exps = self._buf[after:].view(self.rows, -(-pitch // (4 * MA_ACT_GROUP)) * 4)
+        return self._exps
+
+    def _tensors(self):
+        return (self._buf,) if self._buf is not None else (self._codes, self._exps)
 
 
-def _held(c, what: str, rows=None, cols=None):
+def _held(c, what: str, dev, rows=None, cols=None):
     if not isinstance(c, ActCheckpoint):
         raise TypeError("%s must be an ActCheckpoint" % what)
     if rows is not None and (c.rows != rows or c.cols != cols):
         raise ValueError("%s holds %d x %d, the call needs %d x %d" % (what, c.rows, c.cols, rows,
                                                                       cols))
-    if not c.codes.is_cuda or not c.exps.is_cuda:
+    if c.device.type != "cuda":
         raise ValueError("%s must live on the GPU" % what)
-    return c
+    if c.device != dev:
+        raise ValueError("%s is on %s, the call runs on %s" % (what, c.device, dev))
 
 
 def ma_act_pack(x, out: Optional[ActCheckpoint] = None, stream=None) -> ActCheckpoint:
@@ -274,13 +267,14 @@ def ma_act_pack(x, out: Optional[ActCheckpoint] = None, stream=None) -> ActCheck
     rows, cols, ld = _rows(x, "x")
     dev = x.device
     if out is not None:
-        _held(out, "out", rows, cols)
-        _same_device(dev, ("out", out.codes), ("out", out.exps))
-    with _on(dev, stream, (x,) if out is None else (x, out.codes, out.exps)) as on:
-        if out is None:
-            out = ActCheckpoint._empty(x.shape, rows, cols, dev)
-        rc = _abi.load().ma_act_pack(x.data_ptr(), dt, rows, cols, ld, out.codes.data_ptr(),
-                                     out.exps.data_ptr(), on.raw)
+        _held(out, "out", dev, rows, cols)
+    if _elsewhere(dev, stream):
+        with _At(dev, stream, (x,) if out is None else (x, *out._tensors())):
+            return ma_act_pack(x, out)
+    if out is None:
+        out = ActCheckpoint._empty(x.shape, rows, cols, dev)
+    rc = _abi.load().ma_act_pack(x.data_ptr(), dt, rows, cols, ld, out._pc, out._pe,
+                                 _raw_stream(dev.index))
     if rc:
         _fail(rc, "ma_act_pack")
     return out
@@ -288,14 +282,20 @@ def ma_act_pack(x, out: Optional[ActCheckpoint] = None, stream=None) -> ActCheck
 
 def ma_act_unpack(ckpt: ActCheckpoint, dtype=torch.float32, out=None, stream=None):
     """The activation an ActCheckpoint stands for, in `dtype` (or out's)."""
-    _held(ckpt, "ckpt")
-    dev = ckpt.codes.device
-    _same_device(dev, ("exps", ckpt.exps), ("out", out))
-    with _on(dev, stream, (ckpt.codes, ckpt.exps, out)) as on:
+    _held(ckpt, "ckpt", getattr(ckpt, "device", None))
+    dev = ckpt.device
+    _same_device(dev, ("out", out))
+    if _elsewhere(dev, stream):
+        with _At(dev, stream, (*ckpt._tensors(), out)):
+            return ma_act_unpack(ckpt, dtype, out)
+    if out is None:
+        out = torch.empty(ckpt.shape, dtype=dtype, device=dev)
+        ld = ckpt.cols
+    else:
         out = _out_like(out, "out", ckpt.shape, dtype, dev)
-        rows, cols, ld = _rows(out, "out")
-        rc = _abi.load().ma_act_unpack(ckpt.codes.data_ptr(), ckpt.exps.data_ptr(), rows, cols,
-                                       out.data_ptr(), _dtype(out, "out"), ld, on.raw)
+        ld = _rows(out, "out")[2]
+    rc = _abi.load().ma_act_unpack(ckpt._pc, ckpt._pe, ckpt.rows, ckpt.cols, out.data_ptr(),
+                                   _dtype(out, "out"), ld, _raw_stream(dev.index))
     if rc:
         _fail(rc, "ma_act_unpack")
     return out
@@ -305,7 +305,8 @@ def ma_act_unpack(ckpt: ActCheckpoint, dtype=torch.float32, out=None, stream=Non
 
 def ma_embedding_lookup(table, tokens, scale: float = 1.0, out=None, out_dtype=None, stream=None):
     """scale * table[tokens], of shape tokens.shape + (hidden,), in `out_dtype`
-    (default: the table's).  A token outside [0, vocab) gives a row of zeros."""
+    (default: the table's; an `out` passed keeps its own).  A token outside [0,
+    vocab) gives a row of zeros."""
     _check_cuda(table, "table")
     _check_cuda(tokens, "tokens")
     if table.dim() != 2:
@@ -317,21 +318,27 @@ def ma_embedding_lookup(table, tokens, scale: float = 1.0, out=None, out_dtype=N
     dt = _dtype(table, "table")
     dev = table.device
     _same_device(dev, ("tokens", tokens), ("out", out))
-    with _on(dev, stream, (table, tokens, out)) as on:
-        out = _out_like(out, "out", tuple(tokens.shape) + (hidden,), out_dtype or table.dtype, dev)
-        rows, _, old = _rows(out, "out")
-        rc = _abi.load().ma_embedding_lookup(table.data_ptr(), dt, vocab, hidden, ld,
-                                             tokens.data_ptr(), tb, rows, scale, out.data_ptr(),
-                                             _dtype(out, "out"), old, on.raw)
+    if _elsewhere(dev, stream):
+        with _At(dev, stream, (table, tokens, out)):
+            return ma_embedding_lookup(table, tokens, scale, out, out_dtype)
+    if out is None:
+        out = torch.empty((*tokens.shape, hidden), dtype=out_dtype or table.dtype, device=dev)
+        old = hidden
+    else:
+        out = _out_like(out, "out", (*tokens.shape, hidden), None, dev)
+        old = _rows(out, "out")[2]
+    rc = _abi.load().ma_embedding_lookup(table.data_ptr(), dt, vocab, hidden, ld,
+                                         tokens.data_ptr(), tb, tokens.numel(), scale,
+                                         out.data_ptr(), _dtype(out, "out"), old,
+                                         _raw_stream(dev.index))
     if rc:
         _fail(rc, "ma_embedding_lookup")
     return out
 
 
 def ma_embedding_grad_workspace_size(n_tokens: int, vocab: int, hidden: int) -> int:
-    lib = _abi.load()
     n = C.c_size_t()
-    rc = lib.ma_embedding_grad_workspace_size(n_tokens, vocab, hidden, C.byref(n))
+    rc = _abi.load().ma_embedding_grad_workspace_size(n_tokens, vocab, hidden, C.byref(n))
     if rc:
         _fail(rc, "ma_embedding_grad_workspace_size")
     return n.value
@@ -359,17 +366,21 @@ def ma_embedding_grad(dout, tokens, vocab: int, scale: float = 1.0, padding_toke
         raise ValueError("accumulate needs the gradient to add to (out)")
     dev = dout.device
     _same_device(dev, ("tokens", tokens), ("out", out))
+    if _elsewhere(dev, stream):
+        with _At(dev, stream, (dout, tokens, out, workspace)):
+            return ma_embedding_grad(dout, tokens, vocab, scale, padding_token, out, accumulate,
+                                     grad_dtype, workspace)
     vocab = int(vocab)
     need = ma_embedding_grad_workspace_size(rows, vocab, hidden)
-    with _on(dev, stream, (dout, tokens, out, workspace)) as on:
-        out = _out_like(out, "out", (vocab, hidden), grad_dtype, dev)
-        if not out.is_contiguous():
-            raise ValueError("out must be contiguous")
-        ws, ws_ptr, ws_bytes = _workspace(workspace, need, dev)
-        rc = _abi.load().ma_embedding_grad(dout.data_ptr(), dt, ld, tokens.data_ptr(), tb, rows,
-                                           vocab, hidden, scale, int(padding_token),
-                                           out.data_ptr(), _dtype(out, "out"),
-                                           1 if accumulate else 0, ws_ptr, ws_bytes, on.raw)
+    out = _out_like(out, "out", (vocab, hidden), grad_dtype, dev)
+    if not out.is_contiguous():
+        raise ValueError("out must be contiguous")
+    ws, ws_ptr, ws_bytes = _workspace(workspace, need, dev)
+    rc = _abi.load().ma_embedding_grad(dout.data_ptr(), dt, ld, tokens.data_ptr(), tb, rows,
+                                       vocab, hidden, scale, int(padding_token),
+                                       out.data_ptr(), _dtype(out, "out"),
+                                       1 if accumulate else 0, ws_ptr, ws_bytes,
+                                       _raw_stream(dev.index))
     if rc:
         _fail(rc, "ma_embedding_grad")
     return out
@@ -395,26 +406,28 @@ def ma_linear_grad(dy, x: ActCheckpoint, out=None, accumulate: bool = False,
     _check_cuda(dy, "dy")
     dt = _dtype(dy, "dy")
     rows, n_out, ld = _rows(dy, "dy")
-    _held(x, "x")
-    if x.rows != rows or (len(dy.shape) == len(x.shape) and dy.shape[:-1] != x.shape[:-1]):
+    dev = dy.device
+    _held(x, "x", dev)
+    if x.rows != rows or (dy.dim() == len(x.shape) and dy.shape[:-1] != x.shape[:-1]):
         raise ValueError("dy %s does not belong to x %s" % (tuple(dy.shape), x.shape))
     if accumulate and out is None:
         raise ValueError("accumulate needs the gradient to add to (out)")
-    dev = dy.device
-    _same_device(dev, ("x", x.codes), ("x", x.exps), ("out", out))
+    _same_device(dev, ("out", out))
+    if _elsewhere(dev, stream):
+        with _At(dev, stream, (dy, *x._tensors(), out, workspace)):
+            return ma_linear_grad(dy, x, out, accumulate, grad_dtype, workspace)
     lib = _abi.load()
     size = C.c_size_t()
     rc = lib.ma_linear_grad_workspace_size(rows, n_out, x.cols, dt, C.byref(size))
     if rc:
         _fail(rc, "ma_linear_grad")
-    with _on(dev, stream, (dy, x.codes, x.exps, out, workspace)) as on:
-        out = _out_like(out, "out", (n_out, x.cols), grad_dtype, dev)
-        if not out.is_contiguous():
-            raise ValueError("out must be contiguous")
-        ws, ws_ptr, ws_bytes = _workspace(workspace, size.value, dev)
-        rc = lib.ma_linear_grad(dy.data_ptr(), dt, rows, n_out, ld, x.codes.data_ptr(),
-                                x.exps.data_ptr(), x.cols, out.data_ptr(), _dtype(out, "out"),
-                                1 if accumulate else 0, ws_ptr, ws_bytes, on.raw)
+    out = _out_like(out, "out", (n_out, x.cols), grad_dtype, dev)
+    if not out.is_contiguous():
+        raise ValueError("out must be contiguous")
+    ws, ws_ptr, ws_bytes = _workspace(workspace, size.value, dev)
+    rc = lib.ma_linear_grad(dy.data_ptr(), dt, rows, n_out, ld, x._pc, x._pe, x.cols,
+                            out.data_ptr(), _dtype(out, "out"), 1 if accumulate else 0, ws_ptr,
+                            ws_bytes, _raw_stream(dev.index))
     if rc:
         _fail(rc, "ma_linear_grad")
     return out
@@ -441,23 +454,25 @@ def ma_glu_forward(gate, up, act="silu", out=None, gate_ckpt: Optional[ActCheckp
                                                                tuple(up.shape), up.dtype))
     dt = _dtype(gate, "gate")
     rows, cols, gld = _rows(gate, "gate")
-    _, _, uld = _rows(up, "up")
+    uld = _rows(up, "up")[2]
     dev = gate.device
     _same_device(dev, ("up", up), ("out", out))
     for what, c in (("gate_ckpt", gate_ckpt), ("up_ckpt", up_ckpt)):
         if c is not None:
-            _held(c, what, rows, cols)
-            _same_device(dev, (what, c.codes), (what, c.exps))
-    used = [gate, up, out] + [t for c in (gate_ckpt, up_ckpt) if c is not None
-                              for t in (c.codes, c.exps)]
-    with _on(dev, stream, used) as on:
-        out = _out_as(out, "out", gate)
-        gate_ckpt = gate_ckpt or ActCheckpoint._empty(gate.shape, rows, cols, dev)
-        up_ckpt = up_ckpt or gate_ckpt._like()
-        rc = _abi.load().ma_glu_forward(
-            gate.data_ptr(), up.data_ptr(), dt, rows, cols, gld, uld, _act(act), out.data_ptr(),
-            _rows(out, "out")[2], gate_ckpt.codes.data_ptr(), gate_ckpt.exps.data_ptr(),
-            up_ckpt.codes.data_ptr(), up_ckpt.exps.data_ptr(), on.raw)
+            _held(c, what, dev, rows, cols)
+    if _elsewhere(dev, stream):
+        used = [t for c in (gate_ckpt, up_ckpt) if c is not None for t in c._tensors()]
+        with _At(dev, stream, [gate, up, out] + used):
+            return ma_glu_forward(gate, up, act, out, gate_ckpt, up_ckpt)
+    out = _out_as(out, "out", gate)
+    if gate_ckpt is None:
+        gate_ckpt = ActCheckpoint._empty(gate.shape, rows, cols, dev)
+    if up_ckpt is None:
+        up_ckpt = ActCheckpoint._empty(gate.shape, rows, cols, dev)
+    rc = _abi.load().ma_glu_forward(
+        gate.data_ptr(), up.data_ptr(), dt, rows, cols, gld, uld, _act(act), out.data_ptr(),
+        _rows(out, "out")[2], gate_ckpt._pc, gate_ckpt._pe, up_ckpt._pc, up_ckpt._pe,
+        _raw_stream(dev.index))
     if rc:
         _fail(rc, "ma_glu_forward")
     return out, gate_ckpt, up_ckpt
@@ -473,27 +488,26 @@ def ma_glu_backward(dh, gate: ActCheckpoint, up: ActCheckpoint, act="silu", dgat
     dt = _dtype(dh, "dh")
     rows, cols, ld = _rows(dh, "dh")
     dev = dh.device
-    _held(gate, "gate", rows, cols)
-    _held(up, "up", rows, cols)
-    _same_device(dev, ("gate", gate.codes), ("gate", gate.exps), ("up", up.codes),
-                 ("up", up.exps), ("dgate", dgate), ("dup", dup))
+    _held(gate, "gate", dev, rows, cols)
+    _held(up, "up", dev, rows, cols)
+    _same_device(dev, ("dgate", dgate), ("dup", dup))
     hold = h_ckpt is not None and h_ckpt is not False
-    used = [dh, gate.codes, gate.exps, up.codes, up.exps, dgate, dup]
     if hold and h_ckpt is not True:
-        _held(h_ckpt, "h_ckpt", rows, cols)
-        _same_device(dev, ("h_ckpt", h_ckpt.codes), ("h_ckpt", h_ckpt.exps))
-        used += [h_ckpt.codes, h_ckpt.exps]
-    with _on(dev, stream, used) as on:
-        dgate = _out_as(dgate, "dgate", dh)
-        dup = _out_as(dup, "dup", dh)
-        if hold and h_ckpt is True:
-            h_ckpt = ActCheckpoint._empty(dh.shape, rows, cols, dev)
-        rc = _abi.load().ma_glu_backward(
-            dh.data_ptr(), dt, rows, cols, ld, gate.codes.data_ptr(), gate.exps.data_ptr(),
-            up.codes.data_ptr(), up.exps.data_ptr(), _act(act), dgate.data_ptr(),
-            _rows(dgate, "dgate")[2], dup.data_ptr(), _rows(dup, "dup")[2],
-            h_ckpt.codes.data_ptr() if hold else None, h_ckpt.exps.data_ptr() if hold else None,
-            on.raw)
+        _held(h_ckpt, "h_ckpt", dev, rows, cols)
+    if _elsewhere(dev, stream):
+        used = [dh, *gate._tensors(), *up._tensors(), dgate, dup]
+        if hold and h_ckpt is not True:
+            used += h_ckpt._tensors()
+        with _At(dev, stream, used):
+            return ma_glu_backward(dh, gate, up, act, dgate, dup, h_ckpt)
+    dgate = _out_as(dgate, "dgate", dh)
+    dup = _out_as(dup, "dup", dh)
+    if hold and h_ckpt is True:
+        h_ckpt = ActCheckpoint._empty(dh.shape, rows, cols, dev)
+    rc = _abi.load().ma_glu_backward(
+        dh.data_ptr(), dt, rows, cols, ld, gate._pc, gate._pe, up._pc, up._pe, _act(act),
+        dgate.data_ptr(), _rows(dgate, "dgate")[2], dup.data_ptr(), _rows(dup, "dup")[2],
+        h_ckpt._pc if hold else None, h_ckpt._pe if hold else None, _raw_stream(dev.index))
     if rc:
         _fail(rc, "ma_glu_backward")
     return (dgate, dup, h_ckpt) if hold else (dgate, dup)
