@@ -31,7 +31,7 @@
  * array's type (to nearest, ties to even).
  *
  * Matrices are row-major, `*_stride` elements from row to row.  An input's
- * stride may be any value >= 0 (0 repeats one row); an output's is at least
+ * stride may be any value >= 0 (0 repeats one row) and below 2^31; an output's is at least
  * its columns.  Addresses are multiples of the element size.  Outputs and
  * the workspace must overlap neither each other nor an input, except that
  * rows may interleave (gate and up as two halves of one array, both with its

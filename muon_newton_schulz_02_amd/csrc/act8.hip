@@ -20,23 +20,34 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Where unit u (8 features) of a matrix with `upr` units per row lies.
-struct Unit {
-    int64_t row;
-    int col;
+// The units (8 features) a thread takes: its own index, then every gridDim *
+// kThreads-th.  A matrix has `upr` units per row; the step between a thread's units is
+// given as whole rows and units, so that only its first unit takes a division.
+struct Walk {
+    uint32_t upr, step_rows, step_units;
+    uint32_t rows;
 };
-__device__ __forceinline__ Unit unit_at(int64_t u, uint32_t upr) {
-    Unit r;
-    if (u < (int64_t(1) << 32)) {
-        const uint32_t q = (uint32_t)u / upr;
-        r.row = q;
-        r.col = (int)((uint32_t)u - q * upr) * 8;
-    } else {
-        r.row = u / upr;
-        r.col = (int)(u - r.row * upr) * 8;
+struct At {
+    uint32_t row, unit;
+    __device__ __forceinline__ At(const Walk& w) {
+        const uint32_t u = blockIdx.x * kThreads + threadIdx.x;
+        row = u / w.upr;
+        unit = u - row * w.upr;
     }
-    return r;
-}
+    __device__ __forceinline__ void next(const Walk& w) {
+        row += w.step_rows;
+        unit += w.step_units;
+        if (unit >= w.upr) {
+            unit -= w.upr;
+            ++row;
+        }
+    }
+    __device__ __forceinline__ int col() const { return (int)unit * 8; }
+    // offset of this unit's row in a matrix of the given row length or stride
+    __device__ __forceinline__ int64_t row_at(uint32_t stride) const {
+        return (int64_t)((uint64_t)row * stride);
+    }
+};
 
 // 8 features from column `col` on, zeros past the last column.
 template <typename T, bool AL, bool NT>
@@ -55,37 +66,33 @@ __device__ __forceinline__ void store8(T* row, int col, int cols, const float* v
 }
 
 // Hold 8 features of each lane: codes and exponent byte of its group of four
-// lanes, into the held matrix's row.
+// lanes (active together: every row has a multiple of 16 units), into the held
+// matrix's row.
 template <bool NT>
-__device__ __forceinline__ void hold8(const float* v, int8_t* codes, uint8_t* exps, int64_t row,
-                                      int col, int code_pitch, int exp_pitch) {
+__device__ __forceinline__ void hold8(const float* v, int8_t* codes, uint8_t* exps, const At& at,
+                                      int code_pitch, int exp_pitch) {
     uint32_t top = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) top = max(top, abs_bits(v[e]));
-    top = max(top, (uint32_t)__shfl_xor((int)top, 1, 64));
-    top = max(top, (uint32_t)__shfl_xor((int)top, 2, 64));
+    // the largest of four neighbouring lanes, by lane permutation within them
+    top = max(top, (uint32_t)__builtin_amdgcn_mov_dpp((int)top, 0xB1, 0xf, 0xf, true));     // 1, 0, 3, 2
+    top = max(top, (uint32_t)__builtin_amdgcn_mov_dpp((int)top, 0x4E, 0xf, 0xf, true));     // 2, 3, 0, 1
     const uint32_t b = act_exp_byte(top);
-    const float inv = act_inv_scale(b);
-    u32x2 w = {0u, 0u};
-    if (b != 255u) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            w[0] |= act_code(v[e], inv) << (8 * e);
-            w[1] |= act_code(v[4 + e], inv) << (8 * e);
-        }
-    }
+    const u32x2 w = act_codes(v, b);
+    const int col = at.col();
     if (col < code_pitch) {
-        u32x2* p = reinterpret_cast<u32x2*>(codes + row * code_pitch + col);
+        u32x2* p = reinterpret_cast<u32x2*>(codes + at.row_at(code_pitch) + col);
         if constexpr (NT) __builtin_nontemporal_store(w, p);
         else *p = w;
     }
-    if ((col & 31) == 0) exps[row * exp_pitch + (col >> 5)] = (uint8_t)b;
+    if ((col & 31) == 0) exps[at.row_at(exp_pitch) + (col >> 5)] = (uint8_t)b;
 }
 
-__device__ __forceinline__ void held8(const int8_t* codes, const uint8_t* exps, int64_t row,
-                                      int col, int code_pitch, int exp_pitch, float* v) {
-    const u32x2 w = *reinterpret_cast<const u32x2*>(codes + row * code_pitch + col);
-    const float s = act_scale(exps[row * exp_pitch + (col >> 5)]);
+__device__ __forceinline__ void held8(const int8_t* codes, const uint8_t* exps, const At& at,
+                                      int code_pitch, int exp_pitch, float* v) {
+    const int col = at.col();
+    const u32x2 w = *reinterpret_cast<const u32x2*>(codes + at.row_at(code_pitch) + col);
+    const float s = act_scale(exps[at.row_at(exp_pitch) + (col >> 5)]);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         v[e] = act_value(w[0], e, s);
@@ -94,34 +101,27 @@ __device__ __forceinline__ void held8(const int8_t* codes, const uint8_t* exps, 
 }
 
 template <typename T, bool AL, bool NT>
-__global__ __launch_bounds__(kThreads) void k_act_pack(const T* __restrict__ x, int64_t stride,
+__global__ __launch_bounds__(kThreads) void k_act_pack(const T* __restrict__ x, uint32_t stride,
                                                        int8_t* __restrict__ codes,
                                                        uint8_t* __restrict__ exps, int cols,
-                                                       int code_pitch, int exp_pitch,
-                                                       uint32_t upr, int64_t units) {
-    // (a group's four lanes share a row and are active together: units is a
-    // multiple of 16)
-    for (int64_t u = (int64_t)blockIdx.x * kThreads + threadIdx.x; u < units;
-         u += (int64_t)gridDim.x * kThreads) {
-        const Unit at = unit_at(u, upr);
+                                                       int code_pitch, int exp_pitch, Walk w) {
+    for (At at(w); at.row < w.rows; at.next(w)) {
         float v[8];
-        load8<T, AL, NT>(x + at.row * stride, at.col, cols, v);
-        hold8<NT>(v, codes, exps, at.row, at.col, code_pitch, exp_pitch);
+        load8<T, AL, NT>(x + at.row_at(stride), at.col(), cols, v);
+        hold8<NT>(v, codes, exps, at, code_pitch, exp_pitch);
     }
 }
 
 template <typename T, bool AL, bool NT>
 __global__ __launch_bounds__(kThreads) void k_act_unpack(const int8_t* __restrict__ codes,
                                                          const uint8_t* __restrict__ exps,
-                                                         T* __restrict__ out, int64_t stride,
+                                                         T* __restrict__ out, uint32_t stride,
                                                          int cols, int code_pitch, int exp_pitch,
-                                                         uint32_t upr, int64_t units) {
-    for (int64_t u = (int64_t)blockIdx.x * kThreads + threadIdx.x; u < units;
-         u += (int64_t)gridDim.x * kThreads) {
-        const Unit at = unit_at(u, upr);
+                                                         Walk w) {
+    for (At at(w); at.row < w.rows; at.next(w)) {
         float v[8];
-        held8(codes, exps, at.row, at.col, code_pitch, exp_pitch, v);
-        store8<T, AL, NT>(out + at.row * stride, at.col, cols, v);
+        held8(codes, exps, at, code_pitch, exp_pitch, v);
+        store8<T, AL, NT>(out + at.row_at(stride), at.col(), cols, v);
     }
 }
 
@@ -151,66 +151,72 @@ __device__ __forceinline__ float act_slope(float g, float s) {
 
 template <typename T, bool AL, bool NT, int ACT>
 __global__ __launch_bounds__(kThreads) void k_glu_forward(GluArgs a, int cols, int code_pitch,
-                                                          int exp_pitch, uint32_t upr,
-                                                          int64_t units) {
+                                                          int exp_pitch, Walk w) {
     const T* gate = static_cast<const T*>(a.gate);
     const T* up = static_cast<const T*>(a.up);
     T* h = static_cast<T*>(a.h);
-    for (int64_t u = (int64_t)blockIdx.x * kThreads + threadIdx.x; u < units;
-         u += (int64_t)gridDim.x * kThreads) {
-        const Unit at = unit_at(u, upr);
+    const uint32_t gs = (uint32_t)a.gate_stride, us = (uint32_t)a.up_stride, hs = (uint32_t)a.h_stride;
+    for (At at(w); at.row < w.rows; at.next(w)) {
         float gv[8], uv[8], hv[8];
-        load8<T, AL, NT>(gate + at.row * a.gate_stride, at.col, cols, gv);
-        load8<T, AL, NT>(up + at.row * a.up_stride, at.col, cols, uv);
+        load8<T, AL, NT>(gate + at.row_at(gs), at.col(), cols, gv);
+        load8<T, AL, NT>(up + at.row_at(us), at.col(), cols, uv);
 #pragma unroll
         for (int e = 0; e < 8; ++e) hv[e] = gv[e] * act_sig<ACT>(gv[e]) * uv[e];
-        store8<T, AL, NT>(h + at.row * a.h_stride, at.col, cols, hv);
-        hold8<NT>(gv, a.gate_codes, a.gate_exps, at.row, at.col, code_pitch, exp_pitch);
-        hold8<NT>(uv, a.up_codes, a.up_exps, at.row, at.col, code_pitch, exp_pitch);
+        store8<T, AL, NT>(h + at.row_at(hs), at.col(), cols, hv);
+        hold8<NT>(gv, a.gate_codes, a.gate_exps, at, code_pitch, exp_pitch);
+        hold8<NT>(uv, a.up_codes, a.up_exps, at, code_pitch, exp_pitch);
     }
 }
 
 template <typename T, bool AL, bool NT, int ACT, bool HOLD>
 __global__ __launch_bounds__(kThreads) void k_glu_backward(GluArgs a, int cols, int code_pitch,
-                                                           int exp_pitch, uint32_t upr,
-                                                           int64_t units) {
+                                                           int exp_pitch, Walk w) {
     const T* dh = static_cast<const T*>(a.dh);
     T* dgate = static_cast<T*>(a.dgate);
     T* dup = static_cast<T*>(a.dup);
-    for (int64_t u = (int64_t)blockIdx.x * kThreads + threadIdx.x; u < units;
-         u += (int64_t)gridDim.x * kThreads) {
-        const Unit at = unit_at(u, upr);
+    const uint32_t ds = (uint32_t)a.dh_stride, gs = (uint32_t)a.dgate_stride, us = (uint32_t)a.dup_stride;
+    for (At at(w); at.row < w.rows; at.next(w)) {
+        const int col = at.col();
         float gv[8], uv[8], dv[8], o[8], hv[8];
-        if (!HOLD || at.col < code_pitch) {
-            held8(a.gate_codes, a.gate_exps, at.row, at.col, code_pitch, exp_pitch, gv);
-            held8(a.up_codes, a.up_exps, at.row, at.col, code_pitch, exp_pitch, uv);
+        load8<T, AL, NT>(dh + at.row_at(ds), col, cols, dv);
+        if (!HOLD || col < code_pitch) {
+            held8(a.gate_codes, a.gate_exps, at, code_pitch, exp_pitch, gv);
+            held8(a.up_codes, a.up_exps, at, code_pitch, exp_pitch, uv);
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) gv[e] = uv[e] = 0.f;
         }
-        load8<T, AL, NT>(dh + at.row * a.dh_stride, at.col, cols, dv);
         float sv[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) sv[e] = act_sig<ACT>(gv[e]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] = dv[e] * uv[e] * act_slope<ACT>(gv[e], sv[e]);
-        store8<T, AL, NT>(dgate + at.row * a.dgate_stride, at.col, cols, o);
+        store8<T, AL, NT>(dgate + at.row_at(gs), col, cols, o);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const float av = gv[e] * sv[e];
             o[e] = dv[e] * av;
-            hv[e] = at.col + e < cols ? av * uv[e] : 0.f;
+            hv[e] = col + e < cols ? av * uv[e] : 0.f;
         }
-        store8<T, AL, NT>(dup + at.row * a.dup_stride, at.col, cols, o);
-        if (HOLD) hold8<NT>(hv, a.h_codes, a.h_exps, at.row, at.col, code_pitch, exp_pitch);
+        store8<T, AL, NT>(dup + at.row_at(us), col, cols, o);
+        if (HOLD) hold8<NT>(hv, a.h_codes, a.h_exps, at, code_pitch, exp_pitch);
     }
 }
 
-// Workgroups of a streaming launch: every unit once, at most 16 rounds of a
-// full GPU (8 workgroups per CU); longer matrices loop.
-int64_t stream_grid(int64_t units) {
-    return std::min<int64_t>(ceil_div(units, kThreads), (int64_t)kCus * 8 * 16);
-}
+// A streaming launch over rows of `upr` units: every unit once, in at most 16
+// rounds of a full GPU (8 workgroups per CU).
+struct Grid {
+    dim3 dim;
+    Walk walk;
+    Grid(int64_t rows, int64_t upr) {
+        const int64_t n = std::min<int64_t>(ceil_div(rows * upr, kThreads), (int64_t)kCus * 8 * 16);
+        dim = dim3((unsigned)n);
+        walk.upr = (uint32_t)upr;
+        walk.rows = (uint32_t)rows;
+        walk.step_rows = (uint32_t)(n * kThreads / upr);
+        walk.step_units = (uint32_t)(n * kThreads % upr);
+    }
+};
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
@@ -251,15 +257,13 @@ int launch_act_pack(const void* x, int32_t dtype, int64_t rows, int64_t cols, in
                     int8_t* codes, uint8_t* exps, void* stream) {
     if (rows == 0) return (int)hipSuccess;
     const int cp = (int)act_code_pitch(cols), ep = (int)act_exp_pitch(cols);
-    const uint32_t upr = (uint32_t)ep * 4;
-    const int64_t units = rows * upr;
-    const dim3 grid((unsigned)stream_grid(units));
+    const Grid grid(rows, (int64_t)ep * 4);
     return by_paths(dtype, al_rows(x, stride, cols, dtype), streams_past_caches(rows * cols, dtype),
                     [&](auto t, auto al, auto nt) {
         using T = decltype(t);
-        hipLaunchKernelGGL((k_act_pack<T, decltype(al)::value, decltype(nt)::value>), grid, dim3(kThreads), 0,
-                           (hipStream_t)stream, static_cast<const T*>(x), stride, codes, exps, (int)cols, cp,
-                           ep, upr, units);
+        hipLaunchKernelGGL((k_act_pack<T, decltype(al)::value, decltype(nt)::value>), grid.dim, dim3(kThreads), 0,
+                           (hipStream_t)stream, static_cast<const T*>(x), (uint32_t)stride, codes, exps, (int)cols, cp,
+                           ep, grid.walk);
     });
 }
 
@@ -267,31 +271,27 @@ int launch_act_unpack(const int8_t* codes, const uint8_t* exps, int64_t rows, in
                       void* out, int32_t dtype, int64_t stride, void* stream) {
     if (rows == 0) return (int)hipSuccess;
     const int cp = (int)act_code_pitch(cols), ep = (int)act_exp_pitch(cols);
-    const uint32_t upr = (uint32_t)cp / 8;
-    const int64_t units = rows * upr;
-    const dim3 grid((unsigned)stream_grid(units));
+    const Grid grid(rows, cp / 8);
     return by_paths(dtype, al_rows(out, stride, cols, dtype), streams_past_caches(rows * cols, dtype),
                     [&](auto t, auto al, auto nt) {
         using T = decltype(t);
-        hipLaunchKernelGGL((k_act_unpack<T, decltype(al)::value, decltype(nt)::value>), grid, dim3(kThreads), 0,
-                           (hipStream_t)stream, codes, exps, static_cast<T*>(out), stride, (int)cols, cp, ep,
-                           upr, units);
+        hipLaunchKernelGGL((k_act_unpack<T, decltype(al)::value, decltype(nt)::value>), grid.dim, dim3(kThreads), 0,
+                           (hipStream_t)stream, codes, exps, static_cast<T*>(out), (uint32_t)stride, (int)cols, cp, ep,
+                           grid.walk);
     });
 }
 
 int launch_glu_forward(const GluArgs& a, void* stream) {
     if (a.rows == 0) return (int)hipSuccess;
     const int cp = (int)act_code_pitch(a.cols), ep = (int)act_exp_pitch(a.cols);
-    const uint32_t upr = (uint32_t)ep * 4;
-    const int64_t units = a.rows * upr;
-    const dim3 grid((unsigned)stream_grid(units));
+    const Grid grid(a.rows, (int64_t)ep * 4);
     const bool al = al_rows(a.gate, a.gate_stride, a.cols, a.dtype) &&
                     al_rows(a.up, a.up_stride, a.cols, a.dtype) &&
                     al_rows(a.h, a.h_stride, a.cols, a.dtype);
     return by_act(a.act, a.dtype, al, streams_past_caches(a.rows * a.cols, a.dtype),
                   [&](auto t, auto w, auto nt, auto act) {
         hipLaunchKernelGGL((k_glu_forward<decltype(t), decltype(w)::value, decltype(nt)::value, decltype(act)::value>),
-                           grid, dim3(kThreads), 0, (hipStream_t)stream, a, (int)a.cols, cp, ep, upr, units);
+                           grid.dim, dim3(kThreads), 0, (hipStream_t)stream, a, (int)a.cols, cp, ep, grid.walk);
     });
 }
 
@@ -299,9 +299,7 @@ int launch_glu_backward(const GluArgs& a, void* stream) {
     if (a.rows == 0) return (int)hipSuccess;
     const int cp = (int)act_code_pitch(a.cols), ep = (int)act_exp_pitch(a.cols);
     const bool hold = a.h_codes != nullptr;
-    const uint32_t upr = hold ? (uint32_t)ep * 4 : (uint32_t)cp / 8;
-    const int64_t units = a.rows * upr;
-    const dim3 grid((unsigned)stream_grid(units));
+    const Grid grid(a.rows, hold ? (int64_t)ep * 4 : cp / 8);
     const bool al = al_rows(a.dh, a.dh_stride, a.cols, a.dtype) &&
                     al_rows(a.dgate, a.dgate_stride, a.cols, a.dtype) &&
                     al_rows(a.dup, a.dup_stride, a.cols, a.dtype);
@@ -311,11 +309,11 @@ int launch_glu_backward(const GluArgs& a, void* stream) {
         constexpr bool AL = decltype(w)::value, NT = decltype(nt)::value;
         constexpr int ACT = decltype(act)::value;
         if (hold)
-            hipLaunchKernelGGL((k_glu_backward<T, AL, NT, ACT, true>), grid, dim3(kThreads), 0, (hipStream_t)stream,
-                               a, (int)a.cols, cp, ep, upr, units);
+            hipLaunchKernelGGL((k_glu_backward<T, AL, NT, ACT, true>), grid.dim, dim3(kThreads), 0, (hipStream_t)stream,
+                               a, (int)a.cols, cp, ep, grid.walk);
         else
-            hipLaunchKernelGGL((k_glu_backward<T, AL, NT, ACT, false>), grid, dim3(kThreads), 0, (hipStream_t)stream,
-                               a, (int)a.cols, cp, ep, upr, units);
+            hipLaunchKernelGGL((k_glu_backward<T, AL, NT, ACT, false>), grid.dim, dim3(kThreads), 0, (hipStream_t)stream,
+                               a, (int)a.cols, cp, ep, grid.walk);
     });
 }
 

@@ -39,11 +39,13 @@ int check_size(const char* fn, const char* what, int64_t v, int64_t least, int64
     return MA_ERR_SHAPE;
 }
 
-// A row stride of at least `least` elements; `rows` of them stay below 2^40.
+// A row stride of at least `least` elements and below 2^31; `rows` of them stay below 2^40.
 int check_stride(const char* fn, const char* what, int64_t stride, int64_t least, int64_t rows) {
-    if (stride >= least && stride <= (int64_t(1) << 40) / (rows > 1 ? rows : 1)) return MA_OK;
-    set_error("%s: %s stride %lld for %lld rows (at least %lld, 2^40 elements in all)", fn, what,
-              (long long)stride, (long long)rows, (long long)least);
+    if (stride >= least && stride < (int64_t(1) << 31) &&
+        stride <= (int64_t(1) << 40) / (rows > 1 ? rows : 1))
+        return MA_OK;
+    set_error("%s: %s stride %lld for %lld rows (at least %lld, below 2^31, 2^40 elements in all)", fn,
+              what, (long long)stride, (long long)rows, (long long)least);
     return MA_ERR_INVALID_ARG;
 }
 

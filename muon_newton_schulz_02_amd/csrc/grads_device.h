@@ -120,11 +120,33 @@ __device__ __forceinline__ float act_inv_scale(uint32_t b) {
 
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
-// Four codes of one 32-bit word, lowest byte first.  A NaN group's inverse
-// scale is 0: its codes are forced to 0 (infinity times 0 converts to 0).
-__device__ __forceinline__ uint32_t act_code(float x, float inv) {
-    const float q = __builtin_amdgcn_fmed3f(rintf(x * inv), -127.f, 127.f);
-    return (uint32_t)(int)q & 0xffu;
+// The codes of 8 values, lowest byte first.  Adding 1.5 2^23 to a quotient rounds
+// it to an integer (nearest, ties to even: the sum's unit is 1) and leaves that
+// in the low bits, so a product and rounding are one fma, and the low byte is the
+// two's complement code.  Only at the largest exponent can a quotient round above
+// 127 and has to be cut.
+__device__ __forceinline__ u32x2 act_codes(const float* v, uint32_t b) {
+    const float inv = act_inv_scale(b);
+    float q[8];
+    if (__builtin_expect(__any(b == 248u), 0)) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            q[e] = __builtin_amdgcn_fmed3f(v[e] * inv, -127.f, 127.f) + 12582912.f;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) q[e] = fmaf(v[e], inv, 12582912.f);
+    }
+    u32x2 w;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        // v_perm_b32 picks bytes of {second, first} = 7..0
+        const uint32_t a = __builtin_amdgcn_perm(__float_as_uint(q[4 * h + 1]), __float_as_uint(q[4 * h]), 0x0c0c0400u);
+        const uint32_t c = __builtin_amdgcn_perm(__float_as_uint(q[4 * h + 3]), __float_as_uint(q[4 * h + 2]), 0x0c0c0400u);
+        w[h] = __builtin_amdgcn_perm(c, a, 0x05040100u);
+    }
+    // (a NaN's payload may end in any byte)
+    if (b == 255u) w = (u32x2){0u, 0u};
+    return w;
 }
 
 __device__ __forceinline__ float act_value(uint32_t w, int byte, float scale) {
