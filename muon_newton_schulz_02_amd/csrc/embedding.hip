@@ -17,7 +17,11 @@
 // kLdsSortTokens one workgroup sorts in its LDS; above, passes over many
 // workgroups.
 //
-// A row is handled in units of 8 columns, one thread each.
+// A row is handled in units of 8 columns, one thread each: kAligned, whole
+// 16-byte aligned units; kShifted, rows at any address, whose last unit begins
+// early enough to end with the row, so that every load is whole and none sits
+// behind a branch (two threads then write the same values to the columns they
+// share, and to add only the owner writes); kTiny, rows of fewer than 8 columns.
 
 #include <hip/hip_runtime.h>
 
@@ -32,13 +36,33 @@ namespace {
 
 constexpr int kThreads = 256;
 
+enum { kAligned = 0, kShifted = 1, kTiny = 2 };
+
+// Columns of unit u: the first one, how many there are, and how many of the first
+// belong to the unit before.
+template <int MODE>
+struct Cols {
+    int at, cnt, shared;
+    __device__ __forceinline__ Cols(int u, int hidden) {
+        at = u * 8;
+        cnt = 8;
+        shared = 0;
+        if (MODE == kShifted) {
+            at = min(u * 8, hidden - 8);
+            shared = u * 8 - at;
+        } else if (MODE == kTiny) {
+            cnt = hidden;
+        }
+    }
+};
+
 // ------------------------------------------------------------- lookup --
 // A row of the output is taken by `lanes` threads (a power of two), each of
 // which moves its column units of kLookRows rows at a time, so that many
 // gathered rows are in flight per thread.
 constexpr int kLookRows = 4;
 
-template <typename TI, typename TO, typename TOK, bool AL, bool NT>
+template <typename TI, typename TO, typename TOK, int MODE, bool NT>
 __global__ __launch_bounds__(kThreads) void k_emb_lookup(const TI* __restrict__ table,
                                                          int64_t table_stride, int64_t vocab,
                                                          const TOK* __restrict__ tokens,
@@ -58,12 +82,13 @@ __global__ __launch_bounds__(kThreads) void k_emb_lookup(const TI* __restrict__ 
             if (row[r] < 0 || row[r] >= vocab) row[r] = -1;
         }
     }
-    for (int col = lane * 8; col < hidden; col += lanes * 8) {
+    for (int u = lane; u * 8 < hidden; u += lanes) {
+        const Cols<MODE> c(u, hidden);
         float v[kLookRows][8];
 #pragma unroll
         for (int r = 0; r < kLookRows; ++r) {
             if (row[r] >= 0) {
-                load_unit<TI, AL>(table + row[r] * table_stride + col, hidden - col, v[r]);
+                load_unit<TI, MODE == kAligned>(table + row[r] * table_stride + c.at, c.cnt, v[r]);
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[r][e] = 0.f;
@@ -77,7 +102,7 @@ __global__ __launch_bounds__(kThreads) void k_emb_lookup(const TI* __restrict__ 
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[r][e] *= scale;
             }
-            store_unit<TO, AL, NT>(out + t * out_stride + col, hidden - col, v[r]);
+            store_unit<TO, MODE == kAligned, NT>(out + t * out_stride + c.at, c.cnt, v[r]);
         }
     }
 }
@@ -133,14 +158,18 @@ __device__ __forceinline__ uint32_t digit_prefix(uint32_t count, uint32_t* wave_
     return base + inc - count;
 }
 
-// Lanes of this wave whose (valid) digit equals this lane's.
+// Lanes of this wave whose (valid) digit equals this lane's: of those that agree so
+// far, those with this lane's value of the next bit.
 __device__ __forceinline__ uint64_t same_digit(uint32_t digit, int bits, bool valid) {
-    uint64_t m = __ballot(valid);
+    const uint64_t all = __ballot(valid);
+    uint32_t lo = (uint32_t)all, hi = (uint32_t)(all >> 32);
     for (int b = 0; b < bits; ++b) {
-        const uint64_t one = __ballot((digit >> b) & 1u);
-        m &= ((digit >> b) & 1u) ? one : ~one;
+        const uint32_t mine = (uint32_t)__builtin_amdgcn_sbfe((int)digit, b, 1);    // all ones or none
+        const uint64_t one = __ballot(mine != 0);
+        lo &= ~((uint32_t)one ^ mine);
+        hi &= ~((uint32_t)(one >> 32) ^ mine);
     }
-    return m;
+    return (uint64_t)hi << 32 | lo;
 }
 
 __device__ __forceinline__ void wave_lds_sync() {
@@ -431,30 +460,38 @@ constexpr int kSumDepth = 8;      // rows of dout in flight per thread
 constexpr int kMaxChunk = 256;
 constexpr int kSumEntries = 2048; // sorted entries a workgroup holds
 
-template <typename TG, bool AL>
-__device__ __forceinline__ void write_row(const SumArgs& a, uint32_t key, int col, float* acc) {
-    TG* g = static_cast<TG*>(a.grad) + (int64_t)key * a.hidden + col;
+// acc (scaled) into a unit of a row of the gradient, or added to it.
+template <typename TG, int MODE>
+__device__ __forceinline__ void write_row(const SumArgs& a, uint32_t key, const Cols<MODE>& c, float* acc) {
+    TG* g = static_cast<TG*>(a.grad) + (int64_t)key * a.hidden + c.at;
     if (a.accumulate) {
         float old[8];
-        load_unit<TG, AL>(g, a.hidden - col, old);
+        load_unit<TG, MODE == kAligned>(g, c.cnt, old);
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[e] = fmaf(acc[e], a.scale, old[e]);
+        if (MODE == kShifted && c.shared > 0) {
+#pragma unroll
+            for (int e = 1; e < 8; ++e)
+                if (e >= c.shared) g[e] = (TG)acc[e];
+            return;
+        }
     } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[e] *= a.scale;
     }
-    store_unit<TG, AL>(g, a.hidden - col, acc);
+    store_unit<TG, MODE == kAligned>(g, c.cnt, acc);
 }
 
-// acc += rows at[0 .. cnt) of dout from column `col` on, in order, kSumDepth at a time.
-template <typename TD, bool AL, typename AT>
-__device__ __forceinline__ void add_rows(float* acc, const TD* dout, int64_t stride, int hidden,
-                                         int col, const AT* at, int cnt) {
+// acc += rows at[0 .. cnt) of dout (its columns c), in order, kSumDepth at a time.
+template <typename TD, int MODE, typename AT>
+__device__ __forceinline__ void add_rows(float* acc, const TD* dout, int64_t stride, const Cols<MODE>& c,
+                                         const AT* at, int cnt) {
     for (int i = 0; i < cnt; i += kSumDepth) {
         float v[kSumDepth][8];
+        // (loads past the last repeat it: no branch)
 #pragma unroll
         for (int k = 0; k < kSumDepth; ++k)
-            if (i + k < cnt) load_unit<TD, AL>(dout + (int64_t)at[i + k] * stride + col, hidden - col, v[k]);
+            load_unit<TD, MODE == kAligned>(dout + (int64_t)at[min(i + k, cnt - 1)] * stride + c.at, c.cnt, v[k]);
 #pragma unroll
         for (int k = 0; k < kSumDepth; ++k) {
             if (i + k >= cnt) break;
@@ -465,7 +502,7 @@ __device__ __forceinline__ void add_rows(float* acc, const TD* dout, int64_t str
 }
 
 // Workgroups [0, sum_blocks): the chunks; the rest: rows without a token.
-template <typename TD, typename TG, bool AL>
+template <typename TD, typename TG, int MODE>
 __global__ __launch_bounds__(kThreads) void k_emb_sum(SumArgs a, FillArgs f) {
     __shared__ uint32_t s_key[kSumEntries];
     __shared__ int32_t s_pos[kSumEntries];
@@ -498,41 +535,44 @@ __global__ __launch_bounds__(kThreads) void k_emb_sum(SumArgs a, FillArgs f) {
         a.through[c] = through;
     }
     const TD* dout = static_cast<const TD*>(a.dout);
-    for (int col = lane * 8; col < a.hidden; col += lanes * 8) {
+    // (entries of no row come last; a load past the others repeats the last of them,
+    // so that no load sits behind a branch)
+    int some = cnt;
+    while (some > 0 && key[some - 1] == none) --some;
+    for (int u = lane; u * 8 < a.hidden && some > 0; u += lanes) {
+        const Cols<MODE> col(u, a.hidden);
         float acc[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[e] = 0.f;
         uint32_t cur = first;
         bool head = from_before;      // the current run began in an earlier chunk
-        float* part = a.partials + c * 2 * a.pitch + col;
-        for (int i = 0; i < cnt && key[i] != none; i += kSumDepth) {
+        float* part = a.partials + c * 2 * a.pitch + col.at;
+        for (int i = 0; i < some; i += kSumDepth) {
             float v[kSumDepth][8];
 #pragma unroll
             for (int k = 0; k < kSumDepth; ++k)
-                if (i + k < cnt && key[i + k] != none)
-                    load_unit<TD, AL>(dout + (int64_t)pos[i + k] * a.dout_stride + col, a.hidden - col, v[k]);
+                load_unit<TD, MODE == kAligned>(dout + (int64_t)pos[min(i + k, some - 1)] * a.dout_stride + col.at,
+                                                col.cnt, v[k]);
 #pragma unroll
             for (int k = 0; k < kSumDepth; ++k) {
-                if (i + k >= cnt) break;
+                if (i + k >= some) break;
                 const uint32_t kk = key[i + k];
                 if (kk != cur) {
-                    if (head) store_unit<float, true>(part, 8, acc);
-                    else write_row<TG, AL>(a, cur, col, acc);
+                    if (head) store_unit<float, MODE == kAligned>(part, 8, acc);
+                    else write_row<TG, MODE>(a, cur, col, acc);
                     head = false;
                     cur = kk;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) acc[e] = 0.f;
                 }
-                if (kk == none) break;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) acc[e] += v[k][e];
             }
         }
-        if (cur == none) continue;
         // (where entries of no row follow cur's run, `last` is theirs)
-        if (head) store_unit<float, true>(part, 8, acc);
-        else if (goes_on && cur == last) store_unit<float, true>(part + a.pitch, 8, acc);
-        else write_row<TG, AL>(a, cur, col, acc);
+        if (head) store_unit<float, MODE == kAligned>(part, 8, acc);
+        else if (goes_on && cur == last) store_unit<float, MODE == kAligned>(part + a.pitch, 8, acc);
+        else write_row<TG, MODE>(a, cur, col, acc);
     }
 }
 
@@ -546,7 +586,7 @@ constexpr int kJoinChunks = kJoinWays;
 constexpr int kJoinShort = 8;
 constexpr int kJoinLanes = kThreads / kJoinWays;    // column units of a slab
 
-template <typename TG, bool AL>
+template <typename TG, int MODE>
 __global__ __launch_bounds__(kThreads) void k_emb_join(SumArgs a) {
     __shared__ float part[kJoinWays][kJoinLanes][8];
     __shared__ int s_pieces[kJoinChunks];
@@ -585,7 +625,9 @@ __global__ __launch_bounds__(kThreads) void k_emb_join(SumArgs a) {
     }
     __syncthreads();
     const int way = threadIdx.x / kJoinLanes, lane = threadIdx.x % kJoinLanes;
-    const int col = ((int)blockIdx.y * kJoinLanes + lane) * 8;
+    const int u = (int)blockIdx.y * kJoinLanes + lane;
+    const bool mine = u * 8 < a.hidden;
+    const Cols<MODE> col(mine ? u : 0, a.hidden);
     // piece p of the run that begins in chunk c
     auto add_pieces = [&](float* acc, int64_t c, int p0, int step, int pieces) {
 #pragma unroll
@@ -593,30 +635,30 @@ __global__ __launch_bounds__(kThreads) void k_emb_join(SumArgs a) {
 #pragma unroll 4
         for (int p = p0; p < pieces; p += step) {
             float v[8];
-            load_unit<float, true>(a.partials + ((c + p) * 2 + (p == 0 ? 1 : 0)) * a.pitch + col, 8, v);
+            load_unit<float, MODE == kAligned>(a.partials + ((c + p) * 2 + (p == 0 ? 1 : 0)) * a.pitch + col.at, 8, v);
 #pragma unroll
             for (int e = 0; e < 8; ++e) acc[e] += v[e];
         }
     };
     float acc[8];
     const int own = s_pieces[way];
-    if (own > 0 && own <= kJoinShort && col < a.hidden) {
+    if (own > 0 && own <= kJoinShort && mine) {
         add_pieces(acc, c0 + way, 0, 1, own);
-        write_row<TG, AL>(a, s_row[way], col, acc);
+        write_row<TG, MODE>(a, s_row[way], col, acc);
     }
     for (int j = 0; j < kJoinChunks; ++j) {
         if (s_pieces[j] <= kJoinShort) continue;
         const int64_t c = c0 + j;
-        if (col < a.hidden) add_pieces(acc, c, way, kJoinWays, s_pieces[j]);
+        if (mine) add_pieces(acc, c, way, kJoinWays, s_pieces[j]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) part[way][lane][e] = acc[e];
         __syncthreads();
-        if (way == 0 && col < a.hidden) {
+        if (way == 0 && mine) {
             for (int w = 1; w < kJoinWays; ++w) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) acc[e] += part[w][lane][e];
             }
-            write_row<TG, AL>(a, s_row[j], col, acc);
+            write_row<TG, MODE>(a, s_row[j], col, acc);
         }
         __syncthreads();
     }
@@ -637,7 +679,7 @@ struct DirectArgs {
     int32_t rows;
 };
 
-template <typename TD, typename TG, bool AL>
+template <typename TD, typename TG, int MODE>
 __global__ __launch_bounds__(kThreads) void k_emb_direct(DirectArgs d) {
     constexpr int W = kThreads / 64;
     __shared__ int s_row[kDirectTokens];        // table rows (local) of the listed tokens,
@@ -702,17 +744,19 @@ __global__ __launch_bounds__(kThreads) void k_emb_direct(DirectArgs d) {
     __syncthreads();
     const int lanes = 1 << a.lane_bits, groups = kThreads >> a.lane_bits;
     const int gl = tid & (lanes - 1), group = tid >> a.lane_bits;
-    const int col = ((int)blockIdx.y * kDirectLanes + gl) * 8;
+    const int u = (int)blockIdx.y * kDirectLanes + gl;
+    const bool mine = u * 8 < a.hidden;
+    const Cols<MODE> col(mine ? u : 0, a.hidden);
     const TD* dout = static_cast<const TD*>(a.dout);
     // lists of up to 16 tokens, and none: a group a row
     for (int r = group; r < rows; r += groups) {
         const int b = s_start[r], cnt = s_start[r + 1] - b;
-        if (cnt > 16 || col >= a.hidden) continue;
+        if (cnt > 16 || !mine) continue;
         float acc[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-        add_rows<TD, AL>(acc, dout, a.dout_stride, a.hidden, col, s_pos + b, cnt);
-        if (cnt > 0 || !a.accumulate) write_row<TG, AL>(a, (uint32_t)(r0 + r), col, acc);
+        add_rows<TD, MODE>(acc, dout, a.dout_stride, col, s_pos + b, cnt);
+        if (cnt > 0 || !a.accumulate) write_row<TG, MODE>(a, (uint32_t)(r0 + r), col, acc);
     }
     // longer ones: all groups (at most W of them) share a row
     const int ways = min(groups, W);
@@ -725,18 +769,17 @@ __global__ __launch_bounds__(kThreads) void k_emb_direct(DirectArgs d) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[e] = 0.f;
         if (group < ways) {
-            if (col < a.hidden)
-                add_rows<TD, AL>(acc, dout, a.dout_stride, a.hidden, col, s_pos + b + p0, p1 - p0);
+            if (mine) add_rows<TD, MODE>(acc, dout, a.dout_stride, col, s_pos + b + p0, p1 - p0);
 #pragma unroll
             for (int e = 0; e < 8; ++e) part[group][gl][e] = acc[e];
         }
         __syncthreads();
-        if (group == 0 && col < a.hidden) {
+        if (group == 0 && mine) {
             for (int w = 1; w < ways; ++w) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) acc[e] += part[w][gl][e];
             }
-            write_row<TG, AL>(a, (uint32_t)(r0 + r), col, acc);
+            write_row<TG, MODE>(a, (uint32_t)(r0 + r), col, acc);
         }
         __syncthreads();
     }
@@ -813,16 +856,17 @@ int launch_embedding_lookup(const void* table, int32_t table_dtype, int64_t voca
     const int lb = lane_bits_for(ceil_div(hidden, 8), 0, 8);
     const int64_t rows = (int64_t)(kThreads >> lb) * kLookRows;
     const dim3 grid((unsigned)ceil_div(n_tokens, rows));
-#define GO(TI, TO, TOK, AL, NT)                                                                 \
-    hipLaunchKernelGGL((k_emb_lookup<TI, TO, TOK, AL, NT>), grid, dim3(kThreads), 0,             \
+#define GO(TI, TO, TOK, MODE, NT)                                                               \
+    hipLaunchKernelGGL((k_emb_lookup<TI, TO, TOK, MODE, NT>), grid, dim3(kThreads), 0,             \
                        (hipStream_t)stream, static_cast<const TI*>(table), table_stride, vocab,  \
                        static_cast<const TOK*>(tokens), n_tokens, scale, static_cast<TO*>(out),   \
                        out_stride, (int)hidden, lb)
 #define GO_AL(TI, TO, TOK)                                                                      \
     do {                                                                                        \
-        if (al && nt) GO(TI, TO, TOK, true, true);                                              \
-        else if (al) GO(TI, TO, TOK, true, false);                                              \
-        else GO(TI, TO, TOK, false, false);                                                     \
+        if (al && nt) GO(TI, TO, TOK, kAligned, true);                                          \
+        else if (al) GO(TI, TO, TOK, kAligned, false);                                          \
+        else if (hidden >= 8) GO(TI, TO, TOK, kShifted, false);                                 \
+        else GO(TI, TO, TOK, kTiny, false);                                                     \
     } while (0)
 #define GO_TOK(TI, TO)                                                                          \
     do {                                                                                        \
@@ -842,12 +886,17 @@ int launch_embedding_lookup(const void* table, int32_t table_dtype, int64_t voca
 
 namespace {
 
-// Calls f(TD{}, TG{}, aligned) with the call's types.
+using Mode0 = std::integral_constant<int, kAligned>;
+using Mode1 = std::integral_constant<int, kShifted>;
+using Mode2 = std::integral_constant<int, kTiny>;
+
+// Calls f(TD{}, TG{}, mode) with the call's types and its rows' mode.
 template <typename F>
-void by_types(bool dout_bf16, bool grad_bf16, bool al, F f) {
+void by_types(bool dout_bf16, bool grad_bf16, bool al, int64_t hidden, F f) {
     auto with = [&](auto td, auto tg) {
-        if (al) f(td, tg, std::true_type{});
-        else f(td, tg, std::false_type{});
+        if (al) f(td, tg, Mode0{});
+        else if (hidden >= 8) f(td, tg, Mode1{});
+        else f(td, tg, Mode2{});
     };
     if (dout_bf16 && grad_bf16) with(__bf16{}, __bf16{});
     else if (dout_bf16) with(__bf16{}, float{});
@@ -933,7 +982,7 @@ int launch_embedding_grad(const EmbGradArgs& g, const EmbPlan& p, void* stream) 
         // about four workgroups per CU, of at most kDirectRows rows
         d.rows = (int)std::min<int64_t>(kDirectRows, std::max<int64_t>(1, ceil_div(g.vocab * slabs, 4 * kCus)));
         const dim3 grid((unsigned)ceil_div(g.vocab, d.rows), slabs);
-        by_types(bd, bg, al, [&](auto td, auto tg, auto w) {
+        by_types(bd, bg, al, g.hidden, [&](auto td, auto tg, auto w) {
             hipLaunchKernelGGL((k_emb_direct<decltype(td), decltype(tg), decltype(w)::value>), grid,
                                dim3(kThreads), 0, st, d);
         });
@@ -971,20 +1020,16 @@ int launch_embedding_grad(const EmbGradArgs& g, const EmbPlan& p, void* stream) 
     const FillArgs rest = share(8);
     const dim3 grid((unsigned)(a.sum_blocks + rest.groups));
     if (grid.x == 0) return (int)hipSuccess;
-    by_types(bd, bg, al, [&](auto td, auto tg, auto w) {
+    by_types(bd, bg, al, g.hidden, [&](auto td, auto tg, auto w) {
         hipLaunchKernelGGL((k_emb_sum<decltype(td), decltype(tg), decltype(w)::value>), grid,
                            dim3(kThreads), 0, st, a, rest);
     });
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.n_chunks < 2) return (int)e;
     const dim3 jgrid((unsigned)ceil_div(a.n_chunks, kJoinChunks), (unsigned)ceil_div(units, kJoinLanes));
-    if (bg) {
-        if (al) hipLaunchKernelGGL((k_emb_join<__bf16, true>), jgrid, dim3(kThreads), 0, st, a);
-        else hipLaunchKernelGGL((k_emb_join<__bf16, false>), jgrid, dim3(kThreads), 0, st, a);
-    } else {
-        if (al) hipLaunchKernelGGL((k_emb_join<float, true>), jgrid, dim3(kThreads), 0, st, a);
-        else hipLaunchKernelGGL((k_emb_join<float, false>), jgrid, dim3(kThreads), 0, st, a);
-    }
+    by_types(bd, bg, al, g.hidden, [&](auto, auto tg, auto w) {
+        hipLaunchKernelGGL((k_emb_join<decltype(tg), decltype(w)::value>), jgrid, dim3(kThreads), 0, st, a);
+    });
     return (int)hipGetLastError();
 }
 

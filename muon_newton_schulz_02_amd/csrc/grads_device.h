@@ -24,7 +24,9 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 // A column unit of 8 elements.  AL: whole and 16-byte aligned; otherwise
 // only the first `cnt` (at least 1) exist, at any element's address: whole units
 // still move as 16-byte accesses (global memory takes them at any alignment), the
-// row's last part element by element.
+// row's last part element by element.  Kernels that keep several loads in flight
+// avoid that branch (after which the compiler waits for what was loaded in it): they
+// shift a row's last unit back to end with the row, over columns of its neighbour.
 typedef unsigned int u32x4u2 __attribute__((ext_vector_type(4), aligned(2)));
 typedef unsigned int u32x4u4 __attribute__((ext_vector_type(4), aligned(4)));
 
@@ -74,8 +76,13 @@ __device__ __forceinline__ void load_unit(const T* p, int cnt, float* v) {
         for (int q = 0; q < (int)sizeof(T) / 2; ++q) w[q] = get16<NT>(reinterpret_cast<const W*>(p) + q);
         widen<T>(w, v);
     } else {
+        // (loads past cnt repeat the last element: without a branch around each, all
+        // are in flight together)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = e < cnt ? (float)p[e] : 0.f;
+        for (int e = 0; e < 8; ++e) {
+            const float x = (float)p[min(e, cnt - 1)];
+            v[e] = e < cnt ? x : 0.f;
+        }
     }
 }
 

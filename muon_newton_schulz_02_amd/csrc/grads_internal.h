@@ -83,15 +83,16 @@ int launch_embedding_grad(const EmbGradArgs& a, const EmbPlan& p, void* stream);
 // Output tiles (256 x 256 for a large product, else 128 x 128), the token axis
 // cut into `slices` of `per` stages of kLgStage tokens; more than one slice
 // leaves float32 partial sums in the workspace for a last launch to add in order.
-// A large product also keeps X in the workspace as bf16, at xt_off.
+// A large product also keeps X in the workspace as bf16, at xt_off, and a copy of
+// dY with aligned rows at dy_off where it needs one (`align`).
 constexpr int kLgStage = 32;
 struct LgPlan {
-    bool big = false;
+    bool big = false, align = false;
     int64_t tiles_n = 0, tiles_k = 0;
     int64_t slices = 1, per = 1;
-    size_t xt_off = 0, total = 0;
+    size_t xt_off = 0, dy_off = 0, total = 0;
 };
-// Whether dY's rows can be copied in 16-byte pieces, as a large product needs.
+// Whether dY's rows can be copied in aligned 16-byte pieces, as a large product does.
 bool linear_grad_big_rows(const void* dy, int64_t n_out, int64_t stride);
 LgPlan linear_grad_plan(int64_t n_tokens, int64_t n_out, int64_t n_in, int32_t dy_dtype,
                         bool big_rows);

@@ -153,28 +153,38 @@ __device__ __forceinline__ void store_wave(ACC acc, float* part, TG* grad, int a
     else by_size(std::false_type{}, grad);
 }
 
-// 8 values as they lie in memory (T's 16 or 32 bytes), zeros past the first cnt.
-template <typename T, bool AL>
-__device__ __forceinline__ void load_raw8(const T* p, int cnt, u32x4* w) {
-    if constexpr (AL) {
-#pragma unroll
-        for (int q = 0; q < (int)sizeof(T) / 2; ++q) w[q] = *(reinterpret_cast<const u32x4*>(p) + q);
-    } else if (cnt >= 8) {
-        if constexpr (sizeof(T) == 4) {
-            w[0] = *reinterpret_cast<const u32x4u4*>(p);
-            w[1] = *(reinterpret_cast<const u32x4u4*>(p) + 1);
-        } else {
-            w[0] = *reinterpret_cast<const u32x4u2*>(p);
-        }
-    } else if constexpr (sizeof(T) == 4) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[e >> 2][e & 3] = e < cnt ? __float_as_uint(p[e]) : 0u;
+// 8 values of a row as they lie in memory (T's 16 or 32 bytes), from any element's
+// address p on.  Where fewer than 8 are left in the row, the load begins `back` elements
+// earlier and the values are shifted down; what comes in above them is of no
+// matter.  No branch: the load stays in flight (the shift waits for it, so it
+// belongs where the values are used).
+template <typename T>
+__device__ __forceinline__ void load_raw8(const T* p, int back, u32x4* w) {
+    if constexpr (sizeof(T) == 4) {
+        w[0] = *reinterpret_cast<const u32x4u4*>(p - back);
+        w[1] = *(reinterpret_cast<const u32x4u4*>(p - back) + 1);
     } else {
-        const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+        w[0] = *reinterpret_cast<const u32x4u2*>(p - back);
+    }
+}
+template <typename T>
+__device__ __forceinline__ void shift_raw8(int back, u32x4* w) {
+    if constexpr (sizeof(T) == 4) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            w[0][e] = (2 * e < cnt ? (uint32_t)h[2 * e] : 0u) |
-                      (2 * e + 1 < cnt ? (uint32_t)h[2 * e + 1] << 16 : 0u);
+        for (int b = 4; b > 0; b /= 2) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t up = e + b < 8 ? w[(e + b) >> 2][(e + b) & 3] : 0u;
+                w[e >> 2][e & 3] = (back & b) ? up : w[e >> 2][e & 3];
+            }
+        }
+    } else {
+        uint64_t lo = (uint64_t)w[0][1] << 32 | w[0][0], hi = (uint64_t)w[0][3] << 32 | w[0][2];
+        lo = (back & 4) ? hi : lo;
+        const int n = 16 * (back & 3);
+        lo = lo >> n | hi << 1 << (63 - n);          // (hi << 64 - n, also for n = 0)
+        hi >>= n;
+        w[0] = (u32x4){(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
     }
 }
 
@@ -226,6 +236,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_linear_grad(LgArgs a, int tiles
     struct Regs {
         u32x4 d[ND], c;
         uint32_t e;
+        bool live;           // !AL: the row is this thread's own
     };
     // Loads are issued in stage order.  AL: buffer loads at running offsets, so that
     // what lies past the slice's last token arrives as zeros without a branch
@@ -243,7 +254,16 @@ __global__ __launch_bounds__(kThreads, 2) void k_linear_grad(LgArgs a, int tiles
     uint32_t vd = (uint32_t)((srow * ld + scol) * es), vc = (uint32_t)(srow * cp + scol);
     uint32_t ve = (uint32_t)(srow * ep + (scol >> 5));
     const uint32_t sd = (uint32_t)(kLgStage * ld * es), sc = (uint32_t)(kLgStage * cp), se = (uint32_t)(kLgStage * ep);
-    const int left = (int)max<int64_t>(0, min<int64_t>(16, a.n_out - n0 - scol));   // columns of dY
+    // !AL: how far back the two chunks of 8 columns begin so as to end with the row, a
+    // column of codes that exists, and where the slice's last stage begins (for loads past it)
+    const bool n8 = a.n_out >= 8;
+    int back[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) back[h] = (int)max<int64_t>(0, n0 + scol + 8 * h + 8 - a.n_out);
+    const int xcol = (int)min<int64_t>(scol, cp - 16 - k0);
+    const char* last_d = bd;
+    const int8_t* last_c = bc;
+    const uint8_t* last_e = be;
     auto load = [&](Regs& v) {
         if constexpr (AL) {
 #pragma unroll
@@ -255,27 +275,34 @@ __global__ __launch_bounds__(kThreads, 2) void k_linear_grad(LgArgs a, int tiles
             vc += sc;
             ve += se;
         } else {
-            // any alignment, stride and size: one of the slice's rows in any case,
-            // cleared if it is not this thread's own
+            // any alignment, stride and size: one of the slice's rows in any case
+            // (`put` clears it if it is not this thread's own)
+            const int64_t row = max<int64_t>(0, min<int64_t>(srow, rows - 1));
+            const char* rowd = rows > 0 ? bd : last_d;
+            const TD* d = reinterpret_cast<const TD*>(rowd) + row * ld + scol;
+            const int8_t* c = (rows > 0 ? bc : last_c) + row * cp + xcol;
+            const uint8_t* e = (rows > 0 ? be : last_e) + row * ep + (xcol >> 5);
+            if (n8) {
 #pragma unroll
-            for (int q = 0; q < ND; ++q) v.d[q] = (u32x4){0u, 0u, 0u, 0u};
-            v.c = (u32x4){0u, 0u, 0u, 0u};
-            v.e = 0;
-            if (rows > 0) {
-                const int64_t row = min<int64_t>(srow, rows - 1);
-                const TD* d = reinterpret_cast<const TD*>(bd) + row * ld + scol;
+                for (int h = 0; h < 2; ++h) load_raw8<TD>(d + 8 * h, back[h], v.d + h * ND / 2);
+            } else {
+                // rows of fewer than 8 columns: the only ones this tile's first chunk has
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    if (left > 8 * h) load_raw8<TD, false>(d + 8 * h, left - 8 * h, v.d + h * ND / 2);
-                if (k0 + scol < cp) {
-                    v.c = *reinterpret_cast<const u32x4*>(bc + row * cp + scol);
-                    v.e = be[row * ep + (scol >> 5)];
+                for (int q = 0; q < ND; ++q) v.d[q] = (u32x4){0u, 0u, 0u, 0u};
+#pragma unroll
+                for (int k = 0; k < 7; ++k) {
+                    if (scol + k >= a.n_out) break;
+                    if constexpr (sizeof(TD) == 4) v.d[k >> 2][k & 3] = __float_as_uint(d[k]);
+                    else v.d[0][k >> 1] |= (uint32_t)__builtin_bit_cast(uint16_t, d[k]) << (16 * (k & 1));
                 }
-                if (srow >= rows) {
-#pragma unroll
-                    for (int q = 0; q < ND; ++q) v.d[q] = (u32x4){0u, 0u, 0u, 0u};
-                    v.e = 0;
-                }
+            }
+            v.c = *reinterpret_cast<const u32x4*>(c);
+            v.e = *e;
+            v.live = srow < rows;
+            if (rows > kLgStage) {
+                last_d = bd + kLgStage * ld * es;
+                last_c = bc + kLgStage * cp;
+                last_e = be + kLgStage * ep;
             }
             rows -= kLgStage;
             bd += kLgStage * ld * es;
@@ -283,7 +310,18 @@ __global__ __launch_bounds__(kThreads, 2) void k_linear_grad(LgArgs a, int tiles
             be += kLgStage * ep;
         }
     };
-    auto put = [&](const Regs& v, char* buf) {
+    auto put = [&](Regs& v, char* buf) {
+        if constexpr (!AL) {
+            if (n8) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) shift_raw8<TD>(min(back[h], 7), v.d + h * ND / 2);
+            }
+#pragma unroll
+            for (int q = 0; q < ND; ++q)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v.d[q][e] = v.live ? v.d[q][e] : 0u;
+            v.e = v.live ? v.e : 0u;
+        }
         if constexpr (NP == 1) {
             *reinterpret_cast<u32x4*>(buf + s0) = v.d[0];
             *reinterpret_cast<u32x4*>(buf + s1) = v.d[1];
@@ -443,6 +481,21 @@ __global__ __launch_bounds__(kThreads) void k_lg_expand(const int8_t* __restrict
     }
 }
 
+// Rows of a dY that cannot be copied in aligned 16-byte pieces, into ones that can
+// (stride n8, n_out rounded up to 8; the columns between are zeros).
+__global__ __launch_bounds__(kThreads) void k_lg_align(const __bf16* __restrict__ dy, int64_t stride,
+                                                       int64_t n_tokens, int64_t n_out,
+                                                       __bf16* __restrict__ out, int64_t n8) {
+    const int64_t col = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 8;
+    if (col >= n8) return;
+    const int cnt = (int)min<int64_t>(8, n_out - col);
+    for (int64_t t = blockIdx.y; t < n_tokens; t += gridDim.y) {
+        float v[8];
+        load_unit<__bf16, false>(dy + t * stride + col, cnt, v);
+        store_unit<__bf16, true>(out + t * n8 + col, 8, v);
+    }
+}
+
 // Buffer resource: base address, stride 0, extent in bytes (accesses past it
 // read zero), raw format.
 __device__ __forceinline__ u32x4 make_rsrc(const void* base, int64_t bytes) {
@@ -487,7 +540,7 @@ struct BigArgs {
     const char* xt;            // the expanded X
     void* grad;
     float* partials;
-    int64_t n_tokens, n_out, n_in, dy_stride, blocks_k;
+    int64_t n_tokens, n_out, n_in, dy_stride, dy_cols, blocks_k;     // dy_cols: n_out, or with padding
     int32_t tiles_n, tiles_k, slices, per;
     int32_t accumulate;
 };
@@ -531,7 +584,7 @@ __global__ __launch_bounds__(kBigThreads) void k_linear_grad_big(BigArgs a) {
 
     BigCopy cp;
     cp.dy = a.dy + (st0 * kLgStage * a.dy_stride + n0) * 2;
-    cp.dy_bytes = ((a.n_tokens - st0 * kLgStage - 1) * a.dy_stride + a.n_out - n0) * 2;
+    cp.dy_bytes = ((a.n_tokens - st0 * kLgStage - 1) * a.dy_stride + a.dy_cols - n0) * 2;
     cp.dy_step = kLgStage * a.dy_stride * 2;
     cp.xt = a.xt + (st0 * a.blocks_k + k0 / 32) * 2048;
     cp.xt_step = a.blocks_k * 2048;
@@ -682,10 +735,12 @@ struct Model {
 };
 constexpr Model kBigModel = {{0.66, 0.0, 0.0}, 0.14, 4.0};
 constexpr Model kSmallBf16 = {{0.48, 0.60, 0.78}, 0.0, 4.7};
+constexpr Model kSmallOdd = {{0.55, 0.75, 1.10}, 0.0, 4.7};      // bf16 rows at any address
 constexpr Model kSmallFp32 = {{1.37, 1.70, 0.0}, 0.0, 5.0};
 constexpr double kLaunchUs = 3.0;
 constexpr double kPartialsPerUs = 7.5e5;   // partial sums written and read back
 constexpr double kExpandPerUs = 1.7e6;     // codes expanded to bf16
+constexpr double kAlignPerUs = 1.2e6;      // values of dY copied into aligned rows
 
 double modelled(const Model& m, int64_t groups, int64_t per, int64_t slices, double elems) {
     int most = 1;
@@ -713,16 +768,18 @@ LgPlan linear_grad_plan(int64_t n_tokens, int64_t n_out, int64_t n_in, int32_t d
     double least = -1.0;
     for (int big = 0; big < 2; ++big) {
         // (below 512 outputs the expansion of X costs more than it saves)
-        if (big && !(big_rows && bf16 && n_out >= 512 && n_in >= 256 && n_tokens >= 512)) continue;
+        if (big && !(bf16 && n_out >= 512 && n_in >= 256 && n_tokens >= 512)) continue;
         const int64_t tile = big ? kBigTile : kTile;
-        const Model& m = big ? kBigModel : bf16 ? kSmallBf16 : kSmallFp32;
+        const Model& m = big ? kBigModel : !bf16 ? kSmallFp32 : big_rows ? kSmallBf16 : kSmallOdd;
         LgPlan p;
         p.big = big != 0;
         p.tiles_n = ceil_div(n_out, tile);
         p.tiles_k = ceil_div(n_in, tile);
         const int64_t tiles = p.tiles_n * p.tiles_k;
-        const double expand =
-            big ? kLaunchUs + (double)n_tokens * (double)round_up(n_in, kBigTile) / kExpandPerUs : 0.0;
+        p.align = big && !big_rows;
+        double expand = 0.0;
+        if (p.big) expand += kLaunchUs + (double)n_tokens * (double)round_up(n_in, kBigTile) / kExpandPerUs;
+        if (p.align) expand += kLaunchUs + (double)n_tokens * (double)n_out / kAlignPerUs;
         for (int64_t n = 1; n <= 64 && n <= std::max<int64_t>(1, stages / 4); ++n) {
             p.per = std::max<int64_t>(1, ceil_div(stages, n));
             p.slices = std::max<int64_t>(1, ceil_div(stages, p.per));
@@ -737,6 +794,10 @@ LgPlan linear_grad_plan(int64_t n_tokens, int64_t n_out, int64_t n_in, int32_t d
     if (best.big) {
         best.xt_off = best.total;
         best.total += (size_t)(stages * kLgStage) * (size_t)round_up(n_in, kBigTile) * 2;
+    }
+    if (best.align) {
+        best.dy_off = best.total;
+        best.total += (size_t)round_up(n_tokens * round_up(n_out, 8) * 2, 256);
     }
     return best;
 }
@@ -754,6 +815,18 @@ int launch_big(const LgArgs& a, const LgPlan& p, hipStream_t st) {
     b.n_out = a.n_out;
     b.n_in = a.n_in;
     b.dy_stride = a.dy_stride;
+    b.dy_cols = a.n_out;
+    if (p.align) {
+        __bf16* rows = reinterpret_cast<__bf16*>(reinterpret_cast<char*>(a.partials) + p.dy_off);
+        const int64_t n8 = round_up(a.n_out, 8);
+        const dim3 agrid((unsigned)ceil_div(n8 / 8, kThreads), (unsigned)std::min<int64_t>(a.n_tokens, 4096));
+        hipLaunchKernelGGL(k_lg_align, agrid, dim3(kThreads), 0, st, static_cast<const __bf16*>(a.dy),
+                           a.dy_stride, a.n_tokens, a.n_out, rows, n8);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return (int)e;
+        b.dy = reinterpret_cast<const char*>(rows);
+        b.dy_stride = b.dy_cols = n8;
+    }
     b.blocks_k = round_up(a.n_in, kBigTile) / 32;
     b.tiles_n = (int)p.tiles_n;
     b.tiles_k = (int)p.tiles_k;

@@ -324,6 +324,36 @@ def test_linear_grad_units(td):
     assert np.array_equal(_f64(M.ma_linear_grad(dy, ident)), _f64(dy)[:k].T)
 
 
+@pytest.mark.parametrize("tg", ["fp32", "bf16"])
+@pytest.mark.parametrize("m,n,k,pad", [(3000, 3001, 2048, 0), (4100, 3004, 2047, 1),
+                                       (3000, 3000, 2048, 7), (8192, 1024, 4096, 0)])
+def test_linear_grad_large_odd(tg, m, n, k, pad):
+    """Large products whose dY rows are not 16-byte aligned (they are copied into
+    ones that are), and one that is cut into slices, against float64 on the GPU."""
+    rng = np.random.default_rng(m + n)
+    dy, wide = _strided(rng.standard_normal((m, n)), pad, "bf16")
+    if pad:
+        wide[:, n:] = float("nan")
+    c = M.ma_act_pack(_dev(_activation(rng, m, k), "bf16"))
+    x = M.ma_act_unpack(c).double()
+    d = dy.double()
+    want = (d.t().contiguous() @ x).cpu().numpy()
+    mag = (d.abs().t().contiguous() @ x.abs()).cpu().numpy()
+    tol = (4 * m + 4) * 2 * R.F32 * mag          # as in the reference module
+    got = M.ma_linear_grad(dy, c, grad_dtype=DT[tg])
+    _close(got, want, R.rounded(want, tol, tg))
+    out = got.clone()
+    M.ma_linear_grad(dy, c, out=out, accumulate=True)
+    twice = want + _f64(got)
+    _close(out, twice, R.rounded(twice, tol + 4 * R.F32 * np.abs(twice), tg))
+    # a sharper look than the bound for any signs: the M / 16 additions of a sum of
+    # random products err by at most a step, 2^-23, of a partial sum that is no larger in
+    # root mean square than the result, and independently, so by less than 2^-23
+    # sqrt(M / 16) = 2.7e-6 of it for M = 8192; rounding to bf16 by at most 2^-8
+    rel = np.linalg.norm(_f64(got) - want) / np.linalg.norm(want)
+    assert rel < (2.7e-6 if tg == "fp32" else 2 ** -8 + 2.7e-6), rel
+
+
 @pytest.mark.parametrize("m", [1024, 1055])
 def test_linear_grad_large_product_values(m):
     """The large-product kernel, value by value: one token of dy is one, so the
