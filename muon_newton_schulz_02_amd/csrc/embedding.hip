@@ -797,7 +797,7 @@ int lane_bits_for(int64_t units, int least, int most) {
 
 }  // namespace
 
-// Up to this many tokens one workgroup sorts: its two passes take 13 us at 4096
+// Up to this many tokens one workgroup sorts: its two passes take 10.8 us at 4096
 // tokens (6 at 2048), the four launches over many workgroups 22.
 static constexpr int64_t kLdsSortTokens = 4096;
 
@@ -818,11 +818,18 @@ EmbPlan embedding_plan(int64_t n_tokens, int64_t vocab, int64_t hidden) {
     p.bits = (nbits + p.passes - 1) / p.passes;
     p.per = std::max<int64_t>(kSortThreads, round_up(ceil_div(n_tokens, 128), kSortThreads));
     p.blocks = ceil_div(n_tokens, p.per);
-    // chunks for about 256 K threads, of 16 entries at least (a chunk may leave
-    // two partial rows)
+    // Chunks of up to 64 entries, so many that each CU gets the same number of
+    // workgroups, or longer ones where that number would pass 4 (a run through very many
+    // chunks is joined by few threads); of 16 entries at least, since a chunk may leave two
+    // partial rows.  (Against chunks for 256 K threads, 16 to 24 entries here: 16384 tokens
+    // into 151000 x 2048 bf16 142 -> 130 us, 65536 into 1000 x 256 34 -> 31, 50021 into
+    // 32003 x 1001 76 -> 74.5.  Always 64: 524288 tokens into 32000 x 1024, half of them
+    // one row, 380 -> 469.)
     p.lane_bits = lane_bits_for(ceil_div(hidden, 8), 3, 8);
-    const int64_t most = std::min<int64_t>(kMaxChunk, kSumEntries / (kThreads >> p.lane_bits));
-    p.chunk = std::min(most, std::max<int64_t>(16, round_up((n_tokens << p.lane_bits) >> 18, 8)));
+    const int64_t per = kThreads >> p.lane_bits;
+    const int64_t most = std::min<int64_t>(kMaxChunk, kSumEntries / per);
+    const int64_t rounds = std::min<int64_t>(4, ceil_div(n_tokens, per * kCus * 64));
+    p.chunk = std::min(most, std::max<int64_t>(16, ceil_div(n_tokens, per * kCus * rounds)));
     p.n_chunks = ceil_div(n_tokens, p.chunk);
     p.pitch = round_up(hidden, 8);
     size_t off = 0;
