@@ -228,6 +228,15 @@ def test_embedding_grad(td, tg, n, v, h, how):
     assert torch.equal(got, again)
 
 
+@pytest.mark.parametrize("td,tg", [("bf16", "fp32"), ("fp32", "bf16")])
+@pytest.mark.parametrize("n,v,h,how", [
+    # chunks of 20, 18, 35 and 69 sorted entries, one to four workgroups per CU
+    (5003, 400, 2040, "mixed"), (5003, 2, 2040, "one"), (9001, 5000, 1001, "zipf"),
+    (70001, 900, 300, "mixed"), (140001, 30, 520, "mixed")])
+def test_embedding_grad_of_long_chunks(td, tg, n, v, h, how):
+    test_embedding_grad(td, tg, n, v, h, how)
+
+
 @pytest.mark.parametrize("tg", ["fp32", "bf16"])
 @pytest.mark.parametrize("n,v,h,how", [(1, 4, 8, "uniform"), (300, 20, 40, "mixed"),
                                        (3000, 900, 33, "zipf"), (0, 6, 8, "none")])
