@@ -73,7 +73,7 @@ __global__ __launch_bounds__(kThreads) void k_emb_lookup(const TI* __restrict__ 
                                                          int hidden, int lane_bits) {
     const int lanes = 1 << lane_bits, per = kThreads >> lane_bits;
     const int lane = threadIdx.x & (lanes - 1), sub = threadIdx.x >> lane_bits;
-    const int64_t t0 = (int64_t)blockIdx.x * per * kLookRows + sub;
+    const int64_t t0 = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * per * kLookRows + sub;
     int64_t row[kLookRows];
 #pragma unroll
     for (int r = 0; r < kLookRows; ++r) {
@@ -873,7 +873,9 @@ int launch_embedding_lookup(const void* table, int32_t table_dtype, int64_t voca
     const bool nt = streams_past_caches(n_tokens * hidden, out_dtype);
     const int lb = lane_bits_for(ceil_div(hidden, 8), 0, 8);
     const int64_t rows = (int64_t)(kThreads >> lb) * kLookRows;
-    const dim3 grid((unsigned)ceil_div(n_tokens, rows));
+    // (a launch's threads along one axis stay below 2^32)
+    const int64_t blocks = ceil_div(n_tokens, rows), wide = std::min<int64_t>(blocks, 65536);
+    const dim3 grid((unsigned)wide, (unsigned)ceil_div(blocks, wide));
 #define GO(TI, TO, TOK, MODE, NT)                                                               \
     hipLaunchKernelGGL((k_emb_lookup<TI, TO, TOK, MODE, NT>), grid, dim3(kThreads), 0,             \
                        (hipStream_t)stream, static_cast<const TI*>(table), table_stride, vocab,  \

@@ -305,7 +305,7 @@ static int check_lg_shape(const char* fn, int64_t n_tokens, int64_t n_out, int64
     TRY(check_size(fn, "n_in", n_in, 1, kMaxHidden));
     TRY(check_elems(fn, "dy", n_tokens, n_out));
     TRY(check_elems(fn, "x", n_tokens, n_in));
-    // (up to 2^26 tiles of work and slices: the grid stays below 2^31)
+    // (about 2^22 tiles at most: a launch's threads stay below 2^32)
     if (n_out > (int64_t(1) << 36) / n_in) {
         set_error("%s: grad has more than 2^36 elements", fn);
         return MA_ERR_SHAPE;

@@ -792,7 +792,10 @@ LgPlan linear_grad_plan(int64_t n_tokens, int64_t n_out, int64_t n_in, int32_t d
         double expand = 0.0;
         if (p.big) expand += kLaunchUs + (double)n_tokens * (double)round_up(n_in, kBigTile) / kExpandPerUs;
         if (p.align) expand += kLaunchUs + (double)n_tokens * (double)n_out / kAlignPerUs;
-        for (int64_t n = 1; n <= 64 && n <= std::max<int64_t>(1, stages / 4); ++n) {
+        // (where the tiles are many, slices only even out the last round, for partial sums of
+        // the gradient's size each: no more than 8 workgroups per CU come of them)
+        const int64_t most = std::min<int64_t>({64, std::max<int64_t>(1, stages / 4), ceil_div(8 * kCus, tiles)});
+        for (int64_t n = 1; n <= most; ++n) {
             p.per = std::max<int64_t>(1, ceil_div(stages, n));
             p.slices = std::max<int64_t>(1, ceil_div(stages, p.per));
             const double t = expand + modelled(m, tiles * p.slices, p.per, p.slices, elems);

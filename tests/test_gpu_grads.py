@@ -200,6 +200,17 @@ def _tokens(rng, how, n, v):
     return np.full(n, -1)      # "none"
 
 
+def test_lookup_of_more_rows_than_one_grid_axis():
+    n, v, h = 4 * 65536 + 5, 301, 1032          # 4 rows a workgroup
+    table = torch.randn(v, h, device="cuda").to(torch.bfloat16)
+    tok = torch.randint(-1, v, (n,), device="cuda")
+    out = torch.full((n + 1, h), 7.0, dtype=torch.bfloat16, device="cuda")
+    M.ma_embedding_lookup(table, tok, out=out[:n])
+    want = torch.cat([table, torch.zeros_like(table[:1])])[tok]
+    assert torch.equal(out[:n], want)
+    assert torch.all(out[n] == 7.0)
+
+
 @pytest.mark.parametrize("td,tg", [("fp32", "fp32"), ("bf16", "fp32"), ("bf16", "bf16"),
                                    ("fp32", "bf16")])
 @pytest.mark.parametrize("n,v,h,how", [
