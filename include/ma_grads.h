@@ -112,7 +112,9 @@ int ma_embedding_grad(const void* dout, int32_t dout_dtype, int64_t dout_stride,
 /* ---- linear layer ----------------------------------------------------------- */
 
 /* Bytes of workspace (256-byte aligned; 0: none, NULL may be passed) one
- * ma_linear_grad call needs.  Errors: INVALID_ARG, SHAPE. */
+ * ma_linear_grad call needs, whatever dy's address and stride.  A large product
+ * takes 2 bytes per element of x in it and, of a float32 dy or one with odd rows, 6 or
+ * 2 per element of dy.  Errors: INVALID_ARG, SHAPE. */
 int ma_linear_grad_workspace_size(int64_t n_tokens, int64_t n_out, int64_t n_in,
                                   int32_t dy_dtype, size_t* bytes);
 

@@ -83,11 +83,12 @@ int launch_embedding_grad(const EmbGradArgs& a, const EmbPlan& p, void* stream);
 // Output tiles (256 x 256 for a large product, else 128 x 128), the token axis
 // cut into `slices` of `per` stages of kLgStage tokens; more than one slice
 // leaves float32 partial sums in the workspace for a last launch to add in order.
-// A large product also keeps X in the workspace as bf16, at xt_off, and a copy of
-// dY with aligned rows at dy_off where it needs one (`align`).
+// A large product also keeps X in the workspace as bf16, at xt_off, and at dy_off a copy of
+// dY with aligned rows where it needs one (`align`), or a float32 dY's three bf16 parts
+// (`split`), which it takes one after the other: three times the stages.
 constexpr int kLgStage = 32;
 struct LgPlan {
-    bool big = false, align = false;
+    bool big = false, align = false, split = false;
     int64_t tiles_n = 0, tiles_k = 0;
     int64_t slices = 1, per = 1;
     size_t xt_off = 0, dy_off = 0, total = 0;

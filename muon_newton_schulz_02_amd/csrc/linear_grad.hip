@@ -8,7 +8,8 @@
 // while it is staged: a held value is exact in bf16.  Products of two bf16
 // values are exact in the matrix cores' float32, so a bf16 dY enters with
 // nothing rounded; a float32 dY is cut into three bf16 parts of 8 bits
-// each, which add up to it, and enters as three products.  Sums are float32.
+// each, which add up to it, and enters as three products, side by side on the small tiles,
+// part after part on the large ones.  Sums are float32.
 //
 // LDS layout of a stage operand of W columns: token row t at t * 2 W bytes,
 // its 16-byte chunk c (8 columns) at slot c ^ ((t & 3) << 2), so the four
@@ -507,6 +508,36 @@ __global__ __launch_bounds__(kThreads) void k_lg_align(const __bf16* __restrict_
     }
 }
 
+// The three bf16 parts of a float32 dY, as three matrices of `rows` token rows (whole stages;
+// those past the last token are zeros) and n8 columns.  The product then runs over the three as
+// over one token axis, and begins X again with each.  Bound by HBM: 8192 x 4096 in 51 us
+// (335 MB, 6.6 TB/s), 32768 x 8192 in 520 (2.7 GB, 5.2).  With it, products by 256 x 256 tiles take
+// 243 us instead of 309 by k_linear_grad's (8192 tokens x 4096 x 1024), 189 instead of 265
+// (2048 x 8192 x 2048) and 2830 instead of 4120 (32768 x 8192 x 2048: 1.17 PFLOP/s of the
+// three products' 3.3 TFLOP in all, 1.36 in the product itself).
+template <bool AL>
+__global__ __launch_bounds__(kThreads) void k_lg_split(const float* __restrict__ dy, int64_t stride,
+                                                       int64_t n_tokens, int64_t n_out,
+                                                       __bf16* __restrict__ out, int64_t rows, int64_t n8) {
+    const int64_t col = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 8;
+    if (col >= n8) return;
+    const int cnt = (int)min<int64_t>(8, n_out - col);
+    for (int64_t t = blockIdx.y; t < rows; t += gridDim.y) {
+        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (t < n_tokens) load_unit<float, AL>(dy + t * stride + col, cnt, v);
+        uint32_t part[3][8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) split3(v[e], part[0][e], part[1][e], part[2][e]);
+#pragma unroll
+        for (int p = 0; p < 3; ++p) {
+            u32x4 w;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = high_halves(part[p][2 * i], part[p][2 * i + 1]);
+            *reinterpret_cast<u32x4*>(out + (p * rows + t) * n8 + col) = w;
+        }
+    }
+}
+
 // Buffer resource: base address, stride 0, extent in bytes (accesses past it
 // read zero), raw format.
 __device__ __forceinline__ u32x4 make_rsrc(const void* base, int64_t bytes) {
@@ -552,6 +583,7 @@ struct BigArgs {
     void* grad;
     float* partials;
     int64_t n_tokens, n_out, n_in, dy_stride, dy_cols, blocks_k;     // dy_cols: n_out, or with padding
+    int64_t xt_stages;         // stages of X: those of dY, or a third where dY is in parts
     int32_t tiles_n, tiles_k, slices, per;
     int32_t accumulate;
 };
@@ -564,6 +596,7 @@ struct BigCopy {
     int64_t dy_bytes;          // extent from dy to the end of the last row
     int64_t dy_step, xt_step;  // bytes from stage to stage
     int64_t left;              // stages not copied yet
+    int64_t xt_left, xt_all;   // stages of X until it begins again, and all of them
     uint32_t voff_d[2], voff_x[2];
     uint32_t wbase;
 
@@ -578,6 +611,10 @@ struct BigCopy {
         xt += xt_step;
         dy_bytes -= dy_step;
         --left;
+        if (--xt_left == 0) {
+            xt -= xt_all * xt_step;
+            xt_left = xt_all;
+        }
     }
 };
 
@@ -597,7 +634,10 @@ __global__ __launch_bounds__(kBigThreads) void k_linear_grad_big(BigArgs a) {
     cp.dy = a.dy + (st0 * kLgStage * a.dy_stride + n0) * 2;
     cp.dy_bytes = ((a.n_tokens - st0 * kLgStage - 1) * a.dy_stride + a.dy_cols - n0) * 2;
     cp.dy_step = kLgStage * a.dy_stride * 2;
-    cp.xt = a.xt + (st0 * a.blocks_k + k0 / 32) * 2048;
+    const int64_t xt0 = st0 % a.xt_stages;
+    cp.xt = a.xt + (xt0 * a.blocks_k + k0 / 32) * 2048;
+    cp.xt_all = a.xt_stages;
+    cp.xt_left = a.xt_stages - xt0;
     cp.xt_step = a.blocks_k * 2048;
     cp.left = nk;
     cp.wbase = (uint32_t)wave * 2048u;
@@ -748,11 +788,12 @@ struct Model {
 constexpr Model kBigModel = {{0.66, 0.0, 0.0}, 0.14, 4.0};
 constexpr Model kSmallBf16 = {{0.48, 0.60, 0.78}, 0.0, 4.7};
 constexpr Model kSmallOdd = {{0.55, 0.75, 1.10}, 0.0, 4.7};      // bf16 rows at any address
-constexpr Model kSmallFp32 = {{1.37, 1.70, 0.0}, 0.0, 5.0};
+constexpr Model kSmallFp32 = {{1.37, 2.10, 0.0}, 0.0, 5.0};
 constexpr double kLaunchUs = 3.0;
 constexpr double kPartialsPerUs = 7.5e5;   // partial sums written and read back
 constexpr double kExpandPerUs = 1.7e6;     // codes expanded to bf16
 constexpr double kAlignPerUs = 1.2e6;      // values of dY copied into aligned rows
+constexpr double kSplitPerUs = 5.5e5;      // float32 values of dY cut into three parts
 
 double modelled(const Model& m, int64_t groups, int64_t per, int64_t slices, double elems) {
     int most = 1;
@@ -780,7 +821,7 @@ LgPlan linear_grad_plan(int64_t n_tokens, int64_t n_out, int64_t n_in, int32_t d
     double least = -1.0;
     for (int big = 0; big < 2; ++big) {
         // (below 512 outputs the expansion of X costs more than it saves)
-        if (big && !(bf16 && n_out >= 512 && n_in >= 256 && n_tokens >= 512)) continue;
+        if (big && !(n_out >= 512 && n_in >= 256 && n_tokens >= 512)) continue;
         const int64_t tile = big ? kBigTile : kTile;
         const Model& m = big ? kBigModel : !bf16 ? kSmallFp32 : big_rows ? kSmallBf16 : kSmallOdd;
         LgPlan p;
@@ -788,16 +829,19 @@ LgPlan linear_grad_plan(int64_t n_tokens, int64_t n_out, int64_t n_in, int32_t d
         p.tiles_n = ceil_div(n_out, tile);
         p.tiles_k = ceil_div(n_in, tile);
         const int64_t tiles = p.tiles_n * p.tiles_k;
-        p.align = big && !big_rows;
+        p.align = big && bf16 && !big_rows;
+        p.split = big && !bf16;
+        const int64_t run = p.split ? 3 * stages : stages;
         double expand = 0.0;
         if (p.big) expand += kLaunchUs + (double)n_tokens * (double)round_up(n_in, kBigTile) / kExpandPerUs;
         if (p.align) expand += kLaunchUs + (double)n_tokens * (double)n_out / kAlignPerUs;
+        if (p.split) expand += kLaunchUs + (double)n_tokens * (double)n_out / kSplitPerUs;
         // (where the tiles are many, slices only even out the last round, for partial sums of
         // the gradient's size each: no more than 8 workgroups per CU come of them)
-        const int64_t most = std::min<int64_t>({64, std::max<int64_t>(1, stages / 4), ceil_div(8 * kCus, tiles)});
+        const int64_t most = std::min<int64_t>({64, std::max<int64_t>(1, run / 4), ceil_div(8 * kCus, tiles)});
         for (int64_t n = 1; n <= most; ++n) {
-            p.per = std::max<int64_t>(1, ceil_div(stages, n));
-            p.slices = std::max<int64_t>(1, ceil_div(stages, p.per));
+            p.per = std::max<int64_t>(1, ceil_div(run, n));
+            p.slices = std::max<int64_t>(1, ceil_div(run, p.per));
             const double t = expand + modelled(m, tiles * p.slices, p.per, p.slices, elems);
             if (least < 0.0 || t < least) {
                 least = t;
@@ -814,12 +858,17 @@ LgPlan linear_grad_plan(int64_t n_tokens, int64_t n_out, int64_t n_in, int32_t d
         best.dy_off = best.total;
         best.total += (size_t)round_up(n_tokens * round_up(n_out, 8) * 2, 256);
     }
+    if (best.split) {
+        best.dy_off = best.total;
+        best.total += (size_t)(3 * stages * kLgStage) * (size_t)round_up(n_out, 8) * 2;
+    }
     return best;
 }
 
 namespace {
 
 int launch_big(const LgArgs& a, const LgPlan& p, hipStream_t st) {
+    const int64_t stages = ceil_div(a.n_tokens, kLgStage);
     char* xt = reinterpret_cast<char*>(a.partials) + p.xt_off;
     BigArgs b{};
     b.dy = static_cast<const char*>(a.dy);
@@ -831,6 +880,7 @@ int launch_big(const LgArgs& a, const LgPlan& p, hipStream_t st) {
     b.n_in = a.n_in;
     b.dy_stride = a.dy_stride;
     b.dy_cols = a.n_out;
+    b.xt_stages = stages;
     if (p.align) {
         __bf16* rows = reinterpret_cast<__bf16*>(reinterpret_cast<char*>(a.partials) + p.dy_off);
         const int64_t n8 = round_up(a.n_out, 8);
@@ -841,6 +891,22 @@ int launch_big(const LgArgs& a, const LgPlan& p, hipStream_t st) {
         if (e != hipSuccess) return (int)e;
         b.dy = reinterpret_cast<const char*>(rows);
         b.dy_stride = b.dy_cols = n8;
+    } else if (p.split) {
+        __bf16* rows = reinterpret_cast<__bf16*>(reinterpret_cast<char*>(a.partials) + p.dy_off);
+        const int64_t n8 = round_up(a.n_out, 8), r = stages * kLgStage;
+        const dim3 sgrid((unsigned)ceil_div(n8 / 8, kThreads), (unsigned)std::min<int64_t>(r, 4096));
+        const float* dy = static_cast<const float*>(a.dy);
+        if (aligned16(dy) && a.n_out % 8 == 0 && a.dy_stride % 4 == 0)
+            hipLaunchKernelGGL((k_lg_split<true>), sgrid, dim3(kThreads), 0, st, dy, a.dy_stride, a.n_tokens,
+                               a.n_out, rows, r, n8);
+        else
+            hipLaunchKernelGGL((k_lg_split<false>), sgrid, dim3(kThreads), 0, st, dy, a.dy_stride, a.n_tokens,
+                               a.n_out, rows, r, n8);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return (int)e;
+        b.dy = reinterpret_cast<const char*>(rows);
+        b.dy_stride = b.dy_cols = n8;
+        b.n_tokens = 3 * r;
     }
     b.blocks_k = round_up(a.n_in, kBigTile) / 32;
     b.tiles_n = (int)p.tiles_n;
@@ -848,7 +914,6 @@ int launch_big(const LgArgs& a, const LgPlan& p, hipStream_t st) {
     b.slices = (int)p.slices;
     b.per = (int)p.per;
     b.accumulate = a.accumulate;
-    const int64_t stages = ceil_div(a.n_tokens, kLgStage);
     const dim3 egrid((unsigned)p.tiles_k, (unsigned)std::min<int64_t>(stages, 65535));
     hipLaunchKernelGGL(k_lg_expand, egrid, dim3(kThreads), 0, st, a.codes, a.exps, xt, a.n_tokens,
                        stages, act_code_pitch(a.n_in), act_exp_pitch(a.n_in), b.blocks_k);

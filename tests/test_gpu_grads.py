@@ -374,6 +374,75 @@ def test_linear_grad_large_odd(tg, m, n, k, pad):
     assert rel < (2.7e-6 if tg == "fp32" else 2 ** -8 + 2.7e-6), rel
 
 
+def _taken_in_parts(m, n, k):
+    """Whether a float32 dY is cut into its three parts before the product: the
+    workspace then holds them."""
+    return M.ma_linear_grad_workspace_size(m, n, k, torch.float32) >= 6 * m * n
+
+
+@pytest.mark.parametrize("tg", ["fp32", "bf16"])
+@pytest.mark.parametrize("m,n,k,pad", [
+    # one slice, two, three (each a part), four, and six of three parts; odd rows and columns
+    (2050, 700, 300, 0), (2050, 512, 520, 4), (700, 2001, 2051, 0), (1025, 700, 4100, 3),
+    (2050, 2001, 1030, 7), (4096, 1024, 2048, 8)])
+def test_linear_grad_large_float32(tg, m, n, k, pad):
+    """Large products of a float32 dY, against float64 on the GPU."""
+    assert _taken_in_parts(m, n, k)
+    rng = np.random.default_rng(m + n)
+    dy, wide = _strided(rng.standard_normal((m, n)), pad, "fp32")
+    if pad:
+        wide[:, n:] = float("nan")
+    c = M.ma_act_pack(_dev(_activation(rng, m, k), "bf16"))
+    x = M.ma_act_unpack(c).double()
+    d = dy.double()
+    want = (d.t().contiguous() @ x).cpu().numpy()
+    mag = (d.abs().t().contiguous() @ x.abs()).cpu().numpy()
+    tol = (4 * m + 4) * 2 * R.F32 * mag          # as in the reference module
+    need = M.ma_linear_grad_workspace_size(m, n, k, torch.float32)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    got = M.ma_linear_grad(dy, c, grad_dtype=DT[tg], workspace=ws)
+    _close(got, want, R.rounded(want, tol, tg))
+    # the 3 M / 16 additions of a sum of random products err by at most a step, 2^-23, of
+    # a partial sum, independently: by less than 2^-23 sqrt(3 M / 16) = 3.4e-6 for M = 4096
+    # in root mean square; rounding to bf16 by at most 2^-8
+    rel = np.linalg.norm(_f64(got) - want) / np.linalg.norm(want)
+    assert rel < (3.4e-6 if tg == "fp32" else 2 ** -8 + 3.4e-6), rel
+    out = got.clone()
+    M.ma_linear_grad(dy, c, out=out, accumulate=True, workspace=ws)
+    twice = want + _f64(got)
+    _close(out, twice, R.rounded(twice, tol + 4 * R.F32 * np.abs(twice), tg))
+    assert torch.equal(got, M.ma_linear_grad(dy, c, out=torch.full_like(got, float("nan"))))
+
+
+@pytest.mark.parametrize("m,n,k", [(2050, 700, 300), (700, 2001, 2051)])
+def test_linear_grad_large_float32_values(m, n, k):
+    """Value by value: x is all ones and one token of each output's dy is not zero, so
+    the output's row is that float32 value, whole: the parts add up to it."""
+    assert _taken_in_parts(m, n, k)
+    rng = np.random.default_rng(8)
+    c = M.ma_act_pack(torch.ones(m, k, device="cuda"))
+    v = (torch.randn(n, device="cuda") * torch.exp2(torch.randint(-40, 40, (n,), device="cuda").float()))
+    v[3] = torch.finfo(torch.float32).max
+    v[4] = -torch.finfo(torch.float32).max
+    at = torch.from_numpy(rng.integers(0, m, n)).cuda()
+    at[:6] = m - 1
+    dy = torch.zeros((m, n), device="cuda")
+    dy[at, torch.arange(n, device="cuda")] = v
+    assert torch.equal(M.ma_linear_grad(dy, c), v[:, None].expand(n, k))
+    dy.view(torch.int32)[m - 1, 5] = 0x7f800001
+    dy[m // 2, 333] = float("inf")
+    xs = torch.ones(m, k, device="cuda")
+    xs[m - 1, 40] = float("nan")
+    got = M.ma_linear_grad(dy, c)
+    assert torch.isnan(got[5]).all() and torch.isinf(got[333]).all()
+    got = M.ma_linear_grad(dy, M.ma_act_pack(xs))
+    assert torch.isnan(got[:, 32:64]).all()
+    rest = torch.ones(n, k, dtype=torch.bool, device="cuda")
+    rest[5] = rest[333] = False
+    rest[:, 32:64] = False
+    assert torch.isfinite(got[rest]).all()
+
+
 @pytest.mark.parametrize("m", [1024, 1055])
 def test_linear_grad_large_product_values(m):
     """The large-product kernel, value by value: one token of dy is one, so the
