@@ -60,8 +60,8 @@ struct Cols {
 // A row of the output is taken by `lanes` threads (a power of two), each of
 // which moves its column units of kLookRows rows at a time, so that many
 // gathered rows are in flight per thread.  Bound by HBM: 65536 rows of 2048 bf16 out of
-// 151000 take 78 to 82 us (75 MB of them read, for the rest of the tokens repeat; 268 MB
-// written), a single launch of 37 rows 2.6 us.
+// 151000 take 76 to 82 us (155 MB read, since tokens repeat, and 268 MB written: 5.3 TB/s), 37 rows of
+// 256 2.6 us.
 constexpr int kLookRows = 4;
 
 template <typename TI, typename TO, typename TOK, int MODE, bool NT>
@@ -508,8 +508,8 @@ __device__ __forceinline__ void add_rows(float* acc, const TD* dout, int64_t str
 
 // Workgroups [0, sum_blocks): the chunks; the rest: rows without a token.  Reads the
 // gathered rows and writes each row of the table once, 8 rows of dout in flight per thread.
-// Bound by HBM where rows are 16-byte aligned (16384 tokens into 151000 x 2048 bf16: 60 us, 5.8 TB/s);
-// 50021 tokens into 32003 x 1001 fp32 take 45 us (3 TB/s: rows of 4004 bytes at any
+// Bound by HBM where rows are 16-byte aligned (16384 tokens into 151000 x 2048 bf16: 60 us, 6.4 TB/s);
+// 50021 tokens into 32003 x 1001 fp32 take 43 us (4.3 TB/s: rows of 4004 bytes at any
 // address, so a store covers parts of lines).
 template <typename TD, typename TG, int MODE>
 __global__ __launch_bounds__(kThreads) void k_emb_sum(SumArgs a, FillArgs f) {
@@ -590,7 +590,7 @@ __global__ __launch_bounds__(kThreads) void k_emb_sum(SumArgs a, FillArgs f) {
 // run's pieces: the tail of that chunk, then the heads of the following ones.  A group adds a
 // run of up to kJoinShort pieces by itself; the groups share a longer one, each taking
 // every kJoinWays-th piece in rising order, and add their sums in group order.  Mostly one launch's
-// latency: 7 us where few runs cross, 8 for 50021 tokens.  Four pieces in flight: with eight
+// latency: 5 us where few runs cross, 7 for 50021 tokens.  Four pieces in flight: with eight
 // a batch of which half is one row (65536 into 1000 x 256) takes 71 us instead of 43.
 constexpr int kJoinWays = 8;
 constexpr int kJoinChunks = kJoinWays;
