@@ -122,11 +122,14 @@ class _At(contextlib.ExitStack):
 
     def __init__(self, dev, stream, tensors):
         super().__init__()
+        if stream is not None and not isinstance(stream, int) and stream.device != dev:
+            raise ValueError("the stream is on %s, the call runs on %s" % (stream.device, dev))
         self.enter_context(torch.cuda.device(dev))
         if stream is None:
             return
         if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=dev)
+            # (torch takes a 0 for no handle, and would make a stream of its own)
+            stream = torch.cuda.ExternalStream(stream, device=dev) if stream else torch.cuda.default_stream(dev)
         if stream.cuda_stream != _raw_stream(dev.index):
             # memory of another stream's tensors is not handed out again before this
             # stream is done with them
@@ -175,7 +178,8 @@ class ActCheckpoint:
     """An activation held in 8 bits: `codes` (int8, rows x code pitch), `exps`
     (uint8, rows x exponent pitch) and its number of features `cols`; `shape` is
     the activation's (default: rows x cols).  It stands for codes * 2^(exps -
-    127), one exponent for every 32 features of a token."""
+    127), one exponent for every 32 features of a token.  The two arrays of one made
+    here share an allocation: torch.save takes their clones, or the checkpoint."""
 
     # (one allocation holds both arrays of a checkpoint made here; its views are
     # made when asked for)
@@ -204,6 +208,10 @@ class ActCheckpoint:
             n *= int(d)
         if self.shape[-1] != cols or n != self.rows * cols:
             raise ValueError("shape %s is not %d rows of %d features" % (self.shape, self.rows, cols))
+
+    def __reduce__(self):
+        # (a copy has arrays, and their addresses, of its own)
+        return ActCheckpoint, (self.codes.clone(), self.exps.clone(), self.cols, self.shape)
 
     @staticmethod
     def empty(shape, device) -> "ActCheckpoint":

@@ -838,6 +838,53 @@ def test_two_captured_graphs():
                 assert torch.equal(a, b), r
 
 
+def test_stream_zero_is_the_default_stream():
+    """A raw handle of 0 names the default stream, whatever stream is current."""
+    from muon_newton_schulz_02_amd import grads as G
+    dev = torch.device("cuda", torch.cuda.current_device())
+    x = torch.randn(50, 96, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        with G._At(dev, 0, (x,)):
+            assert torch.cuda.current_stream().cuda_stream == 0
+        c = M.ma_act_pack(x, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(c.codes, M.ma_act_pack(x).codes)
+
+
+def test_stream_of_another_device_is_refused():
+    from types import SimpleNamespace
+    other = SimpleNamespace(device=torch.device("cuda", torch.cuda.current_device() + 1), cuda_stream=0)
+    x = torch.randn(5, 96, device="cuda")
+    with pytest.raises(ValueError, match="stream is on"):
+        M.ma_act_pack(x, stream=other)
+
+
+def test_copies_of_a_checkpoint_hold_arrays_of_their_own():
+    import copy
+    import io
+    x = torch.randn(6, 7, 100, device="cuda", dtype=torch.bfloat16)
+    c = M.ma_act_pack(x)
+    want = M.ma_act_unpack(c)
+    f = io.BytesIO()
+    torch.save((c.codes.clone(), c.exps.clone(), c.cols, c.shape), f)
+    f.seek(0)
+    loaded = M.ActCheckpoint(*torch.load(f, weights_only=True))
+    g = io.BytesIO()
+    torch.save(c, g)
+    g.seek(0)
+    whole = torch.load(g, weights_only=False)
+    deep = copy.deepcopy(c)
+    copies = (deep, loaded, whole, copy.copy(c))
+    for d in copies:
+        assert d._pc == d.codes.data_ptr() != c._pc and d._pe == d.exps.data_ptr() != c._pe
+        assert d.shape == c.shape and d.cols == c.cols and d.rows == c.rows
+    c.codes.zero_()
+    del c
+    for d in copies:
+        assert torch.equal(M.ma_act_unpack(d), want)
+
+
 def test_two_streams_at_once():
     """Two calls of each operator in flight at once, on two streams."""
     ps = [_layer_inputs(30 + k, tokens=4000, vocab=2000) for k in range(2)]
