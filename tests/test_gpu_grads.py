@@ -249,6 +249,39 @@ def test_embedding_grad_of_long_chunks(td, tg, n, v, h, how):
 
 
 @pytest.mark.parametrize("tg", ["fp32", "bf16"])
+@pytest.mark.parametrize("n,v,h,off", [
+    # many more rows than tokens: few tokens, and tables whose zeroing is told the rows of tokens,
+    # at any address; rows of more than 32 KB; three passes of the sort; one row
+    (0, 4001, 33, 1), (3000, 30011, 264, 0), (3000, 30011, 263, 3), (4097, 40009, 264, 0),
+    (4097, 40009, 264, 8), (4100, 40009, 264, 9), (5000, 50021, 251, 5), (4500, 900, 16392, 16),
+    (5000, 1100003, 16, 24), (200000, 1100003, 8, 64), (200000, 2200003, 4, 0), (5000, 1, 16, 8),
+    (4097, 3, 1, 1)])
+def test_embedding_grad_zeroes_the_other_rows(tg, n, v, h, off):
+    """Rows without a token are zero, whatever they held, and what lies before and
+    behind the gradient is left alone."""
+    rng = np.random.default_rng(n + v + h)
+    ids = torch.from_numpy(rng.integers(-1, v, n)).cuda()
+    d = torch.randn(n, h, device="cuda").to(torch.bfloat16)
+    buf = torch.full((off + v * h + 300,), 7.0, dtype=DT[tg], device="cuda")
+    out = buf[off:off + v * h].view(v, h)
+    M.ma_embedding_grad(d, ids, v, out=out)
+    assert torch.all(buf[:off] == 7.0) and torch.all(buf[off + v * h:] == 7.0)
+    hit = torch.zeros(v, dtype=torch.bool, device="cuda")
+    real = ids >= 0
+    hit[ids[real]] = True
+    assert torch.all(out[~hit] == 0)
+    rows = torch.nonzero(hit)[:, 0]
+    want = torch.zeros(len(rows), h, dtype=torch.float64, device="cuda")
+    mag = torch.zeros_like(want)
+    at = torch.searchsorted(rows, ids[real])
+    want.index_add_(0, at, d[real].double())
+    mag.index_add_(0, at, d[real].double().abs())
+    count = torch.bincount(at, minlength=len(rows))[:, None].double()
+    want, tol = want.cpu().numpy(), ((count + 4) * R.F32 * mag).cpu().numpy()
+    _close(out[rows], want, R.rounded(want, tol, tg))
+
+
+@pytest.mark.parametrize("tg", ["fp32", "bf16"])
 @pytest.mark.parametrize("n,v,h,how", [(1, 4, 8, "uniform"), (300, 20, 40, "mixed"),
                                        (3000, 900, 33, "zipf"), (0, 6, 8, "none")])
 def test_embedding_grad_accumulates(tg, n, v, h, how):
