@@ -1028,6 +1028,8 @@ int launch_embedding_grad(const EmbGradArgs& g, const EmbPlan& p, void* stream) 
     const uintptr_t from = std::min(last, (first + 127) & ~(uintptr_t)127), to = std::max(from, last & ~(uintptr_t)15);
     const int64_t row_bytes = g.hidden * (bg ? 2 : 4);
     int64_t shared = 0;           // pieces that launches have taken
+    bool edges = false;           // and whether one has taken the edges (a gradient of a few
+                                  // bytes has no piece; later shares run beside the sums)
     auto share = [&](int64_t bytes, const uint8_t* flags, int threads) {
         FillArgs f{};
         if (g.accumulate) return f;
@@ -1040,7 +1042,8 @@ int launch_embedding_grad(const EmbGradArgs& g, const EmbPlan& p, void* stream) 
         f.magic = flags ? (uint32_t)(((uint64_t(1) << 32) + f.row - 1) / f.row) : 0;
         const int64_t each = (flags ? kFillDepth : 1) * threads;
         f.groups = std::min<int64_t>(ceil_div(f.pieces, each), (int64_t(1) << 31) / threads);
-        if (shared == 0 && !flags) {
+        if (!edges && !flags) {
+            edges = true;
             f.groups = std::max<int64_t>(f.groups, 1);
             f.edge[0] = reinterpret_cast<uint16_t*>(first);
             f.edge_n[0] = (int)((from - first) / 2);

@@ -282,6 +282,30 @@ def test_embedding_grad_zeroes_the_other_rows(tg, n, v, h, off):
 
 
 @pytest.mark.parametrize("tg", ["fp32", "bf16"])
+@pytest.mark.parametrize("n", [1100, 5000])
+@pytest.mark.parametrize("v,h,off", [(3, 1, 0), (1, 3, 0), (2, 1, 5), (7, 4, 4), (30, 1, 1), (5, 3, 33)])
+def test_embedding_grad_of_few_bytes(tg, n, v, h, off):
+    """A gradient inside one 128-byte line, mostly without a whole 16-byte piece, whose rows have
+    one to three tokens in a batch of padding: each row is written by the launch of the sums
+    itself, beside which nothing may zero it."""
+    rng = np.random.default_rng(n + 7 * v + h + off)
+    ids = np.full(n, -1)
+    places = rng.permutation(n)
+    for r in range(v):
+        for k in range(1 + r % 3):
+            ids[places[3 * r + k]] = r
+    d = _dev(rng.standard_normal((n, h)), "fp32")
+    buf = torch.full((off + v * h + 64,), 7.0, dtype=DT[tg], device="cuda")
+    out = buf[off:off + v * h].view(v, h)
+    want, tol = R.embedding_grad(_f64(d), ids, v, 1.5, -1)
+    for tok in (torch.from_numpy(ids).cuda(), torch.from_numpy(ids).cuda().to(torch.int32)):
+        out.fill_(7.0)
+        M.ma_embedding_grad(d, tok, v, scale=1.5, out=out)
+        _close(out, want, R.rounded(want, tol, tg))
+        assert torch.all(buf[:off] == 7.0) and torch.all(buf[off + v * h:] == 7.0)
+
+
+@pytest.mark.parametrize("tg", ["fp32", "bf16"])
 @pytest.mark.parametrize("n,v,h,how", [(1, 4, 8, "uniform"), (300, 20, 40, "mixed"),
                                        (3000, 900, 33, "zipf"), (0, 6, 8, "none")])
 def test_embedding_grad_accumulates(tg, n, v, h, how):
