@@ -368,6 +368,20 @@ class MuonAdamW:
         nbytes = muon_adamw_workspace_size(self.plan, self.hp.ns_precision)
         self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
 
+    def _buffer(self, kept, i, dtype, stream):
+        """kept[i], of entry i's shape: allocated once, on the stream that writes it (a block
+        of the current stream's pool may still be in use there)."""
+        import torch
+        from . import grads as G
+        p = self.params[i]
+        if kept[i] is None:
+            with G._At(p.device, stream, ()):
+                kept[i] = torch.empty(p.shape, dtype=dtype, device=p.device)
+        elif stream is None:
+            # (an earlier step may have had another stream)
+            kept[i].record_stream(torch.cuda.current_stream(p.device))
+        return kept[i]
+
     def _formed(self, i, g, stream):
         """Entry i's gradient from an EmbeddingGrad or LinearGrad, or a list of
         them (micro-batches, added up in float32), in a buffer this object keeps for
@@ -383,20 +397,17 @@ class MuonAdamW:
         p = self.params[i]
         if p.dim() != 2:
             raise ValueError("grad %d: entry %s is not a matrix" % (i, self.names[i]))
-        if self.grad_buffers[i] is None:
-            self.grad_buffers[i] = torch.empty_like(p, memory_format=torch.contiguous_format)
-        out = self.grad_buffers[i]
+        out = self._buffer(self.grad_buffers, i, p.dtype, stream)
         if len(sources) == 1 or out.dtype == torch.float32:
             for k, s in enumerate(sources):
                 G.form_gradient(s, p.shape, out, k > 0, stream)
             return out
         # bf16 storage: one rounding, after the last micro-batch
-        if self.sum_buffers[i] is None:
-            self.sum_buffers[i] = torch.empty(p.shape, dtype=torch.float32, device=p.device)
+        total = self._buffer(self.sum_buffers, i, torch.float32, stream)
         for k, s in enumerate(sources):
-            G.form_gradient(s, p.shape, self.sum_buffers[i], k > 0, stream)
-        with G._At(p.device, stream, (out, self.sum_buffers[i])):
-            out.copy_(self.sum_buffers[i])
+            G.form_gradient(s, p.shape, total, k > 0, stream)
+        with G._At(p.device, stream, (out, total)):
+            out.copy_(total)
         return out
 
     def step(self, grads, stream=None, grad_norm_out=None, muon_update_out=None):

@@ -795,6 +795,31 @@ def test_step_sources_on_another_stream():
         assert torch.equal(a, b)
 
 
+def test_step_buffers_belong_to_the_step_stream():
+    """A step on another stream, right after work of the current stream whose memory has been
+    given back: the gradient buffers are not that memory.  Then a step on the current stream."""
+    p = _layer_inputs(16)
+    ref, want = _optimizer(p)
+    src = _layer(p)
+    for _ in range(2):
+        ref.step(src)
+    opt, params = _optimizer(p)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    # freed blocks of the buffers' sizes in the current stream's pool
+    freed = [torch.empty_like(q) for q in params for _ in range(4)]
+    held = {t.data_ptr() for t in freed}
+    del freed
+    opt.step(src, stream=side)
+    assert not held & {t.data_ptr() for t in opt.grad_buffers}
+    side.synchronize()
+    opt.step(src)
+    torch.cuda.synchronize()
+    for a, b in zip(params, want):
+        assert torch.equal(a, b)
+
+
 # --------------------------------------------------------- graphs, streams --
 
 def test_capture_and_replay():

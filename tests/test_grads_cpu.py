@@ -271,3 +271,38 @@ def test_step_refuses_wrong_sources():
         _holder().step([M.LinearGrad(None, None), None])
     frozen = _holder(groups=[M.MA_GROUP_NONE])
     assert frozen._formed(0, M.LinearGrad(None, None), None) is None
+
+
+@pytest.mark.parametrize("dtype,buffers", [(torch.float32, 1), (torch.bfloat16, 2)])
+def test_step_allocates_on_the_stream_that_writes(dtype, buffers, monkeypatch):
+    """The buffers that gradients are formed into come from the pool of the step's stream:
+    each allocation is made while that stream is current."""
+    from muon_newton_schulz_02_amd import grads as G
+    now, made = [], []
+
+    class At:
+        def __init__(self, dev, stream, tensors):
+            self.stream = stream
+
+        def __enter__(self):
+            now.append(self.stream)
+
+        def __exit__(self, *exc):
+            now.pop()
+
+    def noted(make):
+        def f(*a, **k):
+            made.append(now[-1] if now else None)
+            return make(*a, **k)
+        return f
+
+    monkeypatch.setattr(G, "_At", At)
+    monkeypatch.setattr(G, "form_gradient", lambda *a, **k: None)
+    for name in ("empty", "empty_like"):
+        monkeypatch.setattr(torch, name, noted(getattr(torch, name)))
+    opt = _holder(params=[torch.zeros(4, 4, dtype=dtype)])
+    src = M.LinearGrad(None, None)
+    out = opt._formed(0, [src, src], "side")
+    assert out is opt.grad_buffers[0] and out.shape == (4, 4) and out.dtype == dtype
+    assert made == ["side"] * buffers
+    assert opt._formed(0, [src, src], "other") is out and len(made) == buffers     # kept
