@@ -16,6 +16,7 @@ in `grads` and under their names here.
 from __future__ import annotations
 
 import ctypes as C
+import importlib.util
 from typing import Dict, List, Optional, Sequence, Tuple
 
 from . import _abi
@@ -32,10 +33,6 @@ __all__ = [
     "muon_adamw_step", "muon_adamw_step_profiled", "muon_adamw_step_noalloc",
     "muon_adamw_plan_free", "muon_adamw_last_error",
     "muon_adamw_version", "MuonAdamW", "load_library",
-    "ActCheckpoint", "EmbeddingGrad", "LinearGrad",
-    "ma_act_pack", "ma_act_unpack", "ma_embedding_lookup", "ma_embedding_grad",
-    "ma_embedding_grad_workspace_size", "ma_linear_grad", "ma_linear_grad_workspace_size",
-    "ma_glu_forward", "ma_glu_backward",
 ]
 
 # The gradient operators need torch at import (the optimizer step only when it
@@ -43,6 +40,20 @@ __all__ = [
 _GRADS = ("ActCheckpoint", "EmbeddingGrad", "LinearGrad", "ma_act_pack", "ma_act_unpack",
           "ma_embedding_lookup", "ma_embedding_grad", "ma_embedding_grad_workspace_size",
           "ma_linear_grad", "ma_linear_grad_workspace_size", "ma_glu_forward", "ma_glu_backward")
+
+
+def _torch_installed() -> bool:
+    try:
+        return importlib.util.find_spec("torch") is not None
+    except ImportError:
+        return False
+    except ValueError:          # (a module without a spec stands in for it)
+        return True
+
+
+# (a star import of the optimizer step alone works without torch)
+if _torch_installed():
+    __all__ += _GRADS
 
 
 def __getattr__(name):

@@ -306,3 +306,19 @@ def test_step_allocates_on_the_stream_that_writes(dtype, buffers, monkeypatch):
     assert out is opt.grad_buffers[0] and out.shape == (4, 4) and out.dtype == dtype
     assert made == ["side"] * buffers
     assert opt._formed(0, [src, src], "other") is out and len(made) == buffers     # kept
+
+
+@pytest.mark.parametrize("torch_there", [False, True])
+def test_star_import_with_and_without_torch(torch_there):
+    """The optimizer step's names need no torch to be imported; the gradient operators' join
+    them where torch is installed."""
+    import subprocess
+    import sys
+    code = ("import sys\n"
+            + ("" if torch_there else "sys.modules['torch'] = None\n") +
+            "sys.path.insert(0, %r)\n"
+            "from muon_newton_schulz_02_amd import *\n"
+            "print(muon_adamw_version(), MuonAdamW.__name__, 'ma_act_pack' in globals())\n" % ROOT)
+    res = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert res.returncode == 0, res.stderr[-2000:]
+    assert res.stdout.split()[-2:] == ["MuonAdamW", str(torch_there)]
