@@ -118,6 +118,13 @@ int ma_embedding_grad(const void* dout, int32_t dout_dtype, int64_t dout_stride,
 int ma_linear_grad_workspace_size(int64_t n_tokens, int64_t n_out, int64_t n_in,
                                   int32_t dy_dtype, size_t* bytes);
 
+/* The same for a dy at this address (its alignment counts; nothing is read) and of this
+ * stride: never more, and without the copy of dy where its rows are aligned.  Errors:
+ * INVALID_ARG, SHAPE. */
+int ma_linear_grad_workspace_size_at(const void* dy, int32_t dy_dtype, int64_t n_tokens,
+                                     int64_t n_out, int64_t dy_stride, int64_t n_in,
+                                     size_t* bytes);
+
 /* grad[n][k] = sum over t of dy[t][n] * x[t][k] (with accumulate = 1, added
  * to grad): the gradient of y = x W^T in the contiguous n_out x n_in W, from dy
  * (n_tokens x n_out) and x (n_tokens x n_in) held in 8 bits.  No factor is

@@ -109,6 +109,8 @@ GRAD_SIGNATURES = [
     ("ma_embedding_grad", C.c_int, [_P, _I32, _I64, _P, _I32, _I64, _I64, _I64, _F64, _I64, _P,
                                     _I32, _I32, _P, _SZ, _P]),
     ("ma_linear_grad_workspace_size", C.c_int, [_I64, _I64, _I64, _I32, C.POINTER(_SZ)]),
+    ("ma_linear_grad_workspace_size_at", C.c_int, [_P, _I32, _I64, _I64, _I64, _I64,
+                                                   C.POINTER(_SZ)]),
     ("ma_linear_grad", C.c_int, [_P, _I32, _I64, _I64, _I64, _P, _P, _I64, _P, _I32, _I32, _P,
                                  _SZ, _P]),
     ("ma_glu_forward", C.c_int, [_P, _P, _I32, _I64, _I64, _I64, _I64, _I32, _P, _I64, _P, _P, _P,

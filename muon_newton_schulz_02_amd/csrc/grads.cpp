@@ -329,6 +329,22 @@ int ma_linear_grad_workspace_size(int64_t n_tokens, int64_t n_out, int64_t n_in,
     return MA_OK;
 }
 
+int ma_linear_grad_workspace_size_at(const void* dy, int32_t dy_dtype, int64_t n_tokens,
+                                     int64_t n_out, int64_t dy_stride, int64_t n_in,
+                                     size_t* bytes) {
+    const char* fn = "ma_linear_grad_workspace_size_at";
+    if (!bytes) {
+        set_error("%s: NULL argument", fn);
+        return MA_ERR_INVALID_ARG;
+    }
+    TRY(check_lg_shape(fn, n_tokens, n_out, n_in, dy_dtype));
+    TRY(check_stride(fn, "dy", dy_stride, 0, n_tokens));
+    *bytes = linear_grad_plan(n_tokens, n_out, n_in, dy_dtype,
+                              linear_grad_big_rows(dy, n_out, dy_stride)).total;
+    clear_error();
+    return MA_OK;
+}
+
 int ma_linear_grad(const void* dy, int32_t dy_dtype, int64_t n_tokens, int64_t n_out,
                    int64_t dy_stride, const int8_t* codes, const uint8_t* exps, int64_t n_in,
                    void* grad, int32_t grad_dtype, int32_t accumulate, void* workspace,

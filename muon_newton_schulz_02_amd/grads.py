@@ -398,6 +398,8 @@ def ma_embedding_grad(dout, tokens, vocab: int, scale: float = 1.0, padding_toke
 
 def ma_linear_grad_workspace_size(n_tokens: int, n_out: int, n_in: int,
                                   dy_dtype=torch.bfloat16) -> int:
+    """Bytes that serve any dy of this shape, whatever its address and stride (a call without
+    a workspace allocates what its own dy needs, which may be much less)."""
     n = C.c_size_t()
     rc = _abi.load().ma_linear_grad_workspace_size(n_tokens, n_out, n_in, _DTYPES[dy_dtype],
                                                    C.byref(n))
@@ -426,7 +428,8 @@ def ma_linear_grad(dy, x: ActCheckpoint, out=None, accumulate: bool = False,
             return ma_linear_grad(dy, x, out, accumulate, grad_dtype, workspace)
     lib = _abi.load()
     size = C.c_size_t()
-    rc = lib.ma_linear_grad_workspace_size(rows, n_out, x.cols, dt, C.byref(size))
+    rc = lib.ma_linear_grad_workspace_size_at(dy.data_ptr(), dt, rows, n_out, ld, x.cols,
+                                              C.byref(size))
     if rc:
         _fail(rc, "ma_linear_grad")
     out = _out_like(out, "out", (n_out, x.cols), grad_dtype, dev)

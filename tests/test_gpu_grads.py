@@ -500,6 +500,24 @@ def test_linear_grad_large_float32_values(m, n, k):
     assert torch.isfinite(got[rest]).all()
 
 
+@pytest.mark.parametrize("pad,copies", [(0, False), (1, True)])
+def test_linear_grad_allocates_what_its_dy_needs(pad, copies):
+    """Without a workspace of the caller's, a call allocates the gradient, x as bf16 and partial
+    sums, and a copy of dy only where its rows are not aligned."""
+    m, n, k = 16384, 4096, 1024
+    dy, _ = _strided(np.zeros((m, n)), pad, "bf16")
+    c = M.ma_act_pack(torch.ones((m, k), dtype=torch.bfloat16, device="cuda"))
+    M.ma_linear_grad(dy, c)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    base = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    M.ma_linear_grad(dy, c)
+    used = torch.cuda.max_memory_allocated() - base
+    # (the few slices' partial sums, of the gradient's size each, are less than a copy of dy)
+    assert (used >= 2 * m * k + 4 * n * k + 2 * m * n) == copies, used
+
+
 @pytest.mark.parametrize("m", [1024, 1055])
 def test_linear_grad_large_product_values(m):
     """The large-product kernel, value by value: one token of dy is one, so the

@@ -322,3 +322,35 @@ def test_star_import_with_and_without_torch(torch_there):
     res = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
     assert res.returncode == 0, res.stderr[-2000:]
     assert res.stdout.split()[-2:] == ["MuonAdamW", str(torch_there)]
+
+
+@pytest.mark.parametrize("m,n,k", [(0, 8, 8), (5, 24, 40), (16001, 256, 1024), (32768, 8192, 2048),
+                                   (3000, 3001, 2048), (8192, 1024, 4096), (4096, 1024, 1024)])
+@pytest.mark.parametrize("dt", [0, 1])
+def test_linear_grad_workspace_of_one_dy(lib, m, n, k, dt):
+    """What a call needs for its own dy: its size is taken and one byte less is refused; never
+    more than the size for any dy, and no copy of a bf16 dy with aligned rows."""
+    worst, size = C.c_size_t(), C.c_size_t()
+    assert lib.ma_linear_grad_workspace_size(m, n, k, dt, C.byref(worst)) == M.MA_OK
+    es = 2 if dt else 4
+    for addr in (at(0), at(0) + es, at(0) + 16):
+        for stride in (n, n + 1, n + 8, 0):
+            assert lib.ma_linear_grad_workspace_size_at(addr, dt, m, n, stride, k,
+                                                        C.byref(size)) == M.MA_OK
+            assert size.value <= worst.value
+
+            def call(bytes_):       # (no gradient: refused after the workspace is looked at)
+                return lib.ma_linear_grad(addr, dt, m, n, stride, at(1), at(2), k, None, 0, 0, at(3),
+                                          bytes_, None)
+            assert call(size.value) == M.MA_ERR_INVALID_ARG and "grad is NULL" in _err()
+            if size.value:
+                assert call(size.value - 1) == M.MA_ERR_WORKSPACE
+            if dt and n % 8 == 0 and m >= 512 and addr % 16 == 0 and stride >= n and stride % 8 == 0:
+                # x as bf16 in whole tiles, and at most 64 slices of partial sums that together
+                # fill 8 workgroups of 128 x 128 outputs per CU
+                x = -(-m // 32) * 32 * (-(-k // 256) * 256) * 2
+                assert size.value <= x + (2 * 8 * 256 * 128 * 128 + 256) * 4
+    assert lib.ma_linear_grad_workspace_size_at(None, dt, m, n, n, k, None) == M.MA_ERR_INVALID_ARG
+    assert lib.ma_linear_grad_workspace_size_at(None, 7, m, n, n, k, C.byref(size)) == M.MA_ERR_INVALID_ARG
+    assert lib.ma_linear_grad_workspace_size_at(None, dt, m, n, -1, k, C.byref(size)) == M.MA_ERR_INVALID_ARG
+    assert lib.ma_linear_grad_workspace_size_at(None, dt, -1, n, n, k, C.byref(size)) == M.MA_ERR_SHAPE
