@@ -124,9 +124,15 @@ class _At(contextlib.ExitStack):
         super().__init__()
         if stream is not None and not isinstance(stream, int) and stream.device != dev:
             raise ValueError("the stream is on %s, the call runs on %s" % (stream.device, dev))
-        self.enter_context(torch.cuda.device(dev))
-        if stream is None:
-            return
+        try:
+            self.enter_context(torch.cuda.device(dev))
+            if stream is not None:
+                self._take(dev, stream, tensors)
+        except BaseException:
+            self.close()
+            raise
+
+    def _take(self, dev, stream, tensors):
         if isinstance(stream, int):
             # (torch takes a 0 for no handle, and would make a stream of its own)
             stream = torch.cuda.ExternalStream(stream, device=dev) if stream else torch.cuda.default_stream(dev)
@@ -158,6 +164,15 @@ def _out_as(out, what: str, x):
     return _out_like(out, what, x.shape, x.dtype, x.device)
 
 
+def _check_workspace(workspace, dev):
+    if workspace is None:
+        return
+    _check_cuda(workspace, "workspace")
+    _same_device(dev, ("workspace", workspace))
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+
+
 def _workspace(workspace, need: int, dev):
     """(tensor, address, bytes) of a call's workspace."""
     if workspace is None:
@@ -165,10 +180,6 @@ def _workspace(workspace, need: int, dev):
             return None, None, 0
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
         return workspace, workspace.data_ptr(), need
-    _check_cuda(workspace, "workspace")
-    _same_device(dev, ("workspace", workspace))
-    if not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -374,6 +385,7 @@ def ma_embedding_grad(dout, tokens, vocab: int, scale: float = 1.0, padding_toke
         raise ValueError("accumulate needs the gradient to add to (out)")
     dev = dout.device
     _same_device(dev, ("tokens", tokens), ("out", out))
+    _check_workspace(workspace, dev)
     if _elsewhere(dev, stream):
         with _At(dev, stream, (dout, tokens, out, workspace)):
             return ma_embedding_grad(dout, tokens, vocab, scale, padding_token, out, accumulate,
@@ -423,6 +435,7 @@ def ma_linear_grad(dy, x: ActCheckpoint, out=None, accumulate: bool = False,
     if accumulate and out is None:
         raise ValueError("accumulate needs the gradient to add to (out)")
     _same_device(dev, ("out", out))
+    _check_workspace(workspace, dev)
     if _elsewhere(dev, stream):
         with _At(dev, stream, (dy, *x._tensors(), out, workspace)):
             return ma_linear_grad(dy, x, out, accumulate, grad_dtype, workspace)

@@ -960,6 +960,20 @@ def test_stream_of_another_device_is_refused():
         M.ma_act_pack(x, stream=other)
 
 
+def test_workspace_is_checked_before_the_stream_is_taken():
+    dy = torch.randn(40, 24, device="cuda")
+    c = M.ma_act_pack(torch.randn(40, 32, device="cuda"))
+    ids = torch.zeros(40, dtype=torch.int64, device="cuda")
+    side = torch.cuda.Stream()
+    for ws, error in ((torch.empty(1 << 20, dtype=torch.uint8), ValueError), ([0], TypeError),
+                      (torch.empty(4, 4, device="cuda").t(), ValueError)):
+        for stream in (None, side):
+            with pytest.raises(error, match="workspace"):
+                M.ma_linear_grad(dy, c, workspace=ws, stream=stream)
+            with pytest.raises(error, match="workspace"):
+                M.ma_embedding_grad(dy, ids, 9, workspace=ws, stream=stream)
+
+
 def test_copies_of_a_checkpoint_hold_arrays_of_their_own():
     import copy
     import io

@@ -354,3 +354,33 @@ def test_linear_grad_workspace_of_one_dy(lib, m, n, k, dt):
     assert lib.ma_linear_grad_workspace_size_at(None, 7, m, n, n, k, C.byref(size)) == M.MA_ERR_INVALID_ARG
     assert lib.ma_linear_grad_workspace_size_at(None, dt, m, n, -1, k, C.byref(size)) == M.MA_ERR_INVALID_ARG
     assert lib.ma_linear_grad_workspace_size_at(None, dt, -1, n, n, k, C.byref(size)) == M.MA_ERR_SHAPE
+
+
+@pytest.mark.parametrize("where", ["record", "stream"])
+def test_a_failed_switch_of_device_and_stream_is_undone(where, monkeypatch):
+    """A call for another device that fails while it takes the device and the stream leaves the
+    current ones as they were."""
+    import contextlib
+    from types import SimpleNamespace
+    from muon_newton_schulz_02_amd import grads as G
+    current = ["first"]
+
+    @contextlib.contextmanager
+    def device(dev):
+        was, current[0] = current[0], dev
+        try:
+            yield
+        finally:
+            current[0] = was
+
+    def fails(*a):
+        raise RuntimeError("no")
+
+    dev = SimpleNamespace(index=1)
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch.cuda, "stream", fails)
+    monkeypatch.setattr(G, "_raw_stream", lambda index: 0)
+    t = SimpleNamespace(record_stream=fails if where == "record" else lambda s: None)
+    with pytest.raises(RuntimeError, match="no"):
+        G._At(dev, SimpleNamespace(device=dev, cuda_stream=5), (t, None))
+    assert current == ["first"]
