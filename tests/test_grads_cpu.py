@@ -360,18 +360,19 @@ def test_linear_grad_workspace_of_one_dy(lib, m, n, k, dt):
 def test_a_failed_switch_of_device_and_stream_is_undone(where, monkeypatch):
     """A call for another device that fails while it takes the device and the stream leaves the
     current ones as they were."""
-    import contextlib
     from types import SimpleNamespace
     from muon_newton_schulz_02_amd import grads as G
     current = ["first"]
 
-    @contextlib.contextmanager
-    def device(dev):
-        was, current[0] = current[0], dev
-        try:
-            yield
-        finally:
-            current[0] = was
+    class device:
+        def __init__(self, dev):
+            self.dev = dev
+
+        def __enter__(self):
+            self.was, current[0] = current[0], self.dev
+
+        def __exit__(self, *exc):
+            current[0] = self.was
 
     def fails(*a):
         raise RuntimeError("no")
