@@ -194,7 +194,7 @@ class ActCheckpoint:
 
     # (one allocation holds both arrays of a checkpoint made here; its views are
     # made when asked for)
-    __slots__ = ("cols", "rows", "shape", "device", "_buf", "_codes", "_exps", "_pc", "_pe")
+    __slots__ = ("cols", "rows", "shape", "device", "_buf", "_codes", "_exps", "_pc", "_pe", "_n")
 
     def __init__(self, codes, exps, cols: int, shape=None):
         cols = int(cols)
@@ -211,7 +211,7 @@ class ActCheckpoint:
         if codes.device != exps.device:
             raise ValueError("codes are on %s, exps on %s" % (codes.device, exps.device))
         self._codes, self._exps, self._buf = codes, exps, None
-        self._pc, self._pe = codes.data_ptr(), exps.data_ptr()
+        self._pc, self._pe, self._n = codes.data_ptr(), exps.data_ptr(), codes.numel()
         self.cols, self.rows, self.device = cols, codes.shape[0], codes.device
         self.shape = (self.rows, cols) if shape is None else tuple(shape)
         n = 1
@@ -263,6 +263,22 @@ class ActCheckpoint:
             self._exps = self._buf[after:].view(self.rows, -(-pitch // (4 * MA_ACT_GROUP)) * 4)
         return self._exps
 
+    def _place(self):
+        """Look at the arrays again where their owner has given them other memory since (a
+        .data, or a storage that was resized)."""
+        c, e, pc = self._codes, self._exps, self._pc
+        if self._buf is None:
+            if c.data_ptr() == pc and e.data_ptr() == self._pe and \
+                    c.numel() == self._n and e.shape[0] == self.rows:
+                return
+        elif self._buf.data_ptr() == pc and (c is None or c.data_ptr() == pc) and \
+                (e is None or e.data_ptr() == self._pe):
+            return
+        for t in self._tensors():
+            if t.numel() and t.untyped_storage().nbytes() < t.storage_offset() + t.numel():
+                raise ValueError("the memory of this ActCheckpoint was freed")
+        self.__init__(self.codes, self.exps, self.cols, self.shape)
+
     def _tensors(self):
         return (self._buf,) if self._buf is not None else (self._codes, self._exps)
 
@@ -270,6 +286,7 @@ class ActCheckpoint:
 def _held(c, what: str, dev, rows=None, cols=None):
     if not isinstance(c, ActCheckpoint):
         raise TypeError("%s must be an ActCheckpoint" % what)
+    c._place()
     if rows is not None and (c.rows != rows or c.cols != cols):
         raise ValueError("%s holds %d x %d, the call needs %d x %d" % (what, c.rows, c.cols, rows,
                                                                       cols))

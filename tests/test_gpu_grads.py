@@ -999,6 +999,32 @@ def test_copies_of_a_checkpoint_hold_arrays_of_their_own():
         assert torch.equal(M.ma_act_unpack(d), want)
 
 
+def test_checkpoint_whose_arrays_move():
+    """Arrays given other memory since are read there; on the CPU, or freed, they are refused."""
+    x = torch.randn(6, 100, device="cuda")
+    c = M.ma_act_pack(x)
+    own = M.ActCheckpoint(c.codes.clone(), c.exps.clone(), 100)
+    twice = (2 * M.ma_act_unpack(c)).clone()
+    for d in (c, own):
+        d.exps.data = d.exps + (d.exps > 0).to(torch.uint8)      # (groups of the padding are 0)
+        d.codes.data = d.codes.clone()
+        assert torch.equal(M.ma_act_unpack(d), twice)
+        g = M.ma_linear_grad(torch.eye(6, device="cuda"), d)
+        assert torch.equal(g, twice)
+        d.codes.data = d.codes.cpu()
+        with pytest.raises(ValueError, match="codes are on cpu"):
+            M.ma_act_unpack(d)
+        d.exps.data = d.exps.cpu()
+        with pytest.raises(ValueError, match="GPU"):
+            M.ma_linear_grad(torch.eye(6, device="cuda"), d)
+    one = M.ma_act_pack(x)
+    for freed in (one, M.ActCheckpoint(torch.zeros_like(one.codes), torch.zeros(9, 4, dtype=torch.uint8,
+                                                                                device="cuda")[3:], 100)):
+        freed.exps.untyped_storage().resize_(0)
+        with pytest.raises(ValueError, match="freed"):
+            M.ma_act_unpack(freed)
+
+
 def test_two_streams_at_once():
     """Two calls of each operator in flight at once, on two streams."""
     ps = [_layer_inputs(30 + k, tokens=4000, vocab=2000) for k in range(2)]

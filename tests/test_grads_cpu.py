@@ -385,3 +385,40 @@ def test_a_failed_switch_of_device_and_stream_is_undone(where, monkeypatch):
     with pytest.raises(RuntimeError, match="no"):
         G._At(dev, SimpleNamespace(device=dev, cuda_stream=5), (t, None))
     assert current == ["first"]
+
+
+def test_checkpoint_follows_its_arrays():
+    """Arrays that their owner has given other memory since are looked at again by the next
+    call: nothing reads where they once were."""
+    def used(c):
+        with pytest.raises(ValueError, match="GPU"):      # (the layout has been looked at)
+            M.ma_act_unpack(c)
+        assert (c._pc, c._pe) == (c.codes.data_ptr(), c.exps.data_ptr())
+
+    codes, exps = torch.zeros(4, 64, dtype=torch.int8), torch.zeros(4, 4, dtype=torch.uint8)
+    c = M.ActCheckpoint(codes, exps, 40, (2, 2, 40))
+    used(c)
+    kept = codes.data, exps.data
+    codes.data = codes.clone()
+    used(c)
+    exps.data = exps.clone()
+    used(c)
+    assert c._pc != kept[0].data_ptr() and c._pe != kept[1].data_ptr()
+    for bad in (torch.zeros(4, 32), torch.zeros(3, 64), torch.zeros(64, 4).t()):
+        codes.data = bad.to(torch.int8)
+        with pytest.raises(ValueError):
+            M.ma_act_unpack(c)
+    # arrays that lie in one allocation
+    c = M.ActCheckpoint.empty((4, 40), "cpu")
+    used(c)
+    c.codes.data = c.codes.clone()
+    used(c)
+    c = M.ActCheckpoint.empty((4, 40), "cpu")
+    c.exps.data = torch.zeros(4, 8, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="do not hold"):
+        M.ma_act_unpack(c)
+    for c in (M.ActCheckpoint.empty((4, 40), "cpu"),
+              M.ActCheckpoint(torch.zeros(4, 64, dtype=torch.int8), torch.zeros(7, 4, dtype=torch.uint8)[3:], 40)):
+        c.exps.untyped_storage().resize_(0)
+        with pytest.raises(ValueError, match="freed"):
+            M.ma_act_unpack(c)
