@@ -8,8 +8,9 @@
 // while it is staged: a held value is exact in bf16.  Products of two bf16
 // values are exact in the matrix cores' float32, so a bf16 dY enters with
 // nothing rounded; a float32 dY is cut into three bf16 parts of 8 bits
-// each, which add up to it, and enters as three products, side by side on the small tiles,
-// part after part on the large ones.  Sums are float32.
+// each, which add up to it (but for bits below 2^-133, which no bf16 has), and enters as
+// three products, side by side on the small tiles, part after part on the large ones.
+// Sums are float32.
 //
 // LDS layout of a stage operand of W columns: token row t at t * 2 W bytes,
 // its 16-byte chunk c (8 columns) at slot c ^ ((t & 3) << 2), so the four
@@ -74,8 +75,9 @@ __device__ __forceinline__ void held16(u32x4 codes, float scale, u32x4& lo, u32x
 }
 
 // The three bf16 parts of a float, as the high halves of words: x = h + m + l
-// exactly (each takes the next 8 bits of the significand, cut, so none can
-// overflow).  An infinity or NaN is all in the first part.
+// (each takes the next 8 bits of the significand, cut, so none can overflow), exactly
+// from |x| = 2^-110 up; below that the bits under 2^-133, bf16's smallest step, are cut
+// off: by less than 2^-133, towards zero.  An infinity or NaN is all in the first part.
 __device__ __forceinline__ void split3(float x, uint32_t& h, uint32_t& m, uint32_t& l) {
     const uint32_t b = __float_as_uint(x);
     const bool finite = (b & 0x7f800000u) != 0x7f800000u;

@@ -518,6 +518,28 @@ def test_linear_grad_allocates_what_its_dy_needs(pad, copies):
     assert (used >= 2 * m * k + 4 * n * k + 2 * m * n) == copies, used
 
 
+@pytest.mark.parametrize("m,n,k", [(64, 96, 64), (2050, 700, 300)])
+def test_linear_grad_float32_small_values(m, n, k):
+    """Float32 values down to the smallest denormal, on the small tiles and in parts: x is all
+    ones and one token of each output's dy is not zero.  A value of at least 2^-110 has no bit
+    under 2^-133, the smallest bf16, and comes out whole; a smaller one has those bits
+    cut off, so it is off by less than 2^-133."""
+    assert _taken_in_parts(m, n, k) == (m > 64)
+    rng = np.random.default_rng(9)
+    v = np.ldexp(1.0 + rng.random(n), rng.integers(-140, -100, n)) * rng.choice([-1.0, 1.0], n)
+    v[:8] = np.ldexp([1.0, 2 - 2.0 ** -23, 1 + 2.0 ** -23, 2 - 2.0 ** -23, 1 + 2.0 ** -23, 1.0, 1.0, 1.0],
+                     [-110, -110, -110, -111, -126, -126, -133, -149])
+    v = v.astype(np.float32)
+    dy = np.zeros((m, n), np.float32)
+    dy[rng.integers(0, m, n), np.arange(n)] = v
+    got = _f64(M.ma_linear_grad(torch.from_numpy(dy).cuda(), M.ma_act_pack(torch.ones(m, k, device="cuda"))))
+    want = np.repeat(v.astype(np.float64)[:, None], k, 1)
+    whole = np.abs(v) >= 2.0 ** -110
+    assert np.array_equal(got[whole], want[whole])
+    assert np.all(np.abs(got - want) < 2.0 ** -133)
+    assert whole.sum() > 10 and (~whole).sum() > 10
+
+
 @pytest.mark.parametrize("m", [1024, 1055])
 def test_linear_grad_large_product_values(m):
     """The large-product kernel, value by value: one token of dy is one, so the
