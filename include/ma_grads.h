@@ -130,7 +130,9 @@ int ma_linear_grad_workspace_size_at(const void* dy, int32_t dy_dtype, int64_t n
  * (n_tokens x n_out) and x (n_tokens x n_in) held in 8 bits.  No factor is
  * rounded: a bfloat16 dy and x as held enter the matrix cores as they are, a
  * float32 dy as three bfloat16 parts that add up to it (below 2^-110 in magnitude less
- * its bits under 2^-133); sums are float32.
+ * its bits under 2^-133); sums are float32, in an order that follows from the sizes,
+ * dy's type and, for a bfloat16 dy, its alignment and stride (the same values elsewhere
+ * may give other last bits).
  * n_tokens may be 0 (the sum is then zero).  Errors: INVALID_ARG, SHAPE,
  * WORKSPACE, HIP. */
 int ma_linear_grad(const void* dy, int32_t dy_dtype, int64_t n_tokens, int64_t n_out,

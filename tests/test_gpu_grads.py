@@ -616,6 +616,36 @@ def test_linear_grad_broadcast_and_batch(td):
     assert torch.equal(M.ma_linear_grad(dy, c3), M.ma_linear_grad(dy.view(150, 72), c))
 
 
+def test_linear_grad_order_of_a_dy_elsewhere():
+    """A dy whose rows are not 16-byte aligned may be cut into other slices: its gradient is as
+    near to the exact one, not bitwise that of the same values in aligned rows; each is bitwise
+    equal on every run."""
+    import ctypes as C
+    from muon_newton_schulz_02_amd import _abi
+    m, n, k = 16001, 256, 1024
+    rng = np.random.default_rng(10)
+    c = M.ma_act_pack(_dev(_activation(rng, m, k), "bf16"))
+    x = M.ma_act_unpack(c).double()
+    flat = torch.empty(m * n + 8, dtype=torch.bfloat16, device="cuda")
+    values = _dev(rng.standard_normal((m, n)), "bf16")
+    sizes = set()
+    for off, pad in ((0, 0), (1, 0), (0, 3)):
+        dy = flat[off:off + m * n].view(m, n) if not pad else _strided(np.zeros((m, n)), pad, "bf16")[0]
+        dy.copy_(values)
+        size = C.c_size_t()
+        assert _abi.load().ma_linear_grad_workspace_size_at(dy.data_ptr(), 1, m, n, n + pad, k,
+                                                            C.byref(size)) == 0
+        sizes.add(size.value)
+        got = M.ma_linear_grad(dy, c)
+        want = (values.double().t().contiguous() @ x).cpu().numpy()
+        mag = (values.double().abs().t().contiguous() @ x.abs()).cpu().numpy()
+        tol = (4 * m + 4) * 2 * R.F32 * mag          # as in the reference module
+        _close(got, want, R.rounded(want, tol, "fp32"))
+        for _ in range(2):
+            assert torch.equal(got, M.ma_linear_grad(dy, c))
+    assert len(sizes) == 2          # (two plans)
+
+
 # ---------------------------------------------------------- gated activation --
 
 @pytest.mark.parametrize("kind", ["fp32", "bf16"])
