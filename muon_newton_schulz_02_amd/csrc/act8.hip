@@ -9,9 +9,9 @@
 //
 // Large ones are bound by HBM.  Measured on 32768 x 8192 bf16: packing 128 us (0.82 GB,
 // 6.3 TB/s), unpacking 131 us (6.2); on 32768 x 8192 gated pairs (silu), holding both
-// inputs: forward 378 us (2.17 GB, 5.7 TB/s), backward 405 to 430 us (2.17 GB, 5.0 to 5.4
-// TB/s; a copy of 1 GB runs at 5.15).  On a few dozen rows each is one launch of 2.5
-// to 3.7 us.  Between them the vector instructions count: the codes' fused
+// inputs: forward 346 to 380 us (2.17 GB, 5.7 to 6.3 TB/s), backward 343 to 415 us (2.17
+// GB, 5.2 to 6.4 TB/s; a copy of 1 GB runs at 5.15).  On a few dozen rows each is one
+// launch of 2.2 to 3.7 us.  Between them the vector instructions count: the codes' fused
 // division and rounding, exponent bytes by permutation instead of a lane exchange through
 // LDS and one division per thread left 73 instructions per 8 features
 // packed of 183 (16384 x 4096: 41 -> 37 us).
@@ -137,7 +137,7 @@ __global__ __launch_bounds__(kThreads) void k_act_unpack(const int8_t* __restric
 // ------------------------------------------------------ gated activation --
 // h = act(g) u, with g and u held in the same pass; and dg = dh u act'(g), du = dh act(g)
 // from the held forms: 3 values read or written per feature each way beside the
-// codes, so the two passes of a backbone's 32768 x 8192 pairs move 4.3 GB in 0.8 ms.
+// codes, so the two passes of a backbone's 32768 x 8192 pairs move 4.3 GB in 0.70 to 0.76 ms.
 // 1 / (1 + 2^(-x log2 e)): saturates to 0 and 1, NaN stays NaN.
 __device__ __forceinline__ float sigmoid(float x) {
     return __builtin_amdgcn_rcpf(1.f + __expf(-x));

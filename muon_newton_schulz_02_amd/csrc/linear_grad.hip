@@ -13,8 +13,10 @@
 // Sums are float32.
 //
 // LDS layout of a stage operand of W columns: token row t at t * 2 W bytes,
-// its 16-byte chunk c (8 columns) at slot c ^ ((t & 3) << 2), so the four
-// rows of 64 bytes that half a wave reads together fall in distinct banks.
+// its 16-byte chunk c (8 columns) at slot c ^ ((t & 3) << 2), so that the four
+// rows of 64 bytes that half a wave reads together lie in distinct banks.  Counted per LDS
+// access: no conflict cycle in the kernel of the large products, 0.34 in the other, which
+// also writes its stages there.
 
 #include <hip/hip_runtime.h>
 
@@ -441,7 +443,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_linear_grad(LgArgs a, int tiles
 // buffer's extent, and arrive as zeros.
 //
 // 32768 tokens x 8192 outputs x 2048 inputs: k_lg_expand 35 us (84 MB read, 134 written: 6.3 TB/s), the products
-// 792 to 850 us: 1.29 to 1.39 PFLOP/s, against 1.39 of the library's bf16 product of three
+// 792 to 880 us: 1.25 to 1.39 PFLOP/s, against 1.39 of the library's bf16 product of three
 // 8192 x 8192 matrices and 920 to 935 us for the library's product of this shape from a
 // bf16 X.  Bound by the matrix cores and the clock they leave.
 // ---------------------------------------------------------------------------
