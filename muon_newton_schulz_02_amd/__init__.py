@@ -385,12 +385,15 @@ class MuonAdamW:
         import torch
         from . import grads as G
         p = self.params[i]
+        raw = (G._raw_stream(p.device.index) if stream is None else
+               stream if isinstance(stream, int) else stream.cuda_stream)
         if kept[i] is None:
             with G._At(p.device, stream, ()):
                 kept[i] = torch.empty(p.shape, dtype=dtype, device=p.device)
-        elif stream is None:
-            # (an earlier step may have had another stream)
-            kept[i].record_stream(torch.cuda.current_stream(p.device))
+            kept[i].home_stream = raw
+        elif getattr(kept[i], "home_stream", None) != raw:      # (or a tensor of the caller's)
+            with G._At(p.device, stream, ()):
+                kept[i].record_stream(torch.cuda.current_stream(p.device))
         return kept[i]
 
     def _formed(self, i, g, stream):

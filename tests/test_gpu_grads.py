@@ -888,6 +888,16 @@ def test_step_buffers_belong_to_the_step_stream():
     torch.cuda.synchronize()
     for a, b in zip(params, want):
         assert torch.equal(a, b)
+    # a third stream, current and given; and a buffer of the caller's
+    third = torch.cuda.Stream()
+    opt.grad_buffers[1] = torch.empty_like(params[1])
+    with torch.cuda.stream(third):
+        opt.step(src, stream=third)
+    third.synchronize()
+    ref.step(src)
+    torch.cuda.synchronize()
+    for a, b in zip(params, want):
+        assert torch.equal(a, b)
 
 
 # --------------------------------------------------------- graphs, streams --

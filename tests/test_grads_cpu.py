@@ -275,14 +275,17 @@ def test_step_refuses_wrong_sources():
 
 @pytest.mark.parametrize("dtype,buffers", [(torch.float32, 1), (torch.bfloat16, 2)])
 def test_step_allocates_on_the_stream_that_writes(dtype, buffers, monkeypatch):
-    """The buffers that gradients are formed into come from the pool of the step's stream:
-    each allocation is made while that stream is current."""
+    """The buffers that gradients are formed into come from the pool of the step's stream: each
+    allocation is made while that stream is current.  A later step on another stream, given or
+    current, is made known to the allocator."""
+    from types import SimpleNamespace
     from muon_newton_schulz_02_amd import grads as G
-    now, made = [], []
+    side, other = SimpleNamespace(cuda_stream=7), SimpleNamespace(cuda_stream=9)
+    now, made, recorded = [other], [], []
 
     class At:
         def __init__(self, dev, stream, tensors):
-            self.stream = stream
+            self.stream = stream or now[-1]
 
         def __enter__(self):
             now.append(self.stream)
@@ -292,20 +295,26 @@ def test_step_allocates_on_the_stream_that_writes(dtype, buffers, monkeypatch):
 
     def noted(make):
         def f(*a, **k):
-            made.append(now[-1] if now else None)
+            made.append(now[-1])
             return make(*a, **k)
         return f
 
     monkeypatch.setattr(G, "_At", At)
+    monkeypatch.setattr(G, "_raw_stream", lambda index: now[-1].cuda_stream)
     monkeypatch.setattr(G, "form_gradient", lambda *a, **k: None)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: now[-1])
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: recorded.append(s))
     for name in ("empty", "empty_like"):
         monkeypatch.setattr(torch, name, noted(getattr(torch, name)))
     opt = _holder(params=[torch.zeros(4, 4, dtype=dtype)])
     src = M.LinearGrad(None, None)
-    out = opt._formed(0, [src, src], "side")
+    out = opt._formed(0, [src, src], side)
     assert out is opt.grad_buffers[0] and out.shape == (4, 4) and out.dtype == dtype
-    assert made == ["side"] * buffers
-    assert opt._formed(0, [src, src], "other") is out and len(made) == buffers     # kept
+    assert made == [side] * buffers and recorded == []
+    for stream, want in ((side, []), (7, []), (None, [other]), (other, [other])):
+        del recorded[:]
+        assert opt._formed(0, [src, src], stream) is out and len(made) == buffers     # kept
+        assert recorded == want * buffers, stream
 
 
 @pytest.mark.parametrize("torch_there", [False, True])
