@@ -83,8 +83,9 @@ def launches(tmp_path_factory):
     subprocess.run([cc, "-O1", "-Wall", "-Werror", "-shared", "-fPIC", "-o", lib,
                     os.path.join(HERE, "c", "launch_trace.c"), "-ldl"], check=True)
     cases = _cases()
+    preload = ":".join([lib] + [x for x in [os.environ.get("LD_PRELOAD")] if x])
     res = subprocess.run([sys.executable, "-c", DRIVER % {"root": ROOT}, json.dumps(cases)],
-                         cwd=ROOT, env=dict(os.environ, LD_PRELOAD=lib), capture_output=True, text=True,
+                         cwd=ROOT, env=dict(os.environ, LD_PRELOAD=preload), capture_output=True, text=True,
                          timeout=600)
     assert res.returncode == 0, res.stderr[-3000:]
     return list(zip(cases, json.loads(res.stdout.splitlines()[-1])))
