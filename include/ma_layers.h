@@ -1,0 +1,110 @@
+/*
+ * ma_layers.h -- C ABI of the operators that a layer's forward and backward
+ * passes are made of, beside those of ma_grads.h, whose 8-bit form of an
+ * activation (codes and exps) they share.
+ *
+ *   ma_rms_norm_forward     s = x + residual, y = norm(s) (w + offset), y held in 8 bits
+ *   ma_rms_norm_backward    ds and dw (+)= from dy, s and the saved 1 / rms
+ *   ma_rotary               feature pairs turned by positions of several axes, and back
+ *
+ * Conventions are those of ma_grads.h: return codes and messages, checks
+ * before any launch, caller-owned memory, the caller's HIP stream, capturable,
+ * a workspace of its own for each of two calls that may run at once, float32
+ * arithmetic with one rounding to an array's type, results that do not depend
+ * on timing, strides in elements.  Written arrays overlap neither each other
+ * nor an input, unless a function allows it.
+ */
+#ifndef MA_LAYERS_H_
+#define MA_LAYERS_H_
+
+#include "ma_grads.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* ---- root-mean-square norm ------------------------------------------------- */
+
+/* Most columns of a norm: a row is kept in one workgroup's registers. */
+#define MA_NORM_MAX_COLS 16384
+
+/* For every row: s = x + residual, inv_rms = 1 / sqrt(mean(s^2) + eps) and
+ * y = s * inv_rms * (weight + weight_offset).
+ *   residual, sum   both or neither NULL; without them s is x.  sum receives s rounded
+ *                   to dtype (the norm is that of the unrounded s).
+ *   y               may be NULL where codes are given
+ *   codes, exps     both or neither NULL: y as rounded to dtype, held in 8 bits: the
+ *                   bytes ma_act_pack gives for y
+ * x, residual, sum and y are rows x cols of one dtype, weight has cols entries of
+ * weight_dtype, inv_rms rows float32 values.  eps is a finite float32, at least
+ * 2^-100.  A row whose squares leave float32's range is summed scaled, so only
+ * a row that holds an infinity or a NaN gives such values.  rows may be 0.
+ * Errors: INVALID_ARG, SHAPE (cols above MA_NORM_MAX_COLS), HIP. */
+int ma_rms_norm_forward(const void* x, int64_t x_stride, const void* residual,
+                        int64_t residual_stride, int32_t dtype, int64_t rows, int64_t cols,
+                        const void* weight, int32_t weight_dtype, double weight_offset, double eps,
+                        void* sum, int64_t sum_stride, void* y, int64_t y_stride, int8_t* codes,
+                        uint8_t* exps, float* inv_rms, void* stream);
+
+/* Bytes of workspace (256-byte aligned) a ma_rms_norm_backward call with a
+ * dweight needs (without one none).  Errors: INVALID_ARG (null), SHAPE. */
+int ma_rms_norm_backward_workspace_size(int64_t rows, int64_t cols, size_t* bytes);
+
+/* The gradient of y in s and the weight, at the s and inv_rms of the forward pass:
+ * with h = s * inv_rms and g = dy * (weight + weight_offset),
+ *   ds = inv_rms * (g - h * mean(g * h)) + dsum
+ *   dweight = sum over rows of dy * h   (with accumulate = 1, added to dweight)
+ * dsum (NULL for none) is the gradient that reaches s past the norm; ds is the
+ * gradient of x and of the residual alike.  dweight, contiguous in dweight_dtype,
+ * may be NULL.  rows may be 0 (dweight's sum is then zero).  The sums over
+ * rows are float32, in an order that follows from rows and cols alone.  Errors:
+ * INVALID_ARG, SHAPE, WORKSPACE, HIP. */
+int ma_rms_norm_backward(const void* dy, int64_t dy_stride, const void* s, int64_t s_stride,
+                         const void* dsum, int64_t dsum_stride, int32_t dtype, int64_t rows,
+                         int64_t cols, const float* inv_rms, const void* weight,
+                         int32_t weight_dtype, double weight_offset, void* ds, int64_t ds_stride,
+                         void* dweight, int32_t dweight_dtype, int32_t accumulate,
+                         void* workspace, size_t ws_bytes, void* stream);
+
+/* ---- rotary positions -------------------------------------------------------- */
+
+#define MA_ROTARY_MAX_PAIRS 256
+#define MA_ROTARY_MAX_AXES  4
+
+/* Where pair i of `pairs` lies in a head's features */
+#define MA_ROTARY_HALF  0   /* features i and pairs + i   */
+#define MA_ROTARY_PAIRS 1   /* features 2 i and 2 i + 1   */
+
+/* Which axis a pair belongs to */
+#define MA_ROTARY_BLOCKS 0  /* the axes' pairs one axis after the other             */
+#define MA_ROTARY_CYCLED 1  /* the axes in turn, without those that are used up     */
+
+/* Fills frequencies (radians per position) and pair_axis, both host arrays of
+ * sum(sections) entries, for axes that own sections[0 .. axes) pairs each.  Pair i
+ * of all `pairs` turns at theta^(-i / pairs); with restart = 1 the j-th pair of an
+ * axis with n turns at theta^(-j / n).  Errors: INVALID_ARG, SHAPE. */
+int ma_rotary_frequencies(const int32_t* sections, int32_t axes, double theta, int32_t order,
+                          int32_t restart, double* frequencies, uint8_t* pair_axis);
+
+/* For token t, head h and pair i, with the angle a = positions[pair_axis[i]][t] *
+ * frequencies[i] and the pair's features (u, v):
+ *   (u, v) -> (u cos a - v sin a, u sin a + v cos a)
+ * and with inverse = 1 by -a, which is the backward pass.  Features past
+ * 2 * pairs are copied.  x and out are n_tokens x heads x head_dim of one dtype, each
+ * head's features contiguous, with strides between tokens and between heads; positions
+ * is axes x n_tokens signed integers of position_bytes (4 or 8), axis_stride from axis
+ * to axis.  out may be x itself with x's strides.  frequencies and pair_axis are
+ * host arrays, read before the call returns.  Angles are formed and reduced in 64 bits.
+ * n_tokens may be 0.  Errors: INVALID_ARG, SHAPE, HIP. */
+int ma_rotary(const void* x, int32_t dtype, int64_t n_tokens, int64_t heads, int64_t head_dim,
+              int64_t x_token_stride, int64_t x_head_stride, const void* positions,
+              int32_t position_bytes, int32_t axes, int64_t axis_stride,
+              const double* frequencies, const uint8_t* pair_axis, int64_t pairs, int32_t layout,
+              int32_t inverse, void* out, int64_t out_token_stride, int64_t out_head_stride,
+              void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* MA_LAYERS_H_ */

@@ -10,7 +10,9 @@ and workspace as torch tensors and calls `muon_adamw_step`.
 
 The operators that produce gradients (include/ma_grads.h: embedding lookup and
 gradient, activations held in 8 bits and the gradients formed from them) are
-in `grads` and under their names here.
+in `grads`, those that a layer's forward and backward passes are made of
+(include/ma_layers.h: norm, rotary positions) in `layers`, and all of them under
+their names here.
 """
 
 from __future__ import annotations
@@ -23,8 +25,9 @@ from . import _abi
 from ._abi import (MA_ACT_GELU_TANH, MA_ACT_GROUP, MA_ACT_SILU, MA_ERR_CAPTURE, MA_ERR_HIP, MA_ERR_INVALID_ARG, MA_ERR_SHAPE, MA_ERR_UNSUPPORTED,  # noqa: F401
                    MA_ERR_WORKSPACE, MA_GROUP_ADAMW, MA_GROUP_MUON, MA_GROUP_NONE,
                    MA_LR_CONSTANT, MA_LR_COSINE_MIN, MA_MODE_ADAMW, MA_MODE_MUON_ADAMW,
-                   MA_NOALLOC_SCRATCH_BYTES, MA_NS_BF16, MA_NS_FP32, MA_OK, MA_PARAM_BF16,
-                   MA_PARAM_FP32)
+                   MA_NOALLOC_SCRATCH_BYTES, MA_NORM_MAX_COLS, MA_NS_BF16, MA_NS_FP32, MA_OK, MA_PARAM_BF16,
+                   MA_PARAM_FP32, MA_ROTARY_BLOCKS, MA_ROTARY_CYCLED, MA_ROTARY_HALF, MA_ROTARY_MAX_AXES,
+                   MA_ROTARY_MAX_PAIRS, MA_ROTARY_PAIRS)
 
 __all__ = [
     "MuonAdamWError", "Plan", "State",
@@ -35,11 +38,13 @@ __all__ = [
     "muon_adamw_version", "MuonAdamW", "load_library",
 ]
 
-# The gradient operators need torch at import (the optimizer step only when it
-# is called), so they are loaded on first use.
+# The operators beside the step need torch at import (the optimizer step only when
+# it is called), so they are loaded on first use.
 _GRADS = ("ActCheckpoint", "EmbeddingGrad", "LinearGrad", "ma_act_pack", "ma_act_unpack",
           "ma_embedding_lookup", "ma_embedding_grad", "ma_embedding_grad_workspace_size",
           "ma_linear_grad", "ma_linear_grad_workspace_size", "ma_glu_forward", "ma_glu_backward")
+_LAYERS = ("Rotary", "ma_rms_norm_forward", "ma_rms_norm_backward", "ma_rms_norm_backward_workspace_size",
+           "ma_rotary")
 
 
 def _torch_installed() -> bool:
@@ -53,7 +58,7 @@ def _torch_installed() -> bool:
 
 # (a star import of the optimizer step alone works without torch)
 if _torch_installed():
-    __all__ += _GRADS
+    __all__ += _GRADS + _LAYERS
 
 
 def __getattr__(name):
@@ -61,6 +66,11 @@ def __getattr__(name):
         from . import grads
         for n in _GRADS:
             globals()[n] = getattr(grads, n)
+        return globals()[name]
+    if name in _LAYERS:
+        from . import layers
+        for n in _LAYERS:
+            globals()[n] = getattr(layers, n)
         return globals()[name]
     raise AttributeError("module %r has no attribute %r" % (__name__, name))
 

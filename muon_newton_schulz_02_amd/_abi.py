@@ -1,4 +1,4 @@
-"""ctypes mirror of include/muon_adamw.h and include/ma_grads.h.
+"""ctypes mirror of include/muon_adamw.h, include/ma_grads.h and include/ma_layers.h.
 
 Argument marshalling only: every step of the optimizer runs in the HIP
 library.  Loading fails loudly when the library has not been built; there is
@@ -29,6 +29,10 @@ MA_PARAM_FP32, MA_PARAM_BF16 = 0, 1
 MA_MAX_NDIM = 8
 MA_ACT_GROUP = 32
 MA_ACT_SILU, MA_ACT_GELU_TANH = 0, 1
+MA_NORM_MAX_COLS = 16384
+MA_ROTARY_MAX_PAIRS, MA_ROTARY_MAX_AXES = 256, 4
+MA_ROTARY_HALF, MA_ROTARY_PAIRS = 0, 1
+MA_ROTARY_BLOCKS, MA_ROTARY_CYCLED = 0, 1
 MA_PROFILE_EVENTS = 5
 MA_NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -119,6 +123,18 @@ GRAD_SIGNATURES = [
                                   _I64, _P, _P, _P]),
 ]
 
+# and of ma_layers.h
+LAYER_SIGNATURES = [
+    ("ma_rms_norm_forward", C.c_int, [_P, _I64, _P, _I64, _I32, _I64, _I64, _P, _I32, _F64, _F64, _P, _I64, _P,
+                                      _I64, _P, _P, _P, _P]),
+    ("ma_rms_norm_backward_workspace_size", C.c_int, [_I64, _I64, C.POINTER(_SZ)]),
+    ("ma_rms_norm_backward", C.c_int, [_P, _I64, _P, _I64, _P, _I64, _I32, _I64, _I64, _P, _P, _I32, _F64, _P,
+                                       _I64, _P, _I32, _I32, _P, _SZ, _P]),
+    ("ma_rotary_frequencies", C.c_int, [_P, _I32, _F64, _I32, _I32, _P, _P]),
+    ("ma_rotary", C.c_int, [_P, _I32, _I64, _I64, _I64, _I64, _I64, _P, _I32, _I32, _I64, _P, _P, _I64, _I32,
+                            _I32, _P, _I64, _I64, _P]),
+]
+
 _lib = None
 
 
@@ -132,7 +148,7 @@ def load(path: str = LIB_PATH):
             "libmuon_adamw.so is not built (%s); run "
             "`python -m muon_newton_schulz_02_amd.build` first" % path)
     lib = C.CDLL(path)
-    for name, res, args in SIGNATURES + GRAD_SIGNATURES:
+    for name, res, args in SIGNATURES + GRAD_SIGNATURES + LAYER_SIGNATURES:
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args

@@ -2,7 +2,7 @@
 
     python -m muon_newton_schulz_02_amd.build        # or build() from Python
 
-libmuon_adamw.so is the optimizer (the C ABI of include/muon_adamw.h);
+libmuon_adamw.so is the optimizer and the operators beside it (the C ABIs in include/);
 libma_peaks.so holds the ceiling probes the benchmark measures beside it
 (csrc/peaks.hip).  Every source is compiled by hipcc with
 --offload-arch=gfx950; packed-fp32 instruction selection is disabled for
@@ -25,7 +25,7 @@ LIB = os.path.join(HERE, "libmuon_adamw.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 
 SOURCES = ["plan.cpp", "step.cpp", "elementwise.hip", "ns_gemm.hip", "noalloc.hip", "grads.cpp",
-           "act8.hip", "embedding.hip", "linear_grad.hip"]
+           "act8.hip", "embedding.hip", "linear_grad.hip", "layers.cpp", "norm.hip", "rotary.hip"]
 PEAKS_SOURCES = ["peaks.hip"]
 PEAKS_LIB = os.path.join(HERE, "libma_peaks.so")
 
@@ -68,7 +68,7 @@ def build(verbose: bool = False) -> str:
     optimizer library's path."""
     hipcc = _hipcc()
     os.makedirs(BUILD_DIR, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=min(5, os.cpu_count() or 1)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
         objs = list(ex.map(lambda s: _compile(hipcc, s), SOURCES + PEAKS_SOURCES))
     _link(hipcc, objs[:len(SOURCES)], LIB)
     _link(hipcc, objs[len(SOURCES):], PEAKS_LIB)

@@ -80,14 +80,8 @@ __device__ __forceinline__ void store8(T* row, int col, int cols, const float* v
 template <bool NT>
 __device__ __forceinline__ void hold8(const float* v, int8_t* codes, uint8_t* exps, const At& at,
                                       int code_pitch, int exp_pitch) {
-    uint32_t top = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) top = max(top, abs_bits(v[e]));
-    // the largest of four neighbouring lanes, by lane permutation within them
-    top = max(top, (uint32_t)__builtin_amdgcn_mov_dpp((int)top, 0xB1, 0xf, 0xf, true));     // 1, 0, 3, 2
-    top = max(top, (uint32_t)__builtin_amdgcn_mov_dpp((int)top, 0x4E, 0xf, 0xf, true));     // 2, 3, 0, 1
-    const uint32_t b = act_exp_byte(top);
-    const u32x2 w = act_codes(v, b);
+    uint32_t b;
+    const u32x2 w = hold_unit(v, b);
     const int col = at.col();
     if (col < code_pitch) {
         u32x2* p = reinterpret_cast<u32x2*>(codes + at.row_at(code_pitch) + col);

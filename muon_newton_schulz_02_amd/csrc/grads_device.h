@@ -156,6 +156,19 @@ __device__ __forceinline__ u32x2 act_codes(const float* v, uint32_t b) {
     return w;
 }
 
+// Hold 8 values of each lane, whose group is four neighbouring lanes (active
+// together): the codes, and the group's exponent byte in b.
+__device__ __forceinline__ u32x2 hold_unit(const float* v, uint32_t& b) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = max(top, abs_bits(v[e]));
+    // the largest of four neighbouring lanes, by lane permutation within them
+    top = max(top, (uint32_t)__builtin_amdgcn_mov_dpp((int)top, 0xB1, 0xf, 0xf, true));     // 1, 0, 3, 2
+    top = max(top, (uint32_t)__builtin_amdgcn_mov_dpp((int)top, 0x4E, 0xf, 0xf, true));     // 2, 3, 0, 1
+    b = act_exp_byte(top);
+    return act_codes(v, b);
+}
+
 __device__ __forceinline__ float act_value(uint32_t w, int byte, float scale) {
     return (float)(int)(int8_t)(w >> (8 * byte)) * scale;
 }

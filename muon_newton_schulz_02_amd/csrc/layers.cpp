@@ -1,0 +1,309 @@
+// The C entry points of the layer operators: argument checks and the calls of
+// their kernels' launchers.  Nothing is launched before every argument has
+// been checked.
+
+#include <cstring>
+
+#include "arg_checks.h"
+#include "layers_internal.h"
+
+using namespace ma;
+
+namespace {
+
+constexpr int64_t kMaxHeads = int64_t(1) << 16;
+
+// tokens x heads x dim with strides between tokens and between heads: none
+// negative or of 2^31 elements or more, and the array within 2^40.
+int check_heads(const char* fn, const char* what, int64_t tokens, int64_t heads, int64_t dim,
+                int64_t token, int64_t head) {
+    const int64_t most = int64_t(1) << 31;
+    if (token < 0 || token >= most || head < 0 || head >= most ||
+        (tokens > 0 && (tokens - 1) * token + (heads - 1) * head + dim > kMaxElems)) {
+        set_error("%s: %s strides %lld and %lld (at least 0, below 2^31, 2^40 elements in all)", fn, what,
+                  (long long)token, (long long)head);
+        return MA_ERR_INVALID_ARG;
+    }
+    return MA_OK;
+}
+
+// Whether no two elements share an address: rows of whole tokens, or of whole heads.
+bool token_rows(int64_t tokens, int64_t heads, int64_t dim, int64_t token, int64_t head) {
+    return (heads == 1 || head >= dim) && (tokens == 1 || token >= (heads - 1) * head + dim);
+}
+bool head_rows(int64_t tokens, int64_t heads, int64_t dim, int64_t token, int64_t head) {
+    return (tokens == 1 || token >= dim) && (heads == 1 || head >= (tokens - 1) * token + dim);
+}
+
+int check_heads_out(const char* fn, const char* what, int64_t tokens, int64_t heads, int64_t dim,
+                    int64_t token, int64_t head) {
+    TRY(check_heads(fn, what, tokens, heads, dim, token, head));
+    if (tokens <= 0 || token_rows(tokens, heads, dim, token, head) || head_rows(tokens, heads, dim, token, head))
+        return MA_OK;
+    set_error("%s: %s strides %lld and %lld: its elements overlap", fn, what, (long long)token, (long long)head);
+    return MA_ERR_INVALID_ARG;
+}
+
+Span heads_of(const char* name, const void* p, int32_t dtype, int64_t tokens, int64_t heads, int64_t dim,
+              int64_t token, int64_t head, bool written) {
+    const int64_t e = (int64_t)type_size(dtype);
+    if (tokens <= 0) return {name, p, 0, 0, 0, (size_t)e, written};
+    if (token_rows(tokens, heads, dim, token, head))
+        return {name, p, tokens, ((heads - 1) * head + dim) * e, token * e, (size_t)e, written};
+    if (head_rows(tokens, heads, dim, token, head))
+        return {name, p, heads, ((tokens - 1) * token + dim) * e, head * e, (size_t)e, written};
+    const int64_t all = ((tokens - 1) * token + (heads - 1) * head + dim) * e;
+    return {name, p, 1, all, all, (size_t)e, written};
+}
+
+int check_pair(const char* fn, const char* one, const void* a, const char* two, const void* b) {
+    if (!a == !b) return MA_OK;
+    set_error("%s: %s and %s must both be given or both be NULL", fn, one, two);
+    return MA_ERR_INVALID_ARG;
+}
+
+int check_norm_shape(const char* fn, int64_t rows, int64_t cols) {
+    TRY(check_size(fn, "rows", rows, 0, kMaxCount));
+    TRY(check_size(fn, "cols", cols, 1, MA_NORM_MAX_COLS));
+    return MA_OK;
+}
+
+int64_t norm_ws_bytes(int64_t rows, int64_t cols) {
+    return round_up(norm_backward_groups(rows, cols) * cols * 4, 256);
+}
+
+}  // namespace
+
+extern "C" {
+
+int ma_rms_norm_forward(const void* x, int64_t x_stride, const void* residual,
+                        int64_t residual_stride, int32_t dtype, int64_t rows, int64_t cols,
+                        const void* weight, int32_t weight_dtype, double weight_offset, double eps,
+                        void* sum, int64_t sum_stride, void* y, int64_t y_stride, int8_t* codes,
+                        uint8_t* exps, float* inv_rms, void* stream) {
+    const char* fn = "ma_rms_norm_forward";
+    TRY(check_dtype(fn, "x", dtype));
+    TRY(check_dtype(fn, "weight", weight_dtype));
+    TRY(check_norm_shape(fn, rows, cols));
+    TRY(check_stride(fn, "x", x_stride, 0, rows));
+    TRY(check_scale(fn, weight_offset));
+    if (!(eps >= 0x1p-100) || !std::isfinite((float)eps)) {
+        set_error("%s: eps must be a finite float32, at least 2^-100", fn);
+        return MA_ERR_INVALID_ARG;
+    }
+    if (rows > 0) {
+        TRY(check_pair(fn, "residual", residual, "sum", sum));
+        TRY(check_pair(fn, "codes", codes, "exps", exps));
+        if (!y && !codes) {
+            set_error("%s: y and codes are both NULL", fn);
+            return MA_ERR_INVALID_ARG;
+        }
+    }
+    if (residual) {
+        TRY(check_stride(fn, "residual", residual_stride, 0, rows));
+        TRY(check_stride(fn, "sum", sum_stride, cols, rows));
+    }
+    if (y) TRY(check_stride(fn, "y", y_stride, cols, rows));
+    const int64_t r = residual ? rows : 0;
+    TRY(check_spans(fn, {matrix("x", x, dtype, rows, cols, x_stride, false),
+                         matrix("residual", residual, dtype, r, cols, residual_stride, false),
+                         flat("weight", weight, rows ? cols * (int64_t)type_size(weight_dtype) : 0,
+                              type_size(weight_dtype), false),
+                         matrix("sum", sum, dtype, r, cols, sum_stride, true),
+                         matrix("y", y, dtype, y ? rows : 0, cols, y_stride, true),
+                         codes_of("codes", codes, codes ? rows : 0, cols, true),
+                         exps_of("exps", exps, codes ? rows : 0, cols, true),
+                         flat("inv_rms", inv_rms, rows * 4, 4, true)}));
+    NormArgs a{};
+    a.x = x;
+    a.res = residual;
+    a.sum = sum;
+    a.y = y;
+    a.weight = weight;
+    a.codes = codes;
+    a.exps = exps;
+    a.inv = inv_rms;
+    a.x_stride = x_stride;
+    a.res_stride = residual_stride;
+    a.sum_stride = sum_stride;
+    a.y_stride = y_stride;
+    a.rows = rows;
+    a.cols = cols;
+    a.offset = (float)weight_offset;
+    a.eps = (float)eps;
+    a.dtype = dtype;
+    a.weight_dtype = weight_dtype;
+    return done(fn, launch_rms_norm_forward(a, stream));
+}
+
+int ma_rms_norm_backward_workspace_size(int64_t rows, int64_t cols, size_t* bytes) {
+    const char* fn = "ma_rms_norm_backward_workspace_size";
+    if (!bytes) {
+        set_error("%s: NULL argument", fn);
+        return MA_ERR_INVALID_ARG;
+    }
+    TRY(check_norm_shape(fn, rows, cols));
+    *bytes = (size_t)norm_ws_bytes(rows, cols);
+    clear_error();
+    return MA_OK;
+}
+
+int ma_rms_norm_backward(const void* dy, int64_t dy_stride, const void* s, int64_t s_stride,
+                         const void* dsum, int64_t dsum_stride, int32_t dtype, int64_t rows,
+                         int64_t cols, const float* inv_rms, const void* weight,
+                         int32_t weight_dtype, double weight_offset, void* ds, int64_t ds_stride,
+                         void* dweight, int32_t dweight_dtype, int32_t accumulate,
+                         void* workspace, size_t ws_bytes, void* stream) {
+    const char* fn = "ma_rms_norm_backward";
+    TRY(check_dtype(fn, "dy", dtype));
+    TRY(check_dtype(fn, "weight", weight_dtype));
+    TRY(check_norm_shape(fn, rows, cols));
+    TRY(check_stride(fn, "dy", dy_stride, 0, rows));
+    TRY(check_stride(fn, "s", s_stride, 0, rows));
+    if (dsum) TRY(check_stride(fn, "dsum", dsum_stride, 0, rows));
+    TRY(check_stride(fn, "ds", ds_stride, cols, rows));
+    TRY(check_scale(fn, weight_offset));
+    TRY(check_flag(fn, "accumulate", accumulate));
+    const int64_t need = dweight ? norm_ws_bytes(rows, cols) : 0;
+    if (dweight) {
+        TRY(check_dtype(fn, "dweight", dweight_dtype));
+        TRY(check_workspace(fn, workspace, ws_bytes, (size_t)need));
+    }
+    const int64_t we = (int64_t)type_size(dweight_dtype);
+    TRY(check_spans(fn, {matrix("dy", dy, dtype, rows, cols, dy_stride, false),
+                         matrix("s", s, dtype, rows, cols, s_stride, false),
+                         matrix("dsum", dsum, dtype, dsum ? rows : 0, cols, dsum_stride, false),
+                         flat("inv_rms", inv_rms, rows * 4, 4, false),
+                         flat("weight", weight, rows ? cols * (int64_t)type_size(weight_dtype) : 0,
+                              type_size(weight_dtype), false),
+                         matrix("ds", ds, dtype, rows, cols, ds_stride, true),
+                         flat("dweight", dweight, dweight ? cols * we : 0, (size_t)we, true),
+                         flat("workspace", workspace, need, 1, true)}));
+    NormArgs a{};
+    a.x = s;
+    a.dy = dy;
+    a.dsum = dsum;
+    a.ds = ds;
+    a.dw = dweight;
+    a.weight = weight;
+    a.inv = const_cast<float*>(inv_rms);
+    a.partials = dweight ? static_cast<float*>(workspace) : nullptr;
+    a.x_stride = s_stride;
+    a.dy_stride = dy_stride;
+    a.dsum_stride = dsum_stride;
+    a.ds_stride = ds_stride;
+    a.rows = rows;
+    a.cols = cols;
+    a.offset = (float)weight_offset;
+    a.dtype = dtype;
+    a.weight_dtype = weight_dtype;
+    a.dw_dtype = dweight_dtype;
+    a.accumulate = accumulate;
+    return done(fn, launch_rms_norm_backward(a, stream));
+}
+
+int ma_rotary_frequencies(const int32_t* sections, int32_t axes, double theta, int32_t order,
+                          int32_t restart, double* frequencies, uint8_t* pair_axis) {
+    const char* fn = "ma_rotary_frequencies";
+    if (!sections || !frequencies || !pair_axis) {
+        set_error("%s: NULL argument", fn);
+        return MA_ERR_INVALID_ARG;
+    }
+    TRY(check_size(fn, "axes", axes, 1, MA_ROTARY_MAX_AXES));
+    TRY(check_flag(fn, "restart", restart));
+    if (order != MA_ROTARY_BLOCKS && order != MA_ROTARY_CYCLED) {
+        set_error("%s: unknown order %d", fn, order);
+        return MA_ERR_INVALID_ARG;
+    }
+    if (!(theta > 0) || !std::isfinite(theta)) {
+        set_error("%s: theta must be positive and finite", fn);
+        return MA_ERR_INVALID_ARG;
+    }
+    int64_t pairs = 0;
+    for (int a = 0; a < axes; ++a) {
+        TRY(check_size(fn, "a section", sections[a], 0, MA_ROTARY_MAX_PAIRS));
+        pairs += sections[a];
+    }
+    TRY(check_size(fn, "pairs", pairs, 1, MA_ROTARY_MAX_PAIRS));
+    int used[MA_ROTARY_MAX_AXES] = {0}, axis = 0;
+    for (int i = 0; i < (int)pairs; ++i) {
+        while (used[axis] == sections[axis]) axis = (axis + 1) % axes;
+        const int j = used[axis]++;
+        pair_axis[i] = (uint8_t)axis;
+        frequencies[i] = std::pow(theta, restart ? -(double)j / sections[axis] : -(double)i / (double)pairs);
+        if (order == MA_ROTARY_CYCLED) axis = (axis + 1) % axes;
+    }
+    clear_error();
+    return MA_OK;
+}
+
+int ma_rotary(const void* x, int32_t dtype, int64_t n_tokens, int64_t heads, int64_t head_dim,
+              int64_t x_token_stride, int64_t x_head_stride, const void* positions,
+              int32_t position_bytes, int32_t axes, int64_t axis_stride,
+              const double* frequencies, const uint8_t* pair_axis, int64_t pairs, int32_t layout,
+              int32_t inverse, void* out, int64_t out_token_stride, int64_t out_head_stride,
+              void* stream) {
+    const char* fn = "ma_rotary";
+    TRY(check_dtype(fn, "x", dtype));
+    TRY(check_size(fn, "n_tokens", n_tokens, 0, kMaxCount));
+    TRY(check_size(fn, "heads", heads, 1, kMaxHeads));
+    TRY(check_size(fn, "head_dim", head_dim, 1, 2 * MA_ROTARY_MAX_PAIRS));
+    TRY(check_size(fn, "pairs", pairs, 1, head_dim / 2));
+    TRY(check_size(fn, "axes", axes, 1, MA_ROTARY_MAX_AXES));
+    TRY(check_flag(fn, "inverse", inverse));
+    if (position_bytes != 4 && position_bytes != 8) {
+        set_error("%s: position_bytes %d (4 or 8)", fn, position_bytes);
+        return MA_ERR_INVALID_ARG;
+    }
+    if (layout != MA_ROTARY_HALF && layout != MA_ROTARY_PAIRS) {
+        set_error("%s: unknown layout %d", fn, layout);
+        return MA_ERR_INVALID_ARG;
+    }
+    TRY(check_heads(fn, "x", n_tokens, heads, head_dim, x_token_stride, x_head_stride));
+    TRY(check_heads_out(fn, "out", n_tokens, heads, head_dim, out_token_stride, out_head_stride));
+    if (axis_stride < 0 || axis_stride > (int64_t(1) << 31)) {
+        set_error("%s: axis stride %lld (at least 0, at most 2^31)", fn, (long long)axis_stride);
+        return MA_ERR_INVALID_ARG;
+    }
+    if (!frequencies || !pair_axis) {
+        set_error("%s: NULL argument", fn);
+        return MA_ERR_INVALID_ARG;
+    }
+    RotaryTable tab;
+    std::memset(&tab, 0, sizeof(tab));
+    for (int i = 0; i < (int)pairs; ++i) {
+        if (pair_axis[i] >= axes || !std::isfinite(frequencies[i])) {
+            set_error("%s: pair %d has axis %d of %d and frequency %g", fn, i, pair_axis[i], axes, frequencies[i]);
+            return MA_ERR_INVALID_ARG;
+        }
+        tab.axis[i] = pair_axis[i];
+        tab.turns[i] = (double)(frequencies[i] / 6.283185307179586476925286766559005768L);
+    }
+    const int64_t reach = n_tokens > 0 ? (axes - 1) * axis_stride + n_tokens : 0;
+    const bool same = out == x && out_token_stride == x_token_stride && out_head_stride == x_head_stride;
+    TRY(check_spans(fn, {heads_of("x", x, dtype, same ? 0 : n_tokens, heads, head_dim, x_token_stride, x_head_stride,
+                                  false),
+                         flat("positions", positions, reach * position_bytes, (size_t)position_bytes, false),
+                         heads_of("out", out, dtype, n_tokens, heads, head_dim, out_token_stride, out_head_stride,
+                                  true)}));
+    RotaryArgs a{};
+    a.x = x;
+    a.positions = positions;
+    a.out = out;
+    a.x_token = x_token_stride;
+    a.x_head = x_head_stride;
+    a.out_token = out_token_stride;
+    a.out_head = out_head_stride;
+    a.axis_stride = axis_stride;
+    a.n_tokens = n_tokens;
+    a.heads = (int32_t)heads;
+    a.dim = (int32_t)head_dim;
+    a.pairs = (int32_t)pairs;
+    a.layout = layout;
+    a.inverse = inverse;
+    a.position_bytes = position_bytes;
+    a.dtype = dtype;
+    return done(fn, launch_rotary(a, tab, stream));
+}
+
+}  // extern "C"

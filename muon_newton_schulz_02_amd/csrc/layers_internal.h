@@ -1,0 +1,47 @@
+// Internal declarations of the layer operators (include/ma_layers.h): the
+// split rules their host code and kernels share, and the kernel launchers.
+// Not part of the C ABI.
+#pragma once
+
+#include "../../include/ma_layers.h"
+#include "grads_internal.h"
+
+namespace ma {
+
+// Each launcher returns a hipError_t as int.
+
+// ---------------------------------------------------------------- norm --
+struct NormArgs {
+    const void *x, *res, *dy, *dsum;      // forward: x, res; backward: s (as x), dy, dsum
+    void *sum, *y, *ds, *dw;
+    const void* weight;
+    int8_t* codes;
+    uint8_t* exps;
+    float* inv;
+    float* partials;
+    int64_t x_stride, res_stride, dy_stride, dsum_stride, sum_stride, y_stride, ds_stride;
+    int64_t rows, cols;
+    float offset, eps;
+    int32_t dtype, weight_dtype, dw_dtype, accumulate;
+};
+// Workgroups of a backward pass, each of which leaves one partial sum of dw.
+int64_t norm_backward_groups(int64_t rows, int64_t cols);
+int launch_rms_norm_forward(const NormArgs& a, void* stream);
+int launch_rms_norm_backward(const NormArgs& a, void* stream);
+
+// -------------------------------------------------------------- rotary --
+// Frequencies in turns per position, and the axis of each pair; they travel as a
+// kernel argument, so a captured launch holds its own copy.
+struct RotaryTable {
+    double turns[MA_ROTARY_MAX_PAIRS];
+    uint8_t axis[MA_ROTARY_MAX_PAIRS];
+};
+struct RotaryArgs {
+    const void *x, *positions;
+    void* out;
+    int64_t x_token, x_head, out_token, out_head, axis_stride, n_tokens;
+    int32_t heads, dim, pairs, layout, inverse, position_bytes, dtype;
+};
+int launch_rotary(const RotaryArgs& a, const RotaryTable& t, void* stream);
+
+}  // namespace ma

@@ -1,0 +1,266 @@
+"""Python binding of include/ma_layers.h: the operators that a layer's forward
+and backward passes are made of, beside those of `grads`.
+
+    ma_rms_norm_forward, ma_rms_norm_backward     norm of a residual stream with the
+                          addition that feeds it, the output also held in 8 bits
+    ma_rotary             feature pairs turned by positions of several axes, and back
+
+Manners are those of `grads`: names and meanings are the C ABI's, outputs and
+workspaces are allocated as torch tensors where the caller passes none,
+everything is asynchronous on `stream` (a torch.cuda.Stream, a raw hipStream_t
+int, or None for torch's current stream of the tensors' device), and no result
+carries autograd history: a forward pass returns what its backward pass takes.
+"""
+
+from __future__ import annotations
+
+import ctypes as C
+from typing import Optional
+
+import torch
+
+from . import _abi
+from ._abi import MA_ROTARY_BLOCKS, MA_ROTARY_CYCLED, MA_ROTARY_HALF, MA_ROTARY_PAIRS
+from .grads import (ActCheckpoint, _At, _check_cuda, _check_workspace, _dtype, _elsewhere, _fail, _held, _out_as,
+                    _out_like, _raw_stream, _rows, _same_device, _workspace)
+
+_LAYOUTS = {"half": MA_ROTARY_HALF, "pairs": MA_ROTARY_PAIRS}
+_ORDERS = {"blocks": MA_ROTARY_BLOCKS, "cycled": MA_ROTARY_CYCLED}
+
+
+def _same_type(x, what: str, like, name: str):
+    if x.shape != like.shape or x.dtype != like.dtype:
+        raise ValueError("%s %s %s does not belong to %s %s %s" % (
+            what, tuple(x.shape), x.dtype, name, tuple(like.shape), like.dtype))
+
+
+def _vector(x, what: str, n: int):
+    _check_cuda(x, what)
+    if x.dim() != 1 or x.shape[0] != n or (n > 1 and x.stride(0) != 1):
+        raise ValueError("%s must be a contiguous vector of %d (got %s)" % (what, n, tuple(x.shape)))
+
+
+def _per_row(x, what: str, shape):
+    """A contiguous float32 value for each row."""
+    _check_cuda(x, what)
+    if x.dtype != torch.float32:
+        raise TypeError("%s must be float32 (got %s)" % (what, x.dtype))
+    if tuple(x.shape) != tuple(shape) or not x.is_contiguous():
+        raise ValueError("%s must be contiguous, of shape %s (got %s)" % (what, tuple(shape), tuple(x.shape)))
+
+
+def _ptr(x):
+    return None if x is None else x.data_ptr()
+
+
+# --------------------------------------------------------------------- norm --
+
+def ma_rms_norm_forward(x, weight, residual=None, eps: float = 1e-6, weight_offset: float = 0.0, out=None,
+                        sum_out=None, y_ckpt=None, stream=None):
+    """(y, s, inv_rms, y held in 8 bits or None) with s = x + residual, inv_rms = 1 / sqrt(mean(s^2) + eps)
+    over the last dimension and y = s * inv_rms * (weight + weight_offset).  Without a
+    residual s is x itself.  y_ckpt (True, or an ActCheckpoint to fill) also holds y in 8 bits: the x of
+    the following linear layers' ma_linear_grad.  With out=False y is only held (and None is returned for
+    it).  s and inv_rms are what ma_rms_norm_backward takes."""
+    _check_cuda(x, "x")
+    dt = _dtype(x, "x")
+    rows, cols, ld = _rows(x, "x")
+    _vector(weight, "weight", cols)
+    wdt = _dtype(weight, "weight")
+    dev = x.device
+    rld = sld = 0
+    if residual is not None:
+        _check_cuda(residual, "residual")
+        _same_type(residual, "residual", x, "x")
+        rld = _rows(residual, "residual")[2]
+    elif sum_out is not None:
+        raise ValueError("sum_out needs a residual (without one s is x)")
+    hold = y_ckpt is not None and y_ckpt is not False
+    if hold and y_ckpt is not True:
+        _held(y_ckpt, "y_ckpt", dev, rows, cols)
+    if out is False and not hold:
+        raise ValueError("out=False needs y_ckpt")
+    given = None if out is False else out
+    _same_device(dev, ("weight", weight), ("residual", residual), ("out", given), ("sum_out", sum_out))
+    if _elsewhere(dev, stream):
+        used = [x, weight, residual, given, sum_out]
+        if hold and y_ckpt is not True:
+            used += y_ckpt._tensors()
+        with _At(dev, stream, used):
+            return ma_rms_norm_forward(x, weight, residual, eps, weight_offset, out, sum_out, y_ckpt)
+    yld = 0
+    y = None
+    if out is not False:
+        y = _out_as(out, "out", x)
+        yld = _rows(y, "out")[2]
+    s = x
+    if residual is not None:
+        s = _out_as(sum_out, "sum_out", x)
+        sld = _rows(s, "sum_out")[2]
+    inv = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+    if hold and y_ckpt is True:
+        y_ckpt = ActCheckpoint._empty(x.shape, rows, cols, dev)
+    rc = _abi.load().ma_rms_norm_forward(
+        x.data_ptr(), ld, _ptr(residual), rld, dt, rows, cols, weight.data_ptr(), wdt, weight_offset, eps,
+        s.data_ptr() if residual is not None else None, sld, _ptr(y), yld, y_ckpt._pc if hold else None,
+        y_ckpt._pe if hold else None, inv.data_ptr(), _raw_stream(dev.index))
+    if rc:
+        _fail(rc, "ma_rms_norm_forward")
+    return y, s, inv, (y_ckpt if hold else None)
+
+
+def ma_rms_norm_backward_workspace_size(rows: int, cols: int) -> int:
+    n = C.c_size_t()
+    rc = _abi.load().ma_rms_norm_backward_workspace_size(rows, cols, C.byref(n))
+    if rc:
+        _fail(rc, "ma_rms_norm_backward_workspace_size")
+    return n.value
+
+
+def ma_rms_norm_backward(dy, s, inv_rms, weight, dsum=None, weight_offset: float = 0.0, ds=None, dweight=None,
+                         accumulate: bool = False, grad_dtype=torch.float32, workspace=None, stream=None):
+    """(ds, dweight) from the gradient dy of y and the forward pass' s and inv_rms.  dsum is the gradient
+    that reaches s past the norm, and is added to ds, which is the gradient of x and of the
+    residual alike.  dweight is allocated in `grad_dtype` where none is passed; with accumulate the sum is
+    added to it; dweight=False leaves it out (and returns None for it)."""
+    _check_cuda(dy, "dy")
+    _check_cuda(s, "s")
+    _same_type(s, "s", dy, "dy")
+    dt = _dtype(dy, "dy")
+    rows, cols, ld = _rows(dy, "dy")
+    sld = _rows(s, "s")[2]
+    _vector(weight, "weight", cols)
+    wdt = _dtype(weight, "weight")
+    _per_row(inv_rms, "inv_rms", dy.shape[:-1])
+    rld = 0
+    if dsum is not None:
+        _check_cuda(dsum, "dsum")
+        _same_type(dsum, "dsum", dy, "dy")
+        rld = _rows(dsum, "dsum")[2]
+    dev = dy.device
+    if accumulate and (dweight is None or dweight is False):
+        raise ValueError("accumulate needs the gradient to add to (dweight)")
+    given = None if dweight is False else dweight
+    _same_device(dev, ("s", s), ("inv_rms", inv_rms), ("weight", weight), ("dsum", dsum), ("ds", ds),
+                 ("dweight", given))
+    _check_workspace(workspace, dev)
+    if _elsewhere(dev, stream):
+        with _At(dev, stream, (dy, s, inv_rms, weight, dsum, ds, given, workspace)):
+            return ma_rms_norm_backward(dy, s, inv_rms, weight, dsum, weight_offset, ds, dweight, accumulate,
+                                        grad_dtype, workspace)
+    ds = _out_as(ds, "ds", dy)
+    ws_ptr, ws_bytes, gdt = None, 0, 0
+    dw = None
+    if dweight is not False:
+        dw = _out_like(dweight, "dweight", (cols,), grad_dtype, dev)
+        if not dw.is_contiguous():
+            raise ValueError("dweight must be contiguous")
+        gdt = _dtype(dw, "dweight")
+        ws, ws_ptr, ws_bytes = _workspace(workspace, ma_rms_norm_backward_workspace_size(rows, cols), dev)
+    rc = _abi.load().ma_rms_norm_backward(
+        dy.data_ptr(), ld, s.data_ptr(), sld, _ptr(dsum), rld, dt, rows, cols, inv_rms.data_ptr(),
+        weight.data_ptr(), wdt, weight_offset, ds.data_ptr(), _rows(ds, "ds")[2], _ptr(dw), gdt,
+        1 if accumulate else 0, ws_ptr, ws_bytes, _raw_stream(dev.index))
+    if rc:
+        _fail(rc, "ma_rms_norm_backward")
+    return ds, dw
+
+
+# ------------------------------------------------------------------- rotary --
+
+def _heads(x, what: str):
+    """(tokens, heads, features, token stride, head stride) of (..., heads, features)."""
+    if x.dim() < 2:
+        raise ValueError("%s must be (..., heads, features)" % what)
+    heads, dim = x.shape[-2:]
+    if dim > 1 and x.stride(-1) != 1 and x.numel():
+        raise ValueError("the last dimension of %s must be contiguous" % what)
+    tokens, stride, run = 1, heads * dim, None
+    for d, st in zip(reversed(x.shape[:-2]), reversed(x.stride()[:-2])):
+        tokens *= d
+        if d == 1:
+            continue
+        if run is None:
+            stride = st
+        elif st != run:
+            raise ValueError("the tokens of %s are not evenly spaced" % what)
+        run = d * st
+    return tokens, heads, dim, stride, (x.stride(-2) if heads > 1 else dim)
+
+
+class Rotary:
+    """How heads turn with positions: `sections` feature pairs for each axis (one number: a single axis),
+    of which pair i of all turns at theta^(-i / pairs) radians per position, or with `restart` the j-th
+    pair of an axis with n at theta^(-j / n).  `order` is 'blocks' (the axes' pairs one axis after the
+    other) or 'cycled' (the axes in turn, without those that are used up), `layout` 'half' (pair i is
+    features i and pairs + i) or 'pairs' (features 2 i and 2 i + 1)."""
+
+    __slots__ = ("sections", "pairs", "axes", "theta", "layout", "order", "restart", "_freq", "_axis", "_layout")
+
+    def __init__(self, sections, theta: float = 10000.0, layout: str = "half", order: str = "blocks",
+                 restart: bool = False):
+        sections = (int(sections),) if isinstance(sections, int) else tuple(int(n) for n in sections)
+        if layout not in _LAYOUTS:
+            raise ValueError("layout must be one of %s" % ", ".join(sorted(_LAYOUTS)))
+        if order not in _ORDERS:
+            raise ValueError("order must be one of %s" % ", ".join(sorted(_ORDERS)))
+        self.sections, self.axes, self.pairs = sections, len(sections), sum(sections)
+        self.theta, self.layout, self.order, self.restart = float(theta), layout, order, bool(restart)
+        n = max(1, self.pairs)
+        self._freq, self._axis, self._layout = (C.c_double * n)(), (C.c_uint8 * n)(), _LAYOUTS[layout]
+        rc = _abi.load().ma_rotary_frequencies((C.c_int32 * max(1, self.axes))(*sections), self.axes, self.theta,
+                                               _ORDERS[order], int(self.restart), self._freq, self._axis)
+        if rc:
+            _fail(rc, "Rotary")
+
+    def __reduce__(self):
+        return Rotary, (self.sections, self.theta, self.layout, self.order, self.restart)
+
+    @property
+    def frequencies(self):
+        """Radians per position of each pair."""
+        return tuple(self._freq)
+
+    @property
+    def pair_axis(self):
+        """The axis of each pair."""
+        return tuple(self._axis)
+
+
+def ma_rotary(x, positions, rotary: Rotary, inverse: bool = False, out=None, stream=None):
+    """x (..., heads, features) with every head's pairs turned by their token's positions: int32 or int64,
+    of shape (axes, ...) or, for a single axis, (...).  Features past the pairs are copied.  With inverse
+    they turn back: the gradient of x from the gradient of the result.  `out` may be x itself."""
+    _check_cuda(x, "x")
+    _check_cuda(positions, "positions")
+    if not isinstance(rotary, Rotary):
+        raise TypeError("rotary must be a Rotary")
+    dt = _dtype(x, "x")
+    tokens, heads, dim, tok, head = _heads(x, "x")
+    if positions.dtype not in (torch.int64, torch.int32):
+        raise TypeError("positions must be int32 or int64 (got %s)" % positions.dtype)
+    lead = tuple(x.shape[:-2])
+    shape = tuple(positions.shape)
+    if shape != (rotary.axes, *lead) and not (rotary.axes == 1 and shape == lead):
+        raise ValueError("positions %s do not belong to x %s and %d axes" % (shape, tuple(x.shape), rotary.axes))
+    axis = 0
+    if shape == (rotary.axes, *lead):
+        axis = positions.stride(0) if rotary.axes > 1 else 0
+        if not positions[0].is_contiguous():
+            raise ValueError("the positions of an axis must be contiguous")
+    elif not positions.is_contiguous():
+        raise ValueError("positions must be contiguous")
+    dev = x.device
+    _same_device(dev, ("positions", positions), ("out", out))
+    if _elsewhere(dev, stream):
+        with _At(dev, stream, (x, positions, out)):
+            return ma_rotary(x, positions, rotary, inverse, out)
+    out = _out_as(out, "out", x)
+    _, _, _, otok, ohead = _heads(out, "out")
+    rc = _abi.load().ma_rotary(x.data_ptr(), dt, tokens, heads, dim, tok, head, positions.data_ptr(),
+                               positions.element_size(), rotary.axes, axis, rotary._freq, rotary._axis,
+                               rotary.pairs, rotary._layout, 1 if inverse else 0, out.data_ptr(), otok, ohead,
+                               _raw_stream(dev.index))
+    if rc:
+        _fail(rc, "ma_rotary")
+    return out

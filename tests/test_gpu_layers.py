@@ -1,0 +1,242 @@
+"""The layer operators (include/ma_layers.h) on the GPU against float64
+references: norm and rotary positions, forward and backward, at the sizes, types,
+strides and values where each can go wrong."""
+
+import numpy as np
+import pytest
+
+from tests import _grads_ref as G
+from tests import _layers_ref as R
+from tests.test_gpu_grads import DT, _close, _dev, _f64, _strided
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+M = pytest.importorskip("muon_newton_schulz_02_amd")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    M.load_library()
+    yield
+    torch.cuda.synchronize()
+
+
+def _stream(rng, rows, cols):
+    x = rng.standard_normal((rows, cols)) * np.exp(0.7 * rng.standard_normal(cols))
+    if rows > 2:
+        x[1] = 0.0
+    return x
+
+
+# --------------------------------------------------------------------- norm --
+
+NORM_SHAPES = [(1, 1, 0), (1, 7, 0), (5, 32, 0), (70, 64, 0), (33, 100, 3), (16, 128, 8), (17, 129, 0), (9, 256, 0),
+               (3, 257, 1), (50, 1000, 0), (50, 1024, 0), (6, 1025, 0), (5, 2048, 8), (4, 2049, 0), (3, 4096, 0),
+               (3, 4104, 0), (2, 8192, 0), (3, 8200, 0), (2, 16384, 0), (1, 16001, 1)]
+
+
+@pytest.mark.parametrize("kind,wkind", [("fp32", "fp32"), ("bf16", "fp32"), ("bf16", "bf16"), ("fp32", "bf16")])
+@pytest.mark.parametrize("rows,cols,pad", NORM_SHAPES)
+def test_norm_forward(kind, wkind, rows, cols, pad):
+    rng = np.random.default_rng(rows * 131 + cols)
+    x, _ = _strided(_stream(rng, rows, cols), pad, kind)
+    res, _ = _strided(_stream(rng, rows, cols), 2 * pad, kind)
+    w = _dev(1 + 0.3 * rng.standard_normal(cols), wkind)
+    for off, r in ((0.0, None), (0.0, res), (1.0, res)):
+        y, s, inv, c = M.ma_rms_norm_forward(x, w, r, eps=1e-5, weight_offset=off, y_ckpt=True)
+        yy, ss, ii, dy, ds, di = R.rms_norm(_f64(x), _f64(w), None if r is None else _f64(r), 1e-5, off)
+        _close(y, yy, R.rounded(yy, dy, kind), "y")
+        assert (s is x) if r is None else True
+        _close(s, ss, R.rounded(ss, ds, kind), "s")
+        _close(inv, ii, di, "inv")
+        # what is held is y as it is stored, byte for byte
+        p = M.ma_act_pack(y)
+        assert torch.equal(p.codes, c.codes)
+        groups = c.codes.shape[1] // 32
+        assert torch.equal(p.exps[:, :groups], c.exps[:, :groups])
+        again = M.ma_rms_norm_forward(x, w, r, eps=1e-5, weight_offset=off)
+        assert again[3] is None and torch.equal(again[0], y) and torch.equal(again[2], inv)
+        none, _, _, only = M.ma_rms_norm_forward(x, w, r, eps=1e-5, weight_offset=off, out=False, y_ckpt=True)
+        assert none is None and torch.equal(only.codes, c.codes)
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+def test_norm_forward_into_strided_outputs(kind):
+    rng = np.random.default_rng(4)
+    x, r = _dev(_stream(rng, 37, 200), kind), _dev(_stream(rng, 37, 200), kind)
+    w = _dev(rng.standard_normal(200))
+    y, s, _, c = M.ma_rms_norm_forward(x, w, r, y_ckpt=True)
+    y2, yw = _strided(np.zeros((37, 200)), 5, kind)
+    s2, sw = _strided(np.zeros((37, 200)), 8, kind)
+    held = M.ActCheckpoint.empty((37, 200), "cuda")
+    got = M.ma_rms_norm_forward(x, w, r, out=y2, sum_out=s2, y_ckpt=held)
+    assert got[0] is y2 and got[1] is s2 and got[3] is held
+    assert torch.equal(y2, y) and torch.equal(s2, s) and torch.equal(held.codes, c.codes)
+    assert torch.all(yw[:, 200:] == 7.0) and torch.all(sw[:, 200:] == 7.0)
+    # a row alone, and a row repeated
+    one = M.ma_rms_norm_forward(x[3], w, r[3])
+    assert torch.equal(one[0], y[3]) and one[2].shape == ()
+    rep = M.ma_rms_norm_forward(x[3].expand(5, 200), w, r[3].expand(5, 200))
+    assert torch.equal(rep[0], y[3].expand(5, 200))
+    none = M.ma_rms_norm_forward(x[:0], w, r[:0], y_ckpt=True)
+    assert none[0].shape == (0, 200) and none[3].rows == 0
+
+
+@pytest.mark.parametrize("cols", [96, 1000, 5000])
+def test_norm_extremes(cols):
+    """Rows of zeros, tiny values, values whose squares leave float32, an infinity, a NaN."""
+    x = np.ones((8, cols), np.float32)
+    x[0] = 0
+    x[1] = 1e-30
+    x[2] = 1e30
+    x[3] = -3e38
+    x[4, ::2], x[4, 1::2] = 2e25, 3e19
+    x[5, 3] = np.inf
+    x[6, 5] = np.nan
+    w = _dev(np.ones(cols))
+    y, _, inv, c = M.ma_rms_norm_forward(torch.from_numpy(x).cuda(), w, eps=1e-6, y_ckpt=True)
+    yy, _, ii, dy, _, di = R.rms_norm(x[:5].astype(np.float64), np.ones(cols), None, 1e-6, 0.0)
+    # (an inverse below 2^-126 keeps fewer bits: 2^-149 apart)
+    _close(inv[:5], ii, di + 2.0 ** -149)
+    _close(y[:5], yy, dy + np.abs(x[:5]) * 2.0 ** -149 + G.TINY)
+    assert inv[5] == 0 and torch.isnan(y[5, 3]) and torch.all(y[5, 4:] == 0)
+    assert torch.isnan(y[6]).all() and torch.isnan(inv[6])
+    assert torch.all(c.exps[6, :(cols + 31) // 32] == 255)
+    assert torch.equal(M.ma_act_pack(y).codes, c.codes)
+    # the gradient at such rows is finite and near the formula's
+    d = np.ones((5, cols), np.float32)
+    d[:, ::3] = -1
+    ds, dw = M.ma_rms_norm_backward(torch.from_numpy(d).cuda(), torch.from_numpy(x[:5]).cuda(), inv[:5].contiguous(), w)
+    want, dwant, tol, wtol = R.rms_norm_backward(d.astype(np.float64), x[:5].astype(np.float64), _f64(inv[:5]),
+                                                 np.ones(cols))
+    _close(ds, want, tol + 2.0 ** -140)
+    _close(dw, dwant, wtol + G.TINY)
+
+
+@pytest.mark.parametrize("kind,wkind,gkind", [("fp32", "fp32", "fp32"), ("bf16", "fp32", "fp32"),
+                                              ("bf16", "bf16", "bf16")])
+@pytest.mark.parametrize("rows,cols,pad", NORM_SHAPES + [(3000, 72, 0), (4000, 256, 0), (900, 2048, 0), (1601, 301, 0)])
+def test_norm_backward(kind, wkind, gkind, rows, cols, pad):
+    rng = np.random.default_rng(rows * 17 + cols)
+    s, _ = _strided(_stream(rng, rows, cols), pad, kind)
+    dy, _ = _strided(rng.standard_normal((rows, cols)), pad, kind)
+    dsum, _ = _strided(rng.standard_normal((rows, cols)), 0, kind)
+    w = _dev(rng.standard_normal(cols), wkind)
+    inv = M.ma_rms_norm_forward(s, w, eps=1e-5)[2]
+    for off, add in ((0.0, None), (1.0, dsum)):
+        ds, dw = M.ma_rms_norm_backward(dy, s, inv, w, add, weight_offset=off, grad_dtype=DT[gkind])
+        want, dwant, tol, wtol = R.rms_norm_backward(_f64(dy), _f64(s), _f64(inv), _f64(w), off,
+                                                     None if add is None else _f64(add))
+        _close(ds, want, R.rounded(want, tol, kind), "ds")
+        _close(dw, dwant, R.rounded(dwant, wtol, gkind), "dw")
+        # reruns are bitwise equal, whatever the workspace held; without a weight gradient too
+        ws = torch.full((M.ma_rms_norm_backward_workspace_size(rows, cols),), 255, dtype=torch.uint8, device="cuda")
+        ds2, dw2 = M.ma_rms_norm_backward(dy, s, inv, w, add, weight_offset=off, workspace=ws, grad_dtype=DT[gkind])
+        assert torch.equal(ds, ds2) and torch.equal(dw, dw2)
+        ds3, none = M.ma_rms_norm_backward(dy, s, inv, w, add, weight_offset=off, dweight=False)
+        assert none is None and torch.equal(ds, ds3)
+        old = _dev(rng.standard_normal(cols), gkind)
+        acc = old.clone()
+        M.ma_rms_norm_backward(dy, s, inv, w, add, weight_offset=off, dweight=acc, accumulate=True)
+        _, dwant, _, wtol = R.rms_norm_backward(_f64(dy), _f64(s), _f64(inv), _f64(w), off, None, _f64(old))
+        _close(acc, dwant, R.rounded(dwant, wtol, gkind), "dw added to")
+
+
+def test_norm_backward_of_no_rows():
+    w = torch.ones(40, device="cuda")
+    e = torch.zeros((0, 40), device="cuda")
+    i = torch.zeros(0, device="cuda")
+    ds, dw = M.ma_rms_norm_backward(e, e, i, w)
+    assert ds.shape == (0, 40) and torch.all(dw == 0)
+    acc = torch.full((40,), 3.0, device="cuda")
+    M.ma_rms_norm_backward(e, e, i, w, dweight=acc, accumulate=True)
+    assert torch.all(acc == 3)
+
+
+def test_norm_gradient_against_differences():
+    """f(x, w) = sum(c y): its slope along a random direction, by central differences of the
+    reference in 64 bits."""
+    rng = np.random.default_rng(11)
+    x, w, c = rng.standard_normal((7, 90)), rng.standard_normal(90), rng.standard_normal((7, 90))
+    y, s, inv, _ = M.ma_rms_norm_forward(_dev(x), _dev(w), eps=1e-5)
+    ds, dw = M.ma_rms_norm_backward(_dev(c), s, inv, _dev(w))
+    f = lambda a, b: np.sum(c * R.rms_norm(a, b, None, 1e-5)[0])
+    for seed in range(4):
+        u, v = np.random.default_rng(seed).standard_normal((7, 90)), np.random.default_rng(seed + 9).standard_normal(90)
+        h = 1e-5
+        slope = (f(x + h * u, w + h * v) - f(x - h * u, w - h * v)) / (2 * h)
+        got = np.sum(_f64(ds) * u) + np.sum(_f64(dw) * v)
+        # float32 inputs and gradients: 630 terms of magnitude about 1, each off by some 2^-22
+        assert abs(got - slope) < 1e-3 * max(1, abs(slope))
+
+
+# ------------------------------------------------------------------- rotary --
+
+PLANS = [((64,), "half", "blocks", False), ((16, 24, 24), "half", "blocks", False), ((16, 24, 24), "pairs", "cycled", False),
+         ((18, 18), "half", "blocks", True), ((18, 18), "pairs", "blocks", True), ((5, 0, 3), "half", "cycled", True),
+         ((1,), "half", "blocks", False), ((128,), "half", "blocks", False), ((3, 5, 2, 1), "pairs", "cycled", False)]
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("sections,layout,order,restart", PLANS)
+@pytest.mark.parametrize("tokens,heads,rest", [(1, 1, 0), (37, 5, 0), (130, 3, 8), (700, 2, 7)])
+def test_rotary(kind, sections, layout, order, restart, tokens, heads, rest):
+    rng = np.random.default_rng(tokens + sum(sections))
+    dim, axes = 2 * sum(sections) + rest, len(sections)
+    plan = M.Rotary(sections, theta=10000.0, layout=layout, order=order, restart=restart)
+    table = R.rotary_table(sections, 10000.0, order, restart)
+    assert plan.pair_axis == tuple(a for a, _ in table)
+    assert np.allclose(plan.frequencies, [f for _, f in table], rtol=1e-14, atol=0)
+    x = _dev(rng.standard_normal((tokens, heads, dim)), kind)
+    pos = rng.integers(-50, 1 << 20, (axes, tokens))
+    for ptype in (torch.int64, torch.int32):
+        p = torch.from_numpy(pos).to("cuda", ptype)
+        for inverse in (False, True):
+            got = M.ma_rotary(x, p if axes > 1 else p[0], plan, inverse=inverse)
+            want, tol = R.rotary(_f64(x), pos, table, layout, inverse)
+            _close(got, want, R.rounded(want, tol, kind))
+            assert torch.equal(got[..., 2 * plan.pairs:], x[..., 2 * plan.pairs:])
+    # in place, and in a part of a wider array whose other heads stay
+    wide = torch.full((tokens, heads + 2, dim + 3), 7.0, dtype=DT[kind], device="cuda")
+    part = wide[:, 1:1 + heads, :dim]
+    part.copy_(x)
+    assert M.ma_rotary(part, p, plan, inverse=True, out=part) is part
+    assert torch.equal(part, got)
+    assert torch.all(wide[:, 0] == 7) and torch.all(wide[:, -1] == 7) and torch.all(wide[:, :, dim:] == 7)
+    # heads outside, tokens inside
+    turned = torch.empty((heads, tokens, dim), dtype=DT[kind], device="cuda").transpose(0, 1)
+    M.ma_rotary(x, p, plan, inverse=True, out=turned)
+    assert torch.equal(turned, got)
+
+
+def test_rotary_far_positions_and_back():
+    plan = M.Rotary((16, 24, 24))
+    x = torch.randn(500, 4, 128, device="cuda")
+    pos = torch.randint(0, 1 << 31, (3, 500), device="cuda")
+    got = M.ma_rotary(x, pos, plan)
+    want, tol = R.rotary(_f64(x), pos.cpu().numpy(), R.rotary_table((16, 24, 24), 10000.0, "blocks", False), "half")
+    _close(got, want, R.rounded(want, tol, "fp32"))
+    back = M.ma_rotary(got, pos, plan, inverse=True)
+    # two turns, each off by its bound on values of at most |u| + |v|
+    assert (back - x).abs().max() < 1e-5
+    # a turn keeps the product of a pair of vectors: <R g, R x> = <g, x>, so the inverse is the gradient
+    g = torch.randn_like(x)
+    a = (g.double() * got.double()).sum()
+    b = (M.ma_rotary(g, pos, plan, inverse=True).double() * x.double()).sum()
+    assert abs(a - b) < 1e-3 * x.numel() ** 0.5
+
+
+def test_rotary_shapes_and_empty():
+    plan = M.Rotary(8)
+    x = torch.randn(2, 9, 3, 16, device="cuda")
+    pos = torch.arange(18, device="cuda").view(2, 9)
+    flat = M.ma_rotary(x.view(18, 3, 16), pos.view(18), plan)
+    assert torch.equal(M.ma_rotary(x, pos, plan).view(18, 3, 16), flat)
+    assert torch.equal(M.ma_rotary(x, pos[None], plan).view(18, 3, 16), flat)
+    assert M.ma_rotary(x[:0], pos[:0], plan).shape == (0, 9, 3, 16)
+    one = M.ma_rotary(x[0, 4], pos[0, 4], plan)
+    assert torch.equal(one, flat[4])
+    assert torch.equal(M.ma_rotary(x, torch.zeros_like(pos), plan), x)
