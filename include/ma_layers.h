@@ -26,7 +26,7 @@ extern "C" {
 /* ---- root-mean-square norm ------------------------------------------------- */
 
 /* Most columns of a norm: a row is kept in one workgroup's registers. */
-#define MA_NORM_MAX_COLS 16384
+#define MA_NORM_MAX_COLS 8192
 
 /* For every row: s = x + residual, inv_rms = 1 / sqrt(mean(s^2) + eps) and
  * y = s * inv_rms * (weight + weight_offset).

@@ -29,7 +29,7 @@ MA_PARAM_FP32, MA_PARAM_BF16 = 0, 1
 MA_MAX_NDIM = 8
 MA_ACT_GROUP = 32
 MA_ACT_SILU, MA_ACT_GELU_TANH = 0, 1
-MA_NORM_MAX_COLS = 16384
+MA_NORM_MAX_COLS = 8192
 MA_ROTARY_MAX_PAIRS, MA_ROTARY_MAX_AXES = 256, 4
 MA_ROTARY_HALF, MA_ROTARY_PAIRS = 0, 1
 MA_ROTARY_BLOCKS, MA_ROTARY_CYCLED = 0, 1
