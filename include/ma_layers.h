@@ -6,6 +6,8 @@
  *   ma_rms_norm_forward     s = x + residual, y = norm(s) (w + offset), y held in 8 bits
  *   ma_rms_norm_backward    ds and dw (+)= from dy, s and the saved 1 / rms
  *   ma_rotary               feature pairs turned by positions of several axes, and back
+ *   ma_token_logprob_forward    log probabilities of given tokens, entropies, top alternatives
+ *   ma_token_logprob_backward   the gradient of the logits
  *
  * Conventions are those of ma_grads.h: return codes and messages, checks
  * before any launch, caller-owned memory, the caller's HIP stream, capturable,
@@ -102,6 +104,47 @@ int ma_rotary(const void* x, int32_t dtype, int64_t n_tokens, int64_t heads, int
               const double* frequencies, const uint8_t* pair_axis, int64_t pairs, int32_t layout,
               int32_t inverse, void* out, int64_t out_token_stride, int64_t out_head_stride,
               void* stream);
+
+/* ---- log probabilities of tokens ---------------------------------------------- */
+
+#define MA_LOGPROB_MAX_TOP 64
+
+/* Bytes of workspace (256-byte aligned; 0: none, NULL may be passed) a forward call
+ * needs.  Errors: INVALID_ARG (null), SHAPE. */
+int ma_token_logprob_workspace_size(int64_t n_tokens, int64_t vocab, int32_t top, size_t* bytes);
+
+/* For every row of logits (n_tokens x vocab), with z = scale * logits[t], scale > 0:
+ *   lse[t]      = ln sum exp z
+ *   logprob[t]  = z[tokens[t]] - lse[t]   (a token outside [0, vocab) selects none: 0)
+ *   entropy[t]  = -sum p ln p, p = exp(z - lse[t])
+ *   top_ids[t][j], top_logprobs[t][j], j < top: the ids of the highest logits, falling,
+ *                 of equal ones the lowest id first, and their z - lse[t]
+ * tokens and top_ids are signed integers of token_bytes (4 or 8); the results are
+ * float32 and contiguous.  logprob (with tokens) and entropy may be NULL, and with
+ * top = 0 top_ids and top_logprobs.  An entry of -infinity has no probability; a row of
+ * nothing else has lse and log probabilities of -infinity and entropy 0.  A row with a
+ * NaN or +infinity gives NaN, and its top ids are some distinct ids.  0 <= top <=
+ * min(MA_LOGPROB_MAX_TOP, vocab).  n_tokens may be 0.  Errors: INVALID_ARG, SHAPE,
+ * WORKSPACE, HIP. */
+int ma_token_logprob_forward(const void* logits, int32_t dtype, int64_t n_tokens, int64_t vocab,
+                             int64_t stride, const void* tokens, int32_t token_bytes, double scale,
+                             float* logprob, float* entropy, float* lse, int32_t top,
+                             void* top_ids, float* top_logprobs, void* workspace, size_t ws_bytes,
+                             void* stream);
+
+/* With p = exp(z - lse[t]), the gradient of sum_t dlogprob[t] * logprob[t] +
+ * dentropy[t] * entropy[t] in the logits:
+ *   dlogits[t][v] = scale * (dlogprob[t] * ([v = tokens[t]] - p[v])
+ *                            - dentropy[t] * p[v] * (ln p[v] + entropy[t]))
+ * A token outside [0, vocab) takes dlogprob as 0.  lse and entropy are the forward pass';
+ * dentropy (with entropy) may be NULL.  A row of nothing but -infinity has gradient 0.
+ * dlogits may be logits itself, with its type and stride.  n_tokens may be 0.
+ * Errors: INVALID_ARG, SHAPE, HIP. */
+int ma_token_logprob_backward(const void* logits, int32_t dtype, int64_t n_tokens, int64_t vocab,
+                              int64_t stride, const void* tokens, int32_t token_bytes,
+                              double scale, const float* lse, const float* entropy,
+                              const float* dlogprob, const float* dentropy, void* dlogits,
+                              int32_t dlogits_dtype, int64_t dlogits_stride, void* stream);
 
 #ifdef __cplusplus
 }

@@ -30,6 +30,7 @@ MA_MAX_NDIM = 8
 MA_ACT_GROUP = 32
 MA_ACT_SILU, MA_ACT_GELU_TANH = 0, 1
 MA_NORM_MAX_COLS = 8192
+MA_LOGPROB_MAX_TOP = 64
 MA_ROTARY_MAX_PAIRS, MA_ROTARY_MAX_AXES = 256, 4
 MA_ROTARY_HALF, MA_ROTARY_PAIRS = 0, 1
 MA_ROTARY_BLOCKS, MA_ROTARY_CYCLED = 0, 1
@@ -133,6 +134,11 @@ LAYER_SIGNATURES = [
     ("ma_rotary_frequencies", C.c_int, [_P, _I32, _F64, _I32, _I32, _P, _P]),
     ("ma_rotary", C.c_int, [_P, _I32, _I64, _I64, _I64, _I64, _I64, _P, _I32, _I32, _I64, _P, _P, _I64, _I32,
                             _I32, _P, _I64, _I64, _P]),
+    ("ma_token_logprob_workspace_size", C.c_int, [_I64, _I64, _I32, C.POINTER(_SZ)]),
+    ("ma_token_logprob_forward", C.c_int, [_P, _I32, _I64, _I64, _I64, _P, _I32, _F64, _P, _P, _P, _I32, _P, _P,
+                                           _P, _SZ, _P]),
+    ("ma_token_logprob_backward", C.c_int, [_P, _I32, _I64, _I64, _I64, _P, _I32, _F64, _P, _P, _P, _P, _P, _I32,
+                                            _I64, _P]),
 ]
 
 _lib = None

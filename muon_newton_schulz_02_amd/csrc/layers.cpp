@@ -72,6 +72,42 @@ int64_t norm_ws_bytes(int64_t rows, int64_t cols) {
     return round_up(norm_backward_groups(rows, cols) * cols * 4, 256);
 }
 
+int check_logprob(const char* fn, int32_t dtype, int64_t n_tokens, int64_t vocab, int64_t stride,
+                  int32_t token_bytes, double scale) {
+    TRY(check_dtype(fn, "logits", dtype));
+    TRY(check_size(fn, "n_tokens", n_tokens, 0, kMaxCount));
+    TRY(check_size(fn, "vocab", vocab, 1, kMaxCount));
+    TRY(check_elems(fn, "logits", n_tokens, vocab));
+    TRY(check_stride(fn, "logits", stride, 0, n_tokens));
+    TRY(check_tokens(fn, token_bytes));
+    if (!(scale >= 0x1p-100) || !std::isfinite((float)scale)) {
+        set_error("%s: scale must be a positive float32, at least 2^-100", fn);
+        return MA_ERR_INVALID_ARG;
+    }
+    return MA_OK;
+}
+
+// Elements of a row's piece: whole units of 8.
+int64_t logprob_piece(int64_t rows, int64_t vocab) {
+    return round_up(ceil_div(vocab, logprob_pieces(rows, vocab)), 8);
+}
+
+struct LogprobSpace {
+    size_t sums = 0, keys = 0, total = 0;
+};
+LogprobSpace logprob_space(int64_t rows, int64_t vocab, int64_t top) {
+    LogprobSpace s;
+    const int64_t pieces = ceil_div(vocab, logprob_piece(rows, vocab));
+    if (pieces == 1 || rows == 0) return s;
+    s.keys = (size_t)round_up(rows * pieces * 16, 256);
+    s.total = s.keys + (size_t)round_up(rows * pieces * top * 8, 256);
+    return s;
+}
+
+int check_top(const char* fn, int32_t top, int64_t vocab) {
+    return check_size(fn, "top", top, 0, vocab < MA_LOGPROB_MAX_TOP ? vocab : MA_LOGPROB_MAX_TOP);
+}
+
 }  // namespace
 
 extern "C" {
@@ -304,6 +340,98 @@ int ma_rotary(const void* x, int32_t dtype, int64_t n_tokens, int64_t heads, int
     a.position_bytes = position_bytes;
     a.dtype = dtype;
     return done(fn, launch_rotary(a, tab, stream));
+}
+
+int ma_token_logprob_workspace_size(int64_t n_tokens, int64_t vocab, int32_t top, size_t* bytes) {
+    const char* fn = "ma_token_logprob_workspace_size";
+    if (!bytes) {
+        set_error("%s: NULL argument", fn);
+        return MA_ERR_INVALID_ARG;
+    }
+    TRY(check_size(fn, "n_tokens", n_tokens, 0, kMaxCount));
+    TRY(check_size(fn, "vocab", vocab, 1, kMaxCount));
+    TRY(check_top(fn, top, vocab));
+    *bytes = logprob_space(n_tokens, vocab, top).total;
+    clear_error();
+    return MA_OK;
+}
+
+int ma_token_logprob_forward(const void* logits, int32_t dtype, int64_t n_tokens, int64_t vocab,
+                             int64_t stride, const void* tokens, int32_t token_bytes, double scale,
+                             float* logprob, float* entropy, float* lse, int32_t top,
+                             void* top_ids, float* top_logprobs, void* workspace, size_t ws_bytes,
+                             void* stream) {
+    const char* fn = "ma_token_logprob_forward";
+    TRY(check_logprob(fn, dtype, n_tokens, vocab, stride, token_bytes, scale));
+    TRY(check_top(fn, top, vocab));
+    if (n_tokens > 0) TRY(check_pair(fn, "tokens", tokens, "logprob", logprob));
+    const LogprobSpace sp = logprob_space(n_tokens, vocab, top);
+    TRY(check_workspace(fn, workspace, ws_bytes, sp.total));
+    const int64_t n4 = n_tokens * 4;
+    TRY(check_spans(fn, {matrix("logits", logits, dtype, n_tokens, vocab, stride, false),
+                         flat("tokens", tokens, tokens ? n_tokens * token_bytes : 0, (size_t)token_bytes, false),
+                         flat("logprob", logprob, logprob ? n4 : 0, 4, true),
+                         flat("entropy", entropy, entropy ? n4 : 0, 4, true), flat("lse", lse, n4, 4, true),
+                         flat("top_ids", top_ids, n_tokens * top * token_bytes, (size_t)token_bytes, true),
+                         flat("top_logprobs", top_logprobs, n4 * top, 4, true),
+                         flat("workspace", workspace, (int64_t)sp.total, 1, true)}));
+    LogprobArgs a{};
+    a.logits = logits;
+    a.tokens = tokens;
+    a.logprob = logprob;
+    a.entropy = entropy;
+    a.lse = lse;
+    a.top_ids = top_ids;
+    a.top_logprobs = top_logprobs;
+    a.sums = static_cast<float*>(workspace);
+    a.keys = reinterpret_cast<uint64_t*>(static_cast<char*>(workspace) + sp.keys);
+    a.rows = n_tokens;
+    a.vocab = vocab;
+    a.stride = stride;
+    a.piece = logprob_piece(n_tokens, vocab);
+    a.scale = (float)scale;
+    a.top = top;
+    a.token_bytes = token_bytes;
+    a.dtype = dtype;
+    return done(fn, launch_logprob_forward(a, stream));
+}
+
+int ma_token_logprob_backward(const void* logits, int32_t dtype, int64_t n_tokens, int64_t vocab,
+                              int64_t stride, const void* tokens, int32_t token_bytes,
+                              double scale, const float* lse, const float* entropy,
+                              const float* dlogprob, const float* dentropy, void* dlogits,
+                              int32_t dlogits_dtype, int64_t dlogits_stride, void* stream) {
+    const char* fn = "ma_token_logprob_backward";
+    TRY(check_logprob(fn, dtype, n_tokens, vocab, stride, token_bytes, scale));
+    TRY(check_dtype(fn, "dlogits", dlogits_dtype));
+    TRY(check_stride(fn, "dlogits", dlogits_stride, vocab, n_tokens));
+    if (n_tokens > 0) TRY(check_pair(fn, "entropy", entropy, "dentropy", dentropy));
+    const bool same = logits == dlogits && dtype == dlogits_dtype && stride == dlogits_stride;
+    const int64_t n4 = n_tokens * 4;
+    TRY(check_spans(fn, {matrix("logits", logits, dtype, same ? 0 : n_tokens, vocab, stride, false),
+                         flat("tokens", tokens, n_tokens * token_bytes, (size_t)token_bytes, false),
+                         flat("lse", lse, n4, 4, false), flat("entropy", entropy, entropy ? n4 : 0, 4, false),
+                         flat("dlogprob", dlogprob, n4, 4, false),
+                         flat("dentropy", dentropy, dentropy ? n4 : 0, 4, false),
+                         matrix("dlogits", dlogits, dlogits_dtype, n_tokens, vocab, dlogits_stride, true)}));
+    LogprobArgs a{};
+    a.logits = logits;
+    a.tokens = tokens;
+    a.lse = const_cast<float*>(lse);
+    a.ent = entropy;
+    a.dlogprob = dlogprob;
+    a.dentropy = dentropy;
+    a.dlogits = dlogits;
+    a.rows = n_tokens;
+    a.vocab = vocab;
+    a.stride = stride;
+    a.dstride = dlogits_stride;
+    a.piece = logprob_piece(n_tokens, vocab);
+    a.scale = (float)scale;
+    a.token_bytes = token_bytes;
+    a.dtype = dtype;
+    a.ddtype = dlogits_dtype;
+    return done(fn, launch_logprob_backward(a, stream));
 }
 
 }  // extern "C"

@@ -44,4 +44,22 @@ struct RotaryArgs {
 };
 int launch_rotary(const RotaryArgs& a, const RotaryTable& t, void* stream);
 
+// ------------------------------------------- token log probabilities --
+struct LogprobArgs {
+    const void *logits, *tokens;
+    float *logprob, *entropy, *lse;                // (backward: lse is read)
+    const float *ent, *dlogprob, *dentropy;
+    void *top_ids, *dlogits;
+    float* top_logprobs;
+    float* sums;                                   // of a row's pieces: m, s, t, unused
+    uint64_t* keys;                                // and their highest
+    int64_t rows, vocab, stride, dstride, piece;
+    float scale;
+    int32_t top, token_bytes, dtype, ddtype;
+};
+// Pieces a row is cut into.
+int64_t logprob_pieces(int64_t rows, int64_t vocab);
+int launch_logprob_forward(const LogprobArgs& a, void* stream);
+int launch_logprob_backward(const LogprobArgs& a, void* stream);
+
 }  // namespace ma

@@ -4,6 +4,8 @@ and backward passes are made of, beside those of `grads`.
     ma_rms_norm_forward, ma_rms_norm_backward     norm of a residual stream with the
                           addition that feeds it, the output also held in 8 bits
     ma_rotary             feature pairs turned by positions of several axes, and back
+    ma_token_logprob_forward, ma_token_logprob_backward     log probabilities of given
+                          tokens, entropies and top alternatives, and the logits' gradient
 
 Manners are those of `grads`: names and meanings are the C ABI's, outputs and
 workspaces are allocated as torch tensors where the caller passes none,
@@ -22,7 +24,7 @@ import torch
 from . import _abi
 from ._abi import MA_ROTARY_BLOCKS, MA_ROTARY_CYCLED, MA_ROTARY_HALF, MA_ROTARY_PAIRS
 from .grads import (ActCheckpoint, _At, _check_cuda, _check_workspace, _dtype, _elsewhere, _fail, _held, _out_as,
-                    _out_like, _raw_stream, _rows, _same_device, _workspace)
+                    _out_like, _raw_stream, _rows, _same_device, _token_bytes, _workspace)
 
 _LAYOUTS = {"half": MA_ROTARY_HALF, "pairs": MA_ROTARY_PAIRS}
 _ORDERS = {"blocks": MA_ROTARY_BLOCKS, "cycled": MA_ROTARY_CYCLED}
@@ -263,4 +265,89 @@ def ma_rotary(x, positions, rotary: Rotary, inverse: bool = False, out=None, str
                                _raw_stream(dev.index))
     if rc:
         _fail(rc, "ma_rotary")
+    return out
+
+
+# -------------------------------------------------- log probabilities of tokens --
+
+def _tokens_of(tokens, what: str, shape):
+    _check_cuda(tokens, what)
+    if tuple(tokens.shape) != tuple(shape):
+        raise ValueError("%s %s do not belong to rows %s" % (what, tuple(tokens.shape), tuple(shape)))
+    if not tokens.is_contiguous():
+        raise ValueError("%s must be contiguous" % what)
+    return _token_bytes(tokens)
+
+
+def ma_token_logprob_workspace_size(n_tokens: int, vocab: int, top: int = 0) -> int:
+    n = C.c_size_t()
+    rc = _abi.load().ma_token_logprob_workspace_size(n_tokens, vocab, top, C.byref(n))
+    if rc:
+        _fail(rc, "ma_token_logprob_workspace_size")
+    return n.value
+
+
+def ma_token_logprob_forward(logits, tokens, scale: float = 1.0, top: int = 0, workspace=None, stream=None):
+    """(logprob, entropy, lse, top_ids, top_logprobs) of softmax(scale * logits) over the last dimension, in
+    float32: the log probability of each row's token (0 for one outside [0, vocab)), the entropy, the log of the
+    sum that the backward pass takes, and the ids (in the tokens' type) and log probabilities of the `top`
+    highest, ties to the lowest id (None for top = 0)."""
+    _check_cuda(logits, "logits")
+    dt = _dtype(logits, "logits")
+    rows, vocab, ld = _rows(logits, "logits")
+    shape = logits.shape[:-1]
+    tb = _tokens_of(tokens, "tokens", shape)
+    dev = logits.device
+    _same_device(dev, ("tokens", tokens))
+    _check_workspace(workspace, dev)
+    if _elsewhere(dev, stream):
+        with _At(dev, stream, (logits, tokens, workspace)):
+            return ma_token_logprob_forward(logits, tokens, scale, top, workspace)
+    top = int(top)
+    need = ma_token_logprob_workspace_size(rows, vocab, top)
+    logprob = torch.empty(shape, dtype=torch.float32, device=dev)
+    entropy, lse = torch.empty_like(logprob), torch.empty_like(logprob)
+    ids = best = None
+    if top > 0:
+        ids = torch.empty((*shape, top), dtype=tokens.dtype, device=dev)
+        best = torch.empty((*shape, top), dtype=torch.float32, device=dev)
+    ws, ws_ptr, ws_bytes = _workspace(workspace, need, dev)
+    rc = _abi.load().ma_token_logprob_forward(
+        logits.data_ptr(), dt, rows, vocab, ld, tokens.data_ptr(), tb, scale, logprob.data_ptr(),
+        entropy.data_ptr(), lse.data_ptr(), top, _ptr(ids), _ptr(best), ws_ptr, ws_bytes, _raw_stream(dev.index))
+    if rc:
+        _fail(rc, "ma_token_logprob_forward")
+    return logprob, entropy, lse, ids, best
+
+
+def ma_token_logprob_backward(logits, tokens, lse, dlogprob, entropy=None, dentropy=None, scale: float = 1.0,
+                              out=None, grad_dtype=None, stream=None):
+    """The gradient of the logits from those of the log probabilities and (with the forward pass' entropy)
+    of the entropies.  It is allocated in `grad_dtype` (default: the logits') where no `out` is passed;
+    `out` may be the logits themselves."""
+    _check_cuda(logits, "logits")
+    dt = _dtype(logits, "logits")
+    rows, vocab, ld = _rows(logits, "logits")
+    shape = logits.shape[:-1]
+    tb = _tokens_of(tokens, "tokens", shape)
+    _per_row(lse, "lse", shape)
+    _per_row(dlogprob, "dlogprob", shape)
+    if (entropy is None) != (dentropy is None):
+        raise ValueError("entropy and dentropy go together")
+    if dentropy is not None:
+        _per_row(entropy, "entropy", shape)
+        _per_row(dentropy, "dentropy", shape)
+    dev = logits.device
+    _same_device(dev, ("tokens", tokens), ("lse", lse), ("dlogprob", dlogprob), ("entropy", entropy),
+                 ("dentropy", dentropy), ("out", out))
+    if _elsewhere(dev, stream):
+        with _At(dev, stream, (logits, tokens, lse, dlogprob, entropy, dentropy, out)):
+            return ma_token_logprob_backward(logits, tokens, lse, dlogprob, entropy, dentropy, scale, out, grad_dtype)
+    out = _out_like(out, "out", logits.shape, grad_dtype or logits.dtype, dev)
+    rc = _abi.load().ma_token_logprob_backward(
+        logits.data_ptr(), dt, rows, vocab, ld, tokens.data_ptr(), tb, scale, lse.data_ptr(), _ptr(entropy),
+        dlogprob.data_ptr(), _ptr(dentropy), out.data_ptr(), _dtype(out, "out"), _rows(out, "out")[2],
+        _raw_stream(dev.index))
+    if rc:
+        _fail(rc, "ma_token_logprob_backward")
     return out

@@ -82,3 +82,68 @@ def rotary(x, pos, table, layout, inverse=False):
 def rounded(v, tol, out):
     """tol widened by the rounding of v (+- tol) to the output type."""
     return tol + (np.abs(v) + tol) * U[out] + TINY
+
+
+def logprob(z, ids, scale, top=0):
+    """(logprob, entropy, lse, ids, top's logprobs, bounds of the five float results): rows of
+    z (tokens, vocab).
+
+    With u = (z - m) k, k = scale log2 e rounded, e = 2^u: u errs by 4 u' |u| (u' = 2^-24: the
+    difference, k, the product), so e by (3 |u| + 2) u' of itself (2^x's own error is one step),
+    and a sum of n terms in pieces by at most n / 8 + 40 roundings more (threads take at least 8
+    elements each in turn; short rows fewer).  The absolute error of ln s is that relative error
+    averaged with weights p, of t / s the same with |u| more.  lse and the products with scale
+    add a few u' of their magnitudes."""
+    n, v = z.shape
+    zs = z * scale
+    m = np.max(zs, 1, keepdims=True)
+    none = np.isneginf(m[:, 0])
+    m = np.where(np.isneginf(m), 0.0, m)
+    with np.errstate(divide="ignore", invalid="ignore"):
+        d = zs - m
+        e = np.exp(d)
+        s = e.sum(1)
+        ls = np.log(s)
+        lse = np.where(none, -np.inf, m[:, 0] + ls)
+        p = np.where(none[:, None], 0.0, e / np.maximum(s, 1e-300)[:, None])
+        far = np.where(p > 0, -d, 0.0)                    # ln units, at least 0
+        ent = np.where(none, 0.0, np.log(np.maximum(s, 1e-300)) + (p * far).sum(1))
+    rel = (p * (5 * far + 3)).sum(1) * F32 + (v / 8 + 40) * F32
+    ls_tol = rel + 2 * F32 * np.abs(np.log(np.maximum(s, 1e-300)))
+    lse_tol = ls_tol + 3 * F32 * (np.abs(m[:, 0]) + np.abs(np.where(none, 0, lse)))
+    ent_tol = 2 * ls_tol + (p * far * (5 * far + 6)).sum(1) * F32 + (v / 8 + 44) * F32 * ((p * far).sum(1) + ent)
+    ok = (ids >= 0) & (ids < v)
+    at = np.where(ok, ids, 0)
+    rows = np.arange(n)
+    # (from the differences: far values less their lse would cancel even in 64 bits)
+    with np.errstate(invalid="ignore"):
+        lp = np.where(ok, np.where(none, -np.inf, d[rows, at] - ls), 0.0)
+    dist = np.abs(np.where(np.isfinite(zs), d, 0.0))
+    lp_tol = ls_tol + 4 * F32 * (dist[rows, at] + np.abs(np.where(np.isfinite(lp), lp, 0)))
+    best = np.lexsort((np.broadcast_to(np.arange(v), z.shape), -z), axis=1)[:, :top]
+    with np.errstate(invalid="ignore"):
+        tl = np.where(none[:, None], -np.inf, np.take_along_axis(d, best, 1) - ls[:, None])
+    tl_tol = ls_tol[:, None] + 4 * F32 * (np.take_along_axis(dist, best, 1) + np.abs(np.where(np.isfinite(tl), tl, 0)))
+    return (lp, ent, lse, best, tl), (lp_tol, ent_tol, lse_tol, None, tl_tol)
+
+
+def logprob_backward(z, ids, scale, lse, g, ent=None, h=None):
+    """(dlogits, bound before rounding).  log p = z scale - lse errs by 2 u' of itself and u'
+    of the product's rounded input, so p by 3 u' |log p| + 2 u'; the rest is a few u'."""
+    none = np.isneginf(lse)
+    with np.errstate(invalid="ignore"):
+        lp = z * scale - np.where(none, 0.0, lse)[:, None]
+    p = np.where(none[:, None], 0.0, np.exp(lp))
+    far = np.where(p > 0, np.where(np.isfinite(lp), lp, 0.0), 0.0)
+    h0 = np.zeros_like(g) if h is None else h
+    e0 = np.zeros_like(g) if ent is None else ent
+    ok = (ids >= 0) & (ids < z.shape[1]) & ~none
+    g1 = np.where((ids >= 0) & (ids < z.shape[1]), g, 0.0)
+    c = g1[:, None] + h0[:, None] * (far + e0[:, None])
+    d = -p * c
+    rows = np.arange(len(ids))[ok]
+    d[rows, ids[ok]] += g[ok]
+    mag = np.abs(g1)[:, None] + np.abs(h0)[:, None] * (np.abs(far) + np.abs(e0)[:, None])
+    tol = p * mag * F32 * (4 * np.abs(far) + 10)
+    tol[rows, ids[ok]] += 3 * F32 * np.abs(g[ok])
+    return d * scale, tol * scale

@@ -1,5 +1,5 @@
 """The layer operators (include/ma_layers.h) on the GPU against float64
-references: norm and rotary positions, forward and backward, at the sizes, types,
+references: norm, rotary positions and token log probabilities, forward and backward, at the sizes, types,
 strides and values where each can go wrong."""
 
 import numpy as np
@@ -240,3 +240,175 @@ def test_rotary_shapes_and_empty():
     one = M.ma_rotary(x[0, 4], pos[0, 4], plan)
     assert torch.equal(one, flat[4])
     assert torch.equal(M.ma_rotary(x, torch.zeros_like(pos), plan), x)
+
+
+# -------------------------------------------------- log probabilities of tokens --
+
+def _check_logprob(z, ids, scale, top, tok=torch.int64):
+    got = M.ma_token_logprob_forward(z, torch.from_numpy(ids).to("cuda", tok), scale=scale, top=top)
+    want, tol = R.logprob(_f64(z), ids, float(np.float32(scale)), top)
+    for name, k in (("logprob", 0), ("entropy", 1), ("lse", 2)):
+        _close(got[k], want[k], tol[k], name)
+    if top:
+        assert got[3].dtype == tok and np.array_equal(got[3].cpu().numpy(), want[3])
+        _close(got[4], want[4], tol[4], "top")
+    else:
+        assert got[3] is None and got[4] is None
+    return got
+
+
+def _logits(rng, rows, vocab, spread=3.0):
+    return rng.standard_normal((rows, vocab)) * spread
+
+
+LOGIT_SHAPES = [(1, 1, 0), (3, 2, 0), (5, 7, 1), (2, 9, 0), (37, 64, 0), (3, 100, 4), (4, 519, 3), (130, 1000, 0),
+                (3, 1001, 0), (2, 4096, 0), (3, 4097, 0), (2, 8200, 0), (3, 16385, 1), (1, 32003, 0), (700, 4133, 0),
+                (600, 17001, 0), (1, 151000, 0), (2, 151003, 5)]
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("rows,vocab,pad", LOGIT_SHAPES)
+def test_logprob(kind, rows, vocab, pad):
+    rng = np.random.default_rng(rows + vocab)
+    z, _ = _strided(_logits(rng, rows, vocab), pad, kind)
+    ids = rng.integers(0, vocab, rows)
+    ids[rows // 2] = vocab if rows > 2 else ids[rows // 2]
+    for top, scale in ((0, 1.0), (1, 0.5), (min(vocab, 20), 1.3), (min(vocab, 64), 1.0)):
+        got = _check_logprob(z, ids, scale, top, torch.int32 if top == 1 else torch.int64)
+    need = M.ma_token_logprob_workspace_size(rows, vocab, min(vocab, 64))
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    again = M.ma_token_logprob_forward(z, torch.from_numpy(ids).cuda(), scale=1.0, top=min(vocab, 64), workspace=ws)
+    for a, b in zip(got, again):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("vocab", [300, 1000, 5001, 20011, 151000])
+def test_logprob_orders(kind, vocab):
+    """Rows in rising and falling order, of one value, of few values, with the highest side by side, at the
+    stride of a workgroup's rounds, at both ends; masked but for a few; with zeros of both signs."""
+    rng = np.random.default_rng(vocab)
+    z = np.zeros((12, vocab))
+    z[0] = np.linspace(-5, 5, vocab)
+    z[1] = z[0][::-1]
+    z[2] = 0.25
+    z[3] = rng.integers(0, 3, vocab)
+    z[4] = rng.standard_normal(vocab)
+    z[4, vocab // 3:vocab // 3 + 70] = 9 + rng.random(70)
+    z[5] = rng.standard_normal(vocab)
+    z[5, ::512 * 8 if vocab > 16384 else 64 * 8] = 7.0
+    z[6, :5], z[6, -5:] = 3.0, 3.0
+    z[7] = -np.inf
+    z[7, rng.integers(0, vocab, 5)] = rng.random(5)
+    z[8] = -3.3e38
+    z[9] = -3.3e38
+    z[9, -1] = 1.0
+    z[10] = np.where(rng.random(vocab) < 0.5, 0.0, -0.0)
+    z[11] = -np.inf
+    t = _dev(z, kind)
+    ids = rng.integers(0, vocab, 12)
+    for top in (1, 5, 20, 64):
+        _check_logprob(t, ids, 1.0, top)
+    # from an odd address on, so that a row's first elements are no whole unit
+    for off in (1, 3):
+        w = torch.zeros(12 * vocab + 8, dtype=DT[kind], device="cuda")
+        o = w[off:off + 12 * vocab].view(12, vocab)
+        o.copy_(t)
+        _check_logprob(o, ids, 1.0, 20)
+
+
+def test_logprob_more_keys_than_the_list():
+    """Thousands of values above the bound that the threads' largest give: the 64 highest threads hold
+    only such values."""
+    z = torch.randn(2, 151000, device="cuda")
+    unit = (torch.arange(151000, device="cuda") // 8) % 512
+    hot = unit < 64
+    z[:, hot] = 20 + torch.rand(2, int(hot.sum()), device="cuda")
+    # (one row, and the same among enough rows for a workgroup each)
+    ids = np.array([5, 77])
+    _check_logprob(z, ids, 1.0, 64)
+    many = z.repeat(300, 1)
+    got = M.ma_token_logprob_forward(many, torch.zeros(600, dtype=torch.int64, device="cuda"), top=64)
+    want = torch.sort(z, dim=1, descending=True, stable=True)[1][:, :64]
+    assert torch.equal(got[3], want.repeat(300, 1))
+
+
+def test_logprob_nonfinite():
+    z = torch.randn(6, 5000, device="cuda")
+    z[0, 17] = float("nan")
+    z[1, 4000] = float("inf")
+    z[3] = float("nan")
+    ids = torch.tensor([1, 2, 3, 4, 5, 6], device="cuda")
+    lp, ent, lse, top, tl = M.ma_token_logprob_forward(z, ids, top=10)
+    for r in (0, 1, 3):
+        assert torch.isnan(lp[r]) and torch.isnan(ent[r]) and torch.isnan(lse[r]) and torch.isnan(tl[r]).any()
+        assert len(set(top[r].tolist())) == 10 and 0 <= int(top[r].min()) and int(top[r].max()) < 5000
+    clean = M.ma_token_logprob_forward(z[[2, 4, 5]].contiguous(), ids[[2, 4, 5]], top=10)
+    for a, b in zip((lp, ent, lse, top, tl), clean):
+        assert torch.equal(a[[2, 4, 5]], b)
+    d = M.ma_token_logprob_backward(z, ids, lse, torch.ones(6, device="cuda"))
+    assert torch.isnan(d[0]).all() and torch.isfinite(d[2]).all()
+
+
+@pytest.mark.parametrize("kind,gkind", [("fp32", "fp32"), ("bf16", "bf16"), ("bf16", "fp32"), ("fp32", "bf16")])
+@pytest.mark.parametrize("rows,vocab,pad", LOGIT_SHAPES)
+def test_logprob_backward(kind, gkind, rows, vocab, pad):
+    rng = np.random.default_rng(rows * 3 + vocab)
+    z = _logits(rng, rows, vocab)
+    if vocab > 50:
+        z[:, 5:40:3] = -np.inf
+    if rows > 4:
+        z[3] = -np.inf
+    z, _ = _strided(z, pad, kind)
+    ids = rng.integers(0, vocab, rows)
+    ids[0] = -1 if rows > 1 else 0
+    tok = torch.from_numpy(ids).cuda()
+    g, h = _dev(rng.standard_normal(rows)), _dev(rng.standard_normal(rows))
+    scale = 1.25
+    _, ent, lse, _, _ = M.ma_token_logprob_forward(z, tok, scale=scale)
+    out, wide = _strided(np.zeros((rows, vocab)), pad + 1, gkind)
+    for e, k in ((None, None), (ent, h)):
+        M.ma_token_logprob_backward(z, tok, lse, g, entropy=e, dentropy=k, scale=scale, out=out)
+        want, tol = R.logprob_backward(_f64(z), ids, scale, _f64(lse), _f64(g), None if e is None else _f64(e),
+                                       None if k is None else _f64(k))
+        _close(out, want, R.rounded(want, tol, gkind))
+        assert torch.all(wide[:, vocab:] == 7.0)
+        assert torch.equal(M.ma_token_logprob_backward(z, tok.to(torch.int32), lse, g, entropy=e, dentropy=k,
+                                                       scale=scale, grad_dtype=DT[gkind]), out)
+    if kind == gkind:                                        # over the logits themselves
+        into = z.clone()
+        M.ma_token_logprob_backward(into, tok, lse, g, entropy=ent, dentropy=h, scale=scale, out=into)
+        assert torch.equal(into, out)
+
+
+def test_logprob_gradient_against_differences():
+    rng = np.random.default_rng(8)
+    z, ids = rng.standard_normal((5, 300)) * 2, rng.integers(0, 300, 5)
+    g, h = rng.standard_normal(5), rng.standard_normal(5)
+    _, ent, lse, _, _ = M.ma_token_logprob_forward(_dev(z), torch.from_numpy(ids).cuda(), scale=0.7)
+    d = _f64(M.ma_token_logprob_backward(_dev(z), torch.from_numpy(ids).cuda(), lse, _dev(g), entropy=ent,
+                                         dentropy=_dev(h), scale=0.7))
+
+    def f(a):
+        (lp, e, _, _, _), _ = R.logprob(a, ids, 0.7)
+        return np.sum(g * lp + h * e)
+
+    for seed in range(4):
+        u = np.random.default_rng(seed).standard_normal(z.shape)
+        slope = (f(z + 1e-5 * u) - f(z - 1e-5 * u)) / 2e-5
+        # gradients sum to a few units, in float32: 2^-20 or so of their magnitudes
+        assert abs(np.sum(d * u) - slope) < 1e-4 * max(1.0, abs(slope))
+
+
+def test_logprob_shapes_and_empty():
+    z = torch.randn(2, 3, 50, device="cuda")
+    ids = torch.randint(0, 50, (2, 3), device="cuda")
+    lp, ent, lse, top, tl = M.ma_token_logprob_forward(z, ids, top=4)
+    flat = M.ma_token_logprob_forward(z.view(6, 50), ids.view(6), top=4)
+    assert lp.shape == (2, 3) and top.shape == (2, 3, 4)
+    assert torch.equal(top.view(6, 4), flat[3]) and torch.equal(lp.view(6), flat[0])
+    d = M.ma_token_logprob_backward(z, ids, lse, torch.ones_like(lp))
+    assert d.shape == z.shape and d.sum(-1).abs().max() < 1e-5
+    e = M.ma_token_logprob_forward(z[:0], ids[:0], top=4)
+    assert e[0].shape == (0, 3) and e[3].shape == (0, 3, 4)
+    assert M.ma_token_logprob_backward(z[:0], ids[:0], lse[:0], lp[:0]).shape == (0, 3, 50)
