@@ -8,6 +8,8 @@
  *   ma_rotary               feature pairs turned by positions of several axes, and back
  *   ma_token_logprob_forward    log probabilities of given tokens, entropies, top alternatives
  *   ma_token_logprob_backward   the gradient of the logits
+ *   ma_attention_forward    softmax(scale q k^T) v over packed sequences with grouped heads
+ *   ma_attention_backward   dq, dk and dv
  *
  * Conventions are those of ma_grads.h: return codes and messages, checks
  * before any launch, caller-owned memory, the caller's HIP stream, capturable,
@@ -145,6 +147,58 @@ int ma_token_logprob_backward(const void* logits, int32_t dtype, int64_t n_token
                               double scale, const float* lse, const float* entropy,
                               const float* dlogprob, const float* dentropy, void* dlogits,
                               int32_t dlogits_dtype, int64_t dlogits_stride, void* stream);
+
+/* ---- attention ------------------------------------------------------------------- */
+
+#define MA_ATTN_MAX_DIM 256
+
+/* tokens x heads x head_dim, each head's features contiguous: strides in elements
+ * between tokens and between heads. */
+typedef struct ma_heads {
+    void*   p;                 /* (not written where a function only reads it) */
+    int64_t token_stride;
+    int64_t head_stride;
+} ma_heads;
+
+/* Packed sequences: queries [cu_q[s], cu_q[s + 1]) attend to keys [cu_k[s], cu_k[s + 1]),
+ * s < n_seqs.  cu_q and cu_k are device arrays of n_seqs + 1 rising int32 values; both NULL for
+ * one sequence of everything (n_seqs = 1).  Queries and keys outside every sequence (behind the
+ * last one) are neither read nor written.  Offsets that fall or leave [0, n] are cut to the
+ * arrays: no access leaves them, but what is then computed is not defined.
+ * Query head h reads key head h / (heads / kv_heads).  With causal = 1 the last query of a
+ * sequence sees its last key: query i of nq sees keys 0 .. i + nk - nq. */
+typedef struct ma_attention {
+    int32_t dtype;             /* of q, k, v, o and their gradients */
+    int32_t heads, kv_heads;   /* heads a multiple of kv_heads */
+    int32_t head_dim;          /* 1 .. MA_ATTN_MAX_DIM */
+    int32_t causal;            /* 0 or 1 */
+    int32_t n_seqs;            /* may be 0 */
+    int64_t n_queries, n_keys;
+    double  scale;             /* of the scores, > 0 */
+    const int32_t* cu_q;
+    const int32_t* cu_k;
+    ma_heads q, k, v;
+    ma_heads o;                /* forward: written; backward: read */
+    float*   lse;              /* heads x n_queries: ln of the softmax's sums; backward: read */
+    ma_heads dout, dq, dk, dv; /* backward only */
+} ma_attention;
+
+/* o = softmax(scale q k^T) v and lse.  A query that sees no key has o = 0 and lse =
+ * -infinity.  Sums, maxima and lse are float32; a bfloat16 call rounds the probabilities
+ * to bfloat16 (at up to 2^8 of the row's largest) for their product with v, as its matrix
+ * instructions take them.  A NaN or infinity in a sequence may make that head of that whole
+ * sequence NaN, and reaches no other.  Errors: INVALID_ARG, SHAPE (n_queries * heads or
+ * n_keys * heads above 2^30, n_seqs * heads above 2^22), HIP. */
+int ma_attention_forward(const ma_attention* a, void* stream);
+
+/* Bytes of workspace (256-byte aligned) a backward call needs.  Errors: INVALID_ARG, SHAPE. */
+int ma_attention_backward_workspace_size(const ma_attention* a, size_t* bytes);
+
+/* dq, dk and dv from dout and the forward pass' o and lse.  dk and dv sum over the query heads
+ * that share them; keys that no query sees get 0.  The probabilities and the scores' gradients
+ * of a bfloat16 call are rounded to bfloat16 for their products.  No atomics: reruns are
+ * bitwise equal.  Errors: as ma_attention_forward, WORKSPACE. */
+int ma_attention_backward(const ma_attention* a, void* workspace, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

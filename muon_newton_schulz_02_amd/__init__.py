@@ -11,7 +11,7 @@ and workspace as torch tensors and calls `muon_adamw_step`.
 The operators that produce gradients (include/ma_grads.h: embedding lookup and
 gradient, activations held in 8 bits and the gradients formed from them) are
 in `grads`, those that a layer's forward and backward passes are made of
-(include/ma_layers.h: norm, rotary positions, token log probabilities) in `layers`, and all of them under
+(include/ma_layers.h: norm, rotary positions, attention, token log probabilities) in `layers`, and all of them under
 their names here.
 """
 
@@ -22,7 +22,7 @@ import importlib.util
 from typing import Dict, List, Optional, Sequence, Tuple
 
 from . import _abi
-from ._abi import (MA_ACT_GELU_TANH, MA_ACT_GROUP, MA_ACT_SILU, MA_ERR_CAPTURE, MA_ERR_HIP, MA_ERR_INVALID_ARG, MA_ERR_SHAPE, MA_ERR_UNSUPPORTED,  # noqa: F401
+from ._abi import (MA_ACT_GELU_TANH, MA_ACT_GROUP, MA_ACT_SILU, MA_ATTN_MAX_DIM, MA_ERR_CAPTURE, MA_ERR_HIP, MA_ERR_INVALID_ARG, MA_ERR_SHAPE, MA_ERR_UNSUPPORTED,  # noqa: F401
                    MA_ERR_WORKSPACE, MA_GROUP_ADAMW, MA_GROUP_MUON, MA_GROUP_NONE,
                    MA_LR_CONSTANT, MA_LR_COSINE_MIN, MA_MODE_ADAMW, MA_MODE_MUON_ADAMW,
                    MA_LOGPROB_MAX_TOP, MA_NOALLOC_SCRATCH_BYTES, MA_NORM_MAX_COLS, MA_NS_BF16, MA_NS_FP32, MA_OK, MA_PARAM_BF16,
@@ -45,7 +45,8 @@ _GRADS = ("ActCheckpoint", "EmbeddingGrad", "LinearGrad", "ma_act_pack", "ma_act
           "ma_linear_grad", "ma_linear_grad_workspace_size", "ma_glu_forward", "ma_glu_backward")
 _LAYERS = ("Rotary", "ma_rms_norm_forward", "ma_rms_norm_backward", "ma_rms_norm_backward_workspace_size",
            "ma_rotary", "ma_token_logprob_forward", "ma_token_logprob_backward",
-           "ma_token_logprob_workspace_size")
+           "ma_token_logprob_workspace_size", "ma_attention_forward", "ma_attention_backward",
+           "ma_attention_backward_workspace_size")
 
 
 def _torch_installed() -> bool:

@@ -31,6 +31,7 @@ MA_ACT_GROUP = 32
 MA_ACT_SILU, MA_ACT_GELU_TANH = 0, 1
 MA_NORM_MAX_COLS = 8192
 MA_LOGPROB_MAX_TOP = 64
+MA_ATTN_MAX_DIM = 256
 MA_ROTARY_MAX_PAIRS, MA_ROTARY_MAX_AXES = 256, 4
 MA_ROTARY_HALF, MA_ROTARY_PAIRS = 0, 1
 MA_ROTARY_BLOCKS, MA_ROTARY_CYCLED = 0, 1
@@ -124,6 +125,17 @@ GRAD_SIGNATURES = [
                                   _I64, _P, _P, _P]),
 ]
 
+class ma_heads(C.Structure):
+    _fields_ = [("p", _P), ("token_stride", _I64), ("head_stride", _I64)]
+
+
+class ma_attention(C.Structure):
+    _fields_ = [("dtype", _I32), ("heads", _I32), ("kv_heads", _I32), ("head_dim", _I32), ("causal", _I32),
+                ("n_seqs", _I32), ("n_queries", _I64), ("n_keys", _I64), ("scale", _F64), ("cu_q", _P), ("cu_k", _P),
+                ("q", ma_heads), ("k", ma_heads), ("v", ma_heads), ("o", ma_heads), ("lse", _P),
+                ("dout", ma_heads), ("dq", ma_heads), ("dk", ma_heads), ("dv", ma_heads)]
+
+
 # and of ma_layers.h
 LAYER_SIGNATURES = [
     ("ma_rms_norm_forward", C.c_int, [_P, _I64, _P, _I64, _I32, _I64, _I64, _P, _I32, _F64, _F64, _P, _I64, _P,
@@ -139,6 +151,9 @@ LAYER_SIGNATURES = [
                                            _P, _SZ, _P]),
     ("ma_token_logprob_backward", C.c_int, [_P, _I32, _I64, _I64, _I64, _P, _I32, _F64, _P, _P, _P, _P, _P, _I32,
                                             _I64, _P]),
+    ("ma_attention_forward", C.c_int, [C.POINTER(ma_attention), _P]),
+    ("ma_attention_backward_workspace_size", C.c_int, [C.POINTER(ma_attention), C.POINTER(_SZ)]),
+    ("ma_attention_backward", C.c_int, [C.POINTER(ma_attention), _P, _SZ, _P]),
 ]
 
 _lib = None

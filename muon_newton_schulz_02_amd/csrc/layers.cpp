@@ -104,6 +104,80 @@ LogprobSpace logprob_space(int64_t rows, int64_t vocab, int64_t top) {
     return s;
 }
 
+int check_attention(const char* fn, const ma_attention* a, bool back) {
+    if (!a) {
+        set_error("%s: NULL argument", fn);
+        return MA_ERR_INVALID_ARG;
+    }
+    TRY(check_dtype(fn, "q", a->dtype));
+    TRY(check_size(fn, "kv_heads", a->kv_heads, 1, kMaxHeads));
+    TRY(check_size(fn, "heads", a->heads, 1, kMaxHeads));
+    TRY(check_size(fn, "head_dim", a->head_dim, 1, MA_ATTN_MAX_DIM));
+    TRY(check_flag(fn, "causal", a->causal));
+    if (a->heads % a->kv_heads) {
+        set_error("%s: %d heads are no multiple of %d key heads", fn, a->heads, a->kv_heads);
+        return MA_ERR_SHAPE;
+    }
+    // (a launch has fewer than 2^32 threads)
+    TRY(check_size(fn, "n_seqs", a->n_seqs, 0, (int64_t(1) << 22) / a->heads));
+    TRY(check_size(fn, "n_queries", a->n_queries, 0, kMaxCount / a->heads));
+    TRY(check_size(fn, "n_keys", a->n_keys, 0, kMaxCount / a->heads));
+    if (!(a->scale >= 0x1p-100) || !std::isfinite((float)a->scale)) {
+        set_error("%s: scale must be a positive float32, at least 2^-100", fn);
+        return MA_ERR_INVALID_ARG;
+    }
+    TRY(check_pair(fn, "cu_q", a->cu_q, "cu_k", a->cu_k));
+    if (!a->cu_q && a->n_seqs != 1) {
+        set_error("%s: %d sequences without offsets", fn, a->n_seqs);
+        return MA_ERR_INVALID_ARG;
+    }
+    struct {
+        const char* name;
+        const ma_heads* x;
+        int64_t n;
+        int32_t heads;
+        bool out;
+    } all[] = {{"q", &a->q, a->n_queries, a->heads, false},  {"k", &a->k, a->n_keys, a->kv_heads, false},
+               {"v", &a->v, a->n_keys, a->kv_heads, false},  {"o", &a->o, a->n_queries, a->heads, !back},
+               {"dout", &a->dout, a->n_queries, a->heads, false}, {"dq", &a->dq, a->n_queries, a->heads, true},
+               {"dk", &a->dk, a->n_keys, a->kv_heads, true}, {"dv", &a->dv, a->n_keys, a->kv_heads, true}};
+    for (int i = 0; i < (back ? 8 : 4); ++i) {
+        const auto& e = all[i];
+        TRY((e.out ? check_heads_out : check_heads)(fn, e.name, e.n, e.heads, a->head_dim, e.x->token_stride,
+                                                    e.x->head_stride));
+    }
+    return MA_OK;
+}
+
+Span attention_span(const ma_attention* a, const char* name, const ma_heads& x, bool keys, bool written) {
+    return heads_of(name, x.p, a->dtype, keys ? a->n_keys : a->n_queries, keys ? a->kv_heads : a->heads, a->head_dim,
+                    x.token_stride, x.head_stride, written);
+}
+
+int64_t attention_ws(const ma_attention* a) { return round_up(a->heads * a->n_queries * 4, 256); }
+
+AttnArgs attention_args(const ma_attention* a) {
+    const auto arr = [](const ma_heads& x) { return AttnArray{x.p, x.token_stride, x.head_stride}; };
+    AttnArgs g{};
+    g.q = arr(a->q);
+    g.k = arr(a->k);
+    g.v = arr(a->v);
+    g.o = arr(a->o);
+    g.lse = a->lse;
+    g.cu_q = a->cu_q;
+    g.cu_k = a->cu_k;
+    g.n_queries = a->n_queries;
+    g.n_keys = a->n_keys;
+    g.scale = (float)a->scale;
+    g.heads = a->heads;
+    g.kv_heads = a->kv_heads;
+    g.dim = a->head_dim;
+    g.n_seqs = a->n_seqs;
+    g.causal = a->causal;
+    g.dtype = a->dtype;
+    return g;
+}
+
 int check_top(const char* fn, int32_t top, int64_t vocab) {
     return check_size(fn, "top", top, 0, vocab < MA_LOGPROB_MAX_TOP ? vocab : MA_LOGPROB_MAX_TOP);
 }
@@ -432,6 +506,51 @@ int ma_token_logprob_backward(const void* logits, int32_t dtype, int64_t n_token
     a.dtype = dtype;
     a.ddtype = dlogits_dtype;
     return done(fn, launch_logprob_backward(a, stream));
+}
+
+int ma_attention_forward(const ma_attention* a, void* stream) {
+    const char* fn = "ma_attention_forward";
+    TRY(check_attention(fn, a, false));
+    const int64_t cu = a->cu_q ? (a->n_seqs + 1) * 4 : 0;
+    TRY(check_spans(fn, {attention_span(a, "q", a->q, false, false), attention_span(a, "k", a->k, true, false),
+                         attention_span(a, "v", a->v, true, false), flat("cu_q", a->cu_q, cu, 4, false),
+                         flat("cu_k", a->cu_k, cu, 4, false), attention_span(a, "o", a->o, false, true),
+                         flat("lse", a->lse, a->heads * a->n_queries * 4, 4, true)}));
+    return done(fn, launch_attention_forward(attention_args(a), stream));
+}
+
+int ma_attention_backward_workspace_size(const ma_attention* a, size_t* bytes) {
+    const char* fn = "ma_attention_backward_workspace_size";
+    if (!bytes) {
+        set_error("%s: NULL argument", fn);
+        return MA_ERR_INVALID_ARG;
+    }
+    TRY(check_attention(fn, a, true));
+    *bytes = (size_t)attention_ws(a);
+    clear_error();
+    return MA_OK;
+}
+
+int ma_attention_backward(const ma_attention* a, void* workspace, size_t ws_bytes, void* stream) {
+    const char* fn = "ma_attention_backward";
+    TRY(check_attention(fn, a, true));
+    const int64_t need = attention_ws(a);
+    TRY(check_workspace(fn, workspace, ws_bytes, (size_t)need));
+    const int64_t cu = a->cu_q ? (a->n_seqs + 1) * 4 : 0;
+    TRY(check_spans(fn, {attention_span(a, "q", a->q, false, false), attention_span(a, "k", a->k, true, false),
+                         attention_span(a, "v", a->v, true, false), attention_span(a, "o", a->o, false, false),
+                         attention_span(a, "dout", a->dout, false, false), flat("cu_q", a->cu_q, cu, 4, false),
+                         flat("cu_k", a->cu_k, cu, 4, false),
+                         flat("lse", a->lse, a->heads * a->n_queries * 4, 4, false),
+                         attention_span(a, "dq", a->dq, false, true), attention_span(a, "dk", a->dk, true, true),
+                         attention_span(a, "dv", a->dv, true, true), flat("workspace", workspace, need, 1, true)}));
+    AttnArgs g = attention_args(a);
+    g.dout = {a->dout.p, a->dout.token_stride, a->dout.head_stride};
+    g.dq = {a->dq.p, a->dq.token_stride, a->dq.head_stride};
+    g.dk = {a->dk.p, a->dk.token_stride, a->dk.head_stride};
+    g.dv = {a->dv.p, a->dv.token_stride, a->dv.head_stride};
+    g.delta = static_cast<float*>(workspace);
+    return done(fn, launch_attention_backward(g, stream));
 }
 
 }  // extern "C"

@@ -62,4 +62,21 @@ int64_t logprob_pieces(int64_t rows, int64_t vocab);
 int launch_logprob_forward(const LogprobArgs& a, void* stream);
 int launch_logprob_backward(const LogprobArgs& a, void* stream);
 
+// ------------------------------------------------------------ attention --
+// tokens x heads x dim, with strides between tokens and between heads.
+struct AttnArray {
+    const void* p;
+    int64_t token, head;
+};
+struct AttnArgs {
+    AttnArray q, k, v, o, dout, dq, dk, dv;
+    float *lse, *delta;
+    const int32_t *cu_q, *cu_k;
+    int64_t n_queries, n_keys;
+    float scale;
+    int32_t heads, kv_heads, dim, n_seqs, causal, dtype;
+};
+int launch_attention_forward(const AttnArgs& a, void* stream);
+int launch_attention_backward(const AttnArgs& a, void* stream);
+
 }  // namespace ma

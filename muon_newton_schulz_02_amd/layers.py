@@ -6,6 +6,8 @@ and backward passes are made of, beside those of `grads`.
     ma_rotary             feature pairs turned by positions of several axes, and back
     ma_token_logprob_forward, ma_token_logprob_backward     log probabilities of given
                           tokens, entropies and top alternatives, and the logits' gradient
+    ma_attention_forward, ma_attention_backward     attention over packed sequences with
+                          grouped heads
 
 Manners are those of `grads`: names and meanings are the C ABI's, outputs and
 workspaces are allocated as torch tensors where the caller passes none,
@@ -351,3 +353,115 @@ def ma_token_logprob_backward(logits, tokens, lse, dlogprob, entropy=None, dentr
     if rc:
         _fail(rc, "ma_token_logprob_backward")
     return out
+
+
+# ---------------------------------------------------------------- attention --
+
+def _offsets(cu, what: str):
+    _check_cuda(cu, what)
+    if cu.dtype != torch.int32 or cu.dim() != 1 or cu.shape[0] < 1 or not cu.is_contiguous():
+        raise ValueError("%s must be a contiguous int32 vector of offsets" % what)
+    return cu.shape[0] - 1
+
+
+def _attention_args(q, k, v, cu_q, cu_k, causal, scale):
+    """(args, device) of the inputs that both passes share."""
+    for what, x in (("q", q), ("k", k), ("v", v)):
+        _check_cuda(x, what)
+        if x.dim() != 3:
+            raise ValueError("%s must be tokens x heads x features (got %s)" % (what, tuple(x.shape)))
+    if k.shape != v.shape or k.dtype != q.dtype or v.dtype != q.dtype or k.shape[2] != q.shape[2]:
+        raise ValueError("q %s %s, k %s %s and v %s %s do not belong together" % (
+            tuple(q.shape), q.dtype, tuple(k.shape), k.dtype, tuple(v.shape), v.dtype))
+    if (cu_q is None) != (cu_k is None):
+        raise ValueError("cu_q and cu_k go together")
+    a = _abi.ma_attention()
+    a.dtype = _dtype(q, "q")
+    a.n_queries, a.heads, a.head_dim = q.shape
+    a.n_keys, a.kv_heads = k.shape[:2]
+    a.causal = 1 if causal else 0
+    a.scale = a.head_dim ** -0.5 if scale is None else scale
+    a.n_seqs = 1
+    if cu_q is not None:
+        a.n_seqs = _offsets(cu_q, "cu_q")
+        if _offsets(cu_k, "cu_k") != a.n_seqs:
+            raise ValueError("cu_q and cu_k hold %d and %d offsets" % (cu_q.shape[0], cu_k.shape[0]))
+        a.cu_q, a.cu_k = cu_q.data_ptr(), cu_k.data_ptr()
+    _same_device(q.device, ("k", k), ("v", v), ("cu_q", cu_q), ("cu_k", cu_k))
+    for name, x in (("q", q), ("k", k), ("v", v)):
+        _set_heads(getattr(a, name), x, name)
+    return a, q.device
+
+
+def _set_heads(field, x, what: str):
+    _, _, _, field.token_stride, field.head_stride = _heads(x, what)
+    field.p = x.data_ptr()
+
+
+def ma_attention_forward(q, k, v, cu_q=None, cu_k=None, causal: bool = True, scale: Optional[float] = None, out=None,
+                         stream=None):
+    """(o, lse) of softmax(scale q k^T) v: q (queries, heads, features), k and v (keys, key heads, features), where
+    query head h reads key head h // (heads // key heads).  cu_q and cu_k (int32, one more than there are
+    sequences) hold where packed sequences begin; without them everything is one sequence.  With `causal` the last
+    query of a sequence sees its last key.  scale defaults to features^-1/2.  A query that sees no key
+    has o = 0 and lse = -infinity; queries outside every sequence are left as they are in `out` (and undefined where
+    none is passed).  o and lse (heads x queries, float32) are what ma_attention_backward takes."""
+    a, dev = _attention_args(q, k, v, cu_q, cu_k, causal, scale)
+    _same_device(dev, ("out", out))
+    if _elsewhere(dev, stream):
+        with _At(dev, stream, (q, k, v, cu_q, cu_k, out)):
+            return ma_attention_forward(q, k, v, cu_q, cu_k, causal, scale, out)
+    out = _out_as(out, "out", q)
+    lse = torch.empty((a.heads, a.n_queries), dtype=torch.float32, device=dev)
+    _set_heads(a.o, out, "out")
+    a.lse = lse.data_ptr()
+    rc = _abi.load().ma_attention_forward(C.byref(a), _raw_stream(dev.index))
+    if rc:
+        _fail(rc, "ma_attention_forward")
+    return out, lse
+
+
+def ma_attention_backward_workspace_size(q, k, v) -> int:
+    """Bytes a backward call of these inputs needs."""
+    a, _ = _attention_args(q, k, v, None, None, False, None)
+    a.o.token_stride = a.dout.token_stride = a.dq.token_stride = a.heads * a.head_dim
+    a.o.head_stride = a.dout.head_stride = a.dq.head_stride = a.head_dim
+    a.dk.token_stride = a.dv.token_stride = a.kv_heads * a.head_dim
+    a.dk.head_stride = a.dv.head_stride = a.head_dim
+    n = C.c_size_t()
+    rc = _abi.load().ma_attention_backward_workspace_size(C.byref(a), C.byref(n))
+    if rc:
+        _fail(rc, "ma_attention_backward_workspace_size")
+    return n.value
+
+
+def ma_attention_backward(dout, q, k, v, out, lse, cu_q=None, cu_k=None, causal: bool = True,
+                          scale: Optional[float] = None, dq=None, dk=None, dv=None, workspace=None, stream=None):
+    """(dq, dk, dv) from the gradient dout of ma_attention_forward's output `out`, with its lse and the same
+    other arguments.  Rows outside every sequence are left as they are (and undefined in gradients allocated
+    here)."""
+    a, dev = _attention_args(q, k, v, cu_q, cu_k, causal, scale)
+    _check_cuda(dout, "dout")
+    _check_cuda(out, "out")
+    _same_type(dout, "dout", q, "q")
+    _same_type(out, "out", q, "q")
+    _per_row(lse, "lse", (a.heads, a.n_queries))
+    _same_device(dev, ("dout", dout), ("out", out), ("lse", lse), ("dq", dq), ("dk", dk), ("dv", dv))
+    _check_workspace(workspace, dev)
+    if _elsewhere(dev, stream):
+        with _At(dev, stream, (dout, q, k, v, out, lse, cu_q, cu_k, dq, dk, dv, workspace)):
+            return ma_attention_backward(dout, q, k, v, out, lse, cu_q, cu_k, causal, scale, dq, dk, dv, workspace)
+    dq, dk, dv = _out_as(dq, "dq", q), _out_as(dk, "dk", k), _out_as(dv, "dv", v)
+    for name, x in (("o", out), ("dout", dout), ("dq", dq), ("dk", dk), ("dv", dv)):
+        _set_heads(getattr(a, name), x, name)
+    a.lse = lse.data_ptr()
+    lib = _abi.load()
+    n = C.c_size_t()
+    rc = lib.ma_attention_backward_workspace_size(C.byref(a), C.byref(n))
+    if rc:
+        _fail(rc, "ma_attention_backward")
+    ws, ws_ptr, ws_bytes = _workspace(workspace, n.value, dev)
+    rc = lib.ma_attention_backward(C.byref(a), ws_ptr, ws_bytes, _raw_stream(dev.index))
+    if rc:
+        _fail(rc, "ma_attention_backward")
+    return dq, dk, dv

@@ -6,7 +6,7 @@ value.  `tol` arrays are absolute bounds per element."""
 
 import numpy as np
 
-from tests._grads_ref import F32, TINY, U
+from tests._grads_ref import F32, TINY, U, UNDER
 
 
 def rms_norm(x, w, res=None, eps=1e-6, off=0.0):
@@ -147,3 +147,93 @@ def logprob_backward(z, ids, scale, lse, g, ent=None, h=None):
     tol = p * mag * F32 * (4 * np.abs(far) + 10)
     tol[rows, ids[ok]] += 3 * F32 * np.abs(g[ok])
     return d * scale, tol * scale
+
+
+def _attend(q, k, scale, causal):
+    """(scores, mask of what is seen, bound of the scores): one head of one sequence.  A product of d
+    terms is summed by the matrix cores in float32, each addition off by at most one step (they may
+    cut instead of rounding), from exact products of bfloat16 and rounded ones of float32; scale and the
+    softmax's arguments by 6 u of the score."""
+    n, m = q.shape[0], k.shape[0]
+    z = scale * (q @ k.T)
+    seen = np.ones((n, m), bool)
+    if causal:
+        seen = np.arange(m)[None] <= np.arange(n)[:, None] + m - n
+    tol = scale * (2 * q.shape[1] + 4) * 2 * F32 * (np.abs(q) @ np.abs(k).T) + 6 * F32 * np.abs(z)
+    return z, seen, tol
+
+
+def _packed(cu_q, cu_k, heads, kv_heads):
+    for a, b, c, d in zip(cu_q, cu_q[1:], cu_k, cu_k[1:]):
+        for h in range(heads):
+            yield slice(a, b), slice(c, d), h, h // (heads // kv_heads)
+
+
+def attention(q, k, v, cu_q, cu_k, causal, scale, kind):
+    """(o, lse, bounds before rounding; NaN where no sequence is).  The probabilities of a
+    bfloat16 call are rounded once more for their product with v."""
+    up = U[kind] if kind == "bf16" else 0.0
+    o, lse = np.full(q.shape, np.nan), np.full((q.shape[1], q.shape[0]), np.nan)
+    otol, ltol = np.zeros(q.shape), np.zeros(lse.shape)
+    for a, b, h, g in _packed(cu_q, cu_k, q.shape[1], k.shape[1]):
+        z, seen, zt = _attend(q[a, h], k[b, g], scale, causal)
+        n, m = z.shape
+        if n == 0:
+            continue
+        if m == 0:
+            o[a, h], lse[h, a] = 0.0, -np.inf
+            continue
+        z = np.where(seen, z, -np.inf)
+        top = np.max(z, 1, keepdims=True)
+        none = np.isneginf(top[:, 0])
+        e = np.exp(z - np.where(np.isneginf(top), 0.0, top))
+        s = e.sum(1)
+        p = e / np.where(none, 1.0, s)[:, None]
+        # (the reference of the exponent may be 2^8 below the top: 8 ln 2 more in its argument)
+        zt = np.where(seen, zt, 0.0) + 6 * F32 * np.where(p > 0, np.abs(z - np.where(seen, top, 0.0)) + 6, 0.0) * seen
+        o[a, h] = p @ v[b, g]
+        lse[h, a] = np.where(none, -np.inf, np.where(none, 0.0, top[:, 0]) + np.log(np.where(none, 1.0, s)))
+        mean = (p * zt).sum(1, keepdims=True) + (m + 8) * F32
+        otol[a, h] = (p * (zt + mean + up * (1 + 2.0 ** -8) + (2 * m + 8) * F32)) @ np.abs(v[b, g])
+        otol[a, h] += (seen * UNDER) @ np.abs(v[b, g])
+        ltol[h, a] = mean[:, 0] + 4 * F32 * (np.abs(np.where(none, 0, lse[h, a])) + np.abs(np.where(none, 0, top[:, 0])))
+    return o, lse, otol, ltol
+
+
+def attention_backward(do, q, k, v, o, lse, cu_q, cu_k, causal, scale, kind):
+    """(dq, dk, dv, their bounds before rounding; NaN where no sequence is).  A probability below
+    2^-126, the smallest normal float, may be 0 (the hardware's 2^x and matrix instructions have no
+    denormal results), and so may a score's gradient: an absolute 2^-126 of each, times what it
+    is multiplied with (with |dp - delta| of 30, queries of 8 and 400 terms up to 1e-33)."""
+    up = U[kind] * (1 + 2.0 ** -8) if kind == "bf16" else 0.0
+    res = [np.full(q.shape, np.nan), np.full(k.shape, np.nan), np.full(v.shape, np.nan)]
+    tol = [np.zeros(q.shape), np.zeros(k.shape), np.zeros(v.shape)]
+    for x, cu in zip(res, (cu_q, cu_k, cu_k)):
+        for a, b in zip(cu, cu[1:]):
+            x[a:b] = 0.0
+    d2 = 2 * q.shape[2] + 8
+    for a, b, h, g in _packed(cu_q, cu_k, q.shape[1], k.shape[1]):
+        z, seen, zt = _attend(q[a, h], k[b, g], scale, causal)
+        n, m = z.shape
+        if n == 0 or m == 0:
+            continue
+        L = lse[h, a][:, None]
+        none = np.isneginf(L)
+        p = np.where(seen & ~none, np.exp(z - np.where(none, 0.0, L)), 0.0)
+        rel = zt + 6 * F32 * (np.abs(np.where(none, 0.0, L)) + np.abs(z) + 2)
+        dh, oh = do[a, h], o[a, h]
+        delta = (dh * oh).sum(1, keepdims=True)
+        dt = d2 * F32 * (np.abs(dh) * np.abs(oh)).sum(1, keepdims=True)
+        dp = dh @ v[b, g].T
+        pt = d2 * 2 * F32 * (np.abs(dh) @ np.abs(v[b, g]).T)
+        ds = p * (dp - delta)
+        st = np.abs(ds) * (rel + up + 3 * F32) + p * (pt + dt + 2 * F32 * (np.abs(dp) + np.abs(delta)))
+        st += seen * UNDER * (np.abs(dp) + np.abs(delta) + 1)
+        res[0][a, h] += scale * ds @ k[b, g]
+        tol[0][a, h] += scale * (st + (2 * m + 8) * F32 * np.abs(ds)) @ np.abs(k[b, g])
+        more = (2 * n * (q.shape[1] // k.shape[1]) + 8) * F32
+        res[1][b, g] += scale * ds.T @ q[a, h]
+        tol[1][b, g] += scale * (st + more * np.abs(ds)).T @ np.abs(q[a, h])
+        res[2][b, g] += p.T @ dh
+        tol[2][b, g] += (p * (rel + up + more) + seen * UNDER).T @ np.abs(dh)
+    return res, tol

@@ -412,3 +412,180 @@ def test_logprob_shapes_and_empty():
     e = M.ma_token_logprob_forward(z[:0], ids[:0], top=4)
     assert e[0].shape == (0, 3) and e[3].shape == (0, 3, 4)
     assert M.ma_token_logprob_backward(z[:0], ids[:0], lse[:0], lp[:0]).shape == (0, 3, 50)
+
+
+# ---------------------------------------------------------------- attention --
+
+def _offsets(lens):
+    return np.concatenate([[0], np.cumsum(lens)]).astype(np.int64)
+
+
+def _cu(off):
+    return torch.from_numpy(off.astype(np.int32)).cuda()
+
+
+def _heads_first(x):
+    """The same values with heads outside and tokens inside."""
+    return x.transpose(0, 1).contiguous().transpose(0, 1)
+
+
+def _inputs(rng, nq, nk, heads, kv, dim, kind):
+    return [_dev(rng.standard_normal(s), kind) for s in ((nq, heads, dim), (nk, kv, dim), (nk, kv, dim), (nq, heads, dim))]
+
+
+def _check_attention(q, k, v, do, cq, ck, causal, scale, kind):
+    nq = int(cq[-1])
+    cu = (_cu(cq), _cu(ck))
+    o, lse = torch.full_like(q, 7.0), None
+    o, lse = M.ma_attention_forward(q, k, v, *cu, causal=causal, scale=scale, out=o)
+    s = q.shape[2] ** -0.5 if scale is None else float(np.float32(scale))
+    want, wl, ot, lt = R.attention(_f64(q), _f64(k), _f64(v), cq, ck, causal, s, kind)
+    _close(o[:nq], want[:nq], R.rounded(want, ot, kind)[:nq], "o")
+    _close(lse[:, :nq], wl[:, :nq], lt[:, :nq], "lse")
+    assert torch.all(o[nq:] == 7.0)
+    g = [torch.full_like(x, 7.0) for x in (q, k, v)]
+    M.ma_attention_backward(do, q, k, v, o, lse, *cu, causal=causal, scale=scale, dq=g[0], dk=g[1], dv=g[2])
+    want, tol = R.attention_backward(_f64(do), _f64(q), _f64(k), _f64(v), _f64(o), _f64(lse), cq, ck, causal, s, kind)
+    for x, w, t, n, name in zip(g, want, tol, (nq, int(ck[-1]), int(ck[-1])), ("dq", "dk", "dv")):
+        _close(x[:n], w[:n], R.rounded(w, t, kind)[:n], name)
+        assert torch.all(x[n:] == 7.0), name
+    return o, lse, g
+
+
+ATTN = [  # lengths of queries, of keys (None: the same), heads, key heads, dim, causal
+    ([1], None, 1, 1, 64, True), ([1], [1], 2, 1, 128, False), ([33], None, 2, 2, 64, True), ([7, 1, 0, 70], None, 4, 2, 128, True),
+    ([128], None, 1, 1, 128, True), ([129], [257], 2, 1, 64, True), ([50, 50], [261, 130], 4, 1, 256, False),
+    ([200, 3, 140], None, 4, 4, 80, True), ([64, 65], [64, 1], 2, 1, 72, False), ([90, 5], [30, 200], 2, 2, 128, True),
+    ([5, 0, 9], [0, 7, 300], 3, 1, 40, False), ([300], None, 6, 2, 24, True), ([31], [500], 1, 1, 200, True),
+    ([260], [129], 2, 1, 33, True), ([100, 28], None, 2, 1, 7, True), ([513], None, 2, 1, 256, True), ([1] * 40, None, 2, 1, 64, True),
+    ([3], [2000], 2, 2, 128, False), ([700], None, 2, 1, 128, True)]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+@pytest.mark.parametrize("lq,lk,heads,kv,dim,causal", ATTN)
+def test_attention(kind, lq, lk, heads, kv, dim, causal):
+    rng = np.random.default_rng(sum(lq) + dim)
+    cq, ck = _offsets(lq), _offsets(lk or lq)
+    # (rows behind the last sequence)
+    q, k, v, do = _inputs(rng, int(cq[-1]) + 3, int(ck[-1]) + 5, heads, kv, dim, kind)
+    for x in (q, do):
+        x[int(cq[-1]):] = float("nan")
+    for x in (k, v):
+        x[int(ck[-1]):] = float("nan")
+    o, lse, g = _check_attention(q, k, v, do, cq, ck, causal, None, kind)
+    # bitwise the same for other layouts: heads outside, a part of wider rows, odd addresses
+    cu = (_cu(cq), _cu(ck))
+    nq, nk = int(cq[-1]), int(ck[-1])
+    q2, k2, v2, do2 = (_heads_first(x) for x in (q, k, v, do))
+    o2, lse2 = M.ma_attention_forward(q2, k2, v2, *cu, causal=causal, out=_heads_first(torch.zeros_like(q)))
+    assert torch.equal(o2[:nq], o[:nq]) and torch.equal(lse2[:, :nq], lse[:, :nq])
+    wide = [torch.zeros((x.shape[0], x.shape[1], dim + 3), dtype=x.dtype, device="cuda")[:, :, 1:1 + dim] for x in (q, k, v, do)]
+    for a, b in zip(wide, (q, k, v, do)):
+        a.copy_(b)
+    o3, _ = M.ma_attention_forward(*wide[:3], *cu, causal=causal)
+    assert torch.equal(o3[:nq], o[:nq])
+    g2 = M.ma_attention_backward(do2, q2, k2, v2, o2, lse2, *cu, causal=causal)
+    g3 = M.ma_attention_backward(wide[3], *wide[:3], o3, lse, *cu, causal=causal)
+    for a, b, c, n in zip(g, g2, g3, (nq, nk, nk)):
+        assert torch.equal(a[:n], b[:n]) and torch.equal(a[:n], c[:n])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+def test_attention_one_sequence_without_offsets(kind):
+    rng = np.random.default_rng(2)
+    q, k, v, do = _inputs(rng, 150, 190, 4, 2, 64, kind)
+    cu = (_cu(_offsets([150])), _cu(_offsets([190])))
+    for causal in (True, False):
+        o, lse = M.ma_attention_forward(q, k, v, causal=causal, scale=0.3)
+        o2, lse2 = M.ma_attention_forward(q, k, v, *cu, causal=causal, scale=0.3)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+        for a, b in zip(M.ma_attention_backward(do, q, k, v, o, lse, causal=causal, scale=0.3),
+                        M.ma_attention_backward(do, q, k, v, o, lse, *cu, causal=causal, scale=0.3)):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+def test_attention_sharp_rows(kind):
+    """Scores far apart, rising and falling along the keys (the softmax's reference moves at every tile, or
+    never), and one key that takes everything."""
+    rng = np.random.default_rng(5)
+    n, d = 400, 64
+    q, k, v, do = _inputs(rng, n, n, 3, 3, d, kind)
+    ramp = torch.linspace(-30, 30, n, device="cuda")
+    q[:, :, 0] = 8.0
+    k[:, 0, 0], k[:, 1, 0], k[:, 2, 0] = ramp, -ramp, 0.0
+    k[17, 2, 0] = 60.0
+    _check_attention(q, k, v, do, _offsets([n]), _offsets([n]), False, 0.25, kind)
+    _check_attention(q, k, v, do, _offsets([150, 250]), _offsets([150, 250]), True, 0.25, kind)
+
+
+def test_attention_nan_stays_in_its_sequence():
+    rng = np.random.default_rng(6)
+    lens = [40, 100, 60]
+    cq = _offsets(lens)
+    q, k, v, do = _inputs(rng, 200, 200, 2, 1, 64, "bf16")
+    o, lse = M.ma_attention_forward(q, k, v, _cu(cq), _cu(cq))
+    g = M.ma_attention_backward(do, q, k, v, o, lse, _cu(cq), _cu(cq))
+    for bad in (float("nan"), float("inf")):
+        q2, k2, v2, do2 = (x.clone() for x in (q, k, v, do))
+        for x in (q2, k2, v2, do2):
+            x[60:130] = bad
+        o2, lse2 = M.ma_attention_forward(q2, k2, v2, _cu(cq), _cu(cq))
+        g2 = M.ma_attention_backward(do2, q2, k2, v2, o2, lse2, _cu(cq), _cu(cq))
+        for s in (slice(0, 40), slice(140, 200)):
+            assert torch.equal(o2[s], o[s]) and torch.equal(lse2[:, s], lse[:, s])
+            for a, b in zip(g2, g):
+                assert torch.equal(a[s], b[s])
+        assert torch.isnan(o2[70:140]).all()
+
+
+def test_attention_bad_offsets_stay_inside():
+    """Offsets that fall, are negative or too large: what is computed is not defined, but nothing outside the
+    arrays is touched."""
+    rng = np.random.default_rng(7)
+    for cu in ([0, 500, 100], [-7, 30, 100], [50, 20, 90], [0, 2 ** 31 - 1, 5], [90, 100, 300]):
+        c = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        q, k, v, do = _inputs(rng, 100, 100, 2, 1, 64, "bf16")
+        guard = torch.full((300, 2, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+        o, lse = M.ma_attention_forward(q, k, v, c, c, out=guard[100:200])
+        M.ma_attention_backward(do, q, k, v, o, lse.nan_to_num(), c, c)
+        assert torch.all(guard[:100] == 7.0) and torch.all(guard[200:] == 7.0)
+
+
+def test_attention_gradient_against_differences():
+    rng = np.random.default_rng(9)
+    n, heads, kv, d = 20, 2, 1, 8
+    x = [rng.standard_normal(s) for s in ((n, heads, d), (n, kv, d), (n, kv, d))]
+    c = rng.standard_normal((n, heads, d))
+    cq = _offsets([12, 8])
+    t = [_dev(a) for a in x]
+    o, lse = M.ma_attention_forward(*t, _cu(cq), _cu(cq))
+    g = [_f64(a) for a in M.ma_attention_backward(_dev(c), *t, o, lse, _cu(cq), _cu(cq))]
+
+    def f(y):
+        return np.sum(c * R.attention(*y, cq, cq, True, d ** -0.5, "fp32")[0])
+
+    for seed in range(4):
+        r = np.random.default_rng(seed)
+        u = [r.standard_normal(a.shape) for a in x]
+        slope = (f([a + 1e-5 * b for a, b in zip(x, u)]) - f([a - 1e-5 * b for a, b in zip(x, u)])) / 2e-5
+        got = sum(np.sum(a * b) for a, b in zip(g, u))
+        # some 640 terms of about 1, each off by a few 2^-24 of its parts
+        assert abs(got - slope) < 1e-3 * max(1.0, abs(slope))
+
+
+def test_attention_empty():
+    e = torch.zeros((0, 2, 64), device="cuda")
+    z = torch.zeros(1, dtype=torch.int32, device="cuda")
+    o, lse = M.ma_attention_forward(e, e, e)
+    assert o.shape == (0, 2, 64) and lse.shape == (2, 0)
+    assert M.ma_attention_backward(e, e, e, e, o, lse)[0].shape == (0, 2, 64)
+    x = torch.randn(5, 2, 64, device="cuda")
+    o, lse = M.ma_attention_forward(x, x, x, z, z, out=torch.full_like(x, 7.0))        # no sequence
+    assert torch.all(o == 7.0)
+    o, lse = M.ma_attention_forward(x, e, e, causal=False)                              # no keys
+    assert torch.all(o == 0) and torch.all(lse == -float("inf"))
+    dq, dk, dv = M.ma_attention_backward(x, x, e, e, o, lse, causal=False)
+    assert torch.all(dq == 0) and dk.shape == (0, 2, 64)
+    dq, dk, dv = M.ma_attention_backward(e, e, x, x, e, lse[:, :0].contiguous(), causal=False)   # no queries
+    assert torch.all(dk == 0) and torch.all(dv == 0)
