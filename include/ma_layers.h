@@ -183,13 +183,17 @@ typedef struct ma_attention {
     ma_heads dout, dq, dk, dv; /* backward only */
 } ma_attention;
 
+/* Bytes of workspace (256-byte aligned; 0: none, NULL may be passed) a forward call needs: calls
+ * of few rows cut their walk over the keys into pieces and join them.  Errors: INVALID_ARG, SHAPE. */
+int ma_attention_forward_workspace_size(const ma_attention* a, size_t* bytes);
+
 /* o = softmax(scale q k^T) v and lse.  A query that sees no key has o = 0 and lse =
  * -infinity.  Sums, maxima and lse are float32; a bfloat16 call rounds the probabilities
  * to bfloat16 (at up to 2^8 of the row's largest) for their product with v, as its matrix
  * instructions take them.  A NaN or infinity in a sequence may make that head of that whole
  * sequence NaN, and reaches no other.  Errors: INVALID_ARG, SHAPE (n_queries * heads or
- * n_keys * heads above 2^30, n_seqs * heads above 2^22), HIP. */
-int ma_attention_forward(const ma_attention* a, void* stream);
+ * n_keys * heads above 2^28, n_seqs * heads above 2^22), WORKSPACE, HIP. */
+int ma_attention_forward(const ma_attention* a, void* workspace, size_t ws_bytes, void* stream);
 
 /* Bytes of workspace (256-byte aligned) a backward call needs.  Errors: INVALID_ARG, SHAPE. */
 int ma_attention_backward_workspace_size(const ma_attention* a, size_t* bytes);
@@ -197,7 +201,7 @@ int ma_attention_backward_workspace_size(const ma_attention* a, size_t* bytes);
 /* dq, dk and dv from dout and the forward pass' o and lse.  dk and dv sum over the query heads
  * that share them; keys that no query sees get 0.  The probabilities and the scores' gradients
  * of a bfloat16 call are rounded to bfloat16 for their products.  No atomics: reruns are
- * bitwise equal.  Errors: as ma_attention_forward, WORKSPACE. */
+ * bitwise equal.  Errors: as ma_attention_forward. */
 int ma_attention_backward(const ma_attention* a, void* workspace, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus

@@ -46,7 +46,7 @@ _GRADS = ("ActCheckpoint", "EmbeddingGrad", "LinearGrad", "ma_act_pack", "ma_act
 _LAYERS = ("Rotary", "ma_rms_norm_forward", "ma_rms_norm_backward", "ma_rms_norm_backward_workspace_size",
            "ma_rotary", "ma_token_logprob_forward", "ma_token_logprob_backward",
            "ma_token_logprob_workspace_size", "ma_attention_forward", "ma_attention_backward",
-           "ma_attention_backward_workspace_size")
+           "ma_attention_forward_workspace_size", "ma_attention_backward_workspace_size")
 
 
 def _torch_installed() -> bool:

@@ -151,7 +151,8 @@ LAYER_SIGNATURES = [
                                            _P, _SZ, _P]),
     ("ma_token_logprob_backward", C.c_int, [_P, _I32, _I64, _I64, _I64, _P, _I32, _F64, _P, _P, _P, _P, _P, _I32,
                                             _I64, _P]),
-    ("ma_attention_forward", C.c_int, [C.POINTER(ma_attention), _P]),
+    ("ma_attention_forward_workspace_size", C.c_int, [C.POINTER(ma_attention), C.POINTER(_SZ)]),
+    ("ma_attention_forward", C.c_int, [C.POINTER(ma_attention), _P, _SZ, _P]),
     ("ma_attention_backward_workspace_size", C.c_int, [C.POINTER(ma_attention), C.POINTER(_SZ)]),
     ("ma_attention_backward", C.c_int, [C.POINTER(ma_attention), _P, _SZ, _P]),
 ]

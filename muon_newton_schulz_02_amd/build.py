@@ -26,7 +26,7 @@ BUILD_DIR = os.path.join(HERE, "_build")
 
 SOURCES = ["plan.cpp", "step.cpp", "elementwise.hip", "ns_gemm.hip", "noalloc.hip", "grads.cpp",
            "act8.hip", "embedding.hip", "linear_grad.hip", "layers.cpp", "norm.hip", "rotary.hip",
-           "logprob.hip", "attention.hip"]
+           "logprob.hip", "attention.hip", "attention_dq.hip", "attention_dkv.hip"]
 PEAKS_SOURCES = ["peaks.hip"]
 PEAKS_LIB = os.path.join(HERE, "libma_peaks.so")
 

@@ -1,0 +1,158 @@
+// The gradients of the keys and values: a workgroup takes 32 key rows a wave of one key head
+// and walks the queries of the heads that share it, recomputing the scores S = Q K^T and P =
+// 2^(S - lse), with dP = dout V^T and dS = P (dP - delta) summing dv^T += dout^T P and dk^T +=
+// Q^T dS: four products a tile.
+
+#include <hip/hip_runtime.h>
+
+#include "attention_tile.h"
+
+namespace ma {
+namespace {
+
+// Whether a workgroup's rows of V stay in LDS instead of registers, which then fit two waves.
+template <typename T, int DP>
+constexpr bool kStage = DP * (int)sizeof(T) == 256;
+
+template <typename T, int DP, bool AL, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, (kPer<T, DP>)) void k_attention_dkv(AttnArgs a, AttnGrid grid) {
+    constexpr int BLOCK = 32 * WAVES, QT = 32, RING = 2;
+    using QTile = Tile<T, DP, QT, 64 * WAVES>;
+    using VTile = Tile<T, DP, BLOCK, 64 * WAVES>;
+    constexpr bool STAGE = kStage<T, DP>;
+    __shared__ __attribute__((aligned(1024))) char lds[RING][2][QTile::kBytes];
+    __shared__ __attribute__((aligned(1024))) char vlds[STAGE ? VTile::kBytes : 16];
+    __shared__ __attribute__((aligned(256))) float stat[RING][WAVES][2 * QT];
+    const Job j = job_of<true, BLOCK>(a, grid);        // (its head is a key head)
+    if (!j.any) return;
+    const int lane = threadIdx.x & 63, h = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int group = a.heads / a.kv_heads;
+    const int key = j.row0 + 32 * wave + (lane & 31);
+    const Rows<T> vx = rows_of<T>(a.v, j.head, j.k_at, j.k_len, a.dim);
+    const Own<T, DP, AL> kf(rows_of<T>(a.k, j.head, j.k_at, j.k_len, a.dim), key);
+    const Own<T, DP, AL, kHold<T, DP> && !STAGE> vown(vx, key);
+    if constexpr (STAGE) {
+        const typename VTile::template Copy<AL> copy_v(vx);
+        copy_v(vlds, vx, j.row0);
+    }
+    auto vf = [&](int d) {
+        if constexpr (STAGE) return VTile::rows(vlds, 32 * wave, d);
+        else return vown(d);
+    };
+    f32x16 dk[DP / 32], dv[DP / 32];
+#pragma unroll
+    for (int b = 0; b < DP / 32; ++b) dk[b] = dv[b] = zero16();
+    const float k = a.scale * kLog2e;
+    // the first tile with a query that sees this workgroup's first key
+    const int off = j.k_len - j.q_len;
+    const int first = a.causal ? max(0, j.row0 - off) / QT : 0;
+    const int per = max(0, (j.q_len + QT - 1) / QT - first);
+    const Share sh(per * group, j.piece, grid.pieces);
+    const typename QTile::template Copy<AL> copy_q(rows_of<T>(a.q, 0, 0, 0, a.dim)), copy_d(rows_of<T>(a.dout, 0, 0, 0, a.dim));
+    // the next tile to copy: its number, its head of the group, and which of the head's it is
+    int next = sh.first, nhead = per ? sh.first / per : 0, ntile = sh.first - nhead * per, ahead = 0;
+    auto fetch = [&]() {
+        const bool in = next < sh.last;          // (past the last tile the copies are empty)
+        const int head = j.head * group + (in ? nhead : 0), q0 = in ? (first + ntile) * QT : j.q_len;
+        copy_q(lds[ahead][0], rows_of<T>(a.q, head, j.q_at, j.q_len, a.dim), q0);
+        copy_d(lds[ahead][1], rows_of<T>(a.dout, head, j.q_at, j.q_len, a.dim), q0);
+        const float* s = a.stats + ((int64_t)head * a.n_queries + j.q_at + q0) * 2;
+        dma4(make_rsrc(s, (int64_t)(j.q_len - q0) * 8), lds_addr(stat[ahead][wave]), lane * 4u);
+        ahead ^= 1;
+        ++next;
+        if (++ntile == per) {
+            ntile = 0;
+            ++nhead;
+        }
+    };
+    int slot = 0;
+    auto tile = [&](int n, auto part) {
+        copies_barrier<0>();
+        fetch();
+        const char* qt = lds[slot][0];
+        const char* dt = lds[slot][1];
+        const float* sd = stat[slot][wave];
+        slot ^= 1;
+        f32x16 s = zero16(), p = zero16();
+#pragma unroll
+        for (int d = 0; d < DP / 16; ++d) s = mma(QTile::rows(qt, 0, d), kf(d), s);
+#pragma unroll
+        for (int d = 0; d < DP / 16; ++d) p = mma(QTile::rows(dt, 0, d), vf(d), p);
+        // (operands of the next products loaded up here would not fit the registers)
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            // lse and delta of four queries
+            const f32x4 x = *reinterpret_cast<const f32x4*>(sd + 16 * g + 8 * h);
+            const f32x4 y = *reinterpret_cast<const f32x4*>(sd + 16 * g + 8 * h + 4);
+            const float l4[4] = {x[0], x[2], y[0], y[2]}, d4[4] = {x[1], x[3], y[1], y[3]};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = 4 * g + e;
+                s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], k, -l4[e]));
+                p[i] = s[i] * (p[i] - d4[e]);
+            }
+        }
+        if constexpr (decltype(part)::value) {
+            // the first query of the tile that sees this lane's key
+            const int from = key - off - (first + n) * QT;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const bool in = result_row(i, h) >= from;
+                s[i] = in ? s[i] : 0.f;
+                p[i] = in ? p[i] : 0.f;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const Frag<T> fs = frag_of<T>(s, u);
+#pragma unroll
+            for (int b = 0; b < DP / 32; ++b) dv[b] = mma(QTile::cols(dt, 16 * u, 32 * b), fs, dv[b]);
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const Frag<T> fp = frag_of<T>(p, u);
+#pragma unroll
+            for (int b = 0; b < DP / 32; ++b) dk[b] = mma(QTile::cols(qt, 16 * u, 32 * b), fp, dk[b]);
+        }
+    };
+    if (sh.first < sh.last) {
+        // of a head's tiles the first `partial` hold queries that do not see every key of the
+        // workgroup
+        const int partial = a.causal ? max(0, (j.row0 + BLOCK - 1 - off + QT - 1) / QT - first) : 0;
+        int n = ntile;
+        fetch();
+        for (int t = sh.first; t < sh.last;) {
+            const int stop = min(per, n + sh.last - t);
+            t += stop - n;
+            for (; n < min(stop, partial); ++n) tile(n, std::true_type{});
+            for (; n < stop; ++n) tile(n, std::false_type{});
+            n = 0;
+        }
+    }
+    if (key >= j.k_len) return;
+    const int64_t row = (int64_t)j.k_at + key;
+    if (grid.pieces > 1) {
+        store_row<float, DP / 32>(part_row(a.parts, j.piece, a.kv_heads, j.head, a.n_keys, row, a.dim), a.dim, dk,
+                                  a.scale, a.dim % 4 == 0);
+        store_row<float, DP / 32>(part_row(a.parts, grid.pieces + j.piece, a.kv_heads, j.head, a.n_keys, row, a.dim), a.dim,
+                                  dv, 1.f, a.dim % 4 == 0);
+    } else {
+        store_row<T, DP / 32>(row_of<T>(a.dk, j.head, row), a.dim, dk, a.scale, AL);
+        store_row<T, DP / 32>(row_of<T>(a.dv, j.head, row), a.dim, dv, 1.f, AL);
+    }
+}
+
+}  // namespace
+
+int launch_attention_dkv(const AttnArgs& a, const AttnSplit& sp, bool al, void* stream) {
+    return by_kind(a, al, sp.waves, [&](auto t, auto dp, auto w, auto wv) {
+        constexpr int WAVES = decltype(wv)::value;
+        const AttnGrid g = grid_of(a.n_keys, a.n_seqs, a.kv_heads, WAVES, sp.pieces);
+        hipLaunchKernelGGL((k_attention_dkv<decltype(t), decltype(dp)::value, decltype(w)::value, WAVES>),
+                           dim3((unsigned)g.slots * a.kv_heads * g.pieces), dim3(64 * WAVES), 0, (hipStream_t)stream, a, g);
+    });
+}
+
+}  // namespace ma

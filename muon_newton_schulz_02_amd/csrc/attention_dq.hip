@@ -1,0 +1,101 @@
+// The gradient of the queries: a workgroup takes 32 query rows a wave of one head and walks
+// the keys, recomputing the scores S^T = K Q^T and P^T = 2^(S^T - lse), with dP^T = V dout^T
+// and dS^T = P^T (dP^T - delta) summing dq^T += K^T dS^T: three products a tile.
+
+#include <hip/hip_runtime.h>
+
+#include "attention_tile.h"
+
+namespace ma {
+namespace {
+
+// The copies of tile t + RING - 1 are under way while tile t is worked on.
+template <typename T, int DP>
+constexpr int kRing = DP * (int)sizeof(T) <= 256 ? 3 : 2;
+template <typename T, int DP, bool AL, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, (kPer<T, DP>)) void k_attention_dq(AttnArgs a, AttnGrid grid) {
+    constexpr int BLOCK = 32 * WAVES, KV = 32, RING = kRing<T, DP>;
+    using KT = Tile<T, DP, KV, 64 * WAVES>;
+    constexpr int kTileCopies = AL ? 2 * KT::kCopies : 0;
+    __shared__ __attribute__((aligned(1024))) char lds[RING][2][KT::kBytes];
+    const Job j = job_of<false, BLOCK>(a, grid);
+    if (!j.any) return;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, h = lane >> 5;
+    const int kvh = j.head / (a.heads / a.kv_heads);
+    const Rows<T> kx = rows_of<T>(a.k, kvh, j.k_at, j.k_len, a.dim);
+    const Rows<T> vx = rows_of<T>(a.v, kvh, j.k_at, j.k_len, a.dim);
+    const int q = j.row0 + 32 * wave + (lane & 31);
+    const Own<T, DP, AL> qf(rows_of<T>(a.q, j.head, j.q_at, j.q_len, a.dim), q);
+    const Own<T, DP, AL> df(rows_of<T>(a.dout, j.head, j.q_at, j.q_len, a.dim), q);
+    const float* st = a.stats + ((int64_t)j.head * a.n_queries + j.q_at + q) * 2;
+    const float ls = q < j.q_len ? st[0] : kInf, delta = q < j.q_len ? st[1] : 0.f;
+
+    f32x16 dq[DP / 32];
+#pragma unroll
+    for (int b = 0; b < DP / 32; ++b) dq[b] = zero16();
+    const float k = a.scale * kLog2e;
+    const int end = min(j.row0 + BLOCK, j.q_len) - 1;
+    const Share sh(max(0, seen(a, j, end) + KV - 1) / KV, j.piece, grid.pieces);
+    const int sees = seen(a, j, q);
+    const typename KT::template Copy<AL> copy_k(kx), copy_v(vx);
+    int slot = 0, ahead = 0;
+    // (past the last tile the copies are empty)
+    auto fetch = [&](int t) {
+        const int row = t < sh.last ? t * KV : j.k_len;
+        copy_k(lds[ahead][0], kx, row);
+        copy_v(lds[ahead][1], vx, row);
+        ahead = ahead == RING - 1 ? 0 : ahead + 1;
+    };
+    auto tile = [&](int t, auto part) {
+        copies_barrier<(RING - 2) * kTileCopies>();
+        fetch(t + RING - 1);
+        const char* kt = lds[slot][0];
+        const char* vt = lds[slot][1];
+        slot = slot == RING - 1 ? 0 : slot + 1;
+        f32x16 s = zero16(), p = zero16();
+#pragma unroll
+        for (int d = 0; d < DP / 16; ++d) s = mma(KT::rows(kt, 0, d), qf(d), s);
+#pragma unroll
+        for (int d = 0; d < DP / 16; ++d) p = mma(KT::rows(vt, 0, d), df(d), p);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) p[i] = __builtin_amdgcn_exp2f(fmaf(s[i], k, -ls)) * (p[i] - delta);
+        if constexpr (decltype(part)::value) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) p[i] = t * KV + result_row(i, h) < sees ? p[i] : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const Frag<T> f = frag_of<T>(p, u);
+#pragma unroll
+            for (int b = 0; b < DP / 32; ++b) dq[b] = mma(KT::cols(kt, 16 * u, 32 * b), f, dq[b]);
+        }
+    };
+    if (sh.first < sh.last) {
+        for (int i = 0; i < RING - 1; ++i) fetch(sh.first + i);
+        // tiles that every row of the workgroup sees whole, and the others
+        const int whole = min(max(seen(a, j, j.row0), 0) / KV, sh.last);
+        int t = sh.first;
+        for (; t < whole; ++t) tile(t, std::false_type{});
+        for (; t < sh.last; ++t) tile(t, std::true_type{});
+    }
+    if (q >= j.q_len) return;
+    const int64_t row = (int64_t)j.q_at + q;
+    if (grid.pieces > 1)
+        store_row<float, DP / 32>(part_row(a.parts, j.piece, a.heads, j.head, a.n_queries, row, a.dim), a.dim, dq,
+                                  a.scale, a.dim % 4 == 0);
+    else
+        store_row<T, DP / 32>(row_of<T>(a.dq, j.head, row), a.dim, dq, a.scale, AL);
+}
+
+}  // namespace
+
+int launch_attention_dq(const AttnArgs& a, const AttnSplit& sp, bool al, void* stream) {
+    return by_kind(a, al, sp.waves, [&](auto t, auto dp, auto w, auto wv) {
+        constexpr int WAVES = decltype(wv)::value;
+        const AttnGrid g = grid_of(a.n_queries, a.n_seqs, a.heads, WAVES, sp.pieces);
+        hipLaunchKernelGGL((k_attention_dq<decltype(t), decltype(dp)::value, decltype(w)::value, WAVES>),
+                           dim3((unsigned)g.slots * a.heads * g.pieces), dim3(64 * WAVES), 0, (hipStream_t)stream, a, g);
+    });
+}
+
+}  // namespace ma

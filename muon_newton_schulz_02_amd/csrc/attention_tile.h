@@ -87,11 +87,20 @@ __device__ __forceinline__ void dma16(u32x4 rsrc, uint32_t lds, uint32_t voff) {
                  : "memory");
 }
 
-// All of this wave's copies have landed, and every wave's LDS reads before are done.
+// 4 bytes per lane, the same way.
+__device__ __forceinline__ void dma4(u32x4 rsrc, uint32_t lds, uint32_t voff) {
+    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+                 :
+                 : "s"(lds), "v"(voff), "s"(rsrc)
+                 : "memory");
+}
+
+// All but the last N of this wave's copies have landed, its LDS accesses are done, and so
+// is every wave's.  (A release fence would wait for all copies.)
+template <int N>
 __device__ __forceinline__ void copies_barrier() {
     __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(0x0F70);          // vmcnt(0)
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
+    __builtin_amdgcn_s_waitcnt((N & 15) | 0x70 | (N >> 4 << 14));      // vmcnt(N) lgkmcnt(0)
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
     __builtin_amdgcn_sched_barrier(0);
@@ -122,47 +131,48 @@ struct Tile {
         else return (row >> 1 & 1) << 2 | (row >> 2 & 3);
     }
 
-    // Where this thread's copy i comes from: its row of the tile and first column.
-    struct From {
-        int row, col;
-    };
-    __device__ static __forceinline__ From from(int i) {
-        const int s = i * NT + (int)threadIdx.x, row = s / kChunks;
-        return {row, ((s % kChunks) ^ turn(row)) * (16 / (int)sizeof(T))};
-    }
-
-    // Copies rows [row0, row0 + ROWS) of x into `lds`; rows past x.len and columns past x.dim
-    // become zeros.  AL: rows and dim are whole 16-byte chunks, and the copies go straight into
-    // LDS (they have landed after copies_barrier); extents within a tile stay below 2^31.
+    // Copies of rows of one array into LDS by all threads.  AL: rows and dim are whole 16-byte
+    // chunks, rows do not overlap and extents within a tile stay below 2^31: the copies go straight
+    // into LDS (they have landed after copies_barrier).
     template <bool AL>
-    __device__ static __forceinline__ void copy(char* lds, const Rows<T>& x, int row0) {
-        const int left = min(x.len - row0, ROWS);
-        const T* base = x.p + (int64_t)row0 * x.stride;
-        if constexpr (AL) {
-            const u32x4 rsrc =
-                make_rsrc(base, left > 0 ? ((int64_t)(left - 1) * x.stride + x.dim) * (int64_t)sizeof(T) : 0);
-            const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 1024u;
+    struct Copy {
+        uint32_t from[AL ? kCopies : 1];         // byte offset of this thread's chunk; past any extent where there is none
+        __device__ __forceinline__ explicit Copy(const Rows<T>& x) {
+            if constexpr (AL)
 #pragma unroll
-            for (int i = 0; i < kCopies; ++i) {
-                const From f = from(i);
-                const uint32_t at = (uint32_t)f.row * (uint32_t)(x.stride * sizeof(T)) + (uint32_t)(f.col * sizeof(T));
-                dma16(rsrc, lds_addr(lds) + (uint32_t)(i * NT * 16) + wave,
-                      f.col < x.dim && f.row < left ? at : 0x80000000u);
-            }
-        } else {
+                for (int i = 0; i < kCopies; ++i) {
+                    const int s = i * NT + (int)threadIdx.x, row = s / kChunks;
+                    const int col = ((s % kChunks) ^ turn(row)) * (16 / (int)sizeof(T));
+                    from[i] = col < x.dim ? (uint32_t)row * (uint32_t)(x.stride * sizeof(T)) + (uint32_t)(col * sizeof(T))
+                                          : 0x80000000u;
+                }
+        }
+        // Rows [row0, row0 + ROWS) of x into `lds`; rows past x.len and columns past x.dim become
+        // zeros.
+        __device__ __forceinline__ void operator()(char* lds, const Rows<T>& x, int row0) const {
+            const int left = min(x.len - row0, ROWS);
+            const T* base = x.p + (int64_t)row0 * x.stride;
+            if constexpr (AL) {
+                const u32x4 rsrc =
+                    make_rsrc(base, left > 0 ? ((int64_t)(left - 1) * x.stride + x.dim) * (int64_t)sizeof(T) : 0);
+                const uint32_t at = lds_addr(lds) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 1024u;
 #pragma unroll
-            for (int i = 0; i < kCopies; ++i) {
-                const From f = from(i);
-                const T* p = base + (int64_t)f.row * x.stride + f.col;
-                T v[16 / sizeof(T)];
+                for (int i = 0; i < kCopies; ++i) dma16(rsrc, at + (uint32_t)(i * NT * 16), from[i]);
+            } else {
 #pragma unroll
-                for (int e = 0; e < 16 / (int)sizeof(T); ++e)
-                    v[e] = f.row < left && f.col + e < x.dim ? p[e] : (T)0.f;
-                *reinterpret_cast<u32x4*>(lds + (i * NT + (int)threadIdx.x) * 16) =
-                    __builtin_bit_cast(u32x4, v);
+                for (int i = 0; i < kCopies; ++i) {
+                    const int s = i * NT + (int)threadIdx.x, row = s / kChunks;
+                    const int col = ((s % kChunks) ^ turn(row)) * (16 / (int)sizeof(T));
+                    const T* p = base + (int64_t)row * x.stride + col;
+                    T v[16 / sizeof(T)];
+#pragma unroll
+                    for (int e = 0; e < 16 / (int)sizeof(T); ++e)
+                        v[e] = row < left && col + e < x.dim ? p[e] : (T)0.f;
+                    *reinterpret_cast<u32x4*>(lds + s * 16) = __builtin_bit_cast(u32x4, v);
+                }
             }
         }
-    }
+    };
 
     // Straight operand: row row0 + l (row0 a multiple of 32), columns 16 step + 8 h + j.
     __device__ static __forceinline__ Frag<T> rows(const char* lds, int row0, int step) {
@@ -209,21 +219,24 @@ struct Tile {
     }
 };
 
-// Straight operands of row `row` of x (zeros past its length and dim), from global memory.
+// The straight operand of step s of row `row` of x (zeros past its length and dim), from
+// global memory; all of them.
+template <typename T, bool AL>
+__device__ __forceinline__ Frag<T> load_step(const Rows<T>& x, int row, int s) {
+    const int col = 16 * s + 8 * ((threadIdx.x & 63) >> 5);
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = 0.f;
+    if (row < x.len && col < x.dim) load_unit<T, AL>(x.p + (int64_t)row * x.stride + col, x.dim - col, v);
+    Frag<T> f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = (T)v[e];
+    return f;
+}
 template <typename T, int DP, bool AL>
 __device__ __forceinline__ void load_row(const Rows<T>& x, int row, Frag<T>* f) {
-    const int h = (threadIdx.x & 63) >> 5;
-    const T* p = x.p + (int64_t)row * x.stride;
 #pragma unroll
-    for (int s = 0; s < DP / 16; ++s) {
-        const int col = 16 * s + 8 * h;
-        float v[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = 0.f;
-        if (row < x.len && col < x.dim) load_unit<T, AL>(p + col, x.dim - col, v);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[s][e] = (T)v[e];
-    }
+    for (int s = 0; s < DP / 16; ++s) f[s] = load_step<T, AL>(x, row, s);
 }
 
 // Stores a wave's transposed results (columns of x by rows of 32 at a time) as row `row`:
@@ -277,6 +290,191 @@ __device__ __forceinline__ Place place_of(const int32_t* cu, int n_seqs, int64_t
         else hi = mid - 1;
     }
     return {lo, slot - (seq_at(cu, lo, n_seqs, total) / tile + lo)};
+}
+
+// The same in falling order of work: slot 0 is a tile of the largest number, tiles of one number
+// (counted from a sequence's first, from 1) are neighbours, in the order of the sequences.  A tile
+// of number r lies behind the sum over sequences of max(0, tiles - r) others, which a wave
+// counts and searches for the slot's r.
+constexpr int kOrderedSeqs = 512;
+__device__ __forceinline__ Place ordered_place_of(const int32_t* cu, int n_seqs, int64_t total, int tile, int slot) {
+    const int lane = threadIdx.x & 63;
+    int own[kOrderedSeqs / 64], most = 0;
+#pragma unroll
+    for (int i = 0; i < kOrderedSeqs / 64; ++i) {
+        const int s = 64 * i + lane;
+        own[i] = s < n_seqs ? max(0, seq_at(cu, s + 1, n_seqs, total) - seq_at(cu, s, n_seqs, total) + tile - 1) / tile : 0;
+        most = max(most, own[i]);
+    }
+    auto all = [](int v) {
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m, 64);
+        return v;
+    };
+    auto above = [&](int r) {
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < kOrderedSeqs / 64; ++i) n += max(0, own[i] - r);
+        return all(n);
+    };
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) most = max(most, __shfl_xor(most, m, 64));
+    int lo = 0, hi = most;               // the smallest r with above(r) <= slot
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (above(mid) <= slot) hi = mid;
+        else lo = mid + 1;
+    }
+    if (lo == 0) return {0, -1};         // more slots than tiles
+    int left = slot - above(lo);         // which of the sequences with lo tiles or more
+    Place p = {0, -1};
+#pragma unroll
+    for (int i = 0; i < kOrderedSeqs / 64; ++i) {
+        const uint64_t who = __ballot(own[i] >= lo);
+        const int n = __popcll(who);
+        if (p.tile < 0 && left < n) {
+            uint64_t w = who;
+            for (; left > 0; --left) w &= w - 1;
+            p = {64 * i + __ffsll((unsigned long long)w) - 1, lo - 1};
+        } else if (p.tile < 0) {
+            left -= n;
+        }
+    }
+    return p;
+}
+
+// How a launch's workgroups are laid out.
+struct AttnGrid {
+    int32_t slots, pieces;
+    bool ordered;
+};
+
+// One workgroup's sequence, head, first row and piece of its walk.
+struct Job {
+    int q_at, q_len, k_at, k_len, head, row0, piece;
+    bool any;
+};
+template <bool KEYS, int BLOCK>
+__device__ __forceinline__ Job job_of(const AttnArgs& a, const AttnGrid& g) {
+    Job j;
+    // Heads are neighbours in the launch, those that share keys a multiple of the key heads
+    // apart: workgroups go to the XCDs in turn, so fewer XCDs read each key head.
+    const int heads = KEYS ? a.kv_heads : a.heads;
+    const int head = blockIdx.x % heads, rest = blockIdx.x / heads;
+    const int slot = rest % g.slots;
+    j.head = KEYS ? head : head % a.kv_heads * (a.heads / a.kv_heads) + head / a.kv_heads;
+    j.piece = rest / g.slots;
+    const int32_t* cu = KEYS ? a.cu_k : a.cu_q;
+    const int64_t total = KEYS ? a.n_keys : a.n_queries;
+    Place p = g.ordered ? ordered_place_of(cu, a.n_seqs, total, BLOCK, slot) : place_of(cu, a.n_seqs, total, BLOCK, slot);
+    if (KEYS && g.ordered && p.tile >= 0) {
+        // (the first keys have the most queries behind them)
+        const int n = seq_at(cu, p.seq + 1, a.n_seqs, total) - seq_at(cu, p.seq, a.n_seqs, total);
+        p.tile = (n + BLOCK - 1) / BLOCK - 1 - p.tile;
+    }
+    // (the same in every lane: kept in scalar registers, where buffer descriptors need them)
+    p.seq = __builtin_amdgcn_readfirstlane(p.seq);
+    p.tile = __builtin_amdgcn_readfirstlane(p.tile);
+    j.q_at = seq_at(a.cu_q, p.seq, a.n_seqs, a.n_queries);
+    j.q_len = max(0, seq_at(a.cu_q, p.seq + 1, a.n_seqs, a.n_queries) - j.q_at);
+    j.k_at = seq_at(a.cu_k, p.seq, a.n_seqs, a.n_keys);
+    j.k_len = max(0, seq_at(a.cu_k, p.seq + 1, a.n_seqs, a.n_keys) - j.k_at);
+    j.any = p.tile >= 0 && (int64_t)p.tile * BLOCK < (KEYS ? j.k_len : j.q_len);
+    j.row0 = j.any ? p.tile * BLOCK : 0;
+    return j;
+}
+
+template <typename T>
+__device__ __forceinline__ Rows<T> rows_of(const AttnArray& x, int head, int at, int len, int dim) {
+    return {static_cast<const T*>(x.p) + (int64_t)at * x.token + (int64_t)head * x.head, x.token, len, dim};
+}
+template <typename T>
+__device__ __forceinline__ T* row_of(const AttnArray& x, int head, int64_t row) {
+    return static_cast<T*>(const_cast<void*>(x.p)) + row * x.token + (int64_t)head * x.head;
+}
+
+// Keys that query `q` sees: those before this one.
+__device__ __forceinline__ int seen(const AttnArgs& a, const Job& j, int q) {
+    return a.causal ? min(j.k_len, q + 1 + j.k_len - j.q_len) : j.k_len;
+}
+
+// This piece's share [first, last) of n tiles.
+struct Share {
+    int first, last;
+    __device__ __forceinline__ Share(int n, int piece, int pieces)
+        : first((int)((int64_t)n * piece / pieces)), last((int)((int64_t)n * (piece + 1) / pieces)) {}
+};
+
+// A row of a piece's float32 results.
+__device__ __forceinline__ float* part_row(float* parts, int piece, int heads, int head, int64_t rows, int64_t row,
+                                           int dim) {
+    return parts + (((int64_t)piece * heads + head) * rows + row) * dim;
+}
+
+// Workgroups of 4 waves on a CU (which bounds the registers: 256 or 512 a lane).
+template <typename T, int DP>
+constexpr int kPer = DP * (int)sizeof(T) <= 256 ? 2 : 1;
+
+// Whether the operands of a wave's own rows stay in registers: else they are read
+// again from the caches for every tile (in float32 and 256 features they would not fit beside
+// the sums).
+template <typename T, int DP>
+constexpr bool kHold = DP * (int)sizeof(T) <= 512;
+
+// The straight operand of one step of a row, held or read again.
+template <typename T, int DP, bool AL, bool HOLD = kHold<T, DP>>
+struct Own {
+    Rows<T> x;
+    int row;
+    Frag<T> f[HOLD ? DP / 16 : 1];
+    __device__ __forceinline__ Own(const Rows<T>& r, int at) : x(r), row(at) {
+        if constexpr (HOLD) load_row<T, DP, AL>(x, row, f);
+    }
+    __device__ __forceinline__ Frag<T> operator()(int s) const {
+        if constexpr (HOLD) return f[s];
+        else return load_step<T, AL>(x, row, s);
+    }
+};
+
+// Whole 16-byte chunks: what copies into LDS and wide stores need.
+inline bool al_heads(const AttnArray& x, int32_t dim, int32_t dtype) {
+    const int64_t per = dtype == MA_PARAM_BF16 ? 8 : 4;
+    // (a copy's offsets within a tile of at most 128 rows stay below 2^31 bytes, and its rows past
+    // the last lie past its extent)
+    return (reinterpret_cast<uintptr_t>(x.p) & 15) == 0 && x.token % per == 0 && x.head % per == 0 && dim % 8 == 0 &&
+           x.token >= dim && x.token <= (int64_t(1) << 22);
+}
+
+template <int V>
+using Int = std::integral_constant<int, V>;
+
+// Calls f(T{}, padded dim, aligned, waves).
+template <typename F>
+int by_kind(const AttnArgs& a, bool al, int waves, F f) {
+    auto each = [&](auto t, auto dp) {
+        if (!al) f(t, dp, std::false_type{}, Int<4>{});
+        else if (waves == 4) f(t, dp, std::true_type{}, Int<4>{});
+        else f(t, dp, std::true_type{}, Int<2>{});
+    };
+    auto dims = [&](auto t) {
+        if (a.dim <= 64) each(t, Int<64>{});
+        else if (a.dim <= 128) each(t, Int<128>{});
+        else each(t, Int<256>{});
+    };
+    if (a.dtype == MA_PARAM_BF16) dims(__bf16{});
+    else dims(float{});
+    return (int)hipGetLastError();
+}
+
+// A launch's slots for row blocks of `waves` waves, and how they are taken: in falling order of
+// work where more workgroups are queued than run at once, so that the last to begin are
+// short (7 causal sequences of 20011 tokens: forward 392 -> 332 us, dq 555 -> 458).
+inline AttnGrid grid_of(int64_t total, int64_t n_seqs, int64_t heads, int waves, int pieces) {
+    AttnGrid g;
+    g.slots = (int32_t)(total / (32 * waves) + n_seqs);
+    g.pieces = pieces;
+    g.ordered = n_seqs <= kOrderedSeqs && (int64_t)g.slots * heads * pieces > 2 * kCus;
+    return g;
 }
 
 }  // namespace

@@ -120,8 +120,8 @@ int check_attention(const char* fn, const ma_attention* a, bool back) {
     }
     // (a launch has fewer than 2^32 threads)
     TRY(check_size(fn, "n_seqs", a->n_seqs, 0, (int64_t(1) << 22) / a->heads));
-    TRY(check_size(fn, "n_queries", a->n_queries, 0, kMaxCount / a->heads));
-    TRY(check_size(fn, "n_keys", a->n_keys, 0, kMaxCount / a->heads));
+    TRY(check_size(fn, "n_queries", a->n_queries, 0, kMaxCount / 4 / a->heads));
+    TRY(check_size(fn, "n_keys", a->n_keys, 0, kMaxCount / 4 / a->heads));
     if (!(a->scale >= 0x1p-100) || !std::isfinite((float)a->scale)) {
         set_error("%s: scale must be a positive float32, at least 2^-100", fn);
         return MA_ERR_INVALID_ARG;
@@ -154,8 +154,6 @@ Span attention_span(const ma_attention* a, const char* name, const ma_heads& x, 
                     x.token_stride, x.head_stride, written);
 }
 
-int64_t attention_ws(const ma_attention* a) { return round_up(a->heads * a->n_queries * 4, 256); }
-
 AttnArgs attention_args(const ma_attention* a) {
     const auto arr = [](const ma_heads& x) { return AttnArray{x.p, x.token_stride, x.head_stride}; };
     AttnArgs g{};
@@ -176,6 +174,32 @@ AttnArgs attention_args(const ma_attention* a) {
     g.causal = a->causal;
     g.dtype = a->dtype;
     return g;
+}
+
+// Workspace: the rows' numbers, then the pieces' results.
+struct AttnSpace {
+    int64_t parts = 0, total = 0;
+};
+AttnSpace attention_space(const AttnArgs& g, bool back) {
+    AttnSpace s;
+    const int64_t rows = g.heads * g.n_queries, keys = (int64_t)g.kv_heads * g.n_keys;
+    const int64_t pq = attention_query_split(g).pieces, pk = attention_key_split(g).pieces;
+    int64_t floats = pq > 1 ? pq * rows * g.dim : 0;
+    if (back && pk > 1 && 2 * pk * keys * g.dim > floats) floats = 2 * pk * keys * g.dim;
+    s.parts = round_up(back ? rows * 8 : pq > 1 ? pq * rows * 8 : 0, 256);
+    s.total = s.parts + round_up(floats * 4, 256);
+    return s;
+}
+
+int attention_size(const char* fn, const ma_attention* a, bool back, size_t* bytes) {
+    if (!bytes) {
+        set_error("%s: NULL argument", fn);
+        return MA_ERR_INVALID_ARG;
+    }
+    TRY(check_attention(fn, a, back));
+    *bytes = (size_t)attention_space(attention_args(a), back).total;
+    clear_error();
+    return MA_OK;
 }
 
 int check_top(const char* fn, int32_t top, int64_t vocab) {
@@ -508,48 +532,51 @@ int ma_token_logprob_backward(const void* logits, int32_t dtype, int64_t n_token
     return done(fn, launch_logprob_backward(a, stream));
 }
 
-int ma_attention_forward(const ma_attention* a, void* stream) {
+int ma_attention_forward_workspace_size(const ma_attention* a, size_t* bytes) {
+    return attention_size("ma_attention_forward_workspace_size", a, false, bytes);
+}
+
+int ma_attention_forward(const ma_attention* a, void* workspace, size_t ws_bytes, void* stream) {
     const char* fn = "ma_attention_forward";
     TRY(check_attention(fn, a, false));
-    const int64_t cu = a->cu_q ? (a->n_seqs + 1) * 4 : 0;
+    AttnArgs g = attention_args(a);
+    const AttnSpace sp = attention_space(g, false);
+    TRY(check_workspace(fn, workspace, ws_bytes, (size_t)sp.total));
+    const int64_t cu = a->cu_q ? ((int64_t)a->n_seqs + 1) * 4 : 0;
     TRY(check_spans(fn, {attention_span(a, "q", a->q, false, false), attention_span(a, "k", a->k, true, false),
                          attention_span(a, "v", a->v, true, false), flat("cu_q", a->cu_q, cu, 4, false),
                          flat("cu_k", a->cu_k, cu, 4, false), attention_span(a, "o", a->o, false, true),
-                         flat("lse", a->lse, a->heads * a->n_queries * 4, 4, true)}));
-    return done(fn, launch_attention_forward(attention_args(a), stream));
+                         flat("lse", a->lse, a->heads * a->n_queries * 4, 4, true),
+                         flat("workspace", workspace, sp.total, 1, true)}));
+    g.stats = static_cast<float*>(workspace);
+    g.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + sp.parts);
+    return done(fn, launch_attention_forward(g, stream));
 }
 
 int ma_attention_backward_workspace_size(const ma_attention* a, size_t* bytes) {
-    const char* fn = "ma_attention_backward_workspace_size";
-    if (!bytes) {
-        set_error("%s: NULL argument", fn);
-        return MA_ERR_INVALID_ARG;
-    }
-    TRY(check_attention(fn, a, true));
-    *bytes = (size_t)attention_ws(a);
-    clear_error();
-    return MA_OK;
+    return attention_size("ma_attention_backward_workspace_size", a, true, bytes);
 }
 
 int ma_attention_backward(const ma_attention* a, void* workspace, size_t ws_bytes, void* stream) {
     const char* fn = "ma_attention_backward";
     TRY(check_attention(fn, a, true));
-    const int64_t need = attention_ws(a);
-    TRY(check_workspace(fn, workspace, ws_bytes, (size_t)need));
-    const int64_t cu = a->cu_q ? (a->n_seqs + 1) * 4 : 0;
+    AttnArgs g = attention_args(a);
+    const AttnSpace sp = attention_space(g, true);
+    TRY(check_workspace(fn, workspace, ws_bytes, (size_t)sp.total));
+    const int64_t cu = a->cu_q ? ((int64_t)a->n_seqs + 1) * 4 : 0;
     TRY(check_spans(fn, {attention_span(a, "q", a->q, false, false), attention_span(a, "k", a->k, true, false),
                          attention_span(a, "v", a->v, true, false), attention_span(a, "o", a->o, false, false),
                          attention_span(a, "dout", a->dout, false, false), flat("cu_q", a->cu_q, cu, 4, false),
                          flat("cu_k", a->cu_k, cu, 4, false),
                          flat("lse", a->lse, a->heads * a->n_queries * 4, 4, false),
                          attention_span(a, "dq", a->dq, false, true), attention_span(a, "dk", a->dk, true, true),
-                         attention_span(a, "dv", a->dv, true, true), flat("workspace", workspace, need, 1, true)}));
-    AttnArgs g = attention_args(a);
+                         attention_span(a, "dv", a->dv, true, true), flat("workspace", workspace, sp.total, 1, true)}));
     g.dout = {a->dout.p, a->dout.token_stride, a->dout.head_stride};
     g.dq = {a->dq.p, a->dq.token_stride, a->dq.head_stride};
     g.dk = {a->dk.p, a->dk.token_stride, a->dk.head_stride};
     g.dv = {a->dv.p, a->dv.token_stride, a->dv.head_stride};
-    g.delta = static_cast<float*>(workspace);
+    g.stats = static_cast<float*>(workspace);
+    g.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + sp.parts);
     return done(fn, launch_attention_backward(g, stream));
 }
 

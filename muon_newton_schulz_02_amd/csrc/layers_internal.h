@@ -70,13 +70,25 @@ struct AttnArray {
 };
 struct AttnArgs {
     AttnArray q, k, v, o, dout, dq, dk, dv;
-    float *lse, *delta;
+    float *lse;
+    float *stats;          // forward: m and l of every row of a piece; backward: lse in base 2 and delta of every row
+    float *parts;          // float32 results of pieces
     const int32_t *cu_q, *cu_k;
     int64_t n_queries, n_keys;
     float scale;
     int32_t heads, kv_heads, dim, n_seqs, causal, dtype;
 };
+// How many waves a workgroup has, and how many pieces its walk over the other side is
+// cut into.
+struct AttnSplit {
+    int32_t waves = 4, pieces = 1;
+};
+AttnSplit attention_query_split(const AttnArgs& a);
+AttnSplit attention_key_split(const AttnArgs& a);
 int launch_attention_forward(const AttnArgs& a, void* stream);
 int launch_attention_backward(const AttnArgs& a, void* stream);
+// Its two walks (al: every array has rows of whole 16-byte chunks).
+int launch_attention_dq(const AttnArgs& a, const AttnSplit& sp, bool al, void* stream);
+int launch_attention_dkv(const AttnArgs& a, const AttnSplit& sp, bool al, void* stream);
 
 }  // namespace ma

@@ -25,7 +25,7 @@ import torch
 
 from . import _abi
 from ._abi import MA_ROTARY_BLOCKS, MA_ROTARY_CYCLED, MA_ROTARY_HALF, MA_ROTARY_PAIRS
-from .grads import (ActCheckpoint, _At, _check_cuda, _check_workspace, _dtype, _elsewhere, _fail, _held, _out_as,
+from .grads import (_DTYPES, ActCheckpoint, _At, _check_cuda, _check_workspace, _dtype, _elsewhere, _fail, _held, _out_as,
                     _out_like, _raw_stream, _rows, _same_device, _token_bytes, _workspace)
 
 _LAYOUTS = {"half": MA_ROTARY_HALF, "pairs": MA_ROTARY_PAIRS}
@@ -399,7 +399,7 @@ def _set_heads(field, x, what: str):
 
 
 def ma_attention_forward(q, k, v, cu_q=None, cu_k=None, causal: bool = True, scale: Optional[float] = None, out=None,
-                         stream=None):
+                         workspace=None, stream=None):
     """(o, lse) of softmax(scale q k^T) v: q (queries, heads, features), k and v (keys, key heads, features), where
     query head h reads key head h // (heads // key heads).  cu_q and cu_k (int32, one more than there are
     sequences) hold where packed sequences begin; without them everything is one sequence.  With `causal` the last
@@ -408,31 +408,52 @@ def ma_attention_forward(q, k, v, cu_q=None, cu_k=None, causal: bool = True, sca
     none is passed).  o and lse (heads x queries, float32) are what ma_attention_backward takes."""
     a, dev = _attention_args(q, k, v, cu_q, cu_k, causal, scale)
     _same_device(dev, ("out", out))
+    _check_workspace(workspace, dev)
     if _elsewhere(dev, stream):
-        with _At(dev, stream, (q, k, v, cu_q, cu_k, out)):
-            return ma_attention_forward(q, k, v, cu_q, cu_k, causal, scale, out)
+        with _At(dev, stream, (q, k, v, cu_q, cu_k, out, workspace)):
+            return ma_attention_forward(q, k, v, cu_q, cu_k, causal, scale, out, workspace)
     out = _out_as(out, "out", q)
     lse = torch.empty((a.heads, a.n_queries), dtype=torch.float32, device=dev)
     _set_heads(a.o, out, "out")
     a.lse = lse.data_ptr()
-    rc = _abi.load().ma_attention_forward(C.byref(a), _raw_stream(dev.index))
+    lib = _abi.load()
+    ws, ws_ptr, ws_bytes = _workspace(workspace, _space(lib.ma_attention_forward_workspace_size, a), dev)
+    rc = lib.ma_attention_forward(C.byref(a), ws_ptr, ws_bytes, _raw_stream(dev.index))
     if rc:
         _fail(rc, "ma_attention_forward")
     return out, lse
 
 
-def ma_attention_backward_workspace_size(q, k, v) -> int:
-    """Bytes a backward call of these inputs needs."""
-    a, _ = _attention_args(q, k, v, None, None, False, None)
-    a.o.token_stride = a.dout.token_stride = a.dq.token_stride = a.heads * a.head_dim
-    a.o.head_stride = a.dout.head_stride = a.dq.head_stride = a.head_dim
-    a.dk.token_stride = a.dv.token_stride = a.kv_heads * a.head_dim
-    a.dk.head_stride = a.dv.head_stride = a.head_dim
+def _space(size_of, a) -> int:
     n = C.c_size_t()
-    rc = _abi.load().ma_attention_backward_workspace_size(C.byref(a), C.byref(n))
+    rc = size_of(C.byref(a), C.byref(n))
     if rc:
-        _fail(rc, "ma_attention_backward_workspace_size")
+        _fail(rc, size_of.__name__)
     return n.value
+
+
+def _sizes_args(n_queries, n_keys, heads, kv_heads, head_dim, n_seqs, dtype):
+    """Arguments of contiguous arrays of these sizes."""
+    a = _abi.ma_attention()
+    a.dtype, a.heads, a.kv_heads, a.head_dim = _DTYPES[dtype], heads, kv_heads, head_dim
+    a.n_queries, a.n_keys, a.n_seqs, a.scale = n_queries, n_keys, n_seqs, 1.0
+    a.cu_q = a.cu_k = 256          # (only looked at for being there)
+    for field, n in ((a.q, heads), (a.k, kv_heads), (a.v, kv_heads), (a.o, heads), (a.dout, heads), (a.dq, heads),
+                     (a.dk, kv_heads), (a.dv, kv_heads)):
+        field.token_stride, field.head_stride = n * head_dim, head_dim
+    return a
+
+
+def ma_attention_forward_workspace_size(n_queries: int, n_keys: int, heads: int, kv_heads: int, head_dim: int,
+                                        n_seqs: int = 1, dtype=torch.bfloat16) -> int:
+    a = _sizes_args(n_queries, n_keys, heads, kv_heads, head_dim, n_seqs, dtype)
+    return _space(_abi.load().ma_attention_forward_workspace_size, a)
+
+
+def ma_attention_backward_workspace_size(n_queries: int, n_keys: int, heads: int, kv_heads: int, head_dim: int,
+                                         n_seqs: int = 1, dtype=torch.bfloat16) -> int:
+    a = _sizes_args(n_queries, n_keys, heads, kv_heads, head_dim, n_seqs, dtype)
+    return _space(_abi.load().ma_attention_backward_workspace_size, a)
 
 
 def ma_attention_backward(dout, q, k, v, out, lse, cu_q=None, cu_k=None, causal: bool = True,
@@ -456,11 +477,7 @@ def ma_attention_backward(dout, q, k, v, out, lse, cu_q=None, cu_k=None, causal:
         _set_heads(getattr(a, name), x, name)
     a.lse = lse.data_ptr()
     lib = _abi.load()
-    n = C.c_size_t()
-    rc = lib.ma_attention_backward_workspace_size(C.byref(a), C.byref(n))
-    if rc:
-        _fail(rc, "ma_attention_backward")
-    ws, ws_ptr, ws_bytes = _workspace(workspace, n.value, dev)
+    ws, ws_ptr, ws_bytes = _workspace(workspace, _space(lib.ma_attention_backward_workspace_size, a), dev)
     rc = lib.ma_attention_backward(C.byref(a), ws_ptr, ws_bytes, _raw_stream(dev.index))
     if rc:
         _fail(rc, "ma_attention_backward")
