@@ -151,35 +151,61 @@ __device__ __forceinline__ JoinRow join_row(const int32_t* cu, int n_seqs, int64
     return j;
 }
 
+// put(c, v) for every column c of a row, v = add(p, x, v) over its pieces' x in order: four
+// columns a lane where they are whole 16-byte chunks.
+template <typename A, typename P>
+__device__ __forceinline__ void each_column(int dim, const float* x, int pieces, int64_t step, A add, P put) {
+    const int lane = threadIdx.x & 63;
+    if (dim % 4 == 0) {
+        const int c = 4 * lane;          // (a head has at most 256)
+        const float* y = x + min(c, dim - 4);
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+        for (int p = 0; p < pieces; ++p) {
+            const f32x4 w = *reinterpret_cast<const f32x4*>(y + p * step);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = add(p, w[e], v[e]);
+        }
+        if (c < dim)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) put(c + e, v[e]);
+    } else {
+        for (int c0 = 0; c0 < dim; c0 += 64) {
+            const float* y = x + min(c0 + lane, dim - 1);
+            float v = 0.f;
+#pragma unroll 8
+            for (int p = 0; p < pieces; ++p) v = add(p, y[p * step], v);
+            if (c0 + lane < dim) put(c0 + lane, v);
+        }
+    }
+}
+
 // o and lse of a row from its pieces' sums: as one running softmax would have joined them.
+// Lane p holds what piece p (of at most 64) brings; every piece is added in its order.
 template <typename T>
 __global__ __launch_bounds__(256) void k_attention_join(AttnArgs a, int pieces) {
     const JoinRow j = join_row(a.cu_q, a.n_seqs, a.n_queries, a.heads);
     if (!j.in) return;
+    const int lane = threadIdx.x & 63;
     const float k = a.scale * kLog2e;
     const int64_t step = (int64_t)a.heads * a.n_queries, at = (int64_t)j.head * a.n_queries + j.row;
-    float m = -kInf, l = 0.f;
-    for (int p = 0; p < pieces; ++p) m = fmaxf(m, a.stats[(p * step + at) * 2]);
+    const float* s = a.stats + (lane * step + at) * 2;
+    const float mp = lane < pieces ? s[0] : -kInf, lp = lane < pieces ? s[1] : 0.f;
+    float m = mp;
+#pragma unroll
+    for (int x = 1; x < 64; x <<= 1) m = fmaxf(m, __shfl_xor(m, x, 64));
     // (a piece whose keys are all hidden has m = -infinity and sums of 0)
-    auto weight = [&](int p) {
-        const float mp = a.stats[(p * step + at) * 2];
-        return mp == -kInf ? 0.f : __builtin_amdgcn_exp2f((mp - m) * k);
-    };
-    for (int p = 0; p < pieces; ++p) {
-        const float mp = a.stats[(p * step + at) * 2], lp = a.stats[(p * step + at) * 2 + 1];
-        l += mp == -kInf ? lp : weight(p) * lp;
-    }
+    const float w = mp == -kInf ? 0.f : __builtin_amdgcn_exp2f((mp - m) * k);
+    float l = mp == -kInf ? lp : w * lp;
+#pragma unroll
+    for (int x = 1; x < 64; x <<= 1) l += __shfl_xor(l, x, 64);
     const float r = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
     T* o = row_of<T>(a.o, j.head, j.row);
-    for (int c = threadIdx.x & 63; c < a.dim; c += 64) {
-        float v = 0.f;
-        for (int p = 0; p < pieces; ++p) {
-            const float w = weight(p), x = a.parts[(p * step + at) * a.dim + c];
-            v = w == 0.f ? v : fmaf(w, x, v);
-        }
-        o[c] = (T)(v * r);
-    }
-    if ((threadIdx.x & 63) == 0) a.lse[at] = l == 0.f ? -kInf : fmaf(m, a.scale, logf(l));
+    each_column(a.dim, a.parts + at * a.dim, pieces, step * a.dim, [&](int p, float x, float v) {
+        const float u = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), p));
+        return u == 0.f ? v : fmaf(u, x, v);
+    }, [&](int c, float v) { o[c] = (T)(v * r); });
+    if (lane == 0) a.lse[at] = l == 0.f ? -kInf : fmaf(m, a.scale, logf(l));
 }
 
 // The sum of a row's pieces: dq, or dk and dv.
@@ -190,18 +216,15 @@ __global__ __launch_bounds__(256) void k_attention_sum(AttnArgs a, int pieces) {
     const JoinRow j = join_row(KEYS ? a.cu_k : a.cu_q, a.n_seqs, rows, heads);
     if (!j.in) return;
     const int64_t step = (int64_t)heads * rows * a.dim, at = ((int64_t)j.head * rows + j.row) * a.dim;
-    for (int c = threadIdx.x & 63; c < a.dim; c += 64) {
-        float u = 0.f, v = 0.f;
-        for (int p = 0; p < pieces; ++p) {
-            u += a.parts[p * step + at + c];
-            if (KEYS) v += a.parts[(pieces + p) * step + at + c];
-        }
-        if (KEYS) {
-            row_of<T>(a.dk, j.head, j.row)[c] = (T)u;
-            row_of<T>(a.dv, j.head, j.row)[c] = (T)v;
-        } else {
-            row_of<T>(a.dq, j.head, j.row)[c] = (T)u;
-        }
+    auto add = [](int, float x, float v) { return v + x; };
+    if (KEYS) {
+        T* dk = row_of<T>(a.dk, j.head, j.row);
+        T* dv = row_of<T>(a.dv, j.head, j.row);
+        each_column(a.dim, a.parts + at, pieces, step, add, [&](int c, float v) { dk[c] = (T)v; });
+        each_column(a.dim, a.parts + pieces * step + at, pieces, step, add, [&](int c, float v) { dv[c] = (T)v; });
+    } else {
+        T* dq = row_of<T>(a.dq, j.head, j.row);
+        each_column(a.dim, a.parts + at, pieces, step, add, [&](int c, float v) { dq[c] = (T)v; });
     }
 }
 
@@ -250,7 +273,7 @@ static AttnSplit split_of(const AttnArgs& a, int64_t rows, int64_t walk, int64_t
     const int64_t blocks = ceil_div(each, 32 * s.waves) * a.n_seqs * heads;
     const int64_t at_once = (int64_t)kCus * (a.dim * (wide ? 4 : 2) <= 256 ? 2 : 1);
     const int64_t want = a.causal ? ceil_div(2 * at_once, blocks) : at_once / blocks;
-    s.pieces = (int32_t)std::max<int64_t>(1, std::min<int64_t>({want, walk / a.n_seqs / (wide ? 32 : 128), 32}));
+    s.pieces = (int32_t)std::max<int64_t>(1, std::min<int64_t>({want, ceil_div(walk, a.n_seqs * (wide ? 32 : 128)), 32}));
     return s;
 }
 AttnSplit attention_query_split(const AttnArgs& a) { return split_of(a, a.n_queries, a.n_keys, a.heads); }

@@ -84,7 +84,7 @@ __device__ __forceinline__ void dma16(u32x4 rsrc, uint32_t lds, uint32_t voff) {
     asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                  :
                  : "s"(lds), "v"(voff), "s"(rsrc)
-                 : "memory");
+                 : "memory", "m0");
 }
 
 // 4 bytes per lane, the same way.
@@ -92,13 +92,15 @@ __device__ __forceinline__ void dma4(u32x4 rsrc, uint32_t lds, uint32_t voff) {
     asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, 0 offen lds"
                  :
                  : "s"(lds), "v"(voff), "s"(rsrc)
-                 : "memory");
+                 : "memory", "m0");
 }
 
 // All but the last N of this wave's copies have landed, its LDS accesses are done, and so
-// is every wave's.  (A release fence would wait for all copies.)
+// is every wave's.  (A release fence would wait for all copies; the empty statement keeps the
+// compiler from moving LDS accesses over the wait, which it takes for no access to memory.)
 template <int N>
 __device__ __forceinline__ void copies_barrier() {
+    asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_waitcnt((N & 15) | 0x70 | (N >> 4 << 14));      // vmcnt(N) lgkmcnt(0)
     __builtin_amdgcn_s_barrier();
@@ -159,15 +161,23 @@ struct Tile {
 #pragma unroll
                 for (int i = 0; i < kCopies; ++i) dma16(rsrc, at + (uint32_t)(i * NT * 16), from[i]);
             } else {
+                // (elements that are not there read others and are dropped: no branch by lane)
 #pragma unroll
                 for (int i = 0; i < kCopies; ++i) {
                     const int s = i * NT + (int)threadIdx.x, row = s / kChunks;
                     const int col = ((s % kChunks) ^ turn(row)) * (16 / (int)sizeof(T));
-                    const T* p = base + (int64_t)row * x.stride + col;
                     T v[16 / sizeof(T)];
+                    if (left > 0) {
+                        const T* p = base + (int64_t)min(row, left - 1) * x.stride;
 #pragma unroll
-                    for (int e = 0; e < 16 / (int)sizeof(T); ++e)
-                        v[e] = row < left && col + e < x.dim ? p[e] : (T)0.f;
+                        for (int e = 0; e < 16 / (int)sizeof(T); ++e) {
+                            const T w = p[min(col + e, x.dim - 1)];
+                            v[e] = row < left && col + e < x.dim ? w : (T)0.f;
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 16 / (int)sizeof(T); ++e) v[e] = (T)0.f;
+                    }
                     *reinterpret_cast<u32x4*>(lds + s * 16) = __builtin_bit_cast(u32x4, v);
                 }
             }
@@ -219,18 +229,27 @@ struct Tile {
     }
 };
 
-// The straight operand of step s of row `row` of x (zeros past its length and dim), from
-// global memory; all of them.
+// The straight operand of step s of row `row` of x (zeros past its length, at least 1, and dim), from
+// global memory; all of them.  Without a branch around them (they would be waited for one by one) all
+// loads are under way together: a row or column that is not there reads another's and drops it.
 template <typename T, bool AL>
 __device__ __forceinline__ Frag<T> load_step(const Rows<T>& x, int row, int s) {
-    const int col = 16 * s + 8 * ((threadIdx.x & 63) >> 5);
-    float v[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = 0.f;
-    if (row < x.len && col < x.dim) load_unit<T, AL>(x.p + (int64_t)row * x.stride + col, x.dim - col, v);
+    const int col = 16 * s + 8 * ((threadIdx.x & 63) >> 5), cnt = x.dim - col;
+    const T* p = x.p + (int64_t)min(row, x.len - 1) * x.stride;
+    const bool in = row < x.len;
     Frag<T> f;
+    if constexpr (AL) {
+        float v[8];
+        load_unit<T, true>(p + min(col, x.dim - 8), 8, v);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = (T)v[e];
+        for (int e = 0; e < 8; ++e) f[e] = (T)(in && cnt > 0 ? v[e] : 0.f);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const T v = p[min(col + e, x.dim - 1)];
+            f[e] = in && e < cnt ? v : (T)0.f;
+        }
+    }
     return f;
 }
 template <typename T, int DP, bool AL>
