@@ -163,7 +163,7 @@ typedef struct ma_heads {
 /* Packed sequences: queries [cu_q[s], cu_q[s + 1]) attend to keys [cu_k[s], cu_k[s + 1]),
  * s < n_seqs.  cu_q and cu_k are device arrays of n_seqs + 1 rising int32 values; both NULL for
  * one sequence of everything (n_seqs = 1).  Queries and keys outside every sequence (behind the
- * last one) are neither read nor written.  Offsets that fall or leave [0, n] are cut to the
+ * last one) have no effect, and their results are not written.  Offsets that fall or leave [0, n] are cut to the
  * arrays: no access leaves them, but what is then computed is not defined.
  * Query head h reads key head h / (heads / kv_heads).  With causal = 1 the last query of a
  * sequence sees its last key: query i of nq sees keys 0 .. i + nk - nq. */
@@ -183,8 +183,10 @@ typedef struct ma_attention {
     ma_heads dout, dq, dk, dv; /* backward only */
 } ma_attention;
 
-/* Bytes of workspace (256-byte aligned; 0: none, NULL may be passed) a forward call needs: calls
- * of few rows cut their walk over the keys into pieces and join them.  Errors: INVALID_ARG, SHAPE. */
+/* Bytes of workspace (256-byte aligned; 0: none, NULL may be passed) a forward call of these
+ * arrays needs (nothing is read): calls of few rows cut their walk over the keys into pieces and
+ * join them, and inputs whose heads are not whole 16-byte chunks at 16-byte addresses with
+ * token strides from head_dim to 2^22 are copied.  Errors: INVALID_ARG, SHAPE. */
 int ma_attention_forward_workspace_size(const ma_attention* a, size_t* bytes);
 
 /* o = softmax(scale q k^T) v and lse.  A query that sees no key has o = 0 and lse =
@@ -195,7 +197,8 @@ int ma_attention_forward_workspace_size(const ma_attention* a, size_t* bytes);
  * n_keys * heads above 2^28, n_seqs * heads above 2^22), WORKSPACE, HIP. */
 int ma_attention_forward(const ma_attention* a, void* workspace, size_t ws_bytes, void* stream);
 
-/* Bytes of workspace (256-byte aligned) a backward call needs.  Errors: INVALID_ARG, SHAPE. */
+/* Bytes of workspace (256-byte aligned) a backward call of these arrays needs.  Errors:
+ * INVALID_ARG, SHAPE. */
 int ma_attention_backward_workspace_size(const ma_attention* a, size_t* bytes);
 
 /* dq, dk and dv from dout and the forward pass' o and lse.  dk and dv sum over the query heads

@@ -25,7 +25,7 @@
 namespace ma {
 namespace {
 
-template <typename T, int DP, int KV, bool AL, int WAVES>
+template <typename T, int DP, int KV, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, (kPer<T, DP>)) void k_attention_forward(AttnArgs a, AttnGrid grid) {
     constexpr int BLOCK = 32 * WAVES;
     using KT = Tile<T, DP, KV, 64 * WAVES>;
@@ -34,12 +34,12 @@ __global__ __launch_bounds__(64 * WAVES, (kPer<T, DP>)) void k_attention_forward
     if (!j.any) return;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, h = lane >> 5;
     const int kvh = j.head / (a.heads / a.kv_heads);
-    const Rows<T> qx = rows_of<T>(a.q, j.head, j.q_at, j.q_len, a.dim);
-    const Rows<T> kx = rows_of<T>(a.k, kvh, j.k_at, j.k_len, a.dim);
-    const Rows<T> vx = rows_of<T>(a.v, kvh, j.k_at, j.k_len, a.dim);
+    const Rows<T> qx = rows_of<T>(a.q, j.head, j.q_at, j.q_len, a.cols);
+    const Rows<T> kx = rows_of<T>(a.k, kvh, j.k_at, j.k_len, a.cols);
+    const Rows<T> vx = rows_of<T>(a.v, kvh, j.k_at, j.k_len, a.cols);
     const int q = j.row0 + 32 * wave + (lane & 31);
     Frag<T> qf[DP / 16];
-    load_row<T, DP, AL>(qx, q, qf);
+    load_row<T, DP>(qx, q, qf);
 
     f32x16 o[DP / 32];
 #pragma unroll
@@ -49,7 +49,7 @@ __global__ __launch_bounds__(64 * WAVES, (kPer<T, DP>)) void k_attention_forward
     // key tiles that some row of the workgroup sees
     const int end = min(j.row0 + BLOCK, j.q_len) - 1;
     const Share sh(max(0, seen(a, j, end) + KV - 1) / KV, j.piece, grid.pieces);
-    const typename KT::template Copy<AL> copy_k(kx), copy_v(vx);
+    const typename KT::Copy copy_k(kx), copy_v(vx);
     if (sh.first < sh.last) {
         copy_k(lds[0][0], kx, sh.first * KV);
         copy_v(lds[0][1], vx, sh.first * KV);
@@ -132,7 +132,8 @@ __global__ __launch_bounds__(64 * WAVES, (kPer<T, DP>)) void k_attention_forward
         }
         return;
     }
-    store_row<T, DP / 32>(row_of<T>(a.o, j.head, row), a.dim, o, l > 0.f ? 1.f / l : l == 0.f ? 0.f : l, AL);
+    store_row<T, DP / 32>(row_of<T>(a.o, j.head, row), a.dim, o, l > 0.f ? 1.f / l : l == 0.f ? 0.f : l,
+                         a.wide);
     if (h == 0) a.lse[(int64_t)j.head * a.n_queries + row] = l == 0.f ? -kInf : fmaf(m, a.scale, logf(l));
 }
 
@@ -283,18 +284,83 @@ AttnSplit attention_key_split(const AttnArgs& a) {
 
 static unsigned join_grid(int64_t rows, int64_t heads) { return (unsigned)ceil_div(rows * heads, 4); }
 
+// The inputs that have no aligned rows of whole chunks (every one where dim is not a multiple of
+// 8), and where their copies lie in the workspace.
+AttnPack attention_pack(const AttnArgs& a, bool back) {
+    AttnPack p;
+    const int64_t cols = round_up(a.dim, 8), size = a.dtype == MA_PARAM_BF16 ? 2 : 4;
+    const AttnArray* in[] = {&a.q, &a.k, &a.v, &a.dout};
+    for (int i = 0; i < (back ? 4 : 3); ++i) {
+        const bool keys = i == 1 || i == 2;
+        if (al_heads(*in[i], a.dim, a.dtype)) continue;
+        p.copied[i] = true;
+        p.at[i] = p.total;
+        p.total += round_up((keys ? a.n_keys * a.kv_heads : a.n_queries * a.heads) * cols * size, 256);
+    }
+    return p;
+}
+
+// Rows (token, head) of x as rows of `cols` columns, zeros past dim: 16 bytes a thread.
+template <typename T>
+__global__ __launch_bounds__(256) void k_attention_pack(AttnArray x, T* out, int64_t rows, int heads, int dim, int cols) {
+    constexpr int kPer = 16 / (int)sizeof(T);
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int per_row = cols / kPer;
+    const int64_t r = i / per_row;
+    if (r >= rows) return;
+    const int c = (int)(i - r * per_row) * kPer;
+    const int64_t t = r / heads;
+    const T* p = row_of<T>(x, (int)(r - t * heads), t);
+    T v[kPer];
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+        const T w = p[min(c + e, dim - 1)];
+        v[e] = c + e < dim ? w : (T)0.f;
+    }
+    *reinterpret_cast<u32x4*>(out + i * kPer) = __builtin_bit_cast(u32x4, v);
+}
+
+// The call's inputs with aligned rows.
+static int pack_inputs(AttnArgs& g, bool back, void* stream) {
+    const AttnPack p = attention_pack(g, back);
+    g.cols = g.dim;
+    if (p.total == 0) return (int)hipSuccess;
+    const int cols = (int)round_up(g.dim, 8);
+    AttnArray* in[] = {&g.q, &g.k, &g.v, &g.dout};
+    for (int i = 0; i < 4; ++i) {
+        const int heads = i == 1 || i == 2 ? g.kv_heads : g.heads;
+        const int64_t rows = heads * (i == 1 || i == 2 ? g.n_keys : g.n_queries);
+        if (!p.copied[i]) continue;
+        char* out = g.packed + p.at[i];
+        auto go = [&](auto t) {
+            using T = decltype(t);
+            const int64_t n = rows * (cols * (int64_t)sizeof(T) / 16);
+            if (n > 0)
+                hipLaunchKernelGGL((k_attention_pack<T>), dim3((unsigned)ceil_div(n, 256)), dim3(256), 0,
+                                   (hipStream_t)stream, *in[i], reinterpret_cast<T*>(out), rows, heads, g.dim, cols);
+        };
+        if (g.dtype == MA_PARAM_BF16) go(__bf16{});
+        else go(float{});
+        *in[i] = {out, (int64_t)heads * cols, cols};
+    }
+    g.cols = cols;
+    return (int)hipGetLastError();
+}
+
 int launch_attention_forward(const AttnArgs& a, void* stream) {
     if (a.n_queries == 0 || a.n_seqs == 0) return (int)hipSuccess;
-    const bool al = al_heads(a.q, a.dim, a.dtype) && al_heads(a.k, a.dim, a.dtype) && al_heads(a.v, a.dim, a.dtype) &&
-                    al_heads(a.o, a.dim, a.dtype);
+    AttnArgs g = a;
+    g.wide = al_heads(a.o, a.dim, a.dtype);
+    int rc = pack_inputs(g, false, stream);
+    if (rc != (int)hipSuccess) return rc;
     const AttnSplit sp = attention_query_split(a);
-    const int rc = by_kind(a, al, sp.waves, [&](auto t, auto dp, auto w, auto wv) {
+    rc = by_kind(a, sp.waves, [&](auto t, auto dp, auto wv) {
         using T = decltype(t);
         constexpr int DP = decltype(dp)::value, WAVES = decltype(wv)::value;
-        const AttnGrid g = grid_of(a.n_queries, a.n_seqs, a.heads, WAVES, sp.pieces);
+        const AttnGrid grid = grid_of(a.n_queries, a.n_seqs, a.heads, WAVES, sp.pieces);
         constexpr int KV = sizeof(T) == 2 ? 64 : 32;
-        hipLaunchKernelGGL((k_attention_forward<T, DP, KV, decltype(w)::value, WAVES>),
-                           dim3((unsigned)g.slots * a.heads * g.pieces), dim3(64 * WAVES), 0, (hipStream_t)stream, a, g);
+        hipLaunchKernelGGL((k_attention_forward<T, DP, KV, WAVES>), dim3((unsigned)grid.slots * a.heads * grid.pieces),
+                           dim3(64 * WAVES), 0, (hipStream_t)stream, g, grid);
     });
     if (rc != (int)hipSuccess || sp.pieces == 1) return rc;
     const dim3 grid(join_grid(a.n_queries, a.heads)), block(256);
@@ -307,9 +373,11 @@ int launch_attention_forward(const AttnArgs& a, void* stream) {
 
 int launch_attention_backward(const AttnArgs& a, void* stream) {
     if (a.n_seqs == 0) return (int)hipSuccess;
-    const bool al = al_heads(a.q, a.dim, a.dtype) && al_heads(a.k, a.dim, a.dtype) && al_heads(a.v, a.dim, a.dtype) &&
-                    al_heads(a.o, a.dim, a.dtype) && al_heads(a.dout, a.dim, a.dtype) &&
-                    al_heads(a.dq, a.dim, a.dtype) && al_heads(a.dk, a.dim, a.dtype) && al_heads(a.dv, a.dim, a.dtype);
+    AttnArgs g = a;
+    g.wide = al_heads(a.dq, a.dim, a.dtype) && al_heads(a.dk, a.dim, a.dtype) && al_heads(a.dv, a.dim, a.dtype);
+    const bool al = al_heads(a.o, a.dim, a.dtype) && al_heads(a.dout, a.dim, a.dtype);
+    int rc = pack_inputs(g, true, stream);
+    if (rc != (int)hipSuccess) return rc;
     // a sum of pieces: the partial sums of dq, then those of dk and dv, take the same space
     auto join = [&](auto keys, int pieces) {
         constexpr bool KEYS = decltype(keys)::value;
@@ -329,15 +397,15 @@ int launch_attention_backward(const AttnArgs& a, void* stream) {
         };
         if (a.dtype == MA_PARAM_BF16) delta(__bf16{});
         else delta(float{});
-        int rc = (int)hipGetLastError();
+        rc = (int)hipGetLastError();
         const AttnSplit sp = attention_query_split(a);
-        if (rc == (int)hipSuccess) rc = launch_attention_dq(a, sp, al, stream);
+        if (rc == (int)hipSuccess) rc = launch_attention_dq(g, sp, stream);
         if (rc == (int)hipSuccess && sp.pieces > 1) rc = join(std::false_type{}, sp.pieces);
         if (rc != (int)hipSuccess) return rc;
     }
     if (a.n_keys == 0) return (int)hipSuccess;
     const AttnSplit sp = attention_key_split(a);
-    const int rc = launch_attention_dkv(a, sp, al, stream);
+    rc = launch_attention_dkv(g, sp, stream);
     if (rc == (int)hipSuccess && sp.pieces > 1) return join(std::true_type{}, sp.pieces);
     return rc;
 }

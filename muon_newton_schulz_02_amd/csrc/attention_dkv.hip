@@ -14,7 +14,7 @@ namespace {
 template <typename T, int DP>
 constexpr bool kStage = DP * (int)sizeof(T) == 256;
 
-template <typename T, int DP, bool AL, int WAVES>
+template <typename T, int DP, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, (kPer<T, DP>)) void k_attention_dkv(AttnArgs a, AttnGrid grid) {
     constexpr int BLOCK = 32 * WAVES, QT = 32, RING = 2;
     using QTile = Tile<T, DP, QT, 64 * WAVES>;
@@ -29,11 +29,11 @@ __global__ __launch_bounds__(64 * WAVES, (kPer<T, DP>)) void k_attention_dkv(Att
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int group = a.heads / a.kv_heads;
     const int key = j.row0 + 32 * wave + (lane & 31);
-    const Rows<T> vx = rows_of<T>(a.v, j.head, j.k_at, j.k_len, a.dim);
-    const Own<T, DP, AL> kf(rows_of<T>(a.k, j.head, j.k_at, j.k_len, a.dim), key);
-    const Own<T, DP, AL, kHold<T, DP> && !STAGE> vown(vx, key);
+    const Rows<T> vx = rows_of<T>(a.v, j.head, j.k_at, j.k_len, a.cols);
+    const Own<T, DP> kf(rows_of<T>(a.k, j.head, j.k_at, j.k_len, a.cols), key);
+    const Own<T, DP, DP * (int)sizeof(T) <= 512 && !STAGE> vown(vx, key);
     if constexpr (STAGE) {
-        const typename VTile::template Copy<AL> copy_v(vx);
+        const typename VTile::Copy copy_v(vx);
         copy_v(vlds, vx, j.row0);
     }
     auto vf = [&](int d) {
@@ -49,14 +49,14 @@ __global__ __launch_bounds__(64 * WAVES, (kPer<T, DP>)) void k_attention_dkv(Att
     const int first = a.causal ? max(0, j.row0 - off) / QT : 0;
     const int per = max(0, (j.q_len + QT - 1) / QT - first);
     const Share sh(per * group, j.piece, grid.pieces);
-    const typename QTile::template Copy<AL> copy_q(rows_of<T>(a.q, 0, 0, 0, a.dim)), copy_d(rows_of<T>(a.dout, 0, 0, 0, a.dim));
+    const typename QTile::Copy copy_q(rows_of<T>(a.q, 0, 0, 0, a.cols)), copy_d(rows_of<T>(a.dout, 0, 0, 0, a.cols));
     // the next tile to copy: its number, its head of the group, and which of the head's it is
     int next = sh.first, nhead = per ? sh.first / per : 0, ntile = sh.first - nhead * per, ahead = 0;
     auto fetch = [&]() {
         const bool in = next < sh.last;          // (past the last tile the copies are empty)
         const int head = j.head * group + (in ? nhead : 0), q0 = in ? (first + ntile) * QT : j.q_len;
-        copy_q(lds[ahead][0], rows_of<T>(a.q, head, j.q_at, j.q_len, a.dim), q0);
-        copy_d(lds[ahead][1], rows_of<T>(a.dout, head, j.q_at, j.q_len, a.dim), q0);
+        copy_q(lds[ahead][0], rows_of<T>(a.q, head, j.q_at, j.q_len, a.cols), q0);
+        copy_d(lds[ahead][1], rows_of<T>(a.dout, head, j.q_at, j.q_len, a.cols), q0);
         const float* s = a.stats + ((int64_t)head * a.n_queries + j.q_at + q0) * 2;
         dma4(make_rsrc(s, (int64_t)(j.q_len - q0) * 8), lds_addr(stat[ahead][wave]), lane * 4u);
         ahead ^= 1;
@@ -139,18 +139,18 @@ __global__ __launch_bounds__(64 * WAVES, (kPer<T, DP>)) void k_attention_dkv(Att
         store_row<float, DP / 32>(part_row(a.parts, grid.pieces + j.piece, a.kv_heads, j.head, a.n_keys, row, a.dim), a.dim,
                                   dv, 1.f, a.dim % 4 == 0);
     } else {
-        store_row<T, DP / 32>(row_of<T>(a.dk, j.head, row), a.dim, dk, a.scale, AL);
-        store_row<T, DP / 32>(row_of<T>(a.dv, j.head, row), a.dim, dv, 1.f, AL);
+        store_row<T, DP / 32>(row_of<T>(a.dk, j.head, row), a.dim, dk, a.scale, a.wide);
+        store_row<T, DP / 32>(row_of<T>(a.dv, j.head, row), a.dim, dv, 1.f, a.wide);
     }
 }
 
 }  // namespace
 
-int launch_attention_dkv(const AttnArgs& a, const AttnSplit& sp, bool al, void* stream) {
-    return by_kind(a, al, sp.waves, [&](auto t, auto dp, auto w, auto wv) {
+int launch_attention_dkv(const AttnArgs& a, const AttnSplit& sp, void* stream) {
+    return by_kind(a, sp.waves, [&](auto t, auto dp, auto wv) {
         constexpr int WAVES = decltype(wv)::value;
         const AttnGrid g = grid_of(a.n_keys, a.n_seqs, a.kv_heads, WAVES, sp.pieces);
-        hipLaunchKernelGGL((k_attention_dkv<decltype(t), decltype(dp)::value, decltype(w)::value, WAVES>),
+        hipLaunchKernelGGL((k_attention_dkv<decltype(t), decltype(dp)::value, WAVES>),
                            dim3((unsigned)g.slots * a.kv_heads * g.pieces), dim3(64 * WAVES), 0, (hipStream_t)stream, a, g);
     });
 }

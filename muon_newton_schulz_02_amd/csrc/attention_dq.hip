@@ -12,21 +12,21 @@ namespace {
 // The copies of tile t + RING - 1 are under way while tile t is worked on.
 template <typename T, int DP>
 constexpr int kRing = DP * (int)sizeof(T) <= 256 ? 3 : 2;
-template <typename T, int DP, bool AL, int WAVES>
+template <typename T, int DP, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, (kPer<T, DP>)) void k_attention_dq(AttnArgs a, AttnGrid grid) {
     constexpr int BLOCK = 32 * WAVES, KV = 32, RING = kRing<T, DP>;
     using KT = Tile<T, DP, KV, 64 * WAVES>;
-    constexpr int kTileCopies = AL ? 2 * KT::kCopies : 0;
+    constexpr int kTileCopies = 2 * KT::kCopies;
     __shared__ __attribute__((aligned(1024))) char lds[RING][2][KT::kBytes];
     const Job j = job_of<false, BLOCK>(a, grid);
     if (!j.any) return;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, h = lane >> 5;
     const int kvh = j.head / (a.heads / a.kv_heads);
-    const Rows<T> kx = rows_of<T>(a.k, kvh, j.k_at, j.k_len, a.dim);
-    const Rows<T> vx = rows_of<T>(a.v, kvh, j.k_at, j.k_len, a.dim);
+    const Rows<T> kx = rows_of<T>(a.k, kvh, j.k_at, j.k_len, a.cols);
+    const Rows<T> vx = rows_of<T>(a.v, kvh, j.k_at, j.k_len, a.cols);
     const int q = j.row0 + 32 * wave + (lane & 31);
-    const Own<T, DP, AL> qf(rows_of<T>(a.q, j.head, j.q_at, j.q_len, a.dim), q);
-    const Own<T, DP, AL> df(rows_of<T>(a.dout, j.head, j.q_at, j.q_len, a.dim), q);
+    const Own<T, DP> qf(rows_of<T>(a.q, j.head, j.q_at, j.q_len, a.cols), q);
+    const Own<T, DP> df(rows_of<T>(a.dout, j.head, j.q_at, j.q_len, a.cols), q);
     const float* st = a.stats + ((int64_t)j.head * a.n_queries + j.q_at + q) * 2;
     const float ls = q < j.q_len ? st[0] : kInf, delta = q < j.q_len ? st[1] : 0.f;
 
@@ -37,7 +37,7 @@ __global__ __launch_bounds__(64 * WAVES, (kPer<T, DP>)) void k_attention_dq(Attn
     const int end = min(j.row0 + BLOCK, j.q_len) - 1;
     const Share sh(max(0, seen(a, j, end) + KV - 1) / KV, j.piece, grid.pieces);
     const int sees = seen(a, j, q);
-    const typename KT::template Copy<AL> copy_k(kx), copy_v(vx);
+    const typename KT::Copy copy_k(kx), copy_v(vx);
     int slot = 0, ahead = 0;
     // (past the last tile the copies are empty)
     auto fetch = [&](int t) {
@@ -84,16 +84,16 @@ __global__ __launch_bounds__(64 * WAVES, (kPer<T, DP>)) void k_attention_dq(Attn
         store_row<float, DP / 32>(part_row(a.parts, j.piece, a.heads, j.head, a.n_queries, row, a.dim), a.dim, dq,
                                   a.scale, a.dim % 4 == 0);
     else
-        store_row<T, DP / 32>(row_of<T>(a.dq, j.head, row), a.dim, dq, a.scale, AL);
+        store_row<T, DP / 32>(row_of<T>(a.dq, j.head, row), a.dim, dq, a.scale, a.wide);
 }
 
 }  // namespace
 
-int launch_attention_dq(const AttnArgs& a, const AttnSplit& sp, bool al, void* stream) {
-    return by_kind(a, al, sp.waves, [&](auto t, auto dp, auto w, auto wv) {
+int launch_attention_dq(const AttnArgs& a, const AttnSplit& sp, void* stream) {
+    return by_kind(a, sp.waves, [&](auto t, auto dp, auto wv) {
         constexpr int WAVES = decltype(wv)::value;
         const AttnGrid g = grid_of(a.n_queries, a.n_seqs, a.heads, WAVES, sp.pieces);
-        hipLaunchKernelGGL((k_attention_dq<decltype(t), decltype(dp)::value, decltype(w)::value, WAVES>),
+        hipLaunchKernelGGL((k_attention_dq<decltype(t), decltype(dp)::value, WAVES>),
                            dim3((unsigned)g.slots * a.heads * g.pieces), dim3(64 * WAVES), 0, (hipStream_t)stream, a, g);
     });
 }

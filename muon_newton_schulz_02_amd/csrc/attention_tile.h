@@ -108,7 +108,8 @@ __device__ __forceinline__ void copies_barrier() {
     __builtin_amdgcn_sched_barrier(0);
 }
 
-// One head of a packed array, as the rows of one sequence.
+// One head of a packed array, as the rows of one sequence: whole 16-byte chunks at
+// 16-byte addresses (other inputs are copied into such rows first).
 template <typename T>
 struct Rows {
     const T* p;          // the sequence's first row
@@ -133,54 +134,27 @@ struct Tile {
         else return (row >> 1 & 1) << 2 | (row >> 2 & 3);
     }
 
-    // Copies of rows of one array into LDS by all threads.  AL: rows and dim are whole 16-byte
-    // chunks, rows do not overlap and extents within a tile stay below 2^31: the copies go straight
-    // into LDS (they have landed after copies_barrier).
-    template <bool AL>
+    // Copies of rows of one array into LDS by all threads, which have landed after copies_barrier.
     struct Copy {
-        uint32_t from[AL ? kCopies : 1];         // byte offset of this thread's chunk; past any extent where there is none
+        uint32_t from[kCopies];          // byte offset of this thread's chunk; past any extent where there is none
         __device__ __forceinline__ explicit Copy(const Rows<T>& x) {
-            if constexpr (AL)
 #pragma unroll
-                for (int i = 0; i < kCopies; ++i) {
-                    const int s = i * NT + (int)threadIdx.x, row = s / kChunks;
-                    const int col = ((s % kChunks) ^ turn(row)) * (16 / (int)sizeof(T));
-                    from[i] = col < x.dim ? (uint32_t)row * (uint32_t)(x.stride * sizeof(T)) + (uint32_t)(col * sizeof(T))
-                                          : 0x80000000u;
-                }
+            for (int i = 0; i < kCopies; ++i) {
+                const int s = i * NT + (int)threadIdx.x, row = s / kChunks;
+                const int col = ((s % kChunks) ^ turn(row)) * (16 / (int)sizeof(T));
+                from[i] = col < x.dim ? (uint32_t)row * (uint32_t)(x.stride * sizeof(T)) + (uint32_t)(col * sizeof(T))
+                                      : 0x80000000u;
+            }
         }
         // Rows [row0, row0 + ROWS) of x into `lds`; rows past x.len and columns past x.dim become
         // zeros.
         __device__ __forceinline__ void operator()(char* lds, const Rows<T>& x, int row0) const {
             const int left = min(x.len - row0, ROWS);
-            const T* base = x.p + (int64_t)row0 * x.stride;
-            if constexpr (AL) {
-                const u32x4 rsrc =
-                    make_rsrc(base, left > 0 ? ((int64_t)(left - 1) * x.stride + x.dim) * (int64_t)sizeof(T) : 0);
-                const uint32_t at = lds_addr(lds) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 1024u;
+            const u32x4 rsrc = make_rsrc(x.p + (int64_t)row0 * x.stride,
+                                         left > 0 ? ((int64_t)(left - 1) * x.stride + x.dim) * (int64_t)sizeof(T) : 0);
+            const uint32_t at = lds_addr(lds) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 1024u;
 #pragma unroll
-                for (int i = 0; i < kCopies; ++i) dma16(rsrc, at + (uint32_t)(i * NT * 16), from[i]);
-            } else {
-                // (elements that are not there read others and are dropped: no branch by lane)
-#pragma unroll
-                for (int i = 0; i < kCopies; ++i) {
-                    const int s = i * NT + (int)threadIdx.x, row = s / kChunks;
-                    const int col = ((s % kChunks) ^ turn(row)) * (16 / (int)sizeof(T));
-                    T v[16 / sizeof(T)];
-                    if (left > 0) {
-                        const T* p = base + (int64_t)min(row, left - 1) * x.stride;
-#pragma unroll
-                        for (int e = 0; e < 16 / (int)sizeof(T); ++e) {
-                            const T w = p[min(col + e, x.dim - 1)];
-                            v[e] = row < left && col + e < x.dim ? w : (T)0.f;
-                        }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 16 / (int)sizeof(T); ++e) v[e] = (T)0.f;
-                    }
-                    *reinterpret_cast<u32x4*>(lds + s * 16) = __builtin_bit_cast(u32x4, v);
-                }
-            }
+            for (int i = 0; i < kCopies; ++i) dma16(rsrc, at + (uint32_t)(i * NT * 16), from[i]);
         }
     };
 
@@ -232,30 +206,21 @@ struct Tile {
 // The straight operand of step s of row `row` of x (zeros past its length, at least 1, and dim), from
 // global memory; all of them.  Without a branch around them (they would be waited for one by one) all
 // loads are under way together: a row or column that is not there reads another's and drops it.
-template <typename T, bool AL>
+template <typename T>
 __device__ __forceinline__ Frag<T> load_step(const Rows<T>& x, int row, int s) {
-    const int col = 16 * s + 8 * ((threadIdx.x & 63) >> 5), cnt = x.dim - col;
-    const T* p = x.p + (int64_t)min(row, x.len - 1) * x.stride;
-    const bool in = row < x.len;
+    const int col = 16 * s + 8 * ((threadIdx.x & 63) >> 5);
+    const bool in = row < x.len && col < x.dim;
+    float v[8];
+    load_unit<T, true>(x.p + (int64_t)min(row, x.len - 1) * x.stride + min(col, x.dim - 8), 8, v);
     Frag<T> f;
-    if constexpr (AL) {
-        float v[8];
-        load_unit<T, true>(p + min(col, x.dim - 8), 8, v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = (T)(in && cnt > 0 ? v[e] : 0.f);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const T v = p[min(col + e, x.dim - 1)];
-            f[e] = in && e < cnt ? v : (T)0.f;
-        }
-    }
+    for (int e = 0; e < 8; ++e) f[e] = (T)(in ? v[e] : 0.f);
     return f;
 }
-template <typename T, int DP, bool AL>
+template <typename T, int DP>
 __device__ __forceinline__ void load_row(const Rows<T>& x, int row, Frag<T>* f) {
 #pragma unroll
-    for (int s = 0; s < DP / 16; ++s) f[s] = load_step<T, AL>(x, row, s);
+    for (int s = 0; s < DP / 16; ++s) f[s] = load_step<T>(x, row, s);
 }
 
 // Stores a wave's transposed results (columns of x by rows of 32 at a time) as row `row`:
@@ -434,28 +399,28 @@ __device__ __forceinline__ float* part_row(float* parts, int piece, int heads, i
 template <typename T, int DP>
 constexpr int kPer = DP * (int)sizeof(T) <= 256 ? 2 : 1;
 
-// Whether the operands of a wave's own rows stay in registers: else they are read
-// again from the caches for every tile (in float32 and 256 features they would not fit beside
-// the sums).
-template <typename T, int DP>
-constexpr bool kHold = DP * (int)sizeof(T) <= 512;
-
-// The straight operand of one step of a row, held or read again.
-template <typename T, int DP, bool AL, bool HOLD = kHold<T, DP>>
+// The straight operands of a wave's own rows, held in registers or, where they do not
+// fit beside the sums (float32 and 256 features), read again from the caches for every tile.
+template <typename T, int DP, bool HOLD = DP * (int)sizeof(T) <= 512>
 struct Own {
     Rows<T> x;
     int row;
     Frag<T> f[HOLD ? DP / 16 : 1];
     __device__ __forceinline__ Own(const Rows<T>& r, int at) : x(r), row(at) {
-        if constexpr (HOLD) load_row<T, DP, AL>(x, row, f);
+        if constexpr (HOLD) load_row<T, DP>(x, row, f);
     }
     __device__ __forceinline__ Frag<T> operator()(int s) const {
         if constexpr (HOLD) return f[s];
-        else return load_step<T, AL>(x, row, s);
+        // (four steps' loads at a time, and not moved out of the tiles' loop)
+        if (s % 4 == 0) __builtin_amdgcn_sched_barrier(0);
+        int r = row;
+        asm volatile("" : "+v"(r));
+        return load_step<T>(x, r, s);
     }
 };
 
-// Whole 16-byte chunks: what copies into LDS and wide stores need.
+// Whether rows are whole 16-byte chunks at 16-byte addresses, which copies into LDS and wide
+// stores need.
 inline bool al_heads(const AttnArray& x, int32_t dim, int32_t dtype) {
     const int64_t per = dtype == MA_PARAM_BF16 ? 8 : 4;
     // (a copy's offsets within a tile of at most 128 rows stay below 2^31 bytes, and its rows past
@@ -467,13 +432,12 @@ inline bool al_heads(const AttnArray& x, int32_t dim, int32_t dtype) {
 template <int V>
 using Int = std::integral_constant<int, V>;
 
-// Calls f(T{}, padded dim, aligned, waves).
+// Calls f(T{}, padded dim, waves).
 template <typename F>
-int by_kind(const AttnArgs& a, bool al, int waves, F f) {
+int by_kind(const AttnArgs& a, int waves, F f) {
     auto each = [&](auto t, auto dp) {
-        if (!al) f(t, dp, std::false_type{}, Int<4>{});
-        else if (waves == 4) f(t, dp, std::true_type{}, Int<4>{});
-        else f(t, dp, std::true_type{}, Int<2>{});
+        if (waves == 4) f(t, dp, Int<4>{});
+        else f(t, dp, Int<2>{});
     };
     auto dims = [&](auto t) {
         if (a.dim <= 64) each(t, Int<64>{});

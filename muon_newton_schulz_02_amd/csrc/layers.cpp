@@ -176,9 +176,9 @@ AttnArgs attention_args(const ma_attention* a) {
     return g;
 }
 
-// Workspace: the rows' numbers, then the pieces' results.
+// Workspace: the rows' numbers, then the pieces' results, then copies of inputs.
 struct AttnSpace {
-    int64_t parts = 0, total = 0;
+    int64_t parts = 0, packed = 0, total = 0;
 };
 AttnSpace attention_space(const AttnArgs& g, bool back) {
     AttnSpace s;
@@ -187,7 +187,8 @@ AttnSpace attention_space(const AttnArgs& g, bool back) {
     int64_t floats = pq > 1 ? pq * rows * g.dim : 0;
     if (back && pk > 1 && 2 * pk * keys * g.dim > floats) floats = 2 * pk * keys * g.dim;
     s.parts = round_up(back ? rows * 8 : pq > 1 ? pq * rows * 8 : 0, 256);
-    s.total = s.parts + round_up(floats * 4, 256);
+    s.packed = s.parts + round_up(floats * 4, 256);
+    s.total = s.packed + attention_pack(g, back).total;
     return s;
 }
 
@@ -197,7 +198,9 @@ int attention_size(const char* fn, const ma_attention* a, bool back, size_t* byt
         return MA_ERR_INVALID_ARG;
     }
     TRY(check_attention(fn, a, back));
-    *bytes = (size_t)attention_space(attention_args(a), back).total;
+    AttnArgs g = attention_args(a);
+    g.dout = {a->dout.p, a->dout.token_stride, a->dout.head_stride};
+    *bytes = (size_t)attention_space(g, back).total;
     clear_error();
     return MA_OK;
 }
@@ -550,6 +553,7 @@ int ma_attention_forward(const ma_attention* a, void* workspace, size_t ws_bytes
                          flat("workspace", workspace, sp.total, 1, true)}));
     g.stats = static_cast<float*>(workspace);
     g.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + sp.parts);
+    g.packed = static_cast<char*>(workspace) + sp.packed;
     return done(fn, launch_attention_forward(g, stream));
 }
 
@@ -561,6 +565,10 @@ int ma_attention_backward(const ma_attention* a, void* workspace, size_t ws_byte
     const char* fn = "ma_attention_backward";
     TRY(check_attention(fn, a, true));
     AttnArgs g = attention_args(a);
+    g.dout = {a->dout.p, a->dout.token_stride, a->dout.head_stride};
+    g.dq = {a->dq.p, a->dq.token_stride, a->dq.head_stride};
+    g.dk = {a->dk.p, a->dk.token_stride, a->dk.head_stride};
+    g.dv = {a->dv.p, a->dv.token_stride, a->dv.head_stride};
     const AttnSpace sp = attention_space(g, true);
     TRY(check_workspace(fn, workspace, ws_bytes, (size_t)sp.total));
     const int64_t cu = a->cu_q ? ((int64_t)a->n_seqs + 1) * 4 : 0;
@@ -571,12 +579,9 @@ int ma_attention_backward(const ma_attention* a, void* workspace, size_t ws_byte
                          flat("lse", a->lse, a->heads * a->n_queries * 4, 4, false),
                          attention_span(a, "dq", a->dq, false, true), attention_span(a, "dk", a->dk, true, true),
                          attention_span(a, "dv", a->dv, true, true), flat("workspace", workspace, sp.total, 1, true)}));
-    g.dout = {a->dout.p, a->dout.token_stride, a->dout.head_stride};
-    g.dq = {a->dq.p, a->dq.token_stride, a->dq.head_stride};
-    g.dk = {a->dk.p, a->dk.token_stride, a->dk.head_stride};
-    g.dv = {a->dv.p, a->dv.token_stride, a->dv.head_stride};
     g.stats = static_cast<float*>(workspace);
     g.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + sp.parts);
+    g.packed = static_cast<char*>(workspace) + sp.packed;
     return done(fn, launch_attention_backward(g, stream));
 }
 

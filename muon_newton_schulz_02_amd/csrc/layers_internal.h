@@ -73,11 +73,20 @@ struct AttnArgs {
     float *lse;
     float *stats;          // forward: m and l of every row of a piece; backward: lse in base 2 and delta of every row
     float *parts;          // float32 results of pieces
+    char *packed;          // copies of inputs with aligned rows
     const int32_t *cu_q, *cu_k;
     int64_t n_queries, n_keys;
     float scale;
     int32_t heads, kv_heads, dim, n_seqs, causal, dtype;
+    int32_t cols;          // of the inputs' rows: dim in whole chunks
+    bool wide;             // whether results are stored 4 at a time
 };
+// Which of q, k, v and dout are copied first, and where to.
+struct AttnPack {
+    bool copied[4] = {false, false, false, false};
+    int64_t at[4] = {0, 0, 0, 0}, total = 0;
+};
+AttnPack attention_pack(const AttnArgs& a, bool back);
 // How many waves a workgroup has, and how many pieces its walk over the other side is
 // cut into.
 struct AttnSplit {
@@ -87,8 +96,8 @@ AttnSplit attention_query_split(const AttnArgs& a);
 AttnSplit attention_key_split(const AttnArgs& a);
 int launch_attention_forward(const AttnArgs& a, void* stream);
 int launch_attention_backward(const AttnArgs& a, void* stream);
-// Its two walks (al: every array has rows of whole 16-byte chunks).
-int launch_attention_dq(const AttnArgs& a, const AttnSplit& sp, bool al, void* stream);
-int launch_attention_dkv(const AttnArgs& a, const AttnSplit& sp, bool al, void* stream);
+// Its two walks, over inputs with aligned rows.
+int launch_attention_dq(const AttnArgs& a, const AttnSplit& sp, void* stream);
+int launch_attention_dkv(const AttnArgs& a, const AttnSplit& sp, void* stream);
 
 }  // namespace ma
