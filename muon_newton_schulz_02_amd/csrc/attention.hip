@@ -26,24 +26,27 @@ namespace ma {
 namespace {
 
 template <typename T, int DP, int KV, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, (kPer<T, DP>)) void k_attention_forward(AttnArgs a, AttnGrid grid) {
-    constexpr int BLOCK = 32 * WAVES;
-    using KT = Tile<T, DP, KV, 64 * WAVES>;
+__global__ __launch_bounds__(64 * WAVES * kHalves<DP>, (kPer<T, DP>)) void k_attention_forward(AttnArgs a,
+                                                                                            AttnGrid grid) {
+    constexpr int BLOCK = 32 * WAVES, HALVES = kHalves<DP>, DW = DP / HALVES;
+    using KT = Tile<T, DP, KV, 64 * WAVES * HALVES>;
     __shared__ __attribute__((aligned(1024))) char lds[2][2][KT::kBytes];
+    __shared__ Exchange<HALVES == 2 ? 2 * WAVES : 0> exchange;
     const Job j = job_of<false, BLOCK>(a, grid);
     if (!j.any) return;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, h = lane >> 5;
+    const int half = __builtin_amdgcn_readfirstlane(wave % HALVES);
     const int kvh = j.head / (a.heads / a.kv_heads);
     const Rows<T> qx = rows_of<T>(a.q, j.head, j.q_at, j.q_len, a.cols);
     const Rows<T> kx = rows_of<T>(a.k, kvh, j.k_at, j.k_len, a.cols);
     const Rows<T> vx = rows_of<T>(a.v, kvh, j.k_at, j.k_len, a.cols);
-    const int q = j.row0 + 32 * wave + (lane & 31);
-    Frag<T> qf[DP / 16];
-    load_row<T, DP>(qx, q, qf);
+    const int q = j.row0 + 32 * (wave / HALVES) + (lane & 31);
+    Frag<T> qf[DW / 16];
+    load_row<T, DW / 16>(qx, q, half * (DW / 16), qf);
 
-    f32x16 o[DP / 32];
+    f32x16 o[DW / 32];
 #pragma unroll
-    for (int b = 0; b < DP / 32; ++b) o[b] = zero16();
+    for (int b = 0; b < DW / 32; ++b) o[b] = zero16();
     float m = -kInf, l = 0.f;
     const float k = a.scale * kLog2e;
     // key tiles that some row of the workgroup sees
@@ -71,7 +74,11 @@ __global__ __launch_bounds__(64 * WAVES, (kPer<T, DP>)) void k_attention_forward
         for (int n = 0; n < KV / 32; ++n) {
             s[n] = zero16();
 #pragma unroll
-            for (int d = 0; d < DP / 16; ++d) s[n] = mma(KT::rows(kt, 32 * n, d), qf[d], s[n]);
+            for (int d = 0; d < DW / 16; ++d) s[n] = mma(KT::rows(kt, 32 * n, half * (DW / 16) + d), qf[d], s[n]);
+        }
+        if constexpr (HALVES == 2) {         // (the sums over either half of the features)
+            static_assert(KV == 32, "one exchange a tile");
+            s[0] += exchange(s[0]);
         }
         if constexpr (decltype(part)::value) {
 #pragma unroll
@@ -94,7 +101,7 @@ __global__ __launch_bounds__(64 * WAVES, (kPer<T, DP>)) void k_attention_forward
             m = to;
             l *= c;
 #pragma unroll
-            for (int b = 0; b < DP / 32; ++b)
+            for (int b = 0; b < DW / 32; ++b)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) o[b][i] *= c;
         }
@@ -112,7 +119,7 @@ __global__ __launch_bounds__(64 * WAVES, (kPer<T, DP>)) void k_attention_forward
         for (int n = 0; n < KV / 16; ++n) {
             const Frag<T> p = frag_of<T>(s[n / 2], n % 2);
 #pragma unroll
-            for (int b = 0; b < DP / 32; ++b) o[b] = mma(KT::cols(vt, 16 * n, 32 * b), p, o[b]);
+            for (int b = 0; b < DW / 32; ++b) o[b] = mma(KT::cols(vt, 16 * n, half * DW + 32 * b), p, o[b]);
         }
     };
     const int whole = min(max(seen(a, j, j.row0), 0) / KV, sh.last);
@@ -122,19 +129,20 @@ __global__ __launch_bounds__(64 * WAVES, (kPer<T, DP>)) void k_attention_forward
     l += other_half(l);
     if (q >= j.q_len) return;
     const int64_t row = (int64_t)j.q_at + q;
+    const bool lead = h == 0 && half == 0;
     if (grid.pieces > 1) {
-        store_row<float, DP / 32>(part_row(a.parts, j.piece, a.heads, j.head, a.n_queries, row, a.dim), a.dim, o, 1.f,
-                                  a.dim % 4 == 0);
-        if (h == 0) {
+        store_row<float, DW / 32>(part_row(a.parts, j.piece, a.heads, j.head, a.n_queries, row, a.dim), a.dim,
+                                  half * DW, o, 1.f, a.dim % 4 == 0);
+        if (lead) {
             float* s = a.stats + (((int64_t)j.piece * a.heads + j.head) * a.n_queries + row) * 2;
             s[0] = m;
             s[1] = l;
         }
         return;
     }
-    store_row<T, DP / 32>(row_of<T>(a.o, j.head, row), a.dim, o, l > 0.f ? 1.f / l : l == 0.f ? 0.f : l,
+    store_row<T, DW / 32>(row_of<T>(a.o, j.head, row), a.dim, half * DW, o, l > 0.f ? 1.f / l : l == 0.f ? 0.f : l,
                          a.wide);
-    if (h == 0) a.lse[(int64_t)j.head * a.n_queries + row] = l == 0.f ? -kInf : fmaf(m, a.scale, logf(l));
+    if (lead) a.lse[(int64_t)j.head * a.n_queries + row] = l == 0.f ? -kInf : fmaf(m, a.scale, logf(l));
 }
 
 // What a launch that joins pieces walks: rows inside sequences x heads, 64 threads a row.
@@ -259,27 +267,34 @@ __global__ __launch_bounds__(256) void k_attention_delta(AttnArgs a, int64_t row
 
 }  // namespace
 
-// Waves of a workgroup, and pieces of its walk, for `rows` rows of n_seqs sequences and `heads`
-// heads against `walk` rows of the other side.  Short sequences take workgroups of 2
-// waves.  Pieces: until as many workgroups are there as run at once, in causal calls twice as
-// many, since the longest walk is twice the mean one and would otherwise end alone (key
-// blocks of 7 sequences of 20011 tokens, 628 workgroups: 1158 us in one piece, 914 + 42 to join in
-// two).  A piece has at least 128 rows to walk, in float32, whose products take 16 times as long, 32.
-static AttnSplit split_of(const AttnArgs& a, int64_t rows, int64_t walk, int64_t heads) {
+// Rows of a workgroup, and pieces of its walk, for `rows` rows of n_seqs sequences and `heads`
+// heads against `walk` rows of the other side.  Rows: `most`, or half as many where the
+// sequences have no more.  Pieces: until as many workgroups are there as run at once, in causal
+// calls twice as many, since the longest walk is twice the mean one and would otherwise end
+// alone (key blocks of 7 sequences of 20011 tokens, 628 workgroups: 1158 us in one piece, 914 +
+// 42 to join in two).  A piece has at least 128 rows to walk, in float32, whose products take
+// 16 times as long, 32.
+static AttnSplit split_of(const AttnArgs& a, int64_t rows, int64_t walk, int64_t heads, int most, int at_once) {
     AttnSplit s;
     if (rows == 0 || a.n_seqs == 0) return s;
     const bool wide = a.dtype == MA_PARAM_FP32;
     const int64_t each = ceil_div(rows, a.n_seqs);
-    s.waves = each <= 64 ? 2 : 4;
-    const int64_t blocks = ceil_div(each, 32 * s.waves) * a.n_seqs * heads;
-    const int64_t at_once = (int64_t)kCus * (a.dim * (wide ? 4 : 2) <= 256 ? 2 : 1);
+    s.rows = each <= most / 2 ? most / 2 : most;
+    const int64_t blocks = ceil_div(each, s.rows) * a.n_seqs * heads;
     const int64_t want = a.causal ? ceil_div(2 * at_once, blocks) : at_once / blocks;
     s.pieces = (int32_t)std::max<int64_t>(1, std::min<int64_t>({want, ceil_div(walk, a.n_seqs * (wide ? 32 : 128)), 32}));
     return s;
 }
-AttnSplit attention_query_split(const AttnArgs& a) { return split_of(a, a.n_queries, a.n_keys, a.heads); }
+// Workgroups of 4 waves (8 for the keys of 256 bfloat16 features): two on a CU where a
+// lane has 256 registers.
+AttnSplit attention_query_split(const AttnArgs& a) {
+    const bool two = a.dtype == MA_PARAM_BF16 || a.dim <= 64;
+    return split_of(a, a.n_queries, a.n_keys, a.heads, a.dim > 128 ? 64 : 128, kCus * (two ? 2 : 1));
+}
 AttnSplit attention_key_split(const AttnArgs& a) {
-    return split_of(a, a.n_keys, a.n_queries * (a.heads / a.kv_heads), a.kv_heads);
+    const bool bf16 = a.dtype == MA_PARAM_BF16;
+    return split_of(a, a.n_keys, a.n_queries * (a.heads / a.kv_heads), a.kv_heads, a.dim > 128 && !bf16 ? 64 : 128,
+                    kCus * (a.dim <= (bf16 ? 128 : 64) ? 2 : 1));
 }
 
 static unsigned join_grid(int64_t rows, int64_t heads) { return (unsigned)ceil_div(rows * heads, 4); }
@@ -354,20 +369,22 @@ int launch_attention_forward(const AttnArgs& a, void* stream) {
     int rc = pack_inputs(g, false, stream);
     if (rc != (int)hipSuccess) return rc;
     const AttnSplit sp = attention_query_split(a);
-    rc = by_kind(a, sp.waves, [&](auto t, auto dp, auto wv) {
+    const AttnGrid grid = grid_of(a.n_queries, a.n_seqs, a.heads, sp.rows, sp.pieces);
+    rc = by_kind(a, sp.rows, [&](auto t, auto dp, auto wv) {
         using T = decltype(t);
         constexpr int DP = decltype(dp)::value, WAVES = decltype(wv)::value;
-        const AttnGrid grid = grid_of(a.n_queries, a.n_seqs, a.heads, WAVES, sp.pieces);
-        constexpr int KV = sizeof(T) == 2 ? 64 : 32;
-        hipLaunchKernelGGL((k_attention_forward<T, DP, KV, WAVES>), dim3((unsigned)grid.slots * a.heads * grid.pieces),
-                           dim3(64 * WAVES), 0, (hipStream_t)stream, g, grid);
+        constexpr int KV = sizeof(T) == 2 && kHalves<DP> == 1 ? 64 : 32;
+        if constexpr (WAVES * kHalves<DP> == 4 || WAVES * kHalves<DP> == 2)
+            hipLaunchKernelGGL((k_attention_forward<T, DP, KV, WAVES>),
+                               dim3((unsigned)grid.slots * a.heads * grid.pieces), dim3(64 * WAVES * kHalves<DP>), 0,
+                               (hipStream_t)stream, g, grid);
     });
     if (rc != (int)hipSuccess || sp.pieces == 1) return rc;
-    const dim3 grid(join_grid(a.n_queries, a.heads)), block(256);
+    const dim3 rows(join_grid(a.n_queries, a.heads)), block(256);
     if (a.dtype == MA_PARAM_BF16)
-        hipLaunchKernelGGL(k_attention_join<__bf16>, grid, block, 0, (hipStream_t)stream, a, sp.pieces);
+        hipLaunchKernelGGL(k_attention_join<__bf16>, rows, block, 0, (hipStream_t)stream, a, sp.pieces);
     else
-        hipLaunchKernelGGL(k_attention_join<float>, grid, block, 0, (hipStream_t)stream, a, sp.pieces);
+        hipLaunchKernelGGL(k_attention_join<float>, rows, block, 0, (hipStream_t)stream, a, sp.pieces);
     return (int)hipGetLastError();
 }
 

@@ -12,37 +12,38 @@ namespace {
 
 // Whether a workgroup's rows of V stay in LDS instead of registers, which then fit two waves.
 template <typename T, int DP>
-constexpr bool kStage = DP * (int)sizeof(T) == 256;
+constexpr bool kStage = sizeof(T) == 2 && DP == 128;
 
 template <typename T, int DP, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, (kPer<T, DP>)) void k_attention_dkv(AttnArgs a, AttnGrid grid) {
-    constexpr int BLOCK = 32 * WAVES, QT = 32, RING = 2;
-    using QTile = Tile<T, DP, QT, 64 * WAVES>;
-    using VTile = Tile<T, DP, BLOCK, 64 * WAVES>;
+__global__ __launch_bounds__(64 * WAVES * kHalves<DP>, (kPer<T, DP>)) void k_attention_dkv(AttnArgs a, AttnGrid grid) {
+    constexpr int BLOCK = 32 * WAVES, QT = 32, RING = 2, HALVES = kHalves<DP>, DW = DP / HALVES, ALL = WAVES * HALVES;
+    using QTile = Tile<T, DP, QT, 64 * ALL>;
+    using VTile = Tile<T, DP, BLOCK, 64 * ALL>;
     constexpr bool STAGE = kStage<T, DP>;
     __shared__ __attribute__((aligned(1024))) char lds[RING][2][QTile::kBytes];
     __shared__ __attribute__((aligned(1024))) char vlds[STAGE ? VTile::kBytes : 16];
-    __shared__ __attribute__((aligned(256))) float stat[RING][WAVES][2 * QT];
+    __shared__ __attribute__((aligned(256))) float stat[RING][ALL][2 * QT];
+    __shared__ Exchange<HALVES == 2 ? ALL : 0> exchange;
     const Job j = job_of<true, BLOCK>(a, grid);        // (its head is a key head)
     if (!j.any) return;
     const int lane = threadIdx.x & 63, h = lane >> 5;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = wave % HALVES;
     const int group = a.heads / a.kv_heads;
-    const int key = j.row0 + 32 * wave + (lane & 31);
+    const int key = j.row0 + 32 * (wave / HALVES) + (lane & 31);
+    const Rows<T> kx = rows_of<T>(a.k, j.head, j.k_at, j.k_len, a.cols);
     const Rows<T> vx = rows_of<T>(a.v, j.head, j.k_at, j.k_len, a.cols);
-    const Own<T, DP> kf(rows_of<T>(a.k, j.head, j.k_at, j.k_len, a.cols), key);
-    const Own<T, DP, DP * (int)sizeof(T) <= 512 && !STAGE> vown(vx, key);
+    // (of two waves one forms the scores, the other dout v)
+    Frag<T> kf[DP / 16], vf[HALVES == 1 && !STAGE ? DP / 16 : 1];
+    load_row<T, DP / 16>(half == 0 ? kx : vx, key, 0, kf);
     if constexpr (STAGE) {
         const typename VTile::Copy copy_v(vx);
         copy_v(vlds, vx, j.row0);
+    } else if constexpr (HALVES == 1) {
+        load_row<T, DP / 16>(vx, key, 0, vf);
     }
-    auto vf = [&](int d) {
-        if constexpr (STAGE) return VTile::rows(vlds, 32 * wave, d);
-        else return vown(d);
-    };
-    f32x16 dk[DP / 32], dv[DP / 32];
+    f32x16 dk[DW / 32], dv[DW / 32];
 #pragma unroll
-    for (int b = 0; b < DP / 32; ++b) dk[b] = dv[b] = zero16();
+    for (int b = 0; b < DW / 32; ++b) dk[b] = dv[b] = zero16();
     const float k = a.scale * kLog2e;
     // the first tile with a query that sees this workgroup's first key
     const int off = j.k_len - j.q_len;
@@ -75,10 +76,23 @@ __global__ __launch_bounds__(64 * WAVES, (kPer<T, DP>)) void k_attention_dkv(Att
         const float* sd = stat[slot][wave];
         slot ^= 1;
         f32x16 s = zero16(), p = zero16();
+        const char* mine = half == 0 ? qt : dt;
 #pragma unroll
-        for (int d = 0; d < DP / 16; ++d) s = mma(QTile::rows(qt, 0, d), kf(d), s);
+        for (int d = 0; d < DP / 16; ++d) s = mma(QTile::rows(mine, 0, d), kf[d], s);
+        if constexpr (HALVES == 1) {
 #pragma unroll
-        for (int d = 0; d < DP / 16; ++d) p = mma(QTile::rows(dt, 0, d), vf(d), p);
+            for (int d = 0; d < DP / 16; ++d) {
+                if constexpr (STAGE) p = mma(QTile::rows(dt, 0, d), VTile::rows(vlds, 32 * wave, d), p);
+                else p = mma(QTile::rows(dt, 0, d), vf[d], p);
+            }
+        } else {
+            p = exchange(s);
+            if (half == 1) {
+                const f32x16 t = s;
+                s = p;
+                p = t;
+            }
+        }
         // (operands of the next products loaded up here would not fit the registers)
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -108,13 +122,13 @@ __global__ __launch_bounds__(64 * WAVES, (kPer<T, DP>)) void k_attention_dkv(Att
         for (int u = 0; u < 2; ++u) {
             const Frag<T> fs = frag_of<T>(s, u);
 #pragma unroll
-            for (int b = 0; b < DP / 32; ++b) dv[b] = mma(QTile::cols(dt, 16 * u, 32 * b), fs, dv[b]);
+            for (int b = 0; b < DW / 32; ++b) dv[b] = mma(QTile::cols(dt, 16 * u, half * DW + 32 * b), fs, dv[b]);
         }
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const Frag<T> fp = frag_of<T>(p, u);
 #pragma unroll
-            for (int b = 0; b < DP / 32; ++b) dk[b] = mma(QTile::cols(qt, 16 * u, 32 * b), fp, dk[b]);
+            for (int b = 0; b < DW / 32; ++b) dk[b] = mma(QTile::cols(qt, 16 * u, half * DW + 32 * b), fp, dk[b]);
         }
     };
     if (sh.first < sh.last) {
@@ -134,24 +148,27 @@ __global__ __launch_bounds__(64 * WAVES, (kPer<T, DP>)) void k_attention_dkv(Att
     if (key >= j.k_len) return;
     const int64_t row = (int64_t)j.k_at + key;
     if (grid.pieces > 1) {
-        store_row<float, DP / 32>(part_row(a.parts, j.piece, a.kv_heads, j.head, a.n_keys, row, a.dim), a.dim, dk,
-                                  a.scale, a.dim % 4 == 0);
-        store_row<float, DP / 32>(part_row(a.parts, grid.pieces + j.piece, a.kv_heads, j.head, a.n_keys, row, a.dim), a.dim,
-                                  dv, 1.f, a.dim % 4 == 0);
+        store_row<float, DW / 32>(part_row(a.parts, j.piece, a.kv_heads, j.head, a.n_keys, row, a.dim), a.dim, half * DW,
+                                  dk, a.scale, a.dim % 4 == 0);
+        store_row<float, DW / 32>(part_row(a.parts, grid.pieces + j.piece, a.kv_heads, j.head, a.n_keys, row, a.dim),
+                                  a.dim, half * DW, dv, 1.f, a.dim % 4 == 0);
     } else {
-        store_row<T, DP / 32>(row_of<T>(a.dk, j.head, row), a.dim, dk, a.scale, a.wide);
-        store_row<T, DP / 32>(row_of<T>(a.dv, j.head, row), a.dim, dv, 1.f, a.wide);
+        store_row<T, DW / 32>(row_of<T>(a.dk, j.head, row), a.dim, half * DW, dk, a.scale, a.wide);
+        store_row<T, DW / 32>(row_of<T>(a.dv, j.head, row), a.dim, half * DW, dv, 1.f, a.wide);
     }
 }
 
 }  // namespace
 
 int launch_attention_dkv(const AttnArgs& a, const AttnSplit& sp, void* stream) {
-    return by_kind(a, sp.waves, [&](auto t, auto dp, auto wv) {
-        constexpr int WAVES = decltype(wv)::value;
-        const AttnGrid g = grid_of(a.n_keys, a.n_seqs, a.kv_heads, WAVES, sp.pieces);
-        hipLaunchKernelGGL((k_attention_dkv<decltype(t), decltype(dp)::value, WAVES>),
-                           dim3((unsigned)g.slots * a.kv_heads * g.pieces), dim3(64 * WAVES), 0, (hipStream_t)stream, a, g);
+    const AttnGrid grid = grid_of(a.n_keys, a.n_seqs, a.kv_heads, sp.rows, sp.pieces);
+    return by_kind(a, sp.rows, [&](auto t, auto dp, auto wv) {
+        constexpr int DP = decltype(dp)::value, WAVES = decltype(wv)::value;
+        // (float32 and 256 features: workgroups of 64 or 32 rows; else 128 or 64)
+        if constexpr (sizeof(t) == 4 && kHalves<DP> == 2 ? WAVES <= 2 : WAVES >= 2)
+            hipLaunchKernelGGL((k_attention_dkv<decltype(t), DP, WAVES>),
+                               dim3((unsigned)grid.slots * a.kv_heads * grid.pieces), dim3(64 * WAVES * kHalves<DP>), 0,
+                               (hipStream_t)stream, a, grid);
     });
 }
 

@@ -13,26 +13,32 @@ namespace {
 template <typename T, int DP>
 constexpr int kRing = DP * (int)sizeof(T) <= 256 ? 3 : 2;
 template <typename T, int DP, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, (kPer<T, DP>)) void k_attention_dq(AttnArgs a, AttnGrid grid) {
-    constexpr int BLOCK = 32 * WAVES, KV = 32, RING = kRing<T, DP>;
-    using KT = Tile<T, DP, KV, 64 * WAVES>;
+__global__ __launch_bounds__(64 * WAVES * kHalves<DP>, (kPer<T, DP>)) void k_attention_dq(AttnArgs a, AttnGrid grid) {
+    constexpr int BLOCK = 32 * WAVES, KV = 32, RING = kRing<T, DP>, HALVES = kHalves<DP>, DW = DP / HALVES;
+    using KT = Tile<T, DP, KV, 64 * WAVES * HALVES>;
     constexpr int kTileCopies = 2 * KT::kCopies;
     __shared__ __attribute__((aligned(1024))) char lds[RING][2][KT::kBytes];
+    __shared__ Exchange<HALVES == 2 ? 2 * WAVES : 0> exchange;
     const Job j = job_of<false, BLOCK>(a, grid);
     if (!j.any) return;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, h = lane >> 5;
+    const int half = __builtin_amdgcn_readfirstlane(wave % HALVES);
     const int kvh = j.head / (a.heads / a.kv_heads);
     const Rows<T> kx = rows_of<T>(a.k, kvh, j.k_at, j.k_len, a.cols);
     const Rows<T> vx = rows_of<T>(a.v, kvh, j.k_at, j.k_len, a.cols);
-    const int q = j.row0 + 32 * wave + (lane & 31);
-    const Own<T, DP> qf(rows_of<T>(a.q, j.head, j.q_at, j.q_len, a.cols), q);
-    const Own<T, DP> df(rows_of<T>(a.dout, j.head, j.q_at, j.q_len, a.cols), q);
+    const Rows<T> qx = rows_of<T>(a.q, j.head, j.q_at, j.q_len, a.cols);
+    const Rows<T> dx = rows_of<T>(a.dout, j.head, j.q_at, j.q_len, a.cols);
+    const int q = j.row0 + 32 * (wave / HALVES) + (lane & 31);
+    // (of two waves one forms the scores, the other dout v)
+    Frag<T> qf[DP / 16], df[HALVES == 1 ? DP / 16 : 1];
+    load_row<T, DP / 16>(half == 0 ? qx : dx, q, 0, qf);
+    if constexpr (HALVES == 1) load_row<T, DP / 16>(dx, q, 0, df);
     const float* st = a.stats + ((int64_t)j.head * a.n_queries + j.q_at + q) * 2;
     const float ls = q < j.q_len ? st[0] : kInf, delta = q < j.q_len ? st[1] : 0.f;
 
-    f32x16 dq[DP / 32];
+    f32x16 dq[DW / 32];
 #pragma unroll
-    for (int b = 0; b < DP / 32; ++b) dq[b] = zero16();
+    for (int b = 0; b < DW / 32; ++b) dq[b] = zero16();
     const float k = a.scale * kLog2e;
     const int end = min(j.row0 + BLOCK, j.q_len) - 1;
     const Share sh(max(0, seen(a, j, end) + KV - 1) / KV, j.piece, grid.pieces);
@@ -53,10 +59,20 @@ __global__ __launch_bounds__(64 * WAVES, (kPer<T, DP>)) void k_attention_dq(Attn
         const char* vt = lds[slot][1];
         slot = slot == RING - 1 ? 0 : slot + 1;
         f32x16 s = zero16(), p = zero16();
+        const char* mine = half == 0 ? kt : vt;
 #pragma unroll
-        for (int d = 0; d < DP / 16; ++d) s = mma(KT::rows(kt, 0, d), qf(d), s);
+        for (int d = 0; d < DP / 16; ++d) s = mma(KT::rows(mine, 0, d), qf[d], s);
+        if constexpr (HALVES == 1) {
 #pragma unroll
-        for (int d = 0; d < DP / 16; ++d) p = mma(KT::rows(vt, 0, d), df(d), p);
+            for (int d = 0; d < DP / 16; ++d) p = mma(KT::rows(vt, 0, d), df[d], p);
+        } else {
+            p = exchange(s);
+            if (half == 1) {
+                const f32x16 t = s;
+                s = p;
+                p = t;
+            }
+        }
 #pragma unroll
         for (int i = 0; i < 16; ++i) p[i] = __builtin_amdgcn_exp2f(fmaf(s[i], k, -ls)) * (p[i] - delta);
         if constexpr (decltype(part)::value) {
@@ -67,7 +83,7 @@ __global__ __launch_bounds__(64 * WAVES, (kPer<T, DP>)) void k_attention_dq(Attn
         for (int u = 0; u < 2; ++u) {
             const Frag<T> f = frag_of<T>(p, u);
 #pragma unroll
-            for (int b = 0; b < DP / 32; ++b) dq[b] = mma(KT::cols(kt, 16 * u, 32 * b), f, dq[b]);
+            for (int b = 0; b < DW / 32; ++b) dq[b] = mma(KT::cols(kt, 16 * u, half * DW + 32 * b), f, dq[b]);
         }
     };
     if (sh.first < sh.last) {
@@ -81,20 +97,22 @@ __global__ __launch_bounds__(64 * WAVES, (kPer<T, DP>)) void k_attention_dq(Attn
     if (q >= j.q_len) return;
     const int64_t row = (int64_t)j.q_at + q;
     if (grid.pieces > 1)
-        store_row<float, DP / 32>(part_row(a.parts, j.piece, a.heads, j.head, a.n_queries, row, a.dim), a.dim, dq,
-                                  a.scale, a.dim % 4 == 0);
+        store_row<float, DW / 32>(part_row(a.parts, j.piece, a.heads, j.head, a.n_queries, row, a.dim), a.dim,
+                                  half * DW, dq, a.scale, a.dim % 4 == 0);
     else
-        store_row<T, DP / 32>(row_of<T>(a.dq, j.head, row), a.dim, dq, a.scale, a.wide);
+        store_row<T, DW / 32>(row_of<T>(a.dq, j.head, row), a.dim, half * DW, dq, a.scale, a.wide);
 }
 
 }  // namespace
 
 int launch_attention_dq(const AttnArgs& a, const AttnSplit& sp, void* stream) {
-    return by_kind(a, sp.waves, [&](auto t, auto dp, auto wv) {
-        constexpr int WAVES = decltype(wv)::value;
-        const AttnGrid g = grid_of(a.n_queries, a.n_seqs, a.heads, WAVES, sp.pieces);
-        hipLaunchKernelGGL((k_attention_dq<decltype(t), decltype(dp)::value, WAVES>),
-                           dim3((unsigned)g.slots * a.heads * g.pieces), dim3(64 * WAVES), 0, (hipStream_t)stream, a, g);
+    const AttnGrid grid = grid_of(a.n_queries, a.n_seqs, a.heads, sp.rows, sp.pieces);
+    return by_kind(a, sp.rows, [&](auto t, auto dp, auto wv) {
+        constexpr int DP = decltype(dp)::value, WAVES = decltype(wv)::value;
+        if constexpr (WAVES * kHalves<DP> == 4 || WAVES * kHalves<DP> == 2)
+            hipLaunchKernelGGL((k_attention_dq<decltype(t), DP, WAVES>),
+                               dim3((unsigned)grid.slots * a.heads * grid.pieces), dim3(64 * WAVES * kHalves<DP>), 0,
+                               (hipStream_t)stream, a, grid);
     });
 }
 

@@ -108,6 +108,9 @@ __device__ __forceinline__ void copies_barrier() {
     __builtin_amdgcn_sched_barrier(0);
 }
 
+// The same for LDS alone: copies may still be under way.
+__device__ __forceinline__ void lds_barrier() { copies_barrier<63>(); }
+
 // One head of a packed array, as the rows of one sequence: whole 16-byte chunks at
 // 16-byte addresses (other inputs are copied into such rows first).
 template <typename T>
@@ -217,22 +220,22 @@ __device__ __forceinline__ Frag<T> load_step(const Rows<T>& x, int row, int s) {
     for (int e = 0; e < 8; ++e) f[e] = (T)(in ? v[e] : 0.f);
     return f;
 }
-template <typename T, int DP>
-__device__ __forceinline__ void load_row(const Rows<T>& x, int row, Frag<T>* f) {
+template <typename T, int N>
+__device__ __forceinline__ void load_row(const Rows<T>& x, int row, int first, Frag<T>* f) {
 #pragma unroll
-    for (int s = 0; s < DP / 16; ++s) f[s] = load_step<T>(x, row, s);
+    for (int s = 0; s < N; ++s) f[s] = load_step<T>(x, row, first + s);
 }
 
 // Stores a wave's transposed results (columns of x by rows of 32 at a time) as row `row`:
-// acc[b] element i is column 32 b + result_row(i, h).
+// acc[b] element i is column col0 + 32 b + result_row(i, h).
 template <typename T, int NB>
-__device__ __forceinline__ void store_row(T* p, int dim, const f32x16* acc, float scale, bool wide) {
+__device__ __forceinline__ void store_row(T* p, int dim, int col0, const f32x16* acc, float scale, bool wide) {
     const int h = (threadIdx.x & 63) >> 5;
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-            const int col = 32 * b + 8 * g + 4 * h;
+            const int col = col0 + 32 * b + 8 * g + 4 * h;
             float v[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = acc[b][4 * g + e] * scale;
@@ -395,29 +398,39 @@ __device__ __forceinline__ float* part_row(float* parts, int piece, int heads, i
     return parts + (((int64_t)piece * heads + head) * rows + row) * dim;
 }
 
-// Workgroups of 4 waves on a CU (which bounds the registers: 256 or 512 a lane).
-template <typename T, int DP>
-constexpr int kPer = DP * (int)sizeof(T) <= 256 ? 2 : 1;
+// Two waves share 32 rows of 256 features: the sums of one's half of the features, and what
+// leads there, fit its registers (in float32 only so, in bfloat16 twice as many waves are on a
+// CU).  The products before the softmax are shared out, and their results go to the other wave
+// through LDS.
+template <int DP>
+constexpr int kHalves = DP > 128 ? 2 : 1;
 
-// The straight operands of a wave's own rows, held in registers or, where they do not
-// fit beside the sums (float32 and 256 features), read again from the caches for every tile.
-template <typename T, int DP, bool HOLD = DP * (int)sizeof(T) <= 512>
-struct Own {
-    Rows<T> x;
-    int row;
-    Frag<T> f[HOLD ? DP / 16 : 1];
-    __device__ __forceinline__ Own(const Rows<T>& r, int at) : x(r), row(at) {
-        if constexpr (HOLD) load_row<T, DP>(x, row, f);
-    }
-    __device__ __forceinline__ Frag<T> operator()(int s) const {
-        if constexpr (HOLD) return f[s];
-        // (four steps' loads at a time, and not moved out of the tiles' loop)
-        if (s % 4 == 0) __builtin_amdgcn_sched_barrier(0);
-        int r = row;
-        asm volatile("" : "+v"(r));
-        return load_step<T>(x, r, s);
+// Waves on a SIMD, which bounds the registers: 256 or 512 a lane.
+template <typename T, int DP>
+constexpr int kPer = sizeof(T) == 2 || DP <= 64 ? 2 : 1;
+
+// N results from the wave that shares this one's rows; `mine` is what it gets.
+template <int WAVES>
+struct Exchange {
+    f32x4 at[WAVES][4][64];
+    __device__ __forceinline__ f32x16 operator()(const f32x16& mine) {
+        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+            at[wave][g][lane] = (f32x4){mine[4 * g], mine[4 * g + 1], mine[4 * g + 2], mine[4 * g + 3]};
+        lds_barrier();
+        f32x16 v;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const f32x4 w = at[wave ^ 1][g][lane];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[4 * g + e] = w[e];
+        }
+        return v;
     }
 };
+template <>
+struct Exchange<0> {};
 
 // Whether rows are whole 16-byte chunks at 16-byte addresses, which copies into LDS and wide
 // stores need.
@@ -432,12 +445,13 @@ inline bool al_heads(const AttnArray& x, int32_t dim, int32_t dtype) {
 template <int V>
 using Int = std::integral_constant<int, V>;
 
-// Calls f(T{}, padded dim, waves).
+// Calls f(T{}, padded dim, waves of 32 rows): those of `rows` rows.
 template <typename F>
-int by_kind(const AttnArgs& a, int waves, F f) {
+int by_kind(const AttnArgs& a, int rows, F f) {
     auto each = [&](auto t, auto dp) {
-        if (waves == 4) f(t, dp, Int<4>{});
-        else f(t, dp, Int<2>{});
+        if (rows == 128) f(t, dp, Int<4>{});
+        else if (rows == 64) f(t, dp, Int<2>{});
+        else f(t, dp, Int<1>{});
     };
     auto dims = [&](auto t) {
         if (a.dim <= 64) each(t, Int<64>{});
@@ -449,12 +463,12 @@ int by_kind(const AttnArgs& a, int waves, F f) {
     return (int)hipGetLastError();
 }
 
-// A launch's slots for row blocks of `waves` waves, and how they are taken: in falling order of
+// A launch's slots for blocks of `block` rows, and how they are taken: in falling order of
 // work where more workgroups are queued than run at once, so that the last to begin are
 // short (7 causal sequences of 20011 tokens: forward 392 -> 332 us, dq 555 -> 458).
-inline AttnGrid grid_of(int64_t total, int64_t n_seqs, int64_t heads, int waves, int pieces) {
+inline AttnGrid grid_of(int64_t total, int64_t n_seqs, int64_t heads, int block, int pieces) {
     AttnGrid g;
-    g.slots = (int32_t)(total / (32 * waves) + n_seqs);
+    g.slots = (int32_t)(total / block + n_seqs);
     g.pieces = pieces;
     g.ordered = n_seqs <= kOrderedSeqs && (int64_t)g.slots * heads * pieces > 2 * kCus;
     return g;

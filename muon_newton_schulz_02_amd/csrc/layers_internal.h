@@ -87,10 +87,10 @@ struct AttnPack {
     int64_t at[4] = {0, 0, 0, 0}, total = 0;
 };
 AttnPack attention_pack(const AttnArgs& a, bool back);
-// How many waves a workgroup has, and how many pieces its walk over the other side is
-// cut into.
+// How many rows a workgroup takes, and how many pieces its walk over the other side is cut
+// into.
 struct AttnSplit {
-    int32_t waves = 4, pieces = 1;
+    int32_t rows = 128, pieces = 1;
 };
 AttnSplit attention_query_split(const AttnArgs& a);
 AttnSplit attention_key_split(const AttnArgs& a);
