@@ -432,9 +432,10 @@ def _space(size_of, a) -> int:
     return n.value
 
 
-def _sizes_args(n_queries, n_keys, heads, kv_heads, head_dim, n_seqs, dtype):
-    """Arguments of contiguous arrays of these sizes."""
+def _sizes_args(n_queries, n_keys, heads, kv_heads, head_dim, n_seqs, causal, dtype):
+    """Arguments of contiguous, aligned arrays of these sizes."""
     a = _abi.ma_attention()
+    a.causal = 1 if causal else 0
     a.dtype, a.heads, a.kv_heads, a.head_dim = _DTYPES[dtype], heads, kv_heads, head_dim
     a.n_queries, a.n_keys, a.n_seqs, a.scale = n_queries, n_keys, n_seqs, 1.0
     a.cu_q = a.cu_k = 256          # (only looked at for being there)
@@ -445,14 +446,18 @@ def _sizes_args(n_queries, n_keys, heads, kv_heads, head_dim, n_seqs, dtype):
 
 
 def ma_attention_forward_workspace_size(n_queries: int, n_keys: int, heads: int, kv_heads: int, head_dim: int,
-                                        n_seqs: int = 1, dtype=torch.bfloat16) -> int:
-    a = _sizes_args(n_queries, n_keys, heads, kv_heads, head_dim, n_seqs, dtype)
+                                        n_seqs: int = 1, causal: bool = True, dtype=torch.bfloat16) -> int:
+    """Bytes that serve contiguous, 16-byte aligned arrays of these sizes (a call without a workspace
+    allocates what its own arrays need)."""
+    a = _sizes_args(n_queries, n_keys, heads, kv_heads, head_dim, n_seqs, causal, dtype)
     return _space(_abi.load().ma_attention_forward_workspace_size, a)
 
 
 def ma_attention_backward_workspace_size(n_queries: int, n_keys: int, heads: int, kv_heads: int, head_dim: int,
-                                         n_seqs: int = 1, dtype=torch.bfloat16) -> int:
-    a = _sizes_args(n_queries, n_keys, heads, kv_heads, head_dim, n_seqs, dtype)
+                                         n_seqs: int = 1, causal: bool = True, dtype=torch.bfloat16) -> int:
+    """Bytes that serve contiguous, 16-byte aligned arrays of these sizes (a call without a workspace
+    allocates what its own arrays need)."""
+    a = _sizes_args(n_queries, n_keys, heads, kv_heads, head_dim, n_seqs, causal, dtype)
     return _space(_abi.load().ma_attention_backward_workspace_size, a)
 
 

@@ -589,3 +589,349 @@ def test_attention_empty():
     assert torch.all(dq == 0) and dk.shape == (0, 2, 64)
     dq, dk, dv = M.ma_attention_backward(e, e, x, x, e, lse[:, :0].contiguous(), causal=False)   # no queries
     assert torch.all(dk == 0) and torch.all(dv == 0)
+
+
+# ------------------------------------------------------------ used together --
+
+LENS = [13, 1, 50, 32]
+HEADS, KV, DIM, VOCAB, HIDDEN = 4, 2, 16, 300, 64
+SECTIONS = (2, 3, 3)
+WEIGHTS = ("table", "w1", "wqkv", "wo", "w2", "head")
+LAYER_NAMES = ["action_expert.embed_tokens.weight", "action_expert.layers.0.input_layernorm.weight",
+               "action_expert.layers.0.self_attn.qkv_proj.weight", "action_expert.layers.0.self_attn.o_proj.weight",
+               "action_expert.norm.weight", "action_expert.lm_head.weight"]
+
+
+def _block_inputs(seed, kind="fp32"):
+    rng = np.random.default_rng(seed)
+    n = sum(LENS)
+    p = dict(ids=torch.from_numpy(rng.integers(0, VOCAB, n)).cuda(), answer=torch.from_numpy(rng.integers(0, VOCAB, n)).cuda(),
+             pos=torch.from_numpy(rng.integers(0, 1000, (3, n))).cuda(),
+             g=_dev(rng.standard_normal(n) / n), h=_dev(np.full(n, 0.1 / n)))
+    for name, shape, std in (("table", (VOCAB, HIDDEN), 0.1), ("wqkv", ((HEADS + 2 * KV) * DIM, HIDDEN), 0.125),
+                             ("wo", (HIDDEN, HEADS * DIM), 0.125), ("head", (VOCAB, HIDDEN), 0.125)):
+        p[name] = _dev(std * rng.standard_normal(shape), kind)
+    for name in ("w1", "w2"):
+        p[name] = _dev(1 + 0.2 * rng.standard_normal(HIDDEN), kind)
+    return p
+
+
+def _block(p, cu, plan):
+    """A transformer block with its loss: embedding, norm, turned queries and keys, attention, residual, norm,
+    answers' log probabilities with a bonus on entropy; forward and backward with the operators, plain matrix
+    products for the layers themselves.  (loss parts, gradients or their sources in the order of WEIGHTS)"""
+    n = p["ids"].numel()
+    x = M.ma_embedding_lookup(p["table"], p["ids"], scale=8.0)
+    y1, s1, inv1, c1 = M.ma_rms_norm_forward(x, p["w1"], y_ckpt=True)
+    qkv = (y1 @ p["wqkv"].t()).view(n, HEADS + 2 * KV, DIM)
+    qk = qkv[:, :HEADS + KV]
+    M.ma_rotary(qk, p["pos"], plan, out=qk)
+    q, k, v = qkv[:, :HEADS], qkv[:, HEADS:HEADS + KV], qkv[:, HEADS + KV:]
+    o, lse = M.ma_attention_forward(q, k, v, cu, cu)
+    a = o.view(n, -1)
+    y2, s2, inv2, c2 = M.ma_rms_norm_forward(a @ p["wo"].t(), p["w2"], x, y_ckpt=True)
+    z = y2 @ p["head"].t()
+    lp, ent, zl, _, _ = M.ma_token_logprob_forward(z, p["answer"])
+    # backward
+    dz = M.ma_token_logprob_backward(z, p["answer"], zl, p["g"], entropy=ent, dentropy=p["h"], out=z)
+    ds2, dw2 = M.ma_rms_norm_backward(dz @ p["head"], s2, inv2, p["w2"])
+    dqkv = torch.empty_like(qkv)
+    dq, dk, dv = dqkv[:, :HEADS], dqkv[:, HEADS:HEADS + KV], dqkv[:, HEADS + KV:]
+    M.ma_attention_backward((ds2 @ p["wo"]).view_as(o), q, k, v, o, lse, cu, cu, dq=dq, dk=dk, dv=dv)
+    dqk = dqkv[:, :HEADS + KV]
+    M.ma_rotary(dqk, p["pos"], plan, inverse=True, out=dqk)
+    dqkv = dqkv.view(n, -1)
+    dx, dw1 = M.ma_rms_norm_backward(dqkv @ p["wqkv"], s1, inv1, p["w1"], ds2)
+    return (lp, ent), [M.EmbeddingGrad(dx, p["ids"], 8.0), dw1, M.LinearGrad(dqkv, c1), M.LinearGrad(ds2, M.ma_act_pack(a)),
+                       dw2, M.LinearGrad(dz, c2)]
+
+
+def _formed(src):
+    return [M.ma_embedding_grad(s.dout, s.tokens, VOCAB, scale=s.scale) if isinstance(s, M.EmbeddingGrad) else
+            M.ma_linear_grad(s.dy, s.x) if isinstance(s, M.LinearGrad) else s for s in src]
+
+
+def _plain_block(p):
+    """The same in torch autograd, float64 on the CPU."""
+    q = {k: t.double().cpu() if t.is_floating_point() else t.cpu() for k, t in p.items()}
+    for k in WEIGHTS:
+        q[k].requires_grad_()
+    n = q["ids"].numel()
+
+    def norm(x, w):
+        return x / torch.sqrt((x * x).mean(-1, keepdim=True) + 1e-6) * w
+
+    x = q["table"][q["ids"]] * 8.0
+    qkv = (norm(x, q["w1"]) @ q["wqkv"].t()).view(n, -1, DIM)
+    ang = torch.stack([q["pos"][a].double() * f for a, f in R.rotary_table(SECTIONS, 10000.0, "blocks", False)], 1)
+    c, s = torch.cos(ang)[:, None], torch.sin(ang)[:, None]
+    a, b = qkv[:, :HEADS + KV, :DIM // 2], qkv[:, :HEADS + KV, DIM // 2:]
+    qk = torch.cat([a * c - b * s, a * s + b * c], -1)
+    o, at = [], 0
+    for m in LENS:
+        r = slice(at, at + m)
+        at += m
+        z = torch.einsum("qhd,khd->hqk", qk[r, :HEADS], qk[r, HEADS:].repeat_interleave(2, 1)) / DIM ** 0.5
+        z = z.masked_fill(torch.ones(m, m, dtype=torch.bool).triu(1), -np.inf)
+        o.append(torch.einsum("hqk,khd->qhd", torch.softmax(z, -1), qkv[r, HEADS + KV:].repeat_interleave(2, 1)))
+    s2 = torch.cat(o).reshape(n, -1) @ q["wo"].t() + x
+    lp = torch.log_softmax(norm(s2, q["w2"]) @ q["head"].t(), -1)
+    ent = -(lp.exp() * lp).sum(-1)
+    got = lp[torch.arange(n), q["answer"]]
+    ((got * q["g"]).sum() + (ent * q["h"]).sum()).backward()
+    return got.detach().numpy(), ent.detach().numpy(), [q[k].grad.numpy() for k in WEIGHTS]
+
+
+def test_block_gradients():
+    """float32 throughout.  Sums of at most 300 terms in a chain of some eight operators, each result off by
+    at most its terms' 2^-24 and twice as much again where one is divided by a norm: 8 x 2 x 300 x 2^-24 = 2.9e-4
+    of a result's norm even if all errors were aligned.  The linear layers' weights see inputs held in 8 bits,
+    off by at most half a step: 1.8 % of a group of 32 normal values."""
+    p = _block_inputs(1)
+    cu, plan = _cu(_offsets(LENS)), M.Rotary(SECTIONS)
+    (lp, ent), src = _block(p, cu, plan)
+    wl, we, want = _plain_block(p)
+    assert np.abs(_f64(lp) - wl).max() < 3e-4 * np.abs(wl).max() and np.abs(_f64(ent) - we).max() < 3e-4 * np.abs(we).max()
+    for g, w, s, name in zip(_formed(src), want, src, WEIGHTS):
+        rel = np.linalg.norm(_f64(g) - w) / np.linalg.norm(w)
+        assert rel < (0.019 if isinstance(s, M.LinearGrad) else 3e-4), (name, rel)
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+def test_block_feeds_the_optimizer(kind):
+    """The step with gradients and their sources is the step with the formed gradients."""
+    p = _block_inputs(2, kind)
+    cu, plan = _cu(_offsets(LENS)), M.Rotary(SECTIONS)
+    outs = []
+    for form in (False, True):
+        params = [p[k].clone() for k in WEIGHTS]
+        opt = M.MuonAdamW(list(zip(LAYER_NAMES, params, [True] * 6)), lr=1e-3)
+        for _ in range(2):
+            src = [s.to(DT[kind]) if isinstance(s, torch.Tensor) else s for s in _block(p, cu, plan)[1]]
+            if form:
+                src = [g.to(DT[kind]) if isinstance(s, torch.Tensor) else
+                       M.ma_embedding_grad(s.dout, s.tokens, VOCAB, scale=s.scale, grad_dtype=DT[kind])
+                       if isinstance(s, M.EmbeddingGrad) else M.ma_linear_grad(s.dy, s.x, grad_dtype=DT[kind])
+                       for s, g in zip(src, src)]
+            opt.step(src)
+        outs.append(params)
+    for a, b, k in zip(*outs, WEIGHTS):
+        assert torch.equal(a, b), k
+        # (an AdamW step moves a weight by about lr = 1e-3: in bfloat16 less than half the 2^-7 or 2^-8
+        # between values near 1, so the norms' weights stay)
+        assert not torch.equal(a, p[k]) or (kind == "bf16" and k in ("w1", "w2")), k
+
+
+def _everything(p, cu, plan, big):
+    """The block, and calls whose work is cut into pieces and joined."""
+    (lp, ent), src = _block(p, cu, plan)
+    q, k, z, ids = big
+    o, lse = M.ma_attention_forward(q, k, k, causal=False)
+    got = M.ma_attention_backward(o, q, k, k, o, lse, causal=False)
+    return [lp, ent, *_formed(src), o, lse, *got, *M.ma_token_logprob_forward(z, ids, top=7)]
+
+
+def _big(seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda").to(torch.bfloat16)
+    return [r(40, 2, 128), r(3000, 1, 128), r(3, 90000), torch.tensor([5, 80000, 17], device="cuda")]
+
+
+def test_block_captured_and_replayed():
+    """Captured once and replayed on changed inputs, with eager work in between, equals the eager
+    results each time."""
+    p, big = _block_inputs(20), _big(20)
+    cu, plan = _cu(_offsets(LENS)), M.Rotary(SECTIONS)
+    _everything(p, cu, plan, big)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        _everything(p, cu, plan, big)
+    side.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        outs = _everything(p, cu, plan, big)
+    del plan                                     # (the graph holds its own frequencies)
+    plan = M.Rotary(SECTIONS)
+    for seed in (21, 22, 23, 24):
+        for k, v in _block_inputs(seed).items():
+            p[k].copy_(v)
+        for a, b in zip(big, _big(seed)):
+            a.copy_(b)
+        for o in outs:
+            o.fill_(float("nan") if o.is_floating_point() else -1)
+        g.replay()
+        torch.cuda.synchronize()
+        got = [o.clone() for o in outs]
+        for i, (a, b) in enumerate(zip(got, _everything(p, cu, plan, big))):
+            assert torch.equal(a, b), (seed, i)
+        torch.cuda.synchronize()
+
+
+def test_two_graphs_and_two_streams():
+    """Two graphs of the same operators on different data replayed in turn, then at once, and two eager
+    streams at once."""
+    ps, bigs = [_block_inputs(50 + k) for k in range(2)], [_big(50 + k) for k in range(2)]
+    cu, plan = _cu(_offsets(LENS)), M.Rotary(SECTIONS)
+    want = [_everything(p, cu, plan, b) for p, b in zip(ps, bigs)]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for p, b in zip(ps, bigs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(_everything(p, cu, plan, b))
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in ps]
+    for r in range(4):
+        for o in outs:
+            for t in o:
+                t.fill_(float("nan") if t.is_floating_point() else -1)
+        torch.cuda.synchronize()
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+            if r < 2:
+                st.synchronize()
+        for st in streams:
+            st.synchronize()
+        for o, w in zip(outs, want):
+            assert all(torch.equal(a, b) for a, b in zip(o, w)), r
+    for _ in range(3):
+        got = []
+        for p, b, st in zip(ps, bigs, streams):
+            with torch.cuda.stream(st):
+                got.append(_everything(p, cu, plan, b))
+        for st in streams:
+            st.synchronize()
+        for o, w in zip(got, want):
+            assert all(torch.equal(a, b) for a, b in zip(o, w))
+
+
+def test_streams_are_taken_as_arguments():
+    """Each call on another stream than the current one, as an object and as a raw handle."""
+    rng = np.random.default_rng(3)
+    x, w, r = _dev(_stream(rng, 30, 96)), _dev(np.ones(96)), _dev(_stream(rng, 30, 96))
+    q, k, v, do = _inputs(rng, 60, 500, 2, 1, 64, "bf16")
+    ids, plan, pos = torch.arange(30, device="cuda"), M.Rotary(32), torch.arange(60, device="cuda")
+    z = _dev(_logits(rng, 30, 20000))
+
+    def all_calls(**kw):
+        y, s, inv, c = M.ma_rms_norm_forward(x, w, r, y_ckpt=True, **kw)
+        ds, dw = M.ma_rms_norm_backward(y, s, inv, w, r, **kw)
+        lp, ent, lse, top, best = M.ma_token_logprob_forward(z, ids, top=3, **kw)
+        dz = M.ma_token_logprob_backward(z, ids, lse, lp, entropy=ent, dentropy=ent, **kw)
+        t = M.ma_rotary(q, pos, plan, **kw)
+        o, l = M.ma_attention_forward(t, k, v, causal=False, **kw)
+        return [y, s, inv, c.codes, ds, dw, lp, ent, lse, top, best, dz, t, o, l,
+                *M.ma_attention_backward(do, t, k, v, o, l, causal=False, **kw)]
+
+    want = all_calls()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream, 0):
+        got = all_calls(stream=stream)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_calls(seed):
+    """Every operator at random sizes, types and strides (each a view of a wider array filled with NaN)."""
+    rng = np.random.default_rng(2000 + seed)
+
+    def size(most):
+        return int(np.exp(rng.random() * np.log(most)))
+
+    def kind():
+        return ("fp32", "bf16")[rng.integers(2)]
+
+    def view(x, k):
+        v, wide = _strided(x, int(rng.integers(0, 20)), k)
+        wide[:, x.shape[1]:] = float("nan")
+        return v
+
+    rows, cols, t, wk = size(3000), size(3000), kind(), kind()
+    x, r, w = view(_stream(rng, rows, cols), t), view(_stream(rng, rows, cols), t), _dev(rng.standard_normal(cols), wk)
+    y, s, inv, c = M.ma_rms_norm_forward(x, w, r, eps=1e-5, weight_offset=0.5, y_ckpt=True)
+    yy, ss, ii, dy, ds, di = R.rms_norm(_f64(x), _f64(w), _f64(r), 1e-5, 0.5)
+    _close(y, yy, R.rounded(yy, dy, t), "y")
+    _close(inv, ii, di, "inv")
+    assert torch.equal(M.ma_act_pack(y).codes, c.codes)
+    g = view(rng.standard_normal((rows, cols)), t)
+    a, b = M.ma_rms_norm_backward(g, s, inv, w, r, weight_offset=0.5, grad_dtype=DT[wk])
+    want, dwant, tol, wtol = R.rms_norm_backward(_f64(g), _f64(s), _f64(inv), _f64(w), 0.5, _f64(r))
+    _close(a, want, R.rounded(want, tol, t), "ds")
+    _close(b, dwant, R.rounded(dwant, wtol, wk), "dw")
+
+    rows, vocab, t = size(300), size(40000), kind()
+    z = view(_logits(rng, rows, vocab), t)
+    ids = rng.integers(0, vocab, rows)
+    _check_logprob(z, ids, 0.8, min(vocab, int(rng.integers(0, 30))))
+    lse = M.ma_token_logprob_forward(z, torch.from_numpy(ids).cuda(), scale=0.8)[2]
+    g = _dev(rng.standard_normal(rows))
+    want, tol = R.logprob_backward(_f64(z), ids, float(np.float32(0.8)), _f64(lse), _f64(g))
+    _close(M.ma_token_logprob_backward(z, torch.from_numpy(ids).cuda(), lse, g, scale=0.8), want, R.rounded(want, tol, t))
+
+    tokens, heads, dim, t = size(2000), int(rng.integers(1, 9)), int(rng.integers(2, 257)), kind()
+    axes = int(rng.integers(1, 5))
+    cut = np.sort(rng.integers(0, dim // 2, axes - 1)) if axes > 1 else np.zeros(0, int)
+    sections = [int(n) for n in np.diff(np.concatenate([[0], cut, [max(1, int(rng.integers(1, dim // 2 + 1)))]]))]
+    if min(sections) >= 0 and sum(sections) > 0:
+        how = (("half", "pairs")[rng.integers(2)], ("blocks", "cycled")[rng.integers(2)], bool(rng.integers(2)))
+        x = view(rng.standard_normal((tokens, heads * dim)), t).unflatten(1, (heads, dim))
+        pos = rng.integers(0, 5000, (axes, tokens))
+        got = M.ma_rotary(x, torch.from_numpy(pos).cuda(), M.Rotary(sections, layout=how[0], order=how[1], restart=how[2]))
+        want, tol = R.rotary(_f64(x), pos, R.rotary_table(sections, 10000.0, how[1], how[2]), how[0])
+        _close(got, want, R.rounded(want, tol, t))
+
+    kv, t = int(rng.integers(1, 4)), kind()
+    heads, dim, n = kv * int(rng.integers(1, 4)), int(rng.integers(1, 257)), int(rng.integers(1, 6))
+    cq, ck = _offsets(rng.integers(0, size(400) + 1, n)), _offsets(rng.integers(0, size(400) + 1, n))
+    arr = [view(rng.standard_normal((max(1, int(m)), h * dim)), t).unflatten(1, (h, dim))
+           for m, h in ((cq[-1], heads), (ck[-1], kv), (ck[-1], kv), (cq[-1], heads))]
+    _check_attention(*arr, cq, ck, bool(rng.integers(2)), None, t)
+
+
+# ----------------------------------------------------- offsets past 32 bits --
+
+def test_long_offsets():
+    """Arrays of more than 2^31 elements (4.4 GB): their far ends."""
+    rows, cols = 540_000, 4096
+    x = torch.zeros((rows, cols), dtype=torch.bfloat16, device="cuda")
+    x[-1] = 2.0
+    w = torch.full((cols,), 3.0, device="cuda")
+    y, _, inv, c = M.ma_rms_norm_forward(x, w, eps=1e-6, y_ckpt=True)
+    assert torch.all(y[-1] == 3.0) and float(y[:-1].abs().max()) == 0.0 and abs(float(inv[-1]) - 0.5) < 1e-6
+    assert torch.all(M.ma_act_unpack(M.ActCheckpoint(c.codes[-1:], c.exps[-1:], cols)) == 3.0)
+    del y, c
+    ds, dw = M.ma_rms_norm_backward(x, x, inv, w)
+    assert float(ds[-1].abs().max()) < 1e-2 and torch.all((dw - 2.0).abs() < 1e-5)
+    del ds
+    t = M.ma_rotary(x.view(rows, 32, 128), torch.arange(rows, device="cuda"), M.Rotary(64))
+    want = M.ma_rotary(x[-1:].view(1, 32, 128), torch.tensor([rows - 1], device="cuda"), M.Rotary(64))
+    assert torch.equal(t[-1:], want) and float(t[:-1].abs().max()) == 0.0
+    del t
+    ids = torch.full((rows,), 7, device="cuda")
+    lp, _, lse, top, _ = M.ma_token_logprob_forward(x, ids, top=2)
+    assert torch.all((lp + np.log(cols)).abs() < 1e-5) and top[-1].tolist() == [0, 1]
+    x[-1, 9] = 12.0
+    lp2 = M.ma_token_logprob_forward(x, torch.full((rows,), 9, device="cuda"))[0]
+    assert float(lp2[-1]) > -1 and torch.equal(lp2[:-1], lp[:-1])
+    d = M.ma_token_logprob_backward(x, ids, lse, torch.ones(rows, device="cuda"), out=x)
+    assert abs(float(d[-1, 7]) - (1 - 1 / cols)) < 1e-2 and abs(float(d[0, 7]) - (1 - 1 / cols)) < 1e-2
+    del x, d
+    torch.cuda.empty_cache()
+    # attention over rows that lie far apart in a cache of 2^32 elements
+    n = 1 << 13
+    cache = torch.empty((n, 1 << 19), dtype=torch.bfloat16, device="cuda")
+    k, v = cache[:, :128].unflatten(1, (1, 128)), cache[:, -128:].unflatten(1, (1, 128))
+    k.normal_(), v.normal_()
+    q = torch.randn(70, 2, 128, device="cuda").to(torch.bfloat16)
+    o, lse = M.ma_attention_forward(q, k, v)
+    o2, lse2 = M.ma_attention_forward(q, k.contiguous(), v.contiguous())
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    g = M.ma_attention_backward(o, q, k, v, o, lse, dk=torch.empty_like(k, memory_format=torch.contiguous_format))
+    for a, b in zip(g, M.ma_attention_backward(o, q, k.contiguous(), v.contiguous(), o, lse)):
+        assert torch.equal(a, b)
+    del cache, k, v
+    torch.cuda.empty_cache()
