@@ -10,9 +10,9 @@
 // The highest `top` come from the same pass.  Every thread knows its largest value's
 // place; the top-th largest of those 512 keys (value, then lowest id) is a bound
 // that at least `top` keys of the row reach, all of them in the `top` threads whose own
-// largest does.  Only those threads' units are read again (a few percent of the row), the keys
-// that reach the bound, hardly more than `top`, are listed in LDS and ranked by
-// counting.  Keys are distinct, so the result does not depend on the order of the list.
+// largest does.  Those threads' units that hold a value so high (each knows its second largest too, so
+// hardly more than one each) are read again, the keys that reach the bound are listed in
+// LDS and ranked by counting.  Keys are distinct, so the result does not depend on the order of the list.
 //
 // Backward: a stream with the row's numbers in registers.
 //
@@ -73,41 +73,82 @@ __device__ __forceinline__ float unordered(uint32_t u) {
 // The larger key is the higher value, of equal ones the lower id.
 __device__ __forceinline__ uint64_t key_of(float z, uint32_t id) { return (uint64_t)ordered(z) << 32 | (uint32_t)~id; }
 
-// A running softmax: reference m (the largest value, at least -FLT_MAX), s and t in terms
-// of 2^((z - m) k).
+// (a value this far down is a mask: products with a scale may leave float32)
+constexpr float kMask = -1e30f;
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float v;         // (the builtin maximum would first quieten each input)
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(v) : "v"(a), "v"(b), "v"(c));
+    return v;
+}
+
+// A running softmax: m the largest value (at least -FLT_MAX), s and t the sums of 2^u and u 2^u.
+// u = z k - mk is one multiply-add from a reference that is m k rounded; what the rounding
+// left out is made up for once, in ln s.  Where m is a mask u is (z - m) k instead.
 struct Soft {
-    float m = -__FLT_MAX__, s = 0.f, t = 0.f;
+    float m, mk, s, t;
+    __device__ __forceinline__ void begin(float k) {
+        m = -__FLT_MAX__;
+        mk = m * k;
+        s = t = 0.f;
+    }
+    // reference `to` less this one, in units of 2^: at most 0
+    __device__ __forceinline__ float below(float to, float k) const {
+        return fmaxf(m < kMask ? (m - to) * k : mk - to * k, kFar);
+    }
     // another reference, not below m
     __device__ __forceinline__ void raise(float to, float k) {
-        const float d = fmaxf((m - to) * k, kFar), c = __builtin_amdgcn_exp2f(d);
+        const float d = below(to, k), c = __builtin_amdgcn_exp2f(d);
         t = fmaf(s, d, t) * c;
         s *= c;
         m = to;
+        mk = to * k;
     }
-    __device__ __forceinline__ void add(float z, float k) {
-        const float u = (z - m) * k, e = __builtin_amdgcn_exp2f(u);
+    __device__ __forceinline__ void add(float u) {
+        const float e = __builtin_amdgcn_exp2f(u);
         s += e;
         t = fmaf(e, fmaxf(u, kFar), t);          // (a NaN is in e)
     }
-    __device__ __forceinline__ void join(float m2, float s2, float t2, float k) {
-        const float to = fmaxf(m, m2);
+    __device__ __forceinline__ void add8(const float* z, float k) {
+        if (__builtin_expect(__any(m < kMask), 0)) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) add(m < kMask ? (z[e] - m) * k : fmaf(z[e], k, -mk));
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) add(fmaf(z[e], k, -mk));
+        }
+    }
+    // of N neighbouring lanes, in each of them
+    template <int N>
+    __device__ __forceinline__ void join(float k) {
+        float to = m;
+#pragma unroll
+        for (int x = 1; x < N; x <<= 1) to = fmaxf(to, __shfl_xor(to, x, 64));
         raise(to, k);
-        const float d = fmaxf((m2 - to) * k, kFar), c = __builtin_amdgcn_exp2f(d);
-        t += fmaf(s2, d, t2) * c;
-        s += s2 * c;
+#pragma unroll
+        for (int x = 1; x < N; x <<= 1) {
+            s += __shfl_xor(s, x, 64);
+            t += __shfl_xor(t, x, 64);
+        }
+    }
+    // ln of the sum of e^(scale (z - m))
+    __device__ __forceinline__ float log_sum(float k) const {
+        return logf(s) - (m < kMask ? 0.f : kLn2 * fmaf(m, k, -mk));
     }
 };
 
+__device__ __forceinline__ Soft soft_of(const float* x, float k) { return {x[0], x[0] * k, x[1], x[2]}; }
+
 // One row's numbers from its joined sums.
 __device__ __forceinline__ void write_row(const LogprobArgs& a, int64_t row, const Soft& f, float zt, bool in) {
-    const float ls = logf(f.s);
+    const float ls = f.log_sum(a.scale * kLog2e);
     const bool none = f.s == 0.f;                // nothing but -infinity
     a.lse[row] = none ? -__builtin_inff() : fmaf(f.m, a.scale, ls);
     if (a.logprob) {
         const float lp = fmaf(zt - f.m, a.scale, -ls);
         a.logprob[row] = !in ? 0.f : none ? -__builtin_inff() : lp;
     }
-    if (a.entropy) a.entropy[row] = none ? 0.f : fmaf(-kLn2, f.t / f.s, ls);
+    if (a.entropy) a.entropy[row] = none ? 0.f : fmaf(-kLn2, f.t / f.s, logf(f.s));
 }
 
 __device__ __forceinline__ int64_t token_of(const LogprobArgs& a, int64_t row) {
@@ -129,7 +170,7 @@ __device__ __forceinline__ void write_top(const LogprobArgs& a, int64_t row, int
     else static_cast<int32_t*>(a.top_ids)[at] = (int32_t)id;
     const uint32_t u = (uint32_t)(key >> 32);
     const float z = u ? unordered(u) : __builtin_nanf("");
-    a.top_logprobs[at] = f.s == 0.f ? -__builtin_inff() : fmaf(z - f.m, a.scale, -logf(f.s));
+    a.top_logprobs[at] = f.s == 0.f ? -__builtin_inff() : fmaf(z - f.m, a.scale, -f.log_sum(a.scale * kLog2e));
 }
 
 // The largest of a workgroup's keys, in every thread.
@@ -152,20 +193,26 @@ struct TopLds {
     uint64_t best[NT];           // every thread's largest key
     uint64_t list[kList<NT>];
     uint64_t slot[NT / 64];
+    uint32_t second[NT];         // the value of its largest in another round than that one's,
+    int round[NT];               // which this is
     int chosen[64];              // the threads whose largest reaches the bound
     uint64_t bound;
     int n_chosen, n;
+    bool more;                   // whether one of them has another value that high
 };
 
 // Writes the `top` largest keys of the piece through put(rank, key).  `best`: this thread's
-// largest key, 0 for none.  The piece has at least `top` elements.
+// largest key, 0 for none, from round `at`; `second`: the largest value of its other rounds.  The
+// piece has at least `top` elements.
 template <int NT, typename T, typename F>
-__device__ __forceinline__ void select_top(const T* z, const Piece<NT>& p, int top, uint64_t best, TopLds<NT>& l,
-                                           F put) {
+__device__ __forceinline__ void select_top(const T* z, const Piece<NT>& p, int top, uint64_t best, int at,
+                                           float second, TopLds<NT>& l, F put) {
     constexpr int kThreads = NT, kWaves = NT / 64, kList = ma::kList<NT>;
     const int tid = threadIdx.x, size = p.last - p.first;
     if (tid == 0) l.n = l.n_chosen = 0;
     l.best[tid] = best;
+    l.round[tid] = at;
+    l.second[tid] = ordered(second);
     __syncthreads();
     // (with fewer units than `top` not enough threads have a key: every key is listed)
     const bool all = min(p.full, kThreads) < top;
@@ -181,6 +228,7 @@ __device__ __forceinline__ void select_top(const T* z, const Piece<NT>& p, int t
 #pragma unroll
             for (int w = 0; w < kWaves; ++w) k[w] = l.best[w * 64 + tid];
             uint64_t b = 0;
+            bool more = false;
             for (int bit = 63; bit >= 0; --bit) {
                 const uint64_t at = b | 1ull << bit;
                 int n = 0;
@@ -200,16 +248,17 @@ __device__ __forceinline__ void select_top(const T* z, const Piece<NT>& p, int t
                 }
                 at = __shfl(at, 0, 64) + __popcll(who & ((1ull << tid) - 1));
                 if (in && at < 64) l.chosen[at] = w * 64 + tid;
+                more |= in && l.second[w * 64 + tid] >= (uint32_t)(b >> 32);
             }
+            more = __any(more);
+            if (tid == 0) l.more = more;
             if (tid == 0) l.bound = b;
         }
         __syncthreads();
         bound = l.bound;
-        const int per = p.rounds + 1, units = l.n_chosen * per;
-        for (int i = tid; i < units; i += kThreads) {
-            const int who = l.chosen[i / per], round = i % per;
+        auto list = [&](int who, int round) {
             const int cnt = p.count(who, round), s = p.start(who, round);
-            if (cnt <= 0) continue;
+            if (cnt <= 0) return;
             float v[8];
             load_unit<T, false, false>(z + s, cnt, v);
 #pragma unroll
@@ -220,6 +269,13 @@ __device__ __forceinline__ void select_top(const T* z, const Piece<NT>& p, int t
                     if (at < kList) l.list[at] = k;
                 }
             }
+        };
+        if (tid < l.n_chosen) list(l.chosen[tid], l.round[l.chosen[tid]]);
+        for (int c = 0; l.more && c < l.n_chosen; ++c) {
+            const int who = l.chosen[c];
+            if (l.second[who] < (uint32_t)(bound >> 32)) continue;
+            for (int round = tid; round <= p.rounds; round += kThreads)
+                if (round != l.round[who]) list(who, round);
         }
         __syncthreads();
     }
@@ -228,6 +284,7 @@ __device__ __forceinline__ void select_top(const T* z, const Piece<NT>& p, int t
         for (int i = tid; i < n; i += kThreads) {
             const uint64_t k = l.list[i];
             int rank = 0;
+#pragma unroll 8
             for (int j = 0; j < n; ++j) rank += l.list[j] > k;
             if (rank < top) put(rank, k);
         }
@@ -269,20 +326,22 @@ __global__ __launch_bounds__(NT) void k_logprob_forward(LogprobArgs a) {
         const int from = (int)min<int64_t>((int64_t)blockIdx.y * a.piece, a.vocab);
         const Piece<NT> p(reinterpret_cast<const char*>(z), sizeof(T), from, (int)min<int64_t>(from + a.piece, a.vocab));
         Soft f;
-        float top = -__builtin_inff();           // the largest value, and the round that held it
+        f.begin(k);
+        // the largest value, the round that held it, and the largest of the other rounds
+        float top = -__builtin_inff(), second = -__builtin_inff();
         // (the elements before the whole units come first, so of equal values a thread's first
         // in its rounds is the lowest)
         const bool head = tid == 0 && p.base > p.first;
         int at = head ? p.rounds : 0;
         auto take = [&](const float* v, int round) {
-            float mu = fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), fmaxf(fmaxf(v[4], v[5]), fmaxf(v[6], v[7])));
+            const float mu = max3(max3(v[0], v[1], v[2]), max3(v[3], v[4], v[5]), max3(v[6], v[7], v[7]));
+            second = __builtin_amdgcn_fmed3f(mu, top, second);
             if (mu > top) {
                 top = mu;
                 at = round;
                 f.raise(fmaxf(mu, f.m), k);
             }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f.add(v[e], k);
+            f.add8(v, k);
         };
         auto part_of = [&](int round) {
             const int cnt = p.count(tid, round);
@@ -294,24 +353,40 @@ __global__ __launch_bounds__(NT) void k_logprob_forward(LogprobArgs a) {
             take(v, round);
         };
         if (head) part_of(p.rounds);
-        const T* q = z + p.base + 8 * tid;
-        int r = 0;
-        constexpr int kAhead = 4 / (sizeof(T) / 2);
-        for (; (r + kAhead) * kThreads <= p.full; r += kAhead) {
-            u32x4 w[kAhead][sizeof(T) / 2];
+        // Whole units in batches, the next one's loads under way while one is worked on.  In the last
+        // round threads without a unit read the last and drop it: no branch by lane around a load.
+        constexpr int kAhead = 6 / (sizeof(T) / 2), kWords = sizeof(T) / 2;
+        u32x4 w[kAhead][kWords];
+        auto load = [&](int round) {
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+                if (round + i < p.rounds) {
+                    const T* q = z + p.base + 8 * (int64_t)min((round + i) * kThreads + tid, p.full - 1);
+#pragma unroll
+                    for (int h = 0; h < kWords; ++h) w[i][h] = reinterpret_cast<const u32x4*>(q)[h];
+                }
+        };
+        if (p.rounds > 0) load(0);
+        for (int r = 0; r < p.rounds; r += kAhead) {
+            u32x4 now[kAhead][kWords];
 #pragma unroll
             for (int i = 0; i < kAhead; ++i)
 #pragma unroll
-                for (int h = 0; h < (int)sizeof(T) / 2; ++h)
-                    w[i][h] = reinterpret_cast<const u32x4*>(q + (int64_t)(r + i) * kThreads * 8)[h];
+                for (int h = 0; h < kWords; ++h) now[i][h] = w[i][h];
+            load(r + kAhead);
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                float v[8];
-                widen<T>(w[i], v);
-                take(v, r + i);
-            }
+            for (int i = 0; i < kAhead; ++i)
+                if (r + i < p.rounds) {
+                    float v[8];
+                    widen<T>(now[i], v);
+                    if (r + i == p.rounds - 1) {
+                        const bool in = (r + i) * kThreads + tid < p.full;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[e] = in ? v[e] : -__builtin_inff();
+                    }
+                    take(v, r + i);
+                }
         }
-        for (; r < p.rounds; ++r) part_of(r);
         if (tid == 1) part_of(p.rounds);
         uint64_t best = 0;
         if constexpr (TOP) {
@@ -325,17 +400,17 @@ __global__ __launch_bounds__(NT) void k_logprob_forward(LogprobArgs a) {
                     if (e < cnt) best = max(best, key_of(v[e], s + e));
             }
         }
-#pragma unroll
-        for (int m = 1; m < 64; m <<= 1)
-            f.join(__shfl_xor(f.m, m, 64), __shfl_xor(f.s, m, 64), __shfl_xor(f.t, m, 64), k);
-        if ((tid & 63) == 0) {
-            part[tid >> 6][0] = f.m;
-            part[tid >> 6][1] = f.s;
-            part[tid >> 6][2] = f.t;
+        f.join<64>(k);
+        if constexpr (kWaves > 1) {
+            if ((tid & 63) == 0) {
+                part[tid >> 6][0] = f.m;
+                part[tid >> 6][1] = f.s;
+                part[tid >> 6][2] = f.t;
+            }
+            __syncthreads();
+            f = soft_of(part[tid & (kWaves - 1)], k);
+            f.join<kWaves>(k);
         }
-        __syncthreads();
-        f = Soft{part[0][0], part[0][1], part[0][2]};
-        for (int w = 1; w < kWaves; ++w) f.join(part[w][0], part[w][1], part[w][2], k);
         const int64_t slot = row * gridDim.y + blockIdx.y;
         if (tid == 0) {
             if (gridDim.y == 1) {
@@ -351,7 +426,7 @@ __global__ __launch_bounds__(NT) void k_logprob_forward(LogprobArgs a) {
             const int n = min(a.top, p.last - p.first);
             uint64_t* keys = a.keys + slot * a.top;
             if (gridDim.y > 1 && tid >= n && tid < a.top) keys[tid] = 0;      // (a last piece of fewer elements)
-            select_top<NT>(z, p, n, best, lds, [&](int rank, uint64_t key) {
+            select_top<NT>(z, p, n, best, at, second, lds, [&](int rank, uint64_t key) {
                 if (gridDim.y == 1) write_top(a, row, rank, key, f);
                 else keys[rank] = key;
             });
@@ -368,8 +443,11 @@ __global__ __launch_bounds__(512) void k_logprob_join(LogprobArgs a, int pieces)
     const float k = a.scale * kLog2e;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const float* s = a.sums + row * pieces * 4;
-        Soft f{s[0], s[1], s[2]};
-        for (int i = 1; i < pieces; ++i) f.join(s[4 * i], s[4 * i + 1], s[4 * i + 2], k);
+        // (at most 64 pieces, one a lane)
+        const int lane = threadIdx.x & 63;
+        const float none[3] = {-__FLT_MAX__, 0.f, 0.f};
+        Soft f = soft_of(lane < pieces ? s + 4 * lane : none, k);
+        f.join<64>(k);
         if (threadIdx.x == 0)
             write_target(a, static_cast<const T*>(a.logits) + row * a.stride, row, f);
         if (a.top == 0) continue;
@@ -385,6 +463,7 @@ __global__ __launch_bounds__(512) void k_logprob_join(LogprobArgs a, int pieces)
                 __syncthreads();
                 keys[threadIdx.x] = j0 + (int)threadIdx.x < n ? g[j0 + threadIdx.x] : 0;
                 __syncthreads();
+#pragma unroll 8
                 for (int j = 0; j < min(kThreads, n - j0); ++j) rank += keys[j] > mine;
             }
             if (mine && rank < a.top) write_top(a, row, rank, mine, f);
@@ -406,46 +485,68 @@ __global__ __launch_bounds__(NT) void k_logprob_backward(LogprobArgs a) {
         const float gs = in ? a.dlogprob[row] * a.scale : 0.f;
         const float hs = a.dentropy ? a.dentropy[row] * a.scale : 0.f;
         const float c0 = a.dentropy ? fmaf(hs, a.ent[row], gs) : gs;
+        // -p (g + h (log p + H)), and g at the token; log p is z scale - lse.  A row of nothing has
+        // gradient 0, one whose lse is NaN is NaN throughout.
         const bool none = lse == -__builtin_inff();
-        // -p (g + h (log p + H)), and g at the token: log p is z scale - lse
-        auto grad = [&](float zv, int id) {
-            float lp = fmaf(zv, a.scale, -lse);
-            lp = lp < kFar ? kFar : lp;
-            const float q = __builtin_amdgcn_exp2f(lp * kLog2e);
-            float o = -q * fmaf(hs, lp, c0);
-            o += id == tok ? gs : 0.f;
-            return none ? 0.f : o;
-        };
-        for (int r = 0; r <= p.rounds; ++r) {
-            const int cnt = p.count(tid, r), s = p.start(tid, r);
-            if (cnt <= 0) continue;
-            float v[8];
-            load_unit<T, false>(z + s, cnt, v);
+        const float c = none ? 0.f : lse != lse ? lse : c0, hc = none ? 0.f : hs, gc = none ? 0.f : gs;
+        auto unit = [&](const float* v, int at, float* o) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = grad(v[e], s + e);
-            store_unit<TG, false>(d + s, cnt, v);
+            for (int e = 0; e < 8; ++e) {
+                const float lp = fmaxf(fmaf(v[e], a.scale, -lse), kFar);
+                o[e] = -__builtin_amdgcn_exp2f(lp * kLog2e) * fmaf(hc, lp, c);
+            }
+            const int64_t t = tok - at;
+            if (in && t >= 0 && t < 8)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] += e == (int)t ? gc : 0.f;
+        };
+        auto part_of = [&](int round) {
+            const int cnt = p.count(tid, round), at = p.start(tid, round);
+            if (cnt <= 0) return;
+            float v[8], o[8];
+            load_unit<T, false>(z + at, cnt, v);
+            unit(v, at, o);
+            store_unit<TG, false>(d + at, cnt, o);
+        };
+        int r = 0;
+        constexpr int kAhead = 2;
+        for (; (r + kAhead) * NT <= p.full; r += kAhead) {
+            float v[kAhead][8], o[8];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) load_unit<T, true>(z + p.start(tid, r + i), 8, v[i]);
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const int at = p.start(tid, r + i);
+                unit(v[i], at, o);
+                store_unit<TG, false>(d + at, 8, o);
+            }
         }
+        for (; r <= p.rounds; ++r) part_of(r);
     }
 }
 
 }  // namespace
 
-// A workgroup for every row, or pieces of rows until the GPU has about two for each CU;
-// a piece has at least 8192 elements, two rounds of the largest workgroup.
+// A workgroup for every row, or pieces of rows until the GPU has about four for each CU; a
+// piece has at least 8192 elements (one row of 151000: 18 pieces 24 us, 36 of them 39, most of it joining).
 int64_t logprob_pieces(int64_t rows, int64_t vocab) {
     if (rows == 0) return 1;
-    const int64_t want = std::max<int64_t>(1, kCus * 2 / rows);
+    const int64_t want = std::max<int64_t>(1, kCus * 4 / rows);
     return std::max<int64_t>(1, std::min<int64_t>({want, vocab / 8192, 64}));
 }
 
 static unsigned row_grid(int64_t rows) { return (unsigned)std::min<int64_t>(rows, int64_t(1) << 20); }
 
-// Calls f(threads of a workgroup): about four rounds of a row or more each.
+// Calls f(threads of a workgroup): the more elements the more, 256 where there is less than one
+// workgroup a CU.  What a row costs beside its elements (joining sums, telling the top ids)
+// grows with its waves, and goes on beside other rows' loads in several small workgroups a CU:
+// 30000 x 8000 bf16 237 us with 256 threads, 151 with 128, 100 with 64; 4096 x 151000 285 with
+// 512 (and 301 without loads ahead), 236 with 256, 271 with 128.
 template <typename F>
-static void by_piece(int64_t piece, F f) {
-    if (piece <= 4096) f(std::integral_constant<int, 64>{});
-    else if (piece <= 16384) f(std::integral_constant<int, 256>{});
-    else f(std::integral_constant<int, 512>{});
+static void by_piece(int64_t piece, int64_t blocks, F f) {
+    if (blocks < kCus || piece > 32768) f(std::integral_constant<int, 256>{});
+    else if (piece > 16384) f(std::integral_constant<int, 128>{});
+    else f(std::integral_constant<int, 64>{});
 }
 
 int launch_logprob_forward(const LogprobArgs& a, void* stream) {
@@ -454,7 +555,7 @@ int launch_logprob_forward(const LogprobArgs& a, void* stream) {
     const dim3 grid(row_grid(a.rows), (unsigned)pieces);
     auto go = [&](auto t) {
         using T = decltype(t);
-        by_piece(a.piece, [&](auto nt) {
+        by_piece(a.piece, a.rows * pieces, [&](auto nt) {
             constexpr int NT = decltype(nt)::value;
             if (a.top > 0)
                 hipLaunchKernelGGL((k_logprob_forward<T, true, NT>), grid, dim3(NT), 0, (hipStream_t)stream, a);
@@ -474,7 +575,13 @@ int launch_logprob_backward(const LogprobArgs& a, void* stream) {
     if (a.rows == 0) return (int)hipSuccess;
     const dim3 grid(row_grid(a.rows), (unsigned)ceil_div(a.vocab, a.piece));
     auto go = [&](auto t, auto g) {
-        by_piece(a.piece, [&](auto nt) {
+        // (4096 x 151000 bf16: 536 us with 512 threads, 499 with 1024)
+        if (a.piece > 32768) {
+            hipLaunchKernelGGL((k_logprob_backward<decltype(t), decltype(g), 1024>), grid, dim3(1024), 0,
+                               (hipStream_t)stream, a);
+            return;
+        }
+        by_piece(a.piece, a.rows * grid.y, [&](auto nt) {
             constexpr int NT = decltype(nt)::value;
             hipLaunchKernelGGL((k_logprob_backward<decltype(t), decltype(g), NT>), grid, dim3(NT), 0,
                                (hipStream_t)stream, a);
