@@ -70,12 +70,12 @@ __global__ __launch_bounds__(64 * WAVES * kHalves<DP>, (kPer<T, DP>)) void k_att
             copy_v(lds[at ^ 1][1], vx, (t + 1) * KV);
         }
         f32x16 s[KV / 32];
+        constexpr int ND = DW / 16, NB = DW / 32;
 #pragma unroll
-        for (int n = 0; n < KV / 32; ++n) {
-            s[n] = zero16();
-#pragma unroll
-            for (int d = 0; d < DW / 16; ++d) s[n] = mma(KT::rows(kt, 32 * n, half * (DW / 16) + d), qf[d], s[n]);
-        }
+        for (int n = 0; n < KV / 32; ++n) s[n] = zero16();
+        read_ahead<KV / 32 * ND, kAhead<T>>(
+            [&](int i) { return KT::rows(kt, 32 * (i / ND), half * ND + i % ND); },
+            [&](int i, const Frag<T>& f) { s[i / ND] = mma(f, qf[i % ND], s[i / ND]); });
         if constexpr (HALVES == 2) {         // (the sums over either half of the features)
             static_assert(KV == 32, "one exchange a tile");
             s[0] += exchange(s[0]);
@@ -115,12 +115,12 @@ __global__ __launch_bounds__(64 * WAVES * kHalves<DP>, (kPer<T, DP>)) void k_att
                 sum[i & 3] += s[n][i];
             }
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        Frag<T> p[KV / 16];
 #pragma unroll
-        for (int n = 0; n < KV / 16; ++n) {
-            const Frag<T> p = frag_of<T>(s[n / 2], n % 2);
-#pragma unroll
-            for (int b = 0; b < DW / 32; ++b) o[b] = mma(KT::cols(vt, 16 * n, half * DW + 32 * b), p, o[b]);
-        }
+        for (int n = 0; n < KV / 16; ++n) p[n] = frag_of<T>(s[n / 2], n % 2);
+        read_ahead<KV / 16 * NB, kAhead<T>>(
+            [&](int i) { return KT::cols(vt, 16 * (i / NB), half * DW + 32 * (i % NB)); },
+            [&](int i, const Frag<T>& f) { o[i % NB] = mma(f, p[i / NB], o[i % NB]); });
     };
     const int whole = min(max(seen(a, j, j.row0), 0) / KV, sh.last);
     int t = sh.first;

@@ -19,6 +19,10 @@ __global__ __launch_bounds__(64 * WAVES * kHalves<DP>, (kPer<T, DP>)) void k_att
     constexpr int BLOCK = 32 * WAVES, QT = 32, RING = 2, HALVES = kHalves<DP>, DW = DP / HALVES, ALL = WAVES * HALVES;
     using QTile = Tile<T, DP, QT, 64 * ALL>;
     using VTile = Tile<T, DP, BLOCK, 64 * ALL>;
+    // with dk and dv of 128 columns in registers there is room for two operands, not four
+    // (20011 tokens, 16 / 4 heads of 128: 1061 us a backward against 1145 with spills and 1135
+    // without reading ahead; of 256: 1110 against 1437 and 1236; of 64, four: 628 against 649)
+    constexpr int AHEAD = DP >= 128 ? 2 : kAhead<T>;
     constexpr bool STAGE = kStage<T, DP>;
     __shared__ __attribute__((aligned(1024))) char lds[RING][2][QTile::kBytes];
     __shared__ __attribute__((aligned(1024))) char vlds[STAGE ? VTile::kBytes : 16];
@@ -76,16 +80,29 @@ __global__ __launch_bounds__(64 * WAVES * kHalves<DP>, (kPer<T, DP>)) void k_att
         const float* sd = stat[slot][wave];
         slot ^= 1;
         f32x16 s = zero16(), p = zero16();
-        const char* mine = half == 0 ? qt : dt;
-#pragma unroll
-        for (int d = 0; d < DP / 16; ++d) s = mma(QTile::rows(mine, 0, d), kf[d], s);
+        constexpr int ND = DP / 16;
         if constexpr (HALVES == 1) {
-#pragma unroll
-            for (int d = 0; d < DP / 16; ++d) {
-                if constexpr (STAGE) p = mma(QTile::rows(dt, 0, d), VTile::rows(vlds, 32 * wave, d), p);
-                else p = mma(QTile::rows(dt, 0, d), vf[d], p);
-            }
+            struct Two {
+                Frag<T> a, v;
+            };
+            read_ahead<2 * ND, AHEAD>(
+                [&](int i) {
+                    Two f;
+                    f.a = QTile::rows(i < ND ? qt : dt, 0, i % ND);
+                    if constexpr (STAGE) {
+                        if (i >= ND) f.v = VTile::rows(vlds, 32 * wave, i % ND);
+                    }
+                    return f;
+                },
+                [&](int i, const Two& f) {
+                    if (i < ND) s = mma(f.a, kf[i], s);
+                    else if constexpr (STAGE) p = mma(f.a, f.v, p);
+                    else p = mma(f.a, vf[i - ND], p);
+                });
         } else {
+            const char* mine = half == 0 ? qt : dt;
+            read_ahead<ND, AHEAD>([&](int d) { return QTile::rows(mine, 0, d); },
+                                      [&](int d, const Frag<T>& f) { s = mma(f, kf[d], s); });
             p = exchange(s);
             if (half == 1) {
                 const f32x16 t = s;
@@ -93,8 +110,6 @@ __global__ __launch_bounds__(64 * WAVES * kHalves<DP>, (kPer<T, DP>)) void k_att
                 p = t;
             }
         }
-        // (operands of the next products loaded up here would not fit the registers)
-        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
             // lse and delta of four queries
@@ -118,18 +133,14 @@ __global__ __launch_bounds__(64 * WAVES * kHalves<DP>, (kPer<T, DP>)) void k_att
                 p[i] = in ? p[i] : 0.f;
             }
         }
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const Frag<T> fs = frag_of<T>(s, u);
-#pragma unroll
-            for (int b = 0; b < DW / 32; ++b) dv[b] = mma(QTile::cols(dt, 16 * u, half * DW + 32 * b), fs, dv[b]);
-        }
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const Frag<T> fp = frag_of<T>(p, u);
-#pragma unroll
-            for (int b = 0; b < DW / 32; ++b) dk[b] = mma(QTile::cols(qt, 16 * u, half * DW + 32 * b), fp, dk[b]);
-        }
+        constexpr int NB = DW / 32;
+        const Frag<T> fs[2] = {frag_of<T>(s, 0), frag_of<T>(s, 1)}, fp[2] = {frag_of<T>(p, 0), frag_of<T>(p, 1)};
+        read_ahead<4 * NB, AHEAD>(
+            [&](int i) { return QTile::cols(i < 2 * NB ? dt : qt, 16 * (i / NB % 2), half * DW + 32 * (i % NB)); },
+            [&](int i, const Frag<T>& f) {
+                if (i < 2 * NB) dv[i % NB] = mma(f, fs[i / NB], dv[i % NB]);
+                else dk[i % NB] = mma(f, fp[i / NB - 2], dk[i % NB]);
+            });
     };
     if (sh.first < sh.last) {
         // of a head's tiles the first `partial` hold queries that do not see every key of the

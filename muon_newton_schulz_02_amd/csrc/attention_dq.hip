@@ -59,13 +59,17 @@ __global__ __launch_bounds__(64 * WAVES * kHalves<DP>, (kPer<T, DP>)) void k_att
         const char* vt = lds[slot][1];
         slot = slot == RING - 1 ? 0 : slot + 1;
         f32x16 s = zero16(), p = zero16();
-        const char* mine = half == 0 ? kt : vt;
-#pragma unroll
-        for (int d = 0; d < DP / 16; ++d) s = mma(KT::rows(mine, 0, d), qf[d], s);
+        constexpr int ND = DP / 16, NB = DW / 32;
         if constexpr (HALVES == 1) {
-#pragma unroll
-            for (int d = 0; d < DP / 16; ++d) p = mma(KT::rows(vt, 0, d), df[d], p);
+            read_ahead<2 * ND, kAhead<T>>([&](int i) { return KT::rows(i < ND ? kt : vt, 0, i % ND); },
+                                          [&](int i, const Frag<T>& f) {
+                                              if (i < ND) s = mma(f, qf[i], s);
+                                              else p = mma(f, df[i - ND], p);
+                                          });
         } else {
+            const char* mine = half == 0 ? kt : vt;
+            read_ahead<ND, kAhead<T>>([&](int d) { return KT::rows(mine, 0, d); },
+                                      [&](int d, const Frag<T>& f) { s = mma(f, qf[d], s); });
             p = exchange(s);
             if (half == 1) {
                 const f32x16 t = s;
@@ -79,12 +83,9 @@ __global__ __launch_bounds__(64 * WAVES * kHalves<DP>, (kPer<T, DP>)) void k_att
 #pragma unroll
             for (int i = 0; i < 16; ++i) p[i] = t * KV + result_row(i, h) < sees ? p[i] : 0.f;
         }
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const Frag<T> f = frag_of<T>(p, u);
-#pragma unroll
-            for (int b = 0; b < DW / 32; ++b) dq[b] = mma(KT::cols(kt, 16 * u, half * DW + 32 * b), f, dq[b]);
-        }
+        const Frag<T> fp[2] = {frag_of<T>(p, 0), frag_of<T>(p, 1)};
+        read_ahead<2 * NB, kAhead<T>>([&](int i) { return KT::cols(kt, 16 * (i / NB), half * DW + 32 * (i % NB)); },
+                                      [&](int i, const Frag<T>& f) { dq[i % NB] = mma(f, fp[i / NB], dq[i % NB]); });
     };
     if (sh.first < sh.last) {
         for (int i = 0; i < RING - 1; ++i) fetch(sh.first + i);

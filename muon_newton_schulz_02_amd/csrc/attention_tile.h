@@ -254,6 +254,28 @@ __device__ __forceinline__ void store_row(T* p, int dim, int col0, const f32x16*
         }
 }
 
+// N steps use(i, f) of matrix instructions whose LDS operands f = load(i) are read AHEAD steps
+// earlier. Left to itself the compiler, short of registers, reads each operand right before its
+// use and waits for LDS every time.
+template <int N, int AHEAD, typename L, typename U>
+__device__ __forceinline__ void read_ahead(L load, U use) {
+    decltype(load(0)) f[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD && i < N; ++i) f[i] = load(i);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        use(i, f[i % AHEAD]);
+        if (i + AHEAD < N) f[i % AHEAD] = load(i + AHEAD);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
+// Four bfloat16 steps ahead where the registers allow it, two float32 ones (a step of float32 is
+// eight instructions of 64 cycles).
+template <typename T>
+constexpr int kAhead = sizeof(T) == 2 ? 4 : 2;
+
 // A value of lane ^ 32.
 __device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32, 64); }
 
