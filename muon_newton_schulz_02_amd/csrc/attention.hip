@@ -241,27 +241,27 @@ __global__ __launch_bounds__(256) void k_attention_sum(AttnArgs a, int pieces) {
 // probabilities are then 0) and delta = sum(dout o) over a head's features, 16 lanes a row.
 template <typename T, bool AL>
 __global__ __launch_bounds__(256) void k_attention_delta(AttnArgs a, int64_t rows) {
-    const int64_t r = (int64_t)blockIdx.x * 16 + threadIdx.x / 16;
-    if (r >= rows) return;
-    const int64_t t = r / a.heads;
-    const int head = (int)(r - t * a.heads);
-    const T* x = row_of<T>(a.dout, head, t);
-    const T* y = row_of<T>(a.o, head, t);
-    float s = 0.f;
-    for (int c = 8 * (threadIdx.x & 15); c < a.dim; c += 128) {
-        float u[8], v[8];
-        load_unit<T, AL>(x + c, a.dim - c, u);
-        load_unit<T, AL>(y + c, a.dim - c, v);
+    for (int64_t r = (int64_t)blockIdx.x * 16 + threadIdx.x / 16; r < rows; r += (int64_t)gridDim.x * 16) {
+        const int64_t t = r / a.heads;
+        const int head = (int)(r - t * a.heads);
+        const T* x = row_of<T>(a.dout, head, t);
+        const T* y = row_of<T>(a.o, head, t);
+        float s = 0.f;
+        for (int c = 8 * (threadIdx.x & 15); c < a.dim; c += 128) {
+            float u[8], v[8];
+            load_unit<T, AL>(x + c, a.dim - c, u);
+            load_unit<T, AL>(y + c, a.dim - c, v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s = fmaf(u[e], c + e < a.dim ? v[e] : 0.f, s);
-    }
+            for (int e = 0; e < 8; ++e) s = fmaf(u[e], c + e < a.dim ? v[e] : 0.f, s);
+        }
 #pragma unroll
-    for (int m = 1; m < 16; m <<= 1) s += __shfl_xor(s, m, 64);
-    if ((threadIdx.x & 15) == 0) {
-        const float lse = a.lse[(int64_t)head * a.n_queries + t];
-        float* o = a.stats + ((int64_t)head * a.n_queries + t) * 2;
-        o[0] = lse == -kInf ? kInf : lse * kLog2e;
-        o[1] = s;
+        for (int m = 1; m < 16; m <<= 1) s += __shfl_xor(s, m, 64);
+        if ((threadIdx.x & 15) == 0) {
+            const float lse = a.lse[(int64_t)head * a.n_queries + t];
+            float* o = a.stats + ((int64_t)head * a.n_queries + t) * 2;
+            o[0] = lse == -kInf ? kInf : lse * kLog2e;
+            o[1] = s;
+        }
     }
 }
 
@@ -297,6 +297,9 @@ AttnSplit attention_key_split(const AttnArgs& a) {
                     kCus * (a.dim <= (bf16 ? 128 : 64) ? 2 : 1));
 }
 
+// Workgroups of 256 threads for n of them, in rounds where a launch does not hold so many.
+static unsigned capped(int64_t n) { return (unsigned)std::min<int64_t>(n, int64_t(1) << 22); }
+
 static unsigned join_grid(int64_t rows, int64_t heads) { return (unsigned)ceil_div(rows * heads, 4); }
 
 // The inputs that have no aligned rows of whole chunks (every one where dim is not a multiple of
@@ -319,20 +322,20 @@ AttnPack attention_pack(const AttnArgs& a, bool back) {
 template <typename T>
 __global__ __launch_bounds__(256) void k_attention_pack(AttnArray x, T* out, int64_t rows, int heads, int dim, int cols) {
     constexpr int kPer = 16 / (int)sizeof(T);
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     const int per_row = cols / kPer;
-    const int64_t r = i / per_row;
-    if (r >= rows) return;
-    const int c = (int)(i - r * per_row) * kPer;
-    const int64_t t = r / heads;
-    const T* p = row_of<T>(x, (int)(r - t * heads), t);
-    T v[kPer];
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * per_row; i += (int64_t)gridDim.x * 256) {
+        const int64_t r = i / per_row;
+        const int c = (int)(i - r * per_row) * kPer;
+        const int64_t t = r / heads;
+        const T* p = row_of<T>(x, (int)(r - t * heads), t);
+        T v[kPer];
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-        const T w = p[min(c + e, dim - 1)];
-        v[e] = c + e < dim ? w : (T)0.f;
+        for (int e = 0; e < kPer; ++e) {
+            const T w = p[min(c + e, dim - 1)];
+            v[e] = c + e < dim ? w : (T)0.f;
+        }
+        *reinterpret_cast<u32x4*>(out + i * kPer) = __builtin_bit_cast(u32x4, v);
     }
-    *reinterpret_cast<u32x4*>(out + i * kPer) = __builtin_bit_cast(u32x4, v);
 }
 
 // The call's inputs with aligned rows.
@@ -351,7 +354,7 @@ static int pack_inputs(AttnArgs& g, bool back, void* stream) {
             using T = decltype(t);
             const int64_t n = rows * (cols * (int64_t)sizeof(T) / 16);
             if (n > 0)
-                hipLaunchKernelGGL((k_attention_pack<T>), dim3((unsigned)ceil_div(n, 256)), dim3(256), 0,
+                hipLaunchKernelGGL((k_attention_pack<T>), dim3(capped(ceil_div(n, 256))), dim3(256), 0,
                                    (hipStream_t)stream, *in[i], reinterpret_cast<T*>(out), rows, heads, g.dim, cols);
         };
         if (g.dtype == MA_PARAM_BF16) go(__bf16{});
@@ -407,7 +410,7 @@ int launch_attention_backward(const AttnArgs& a, void* stream) {
     };
     const int64_t rows = a.n_queries * a.heads;
     if (rows > 0) {
-        const dim3 grid((unsigned)ceil_div(rows, 16)), block(256);
+        const dim3 grid(capped(ceil_div(rows, 16))), block(256);
         auto delta = [&](auto t) {
             if (al) hipLaunchKernelGGL((k_attention_delta<decltype(t), true>), grid, block, 0, (hipStream_t)stream, a, rows);
             else hipLaunchKernelGGL((k_attention_delta<decltype(t), false>), grid, block, 0, (hipStream_t)stream, a, rows);

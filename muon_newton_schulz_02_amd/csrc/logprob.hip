@@ -8,7 +8,7 @@
 // joins the pieces.
 //
 // The highest `top` come from the same pass.  Every thread knows its largest value's
-// place; the top-th largest of those 512 keys (value, then lowest id) is a bound
+// place; the top-th largest of those keys (value, then lowest id) is a bound
 // that at least `top` keys of the row reach, all of them in the `top` threads whose own
 // largest does.  Those threads' units that hold a value so high (each knows its second largest too, so
 // hardly more than one each) are read again, the keys that reach the bound are listed in

@@ -375,6 +375,8 @@ def _attention_args(q, k, v, cu_q, cu_k, causal, scale):
             tuple(q.shape), q.dtype, tuple(k.shape), k.dtype, tuple(v.shape), v.dtype))
     if (cu_q is None) != (cu_k is None):
         raise ValueError("cu_q and cu_k go together")
+    if max(*q.shape[1:], k.shape[1]) >= 1 << 31 or q.shape[2] == 0:
+        raise ValueError("q %s and k %s: heads without features, or more than 2^31" % (tuple(q.shape), tuple(k.shape)))
     a = _abi.ma_attention()
     a.dtype = _dtype(q, "q")
     a.n_queries, a.heads, a.head_dim = q.shape

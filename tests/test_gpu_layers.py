@@ -591,6 +591,33 @@ def test_attention_empty():
     assert torch.all(dk == 0) and torch.all(dv == 0)
 
 
+def test_attention_refuses_heads_without_features():
+    x = torch.zeros((4, 2, 8), device="cuda")
+    many = torch.zeros((1, 1, 8), device="cuda").expand(1, 2 ** 31, 8)
+    none = x[:, :, :0]
+    for q, k in ((none, none), (many, many), (x, many)):
+        with pytest.raises(ValueError, match="heads"):
+            M.ma_attention_forward(q, k, k)
+        with pytest.raises(ValueError, match="heads"):
+            M.ma_attention_backward(q, q, k, k, q, torch.zeros((2, 4), device="cuda"))
+
+
+def test_attention_of_the_most_rows():
+    """2^28 queries of one feature and one key: launches longer than 2^32 threads, done in rounds."""
+    n = 2 ** 28
+    q = torch.empty((n, 1, 1), dtype=torch.bfloat16, device="cuda")
+    q.view(-1)[:] = (torch.arange(n, device="cuda", dtype=torch.int32) % 5).to(torch.bfloat16)
+    k = torch.ones((1, 1, 1), dtype=torch.bfloat16, device="cuda")
+    v = torch.full_like(k, 1.5)
+    o, lse = M.ma_attention_forward(q, k, v, causal=False, scale=1.0)
+    # a probability of 1 (off by less than 2^-20, and bfloat16's half step is 2^-8)
+    assert torch.all(o == 1.5)
+    assert (lse.view(-1) - q.view(-1).float()).abs().max() <= 2.0 ** -20
+    # dv sums 2^28 ones: 2^23 a piece and 2^28 in all, exact in float32
+    dq, dk, dv = M.ma_attention_backward(torch.ones_like(q), q, k, v, o, lse, causal=False, scale=1.0)
+    assert torch.all(dq == 0) and dk.item() == 0 and dv.item() == 2.0 ** 28
+
+
 # ------------------------------------------------------------ used together --
 
 LENS = [13, 1, 50, 32]
