@@ -268,33 +268,46 @@ __global__ __launch_bounds__(256) void k_attention_delta(AttnArgs a, int64_t row
 }  // namespace
 
 // Rows of a workgroup, and pieces of its walk, for `rows` rows of n_seqs sequences and `heads`
-// heads against `walk` rows of the other side.  Rows: `most`, or half as many where the
-// sequences have no more.  Pieces: until as many workgroups are there as run at once, in causal
-// calls twice as many, since the longest walk is twice the mean one and would otherwise end
-// alone (key blocks of 7 sequences of 20011 tokens, 628 workgroups: 1158 us in one piece, 914 +
-// 42 to join in two).  A piece has at least 128 rows to walk, in float32, whose products take
-// 16 times as long, 32.
-static AttnSplit split_of(const AttnArgs& a, int64_t rows, int64_t walk, int64_t heads, int most, int at_once) {
+// heads against `walk` rows of the other side.
+//
+// Pieces: as many as fill the GPU, which runs `at_once` workgroups; each has at least 128 rows
+// to walk, in float32, whose products take 16 times as long, 32.  More cost their joining:
+// twice as many for causal queries would make 102 us of 60 (10000 tokens of 7 sequences, 8 heads
+// of 128, bf16), 75 of 32 (of 40 sequences), 292 of 258 (10700 of one).  Twice as many, since the
+// longest walk of a causal call is twice the mean one or, of sequences with lengths unlike, more,
+// pay in float32 (4000 tokens of 3 sequences, 8 / 2 heads of 128, backward: 787 us without,
+// 567) and for key blocks, each of which walks every query of its group, where a piece keeps
+// 2048 rows (20011 tokens of 7 sequences, 16 / 4 heads, backward: of 64 features 727 us without,
+// 609; of 128 1097 and 1030; 16000 of 2 with 8 / 1 heads 1228 and 1074), but not for one
+// sequence that fills the GPU (10700 tokens: 855 without, 887).
+static AttnSplit split_of(const AttnArgs& a, int64_t rows, int64_t walk, int64_t heads, int most, bool halve,
+                          int at_once, bool keys) {
     AttnSplit s;
     if (rows == 0 || a.n_seqs == 0) return s;
-    const bool wide = a.dtype == MA_PARAM_FP32;
-    const int64_t each = ceil_div(rows, a.n_seqs);
-    s.rows = each <= most / 2 ? most / 2 : most;
+    const int64_t each = ceil_div(rows, a.n_seqs), seen = ceil_div(walk, a.n_seqs);
+    s.rows = halve && each <= most / 2 ? most / 2 : most;
     const int64_t blocks = ceil_div(each, s.rows) * a.n_seqs * heads;
-    const int64_t want = a.causal ? ceil_div(2 * at_once, blocks) : at_once / blocks;
-    s.pieces = (int32_t)std::max<int64_t>(1, std::min<int64_t>({want, ceil_div(walk, a.n_seqs * (wide ? 32 : 128)), 32}));
+    const bool wide = a.dtype == MA_PARAM_FP32;
+    int64_t n = std::min(at_once / blocks, ceil_div(seen, wide ? 32 : 128));
+    if (a.causal && (wide || (keys && (blocks < at_once || a.n_seqs > 1))))
+        n = std::max(n, std::min(ceil_div(2 * at_once, blocks), seen / (wide ? 128 : 2048)));
+    s.pieces = (int32_t)std::max<int64_t>(1, std::min<int64_t>(n, 32));
     return s;
 }
-// Workgroups of 4 waves (8 for the keys of 256 bfloat16 features): two on a CU where a
-// lane has 256 registers.
-AttnSplit attention_query_split(const AttnArgs& a) {
-    const bool two = a.dtype == MA_PARAM_BF16 || a.dim <= 64;
-    return split_of(a, a.n_queries, a.n_keys, a.heads, a.dim > 128 ? 64 : 128, kCus * (two ? 2 : 1));
+// Workgroups of 4 waves (8 for the keys of 256 bfloat16 features): two on a CU where a lane
+// has 256 registers.  Where sequences have no more than half a workgroup's rows it takes half
+// as many (400 sequences of 50, 16 / 4 heads, backward: 267 us, 311 without), in the forward pass
+// only where its LDS lets a CU run twice as many (float32 of 128 features 83 us, 130 without, but
+// bfloat16 of 128 188 and 155, float32 of 256 139 and 116).
+AttnSplit attention_query_split(const AttnArgs& a, bool back) {
+    const bool bf16 = a.dtype == MA_PARAM_BF16;
+    return split_of(a, a.n_queries, a.n_keys, a.heads, a.dim > 128 ? 64 : 128, back || a.dim <= (bf16 ? 64 : 128),
+                    kCus * (bf16 || a.dim <= 64 ? 2 : 1), false);
 }
 AttnSplit attention_key_split(const AttnArgs& a) {
     const bool bf16 = a.dtype == MA_PARAM_BF16;
     return split_of(a, a.n_keys, a.n_queries * (a.heads / a.kv_heads), a.kv_heads, a.dim > 128 && !bf16 ? 64 : 128,
-                    kCus * (a.dim <= (bf16 ? 128 : 64) ? 2 : 1));
+                    true, kCus * (a.dim <= (bf16 ? 128 : 64) ? 2 : 1), true);
 }
 
 // Workgroups of 256 threads for n of them, in rounds where a launch does not hold so many.
@@ -371,13 +384,15 @@ int launch_attention_forward(const AttnArgs& a, void* stream) {
     g.wide = al_heads(a.o, a.dim, a.dtype);
     int rc = pack_inputs(g, false, stream);
     if (rc != (int)hipSuccess) return rc;
-    const AttnSplit sp = attention_query_split(a);
+    const AttnSplit sp = attention_query_split(a, false);
     const AttnGrid grid = grid_of(a.n_queries, a.n_seqs, a.heads, sp.rows, sp.pieces);
     rc = by_kind(a, sp.rows, [&](auto t, auto dp, auto wv) {
         using T = decltype(t);
         constexpr int DP = decltype(dp)::value, WAVES = decltype(wv)::value;
         constexpr int KV = sizeof(T) == 2 && kHalves<DP> == 1 ? 64 : 32;
-        if constexpr (WAVES * kHalves<DP> == 4 || WAVES * kHalves<DP> == 2)
+        // (workgroups of 4 waves, or of 2 where the rule above halves them)
+        constexpr bool HALVE = DP <= (sizeof(T) == 2 ? 64 : 128);
+        if constexpr (WAVES * kHalves<DP> == 4 || (HALVE && WAVES == 2))
             hipLaunchKernelGGL((k_attention_forward<T, DP, KV, WAVES>),
                                dim3((unsigned)grid.slots * a.heads * grid.pieces), dim3(64 * WAVES * kHalves<DP>), 0,
                                (hipStream_t)stream, g, grid);
@@ -418,7 +433,7 @@ int launch_attention_backward(const AttnArgs& a, void* stream) {
         if (a.dtype == MA_PARAM_BF16) delta(__bf16{});
         else delta(float{});
         rc = (int)hipGetLastError();
-        const AttnSplit sp = attention_query_split(a);
+        const AttnSplit sp = attention_query_split(a, true);
         if (rc == (int)hipSuccess) rc = launch_attention_dq(g, sp, stream);
         if (rc == (int)hipSuccess && sp.pieces > 1) rc = join(std::false_type{}, sp.pieces);
         if (rc != (int)hipSuccess) return rc;

