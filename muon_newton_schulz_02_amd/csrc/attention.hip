@@ -16,13 +16,15 @@
 // results a last launch joins in order.  This file has the forward kernel, what is before and
 // behind the others, and the rules for pieces.
 //
-// Bound by the matrix cores and what shares their issue slots: 20011 tokens of 7 sequences, 16 / 4
-// heads of 128, bf16: forward 251 GFLOP in 300 to 330 us (0.8 PFLOP/s; a library product of 8192
-// x 8192 matrices reaches 1.2 to 1.4), matrix instructions on 44 % of a SIMD's cycles.  A tile of 32
-// queries and 64 keys is 1024 cycles of them a wave, and its 2048 scores cost maximum, exponential, sum and
-// rounding, about as many cycles of the vector unit; two waves a SIMD overlap the two in part.
-// One sequence of 14336 tokens with 8 heads: 0.95 PFLOP/s.  Backward (dq, dkv and what is around
-// them) 627 GFLOP counted as five products, seven done, in 1.05 ms.
+// Bound by issue: 20011 tokens of 7 sequences, 16 / 4 heads of 128, bf16: forward 251 GFLOP in
+// 300 to 325 us (0.8 PFLOP/s; a library product of 8192 x 8192 matrices reaches 1.2 to 1.4).
+// A tile of 32 queries and 64 keys is 1024 cycles of matrix instructions a wave, and about 1000
+// of the vector unit's for the maximum, exponential, sum and rounding of 2048 scores, half of it
+// the exponentials.  Matrix instructions take 44 % of a SIMD's cycles, the others 52 %: two
+// waves hardly overlap them, in whatever order (the next tile's scores formed step by step
+// between this one's exponentials: 318 -> 328 us).  One sequence of 14336 tokens with 8 heads: 0.95
+// PFLOP/s.  Backward (dq, dkv and what is around them) 627 GFLOP counted as five products,
+// seven done, in 1.03 to 1.06 ms.
 
 #include <hip/hip_runtime.h>
 
@@ -68,14 +70,14 @@ __global__ __launch_bounds__(64 * WAVES * kHalves<DP>, (kPer<T, DP>)) void k_att
     const int sees = seen(a, j, q);
     // One tile; PART: some row of the workgroup does not see all of it.  (Two bodies: as a
     // condition the masks would be computed for every tile.)
-    auto tile = [&](int t, auto part) {
+    auto tile = [&](int t, auto slot, auto part) {
         copies_barrier<0>();
-        const int at = (t - sh.first) & 1;
-        const char* kt = lds[at][0];
-        const char* vt = lds[at][1];
+        constexpr int AT = decltype(slot)::value;
+        const char* kt = lds[AT][0];
+        const char* vt = lds[AT][1];
         if (t + 1 < sh.last) {
-            copy_k(lds[at ^ 1][0], kx, (t + 1) * KV);
-            copy_v(lds[at ^ 1][1], vx, (t + 1) * KV);
+            copy_k(lds[AT ^ 1][0], kx, (t + 1) * KV);
+            copy_v(lds[AT ^ 1][1], vx, (t + 1) * KV);
         }
         f32x16 s[KV / 32];
         constexpr int ND = DW / 16, NB = DW / 32;
@@ -131,9 +133,17 @@ __global__ __launch_bounds__(64 * WAVES * kHalves<DP>, (kPer<T, DP>)) void k_att
             [&](int i, const Frag<T>& f) { o[i % NB] = mma(f, p[i / NB], o[i % NB]); });
     };
     const int whole = min(max(seen(a, j, j.row0), 0) / KV, sh.last);
+    // Two tiles a turn: with LDS slots as constants addresses differ by constants too, which reads
+    // hold themselves (28 additions a tile less: 323 -> 313 us).
     int t = sh.first;
-    for (; t < whole; ++t) tile(t, std::false_type{});
-    for (; t < sh.last; ++t) tile(t, std::true_type{});
+    for (; t + 1 < whole; t += 2) {
+        tile(t, Int<0>{}, std::false_type{});
+        tile(t + 1, Int<1>{}, std::false_type{});
+    }
+    for (; t < sh.last; t += 2) {
+        tile(t, Int<0>{}, std::true_type{});
+        if (t + 1 < sh.last) tile(t + 1, Int<1>{}, std::true_type{});
+    }
     l += other_half(l);
     if (q >= j.q_len) return;
     const int64_t row = (int64_t)j.q_at + q;

@@ -3,11 +3,10 @@
 // 2^(S - lse), with dP = dout V^T and dS = P (dP - delta) summing dv^T += dout^T P and dk^T +=
 // Q^T dS: four products a tile.
 //
-// Bound by the matrix cores fed from LDS: 20011 tokens of 7 sequences, 16 / 4 heads of 128, bf16,
-// in 605 us (502 GFLOP, 0.83 PFLOP/s) and 41 to join two pieces, matrix instructions on 56 % of
-// a SIMD's cycles.  A wave with 32 keys reads each operand of q and dout for one product only: 1024
-// bytes, at 128 a cycle 8 cycles of the CU's LDS, and 32 for its four SIMDs, as many as a
-// product takes.  64 keys a wave would halve that, but dk and dv alone are then 256 registers.
+// Bound by issue: 20011 tokens of 7 sequences, 16 / 4 heads of 128, bf16, in 605 us (502 GFLOP,
+// 0.83 PFLOP/s) and 41 to join two pieces, matrix instructions on 56 % of a SIMD's cycles, others on
+// 40, LDS reads on 42 % of the CU's.  All 256 registers are taken: constant LDS slots, two
+// tiles a turn as in the other walks, spill.
 
 #include <hip/hip_runtime.h>
 

@@ -2,8 +2,8 @@
 // the keys, recomputing the scores S^T = K Q^T and P^T = 2^(S^T - lse), with dP^T = V dout^T
 // and dS^T = P^T (dP^T - delta) summing dq^T += K^T dS^T: three products a tile.
 //
-// Bound as the forward pass is: 20011 tokens of 7 sequences, 16 / 4 heads of 128, bf16, in 418 us
-// (376 GFLOP, 0.90 PFLOP/s), matrix instructions on 53 % of a SIMD's cycles.
+// Bound by issue as the forward pass is: 20011 tokens of 7 sequences, 16 / 4 heads of 128, bf16,
+// in 400 us (376 GFLOP, 0.94 PFLOP/s), matrix instructions on 53 % of a SIMD's cycles, others on 47.
 
 #include <hip/hip_runtime.h>
 
@@ -47,7 +47,7 @@ __global__ __launch_bounds__(64 * WAVES * kHalves<DP>, (kPer<T, DP>)) void k_att
     const Share sh(max(0, seen(a, j, end) + KV - 1) / KV, j.piece, grid.pieces);
     const int sees = seen(a, j, q);
     const typename KT::Copy copy_k(kx), copy_v(vx);
-    int slot = 0, ahead = 0;
+    int ahead = 0;
     // (past the last tile the copies are empty)
     auto fetch = [&](int t) {
         const int row = t < sh.last ? t * KV : j.k_len;
@@ -55,12 +55,12 @@ __global__ __launch_bounds__(64 * WAVES * kHalves<DP>, (kPer<T, DP>)) void k_att
         copy_v(lds[ahead][1], vx, row);
         ahead = ahead == RING - 1 ? 0 : ahead + 1;
     };
-    auto tile = [&](int t, auto part) {
+    auto tile = [&](int t, auto slot, auto part) {
+        constexpr int AT = decltype(slot)::value;
         copies_barrier<(RING - 2) * kTileCopies>();
         fetch(t + RING - 1);
-        const char* kt = lds[slot][0];
-        const char* vt = lds[slot][1];
-        slot = slot == RING - 1 ? 0 : slot + 1;
+        const char* kt = lds[AT][0];
+        const char* vt = lds[AT][1];
         f32x16 s = zero16(), p = zero16();
         constexpr int ND = DP / 16, NB = DW / 32;
         if constexpr (HALVES == 1) {
@@ -94,9 +94,19 @@ __global__ __launch_bounds__(64 * WAVES * kHalves<DP>, (kPer<T, DP>)) void k_att
         for (int i = 0; i < RING - 1; ++i) fetch(sh.first + i);
         // tiles that every row of the workgroup sees whole, and the others
         const int whole = min(max(seen(a, j, j.row0), 0) / KV, sh.last);
+        // (the ring's slots as constants, as in the forward pass)
         int t = sh.first;
-        for (; t < whole; ++t) tile(t, std::false_type{});
-        for (; t < sh.last; ++t) tile(t, std::true_type{});
+        for (; t + RING <= whole; t += RING) {
+            tile(t, Int<0>{}, std::false_type{});
+            tile(t + 1, Int<1>{}, std::false_type{});
+            if constexpr (RING == 3) tile(t + 2, Int<2>{}, std::false_type{});
+        }
+        for (; t < sh.last; t += RING) {
+            tile(t, Int<0>{}, std::true_type{});
+            if (t + 1 < sh.last) tile(t + 1, Int<1>{}, std::true_type{});
+            if constexpr (RING == 3)
+                if (t + 2 < sh.last) tile(t + 2, Int<2>{}, std::true_type{});
+        }
     }
     if (q >= j.q_len) return;
     const int64_t row = (int64_t)j.q_at + q;

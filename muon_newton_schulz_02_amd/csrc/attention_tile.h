@@ -276,8 +276,12 @@ __device__ __forceinline__ void read_ahead(L load, U use) {
 template <typename T>
 constexpr int kAhead = sizeof(T) == 2 ? 4 : 2;
 
-// A value of lane ^ 32.
-__device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32, 64); }
+// A value of lane ^ 32 (a swap of registers; through LDS a forward pass takes 2 % longer).
+__device__ __forceinline__ float other_half(float v) {
+    const uint32_t x = __float_as_uint(v);
+    const auto both = __builtin_amdgcn_permlane32_swap(x, x, false, false);    // lanes 0 .. 31, 32 .. 63
+    return __uint_as_float(threadIdx.x & 32 ? both[0] : both[1]);
+}
 
 // Offsets of sequence s, kept inside the array whatever the device holds.
 __device__ __forceinline__ int seq_at(const int32_t* cu, int s, int n_seqs, int64_t total) {
