@@ -17,10 +17,10 @@
 // behind the others, and the rules for pieces.
 //
 // Bound by issue: 20011 tokens of 7 sequences, 16 / 4 heads of 128, bf16: forward 251 GFLOP in
-// 300 to 325 us (0.8 PFLOP/s; a library product of 8192 x 8192 matrices reaches 1.2 to 1.4).
+// 290 to 325 us (0.77 to 0.86 PFLOP/s; a library product of 8192 x 8192 matrices reaches 1.2 to 1.4).
 // A tile of 32 queries and 64 keys is 1024 cycles of matrix instructions a wave, and about 1000
 // of the vector unit's for the maximum, exponential, sum and rounding of 2048 scores, half of it
-// the exponentials.  Matrix instructions take 44 % of a SIMD's cycles, the others 52 %: two
+// the exponentials.  Matrix instructions take 48 % of a SIMD's cycles, the others 50 %: two
 // waves hardly overlap them, in whatever order (the next tile's scores formed step by step
 // between this one's exponentials: 318 -> 328 us).  One sequence of 14336 tokens with 8 heads: 0.95
 // PFLOP/s.  Backward (dq, dkv and what is around them) 627 GFLOP counted as five products,

@@ -3,8 +3,8 @@
 // 2^(S - lse), with dP = dout V^T and dS = P (dP - delta) summing dv^T += dout^T P and dk^T +=
 // Q^T dS: four products a tile.
 //
-// Bound by issue: 20011 tokens of 7 sequences, 16 / 4 heads of 128, bf16, in 605 us (502 GFLOP,
-// 0.83 PFLOP/s) and 41 to join two pieces, matrix instructions on 56 % of a SIMD's cycles, others on
+// Bound by issue: 20011 tokens of 7 sequences, 16 / 4 heads of 128, bf16, in 575 to 605 us (502
+// GFLOP, 0.83 to 0.87 PFLOP/s) and 41 to join two pieces, matrix instructions on 56 % of a SIMD's cycles, others on
 // 40, LDS reads on 42 % of the CU's.  All 256 registers are taken: constant LDS slots, two
 // tiles a turn as in the other walks, spill.
 

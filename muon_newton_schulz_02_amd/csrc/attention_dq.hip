@@ -3,7 +3,7 @@
 // and dS^T = P^T (dP^T - delta) summing dq^T += K^T dS^T: three products a tile.
 //
 // Bound by issue as the forward pass is: 20011 tokens of 7 sequences, 16 / 4 heads of 128, bf16,
-// in 400 us (376 GFLOP, 0.94 PFLOP/s), matrix instructions on 53 % of a SIMD's cycles, others on 47.
+// in 385 us (376 GFLOP, 0.98 PFLOP/s), matrix instructions on 58 % of a SIMD's cycles, others on 46.
 
 #include <hip/hip_runtime.h>
 
