@@ -491,6 +491,15 @@ def test_attention(kind, lq, lk, heads, kv, dim, causal):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp32"])
+@pytest.mark.parametrize("lq,lk,heads,kv,dim", [([1500, 900], None, 4, 1, 64), ([40, 1200, 7], [900, 1300, 64], 2, 2, 128),
+                                                ([1111], None, 8, 1, 136)])
+def test_attention_causal_walks_in_pieces(kind, lq, lk, heads, kv, dim):
+    rng = np.random.default_rng(sum(lq) * 3 + dim)
+    cq, ck = _offsets(lq), _offsets(lk or lq)
+    _check_attention(*_inputs(rng, int(cq[-1]), int(ck[-1]), heads, kv, dim, kind), cq, ck, True, None, kind)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
 def test_attention_one_sequence_without_offsets(kind):
     rng = np.random.default_rng(2)
     q, k, v, do = _inputs(rng, 150, 190, 4, 2, 64, kind)
