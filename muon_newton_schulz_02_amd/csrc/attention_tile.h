@@ -19,6 +19,7 @@
 
 #include "grads_device.h"
 #include "layers_internal.h"
+#include "lds_copy.h"
 
 namespace ma {
 namespace {
@@ -60,40 +61,6 @@ __device__ __forceinline__ Frag<T> frag_of(const f32x16& v, int s) {
 
 // The row of a result's element i, and the first of the four rows of its group i / 4.
 __device__ __forceinline__ int result_row(int i, int h) { return 8 * (i >> 2) + 4 * h + (i & 3); }
-
-__device__ __forceinline__ uint32_t lds_addr(const void* p) {
-    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)p;
-}
-
-// Buffer resource: base address, stride 0, extent in bytes (accesses past it
-// read zero), raw format.
-__device__ __forceinline__ u32x4 make_rsrc(const void* base, int64_t bytes) {
-    const uint64_t a = (uint64_t)base;
-    u32x4 r;
-    r.x = (uint32_t)a;
-    r.y = (uint32_t)(a >> 32) & 0xffffu;
-    r.z = bytes <= 0 ? 0u : bytes > 0x7fffffffLL ? 0x7fffffffu : (uint32_t)bytes;
-    r.w = 0x00020000u;
-    return r;
-}
-
-// 16 bytes per lane from global memory straight into LDS: lane t of the wave
-// writes bytes [lds + 16 t, lds + 16 t + 16).  The kernel orders these copies
-// itself, with explicit vmcnt waits and barriers.
-__device__ __forceinline__ void dma16(u32x4 rsrc, uint32_t lds, uint32_t voff) {
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                 :
-                 : "s"(lds), "v"(voff), "s"(rsrc)
-                 : "memory", "m0");
-}
-
-// 4 bytes per lane, the same way.
-__device__ __forceinline__ void dma4(u32x4 rsrc, uint32_t lds, uint32_t voff) {
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, 0 offen lds"
-                 :
-                 : "s"(lds), "v"(voff), "s"(rsrc)
-                 : "memory", "m0");
-}
 
 // All but the last N of this wave's copies have landed, its LDS accesses are done, and so
 // is every wave's.  (A release fence would wait for all copies; the empty statement keeps the

@@ -25,6 +25,7 @@
 
 #include "grads_device.h"
 #include "grads_internal.h"
+#include "lds_copy.h"
 
 namespace ma {
 namespace {
@@ -540,32 +541,6 @@ __global__ __launch_bounds__(kThreads) void k_lg_split(const float* __restrict__
             *reinterpret_cast<u32x4*>(out + (p * rows + t) * n8 + col) = w;
         }
     }
-}
-
-// Buffer resource: base address, stride 0, extent in bytes (accesses past it
-// read zero), raw format.
-__device__ __forceinline__ u32x4 make_rsrc(const void* base, int64_t bytes) {
-    const uint64_t a = (uint64_t)base;
-    u32x4 r;
-    r.x = (uint32_t)a;
-    r.y = (uint32_t)(a >> 32) & 0xffffu;
-    r.z = bytes <= 0 ? 0u : bytes > 0x7fffffffLL ? 0x7fffffffu : (uint32_t)bytes;
-    r.w = 0x00020000u;
-    return r;
-}
-
-__device__ __forceinline__ uint32_t lds_addr(const void* p) {
-    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)p;
-}
-
-// 16 bytes per lane from global memory straight into LDS: lane t of the wave
-// writes bytes [lds + 16 t, lds + 16 t + 16).  The kernel orders these copies
-// itself, with explicit vmcnt waits and barriers.
-__device__ __forceinline__ void dma16(u32x4 rsrc, uint32_t lds, uint32_t voff) {
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                 :
-                 : "s"(lds), "v"(voff), "s"(rsrc)
-                 : "memory", "m0");
 }
 
 // s_waitcnt vmcnt(n) alone, n = 8 or 12.

@@ -59,6 +59,7 @@
 
 #include <utility>
 
+#include "lds_copy.h"
 #include "ma_internal.h"
 
 namespace ma {
@@ -232,40 +233,6 @@ __device__ __forceinline__ void lds_write16(float* dst, const float* v) {
     float4* d4 = reinterpret_cast<float4*>(dst);
 #pragma unroll
     for (int q = 0; q < 4; ++q) d4[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-}
-
-
-// Buffer resource of one operand (gfx9 layout): base address, stride 0,
-// extent in bytes (reads past it return zero) and the raw 32-bit-element
-// format word.
-typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
-
-__device__ __forceinline__ u32x4 make_rsrc(const void* base, int64_t bytes) {
-    const uint64_t a = (uint64_t)base;
-    const uint32_t n = bytes > 0x7fffffffLL ? 0x7fffffffu : (uint32_t)bytes;
-    u32x4 r;
-    r.x = (uint32_t)a;
-    r.y = (uint32_t)(a >> 32) & 0xffffu;
-    r.z = n;
-    r.w = 0x00020000u;
-    return r;
-}
-
-// LDS byte address of a pointer into a __shared__ array.
-__device__ __forceinline__ uint32_t lds_addr(const void* p) {
-    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)p;
-}
-
-// 16 bytes per lane from global memory straight into LDS: lane t of the wave
-// writes bytes [lds + 16 t, lds + 16 t + 16).  Issued as inline assembly so
-// the compiler's own wait-count insertion does not treat every later LDS
-// read as dependent on it (it cannot tell the stage buffers apart); the
-// kernel orders these copies itself with explicit vmcnt waits and barriers.
-__device__ __forceinline__ void dma16(u32x4 rsrc, uint32_t lds, uint32_t voff, uint32_t soff) {
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-                 :
-                 : "s"(lds), "v"(voff), "s"(rsrc), "s"(soff)
-                 : "memory", "m0");
 }
 
 // ---------------------------------------------------------------------------

@@ -28,6 +28,8 @@
 
 #include <cstdint>
 
+#include "lds_copy.h"
+
 namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -168,17 +170,9 @@ __global__ __launch_bounds__(256) void k_peak_stream(f32x4* __restrict__ a, f32x
 // (b * 7919 + s) mod (src_bytes / 32 KB) of the source: a source of a few MB
 // stays in every XCD's L2, a large one streams from the memory-side cache or
 // HBM.
-typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 constexpr int kDmaStage = 32768;
 constexpr int kDmaSlots = 5;
 constexpr int kDmaWaves = 8;
-
-__device__ __forceinline__ void dma_copy16(u32x4 rsrc, uint32_t lds, uint32_t voff, uint32_t soff) {
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-                 :
-                 : "s"(lds), "v"(voff), "s"(rsrc), "s"(soff)
-                 : "memory", "m0");
-}
 
 // vmcnt(n) for n in {0, 4, 8, 12}, the other counters unconstrained
 __device__ __forceinline__ void dma_wait(int n) {
@@ -195,7 +189,7 @@ __global__ __launch_bounds__(kDmaWaves * 64) void k_peak_dma(const char* __restr
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint64_t a = (uint64_t)src;
-    u32x4 rsrc;
+    ma::u32x4 rsrc;
     rsrc.x = (uint32_t)a;
     rsrc.y = (uint32_t)(a >> 32) & 0xffffu;
     rsrc.z = src_bytes;
@@ -209,7 +203,7 @@ __global__ __launch_bounds__(kDmaWaves * 64) void k_peak_dma(const char* __restr
         const uint32_t from = chunk * kDmaStage + (uint32_t)wave * 4096;
         const uint32_t to = lring + (uint32_t)(s % kDmaSlots) * kDmaStage + (uint32_t)wave * 4096;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) dma_copy16(rsrc, to + i * 1024, voff, from + i * 1024);
+        for (int i = 0; i < 4; ++i) ma::dma16(rsrc, to + i * 1024, voff, from + i * 1024);
     };
     const uint64_t t0 = __builtin_readcyclecounter();
     const uint64_t w0 = __builtin_amdgcn_s_memrealtime();
