@@ -97,9 +97,12 @@ struct Soft {
         mk = m * k;
         s = t = 0.f;
     }
-    // reference `to` less this one, in units of 2^: at most 0
+    // reference `to` less this one, in units of 2^: at most 0.  Both are products rounded by
+    // themselves: as a fused multiply-add the difference would be that of a rounded and an exact one.
     __device__ __forceinline__ float below(float to, float k) const {
-        return fmaxf(m < kMask ? (m - to) * k : mk - to * k, kFar);
+#pragma clang fp contract(off)
+        const float nk = to * k;
+        return fmaxf(m < kMask ? (m - to) * k : mk - nk, kFar);
     }
     // another reference, not below m
     __device__ __forceinline__ void raise(float to, float k) {
