@@ -138,6 +138,8 @@ int ma_token_logprob_forward(const void* logits, int32_t dtype, int64_t n_tokens
  * dentropy[t] * entropy[t] in the logits:
  *   dlogits[t][v] = scale * (dlogprob[t] * ([v = tokens[t]] - p[v])
  *                            - dentropy[t] * p[v] * (ln p[v] + entropy[t]))
+ * p errs by |lse[t]| 2^-24 of itself, by which lse is rounded: a row of nothing but a finite
+ * mask value of -1e8, say, has lost its ln vocab there (give it dlogprob and dentropy of 0).
  * A token outside [0, vocab) takes dlogprob as 0.  lse and entropy are the forward pass';
  * dentropy (with entropy) may be NULL.  A row of nothing but -infinity has gradient 0.
  * dlogits may be logits itself, with its type and stride.  n_tokens may be 0.

@@ -78,8 +78,8 @@ __device__ __forceinline__ float unordered(uint32_t u) {
 // The larger key is the higher value, of equal ones the lower id.
 __device__ __forceinline__ uint64_t key_of(float z, uint32_t id) { return (uint64_t)ordered(z) << 32 | (uint32_t)~id; }
 
-// (a value this far down is a mask: products with a scale may leave float32)
-constexpr float kMask = -1e30f;
+// (a product of 2^24 is rounded to whole numbers: beyond, its rounding alone soon leaves the range of 2^u)
+constexpr float kFine = 0x1p24f;
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float v;         // (the builtin maximum would first quieten each input)
@@ -89,28 +89,35 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 
 // A running softmax: m the largest value (at least -FLT_MAX), s and t the sums of 2^u and u 2^u.
 // u = z k - mk is one multiply-add from a reference that is m k rounded; what the rounding
-// left out is made up for once, in ln s.  Where m is a mask u is (z - m) k instead.
+// left out is made up for once, in ln s.  Where |m k| is 2^24 or more (a row of mask values only,
+// say) the reference is m k itself, and u is (z - m) k instead.
 struct Soft {
     float m, mk, s, t;
-    __device__ __forceinline__ void begin(float k) {
+    __device__ __forceinline__ void begin() {
         m = -__FLT_MAX__;
-        mk = m * k;
+        mk = -0.5f * kFine;          // (sums of 0 have any reference: one that needs no care)
         s = t = 0.f;
     }
-    // reference `to` less this one, in units of 2^: at most 0.  Both are products rounded by
+    __device__ __forceinline__ bool far() const { return !(fabsf(mk) < kFine); }
+    // what the reference's rounding left out
+    __device__ __forceinline__ float left(float k) const { return far() ? 0.f : fmaf(m, k, -mk); }
+    // this reference less the one of `o`, in units of 2^: at most 0.  Two rounded ones are products rounded by
     // themselves: as a fused multiply-add the difference would be that of a rounded and an exact one.
-    __device__ __forceinline__ float below(float to, float k) const {
+    __device__ __forceinline__ float below(const Soft& o, float k) const {
 #pragma clang fp contract(off)
-        const float nk = to * k;
-        return fmaxf(m < kMask ? (m - to) * k : mk - nk, kFar);
+        float d = mk - o.mk;
+        // (whether one of them is far: o is not below this one)
+        if (__builtin_expect(!(fmaxf(-mk, o.mk) < kFine), 0)) d = (m - o.m) * k - left(k) + o.left(k);
+        return __builtin_amdgcn_fmed3f(d, kFar, 0.f);
     }
     // another reference, not below m
     __device__ __forceinline__ void raise(float to, float k) {
-        const float d = below(to, k), c = __builtin_amdgcn_exp2f(d);
+        const Soft o = {to, to * k, 0.f, 0.f};
+        const float d = below(o, k), c = __builtin_amdgcn_exp2f(d);
         t = fmaf(s, d, t) * c;
         s *= c;
-        m = to;
-        mk = to * k;
+        m = o.m;
+        mk = o.mk;
     }
     __device__ __forceinline__ void add(float u) {
         const float e = __builtin_amdgcn_exp2f(u);
@@ -118,9 +125,9 @@ struct Soft {
         t = fmaf(e, fmaxf(u, kFar), t);          // (a NaN is in e)
     }
     __device__ __forceinline__ void add8(const float* z, float k) {
-        if (__builtin_expect(__any(m < kMask), 0)) {
+        if (__builtin_expect(__any(far()), 0)) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) add(m < kMask ? (z[e] - m) * k : fmaf(z[e], k, -mk));
+            for (int e = 0; e < 8; ++e) add(far() ? (z[e] - m) * k : fmaf(z[e], k, -mk));
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) add(fmaf(z[e], k, -mk));
@@ -141,7 +148,7 @@ struct Soft {
     }
     // ln of the sum of e^(scale (z - m))
     __device__ __forceinline__ float log_sum(float k) const {
-        return logf(s) - (m < kMask ? 0.f : kLn2 * fmaf(m, k, -mk));
+        return logf(s) - kLn2 * left(k);
     }
 };
 
@@ -334,7 +341,7 @@ __global__ __launch_bounds__(NT) void k_logprob_forward(LogprobArgs a) {
         const int from = (int)min<int64_t>((int64_t)blockIdx.y * a.piece, a.vocab);
         const Piece<NT> p(reinterpret_cast<const char*>(z), sizeof(T), from, (int)min<int64_t>(from + a.piece, a.vocab));
         Soft f;
-        f.begin(k);
+        f.begin();
         // the largest value, the round that held it, and the largest of the other rounds
         float top = -__builtin_inff(), second = -__builtin_inff();
         // (the elements before the whole units come first, so of equal values a thread's first

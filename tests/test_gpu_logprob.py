@@ -54,3 +54,25 @@ def test_rows_far_from_zero(kind, times, vocab):
     ids = rng.integers(0, vocab, 12)
     for scale, top in ((1.0, 5), (0.7, 0)):
         _check(z, times, ids, scale, top)
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("times,vocab", PLANS)
+def test_rows_of_large_values(kind, times, vocab):
+    """Rows of nothing but a finite mask value, such a mask beside a few entries, and logits of up to float32's
+    largest, some of which differ by a few steps of float32 only."""
+    rng = np.random.default_rng(vocab * 3 + times)
+    few = lambda: rng.integers(0, 9, vocab)
+    z = np.zeros((12, vocab))
+    for r, mask in enumerate((-1e9, -1e10, -1e20, -1e30, -3.3e38, 1e10, 3e38)):
+        z[r] = mask
+    z[7] = -1e10
+    z[7, rng.integers(0, vocab, 5)] = rng.standard_normal(5)
+    z[8] = 1e10 + 1024.0 * few()             # (float32 is 1024 apart there)
+    z[9] = -1e10 - 1024.0 * few()
+    z[10] = 2.0 ** 24 * np.log(2) - 4 + few()    # (their exponents of 2 lie around 2^24)
+    z[11] = -2.0 ** 24 * np.log(2) - 4 + few()
+    t = _dev(z, kind)
+    ids = rng.integers(0, vocab, 12)
+    for scale, top in ((1.0, 5), (2.0 ** -10, 20), (0.7, 0)):
+        _check(t, times, ids, scale, top)
