@@ -1,4 +1,5 @@
-"""Log probabilities of tokens on the GPU in each of the kernels a call may take: rows far from zero."""
+"""Log probabilities of tokens on the GPU in each of the kernels a call may take: rows far from zero, every
+order of a row's values, and more high values than are listed at once."""
 
 import numpy as np
 import pytest
@@ -76,3 +77,66 @@ def test_rows_of_large_values(kind, times, vocab):
     ids = rng.integers(0, vocab, 12)
     for scale, top in ((1.0, 5), (2.0 ** -10, 20), (0.7, 0)):
         _check(t, times, ids, scale, top)
+
+
+# threads of the workgroups that rows of a vocabulary get, 264 of them or (for 128 threads) 516
+ORDERS = [(64, 22, 300), (64, 22, 1000), (64, 22, 5001), (64, 22, 20011), (128, 43, 17001), (128, 43, 20011), (256, 1, 5001)]
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("threads,times,vocab", ORDERS)
+def test_orders_in_each_kernel(kind, threads, times, vocab):
+    """Rows in rising and falling order, of one value, of few values, with the highest side by side, in one thread's
+    rounds, at both ends; masked but for a few; with zeros of both signs; from odd addresses on too."""
+    rng = np.random.default_rng(vocab)
+    z = np.zeros((12, vocab))
+    z[0] = np.linspace(-5, 5, vocab)
+    z[1] = z[0][::-1]
+    z[2] = 0.25
+    z[3] = rng.integers(0, 3, vocab)
+    z[4] = rng.standard_normal(vocab)
+    z[4, vocab // 3:vocab // 3 + 70] = 9 + rng.random(70)
+    z[5] = rng.standard_normal(vocab)
+    z[5, ::threads * 8] = 7.0
+    z[6, :5], z[6, -5:] = 3.0, 3.0
+    z[7] = -np.inf
+    z[7, rng.integers(0, vocab, 5)] = rng.random(5)
+    z[8] = -3.3e38
+    z[9] = -3.3e38
+    z[9, -1] = 1.0
+    z[10] = np.where(rng.random(vocab) < 0.5, 0.0, -0.0)
+    z[11] = -np.inf
+    t = _dev(z, kind)
+    ids = rng.integers(0, vocab, 12)
+    for top in (1, 20, 64):
+        _check(t, times, ids, 1.0, top)
+    for off in (1, 3):
+        _check(t, times, ids, 1.0, 20, off)
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("threads,rows,vocab,pieces", [(64, 300, 4096, 1), (128, 600, 20000, 1), (256, 3, 8184, 1),
+                                                       (256, 530, 40000, 1), (256, 2, 16384, 2), (64, 300, 20000, 2)])
+def test_more_high_values_than_are_listed(kind, threads, rows, vocab, pieces):
+    """63 threads of a workgroup hold nothing but high values, a 64th a single value below them: that one is the
+    bound of the top 64, and more keys reach it than a workgroup lists (576) at once."""
+    rng = np.random.default_rng(threads + vocab)
+    piece = -(-vocab // pieces)
+    assert piece % 8 == 0
+    at = np.arange(vocab) % piece
+    thread = at // 8 % threads
+    base = rng.standard_normal((4, vocab)).clip(-4, 4)
+    base = np.where(thread < 63, 20 + rng.random((4, vocab)), base)
+    base[:, (thread == 63) & (at % 8 == 5) & (at < 8 * threads)] = 10.0
+    for p in range(pieces):
+        assert all((base[:, p * piece:(p + 1) * piece] >= 10.0).sum(1) > 576)
+    z = _dev(base, kind).repeat(-(-rows // 4), 1)[:rows].contiguous()
+    ids = torch.zeros(rows, dtype=torch.int64, device="cuda")
+    got = M.ma_token_logprob_forward(z, ids, top=64)
+    want = torch.sort(z[:4].float(), dim=1, descending=True, stable=True)[1][:, :64]
+    assert torch.equal(got[3], want.repeat(-(-rows // 4), 1)[:rows])
+    lse = torch.logsumexp(z[:4].double(), 1)
+    lp = torch.gather(z[:4].double(), 1, want) - lse[:, None]
+    # (values of at most 21 and lse of at most 32 in float32: a few of their half steps, and the sum's own)
+    tol = (vocab / 8 + 40) * 2.0 ** -24 + 8 * 32 * 2.0 ** -24
+    assert (got[4].double() - lp.repeat(-(-rows // 4), 1)[:rows]).abs().max() <= tol
