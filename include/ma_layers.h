@@ -205,7 +205,8 @@ int ma_attention_backward_workspace_size(const ma_attention* a, size_t* bytes);
 
 /* dq, dk and dv from dout and the forward pass' o and lse.  dk and dv sum over the query heads
  * that share them; keys that no query sees get 0.  The probabilities and the scores' gradients
- * of a bfloat16 call are rounded to bfloat16 for their products.  No atomics: reruns are
+ * of a bfloat16 call are rounded to bfloat16 for their products.  The probabilities are formed
+ * from lse and err by |lse| 2^-24 of themselves, by which it is rounded.  No atomics: reruns are
  * bitwise equal.  Errors: as ma_attention_forward. */
 int ma_attention_backward(const ma_attention* a, void* workspace, size_t ws_bytes, void* stream);
 

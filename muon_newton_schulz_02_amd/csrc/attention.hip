@@ -35,6 +35,8 @@
 namespace ma {
 namespace {
 
+constexpr float kFine = 0x1p24f;         // a product below it is rounded by at most 1 / 2
+
 template <typename T, int DP, int KV, int WAVES>
 __global__ __launch_bounds__(64 * WAVES * kHalves<DP>, (kPer<T, DP>)) void k_attention_forward(AttnArgs a,
                                                                                             AttnGrid grid) {
@@ -57,7 +59,10 @@ __global__ __launch_bounds__(64 * WAVES * kHalves<DP>, (kPer<T, DP>)) void k_att
     f32x16 o[DW / 32];
 #pragma unroll
     for (int b = 0; b < DW / 32; ++b) o[b] = zero16();
-    float m = -kInf, l = 0.f;
+    // The running maximum, m k as it is taken off the scores, and the sum.  Lanes whose m k is too coarse once
+    // rounded (from 2^31 on the rounding alone leaves the range of 2^x) take m off first.
+    float m = -kInf, mk = 0.f, l = 0.f;
+    uint64_t coarse = 0;
     const float k = a.scale * kLog2e;
     // key tiles that some row of the workgroup sees
     const int end = min(j.row0 + BLOCK, j.q_len) - 1;
@@ -105,17 +110,26 @@ __global__ __launch_bounds__(64 * WAVES * kHalves<DP>, (kPer<T, DP>)) void k_att
         top = fmaxf(top, other_half(top));
         // The reference m follows the largest score only where that is 2^8 above it: a
         // probability of up to 2^8 is as exact, and most tiles then leave the sums alone.
-        if (__any((top - m) * k > 8.f)) {
+        if (__ballot((top - m) * k > 8.f) | coarse) {
             const float to = fmaxf(m, top);
             const float c = to == -kInf ? 1.f : __builtin_amdgcn_exp2f((m - to) * k);
             m = to;
+            mk = m == -kInf ? 0.f : m * k;
             l *= c;
 #pragma unroll
             for (int b = 0; b < DW / 32; ++b)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) o[b][i] *= c;
+            const bool far = fabsf(mk) >= kFine;
+            coarse = __ballot(far);
+            if (coarse) {
+#pragma unroll
+                for (int n = 0; n < KV / 32; ++n)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) s[n][i] -= far ? m : 0.f;
+                mk = far ? 0.f : mk;
+            }
         }
-        const float mk = m == -kInf ? 0.f : m * k;
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int n = 0; n < KV / 32; ++n)
