@@ -53,6 +53,14 @@ def _dtype(x, what: str) -> int:
         raise TypeError("%s must be float32 or bfloat16 (got %s)" % (what, x.dtype)) from None
 
 
+def _whole(v, what: str, bits: int = 64) -> int:
+    """An integer that C takes in so many bits (ctypes by itself passes the lowest of a longer one)."""
+    v = int(v)
+    if not -(1 << bits - 1) <= v < 1 << bits - 1:
+        raise ValueError("%s %d is outside the range of %d bits" % (what, v, bits))
+    return v
+
+
 def _rows(x, what: str):
     """(rows, columns, row stride) of a tensor read as a matrix."""
     dim = x.dim()
@@ -374,7 +382,8 @@ def ma_embedding_lookup(table, tokens, scale: float = 1.0, out=None, out_dtype=N
 
 def ma_embedding_grad_workspace_size(n_tokens: int, vocab: int, hidden: int) -> int:
     n = C.c_size_t()
-    rc = _abi.load().ma_embedding_grad_workspace_size(n_tokens, vocab, hidden, C.byref(n))
+    rc = _abi.load().ma_embedding_grad_workspace_size(_whole(n_tokens, "n_tokens"), _whole(vocab, "vocab"),
+                                                      _whole(hidden, "hidden"), C.byref(n))
     if rc:
         _fail(rc, "ma_embedding_grad_workspace_size")
     return n.value
@@ -414,7 +423,7 @@ def ma_embedding_grad(dout, tokens, vocab: int, scale: float = 1.0, padding_toke
         raise ValueError("out must be contiguous")
     ws, ws_ptr, ws_bytes = _workspace(workspace, need, dev)
     rc = _abi.load().ma_embedding_grad(dout.data_ptr(), dt, ld, tokens.data_ptr(), tb, rows,
-                                       vocab, hidden, scale, int(padding_token),
+                                       vocab, hidden, scale, _whole(padding_token, "padding_token"),
                                        out.data_ptr(), _dtype(out, "out"),
                                        1 if accumulate else 0, ws_ptr, ws_bytes,
                                        _raw_stream(dev.index))
@@ -430,8 +439,8 @@ def ma_linear_grad_workspace_size(n_tokens: int, n_out: int, n_in: int,
     """Bytes that serve any dy of this shape, whatever its address and stride (a call without
     a workspace allocates what its own dy needs, which may be much less)."""
     n = C.c_size_t()
-    rc = _abi.load().ma_linear_grad_workspace_size(n_tokens, n_out, n_in, _DTYPES[dy_dtype],
-                                                   C.byref(n))
+    rc = _abi.load().ma_linear_grad_workspace_size(_whole(n_tokens, "n_tokens"), _whole(n_out, "n_out"),
+                                                   _whole(n_in, "n_in"), _DTYPES[dy_dtype], C.byref(n))
     if rc:
         _fail(rc, "ma_linear_grad_workspace_size")
     return n.value

@@ -25,8 +25,8 @@ import torch
 
 from . import _abi
 from ._abi import MA_ROTARY_BLOCKS, MA_ROTARY_CYCLED, MA_ROTARY_HALF, MA_ROTARY_PAIRS
-from .grads import (_DTYPES, ActCheckpoint, _At, _check_cuda, _check_workspace, _dtype, _elsewhere, _fail, _held, _out_as,
-                    _out_like, _raw_stream, _rows, _same_device, _token_bytes, _workspace)
+from .grads import (_DTYPES, ActCheckpoint, _At, _check_cuda, _check_workspace, _dtype, _elsewhere, _fail, _held,
+                    _out_as, _out_like, _raw_stream, _rows, _same_device, _token_bytes, _whole, _workspace)
 
 _LAYOUTS = {"half": MA_ROTARY_HALF, "pairs": MA_ROTARY_PAIRS}
 _ORDERS = {"blocks": MA_ROTARY_BLOCKS, "cycled": MA_ROTARY_CYCLED}
@@ -115,7 +115,7 @@ def ma_rms_norm_forward(x, weight, residual=None, eps: float = 1e-6, weight_offs
 
 def ma_rms_norm_backward_workspace_size(rows: int, cols: int) -> int:
     n = C.c_size_t()
-    rc = _abi.load().ma_rms_norm_backward_workspace_size(rows, cols, C.byref(n))
+    rc = _abi.load().ma_rms_norm_backward_workspace_size(_whole(rows, "rows"), _whole(cols, "cols"), C.byref(n))
     if rc:
         _fail(rc, "ma_rms_norm_backward_workspace_size")
     return n.value
@@ -203,14 +203,14 @@ class Rotary:
 
     def __init__(self, sections, theta: float = 10000.0, layout: str = "half", order: str = "blocks",
                  restart: bool = False):
-        sections = (int(sections),) if isinstance(sections, int) else tuple(int(n) for n in sections)
+        sections = tuple(_whole(n, "a section", 32) for n in ((sections,) if isinstance(sections, int) else sections))
         if layout not in _LAYOUTS:
             raise ValueError("layout must be one of %s" % ", ".join(sorted(_LAYOUTS)))
         if order not in _ORDERS:
             raise ValueError("order must be one of %s" % ", ".join(sorted(_ORDERS)))
         self.sections, self.axes, self.pairs = sections, len(sections), sum(sections)
         self.theta, self.layout, self.order, self.restart = float(theta), layout, order, bool(restart)
-        n = max(1, self.pairs)
+        n = min(max(1, self.pairs), _abi.MA_ROTARY_MAX_PAIRS)          # (more are refused)
         self._freq, self._axis, self._layout = (C.c_double * n)(), (C.c_uint8 * n)(), _LAYOUTS[layout]
         rc = _abi.load().ma_rotary_frequencies((C.c_int32 * max(1, self.axes))(*sections), self.axes, self.theta,
                                                _ORDERS[order], int(self.restart), self._freq, self._axis)
@@ -283,7 +283,8 @@ def _tokens_of(tokens, what: str, shape):
 
 def ma_token_logprob_workspace_size(n_tokens: int, vocab: int, top: int = 0) -> int:
     n = C.c_size_t()
-    rc = _abi.load().ma_token_logprob_workspace_size(n_tokens, vocab, top, C.byref(n))
+    rc = _abi.load().ma_token_logprob_workspace_size(_whole(n_tokens, "n_tokens"), _whole(vocab, "vocab"),
+                                                     _whole(top, "top", 32), C.byref(n))
     if rc:
         _fail(rc, "ma_token_logprob_workspace_size")
     return n.value
@@ -359,8 +360,8 @@ def ma_token_logprob_backward(logits, tokens, lse, dlogprob, entropy=None, dentr
 
 def _offsets(cu, what: str):
     _check_cuda(cu, what)
-    if cu.dtype != torch.int32 or cu.dim() != 1 or cu.shape[0] < 1 or not cu.is_contiguous():
-        raise ValueError("%s must be a contiguous int32 vector of offsets" % what)
+    if cu.dtype != torch.int32 or cu.dim() != 1 or not 1 <= cu.shape[0] <= 1 << 31 or not cu.is_contiguous():
+        raise ValueError("%s must be a contiguous int32 vector of at most 2^31 offsets" % what)
     return cu.shape[0] - 1
 
 
@@ -438,8 +439,10 @@ def _sizes_args(n_queries, n_keys, heads, kv_heads, head_dim, n_seqs, causal, dt
     """Arguments of contiguous, aligned arrays of these sizes."""
     a = _abi.ma_attention()
     a.causal = 1 if causal else 0
+    heads, kv_heads, head_dim = _whole(heads, "heads", 32), _whole(kv_heads, "kv_heads", 32), _whole(head_dim, "head_dim", 32)
     a.dtype, a.heads, a.kv_heads, a.head_dim = _DTYPES[dtype], heads, kv_heads, head_dim
-    a.n_queries, a.n_keys, a.n_seqs, a.scale = n_queries, n_keys, n_seqs, 1.0
+    a.n_queries, a.n_keys = _whole(n_queries, "n_queries"), _whole(n_keys, "n_keys")
+    a.n_seqs, a.scale = _whole(n_seqs, "n_seqs", 32), 1.0
     a.cu_q = a.cu_k = 256          # (only looked at for being there)
     for field, n in ((a.q, heads), (a.k, kv_heads), (a.v, kv_heads), (a.o, heads), (a.dout, heads), (a.dq, heads),
                      (a.dk, kv_heads), (a.dv, kv_heads)):
