@@ -46,11 +46,15 @@ def _fail(rc: int, what: str):
 
 # ------------------------------------------------------------- arguments --
 
-def _dtype(x, what: str) -> int:
+def _dtype_code(dtype, what: str) -> int:
     try:
-        return _DTYPES[x.dtype]
+        return _DTYPES[dtype]
     except KeyError:
-        raise TypeError("%s must be float32 or bfloat16 (got %s)" % (what, x.dtype)) from None
+        raise TypeError("%s must be float32 or bfloat16 (got %s)" % (what, dtype)) from None
+
+
+def _dtype(x, what: str) -> int:
+    return _dtype_code(x.dtype, what)
 
 
 def _whole(v, what: str, bits: int = 64) -> int:
@@ -440,7 +444,7 @@ def ma_linear_grad_workspace_size(n_tokens: int, n_out: int, n_in: int,
     a workspace allocates what its own dy needs, which may be much less)."""
     n = C.c_size_t()
     rc = _abi.load().ma_linear_grad_workspace_size(_whole(n_tokens, "n_tokens"), _whole(n_out, "n_out"),
-                                                   _whole(n_in, "n_in"), _DTYPES[dy_dtype], C.byref(n))
+                                                   _whole(n_in, "n_in"), _dtype_code(dy_dtype, "dy"), C.byref(n))
     if rc:
         _fail(rc, "ma_linear_grad_workspace_size")
     return n.value

@@ -25,7 +25,7 @@ import torch
 
 from . import _abi
 from ._abi import MA_ROTARY_BLOCKS, MA_ROTARY_CYCLED, MA_ROTARY_HALF, MA_ROTARY_PAIRS
-from .grads import (_DTYPES, ActCheckpoint, _At, _check_cuda, _check_workspace, _dtype, _elsewhere, _fail, _held,
+from .grads import (ActCheckpoint, _At, _check_cuda, _check_workspace, _dtype, _dtype_code, _elsewhere, _fail, _held,
                     _out_as, _out_like, _raw_stream, _rows, _same_device, _token_bytes, _whole, _workspace)
 
 _LAYOUTS = {"half": MA_ROTARY_HALF, "pairs": MA_ROTARY_PAIRS}
@@ -440,7 +440,7 @@ def _sizes_args(n_queries, n_keys, heads, kv_heads, head_dim, n_seqs, causal, dt
     a = _abi.ma_attention()
     a.causal = 1 if causal else 0
     heads, kv_heads, head_dim = _whole(heads, "heads", 32), _whole(kv_heads, "kv_heads", 32), _whole(head_dim, "head_dim", 32)
-    a.dtype, a.heads, a.kv_heads, a.head_dim = _DTYPES[dtype], heads, kv_heads, head_dim
+    a.dtype, a.heads, a.kv_heads, a.head_dim = _dtype_code(dtype, "q"), heads, kv_heads, head_dim
     a.n_queries, a.n_keys = _whole(n_queries, "n_queries"), _whole(n_keys, "n_keys")
     a.n_seqs, a.scale = _whole(n_seqs, "n_seqs", 32), 1.0
     a.cu_q = a.cu_k = 256          # (only looked at for being there)

@@ -1,5 +1,5 @@
-"""Python integers that do not fit the C type they go into are refused by the
-binding: ctypes would take their lowest bits."""
+"""Python integers that do not fit the C type they go into, and types without kernels, are refused by the
+binding: ctypes would take the lowest bits of one, and a bare dictionary names neither argument nor type."""
 
 import resource
 
@@ -54,6 +54,13 @@ def test_attention_sizes(size):
         for n in BIG64 + (BIG32 if not name.startswith("n_q") and not name.startswith("n_k") else []):
             with pytest.raises(ValueError, match=name):
                 size(**dict(ATTN, **{name: n}))
+    with pytest.raises(TypeError, match="float16"):
+        size(**ATTN, dtype=torch.float16)
+
+
+def test_linear_grad_size_names_the_type():
+    with pytest.raises(TypeError, match="float16"):
+        M.ma_linear_grad_workspace_size(10, 10, 10, dy_dtype=torch.float16)
 
 
 @pytest.mark.parametrize("sections", [(2 ** 32 + 4,), (4, 2 ** 32 + 4), (-2 ** 32 + 4,)])
