@@ -16,15 +16,15 @@
 // results a last launch joins in order.  This file has the forward kernel, what is before and
 // behind the others, and the rules for pieces.
 //
-// Bound by issue: 20011 tokens of 7 sequences, 16 / 4 heads of 128, bf16: forward 251 GFLOP in
-// 290 to 325 us (0.77 to 0.86 PFLOP/s; a library product of 8192 x 8192 matrices reaches 1.2 to 1.4).
-// A tile of 32 queries and 64 keys is 1024 cycles of matrix instructions a wave, and about 1000
-// of the vector unit's for the maximum, exponential, sum and rounding of 2048 scores, half of it
-// the exponentials.  Matrix instructions take 48 % of a SIMD's cycles, the others 50 %: two
-// waves hardly overlap them, in whatever order (the next tile's scores formed step by step
-// between this one's exponentials: 318 -> 328 us).  One sequence of 14336 tokens with 8 heads: 0.95
+// 20011 tokens of 7 sequences, 16 / 4 heads of 128, bf16: forward 251 GFLOP in 290 to 325 us (0.77 to
+// 0.86 PFLOP/s; a library product of 8192 x 8192 matrices reaches 1.2 to 1.4).  Bound by matrix and vector
+// work that hardly overlap: 48 and 44 % of a SIMD's cycles.  A tile of 32 queries and 64 keys is 32
+// matrix instructions of 32 cycles a wave, and (masked tiles and the prologue shared out) some 205
+// vector ones for the maximum, exponential, sum and rounding of 2048 scores, of whose time the
+// exponentials, of 8 cycles each, take 28 %.  The next tile's scores formed step by step between this
+// one's exponentials: 318 -> 328 us.  One sequence of 14336 tokens with 8 heads: 0.95 to 1.0
 // PFLOP/s.  Backward (dq, dkv and what is around them) 627 GFLOP counted as five products,
-// seven done, in 1.03 to 1.06 ms.
+// seven done, in 1.0 to 1.06 ms.
 
 #include <hip/hip_runtime.h>
 

@@ -3,10 +3,14 @@
 // 2^(S - lse), with dP = dout V^T and dS = P (dP - delta) summing dv^T += dout^T P and dk^T +=
 // Q^T dS: four products a tile.
 //
-// Bound by issue: 20011 tokens of 7 sequences, 16 / 4 heads of 128, bf16, in 575 to 605 us (502
-// GFLOP, 0.83 to 0.87 PFLOP/s) and 41 to join two pieces, matrix instructions on 56 % of a SIMD's cycles, others on
-// 40, LDS reads on 42 % of the CU's.  All 256 registers are taken: constant LDS slots, two
+// 20011 tokens of 7 sequences, 16 / 4 heads of 128, bf16, in 575 to 605 us (502 GFLOP, 0.83 to 0.87
+// PFLOP/s) and 41 to join two pieces: matrix instructions on 55 % of a SIMD's cycles, vector ones on 33, LDS reads
+// on 42 % of the CU's.  All 256 registers are taken: constant LDS slots, two
 // tiles a turn as in the other walks, spill.
+//
+// Heads of 256 in bfloat16 spill 16 registers, most of them fragments of K or V that are read back inside the
+// loop over tiles, and each of those reads waits for every copy into LDS too, so the next tile's are not
+// under way during this one: 10011 tokens of 4 sequences, 8 / 1 heads, take 807 us, 0.36 PFLOP/s.
 
 #include <hip/hip_runtime.h>
 

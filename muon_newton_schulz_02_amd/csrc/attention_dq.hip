@@ -2,8 +2,8 @@
 // the keys, recomputing the scores S^T = K Q^T and P^T = 2^(S^T - lse), with dP^T = V dout^T
 // and dS^T = P^T (dP^T - delta) summing dq^T += K^T dS^T: three products a tile.
 //
-// Bound by issue as the forward pass is: 20011 tokens of 7 sequences, 16 / 4 heads of 128, bf16,
-// in 385 us (376 GFLOP, 0.98 PFLOP/s), matrix instructions on 58 % of a SIMD's cycles, others on 46.
+// Bound as the forward pass is: 20011 tokens of 7 sequences, 16 / 4 heads of 128, bf16, in 385 us (376
+// GFLOP, 0.98 PFLOP/s), matrix instructions on 58 % of a SIMD's cycles, vector ones on 39.
 
 #include <hip/hip_runtime.h>
 
