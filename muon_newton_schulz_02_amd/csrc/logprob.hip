@@ -22,7 +22,8 @@
 // rounds go on meanwhile.  Few rows are bound by latency: 37 of 32003 fp32 in pieces 11 us and 4 to join.
 //
 // Units of 8 elements begin at 16-byte addresses: a row's first and last elements, where
-// they are not a whole unit, are taken by one thread each.
+// they are not a whole unit, are taken by one thread each.  So which elements a thread sums follows
+// from the row's address modulo 16 too: the same values elsewhere may differ in their last bits.
 
 #include <hip/hip_runtime.h>
 
