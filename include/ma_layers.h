@@ -14,8 +14,9 @@
  * Conventions are those of ma_grads.h: return codes and messages, checks
  * before any launch, caller-owned memory, the caller's HIP stream, capturable,
  * a workspace of its own for each of two calls that may run at once, float32
- * arithmetic with one rounding to an array's type, results that do not depend
- * on timing, strides in elements.  Written arrays overlap neither each other
+ * arithmetic with one rounding to an array's type (attention in bfloat16 rounds what
+ * its matrix instructions take once more, as its functions say), results that do not
+ * depend on timing, strides in elements.  Written arrays overlap neither each other
  * nor an input, unless a function allows it.
  */
 #ifndef MA_LAYERS_H_
